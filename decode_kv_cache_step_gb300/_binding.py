@@ -24,13 +24,18 @@ LF_ERR_NO_MEMORY = 4
 
 LF_DEVERR_BAD_WRITE_SLOT = 0x1
 LF_DEVERR_WAIT_TIMEOUT = 0x2
+LF_DEVERR_BAD_LENGTH = 0x4
 
 LF_KERNEL_DECODE_STEP = 0
 LF_KERNEL_ATTENTION = 1
 LF_KERNEL_SCORE = 2
+LF_KERNEL_NORM_ROPE = 3
+LF_KERNEL_PACKED_ATTENTION = 4
 KERNEL_NAMES = {LF_KERNEL_DECODE_STEP: "lf_decode_step_kernel",
                 LF_KERNEL_ATTENTION: "lf_decode_step_kernel (attention-only variant)",
-                LF_KERNEL_SCORE: "lf_score_kernel"}
+                LF_KERNEL_SCORE: "lf_score_kernel",
+                LF_KERNEL_NORM_ROPE: "lf_rope_kernel",
+                LF_KERNEL_PACKED_ATTENTION: "lf_attn_kernel"}
 
 LF_STEP_FILL_EMPTY_FIRST = 0x1
 LF_STEP_MASK_EVICTED = 0x2
@@ -42,6 +47,9 @@ EXPORTED = (
     "lf_decode_step", "lf_decode_step_scores", "lf_decode_step_ex", "lf_decode_attention",
     "lf_decode_step_host", "lf_decode_step_noalloc", "lf_step_prepare", "lf_step_run",
     "lf_step_errors", "lf_step_destroy", "lf_step_plan", "lf_device_errors",
+    "lf_qk_norm_rope", "lf_prefill_append", "lf_window_attention",
+    "lf_window_attention_workspace", "lf_decode_step_prefix", "lf_decode_attention_prefix",
+    "lf_decode_prefix_workspace",
     "lf_profile_enable", "lf_profile_collect", "lf_release_workspace", "lf_status_string",
     "lf_last_error", "lf_version",
 )
@@ -101,6 +109,18 @@ def load_library(path: str | None = None):
         lib.lf_step_destroy.restype = I
         lib.lf_step_plan.argtypes = [I] * 6 + [ctypes.POINTER(ctypes.c_int32)]
         lib.lf_step_plan.restype = I
+        L, Z = ctypes.c_int64, ctypes.c_size_t
+        lib.lf_qk_norm_rope.argtypes = [P, L] + [P] * 7 + [I] * 6 + [F, P]
+        lib.lf_prefill_append.argtypes = [P, L] + [P] * 10 + [I] * 8 + [F, P]
+        lib.lf_window_attention.argtypes = [P] * 6 + [I] * 8 + [F, P, Z, P]
+        lib.lf_window_attention_workspace.argtypes = [I] * 8 + [ctypes.POINTER(Z)]
+        lib.lf_decode_step_prefix.argtypes = [P] * 13 + [I, I, P] + [I] * 8 + [F, P, Z, P]
+        lib.lf_decode_attention_prefix.argtypes = [P] * 12 + [I] * 7 + [F, P, Z, P]
+        lib.lf_decode_prefix_workspace.argtypes = [I] * 7 + [ctypes.POINTER(Z)]
+        for fn in (lib.lf_qk_norm_rope, lib.lf_prefill_append, lib.lf_window_attention,
+                   lib.lf_window_attention_workspace, lib.lf_decode_step_prefix,
+                   lib.lf_decode_attention_prefix, lib.lf_decode_prefix_workspace):
+            fn.restype = I
         lib.lf_device_errors.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), I]
         lib.lf_device_errors.restype = I
         lib.lf_profile_enable.argtypes = [I]
@@ -333,6 +353,229 @@ class PreparedStep:
             self.close()
         except Exception:
             pass
+
+
+def _on_device(device, *tensors):
+    """The device guard of a call on `device`, where every tensor has to be."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: all must be on one device")
+    return torch.cuda.device(device)
+
+
+def _workspace(workspace, nbytes, device, stream):
+    """The caller's workspace, or one from torch's allocator on the call's stream."""
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
+            raise TypeError("workspace: expected a uint8 torch.Tensor")
+        if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: must be a contiguous tensor on {device}")
+        return workspace
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv):
+    if not isinstance(qkv, torch.Tensor) or not isinstance(q_out, torch.Tensor):
+        raise TypeError("qkv and q_out: expected torch.Tensors")
+    if q_out.dim() != 3 or qkv.dim() != 3:
+        raise ValueError("qkv must be [T,Hq+2*Hkv,d] and q_out [T,Hq,d]")
+    T, Hq, d = (int(x) for x in q_out.shape)
+    bf = torch.bfloat16
+    _need(q_out, "q_out", bf, (T, Hq, d), True)
+    if qkv.dtype != bf:
+        raise TypeError(f"qkv: dtype {qkv.dtype}, expected {bf}")
+    if tuple(qkv.shape) != (T, Hq + 2 * Hkv, d):
+        raise ValueError(f"qkv: shape {tuple(qkv.shape)}, expected {(T, Hq + 2 * Hkv, d)}")
+    if not qkv.is_cuda:
+        raise ValueError("qkv: must be a CUDA tensor")
+    if qkv.stride(2) != 1 or qkv.stride(1) != d:
+        raise ValueError("qkv: a row's heads must be contiguous")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight must both be given or both be None")
+    if q_weight is not None:
+        _need(q_weight, "q_weight", bf, (d,), True)
+        _need(k_weight, "k_weight", bf, (d,), True)
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a [rot/2] tensor")
+    _need(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), True)
+    stride = qkv.stride(0) if T > 1 else max(int(qkv.stride(0)), (Hq + 2 * Hkv) * d)
+    if T == 1 and stride % 8:
+        stride = (Hq + 2 * Hkv) * d  # a single row has no stride to speak of
+    return T, Hq, d, 2 * inv_freq.numel(), stride
+
+
+def qk_norm_rope(qkv, q_weight, k_weight, inv_freq, positions, q_out, k_out, v_out, eps=1e-6,
+                 interleaved=False, stream=None):
+    """lf_qk_norm_rope: per-head norm (weights None: none) and rotation of the
+    query and key heads of qkv [T,Hq+2*Hkv,d] (rows may be strided), values
+    copied, into q_out [T,Hq,d] and k_out, v_out [T,Hkv,d]: decode_step's q,
+    new_k and new_v for T = B. inv_freq [rot/2] fp32, positions [T] int32."""
+    lib = load_library()
+    if not isinstance(k_out, torch.Tensor) or k_out.dim() != 3:
+        raise ValueError("k_out must be [T,Hkv,d]")
+    Hkv = int(k_out.shape[1])
+    T, Hq, d, rot, stride = _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv)
+    bf = torch.bfloat16
+    _need(k_out, "k_out", bf, (T, Hkv, d), True)
+    _need(v_out, "v_out", bf, (T, Hkv, d), True)
+    _need(positions, "positions", torch.int32, (T,), True)
+    with _on_device(qkv.device, q_weight, k_weight, inv_freq, positions, q_out, k_out, v_out):
+        _check(lib, lib.lf_qk_norm_rope(
+            qkv.data_ptr(), stride, _ptr(q_weight), _ptr(k_weight), inv_freq.data_ptr(),
+            positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), T, Hq, Hkv,
+            d, rot, int(bool(interleaved)), float(eps), _stream_handle(stream)))
+
+
+def prefill_append(qkv, q_weight, k_weight, inv_freq, q_start, kv_len, q_out, k_cache, v_cache,
+                   mask, eps=1e-6, interleaved=False, pos_offset=None, stream=None):
+    """lf_prefill_append: qk_norm_rope of prompt tokens, their keys, values and
+    ages straight into the caches. Rows q_start[b]..q_start[b+1] of qkv are
+    the last tokens of sequence b's kv_len[b]."""
+    lib = load_library()
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be [B,Hkv,S,d]")
+    B, Hkv, S = (int(x) for x in k_cache.shape[:3])
+    T, Hq, d, rot, stride = _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv)
+    bf, i32 = torch.bfloat16, torch.int32
+    _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
+    _need(v_cache, "v_cache", bf, (B, Hkv, S, d), True)
+    _need(mask, "mask", i32, (B, Hkv, S), True)
+    _need(q_start, "q_start", i32, (B + 1,), True)
+    _need(kv_len, "kv_len", i32, (B,), True)
+    if pos_offset is not None:
+        _need(pos_offset, "pos_offset", i32, (B,), True)
+    with _on_device(qkv.device, q_weight, k_weight, inv_freq, q_start, kv_len, pos_offset, q_out,
+                    k_cache, v_cache, mask):
+        _check(lib, lib.lf_prefill_append(
+            qkv.data_ptr(), stride, _ptr(q_weight), _ptr(k_weight), inv_freq.data_ptr(),
+            q_start.data_ptr(), kv_len.data_ptr(), _ptr(pos_offset), q_out.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(), T, B, Hq, Hkv, d, S, rot,
+            int(bool(interleaved)), float(eps), _stream_handle(stream)))
+
+
+def window_attention_workspace(T, B, Hq, Hkv, d, S, window=0, sinks=0) -> int:
+    """Workspace bytes of window_attention for these sizes on the current device."""
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib, lib.lf_window_attention_workspace(int(T), int(B), int(Hq), int(Hkv), int(d),
+                                                  int(S), int(window), int(sinks),
+                                                  ctypes.byref(n)))
+    return int(n.value)
+
+
+def window_attention(q, k_cache, v_cache, q_start, kv_len, out, window, sinks, scale,
+                     workspace=None, stream=None):
+    """lf_window_attention: packed rows q [T,Hq,d] over in-order caches
+    [B,Hkv,S,d]; a token sees its last `window` keys (0: all) and the first
+    `sinks`. workspace: uint8 of window_attention_workspace bytes (None: taken
+    from torch's allocator)."""
+    lib = load_library()
+    if not isinstance(q, torch.Tensor) or not isinstance(k_cache, torch.Tensor):
+        raise TypeError("q and k_cache: expected torch.Tensors")
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [T,Hq,d] and k_cache [B,Hkv,S,d]")
+    T, Hq, d = (int(x) for x in q.shape)
+    B, Hkv, S = (int(x) for x in k_cache.shape[:3])
+    bf, i32 = torch.bfloat16, torch.int32
+    _need(q, "q", bf, (T, Hq, d), True)
+    _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
+    _need(v_cache, "v_cache", bf, (B, Hkv, S, d), True)
+    _need(q_start, "q_start", i32, (B + 1,), True)
+    _need(kv_len, "kv_len", i32, (B,), True)
+    _need(out, "out", bf, (T, Hq, d), True)
+    with _on_device(q.device, k_cache, v_cache, q_start, kv_len, out):
+        n = window_attention_workspace(T, B, Hq, Hkv, d, S, window, sinks)
+        ws = _workspace(workspace, n, q.device, stream) if n or workspace is not None else None
+        _check(lib, lib.lf_window_attention(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), q_start.data_ptr(),
+            kv_len.data_ptr(), out.data_ptr(), T, B, Hq, Hkv, d, S, int(window), int(sinks),
+            float(scale), _ptr(ws), 0 if ws is None else ws.numel(), _stream_handle(stream)))
+
+
+def decode_prefix_workspace(B, Hq, Hkv, d, S, N, P) -> int:
+    """Workspace bytes of the *_prefix calls for these sizes on the current device."""
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib, lib.lf_decode_prefix_workspace(int(B), int(Hq), int(Hkv), int(d), int(S), int(N),
+                                               int(P), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _check_prefix(k_prefix, v_prefix, prefix_start, prefix_len, Hkv, d):
+    if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 4:
+        raise ValueError("k_prefix must be [N,Hkv,P,d]")
+    N, P = int(k_prefix.shape[0]), int(k_prefix.shape[2])
+    bf, i32 = torch.bfloat16, torch.int32
+    _need(k_prefix, "k_prefix", bf, (N, Hkv, P, d), True)
+    _need(v_prefix, "v_prefix", bf, (N, Hkv, P, d), True)
+    _need(prefix_start, "prefix_start", i32, (N + 1,), True)
+    _need(prefix_len, "prefix_len", i32, (N,), True)
+    return N, P
+
+
+def decode_attention_prefix(q, k_cache, v_cache, mask, new_k, new_v, write_slot, k_prefix,
+                            v_prefix, prefix_start, prefix_len, out, scale, workspace=None,
+                            stream=None):
+    """lf_decode_attention_prefix: decode_attention whose sequences
+    prefix_start[n]..prefix_start[n+1] also see the prefix_len[n] tokens of
+    prefix n (k_prefix, v_prefix [N,Hkv,P,d]), in one softmax."""
+    lib = load_library()
+    B, Hq, Hkv, d, S = _shapes(q, k_cache)
+    bf, i32 = torch.bfloat16, torch.int32
+    _need(q, "q", bf, (B, Hq, d), True)
+    _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
+    _need(v_cache, "v_cache", bf, (B, Hkv, S, d), True)
+    _need(mask, "mask", i32, (B, Hkv, S), True)
+    _need(new_k, "new_k", bf, (B, Hkv, d), True)
+    _need(new_v, "new_v", bf, (B, Hkv, d), True)
+    _need(write_slot, "write_slot", i32, (B, Hkv), True)
+    _need(out, "out", bf, (B, Hq, d), True)
+    N, P = _check_prefix(k_prefix, v_prefix, prefix_start, prefix_len, Hkv, d)
+    with _on_device(q.device, k_cache, v_cache, mask, new_k, new_v, write_slot, out, k_prefix,
+                    v_prefix, prefix_start, prefix_len):
+        ws = _workspace(workspace, 0 if workspace is not None else
+                        decode_prefix_workspace(B, Hq, Hkv, d, S, N, P), q.device, stream)
+        _check(lib, lib.lf_decode_attention_prefix(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(),
+            new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(), k_prefix.data_ptr(),
+            v_prefix.data_ptr(), prefix_start.data_ptr(), prefix_len.data_ptr(), out.data_ptr(),
+            B, Hq, Hkv, d, S, N, P, float(scale), ws.data_ptr(), ws.numel(),
+            _stream_handle(stream)))
+
+
+def decode_step_prefix(q, k_cache, v_cache, mask, new_k, new_v, write_slot, k_prefix, v_prefix,
+                       prefix_start, prefix_len, out, next_slots, W, scale, k=None, flags=0,
+                       scores=None, workspace=None, stream=None):
+    """lf_decode_step_prefix: decode_step_ex over shared prefixes and the
+    sequences' own slots. next_slots [B,Hkv] (k None: the argmin) or
+    [B,Hkv,k]; only own slots are scored, with weights normalised over both."""
+    lib = load_library()
+    B, Hq, Hkv, d, S = _check_step(q, k_cache, v_cache, mask, new_k, new_v, write_slot, out,
+                                   next_slots, k=k)
+    if scores is not None:
+        _need(scores, "scores", torch.float32, (B, Hkv, S), True)
+    N, P = _check_prefix(k_prefix, v_prefix, prefix_start, prefix_len, Hkv, d)
+    with _on_device(q.device, k_cache, v_cache, mask, new_k, new_v, write_slot, out, next_slots,
+                    scores, k_prefix, v_prefix, prefix_start, prefix_len):
+        ws = _workspace(workspace, 0 if workspace is not None else
+                        decode_prefix_workspace(B, Hq, Hkv, d, S, N, P), q.device, stream)
+        _check(lib, lib.lf_decode_step_prefix(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(),
+            new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(), k_prefix.data_ptr(),
+            v_prefix.data_ptr(), prefix_start.data_ptr(), prefix_len.data_ptr(), out.data_ptr(),
+            next_slots.data_ptr(), 1 if k is None else int(k), int(flags),
+            None if scores is None else scores.data_ptr(), B, Hq, Hkv, d, S, N, P, int(W),
+            float(scale), ws.data_ptr(), ws.numel(), _stream_handle(stream)))
 
 
 def step_plan(B: int, Hq: int, Hkv: int, d: int, S: int, topk: int = 1) -> dict:

@@ -28,6 +28,7 @@ static_assert(LF_STEP_FILL_EMPTY_FIRST == lf::kFlagFillEmptyFirst &&
                   LF_STEP_MASK_EVICTED == lf::kFlagMaskEvicted &&
                   LF_STEP_LOG2_SCORES == lf::kFlagLog2Scores,
               "step flag bits");
+static_assert(LF_DEVERR_BAD_LENGTH == lf::kErrBadLength, "error bits");
 constexpr int kMaxNChunk = 1024;
 constexpr int kMaxS = 1 << 20;
 
@@ -268,6 +269,34 @@ constexpr int kSplitMinSlots = 8192;
 // (smaller ones are tried where it cannot be placed).
 constexpr int kDefaultClusterChunks = 16;
 
+// Whether a step scores in a second kernel, and from which unit on (allowed:
+// a top-1 step without a cluster merge).
+void plan_split_finish(Plan* pl, int S, int units, int sms, bool allowed) {
+    // Top-1 steps over long units without clusters score in a second kernel:
+    // the last CTA's scan of every slot would otherwise run on the step's
+    // tail at one SM's share of the memory system. LF_SPLIT=0 / 1 forces it
+    // off / on (on: for every top-1 step without clusters).
+    const char* senv = std::getenv("LF_SPLIT");
+    const int smode = senv ? std::atoi(senv) : -1;
+    pl->split = allowed && smode != 0 && (smode == 1 || S >= kSplitMinSlots);
+    // A split grid of many waves merges its first units long before the
+    // scoring kernel can start (it starts with the decode grid's last wave),
+    // and by then their score terms have left L2. So the first 3/8 of the
+    // units still scan in their last CTA while their terms are in L2, and
+    // the scoring kernel takes the rest (measured on the 16K-slot workload,
+    // 256 units of 16 chunks, about 9 waves; us per step, per event pair:
+    // every unit split 199.6, the last 224 / 192 / 160 / 128 / 96 units
+    // split 199.4 / 198.6 / 198.3 / 198.4 / 198.9). LF_SPLIT_TAIL sets how
+    // many of the last units the scoring kernel takes.
+    pl->split_from = 0;
+    if (pl->split) {
+        const long long ctas = static_cast<long long>(units) * pl->nchunk;
+        if (ctas >= 4LL * 3 * sms) pl->split_from = units * 3 / 8;
+        if (const char* env = std::getenv("LF_SPLIT_TAIL"))
+            pl->split_from = std::max(0, units - std::max(1, std::atoi(env)));
+    }
+}
+
 // Split the slot axis of every unit into nchunk chunks of chunk_tiles tiles.
 // Each CTA costs a fixed start-up and merge, so chunks stay long (13 to 32
 // tiles) while the grid still has about 27 CTAs per SM (about 4100), the
@@ -385,29 +414,7 @@ Plan plan_split(int S, int units, int sms, bool want_cluster, int D, int G, bool
             if (take_deep) pl.stages = lf::kDeepStages;
         }
     }
-    // Top-1 steps over long units without clusters score in a second kernel:
-    // the last CTA's scan of every slot would otherwise run on the step's
-    // tail at one SM's share of the memory system. LF_SPLIT=0 / 1 forces it
-    // off / on (on: for every top-1 step without clusters).
-    const char* senv = std::getenv("LF_SPLIT");
-    const int smode = senv ? std::atoi(senv) : -1;
-    pl.split = want_cluster && !pl.cluster && smode != 0 && (smode == 1 || S >= kSplitMinSlots);
-    // A split grid of many waves merges its first units long before the
-    // scoring kernel can start (it starts with the decode grid's last wave),
-    // and by then their score terms have left L2. So the first 3/8 of the
-    // units still scan in their last CTA while their terms are in L2, and
-    // the scoring kernel takes the rest (measured on the 16K-slot workload,
-    // 256 units of 16 chunks, about 9 waves; us per step, per event pair:
-    // every unit split 199.6, the last 224 / 192 / 160 / 128 / 96 units
-    // split 199.4 / 198.6 / 198.3 / 198.4 / 198.9). LF_SPLIT_TAIL sets how
-    // many of the last units the scoring kernel takes.
-    pl.split_from = 0;
-    if (pl.split) {
-        const long long ctas = static_cast<long long>(units) * pl.nchunk;
-        if (ctas >= 4LL * 3 * sms) pl.split_from = units * 3 / 8;
-        if (const char* env = std::getenv("LF_SPLIT_TAIL"))
-            pl.split_from = std::max(0, units - std::max(1, std::atoi(env)));
-    }
+    plan_split_finish(&pl, S, units, sms, want_cluster && !pl.cluster);
     return pl;
 }
 
@@ -454,6 +461,10 @@ struct StepArgs {
     int topk = 1;        // slots returned per unit into next_slot[B][Hkv][topk]
     int flags = 0;       // LF_STEP_* bits
     bool score = true;   // false: attention only (no score, no eviction, no ageing)
+    // Shared-prefix pieces joined in the merge (pre_pieces > 0).
+    const float2* pre_ml = nullptr;
+    const float* pre_o = nullptr;
+    int pre_pieces = 0;
 };
 
 lf_status check_args(const StepArgs& a, const Shape& s) {
@@ -545,6 +556,9 @@ lf_status build_launch(const StepArgs& a, const Shape& s, char* base, uint32_t* 
     sp.flags = a.score ? a.flags : 0;
     sp.split = (a.score && pl.split && sp.topk == 1) ? 1 : 0;
     sp.split_from = sp.split ? pl.split_from : 0;
+    sp.pre_ml = a.pre_ml;
+    sp.pre_o = a.pre_o;
+    sp.pre_pieces = a.pre_pieces;
     if (!lf::step_fits(s.d, g, pl.stages, a.score, pl.nchunk, sp.topk))
         return fail(LF_ERR_UNSUPPORTED,
                     "k = %d with %d chunks of the slot axis does not fit in shared memory",
@@ -571,8 +585,11 @@ lf_status launch(const Launch& r, cudaStream_t stream) {
     NvtxRange range(r.score ? "lf_decode_step" : "lf_decode_attention");
     ProfScope prof(r.score ? LF_KERNEL_DECODE_STEP : LF_KERNEL_ATTENTION, stream);
     const bool cluster = r.pl.cluster && r.sp.topk == 1;
-    e = lf::launch_decode_step(r.d, r.g, r.pl.stages, r.score, cluster, r.tmK, r.tmV, r.sp,
-                               r.units, stream);
+    if (r.sp.pre_pieces > 0)
+        e = lf::launch_decode_step_prefix(r.d, r.g, r.score, r.tmK, r.tmV, r.sp, r.units, stream);
+    else
+        e = lf::launch_decode_step(r.d, r.g, r.pl.stages, r.score, cluster, r.tmK, r.tmV, r.sp,
+                                   r.units, stream);
     if (e != cudaSuccess && cluster) {
         // A cluster that cannot be scheduled: the last-CTA merge, scoring
         // in the same kernel.
@@ -680,6 +697,240 @@ void free_handle(lf_step_handle* h) {
     if (h->mem) cudaFree(h->mem);
     if (h->words) cudaFree(h->words);
     delete h;
+}
+
+}  // namespace
+
+// ------------------------------------- prompt and shared-prefix operators --
+//
+// These entry points own no scratch: what they need beyond their arguments
+// comes from the caller's workspace, so two calls (or two captured graphs)
+// with workspaces of their own never share state. Their device error bits go
+// to the static error word of lf_decode_step_noalloc.
+
+namespace {
+
+constexpr int kMaxRows = 1 << 22;    // packed tokens of a call
+constexpr int kMaxPosWindow = 1 << 30;
+
+lf_status static_err_word(int dev, uint32_t** out) {
+    void* base = nullptr;
+    lf_status st = static_scratch_base(dev, &base);
+    if (st != LF_OK) return st;
+    *out = reinterpret_cast<uint32_t*>(static_cast<char*>(base) + kStaticErrOff);
+    return LF_OK;
+}
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+lf_status check_rows(int T) {
+    if (T < 1) return fail(LF_ERR_INVALID_ARG, "T must be >= 1 (got %d)", T);
+    if (T > kMaxRows) return fail(LF_ERR_UNSUPPORTED, "T = %d exceeds %d", T, kMaxRows);
+    return LF_OK;
+}
+
+struct RopeArgs {
+    const void* qkv;
+    int64_t stride;
+    const void *wq, *wk;
+    const float* freq;
+    int rot, interleaved;
+    float eps;
+    void *q_out, *k_out, *v_out;
+    size_t kv_bytes;  // of k_out (and v_out)
+};
+
+lf_status check_rope(const RopeArgs& a, int T, const Shape& s) {
+    lf_status st;
+    if ((st = check_ptr(a.qkv, 16, "qkv")) != LF_OK) return st;
+    if ((st = check_ptr(a.freq, 4, "inv_freq")) != LF_OK) return st;
+    if ((st = check_ptr(a.q_out, 16, "q_out")) != LF_OK) return st;
+    if ((st = check_ptr(a.k_out, 16, "k_out")) != LF_OK) return st;
+    if ((st = check_ptr(a.v_out, 16, "v_out")) != LF_OK) return st;
+    if ((a.wq == nullptr) != (a.wk == nullptr))
+        return fail(LF_ERR_INVALID_ARG, "q_weight and k_weight must both be given or both be NULL");
+    if (a.wq && (!aligned(a.wq, 16) || !aligned(a.wk, 16)))
+        return fail(LF_ERR_INVALID_ARG, "a norm weight is not 16-byte aligned");
+    if ((st = check_rows(T)) != LF_OK) return st;
+    if ((st = check_shape(s)) != LF_OK) return st;
+    const int64_t width = (static_cast<int64_t>(s.Hq) + 2 * s.Hkv) * s.d;
+    if (a.stride < width || a.stride % 8 != 0)
+        return fail(LF_ERR_INVALID_ARG, "qkv_stride %lld must be a multiple of 8 and at least %lld",
+                    static_cast<long long>(a.stride), static_cast<long long>(width));
+    if (static_cast<int64_t>(T) * (s.Hq + 2 * s.Hkv) > (int64_t(1) << 30))
+        return fail(LF_ERR_UNSUPPORTED, "T * (Hq + 2 Hkv) exceeds 2^30");
+    if (a.rot < 16 || a.rot > s.d || a.rot % 16 != 0)
+        return fail(LF_ERR_INVALID_ARG, "rot = %d must be a multiple of 16 in [16, d]", a.rot);
+    if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return fail(LF_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    const size_t in = (static_cast<size_t>(T - 1) * a.stride + width) * 2;
+    const size_t qb = static_cast<size_t>(T) * s.Hq * s.d * 2;
+    if (overlaps(a.qkv, in, a.q_out, qb) || overlaps(a.qkv, in, a.k_out, a.kv_bytes) ||
+        overlaps(a.qkv, in, a.v_out, a.kv_bytes) || overlaps(a.q_out, qb, a.k_out, a.kv_bytes) ||
+        overlaps(a.q_out, qb, a.v_out, a.kv_bytes) || overlaps(a.k_out, a.kv_bytes, a.v_out, a.kv_bytes))
+        return fail(LF_ERR_INVALID_ARG, "qkv and the outputs overlap");
+    return LF_OK;
+}
+
+lf_status run_rope(const RopeArgs& a, lf::RopeParams rp, const Shape& s, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    lf_status st = static_err_word(dev, &rp.dev_err);
+    if (st != LF_OK) return st;
+    rp.qkv = static_cast<const __nv_bfloat16*>(a.qkv);
+    rp.stride = a.stride;
+    rp.q_weight = static_cast<const __nv_bfloat16*>(a.wq);
+    rp.k_weight = static_cast<const __nv_bfloat16*>(a.wk);
+    rp.inv_freq = a.freq;
+    rp.q_out = static_cast<__nv_bfloat16*>(a.q_out);
+    rp.k_out = static_cast<__nv_bfloat16*>(a.k_out);
+    rp.v_out = static_cast<__nv_bfloat16*>(a.v_out);
+    rp.Hq = s.Hq;
+    rp.Hkv = s.Hkv;
+    rp.S = s.S;
+    rp.rot = a.rot;
+    rp.interleaved = a.interleaved != 0;
+    rp.eps = a.eps;
+    g_last_error[0] = '\0';
+    ProfScope prof(LF_KERNEL_NORM_ROPE, stream);
+    if ((e = lf::launch_rope(s.d, rp, sm_count(dev), stream)) != cudaSuccess)
+        return cuda_fail(e, "norm-and-rotation launch");
+    return LF_OK;
+}
+
+// What attention a call asks for, and the workspace it takes.
+lf_status check_window(int T, const Shape& s, int window, int sinks) {
+    lf_status st;
+    if ((st = check_rows(T)) != LF_OK) return st;
+    if ((st = check_shape(s)) != LF_OK) return st;
+    if (window < 0 || window > kMaxPosWindow || sinks < 0 || sinks > kMaxPosWindow)
+        return fail(LF_ERR_INVALID_ARG, "window and sinks must be in [0, 2^30] (got %d, %d)", window, sinks);
+    return LF_OK;
+}
+
+size_t piece_bytes(int pieces, size_t rows, int d) {
+    return align_up(pieces * rows * sizeof(float2), 256) + pieces * rows * d * sizeof(float);
+}
+
+lf_status window_pieces(int T, const Shape& s, int window, int sinks, int* pieces) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    *pieces = lf::attention_pieces(T, s.B, s.Hq, s.Hkv, s.S, true, window, sinks, sm_count(dev));
+    return LF_OK;
+}
+
+struct PrefixShape {
+    int N, P;
+};
+
+lf_status check_prefix_shape(const Shape& s, const PrefixShape& x) {
+    lf_status st = check_shape(s);
+    if (st != LF_OK) return st;
+    if (x.N < 1 || x.P < 1)
+        return fail(LF_ERR_INVALID_ARG, "sizes must be >= 1 (N=%d P=%d)", x.N, x.P);
+    if (x.P > kMaxS) return fail(LF_ERR_UNSUPPORTED, "P = %d exceeds %d", x.P, kMaxS);
+    if (static_cast<long>(x.N) * s.Hkv > 65535)
+        return fail(LF_ERR_UNSUPPORTED, "N * Hkv = %ld exceeds 65535", static_cast<long>(x.N) * s.Hkv);
+    return LF_OK;
+}
+
+// Workspace of a step with shared prefixes: the counters and the pieces'
+// (m, l), both zeroed by every call, then the step's scratch and the pieces'
+// outputs.
+struct PrefixLayout {
+    Plan pl;
+    Layout step;
+    int pieces;
+    size_t ml, zeroed, scratch, o, total;
+};
+
+lf_status prefix_layout(const Shape& s, const PrefixShape& x, bool score, PrefixLayout* out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const int units = s.B * s.Hkv;
+    const int sms = sm_count(dev);
+    PrefixLayout& L = *out;
+    // No cluster merge: the merge that joins the prefix is the last CTA's.
+    L.pl = plan_split(s.S, units, sms, false, s.d, s.Hq / s.Hkv, score);
+    L.pl.stages = 2;
+    plan_split_finish(&L.pl, s.S, units, sms, true);
+    L.step = scratch_layout(s, L.pl, 0);
+    L.pieces = lf::attention_pieces(s.B, x.N, s.Hq, s.Hkv, x.P, false, 0, 0, sms);
+    const size_t rows = static_cast<size_t>(s.B) * s.Hq;
+    L.ml = align_up(lf::kCounterWordsPerUnit * static_cast<size_t>(units) * sizeof(uint32_t), 256);
+    L.zeroed = L.ml + L.pieces * rows * sizeof(float2);
+    L.scratch = align_up(L.zeroed, 256);
+    L.o = align_up(L.scratch + L.step.total, 256);
+    L.total = L.o + L.pieces * rows * s.d * sizeof(float);
+    return LF_OK;
+}
+
+lf_status run_prefix(StepArgs a, const Shape& s, const void* k_prefix, const void* v_prefix,
+                     const int32_t* prefix_start, const int32_t* prefix_len, const PrefixShape& x,
+                     void* workspace, size_t workspace_bytes, void* stream_v) {
+    lf_status st = check_args(a, s);
+    if (st != LF_OK) return st;
+    if ((st = check_ptr(k_prefix, 16, "k_prefix")) != LF_OK) return st;
+    if ((st = check_ptr(v_prefix, 16, "v_prefix")) != LF_OK) return st;
+    if ((st = check_ptr(prefix_start, 4, "prefix_start")) != LF_OK) return st;
+    if ((st = check_ptr(prefix_len, 4, "prefix_len")) != LF_OK) return st;
+    if ((st = check_ptr(workspace, 256, "workspace")) != LF_OK) return st;
+    if ((st = check_prefix_shape(s, x)) != LF_OK) return st;
+    const size_t own = static_cast<size_t>(s.B) * s.Hkv * s.S * s.d * 2;
+    const size_t pre = static_cast<size_t>(x.N) * s.Hkv * x.P * s.d * 2;
+    const size_t qb = static_cast<size_t>(s.B) * s.Hq * s.d * 2;
+    if (overlaps(a.q, qb, a.out, qb) || overlaps(k_prefix, pre, a.k_cache, own) ||
+        overlaps(v_prefix, pre, a.v_cache, own))
+        return fail(LF_ERR_INVALID_ARG, "out overlaps q, or a prefix the cache");
+    PrefixLayout L;
+    if ((st = prefix_layout(s, x, a.score, &L)) != LF_OK) return st;
+    if (workspace_bytes < L.total)
+        return fail(LF_ERR_INVALID_ARG, "workspace of %zu bytes; this call needs %zu", workspace_bytes, L.total);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    uint32_t* err = nullptr;
+    if ((st = static_err_word(dev, &err)) != LF_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    lf::AttnParams ap = {};
+    ap.q = static_cast<const __nv_bfloat16*>(a.q);
+    ap.k = static_cast<const __nv_bfloat16*>(k_prefix);
+    ap.v = static_cast<const __nv_bfloat16*>(v_prefix);
+    ap.q_start = prefix_start;
+    ap.kv_len = prefix_len;
+    ap.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+    ap.part_o = reinterpret_cast<float*>(ws + L.o);
+    ap.dev_err = err;
+    ap.T = s.B;
+    ap.N = x.N;
+    ap.Hq = s.Hq;
+    ap.Hkv = s.Hkv;
+    ap.S = x.P;
+    ap.causal = false;
+    ap.pieces = L.pieces;
+    ap.scale_log2 = static_cast<float>(static_cast<double>(s.scale) * 1.4426950408889634);
+    a.pre_ml = ap.part_ml;
+    a.pre_o = ap.part_o;
+    a.pre_pieces = L.pieces;
+    Launch r;
+    if ((st = build_launch(a, s, ws + L.scratch, reinterpret_cast<uint32_t*>(ws), err, L.step, L.pl,
+                           &r)) != LF_OK)
+        return st;
+    g_last_error[0] = '\0';
+    if ((e = cudaMemsetAsync(ws, 0, L.zeroed, stream)) != cudaSuccess)
+        return cuda_fail(e, "cudaMemsetAsync(workspace)");
+    {
+        ProfScope prof(LF_KERNEL_PACKED_ATTENTION, stream);
+        if ((e = lf::launch_attention(s.d, s.Hq / s.Hkv, ap, stream)) != cudaSuccess)
+            return cuda_fail(e, "prefix-attention launch");
+    }
+    return launch(r, stream);
 }
 
 }  // namespace
@@ -835,6 +1086,159 @@ lf_status lf_decode_step_noalloc(const void* q, void* k_cache, void* v_cache, in
         return st;
     g_last_error[0] = '\0';
     return launch(r, stream);
+}
+
+lf_status lf_qk_norm_rope(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                          const void* k_weight, const float* inv_freq, const int32_t* positions,
+                          void* q_out, void* k_out, void* v_out, int T, int Hq, int Hkv, int d,
+                          int rot, int interleaved, float eps, void* stream) {
+    const Shape s{1, Hq, Hkv, d, 1, 0, 1.f};
+    lf_status st;
+    if ((st = check_ptr(positions, 4, "positions")) != LF_OK) return st;
+    const size_t kv = (T > 0 && Hkv > 0 && d > 0) ? static_cast<size_t>(T) * Hkv * d * 2 : 0;
+    const RopeArgs a{qkv, qkv_stride, q_weight, k_weight, inv_freq, rot, interleaved, eps,
+                     q_out, k_out, v_out, kv};
+    if ((st = check_rope(a, T, s)) != LF_OK) return st;
+    lf::RopeParams rp = {};
+    rp.positions = positions;
+    rp.T = T;
+    rp.B = 1;
+    return run_rope(a, rp, s, static_cast<cudaStream_t>(stream));
+}
+
+lf_status lf_prefill_append(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                            const void* k_weight, const float* inv_freq, const int32_t* q_start,
+                            const int32_t* kv_len, const int32_t* pos_offset, void* q_out,
+                            void* k_cache, void* v_cache, int32_t* mask, int T, int B, int Hq,
+                            int Hkv, int d, int S, int rot, int interleaved, float eps,
+                            void* stream) {
+    const Shape s{B, Hq, Hkv, d, S, 0, 1.f};
+    lf_status st;
+    if ((st = check_ptr(q_start, 4, "q_start")) != LF_OK) return st;
+    if ((st = check_ptr(kv_len, 4, "kv_len")) != LF_OK) return st;
+    if ((st = check_ptr(mask, 4, "mask")) != LF_OK) return st;
+    if (pos_offset && !aligned(pos_offset, 4)) return fail(LF_ERR_INVALID_ARG, "pos_offset is not 4-byte aligned");
+    if ((st = check_shape(s)) != LF_OK) return st;
+    const RopeArgs a{qkv, qkv_stride, q_weight, k_weight, inv_freq, rot, interleaved, eps,
+                     q_out, k_cache, v_cache, static_cast<size_t>(B) * Hkv * S * d * 2};
+    if ((st = check_rope(a, T, s)) != LF_OK) return st;
+    lf::RopeParams rp = {};
+    rp.q_start = q_start;
+    rp.kv_len = kv_len;
+    rp.pos_offset = pos_offset;
+    rp.mask = mask;
+    rp.T = T;
+    rp.B = B;
+    return run_rope(a, rp, s, static_cast<cudaStream_t>(stream));
+}
+
+lf_status lf_window_attention_workspace(int T, int B, int Hq, int Hkv, int d, int S, int window,
+                                        int sinks, size_t* bytes) {
+    if (!bytes) return fail(LF_ERR_INVALID_ARG, "bytes is NULL");
+    const Shape s{B, Hq, Hkv, d, S, 0, 1.f};
+    lf_status st = check_window(T, s, window, sinks);
+    if (st != LF_OK) return st;
+    int pieces = 0;
+    if ((st = window_pieces(T, s, window, sinks, &pieces)) != LF_OK) return st;
+    *bytes = piece_bytes(pieces, static_cast<size_t>(T) * Hq, d);
+    return LF_OK;
+}
+
+lf_status lf_window_attention(const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* q_start, const int32_t* kv_len, void* out, int T,
+                              int B, int Hq, int Hkv, int d, int S, int window, int sinks,
+                              float scale, void* workspace, size_t workspace_bytes,
+                              void* stream_v) {
+    lf_status st;
+    if ((st = check_ptr(q, 16, "q")) != LF_OK) return st;
+    if ((st = check_ptr(k_cache, 16, "k_cache")) != LF_OK) return st;
+    if ((st = check_ptr(v_cache, 16, "v_cache")) != LF_OK) return st;
+    if ((st = check_ptr(q_start, 4, "q_start")) != LF_OK) return st;
+    if ((st = check_ptr(kv_len, 4, "kv_len")) != LF_OK) return st;
+    if ((st = check_ptr(out, 16, "out")) != LF_OK) return st;
+    const Shape s{B, Hq, Hkv, d, S, 0, scale};
+    if ((st = check_window(T, s, window, sinks)) != LF_OK) return st;
+    const size_t rows = static_cast<size_t>(T) * Hq;
+    if (overlaps(q, rows * d * 2, out, rows * d * 2))
+        return fail(LF_ERR_INVALID_ARG, "out overlaps q");
+    int pieces = 0;
+    if ((st = window_pieces(T, s, window, sinks, &pieces)) != LF_OK) return st;
+    const size_t need = piece_bytes(pieces, rows, d);
+    if (need > 0) {
+        if ((st = check_ptr(workspace, 256, "workspace")) != LF_OK) return st;
+        if (workspace_bytes < need)
+            return fail(LF_ERR_INVALID_ARG, "workspace of %zu bytes; this call needs %zu", workspace_bytes, need);
+    }
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    lf::AttnParams ap = {};
+    if ((st = static_err_word(dev, &ap.dev_err)) != LF_OK) return st;
+    ap.q = static_cast<const __nv_bfloat16*>(q);
+    ap.k = static_cast<const __nv_bfloat16*>(k_cache);
+    ap.v = static_cast<const __nv_bfloat16*>(v_cache);
+    ap.q_start = q_start;
+    ap.kv_len = kv_len;
+    ap.out = static_cast<__nv_bfloat16*>(out);
+    ap.part_ml = static_cast<float2*>(workspace);
+    ap.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                         align_up(pieces * rows * sizeof(float2), 256));
+    ap.T = T;
+    ap.N = B;
+    ap.Hq = Hq;
+    ap.Hkv = Hkv;
+    ap.S = S;
+    ap.window = window;
+    ap.sinks = sinks;
+    ap.causal = true;
+    ap.pieces = pieces;
+    ap.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    g_last_error[0] = '\0';
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    ProfScope prof(LF_KERNEL_PACKED_ATTENTION, stream);
+    if ((e = lf::launch_attention(d, Hq / Hkv, ap, stream)) != cudaSuccess)
+        return cuda_fail(e, "window-attention launch");
+    return LF_OK;
+}
+
+lf_status lf_decode_prefix_workspace(int B, int Hq, int Hkv, int d, int S, int N, int P,
+                                     size_t* bytes) {
+    if (!bytes) return fail(LF_ERR_INVALID_ARG, "bytes is NULL");
+    const Shape s{B, Hq, Hkv, d, S, 0, 1.f};
+    const PrefixShape x{N, P};
+    lf_status st = check_prefix_shape(s, x);
+    if (st != LF_OK) return st;
+    PrefixLayout L;
+    if ((st = prefix_layout(s, x, true, &L)) != LF_OK) return st;
+    *bytes = L.total;
+    return LF_OK;
+}
+
+lf_status lf_decode_step_prefix(const void* q, void* k_cache, void* v_cache, int32_t* mask,
+                                const void* new_k, const void* new_v, const int32_t* write_slot,
+                                const void* k_prefix, const void* v_prefix,
+                                const int32_t* prefix_start, const int32_t* prefix_len, void* out,
+                                int32_t* next_slots, int k, int flags, float* scores, int B,
+                                int Hq, int Hkv, int d, int S, int N, int P, int W, float scale,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    StepArgs a{q, k_cache, v_cache, mask, new_k, new_v, write_slot, out, next_slots, scores};
+    a.topk = k;
+    a.flags = flags;
+    return run_prefix(a, Shape{B, Hq, Hkv, d, S, W, scale}, k_prefix, v_prefix, prefix_start,
+                      prefix_len, PrefixShape{N, P}, workspace, workspace_bytes, stream);
+}
+
+lf_status lf_decode_attention_prefix(const void* q, void* k_cache, void* v_cache, int32_t* mask,
+                                     const void* new_k, const void* new_v,
+                                     const int32_t* write_slot, const void* k_prefix,
+                                     const void* v_prefix, const int32_t* prefix_start,
+                                     const int32_t* prefix_len, void* out, int B, int Hq, int Hkv,
+                                     int d, int S, int N, int P, float scale, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    StepArgs a{q, k_cache, v_cache, mask, new_k, new_v, write_slot, out, nullptr, nullptr};
+    a.score = false;
+    return run_prefix(a, Shape{B, Hq, Hkv, d, S, 0, scale}, k_prefix, v_prefix, prefix_start,
+                      prefix_len, PrefixShape{N, P}, workspace, workspace_bytes, stream);
 }
 
 lf_status lf_step_plan(int B, int Hq, int Hkv, int d, int S, int topk, int32_t* plan) {

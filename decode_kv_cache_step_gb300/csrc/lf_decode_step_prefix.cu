@@ -1,0 +1,31 @@
+// Instantiations of the decode-step kernel whose merge joins a shared-prefix
+// attention: the unit's slots and the prefix share one softmax, so the output
+// and LongFlowScore's weights are normalised over both.
+#include "lf_step_kernel.cuh"
+
+namespace lf {
+namespace {
+
+template <int D, int G>
+cudaError_t launch_dg(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepParams& p,
+                      int units, cudaStream_t stream, bool score, bool pdl) {
+    return score ? launch_t<D, G, 2, true, false, true>(tmK, tmV, p, units, stream, pdl)
+                 : launch_t<D, G, 2, false, false, true>(tmK, tmV, p, units, stream, pdl);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_step_prefix(int D, int G, bool score, const CUtensorMap& tmK,
+                                      const CUtensorMap& tmV, const StepParams& p, int units,
+                                      cudaStream_t stream) {
+    const char* env = std::getenv("LF_PDL");
+    const bool pdl = !(env && std::atoi(env) == 0);
+#define LF_STEP_CASE(DD, GG) \
+    if (D == DD && G == GG) return launch_dg<DD, GG>(tmK, tmV, p, units, stream, score, pdl);
+    LF_STEP_CASE(64, 1) LF_STEP_CASE(64, 2) LF_STEP_CASE(64, 4) LF_STEP_CASE(64, 8)
+    LF_STEP_CASE(128, 1) LF_STEP_CASE(128, 2) LF_STEP_CASE(128, 4) LF_STEP_CASE(128, 8)
+#undef LF_STEP_CASE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace lf

@@ -59,6 +59,12 @@ struct StepParams {
     // before the mask tells which tiles hold a live slot (the grid's first
     // wave; set by the launch).
     int spec_ctas = 0;
+    // Shared-prefix attention joined in the merge (kPrefix instances): per
+    // piece of the prefix keys and query row b * Hq + h, the softmax (m, l)
+    // in the log2 domain (l = 0: no key) and the unnormalised output, base m.
+    const float2* pre_ml = nullptr;  // [pre_pieces][B * Hq]
+    const float* pre_o = nullptr;    // [pre_pieces][B * Hq][D]
+    int pre_pieces = 0;
 };
 
 constexpr int kFlagFillEmptyFirst = 1;  // empty (masked) slots are returned before any score
@@ -97,6 +103,12 @@ cudaError_t launch_decode_step_cluster(int D, int G, int stages, bool score,
                                        const StepParams& p, int units, cudaStream_t stream,
                                        bool pdl);
 
+// The step with the prefix pieces of p.pre_* in its merge
+// (lf_decode_step_prefix.cu): last-CTA merge, 2-stage ring.
+cudaError_t launch_decode_step_prefix(int D, int G, bool score, const CUtensorMap& tmK,
+                                      const CUtensorMap& tmV, const StepParams& p, int units,
+                                      cudaStream_t stream);
+
 // How many clusters of csize CTAs (one unit each) of the cluster instance
 // (stages 2 or kDeepStages) can be resident at once on the current device;
 // 0 if none can or the query fails. Cached per device and instance.
@@ -111,6 +123,97 @@ int deep_term_slots(int D, int G);
 // terms and c_h, and the unit's last CTA writes next_slot (and masks it with
 // kFlagMaskEvicted). It does not wait for the decode-step grid as a whole.
 cudaError_t launch_score(int G, const StepParams& p, int units, cudaStream_t stream);
+
+// Norm and rotation of query and key heads (lf_rope.cu). Row t of qkv holds
+// Hq query, Hkv key and Hkv value heads of D. Without q_start, row t has
+// position positions[t] and goes to row t of the outputs. With q_start
+// (prompt rows into a cache), the rows q_start[b] .. q_start[b + 1] are the
+// last tokens of sequence b's kv_len[b] tokens: token i of the sequence has
+// position i (+ pos_offset[b]) and slot i, and mask gets the tokens' ages.
+struct RopeParams {
+    const __nv_bfloat16* qkv;
+    int64_t stride;                 // elements between rows
+    const __nv_bfloat16* q_weight;  // [D] or nullptr: no norm
+    const __nv_bfloat16* k_weight;
+    const float* inv_freq;          // [rot / 2]
+    const int32_t* positions;       // [T]
+    const int32_t* q_start;         // [B + 1] or nullptr
+    const int32_t* kv_len;          // [B]
+    const int32_t* pos_offset;      // [B] or nullptr
+    __nv_bfloat16* q_out;           // [T][Hq][D]
+    __nv_bfloat16* k_out;           // [T][Hkv][D], or the cache [B][Hkv][S][D]
+    __nv_bfloat16* v_out;
+    int32_t* mask;                  // [B][Hkv][S]
+    uint32_t* dev_err;
+    int T, B, Hq, Hkv, S, rot;
+    bool interleaved;
+    float eps;
+};
+cudaError_t launch_rope(int D, const RopeParams& p, int sms, cudaStream_t stream);
+
+// Attention of packed query rows over in-order caches (lf_attn.cu). Rows
+// q_start[n] .. q_start[n + 1] of q belong to sequence n, whose cache holds
+// kv_len[n] tokens. causal: they are the sequence's last tokens, and the
+// token at position i sees key j iff j <= i and (window == 0 or
+// i - j < window or j < sinks). Otherwise every row sees all kv_len[n] keys.
+struct AttnParams {
+    const __nv_bfloat16* q;      // [T][Hq][D]
+    const __nv_bfloat16* k;      // [N][Hkv][S][D]
+    const __nv_bfloat16* v;
+    const int32_t* q_start;      // [N + 1]
+    const int32_t* kv_len;       // [N]
+    __nv_bfloat16* out;          // [T][Hq][D] (pieces == 0: written directly)
+    float2* part_ml;             // [pieces][T * Hq]
+    float* part_o;               // [pieces][T * Hq][D]
+    uint32_t* dev_err;
+    int T, N, Hq, Hkv, S;
+    int window, sinks;
+    bool causal;
+    int pieces;
+    float scale_log2;            // scale * log2(e)
+};
+// Pieces of the key axis such a call writes (0: the output directly), a rule
+// on its sizes alone. The plan for the prefix (causal false) has at least one.
+int attention_pieces(int T, int N, int Hq, int Hkv, int S, bool causal, int window, int sinks,
+                     int sms);
+cudaError_t launch_attention(int D, int G, const AttnParams& p, cudaStream_t stream);
+
+// Error bit of lengths that do not fit (LF_DEVERR_BAD_LENGTH).
+constexpr uint32_t kErrBadLength = 0x4u;
+
+// Range of sequence n in packed rows and its cache length; false (and the
+// error bit) when they do not fit: the sequence is then skipped.
+struct SeqRange {
+    int q0, n, kv;
+};
+__device__ __forceinline__ bool seq_range(const int32_t* q_start, const int32_t* kv_len, int b,
+                                          int T, int S, bool causal, uint32_t* dev_err,
+                                          SeqRange* r) {
+    const int q0 = q_start[b];
+    const int q1 = q_start[b + 1];
+    const int kv = kv_len[b];
+    r->q0 = q0;
+    r->n = q1 - q0;
+    r->kv = kv;
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= T && kv >= 0 && kv <= S &&
+                    (!causal || q1 - q0 <= kv);
+    if (!ok) atomicOr(dev_err, kErrBadLength);
+    return ok;
+}
+
+// The sequence of packed row t: the last b with q_start[b] <= t (0 if none;
+// the caller checks its range).
+__device__ __forceinline__ int seq_of_row(const int32_t* q_start, int B, int t) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (q_start[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
 
 
 }  // namespace lf

@@ -446,9 +446,31 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
                                  uint8_t* topk_area, uint8_t* scan_area, int scan_bytes,
                                  uint64_t* scan_bars, int tid);
 
+// Running maximum and sum of a query row's shared-prefix pieces (log2 domain).
+__device__ __forceinline__ float prefix_max(const StepParams& p, size_t row, size_t rows, float m) {
+    for (int c = 0; c < p.pre_pieces; ++c) {
+        const float2 v = __ldcg(&p.pre_ml[c * rows + row]);
+        if (v.y != 0.f) m = fmaxf(m, v.x);
+    }
+    return m;
+}
+
+__device__ __forceinline__ float prefix_sum(const StepParams& p, size_t row, size_t rows, float m) {
+    float l = 0.f;
+    for (int c = 0; c < p.pre_pieces; ++c) {
+        const float2 v = __ldcg(&p.pre_ml[c * rows + row]);
+        if (v.y != 0.f) l += v.y * exp2f(v.x - m);
+    }
+    return l;
+}
+
 // Merge of the unit's chunks by its last CTA (consumer threads only). The
 // shared memory below `usable` is free; scan_bars are two spare mbarriers.
-template <int D, int G, bool kScore>
+// kPrefix: the pieces of the unit's shared-prefix attention (pre_ml, pre_o of
+// the unit's sequence and heads) join the chunks in the softmax, so m_h, l_h,
+// the output and the scores' normalisation cover the prefix and the slots. A
+// piece with l = 0 holds no key and its output is not read.
+template <int D, int G, bool kScore, bool kPrefix>
 __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usable,
                             uint64_t* scan_bars, int tid) {
     const int nchunk = p.nchunk;
@@ -461,15 +483,20 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
     // [nchunk]: the chunk's live-tile bit mask (0: no live slot; all ones
     // when the masks were not kept)
     int* s_live = s_ncand + 4;
+    // kPrefix, [pieces][G]: 2^(m_piece - m) / l
+    float* s_wp = reinterpret_cast<float*>(s_live + nchunk);
     uint8_t* topk_area = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(s_live + nchunk) + 15) & ~static_cast<uintptr_t>(15));
+        (reinterpret_cast<uintptr_t>(s_wp + (kPrefix ? p.pre_pieces * G : 0)) + 15) &
+        ~static_cast<uintptr_t>(15));
     uint8_t* scan_area = topk_area + (p.topk > 1 ? kTopKAreaBytes : 0);
     const int scan_bytes = usable - static_cast<int>(scan_area - smem);
     const float2* ml = p.part_ml + static_cast<size_t>(u) * nchunk * G;
     const int b = u / p.Hkv;
     const int kvh = u - b * p.Hkv;
     const float* po = p.part_o + static_cast<size_t>(u) * nchunk * G * D;
-    __nv_bfloat16* out = p.out + (static_cast<size_t>(b) * p.Hq + kvh * G) * D;
+    const size_t row0 = static_cast<size_t>(b) * p.Hq + kvh * G;  // the unit's first query row
+    __nv_bfloat16* out = p.out + row0 * D;
+    const size_t pre_rows = kPrefix ? static_cast<size_t>(gridDim.y) / p.Hkv * p.Hq : 0;  // B * Hq
 
     // The partial outputs of the first four chunks are requested first: they
     // do not depend on (m, l), so their round trip overlaps the weights'.
@@ -507,10 +534,12 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
 #pragma unroll
             for (int c = 0; c < kFastChunks; ++c)
                 if (c < nchunk) m = fmaxf(m, mlv[c].x);
+            if constexpr (kPrefix) m = prefix_max(p, row0 + tid, pre_rows, m);
             float l = 0.f;
 #pragma unroll
             for (int c = 0; c < kFastChunks; ++c)
                 if (c < nchunk && mlv[c].x != -INFINITY) l += mlv[c].y * exp2f(mlv[c].x - m);
+            if constexpr (kPrefix) l += prefix_sum(p, row0 + tid, pre_rows, m);
             const float il = (l > 0.f) ? 1.f / l : 0.f;
             s_m[tid] = m;
             s_il[tid] = il;
@@ -525,13 +554,21 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
         } else {
             float m = -INFINITY;
             for (int c = 0; c < nchunk; ++c) m = fmaxf(m, __ldcg(&ml[c * G + tid]).x);
+            if constexpr (kPrefix) m = prefix_max(p, row0 + tid, pre_rows, m);
             float l = 0.f;
             for (int c = 0; c < nchunk; ++c) {
                 const float2 v = __ldcg(&ml[c * G + tid]);
                 if (v.x != -INFINITY) l += v.y * exp2f(v.x - m);
             }
+            if constexpr (kPrefix) l += prefix_sum(p, row0 + tid, pre_rows, m);
             s_m[tid] = m;
             s_il[tid] = (l > 0.f) ? 1.f / l : 0.f;
+        }
+        if constexpr (kPrefix) {
+            for (int c = 0; c < p.pre_pieces; ++c) {
+                const float2 v = __ldcg(&p.pre_ml[c * pre_rows + row0 + tid]);
+                s_wp[c * G + tid] = v.y == 0.f ? 0.f : exp2f(v.x - s_m[tid]) * s_il[tid];
+            }
         }
     }
     if (kScore && ptl) {
@@ -558,6 +595,34 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
     float o[kPerT];
 #pragma unroll
     for (int k = 0; k < kPerT; ++k) o[k] = 0.f;
+    if constexpr (kPrefix) {
+        // Four pieces' loads in flight at a time; the row's address is in
+        // bounds for every piece, and a piece without a key is selected away.
+        for (int c0 = 0; c0 < p.pre_pieces; c0 += 4) {
+            float v[4][kPerT];
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+                const int c = min(c0 + cc, p.pre_pieces - 1);
+#pragma unroll
+                for (int k = 0; k < kPerT; ++k) {
+                    const int e = tid + k * kConsumers;
+                    v[cc][k] =
+                        (e < G * D) ? __ldcg(&p.pre_o[(c * pre_rows + row0) * D + e]) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+                const int c = c0 + cc;
+                if (c >= p.pre_pieces) break;
+#pragma unroll
+                for (int k = 0; k < kPerT; ++k) {
+                    const int e = tid + k * kConsumers;
+                    const float w = (e < G * D) ? s_wp[c * G + e / D] : 0.f;
+                    o[k] += (w != 0.f) ? w * v[cc][k] : 0.f;
+                }
+            }
+        }
+    }
     for (int c0 = 0; c0 < nchunk; c0 += 4) {
         float v[4][kPerT];
         if (c0 == 0) {
@@ -1309,7 +1374,9 @@ __device__ __forceinline__ void push_barriers_init(uint8_t* pbase, int nchunk) {
 // kStages-deep TMA ring; 3 stages run 2 CTAs per SM, 2 stages run 3.
 // kScore = false is the attention-only variant (no ageing, score or eviction).
 // kCluster: the grid is launched in clusters of nchunk CTAs (one per unit).
-template <int D, int G, int kStages, bool kScore, bool kCluster>
+// kPrefix: the merge adds the pieces of a shared-prefix attention (StepParams
+// pre_*), computed by the kernel before this one; not with kCluster.
+template <int D, int G, int kStages, bool kScore, bool kCluster, bool kPrefix = false>
 __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2 : 1))
     lf_decode_step_kernel(const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const StepParams p) {
@@ -1800,16 +1867,16 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
     }
     consumer_bar_sync();
     if (!misc[2]) return;
-    finish_unit<D, G, kScore>(p, u, smem, L::kBarOff,
+    finish_unit<D, G, kScore, kPrefix>(p, u, smem, L::kBarOff,
                               reinterpret_cast<uint64_t*>(smem + L::kScanBarOff), tid);
 }
 
 // Sets the kernel's function attributes (shared memory above 48 KB; cluster
 // instances: clusters of more than 8 CTAs, an opt-in size) once per device.
-template <int D, int G, int kStages, bool kScore, bool kCluster>
+template <int D, int G, int kStages, bool kScore, bool kCluster, bool kPrefix = false>
 cudaError_t configure_t() {
     using A = StepAlloc<D, G, kStages, kCluster>;
-    auto kernel = lf_decode_step_kernel<D, G, kStages, kScore, kCluster>;
+    auto kernel = lf_decode_step_kernel<D, G, kStages, kScore, kCluster, kPrefix>;
     static int configured_for = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1853,7 +1920,7 @@ int max_active_clusters_t(int csize) {
 
 // How many CTAs of the (non-cluster) instance are resident at once on the
 // current device: the grid's first wave. Cached per device.
-template <int D, int G, int kStages, bool kScore>
+template <int D, int G, int kStages, bool kScore, bool kPrefix = false>
 int first_wave_t() {
     static int cached_for = -1;
     static int ctas = 0;
@@ -1862,7 +1929,7 @@ int first_wave_t() {
     if (cached_for != dev) {
         int per_sm = 0, sms = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &per_sm, lf_decode_step_kernel<D, G, kStages, kScore, false>, kThreads,
+                &per_sm, lf_decode_step_kernel<D, G, kStages, kScore, false, kPrefix>, kThreads,
                 StepAlloc<D, G, kStages, false>::kAlloc) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
             (void)cudaGetLastError();
@@ -1874,14 +1941,17 @@ int first_wave_t() {
     return ctas;
 }
 
-template <int D, int G, int kStages, bool kScore, bool kCluster>
+template <int D, int G, int kStages, bool kScore, bool kCluster, bool kPrefix = false>
 cudaError_t launch_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepParams& p_in,
                      int units, cudaStream_t stream, bool pdl) {
     using L = StepSmem<D, kStages>;
-    if (finish_smem_bytes(p_in.nchunk, G, kScore ? p_in.topk : 1) > static_cast<size_t>(L::kBarOff))
+    static_assert(!(kCluster && kPrefix), "the cluster merge takes no prefix pieces");
+    if (finish_smem_bytes(p_in.nchunk, G, kScore ? p_in.topk : 1) +
+            (kPrefix ? static_cast<size_t>(p_in.pre_pieces) * G * 4 : 0) >
+        static_cast<size_t>(L::kBarOff))
         return cudaErrorInvalidConfiguration;
-    auto kernel = lf_decode_step_kernel<D, G, kStages, kScore, kCluster>;
-    cudaError_t e = configure_t<D, G, kStages, kScore, kCluster>();
+    auto kernel = lf_decode_step_kernel<D, G, kStages, kScore, kCluster, kPrefix>;
+    cudaError_t e = configure_t<D, G, kStages, kScore, kCluster, kPrefix>();
     if (e != cudaSuccess) return e;
     // Speculative first tiles in the first wave (LF_SPEC=0: off; cluster
     // grids, one wave by construction, always speculate).
@@ -1891,7 +1961,7 @@ cudaError_t launch_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepP
     if constexpr (kCluster)
         p.spec_ctas = spec ? INT_MAX : 0;
     else
-        p.spec_ctas = spec ? first_wave_t<D, G, kStages, kScore>() : 0;
+        p.spec_ctas = spec ? first_wave_t<D, G, kStages, kScore, kPrefix>() : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.nchunk, units);
     cfg.blockDim = dim3(kThreads);

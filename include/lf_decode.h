@@ -98,6 +98,7 @@ typedef enum lf_status {
 
 /* Bits of the device error word (lf_device_errors). */
 #define LF_DEVERR_BAD_WRITE_SLOT 0x1u /* a write_slot outside [-1, S) was ignored */
+#define LF_DEVERR_BAD_LENGTH 0x4u     /* a sequence whose row range or length does not fit was skipped */
 #define LF_DEVERR_WAIT_TIMEOUT 0x2u   /* a pipeline wait gave up; that step's results are invalid */
 
 /*
@@ -111,7 +112,9 @@ typedef enum lf_status {
 #define LF_KERNEL_DECODE_STEP 0 /* slot write, mask ageing, attention (+ score, eviction) */
 #define LF_KERNEL_ATTENTION 1   /* lf_decode_attention: slot write and attention only */
 #define LF_KERNEL_SCORE 2       /* split finish: LongFlowScore and eviction */
-#define LF_KERNEL_COUNT 3
+#define LF_KERNEL_NORM_ROPE 3        /* lf_qk_norm_rope, lf_prefill_append */
+#define LF_KERNEL_PACKED_ATTENTION 4 /* lf_window_attention; the prefix part of lf_decode_*_prefix */
+#define LF_KERNEL_COUNT 5
 
 /* Flags of lf_decode_step_ex. */
 #define LF_STEP_FILL_EMPTY_FIRST 0x1 /* return empty (masked) slots, lowest first, before any score */
@@ -302,6 +305,128 @@ lf_status lf_step_destroy(lf_step_handle* handle);
  * *flags receives an OR of LF_DEVERR_* bits, 0 if no step has set one.
  */
 lf_status lf_device_errors(void* stream, uint32_t* flags, int clear);
+
+/*
+ * Operators around the step: what brings a token to it, what fills the cache
+ * from a prompt, and one prompt shared by many sequences.
+ *
+ * They own no scratch. Calls that need any take a workspace of the caller
+ * (device memory, 256-byte aligned, at least the bytes the matching
+ * *_workspace function returns for the same sizes on the same device; its
+ * contents need not be kept between calls). Calls that may overlap on the
+ * GPU, and captured graphs that may be replayed at the same time, need
+ * workspaces of their own. The first call on a device looks up the library's
+ * error word: make it before any stream capture, as with
+ * lf_decode_step_noalloc, whose error word they share (lf_device_errors).
+ *
+ * Lengths that live on the device (q_start, kv_len, prefix_start, prefix_len)
+ * cannot be checked on the host. A sequence whose rows or length do not fit
+ * (q_start not ascending or outside [0, T], a length outside [0, S], more
+ * rows than tokens) is skipped and raises LF_DEVERR_BAD_LENGTH.
+ *
+ * lf_qk_norm_rope: head norms and rotation of single tokens.
+ *
+ * qkv        in  bf16 [T] rows of (Hq + 2 Hkv) heads of d (queries, keys,
+ *                values: a fused projection's output), qkv_stride elements
+ *                apart (a multiple of 8)
+ * q_weight,
+ * k_weight   in  bf16 [d] norm weights, or both NULL for no norm. A query or
+ *                key head becomes y = x * weight / sqrt(mean(x^2) + eps).
+ * inv_freq   in  float [rot / 2]: pair i of a token at position n turns by
+ *                n * inv_freq[i] (formed in fp64). rot is a multiple of 16 in
+ *                [16, d]; values from rot on stay as they are. The pairs are
+ *                (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved != 0.
+ * positions  in  int32 [T]
+ * q_out      out bf16 [T][Hq][d]
+ * k_out,
+ * v_out      out bf16 [T][Hkv][d]: with T = B, lf_decode_step's q, new_k and
+ *                new_v. Values are copied. The arithmetic is fp32, rounded
+ *                once. Inputs and outputs must not overlap.
+ */
+lf_status lf_qk_norm_rope(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                          const void* k_weight, const float* inv_freq, const int32_t* positions,
+                          void* q_out, void* k_out, void* v_out, int T, int Hq, int Hkv, int d,
+                          int rot, int interleaved, float eps, void* stream);
+
+/*
+ * The same for prompt tokens, their keys and values straight into the cache.
+ *
+ * q_start    in  int32 [B + 1]: rows q_start[b] .. q_start[b + 1] - 1 of qkv
+ *                are the last tokens of sequence b (possibly none)
+ * kv_len     in  int32 [B]: tokens of sequence b in its cache after the call,
+ *                earlier chunks included. Token i takes slot i, and position
+ *                i + pos_offset[b] (pos_offset NULL: 0), as after a shared
+ *                prefix of that length.
+ * mask       in/out int32 [B][Hkv][S]: slots below kv_len[b] get the ages of
+ *                an in-order cache (kv_len[b] - 1 - slot); the rest stays.
+ * Rows of q_out outside every sequence stay as they were. The caches are
+ * meant to hold a sequence's tokens in order: call this before the first
+ * step that overwrites a slot.
+ */
+lf_status lf_prefill_append(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                            const void* k_weight, const float* inv_freq, const int32_t* q_start,
+                            const int32_t* kv_len, const int32_t* pos_offset, void* q_out,
+                            void* k_cache, void* v_cache, int32_t* mask, int T, int B, int Hq,
+                            int Hkv, int d, int S, int rot, int interleaved, float eps,
+                            void* stream);
+
+/*
+ * Attention over in-order caches with a sliding window and visible first
+ * tokens: whole prompts, chunks of prompts and single tokens of a batch.
+ *
+ * q          in  bf16 [T][Hq][d]; q_start, kv_len as in lf_prefill_append
+ * k_cache,
+ * v_cache    in  bf16 [B][Hkv][S][d], tokens in slot order
+ * out        out bf16 [T][Hq][d]; rows outside every sequence stay as they
+ *                were; must not overlap q
+ * window, sinks  the token at position i sees key j iff j <= i and
+ *                (window == 0 or i - j < window or j < sinks)
+ * Slots from kv_len[b] on, and keys a row does not see, may hold anything
+ * (NaN and infinities included) without changing the row.
+ */
+lf_status lf_window_attention(const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* q_start, const int32_t* kv_len, void* out, int T,
+                              int B, int Hq, int Hkv, int d, int S, int window, int sinks,
+                              float scale, void* workspace, size_t workspace_bytes, void* stream);
+/* Workspace bytes of that call (may be 0: workspace may then be NULL). */
+lf_status lf_window_attention_workspace(int T, int B, int Hq, int Hkv, int d, int S, int window,
+                                        int sinks, size_t* bytes);
+
+/*
+ * The decode step for sequences that share long prefixes (samples of one
+ * prompt): a prefix's keys are attended once for all its sequences' queries,
+ * and joined with each sequence's own slots in one softmax.
+ *
+ * k_prefix,
+ * v_prefix     in bf16 [N][Hkv][P][d]: N prefixes (lf_prefill_append fills
+ *                 one as a batch of N), never written
+ * prefix_start in int32 [N + 1]: sequences prefix_start[n] ..
+ *                 prefix_start[n + 1] - 1 see prefix n; sequences outside
+ *                 every range see none
+ * prefix_len   in int32 [N]: tokens of prefix n (0 .. P)
+ * The other arguments are those of lf_decode_step_ex. LongFlowScore's weights
+ * p are normalised over prefix and slots; only slots are scored and returned.
+ * A prefix must not overlap the caches, nor out overlap q.
+ */
+lf_status lf_decode_step_prefix(const void* q, void* k_cache, void* v_cache, int32_t* mask,
+                                const void* new_k, const void* new_v, const int32_t* write_slot,
+                                const void* k_prefix, const void* v_prefix,
+                                const int32_t* prefix_start, const int32_t* prefix_len, void* out,
+                                int32_t* next_slots, int k, int flags, float* scores, int B,
+                                int Hq, int Hkv, int d, int S, int N, int P, int W, float scale,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* lf_decode_attention with shared prefixes: slot write and attention alone. */
+lf_status lf_decode_attention_prefix(const void* q, void* k_cache, void* v_cache, int32_t* mask,
+                                     const void* new_k, const void* new_v,
+                                     const int32_t* write_slot, const void* k_prefix,
+                                     const void* v_prefix, const int32_t* prefix_start,
+                                     const int32_t* prefix_len, void* out, int B, int Hq, int Hkv,
+                                     int d, int S, int N, int P, float scale, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+/* Workspace bytes of either call, for any k and flags. */
+lf_status lf_decode_prefix_workspace(int B, int Hq, int Hkv, int d, int S, int N, int P,
+                                     size_t* bytes);
 
 /*
  * The launch plan lf_decode_step / lf_decode_step_ex (k = topk, score on)
