@@ -801,11 +801,50 @@ lf_status run_rope(const RopeArgs& a, lf::RopeParams rp, const Shape& s, cudaStr
     return LF_OK;
 }
 
+// q [T][Hq][D] in boxes of 128 / g tokens, the g heads of a group and 64
+// columns: a box is one 128-row panel of a query tile.
+lf_status encode_query_map(CUtensorMap* m, const void* q, int D, int Hq, int g, int T) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return fail(LF_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                          static_cast<cuuint64_t>(T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(128 / g)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+                     estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(LF_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", int(r));
+    return LF_OK;
+}
+
+// Tensor maps and launch of an attention call; p holds everything else.
+lf_status run_attention(lf::AttnParams p, int d, float scale, int dev, cudaStream_t stream) {
+    CUtensorMap tmQ, tmK, tmV;
+    lf_status st = encode_query_map(&tmQ, p.q, d, p.Hq, p.Hq / p.Hkv, p.T);
+    if (st != LF_OK) return st;
+    const int units = p.N * p.Hkv;
+    if ((st = encode_cache_map(&tmK, const_cast<__nv_bfloat16*>(p.k), d, p.S, units)) != LF_OK) return st;
+    if ((st = encode_cache_map(&tmV, const_cast<__nv_bfloat16*>(p.v), d, p.S, units)) != LF_OK) return st;
+    // Not 0: the kernel multiplies masked logits (-inf) by it. Any logit below
+    // 1e-6 in magnitude weighs like 0.
+    p.scale_log2 = std::max(
+        static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634), 1e-30f);
+    p.negate = scale < 0.f;
+    p.wait_limit_ns = wait_limit_ns();
+    ProfScope prof(LF_KERNEL_PACKED_ATTENTION, stream);
+    cudaError_t e = lf::launch_attention(d, tmQ, tmK, tmV, p, sm_count(dev), stream);
+    if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+    return LF_OK;
+}
+
 // What attention a call asks for, and the workspace it takes.
 lf_status check_window(int T, const Shape& s, int window, int sinks) {
     lf_status st;
     if ((st = check_rows(T)) != LF_OK) return st;
     if ((st = check_shape(s)) != LF_OK) return st;
+    if (static_cast<int64_t>(T) * s.Hq > (int64_t(1) << 30))
+        return fail(LF_ERR_UNSUPPORTED, "T * Hq exceeds 2^30");
     if (window < 0 || window > kMaxPosWindow || sinks < 0 || sinks > kMaxPosWindow)
         return fail(LF_ERR_INVALID_ARG, "window and sinks must be in [0, 2^30] (got %d, %d)", window, sinks);
     return LF_OK;
@@ -914,7 +953,6 @@ lf_status run_prefix(StepArgs a, const Shape& s, const void* k_prefix, const voi
     ap.S = x.P;
     ap.causal = false;
     ap.pieces = L.pieces;
-    ap.scale_log2 = static_cast<float>(static_cast<double>(s.scale) * 1.4426950408889634);
     a.pre_ml = ap.part_ml;
     a.pre_o = ap.part_o;
     a.pre_pieces = L.pieces;
@@ -925,11 +963,7 @@ lf_status run_prefix(StepArgs a, const Shape& s, const void* k_prefix, const voi
     g_last_error[0] = '\0';
     if ((e = cudaMemsetAsync(ws, 0, L.zeroed, stream)) != cudaSuccess)
         return cuda_fail(e, "cudaMemsetAsync(workspace)");
-    {
-        ProfScope prof(LF_KERNEL_PACKED_ATTENTION, stream);
-        if ((e = lf::launch_attention(s.d, s.Hq / s.Hkv, ap, stream)) != cudaSuccess)
-            return cuda_fail(e, "prefix-attention launch");
-    }
+    if ((st = run_attention(ap, s.d, s.scale, dev, stream)) != LF_OK) return st;
     return launch(r, stream);
 }
 
@@ -1192,13 +1226,8 @@ lf_status lf_window_attention(const void* q, const void* k_cache, const void* v_
     ap.sinks = sinks;
     ap.causal = true;
     ap.pieces = pieces;
-    ap.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     g_last_error[0] = '\0';
-    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-    ProfScope prof(LF_KERNEL_PACKED_ATTENTION, stream);
-    if ((e = lf::launch_attention(d, Hq / Hkv, ap, stream)) != cudaSuccess)
-        return cuda_fail(e, "window-attention launch");
-    return LF_OK;
+    return run_attention(ap, d, scale, dev, static_cast<cudaStream_t>(stream_v));
 }
 
 lf_status lf_decode_prefix_workspace(int B, int Hq, int Hkv, int d, int S, int N, int P,

@@ -1,17 +1,121 @@
 // Attention of packed query rows over in-order caches (sm_103a): the sliding
 // window with visible first tokens, and the shared prefix of a decode batch.
 //
-// One pass over a row's visible keys with the running maximum m and sum l of
-// its softmax (log2 domain): s = scale * q.k, p = 2^(s - m), O += p v. The
-// row's output is O / l; with pieces, (m, l) and the unnormalised O are
+// One pass over a row's visible keys with the running reference m and sum l
+// of its softmax (log2 domain): s = scale * q.k, p = 2^(s - m), O += p v.
+// The row's output is O / l; with pieces, (m, l) and the unnormalised O are
 // written instead and a later kernel joins them.
+//
+// Tensor cores do both products. A tile has 128 query rows: 128 / g tokens
+// times the g query heads that share a KV head, so a K/V tile in shared
+// memory serves the whole group, for single tokens as for prompts. Two
+// streams run against each other, each with its own S and O accumulators in
+// tensor memory and its own four softmax warps, so one stream's products run
+// under the other's exponentials:
+//   rows mode  the streams are two query tiles over the same K/V tiles (each
+//              K/V tile is read from L2 once per 256 rows);
+//   keys mode  (at most 128 rows per sequence on average) the streams are
+//              the even and odd K/V tiles of one query tile, joined later
+//              like any other pieces of the key axis.
+// Warp roles of a CTA (one per SM: 224 KB of shared memory, all of TMEM):
+//   warps 0-3, 4-7  softmax of stream 0, 1; a thread owns a row: S from
+//                   tensor memory, m, l, P (bf16) back over S, at the end O
+//   warp 8          issues S = Q K^T (both in shared memory) and O += P V (P
+//                   in tensor memory, V as it lies in the cache)
+//   warp 9          TMA loads: Q once, K and V tiles through a ring
+//   warps 10, 11    nothing (they complete the third warpgroup)
+// The reference m is not the exact running maximum: it moves, and O is
+// rescaled, only when a row's maximum grows by more than 2^8, which l and O
+// hold easily in fp32 (most rows rescale once or never).
+// P is rounded to bf16 (2^-9 of each weight) because the tensor cores take
+// it; l sums the unrounded weights.
+//
+// Keys a row does not see are removed by select before the exponentials, and
+// cache rows no row of the tile sees are zeroed in shared memory, so what
+// lies there does not matter. A NaN or infinity in a row that others of the
+// tile do see would still reach this row's O as 0 * NaN: a row whose result
+// is not finite is computed again by attn_row, key by key.
 #include <math.h>
+#include <stdlib.h>
 
+#include <algorithm>
+
+#include "../../include/lf_decode.h"
 #include "lf_kernels.h"
-#include "lf_ptx.cuh"
+#include "lf_tcgen05.cuh"
 
 namespace lf {
 namespace {
+
+constexpr int kRows = 128;    // query rows of a tile
+constexpr int kKeys = 128;    // keys of a tile
+constexpr int kSoftmaxThreads = 256;
+constexpr int kAttnThreads = kSoftmaxThreads + 128;
+// Registers: 384 threads launch with 168 each (64512 in all); the softmax
+// warps, which hold a row's 128 scores, then take 224 and the others 56
+// (256 * 224 + 128 * 56 = 64512).
+constexpr int kSoftmaxRegs = 224;
+constexpr int kOtherRegs = 56;
+constexpr int kPanel = kRows * 128;  // bytes of 64 columns of a tile
+constexpr float kRescale = 8.f;      // log2 growth of the maximum that moves m
+
+template <int D>
+struct AttnSmem {
+    static constexpr int kTileBytes = kRows * D * 2;
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kRingOff = 2 * kTileBytes;  // after the two Q tiles
+    static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
+    // barriers: q, full[], empty[], s_full[2], p_full[2], o_done[2], drain
+    static constexpr int kBars = 1 + 2 * kStages + 7;
+    static constexpr int kMiscOff = kBarOff + kBars * 8;
+    static constexpr int kAlloc = kMiscOff + 64 + 1024;
+    static_assert(kAlloc <= 232448, "shared memory of a CTA");
+};
+
+// What a CTA works on, found by warp 0.
+struct Item {
+    int seq, tok0, ntok;  // sequence, first packed row (token) of the tile, its tokens
+    int pos0;             // position of the first token (causal)
+    int lo, hi;           // keys some row sees: [lo, hi) and below sinks
+    int sinks;
+    int nsink, t0;        // tile i of the list: i, or t0 + i - nsink from nsink on
+    int first, count;     // this CTA's part of the list
+};
+
+__device__ __forceinline__ int tile_of(const Item& it, int i) {
+    return i < it.nsink ? i : it.t0 + i - it.nsink;
+}
+
+struct AttnPlan {
+    bool rows_mode;
+    int tok_shift;  // log2 tokens of a work item
+    int nsplit;     // CTAs over an item's K/V tiles
+    int items;
+};
+
+AttnPlan attn_plan(int T, int N, int Hq, int Hkv, int S, bool causal, int window, int sinks,
+                   int sms) {
+    const int g = Hq / Hkv;
+    int gs = 0;
+    while ((1 << gs) < g) ++gs;
+    AttnPlan pl;
+    // Two query tiles per CTA once sequences have more than one on average.
+    const long long avg = (static_cast<long long>(T) + N - 1) / N;
+    pl.rows_mode = avg * g > kRows;
+    pl.tok_shift = (pl.rows_mode ? 8 : 7) - gs;
+    const int tok = 1 << pl.tok_shift;
+    pl.items = (T >> pl.tok_shift) + N;
+    // Split the keys when the items (about this many hold rows) leave SMs idle.
+    const long long busy = std::min<long long>(pl.items, N * ((avg + tok - 1) / tok)) * Hkv;
+    long long keys = S;
+    if (causal && window > 0)
+        keys = std::min<long long>(S, static_cast<long long>(window) + std::min<long long>(tok, avg) + sinks);
+    const long long tiles = (keys + kKeys - 1) / kKeys;
+    const long long most = std::max<long long>(1, tiles / 2);
+    pl.nsplit = static_cast<int>(
+        std::max<long long>(1, std::min<long long>({most, sms / std::max<long long>(busy, 1), 16})));
+    return pl;
+}
 
 // One warp, one query row, keys visible by select: lane i scores key j0 + i of
 // each 32, then the lanes share the values' columns. (m, l) and the lane's
@@ -32,7 +136,6 @@ __device__ void attn_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const _
             const uint4* kr = reinterpret_cast<const uint4*>(k + static_cast<size_t>(j) * D);
             const uint4* qr = reinterpret_cast<const uint4*>(q);
             float a = 0.f;
-#pragma unroll
             for (int c = 0; c < D / 8; ++c) {
                 const uint4 kk = __ldg(kr + c), qq = __ldg(qr + c);
                 const __nv_bfloat162* kb = reinterpret_cast<const __nv_bfloat162*>(&kk);
@@ -70,60 +173,547 @@ __device__ void attn_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const _
     }
 }
 
-constexpr int kRowWarps = 8;
-
-// The simplest form: one warp per query row, every key of the row in one piece.
+// A stream's row again, over the stream's tiles; the warp writes its result.
 template <int D>
-__global__ void __launch_bounds__(kRowWarps * 32) lf_attn_rows_kernel(const AttnParams p) {
+__device__ __noinline__ void redo_row(const AttnParams& p, const Item& it, size_t row,
+                                      size_t cache, int first, int step, int lo, int hi, int piece) {
     const int lane = threadIdx.x & 31;
-    const size_t row = static_cast<size_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-    if (row >= static_cast<size_t>(p.T) * p.Hq) return;
-    const int t = static_cast<int>(row / p.Hq);
-    const int h = static_cast<int>(row - static_cast<size_t>(t) * p.Hq);
-    const int n = seq_of_row(p.q_start, p.N, t);
-    SeqRange r;
-    if (!seq_range(p.q_start, p.kv_len, n, p.T, p.S, p.causal, p.dev_err, &r)) return;
-    if (t < r.q0 || t >= r.q0 + r.n) return;
-    int lo = 0, hi = r.kv, sinks = 0;
-    if (p.causal) {
-        hi = r.kv - r.n + (t - r.q0) + 1;
-        if (p.window > 0) lo = max(0, hi - p.window);
-        sinks = p.sinks;
-    }
-    const size_t base = (static_cast<size_t>(n) * p.Hkv + h / (p.Hq / p.Hkv)) * p.S * D;
-    const __nv_bfloat16* q = p.q + row * D;
     float m = -INFINITY, l = 0.f, o[D / 32];
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
-    const int first = min(sinks, lo);
-    attn_row<D>(q, p.k + base, p.v + base, 0, first, lo, hi, sinks, p.scale_log2, m, l, o);
-    attn_row<D>(q, p.k + base, p.v + base, lo, hi, lo, hi, sinks, p.scale_log2, m, l, o);
+    for (int i = first; i < it.count; i += step) {
+        const int j0 = tile_of(it, it.first + i) * kKeys;
+        attn_row<D>(p.q + row * D, p.k + cache, p.v + cache, j0, j0 + kKeys, lo, hi, it.sinks,
+                    p.negate ? -p.scale_log2 : p.scale_log2, m, l, o);
+    }
     if (p.pieces == 0) {
-        const float il = l == 0.f ? 0.f : 1.f / l;
+        const float il = 1.f / l;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
             p.out[row * D + lane * (D / 32) + c] = __float2bfloat16_rn(l == 0.f ? 0.f : o[c] * il);
     } else {
-        if (lane == 0) p.part_ml[row] = make_float2(m, l);
+        const size_t at = static_cast<size_t>(piece) * p.T * p.Hq + row;
+        if (lane == 0) p.part_ml[at] = make_float2(m, l);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) p.part_o[row * D + lane * (D / 32) + c] = o[c];
+        for (int c = 0; c < D / 32; ++c) p.part_o[at * D + lane * (D / 32) + c] = o[c];
     }
+}
+
+// TMA load without an L2 hint: K and V tiles are read again by other CTAs.
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Warp 0: the sequence and rows of work item x, and the K/V tiles it reads.
+// Sequence b's items start at floor(q_start[b] / tok) + b: enough for its
+// rows wherever they start, so no prefix sum over the sequences is needed.
+__device__ bool find_item(const AttnParams& p, int x, int tok_shift, int split, int nsplit, Item* it) {
+    const int lane = threadIdx.x & 31;
+    int b = 0, len = p.N;
+    while (len > 1) {
+        const int step = (len + 31) >> 5;
+        const int i = b + lane * step;
+        const bool le = lane * step < len && (p.q_start[i] >> tok_shift) + i <= x;
+        const unsigned hit = __ballot_sync(0xffffffffu, le);
+        const int top = hit ? 31 - __clz(hit) : 0;
+        b += top * step;
+        len = min(step, len - top * step);
+    }
+    SeqRange r;
+    if (!seq_range(p.q_start, p.kv_len, b, p.T, p.S, p.causal, p.dev_err, &r)) return false;
+    const int rel = (x - (r.q0 >> tok_shift) - b) << tok_shift;
+    if (rel < 0 || rel >= r.n) return false;
+    it->seq = b;
+    it->tok0 = r.q0 + rel;
+    it->ntok = min(1 << tok_shift, r.n - rel);
+    it->pos0 = r.kv - r.n + rel;
+    it->hi = p.causal ? it->pos0 + it->ntok : r.kv;
+    it->lo = (p.causal && p.window > 0) ? max(0, it->pos0 + 1 - p.window) : 0;
+    it->sinks = p.causal ? p.sinks : 0;
+    it->nsink = (min(it->sinks, it->lo) + kKeys - 1) / kKeys;
+    it->t0 = max(it->nsink, it->lo / kKeys);
+    const int tiles = it->nsink + max(0, (it->hi + kKeys - 1) / kKeys - it->t0);
+    const int per = (tiles + nsplit - 1) / nsplit;
+    it->first = split * per;
+    it->count = max(0, min(tiles - it->first, per));
+    return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    lf_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const AttnParams p, const AttnPlan pl) {
+    using L = AttnSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+    uint64_t* full = q_full + 1;
+    uint64_t* empty = full + L::kStages;
+    uint64_t* s_full = empty + L::kStages;
+    uint64_t* p_full = s_full + 2;
+    uint64_t* o_done = p_full + 2;
+    uint64_t* drain = o_done + 2;
+    volatile int* misc = reinterpret_cast<int*>(smem + L::kMiscOff);  // [0] TMEM base, [1] abort, [2] work
+    __shared__ Item s_item;
+
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const int lane = tid & 31;
+    // The last items (the longest rows of a causal prompt) start first.
+    const int split = blockIdx.x % pl.nsplit;
+    const int rest = blockIdx.x / pl.nsplit;
+    const int kvh = rest % p.Hkv;
+    const int x = pl.items - 1 - rest / p.Hkv;
+
+    allow_dependent_launch();
+    if (warp == 0) {
+        Item it;
+        const bool ok = find_item(p, x, pl.tok_shift, split, pl.nsplit, &it);
+        if (lane == 0) {
+            if (ok) s_item = it;
+            misc[1] = 0;
+            misc[2] = ok;
+        }
+    } else if (warp == 8) {
+        tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kMiscOff), 512);
+    } else if (warp == 9 && lane == 0) {
+        mbar_init(q_full, 1);
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], 4);
+            mbar_init(&o_done[s], 1);
+        }
+        mbar_init(drain, 1);
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+    const Item it = s_item;
+    // Work units of the streams: unit j belongs to stream j & 1 and reads K/V
+    // tile j >> 1 (rows mode) or j (keys mode) of the CTA's part of the list.
+    const bool rows = pl.rows_mode;
+    const int units = misc[2] ? (rows ? 2 * it.count : it.count) : 0;
+    const int g = p.Hq / p.Hkv;
+    const int gs = __ffs(g) - 1;
+
+    // A wait of a whole warp: every lane learns whether all of them saw the
+    // barrier complete.
+    auto warp_wait = [&](uint64_t* bar, int parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_limit_ns)) != 0;
+    };
+    auto give_up = [&]() {
+        misc[1] = 1;
+        atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT);
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 9) {
+        // ------------------------------------------------------- producer --
+        if (lane == 0 && units > 0) {
+            const int unit = it.seq * p.Hkv + kvh;
+            mbar_arrive_expect_tx(q_full, (rows ? 2 : 1) * L::kTileBytes);
+            for (int s = 0; s < (rows ? 2 : 1); ++s)
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load(smem + s * L::kTileBytes + c * kPanel, &tmQ, c * 64, kvh * g,
+                             it.tok0 + s * (kRows >> gs), q_full);
+            int n = 0;  // ring entries issued
+            bool ok = true;
+            auto load = [&](const CUtensorMap* map, int i) {
+                const int st = n % L::kStages;
+                if (!mbar_wait(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_limit_ns)) return false;
+                mbar_arrive_expect_tx(&full[st], L::kTileBytes);
+                uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes;
+                const int y = tile_of(it, it.first + i) * kKeys;
+                for (int c = 0; c < D / 64; ++c)
+                    for (int h = 0; h < 2; ++h)
+                        tma_load(dst + c * kPanel + h * (kPanel / 2), map, c * 64, y + h * 64, unit,
+                                 &full[st]);
+                ++n;
+                return true;
+            };
+            // The order in which the products take the tiles.
+            ok = load(&tmK, 0);
+            if (ok && !rows && units > 1) ok = load(&tmK, 1);
+            for (int j = 0; ok && j < units; ++j) {
+                if (rows && (j & 1)) continue;
+                ok = load(&tmV, rows ? j >> 1 : j);
+                if (ok && j + 2 < units) ok = load(&tmK, rows ? (j >> 1) + 1 : j + 2);
+            }
+            if (!ok) {
+                give_up();
+                // No copy may be in flight when the CTA leaves.
+                mbar_wait(q_full, 0);
+                for (int k = max(0, n - L::kStages); k < n; ++k)
+                    mbar_wait(&full[k % L::kStages], (k / L::kStages) & 1);
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------ matrix products --
+        if (units > 0) {
+            const uint32_t idesc_s = instr_desc(kRows, kKeys, false) | (p.negate ? kInstrNegateA : 0u);
+            constexpr uint32_t idesc_o = instr_desc(kRows, D, true);
+            const uint32_t qs = smem_u32(smem);
+            const uint32_t ring = smem_u32(smem + L::kRingOff);
+            int n = 0;            // ring entries taken
+            int kst = 0, vst = 0; // stages of the current K and V tiles
+            bool ok = warp_wait(q_full, 0);
+            auto take = [&](int* st) {
+                *st = n % L::kStages;
+                const bool got = warp_wait(&full[*st], (n / L::kStages) & 1);
+                ++n;
+                return got;
+            };
+            // S of unit j: Q tile times K tile.
+            auto scores = [&](int j) {
+                const int s = j & 1;
+                if (!(rows && s) && !take(&kst)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t qa = qs + (rows && s ? L::kTileBytes : 0);
+                    const uint32_t ka = ring + kst * L::kTileBytes;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
+                        mma_ss(tmem + s * kKeys, smem_desc(qa + off, 16, 1024),
+                               smem_desc(ka + off, 16, 1024), idesc_s, k > 0);
+                    }
+                    if (!rows || s) mma_commit(&empty[kst]);
+                    mma_commit(&s_full[s]);
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = ok && scores(0);
+            if (ok && units > 1) ok = scores(1);
+            for (int j = 0; ok && j < units; ++j) {
+                const int s = j & 1;
+                if (!(rows && s)) {
+                    ok = take(&vst);
+                    if (!ok) break;
+                    // Cache rows that no row of the item sees: zero, so that
+                    // 0 * garbage stays 0.
+                    const int j0 = tile_of(it, it.first + (rows ? j >> 1 : j)) * kKeys;
+                    if (j0 + kKeys > it.hi || (j0 < it.lo && j0 + kKeys > it.sinks)) {
+                        uint8_t* vt = smem + L::kRingOff + vst * L::kTileBytes;
+                        for (int i = lane; i < kKeys * (D / 64) * 8; i += 32) {
+                            const int r = (i >> 3) & (kKeys - 1);
+                            const int key = j0 + r;
+                            if (key >= it.hi || (key < it.lo && key >= it.sinks))
+                                *reinterpret_cast<uint4*>(vt + (i >> 10) * kPanel + r * 128 +
+                                                          (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                if (!warp_wait(&p_full[s], (j >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t va = ring + vst * L::kTileBytes;
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_ts(tmem + 2 * kKeys + s * D, tmem + s * kKeys + k * 8,
+                               smem_desc(va + k * 2048, kPanel, 1024), idesc_o, j > 1 || k > 0);
+                    if (!rows || s) mma_commit(&empty[vst]);
+                    mma_commit(&o_done[s]);
+                }
+                __syncwarp();
+                if (j + 2 < units) ok = scores(j + 2);
+            }
+            if (!ok && lane == 0) give_up();
+            // No product may be in flight when tensor memory is freed.
+            if (lane == 0) {
+                mma_commit(drain);
+                mbar_wait(drain, 0);
+            }
+            __syncwarp();
+        }
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (misc[2]) {
+        // --------------------------------------------------------- softmax --
+        const int s = warp >> 2;
+        const int r = tid & (kRows - 1);
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's lanes
+        const uint32_t ts = tmem + lanes + s * kKeys;
+        const uint32_t to = tmem + lanes + 2 * kKeys + s * D;
+        const int tt = (rows && s ? kRows >> gs : 0) + (r >> gs);  // token of the item
+        const bool valid = tt < it.ntok;
+        const bool any_valid = __any_sync(0xffffffffu, valid);
+        const int row_hi = p.causal ? it.pos0 + tt + 1 : it.hi;
+        const int row_lo = (p.causal && p.window > 0) ? max(0, row_hi - p.window) : 0;
+        // Keys every row of the warp sees: [all_lo, all_hi), and below sinks.
+        const int all_hi = __shfl_sync(0xffffffffu, row_hi, 0);
+        const int all_lo = __shfl_sync(0xffffffffu, row_lo, 31);
+        const float c = p.scale_log2;
+        const uint64_t c2 = pack_f32x2(c, c);
+        float m = -INFINITY, l = 0.f;
+        int n = 0;  // units of this stream done
+        bool ok = true;
+        for (int j = s; j < units; j += 2, ++n) {
+            if (!warp_wait(&s_full[s], n & 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (any_valid) {
+                const int j0 = tile_of(it, it.first + (rows ? j >> 1 : j)) * kKeys;
+                uint32_t x[kKeys];
+#pragma unroll
+                for (int k = 0; k < kKeys; k += 32) tmem_ld32(ts + k, x + k);
+                tmem_wait_ld();
+                if (!(j0 + kKeys <= all_hi && (j0 >= all_lo || j0 + kKeys <= it.sinks))) {
+                    const int h = row_hi - j0, lw = row_lo - j0, sk = it.sinks - j0;
+#pragma unroll
+                    for (int k = 0; k < kKeys; ++k)
+                        if (!(k < h && (k >= lw || k < sk))) x[k] = 0xff800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < kKeys; k += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[k + e]),
+                                                   __uint_as_float(x[k + e + 4])));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const bool grow = m != -INFINITY && top > m + kRescale;
+                if (__any_sync(0xffffffffu, grow)) {
+                    // n >= 1 here: m was set by an earlier unit.
+                    if (!warp_wait(&o_done[s], (n - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float f = grow ? ex2_approx(m - top) : 1.f;
+                    l *= f;
+                    const uint64_t f2 = pack_f32x2(f, f);
+#pragma unroll
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(to + k, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a, b;
+                            unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[e]),
+                                                              __uint_as_float(o[e + 1])), f2), a, b);
+                            o[e] = __float_as_uint(a);
+                            o[e + 1] = __float_as_uint(b);
+                        }
+                        tmem_st32(to + k, o);
+                    }
+                    tmem_wait_st();
+                }
+                if (grow || m == -INFINITY) m = top;
+                const float base = m == -INFINITY ? 0.f : -m;
+                const uint64_t b2 = pack_f32x2(base, base);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int k = 0; k < kKeys; k += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, b;
+                        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[k + e]),
+                                                          __uint_as_float(x[k + e + 1])), c2, b2), a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
+                        w[e >> 1] = pack_bf16x2(a, b);
+                    }
+                    tmem_st16(ts + (k >> 1), w);
+                }
+                tmem_wait_st();
+                float a, b;
+                unpack_f32x2(add_f32x2(sum[0], sum[1]), a, b);
+                l += a + b;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[s]);
+        }
+        if (ok && n > 0) ok = warp_wait(&o_done[s], (n - 1) & 1);
+        if (!ok && lane == 0) give_up();
+        tc_fence_after();
+        if (ok && any_valid) {
+            const size_t row = static_cast<size_t>(it.tok0 + tt) * p.Hq + kvh * g + (r & (g - 1));
+            const int piece = rows ? split : split * 2 + s;
+            const size_t at = static_cast<size_t>(piece) * p.T * p.Hq + row;
+            const bool some = valid && l != 0.f;
+            // 0 unless a value is not finite.
+            float bad = l * 0.f;
+            const float il = some ? 1.f / l : 0.f;
+#pragma unroll
+            for (int k = 0; k < D; k += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(to + k, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    if (!some) o[e] = 0u;
+                    bad = fmaf(__uint_as_float(o[e]), 0.f, bad);
+                }
+                if (p.pieces == 0) {
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 w;
+                            w.x = pack_bf16x2(__uint_as_float(o[e]) * il, __uint_as_float(o[e + 1]) * il);
+                            w.y = pack_bf16x2(__uint_as_float(o[e + 2]) * il, __uint_as_float(o[e + 3]) * il);
+                            w.z = pack_bf16x2(__uint_as_float(o[e + 4]) * il, __uint_as_float(o[e + 5]) * il);
+                            w.w = pack_bf16x2(__uint_as_float(o[e + 6]) * il, __uint_as_float(o[e + 7]) * il);
+                            *reinterpret_cast<uint4*>(p.out + row * D + k + e) = w;
+                        }
+                    }
+                } else if (some) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4*>(p.part_o + at * D + k + e) =
+                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            if (valid && p.pieces > 0) p.part_ml[at] = make_float2(m, l);
+            __syncwarp();
+            unsigned redo = __ballot_sync(0xffffffffu, some && !(bad == 0.f));
+            for (; redo; redo &= redo - 1) {
+                const int from = __ffs(redo) - 1;
+                const unsigned lo32 = static_cast<unsigned>(row), hi32 = static_cast<unsigned>(row >> 32);
+                const size_t rr = static_cast<size_t>(__shfl_sync(0xffffffffu, hi32, from)) << 32 |
+                                  __shfl_sync(0xffffffffu, lo32, from);
+                redo_row<D>(p, s_item, rr, (static_cast<size_t>(it.seq) * p.Hkv + kvh) * p.S * D,
+                            rows ? 0 : s, rows ? 1 : 2, __shfl_sync(0xffffffffu, row_lo, from),
+                            __shfl_sync(0xffffffffu, row_hi, from), piece);
+            }
+        }
+    }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of the key axis: one warp per query row.
+constexpr int kMergeWarps = 4;
+constexpr int kMaxPieces = 32;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) lf_attn_merge_kernel(const AttnParams p) {
+    const int lane = threadIdx.x & 31;
+    const size_t rows = static_cast<size_t>(p.T) * p.Hq;
+    const size_t at = static_cast<size_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+    allow_dependent_launch();
+    const size_t row = at < rows ? at : rows - 1;
+    const int t = static_cast<int>(row / p.Hq);
+    // A batch of single tokens has its row t in sequence t. (The lengths were
+    // there before the attention kernel started: they need no wait.)
+    int n = min(t, p.N - 1);
+    if (!(p.q_start[n] <= t && t < p.q_start[n + 1])) n = seq_of_row(p.q_start, p.N, t);
+    SeqRange r;
+    const bool mine = seq_range(p.q_start, p.kv_len, n, p.T, p.S, p.causal, p.dev_err, &r) &&
+                      t >= r.q0 && t < r.q0 + r.n && at < rows;
+    // Every thread waits, so this grid ends after the attention grid.
+    grid_dependency_wait();
+    if (!mine) return;
+    const float2 ml = lane < p.pieces ? __ldcg(&p.part_ml[lane * rows + row])
+                                      : make_float2(-INFINITY, 0.f);
+    float m = ml.y != 0.f ? ml.x : -INFINITY;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float w = ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
+    float l = ml.y * w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    w = l == 0.f ? 0.f : w / l;
+    constexpr int kC = D / 32;
+    float o[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) o[c] = 0.f;
+    for (int i = 0; i < p.pieces; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        if (wi == 0.f) continue;  // nothing visible: the piece's output was not written
+        const float* po = p.part_o + (i * rows + row) * D + lane * kC;
+#pragma unroll
+        for (int c = 0; c < kC; c += 2) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(po + c));
+            o[c] += wi * v.x;
+            o[c + 1] += wi * v.y;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kC; c += 2)
+        *reinterpret_cast<uint32_t*>(p.out + row * D + lane * kC + c) = pack_bf16x2(o[c], o[c + 1]);
+}
+
+template <int D>
+cudaError_t launch_attention_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                               const CUtensorMap& tmV, const AttnParams& p, const AttnPlan& pl,
+                               cudaStream_t stream) {
+    using L = AttnSmem<D>;
+    auto kernel = lf_attn_kernel<D>;
+    static int configured_for = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (configured_for != dev) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        if (e != cudaSuccess) return e;
+        configured_for = dev;
+    }
+    const unsigned grid = static_cast<unsigned>(pl.items) * p.Hkv * pl.nsplit;
+    kernel<<<grid, kAttnThreads, L::kAlloc, stream>>>(tmQ, tmK, tmV, p, pl);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.pieces == 0 || !p.out) return e;
+    const size_t rows = static_cast<size_t>(p.T) * p.Hq;
+    const char* env = std::getenv("LF_PDL");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (env && std::atoi(env) == 0) ? 0 : 1;
+    e = cudaLaunchKernelEx(&cfg, lf_attn_merge_kernel<D>, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-int attention_pieces(int, int, int, int, int, bool causal, int, int, int) { return causal ? 0 : 1; }
+int attention_pieces(int T, int N, int Hq, int Hkv, int S, bool causal, int window, int sinks,
+                     int sms) {
+    const AttnPlan pl = attn_plan(T, N, Hq, Hkv, S, causal, window, sinks, sms);
+    if (pl.rows_mode) return causal && pl.nsplit == 1 ? 0 : pl.nsplit;
+    return 2 * pl.nsplit;
+}
 
-cudaError_t launch_attention(int D, int G, const AttnParams& p, cudaStream_t stream) {
-    const size_t rows = static_cast<size_t>(p.T) * p.Hq;
-    const unsigned grid = static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps);
-    if (D == 64)
-        lf_attn_rows_kernel<64><<<grid, kRowWarps * 32, 0, stream>>>(p);
-    else if (D == 128)
-        lf_attn_rows_kernel<128><<<grid, kRowWarps * 32, 0, stream>>>(p);
-    else
-        return cudaErrorInvalidValue;
-    return cudaGetLastError();
+cudaError_t launch_attention(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                             const CUtensorMap& tmV, const AttnParams& p, int sms,
+                             cudaStream_t stream) {
+    const AttnPlan pl = attn_plan(p.T, p.N, p.Hq, p.Hkv, p.S, p.causal, p.window, p.sinks, sms);
+    if (p.pieces > kMaxPieces) return cudaErrorInvalidConfiguration;
+    if (D == 64) return launch_attention_t<64>(tmQ, tmK, tmV, p, pl, stream);
+    if (D == 128) return launch_attention_t<128>(tmQ, tmK, tmV, p, pl, stream);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace lf

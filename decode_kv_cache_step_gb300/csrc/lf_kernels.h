@@ -170,13 +170,20 @@ struct AttnParams {
     int window, sinks;
     bool causal;
     int pieces;
-    float scale_log2;            // scale * log2(e)
+    float scale_log2;            // |scale| * log2(e)
+    bool negate;                 // scale < 0: the kernel negates q
+    uint64_t wait_limit_ns;
 };
 // Pieces of the key axis such a call writes (0: the output directly), a rule
 // on its sizes alone. The plan for the prefix (causal false) has at least one.
 int attention_pieces(int T, int N, int Hq, int Hkv, int S, bool causal, int window, int sinks,
                      int sms);
-cudaError_t launch_attention(int D, int G, const AttnParams& p, cudaStream_t stream);
+// tmQ: q as [T][Hq][D] in boxes of 128 / g tokens x g heads x 64; tmK, tmV:
+// the caches in boxes of kTile slots x 64 (128-byte swizzle). Writes out, or
+// the pieces and, where out is given, their join.
+cudaError_t launch_attention(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                             const CUtensorMap& tmV, const AttnParams& p, int sms,
+                             cudaStream_t stream);
 
 // Error bit of lengths that do not fit (LF_DEVERR_BAD_LENGTH).
 constexpr uint32_t kErrBadLength = 0x4u;
