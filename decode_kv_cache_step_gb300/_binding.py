@@ -355,12 +355,37 @@ class PreparedStep:
             pass
 
 
+class _Here:
+    """The guard of a call on the current device: nothing to switch."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
 def _on_device(device, *tensors):
     """The device guard of a call on `device`, where every tensor has to be."""
+    index = device.index
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors on {device} and {t.device}: all must be on one device")
-    return torch.cuda.device(device)
+    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(device)
+
+
+# The current stream's handle without a Stream object, where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call_stream(stream, device):
+    """_stream_handle for a call on `device`."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream_handle(stream)
 
 
 def _workspace(workspace, nbytes, device, stream):
@@ -433,7 +458,7 @@ def qk_norm_rope(qkv, q_weight, k_weight, inv_freq, positions, q_out, k_out, v_o
         _check(lib, lib.lf_qk_norm_rope(
             qkv.data_ptr(), stride, _ptr(q_weight), _ptr(k_weight), inv_freq.data_ptr(),
             positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), T, Hq, Hkv,
-            d, rot, int(bool(interleaved)), float(eps), _stream_handle(stream)))
+            d, rot, int(bool(interleaved)), float(eps), _call_stream(stream, qkv.device)))
 
 
 def prefill_append(qkv, q_weight, k_weight, inv_freq, q_start, kv_len, q_out, k_cache, v_cache,
@@ -460,7 +485,7 @@ def prefill_append(qkv, q_weight, k_weight, inv_freq, q_start, kv_len, q_out, k_
             qkv.data_ptr(), stride, _ptr(q_weight), _ptr(k_weight), inv_freq.data_ptr(),
             q_start.data_ptr(), kv_len.data_ptr(), _ptr(pos_offset), q_out.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(), T, B, Hq, Hkv, d, S, rot,
-            int(bool(interleaved)), float(eps), _stream_handle(stream)))
+            int(bool(interleaved)), float(eps), _call_stream(stream, qkv.device)))
 
 
 def window_attention_workspace(T, B, Hq, Hkv, d, S, window=0, sinks=0) -> int:
@@ -499,7 +524,7 @@ def window_attention(q, k_cache, v_cache, q_start, kv_len, out, window, sinks, s
         _check(lib, lib.lf_window_attention(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), q_start.data_ptr(),
             kv_len.data_ptr(), out.data_ptr(), T, B, Hq, Hkv, d, S, int(window), int(sinks),
-            float(scale), _ptr(ws), 0 if ws is None else ws.numel(), _stream_handle(stream)))
+            float(scale), _ptr(ws), 0 if ws is None else ws.numel(), _call_stream(stream, q.device)))
 
 
 def decode_prefix_workspace(B, Hq, Hkv, d, S, N, P) -> int:
@@ -550,7 +575,7 @@ def decode_attention_prefix(q, k_cache, v_cache, mask, new_k, new_v, write_slot,
             new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(), k_prefix.data_ptr(),
             v_prefix.data_ptr(), prefix_start.data_ptr(), prefix_len.data_ptr(), out.data_ptr(),
             B, Hq, Hkv, d, S, N, P, float(scale), ws.data_ptr(), ws.numel(),
-            _stream_handle(stream)))
+            _call_stream(stream, q.device)))
 
 
 def decode_step_prefix(q, k_cache, v_cache, mask, new_k, new_v, write_slot, k_prefix, v_prefix,
@@ -575,7 +600,7 @@ def decode_step_prefix(q, k_cache, v_cache, mask, new_k, new_v, write_slot, k_pr
             v_prefix.data_ptr(), prefix_start.data_ptr(), prefix_len.data_ptr(), out.data_ptr(),
             next_slots.data_ptr(), 1 if k is None else int(k), int(flags),
             None if scores is None else scores.data_ptr(), B, Hq, Hkv, d, S, N, P, int(W),
-            float(scale), ws.data_ptr(), ws.numel(), _stream_handle(stream)))
+            float(scale), ws.data_ptr(), ws.numel(), _call_stream(stream, q.device)))
 
 
 def step_plan(B: int, Hq: int, Hkv: int, d: int, S: int, topk: int = 1) -> dict:
