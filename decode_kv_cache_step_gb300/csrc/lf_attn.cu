@@ -17,13 +17,18 @@
 //   keys mode  (at most 128 rows per sequence on average) the streams are
 //              the even and odd K/V tiles of one query tile, joined later
 //              like any other pieces of the key axis.
-// Warp roles of a CTA (one per SM: 224 KB of shared memory, all of TMEM):
+// A CTA (one per SM: 224 KB of shared memory, all of TMEM) keeps taking work
+// items until the grid has none left (cluster launch control hands it the
+// index of a CTA that has not started), so one item's loads and products run
+// under the epilogue of the one before. Its warps:
 //   warps 0-3, 4-7  softmax of stream 0, 1; a thread owns a row: S from
 //                   tensor memory, m, l, P (bf16) back over S, at the end O
 //   warp 8          issues S = Q K^T (both in shared memory) and O += P V (P
 //                   in tensor memory, V as it lies in the cache)
-//   warp 9          TMA loads: Q once, K and V tiles through a ring
-//   warps 10, 11    nothing (they complete the third warpgroup)
+//   warp 9          TMA loads: Q, then K and V tiles through a ring
+//   warp 10         next work item: cancels a pending CTA, finds the item's
+//                   sequence, rows and tiles, hands it to the others
+//   warp 11         nothing (it completes the third warpgroup)
 // The reference m is not the exact running maximum: it moves, and O is
 // rescaled, only when a row's maximum grows by more than 2^8, which l and O
 // hold easily in fp32 (most rows rescale once or never).
@@ -59,37 +64,49 @@ constexpr int kOtherRegs = 56;
 constexpr int kPanel = kRows * 128;  // bytes of 64 columns of a tile
 constexpr float kRescale = 8.f;      // log2 growth of the maximum that moves m
 
+constexpr int kItemSlots = 3;        // items in flight between the warps
+constexpr int kAskTiles = 2;         // K/V tiles of an item left to load when the next is asked for
+
+// What the warps work on.
+struct Item {
+    int seq, tok0, ntok;  // sequence, first packed row (token) of the tile, its tokens
+    int pos0;             // position of the first token (causal)
+    int lo, hi;           // keys some row sees: [lo, hi) and below sinks
+    int sinks;
+    int nsink;            // tile i of the list starts at key i * kKeys below nsink (its keys end
+                          // at sinks), at lo + (i - nsink) * kKeys from there (its keys end at hi)
+    int first, count;     // this item's part of the list
+    int kvh, split;
+    int stop;             // no more work
+};
+
 template <int D>
 struct AttnSmem {
     static constexpr int kTileBytes = kRows * D * 2;
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRingOff = 2 * kTileBytes;  // after the two Q tiles
     static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
-    // barriers: q, full[], empty[], s_full[2], p_full[2], o_done[2], drain
-    static constexpr int kBars = 1 + 2 * kStages + 7;
-    static constexpr int kMiscOff = kBarOff + kBars * 8;
-    static constexpr int kAlloc = kMiscOff + 64 + 1024;
+    // barriers: q_full[2], q_empty[2], full[], empty[], s_full[2], p_full[2],
+    // o_done[2], o_free[2], item_full[], item_empty[], drain, next, want
+    static constexpr int kBars = 4 + 2 * kStages + 8 + 2 * kItemSlots + 3;
+    static constexpr int kItemOff = kBarOff + kBars * 8;
+    static constexpr int kNextOff = (kItemOff + kItemSlots * static_cast<int>(sizeof(Item)) + 15) / 16 * 16;
+    static constexpr int kMiscOff = kNextOff + 16;  // TMEM base, abort flag
+    static constexpr int kAlloc = kMiscOff + 16 + 1024;
     static_assert(kAlloc <= 232448, "shared memory of a CTA");
 };
 
-// What a CTA works on, found by warp 0.
-struct Item {
-    int seq, tok0, ntok;  // sequence, first packed row (token) of the tile, its tokens
-    int pos0;             // position of the first token (causal)
-    int lo, hi;           // keys some row sees: [lo, hi) and below sinks
-    int sinks;
-    int nsink, t0;        // tile i of the list: i, or t0 + i - nsink from nsink on
-    int first, count;     // this CTA's part of the list
-};
-
-__device__ __forceinline__ int tile_of(const Item& it, int i) {
-    return i < it.nsink ? i : it.t0 + i - it.nsink;
+__device__ __forceinline__ int tile_start(const Item& it, int i) {
+    return i < it.nsink ? i * kKeys : it.lo + (i - it.nsink) * kKeys;
+}
+__device__ __forceinline__ int tile_end(const Item& it, int i) {
+    return i < it.nsink ? it.sinks : it.hi;
 }
 
 struct AttnPlan {
     bool rows_mode;
     int tok_shift;  // log2 tokens of a work item
-    int nsplit;     // CTAs over an item's K/V tiles
+    int nsplit;     // work items over a query tile's K/V tiles
     int items;
 };
 
@@ -182,8 +199,9 @@ __device__ __noinline__ void redo_row(const AttnParams& p, const Item& it, size_
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
     for (int i = first; i < it.count; i += step) {
-        const int j0 = tile_of(it, it.first + i) * kKeys;
-        attn_row<D>(p.q + row * D, p.k + cache, p.v + cache, j0, j0 + kKeys, lo, hi, it.sinks,
+        const int j0 = tile_start(it, it.first + i);
+        attn_row<D>(p.q + row * D, p.k + cache, p.v + cache, j0,
+                    min(j0 + kKeys, tile_end(it, it.first + i)), lo, hi, it.sinks,
                     p.negate ? -p.scale_log2 : p.scale_log2, m, l, o);
     }
     if (p.pieces == 0) {
@@ -209,16 +227,21 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
-// Warp 0: the sequence and rows of work item x, and the K/V tiles it reads.
-// Sequence b's items start at floor(q_start[b] / tok) + b: enough for its
-// rows wherever they start, so no prefix sum over the sequences is needed.
-__device__ bool find_item(const AttnParams& p, int x, int tok_shift, int split, int nsplit, Item* it) {
+// One warp: the sequence and rows of query tile x, and its part of the K/V
+// tiles. Sequence b's tiles start at index floor(q_start[b] / tok) + b: enough
+// for its rows wherever they start, so no prefix sum over the sequences is
+// needed. False where the tile holds no rows.
+__device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int work, Item* it) {
     const int lane = threadIdx.x & 31;
+    // The last tiles (the longest rows of a causal prompt) come first.
+    const int split = work % pl.nsplit;
+    const int rest = work / pl.nsplit;
+    const int x = pl.items - 1 - rest / p.Hkv;
     int b = 0, len = p.N;
     while (len > 1) {
         const int step = (len + 31) >> 5;
         const int i = b + lane * step;
-        const bool le = lane * step < len && (p.q_start[i] >> tok_shift) + i <= x;
+        const bool le = lane * step < len && (p.q_start[i] >> pl.tok_shift) + i <= x;
         const unsigned hit = __ballot_sync(0xffffffffu, le);
         const int top = hit ? 31 - __clz(hit) : 0;
         b += top * step;
@@ -226,215 +249,279 @@ __device__ bool find_item(const AttnParams& p, int x, int tok_shift, int split, 
     }
     SeqRange r;
     if (!seq_range(p.q_start, p.kv_len, b, p.T, p.S, p.causal, p.dev_err, &r)) return false;
-    const int rel = (x - (r.q0 >> tok_shift) - b) << tok_shift;
+    const int rel = (x - (r.q0 >> pl.tok_shift) - b) << pl.tok_shift;
     if (rel < 0 || rel >= r.n) return false;
     it->seq = b;
     it->tok0 = r.q0 + rel;
-    it->ntok = min(1 << tok_shift, r.n - rel);
+    it->ntok = min(1 << pl.tok_shift, r.n - rel);
     it->pos0 = r.kv - r.n + rel;
     it->hi = p.causal ? it->pos0 + it->ntok : r.kv;
     it->lo = (p.causal && p.window > 0) ? max(0, it->pos0 + 1 - p.window) : 0;
     it->sinks = p.causal ? p.sinks : 0;
-    it->nsink = (min(it->sinks, it->lo) + kKeys - 1) / kKeys;
-    it->t0 = max(it->nsink, it->lo / kKeys);
-    const int tiles = it->nsink + max(0, (it->hi + kKeys - 1) / kKeys - it->t0);
-    const int per = (tiles + nsplit - 1) / nsplit;
+    if (it->sinks >= it->lo) {
+        it->lo = 0;  // one range
+        it->nsink = 0;
+    } else {
+        it->nsink = (it->sinks + kKeys - 1) / kKeys;
+    }
+    const int tiles = it->nsink + (it->hi - it->lo + kKeys - 1) / kKeys;
+    const int per = (tiles + pl.nsplit - 1) / pl.nsplit;
     it->first = split * per;
     it->count = max(0, min(tiles - it->first, per));
+    it->kvh = rest % p.Hkv;
+    it->split = split;
+    it->stop = 0;
     return true;
+}
+
+// Bits [0, n) of a 32-key chunk.
+__device__ __forceinline__ uint32_t below(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     lf_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const AttnParams p, const AttnPlan pl) {
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnParams p,
+                   const __grid_constant__ AttnPlan pl) {
     using L = AttnSmem<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-    uint64_t* full = q_full + 1;
+    uint64_t* q_empty = q_full + 2;
+    uint64_t* full = q_empty + 2;
     uint64_t* empty = full + L::kStages;
     uint64_t* s_full = empty + L::kStages;
     uint64_t* p_full = s_full + 2;
     uint64_t* o_done = p_full + 2;
-    uint64_t* drain = o_done + 2;
-    volatile int* misc = reinterpret_cast<int*>(smem + L::kMiscOff);  // [0] TMEM base, [1] abort, [2] work
-    __shared__ Item s_item;
+    uint64_t* o_free = o_done + 2;
+    uint64_t* item_full = o_free + 2;
+    uint64_t* item_empty = item_full + kItemSlots;
+    uint64_t* drain = item_empty + kItemSlots;
+    uint64_t* next = drain + 1;
+    uint64_t* want = next + 1;
+    Item* items = reinterpret_cast<Item*>(smem + L::kItemOff);
+    volatile uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
     const int lane = tid & 31;
-    // The last items (the longest rows of a causal prompt) start first.
-    const int split = blockIdx.x % pl.nsplit;
-    const int rest = blockIdx.x / pl.nsplit;
-    const int kvh = rest % p.Hkv;
-    const int x = pl.items - 1 - rest / p.Hkv;
 
     allow_dependent_launch();
-    if (warp == 0) {
-        Item it;
-        const bool ok = find_item(p, x, pl.tok_shift, split, pl.nsplit, &it);
-        if (lane == 0) {
-            if (ok) s_item = it;
-            misc[1] = 0;
-            misc[2] = ok;
-        }
-    } else if (warp == 8) {
+    if (warp == 8) {
         tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kMiscOff), 512);
     } else if (warp == 9 && lane == 0) {
-        mbar_init(q_full, 1);
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 1);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 4);
             mbar_init(&o_done[s], 1);
+            mbar_init(&o_free[s], 4);
+        }
+        for (int s = 0; s < kItemSlots; ++s) {
+            mbar_init(&item_full[s], 1);
+            mbar_init(&item_empty[s], 10);  // producer, products, eight softmax warps
         }
         mbar_init(drain, 1);
+        mbar_init(next, 1);
+        mbar_init(want, 1);
         fence_barrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = static_cast<uint32_t>(misc[0]);
-    const Item it = s_item;
-    // Work units of the streams: unit j belongs to stream j & 1 and reads K/V
-    // tile j >> 1 (rows mode) or j (keys mode) of the CTA's part of the list.
+    const uint32_t tmem = misc[0];
+    // Work units of the streams: unit j of an item belongs to stream j & 1 and
+    // reads K/V tile j >> 1 (rows mode) or j (keys mode) of the item's part of
+    // the list.
     const bool rows = pl.rows_mode;
-    const int units = misc[2] ? (rows ? 2 * it.count : it.count) : 0;
-    const int g = p.Hq / p.Hkv;
-    const int gs = __ffs(g) - 1;
+    const int gs = __ffs(p.Hq / p.Hkv) - 1;
 
     // A wait of a whole warp: every lane learns whether all of them saw the
     // barrier complete.
     auto warp_wait = [&](uint64_t* bar, int parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_limit_ns)) != 0;
     };
-    auto give_up = [&]() {
-        misc[1] = 1;
-        atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT);
-    };
+    auto give_up = [&]() { atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT); };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 9) {
-        // ------------------------------------------------------- producer --
-        if (lane == 0 && units > 0) {
-            const int unit = it.seq * p.Hkv + kvh;
-            mbar_arrive_expect_tx(q_full, (rows ? 2 : 1) * L::kTileBytes);
-            for (int s = 0; s < (rows ? 2 : 1); ++s)
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load(smem + s * L::kTileBytes + c * kPanel, &tmQ, c * 64, kvh * g,
-                             it.tok0 + s * (kRows >> gs), q_full);
-            int n = 0;  // ring entries issued
+        if (warp == 9 && lane == 0) {
+            // --------------------------------------------------- producer --
+            int n = 0;     // ring entries issued
+            int done = 0;  // items with work
             bool ok = true;
-            auto load = [&](const CUtensorMap* map, int i) {
-                const int st = n % L::kStages;
-                if (!mbar_wait(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_limit_ns)) return false;
-                mbar_arrive_expect_tx(&full[st], L::kTileBytes);
-                uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes;
-                const int y = tile_of(it, it.first + i) * kKeys;
-                for (int c = 0; c < D / 64; ++c)
-                    for (int h = 0; h < 2; ++h)
-                        tma_load(dst + c * kPanel + h * (kPanel / 2), map, c * 64, y + h * 64, unit,
-                                 &full[st]);
-                ++n;
-                return true;
-            };
-            // The order in which the products take the tiles.
-            ok = load(&tmK, 0);
-            if (ok && !rows && units > 1) ok = load(&tmK, 1);
-            for (int j = 0; ok && j < units; ++j) {
-                if (rows && (j & 1)) continue;
-                ok = load(&tmV, rows ? j >> 1 : j);
-                if (ok && j + 2 < units) ok = load(&tmK, rows ? (j >> 1) + 1 : j + 2);
+            for (int w = 0;; ++w) {
+                const int slot = w % kItemSlots;
+                ok = mbar_wait(&item_full[slot], (w / kItemSlots) & 1, p.wait_limit_ns);
+                if (!ok) break;
+                const Item& it = items[slot];
+                if (it.stop) break;
+                const int units = rows ? 2 * it.count : it.count;
+                if (units > 0) {
+                    const int unit = it.seq * p.Hkv + it.kvh;
+                    // Q: both tiles in rows mode, alternating buffers in keys mode.
+                    const int qb = rows ? 0 : done & 1;
+                    const int use = rows ? done : done >> 1;
+                    ok = mbar_wait(&q_empty[qb], (use & 1) ^ 1, p.wait_limit_ns);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&q_full[qb], (rows ? 2 : 1) * L::kTileBytes);
+                    for (int s = 0; s < (rows ? 2 : 1); ++s)
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load(smem + (s + qb) * L::kTileBytes + c * kPanel, &tmQ, c * 64,
+                                     it.kvh << gs, it.tok0 + s * (kRows >> gs), &q_full[qb]);
+                    auto load = [&](const CUtensorMap* map, int i) {
+                        const int st = n % L::kStages;
+                        if (!mbar_wait(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_limit_ns))
+                            return false;
+                        uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes;
+                        const int y = tile_start(it, it.first + i);
+                        // The second half only where it holds a key.
+                        const int halves = tile_end(it, it.first + i) - y > 64 ? 2 : 1;
+                        mbar_arrive_expect_tx(&full[st], halves * (L::kTileBytes / 2));
+                        for (int h = 0; h < halves; ++h)
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load(dst + c * kPanel + h * (kPanel / 2), map, c * 64, y + h * 64,
+                                         unit, &full[st]);
+                        ++n;
+                        return true;
+                    };
+                    // Late enough that another CTA may still be the one to take
+                    // the next item, early enough that it is found in time.
+                    const int ask = max(0, units - (rows ? 2 * kAskTiles : kAskTiles));
+                    // The order in which the products take the tiles.
+                    ok = load(&tmK, 0);
+                    if (ok && !rows && units > 1) ok = load(&tmK, 1);
+                    for (int j = 0; ok && j < units; ++j) {
+                        if (rows && (j & 1)) continue;
+                        if (j == ask) mbar_arrive(want);
+                        ok = load(&tmV, rows ? j >> 1 : j);
+                        if (ok && j + 2 < units) ok = load(&tmK, rows ? (j >> 1) + 1 : j + 2);
+                    }
+                    if (!ok) break;
+                    ++done;
+                } else {
+                    mbar_arrive(want);
+                }
+                mbar_arrive(&item_empty[slot]);
             }
             if (!ok) {
                 give_up();
                 // No copy may be in flight when the CTA leaves.
-                mbar_wait(q_full, 0);
                 for (int k = max(0, n - L::kStages); k < n; ++k)
                     mbar_wait(&full[k % L::kStages], (k / L::kStages) & 1);
+                for (int k = max(0, done - 1); k < done + 1; ++k) {
+                    const int use = rows ? k : k >> 1;
+                    mbar_wait(&q_full[rows ? 0 : k & 1], use & 1, 1000000);
+                }
             }
-        }
-    } else if (warp == 8) {
-        // ------------------------------------------------ matrix products --
-        if (units > 0) {
+        } else if (warp == 8) {
+            // -------------------------------------------- matrix products --
             const uint32_t idesc_s = instr_desc(kRows, kKeys, false) | (p.negate ? kInstrNegateA : 0u);
             constexpr uint32_t idesc_o = instr_desc(kRows, D, true);
-            const uint32_t qs = smem_u32(smem);
             const uint32_t ring = smem_u32(smem + L::kRingOff);
-            int n = 0;            // ring entries taken
-            int kst = 0, vst = 0; // stages of the current K and V tiles
-            bool ok = warp_wait(q_full, 0);
-            auto take = [&](int* st) {
-                *st = n % L::kStages;
-                const bool got = warp_wait(&full[*st], (n / L::kStages) & 1);
-                ++n;
-                return got;
-            };
-            // S of unit j: Q tile times K tile.
-            auto scores = [&](int j) {
-                const int s = j & 1;
-                if (!(rows && s) && !take(&kst)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t qa = qs + (rows && s ? L::kTileBytes : 0);
-                    const uint32_t ka = ring + kst * L::kTileBytes;
+            int n = 0;                  // ring entries taken
+            int done = 0;               // items with work
+            int pdone[2] = {0, 0};      // units of each stream whose P was taken
+            int odone[2] = {0, 0};      // items in which each stream had units
+            int kst = 0, vst = 0;       // stages of the current K and V tiles
+            bool ok = true;
+            for (int w = 0;; ++w) {
+                const int slot = w % kItemSlots;
+                ok = warp_wait(&item_full[slot], (w / kItemSlots) & 1);
+                if (!ok) break;
+                const Item& it = items[slot];
+                if (it.stop) break;
+                const int units = rows ? 2 * it.count : it.count;
+                if (units > 0) {
+                    const int qb = rows ? 0 : done & 1;
+                    const uint32_t qs = smem_u32(smem) + qb * L::kTileBytes;
+                    ok = warp_wait(&q_full[qb], (rows ? done : done >> 1) & 1);
+                    auto take = [&](int* st) {
+                        *st = n % L::kStages;
+                        const bool got = warp_wait(&full[*st], (n / L::kStages) & 1);
+                        ++n;
+                        return got;
+                    };
+                    // S of unit j: Q tile times K tile.
+                    auto scores = [&](int j) {
+                        const int s = j & 1;
+                        if (!(rows && s) && !take(&kst)) return false;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint32_t qa = qs + (rows && s ? L::kTileBytes : 0);
+                            const uint32_t ka = ring + kst * L::kTileBytes;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-                        mma_ss(tmem + s * kKeys, smem_desc(qa + off, 16, 1024),
-                               smem_desc(ka + off, 16, 1024), idesc_s, k > 0);
-                    }
-                    if (!rows || s) mma_commit(&empty[kst]);
-                    mma_commit(&s_full[s]);
-                }
-                __syncwarp();
-                return true;
-            };
-            ok = ok && scores(0);
-            if (ok && units > 1) ok = scores(1);
-            for (int j = 0; ok && j < units; ++j) {
-                const int s = j & 1;
-                if (!(rows && s)) {
-                    ok = take(&vst);
-                    if (!ok) break;
-                    // Cache rows that no row of the item sees: zero, so that
-                    // 0 * garbage stays 0.
-                    const int j0 = tile_of(it, it.first + (rows ? j >> 1 : j)) * kKeys;
-                    if (j0 + kKeys > it.hi || (j0 < it.lo && j0 + kKeys > it.sinks)) {
-                        uint8_t* vt = smem + L::kRingOff + vst * L::kTileBytes;
-                        for (int i = lane; i < kKeys * (D / 64) * 8; i += 32) {
-                            const int r = (i >> 3) & (kKeys - 1);
-                            const int key = j0 + r;
-                            if (key >= it.hi || (key < it.lo && key >= it.sinks))
-                                *reinterpret_cast<uint4*>(vt + (i >> 10) * kPanel + r * 128 +
-                                                          (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
+                                mma_ss(tmem + s * kKeys, smem_desc(qa + off, 16, 1024),
+                                       smem_desc(ka + off, 16, 1024), idesc_s, k > 0);
+                            }
+                            mma_commit(&s_full[s]);
+                            if (!rows || s) mma_commit(&empty[kst]);
+                            if (j == units - 1) mma_commit(&q_empty[qb]);
                         }
-                        fence_proxy_async_smem();
                         __syncwarp();
-                    }
-                }
-                if (!warp_wait(&p_full[s], (j >> 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t va = ring + vst * L::kTileBytes;
+                        return true;
+                    };
+                    ok = ok && scores(0);
+                    if (ok && units > 1) ok = scores(1);
+                    for (int j = 0; ok && j < units; ++j) {
+                        const int s = j & 1;
+                        if (!(rows && s)) {
+                            ok = take(&vst);
+                            if (!ok) break;
+                            // V rows behind the tile's last key (and what an
+                            // earlier tile left there): zero, so that
+                            // 0 * garbage stays 0.
+                            const int i = it.first + (rows ? j >> 1 : j);
+                            const int keep = tile_end(it, i) - tile_start(it, i);
+                            if (keep < kKeys) {
+                                uint8_t* vt = smem + L::kRingOff + vst * L::kTileBytes;
+                                for (int c = 0; c < D / 64; ++c)
+                                    for (int e = keep * 8 + lane; e < kKeys * 8; e += 32)
+                                        *reinterpret_cast<uint4*>(vt + c * kPanel + e * 16) =
+                                            make_uint4(0, 0, 0, 0);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                        }
+                        if (j < 2) {
+                            // The stream's previous O has been read.
+                            if (odone[s] > 0 && !warp_wait(&o_free[s], (odone[s] - 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            ++odone[s];
+                        }
+                        if (!warp_wait(&p_full[s], pdone[s] & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        ++pdone[s];
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint32_t va = ring + vst * L::kTileBytes;
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(tmem + 2 * kKeys + s * D, tmem + s * kKeys + k * 8,
-                               smem_desc(va + k * 2048, kPanel, 1024), idesc_o, j > 1 || k > 0);
-                    if (!rows || s) mma_commit(&empty[vst]);
-                    mma_commit(&o_done[s]);
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                mma_ts(tmem + 2 * kKeys + s * D, tmem + s * kKeys + k * 8,
+                                       smem_desc(va + k * 2048, kPanel, 1024), idesc_o, j > 1 || k > 0);
+                            mma_commit(&o_done[s]);
+                            if (!rows || s) mma_commit(&empty[vst]);
+                        }
+                        __syncwarp();
+                        if (j + 2 < units) ok = scores(j + 2);
+                    }
+                    if (!ok) break;
+                    ++done;
                 }
-                __syncwarp();
-                if (j + 2 < units) ok = scores(j + 2);
+                if (lane == 0) mbar_arrive(&item_empty[slot]);
             }
             if (!ok && lane == 0) give_up();
             // No product may be in flight when tensor memory is freed.
@@ -443,168 +530,228 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mbar_wait(drain, 0);
             }
             __syncwarp();
+        } else if (warp == 10) {
+            // ------------------------------------------------- next items --
+            int w = 0;  // items handed out
+            bool ok = true;
+            int work = blockIdx.x;
+            for (int round = 0;; ++round) {
+                Item it;
+                if (work >= 0) {
+                    if (find_item(p, pl, work, &it)) {
+                        it.stop = 0;
+                    } else {
+                        it.stop = -1;  // no rows here: ask again
+                    }
+                } else {
+                    it.stop = 1;
+                }
+                if (it.stop >= 0) {
+                    const int slot = w % kItemSlots;
+                    ok = warp_wait(&item_empty[slot], ((w / kItemSlots) & 1) ^ 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        items[slot] = it;
+                        mbar_arrive(&item_full[slot]);
+                    }
+                    __syncwarp();
+                    if (it.stop) break;
+                    ok = warp_wait(want, w & 1);
+                    if (!ok) break;
+                    ++w;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(next, 16);
+                    cancel_next_cta(smem + L::kNextOff, next);
+                }
+                ok = warp_wait(next, round & 1);
+                if (!ok) break;
+                work = cancelled_cta(smem + L::kNextOff);
+                fence_proxy_async_smem();  // the answer is read before the next one lands
+                __syncwarp();
+            }
+            if (!ok && lane == 0) {
+                give_up();
+                mbar_wait(next, 0, 1000000);  // an answer under way lands before the CTA leaves
+                mbar_wait(next, 1, 1000000);
+            }
         }
-    }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    if (misc[2]) {
         // --------------------------------------------------------- softmax --
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int s = warp >> 2;
         const int r = tid & (kRows - 1);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's lanes
         const uint32_t ts = tmem + lanes + s * kKeys;
         const uint32_t to = tmem + lanes + 2 * kKeys + s * D;
         const int tt = (rows && s ? kRows >> gs : 0) + (r >> gs);  // token of the item
-        const bool valid = tt < it.ntok;
-        const bool any_valid = __any_sync(0xffffffffu, valid);
-        const int row_hi = p.causal ? it.pos0 + tt + 1 : it.hi;
-        const int row_lo = (p.causal && p.window > 0) ? max(0, row_hi - p.window) : 0;
-        // Keys every row of the warp sees: [all_lo, all_hi), and below sinks.
-        const int all_hi = __shfl_sync(0xffffffffu, row_hi, 0);
-        const int all_lo = __shfl_sync(0xffffffffu, row_lo, 31);
         const float c = p.scale_log2;
         const uint64_t c2 = pack_f32x2(c, c);
-        float m = -INFINITY, l = 0.f;
-        int n = 0;  // units of this stream done
+        int n = 0;  // units of this stream so far
         bool ok = true;
-        for (int j = s; j < units; j += 2, ++n) {
-            if (!warp_wait(&s_full[s], n & 1)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            if (any_valid) {
-                const int j0 = tile_of(it, it.first + (rows ? j >> 1 : j)) * kKeys;
-                uint32_t x[kKeys];
-#pragma unroll
-                for (int k = 0; k < kKeys; k += 32) tmem_ld32(ts + k, x + k);
-                tmem_wait_ld();
-                if (!(j0 + kKeys <= all_hi && (j0 >= all_lo || j0 + kKeys <= it.sinks))) {
-                    const int h = row_hi - j0, lw = row_lo - j0, sk = it.sinks - j0;
-#pragma unroll
-                    for (int k = 0; k < kKeys; ++k)
-                        if (!(k < h && (k >= lw || k < sk))) x[k] = 0xff800000u;
+        for (int w = 0;; ++w) {
+            const int slot = w % kItemSlots;
+            ok = warp_wait(&item_full[slot], (w / kItemSlots) & 1);
+            if (!ok) break;
+            const Item& it = items[slot];
+            if (it.stop) break;
+            const int units = rows ? 2 * it.count : it.count;
+            const bool valid = tt < it.ntok;
+            const bool any_valid = __any_sync(0xffffffffu, valid);
+            const int row_hi = p.causal ? it.pos0 + tt + 1 : it.hi;
+            const int row_lo = (p.causal && p.window > 0) ? max(0, row_hi - p.window) : 0;
+            // Keys every row of the warp sees: [all_lo, all_hi), and below sinks.
+            const int all_hi = __shfl_sync(0xffffffffu, row_hi, 0);
+            const int all_lo = __shfl_sync(0xffffffffu, row_lo, 31);
+            float m = -INFINITY, l = 0.f;
+            for (int j = s; j < units; j += 2, ++n) {
+                if (!warp_wait(&s_full[s], n & 1)) {
+                    ok = false;
+                    break;
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tc_fence_after();
+                if (any_valid) {
+                    const int i = it.first + (rows ? j >> 1 : j);
+                    const int j0 = tile_start(it, i);
+                    const int end = tile_end(it, i);
+                    uint32_t x[kKeys];
 #pragma unroll
-                for (int k = 0; k < kKeys; k += 8)
+                    for (int k = 0; k < kKeys; k += 32) tmem_ld32(ts + k, x + k);
+                    tmem_wait_ld();
+                    if (!(j0 + kKeys <= min(all_hi, end) && (j0 >= all_lo || j0 + kKeys <= it.sinks))) {
+                        const int h = min(row_hi, end) - j0, lw = row_lo - j0, sk = it.sinks - j0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[k + e]),
-                                                   __uint_as_float(x[k + e + 4])));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                const bool grow = m != -INFINITY && top > m + kRescale;
-                if (__any_sync(0xffffffffu, grow)) {
-                    // n >= 1 here: m was set by an earlier unit.
-                    if (!warp_wait(&o_done[s], (n - 1) & 1)) {
-                        ok = false;
-                        break;
+                        for (int k = 0; k < kKeys; k += 32) {
+                            const uint32_t vis = below(h - k) & (~below(lw - k) | below(sk - k));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(vis & (1u << e))) x[k + e] = 0xff800000u;
+                        }
                     }
-                    tc_fence_after();
-                    const float f = grow ? ex2_approx(m - top) : 1.f;
-                    l *= f;
-                    const uint64_t f2 = pack_f32x2(f, f);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + k, o);
-                        tmem_wait_ld();
+                    for (int k = 0; k < kKeys; k += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[k + e]),
+                                                       __uint_as_float(x[k + e + 4])));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    const bool grow = m != -INFINITY && top > m + kRescale;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        // Not the item's first unit: m was set by an earlier one.
+                        if (!warp_wait(&o_done[s], (n - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const float f = grow ? ex2_approx(m - top) : 1.f;
+                        l *= f;
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(to + k, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(to + k, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    if (grow || m == -INFINITY) m = top;
+                    const float base = m == -INFINITY ? 0.f : -m;
+                    const uint64_t b2 = pack_f32x2(base, base);
+                    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int k = 0; k < kKeys; k += 32) {
+                        uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float a, b;
-                            unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[e]),
-                                                              __uint_as_float(o[e + 1])), f2), a, b);
-                            o[e] = __float_as_uint(a);
-                            o[e + 1] = __float_as_uint(b);
+                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[k + e]),
+                                                              __uint_as_float(x[k + e + 1])), c2, b2), a, b);
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                            sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
+                            pk[e >> 1] = pack_bf16x2(a, b);
                         }
-                        tmem_st32(to + k, o);
+                        tmem_st16(ts + (k >> 1), pk);
                     }
                     tmem_wait_st();
+                    float a, b;
+                    unpack_f32x2(add_f32x2(sum[0], sum[1]), a, b);
+                    l += a + b;
                 }
-                if (grow || m == -INFINITY) m = top;
-                const float base = m == -INFINITY ? 0.f : -m;
-                const uint64_t b2 = pack_f32x2(base, base);
-                uint64_t sum[2] = {0ull, 0ull};
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[s]);
+            }
+            if (!ok) break;
+            const bool worked = units > s;  // the stream had a unit
+            if (worked) {
+                ok = warp_wait(&o_done[s], (n - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const size_t row = static_cast<size_t>(it.tok0 + tt) * p.Hq + (it.kvh << gs) +
+                               (r & ((1 << gs) - 1));
+            const int piece = rows ? it.split : it.split * 2 + s;
+            const size_t at = static_cast<size_t>(piece) * p.T * p.Hq + row;
+            const bool some = valid && l != 0.f;
+            float bad = l * 0.f;  // 0 unless a value is not finite
+            if (any_valid) {
+                const float il = some ? 1.f / l : 0.f;
 #pragma unroll
-                for (int k = 0; k < kKeys; k += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float a, b;
-                        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[k + e]),
-                                                          __uint_as_float(x[k + e + 1])), c2, b2), a, b);
-                        a = ex2_approx(a);
-                        b = ex2_approx(b);
-                        sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
-                        w[e >> 1] = pack_bf16x2(a, b);
+                for (int k = 0; k < D; k += 32) {
+                    uint32_t o[32];
+                    if (worked) {
+                        tmem_ld32(to + k, o);
+                        tmem_wait_ld();
                     }
-                    tmem_st16(ts + (k >> 1), w);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if (!some) o[e] = 0u;
+                        bad = fmaf(__uint_as_float(o[e]), 0.f, bad);
+                    }
+                    if (p.pieces == 0) {
+                        if (valid) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                uint4 v;
+                                v.x = pack_bf16x2(__uint_as_float(o[e]) * il, __uint_as_float(o[e + 1]) * il);
+                                v.y = pack_bf16x2(__uint_as_float(o[e + 2]) * il, __uint_as_float(o[e + 3]) * il);
+                                v.z = pack_bf16x2(__uint_as_float(o[e + 4]) * il, __uint_as_float(o[e + 5]) * il);
+                                v.w = pack_bf16x2(__uint_as_float(o[e + 6]) * il, __uint_as_float(o[e + 7]) * il);
+                                *reinterpret_cast<uint4*>(p.out + row * D + k + e) = v;
+                            }
+                        }
+                    } else if (some) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(p.part_o + at * D + k + e) =
+                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
                 }
-                tmem_wait_st();
-                float a, b;
-                unpack_f32x2(add_f32x2(sum[0], sum[1]), a, b);
-                l += a + b;
+                if (valid && p.pieces > 0) p.part_ml[at] = make_float2(m, l);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[s]);
-        }
-        if (ok && n > 0) ok = warp_wait(&o_done[s], (n - 1) & 1);
-        if (!ok && lane == 0) give_up();
-        tc_fence_after();
-        if (ok && any_valid) {
-            const size_t row = static_cast<size_t>(it.tok0 + tt) * p.Hq + kvh * g + (r & (g - 1));
-            const int piece = rows ? split : split * 2 + s;
-            const size_t at = static_cast<size_t>(piece) * p.T * p.Hq + row;
-            const bool some = valid && l != 0.f;
-            // 0 unless a value is not finite.
-            float bad = l * 0.f;
-            const float il = some ? 1.f / l : 0.f;
-#pragma unroll
-            for (int k = 0; k < D; k += 32) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(to + k, o);
-                    tmem_wait_ld();
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    if (!some) o[e] = 0u;
-                    bad = fmaf(__uint_as_float(o[e]), 0.f, bad);
-                }
-                if (p.pieces == 0) {
-                    if (valid) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 w;
-                            w.x = pack_bf16x2(__uint_as_float(o[e]) * il, __uint_as_float(o[e + 1]) * il);
-                            w.y = pack_bf16x2(__uint_as_float(o[e + 2]) * il, __uint_as_float(o[e + 3]) * il);
-                            w.z = pack_bf16x2(__uint_as_float(o[e + 4]) * il, __uint_as_float(o[e + 5]) * il);
-                            w.w = pack_bf16x2(__uint_as_float(o[e + 6]) * il, __uint_as_float(o[e + 7]) * il);
-                            *reinterpret_cast<uint4*>(p.out + row * D + k + e) = w;
-                        }
-                    }
-                } else if (some) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4*>(p.part_o + at * D + k + e) =
-                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                }
-            }
-            if (valid && p.pieces > 0) p.part_ml[at] = make_float2(m, l);
-            __syncwarp();
-            unsigned redo = __ballot_sync(0xffffffffu, some && !(bad == 0.f));
-            for (; redo; redo &= redo - 1) {
+            if (worked && lane == 0) mbar_arrive(&o_free[s]);
+            for (unsigned redo = __ballot_sync(0xffffffffu, some && !(bad == 0.f)); redo;
+                 redo &= redo - 1) {
                 const int from = __ffs(redo) - 1;
-                const unsigned lo32 = static_cast<unsigned>(row), hi32 = static_cast<unsigned>(row >> 32);
-                const size_t rr = static_cast<size_t>(__shfl_sync(0xffffffffu, hi32, from)) << 32 |
-                                  __shfl_sync(0xffffffffu, lo32, from);
-                redo_row<D>(p, s_item, rr, (static_cast<size_t>(it.seq) * p.Hkv + kvh) * p.S * D,
+                const size_t rr =
+                    static_cast<size_t>(__shfl_sync(0xffffffffu, static_cast<unsigned>(row >> 32), from))
+                        << 32 |
+                    __shfl_sync(0xffffffffu, static_cast<unsigned>(row), from);
+                redo_row<D>(p, it, rr, (static_cast<size_t>(it.seq) * p.Hkv + it.kvh) * p.S * D,
                             rows ? 0 : s, rows ? 1 : 2, __shfl_sync(0xffffffffu, row_lo, from),
                             __shfl_sync(0xffffffffu, row_hi, from), piece);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[slot]);
         }
-    }
+        if (!ok && lane == 0) give_up();
     }
     tc_fence_before();
     __syncthreads();
