@@ -23,21 +23,27 @@
 // under the epilogue of the one before. Its warps:
 //   warps 0-3, 4-7  softmax of stream 0, 1; a thread owns a row: S from
 //                   tensor memory, m, l, P (bf16) back over S, at the end O
-//   warp 8          issues S = Q K^T (both in shared memory) and O += P V (P
-//                   in tensor memory, V as it lies in the cache)
+//   warp 8          one thread issues S = Q K^T (both in shared memory) and
+//                   O += P V (P in tensor memory, V as it lies in the cache)
 //   warp 9          TMA loads: Q, then K and V tiles through a ring
 //   warp 10         next work item: cancels a pending CTA, finds the item's
 //                   sequence, rows and tiles, hands it to the others
-//   warp 11         nothing (it completes the third warpgroup)
-// The reference m is not the exact running maximum: it moves, and O is
-// rescaled, only when a row's maximum grows by more than 2^8, which l and O
-// hold easily in fp32 (most rows rescale once or never).
+//   warp 11         zeroes the rows of V tiles behind a range's last key
+// A tensor product of 128 x 128 x 128 takes 512 cycles; a pair of tiles needs
+// four of them per 128 keys, and the two streams' softmax must fit in between.
+// So the chain from S to P is kept short: the exponentials start on the first
+// 32 columns of S, with the reference m left by the tiles before. m moves to
+// a row's maximum only after a tile that exceeds it by more than 2^8 (O and l
+// are rescaled before the next tile's P), which is rare. Until then the
+// weights stay as they are, relative precision and all: bf16 and fp32 hold up
+// to 2^127, and a row that outgrows 2^100 within one tile is computed again. P is handed over in two halves, the first
+// while the second is still in the making.
 // P is rounded to bf16 (2^-9 of each weight) because the tensor cores take
 // it; l sums the unrounded weights.
 //
 // Keys a row does not see are removed by select before the exponentials, and
-// cache rows no row of the tile sees are zeroed in shared memory, so what
-// lies there does not matter. A NaN or infinity in a row that others of the
+// what a V tile holds behind the range's last key is zeroed in shared memory,
+// so it does not matter what lies there. A NaN or infinity in a row that others of the
 // tile do see would still reach this row's O as 0 * NaN: a row whose result
 // is not finite is computed again by attn_row, key by key.
 #include <math.h>
@@ -63,6 +69,7 @@ constexpr int kSoftmaxRegs = 224;
 constexpr int kOtherRegs = 56;
 constexpr int kPanel = kRows * 128;  // bytes of 64 columns of a tile
 constexpr float kRescale = 8.f;      // log2 growth of the maximum that moves m
+constexpr float kMaxGrowth = 100.f;  // log2 growth within one tile that l and O are trusted with
 
 constexpr int kItemSlots = 3;        // items in flight between the warps
 constexpr int kAskTiles = 2;         // K/V tiles of an item left to load when the next is asked for
@@ -86,12 +93,13 @@ struct AttnSmem {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRingOff = 2 * kTileBytes;  // after the two Q tiles
     static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
-    // barriers: q_full[2], q_empty[2], full[], empty[], s_full[2], p_full[2],
-    // o_done[2], o_free[2], item_full[], item_empty[], drain, next, want
-    static constexpr int kBars = 4 + 2 * kStages + 8 + 2 * kItemSlots + 3;
+    // barriers: q_full[2], q_empty[2], full[], empty[], s_full[2], p_half[2],
+    // p_full[2], o_done[2], o_free[2], item_full[], item_empty[], v_ask,
+    // v_clean, drain, next, want
+    static constexpr int kBars = 4 + 2 * kStages + 10 + 2 * kItemSlots + 5;
     static constexpr int kItemOff = kBarOff + kBars * 8;
     static constexpr int kNextOff = (kItemOff + kItemSlots * static_cast<int>(sizeof(Item)) + 15) / 16 * 16;
-    static constexpr int kMiscOff = kNextOff + 16;  // TMEM base, abort flag
+    static constexpr int kMiscOff = kNextOff + 16;  // TMEM base; V tile to clean, its rows to keep
     static constexpr int kAlloc = kMiscOff + 16 + 1024;
     static_assert(kAlloc <= 232448, "shared memory of a CTA");
 };
@@ -293,19 +301,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* full = q_empty + 2;
     uint64_t* empty = full + L::kStages;
     uint64_t* s_full = empty + L::kStages;
-    uint64_t* p_full = s_full + 2;
+    uint64_t* p_half = s_full + 2;
+    uint64_t* p_full = p_half + 2;
     uint64_t* o_done = p_full + 2;
     uint64_t* o_free = o_done + 2;
     uint64_t* item_full = o_free + 2;
     uint64_t* item_empty = item_full + kItemSlots;
-    uint64_t* drain = item_empty + kItemSlots;
+    uint64_t* v_ask = item_empty + kItemSlots;
+    uint64_t* v_clean = v_ask + 1;
+    uint64_t* drain = v_clean + 1;
     uint64_t* next = drain + 1;
     uint64_t* want = next + 1;
     Item* items = reinterpret_cast<Item*>(smem + L::kItemOff);
     volatile uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
 
     const int tid = threadIdx.x;
-    const int warp = tid >> 5;
+    // From one lane, so the compiler knows that a warp's role is uniform.
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int lane = tid & 31;
 
     allow_dependent_launch();
@@ -320,6 +332,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(&q_full[s], 1);
             mbar_init(&q_empty[s], 1);
             mbar_init(&s_full[s], 1);
+            mbar_init(&p_half[s], 4);
             mbar_init(&p_full[s], 4);
             mbar_init(&o_done[s], 1);
             mbar_init(&o_free[s], 4);
@@ -328,6 +341,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(&item_full[s], 1);
             mbar_init(&item_empty[s], 10);  // producer, products, eight softmax warps
         }
+        mbar_init(v_ask, 1);
+        mbar_init(v_clean, 1);
         mbar_init(drain, 1);
         mbar_init(next, 1);
         mbar_init(want, 1);
@@ -336,7 +351,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0];
+    const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     // Work units of the streams: unit j of an item belongs to stream j & 1 and
     // reads K/V tile j >> 1 (rows mode) or j (keys mode) of the item's part of
     // the list.
@@ -421,20 +436,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     mbar_wait(&q_full[rows ? 0 : k & 1], use & 1, 1000000);
                 }
             }
-        } else if (warp == 8) {
+        } else if (warp == 8 && elect_one()) {
             // -------------------------------------------- matrix products --
+            // All of it in one thread: with the whole warp in the loop and
+            // only the products elected, 8 of them took 700 to 1000 cycles to
+            // issue instead of 300 (the queue's depth) to 500 (their rate).
             const uint32_t idesc_s = instr_desc(kRows, kKeys, false) | (p.negate ? kInstrNegateA : 0u);
             constexpr uint32_t idesc_o = instr_desc(kRows, D, true);
             const uint32_t ring = smem_u32(smem + L::kRingOff);
             int n = 0;                  // ring entries taken
             int done = 0;               // items with work
+            int cleaned = 0;            // V tiles that had rows to zero
             int pdone[2] = {0, 0};      // units of each stream whose P was taken
             int odone[2] = {0, 0};      // items in which each stream had units
             int kst = 0, vst = 0;       // stages of the current K and V tiles
+            bool clean = false;         // the V tile has rows to zero
             bool ok = true;
+            auto wait = [&](uint64_t* bar, int parity) {
+                return mbar_wait(bar, parity, p.wait_limit_ns);
+            };
             for (int w = 0;; ++w) {
                 const int slot = w % kItemSlots;
-                ok = warp_wait(&item_full[slot], (w / kItemSlots) & 1);
+                ok = wait(&item_full[slot], (w / kItemSlots) & 1);
                 if (!ok) break;
                 const Item& it = items[slot];
                 if (it.stop) break;
@@ -442,10 +465,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (units > 0) {
                     const int qb = rows ? 0 : done & 1;
                     const uint32_t qs = smem_u32(smem) + qb * L::kTileBytes;
-                    ok = warp_wait(&q_full[qb], (rows ? done : done >> 1) & 1);
+                    ok = wait(&q_full[qb], (rows ? done : done >> 1) & 1);
                     auto take = [&](int* st) {
                         *st = n % L::kStages;
-                        const bool got = warp_wait(&full[*st], (n / L::kStages) & 1);
+                        const bool got = wait(&full[*st], (n / L::kStages) & 1);
                         ++n;
                         return got;
                     };
@@ -454,20 +477,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         const int s = j & 1;
                         if (!(rows && s) && !take(&kst)) return false;
                         tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t qa = qs + (rows && s ? L::kTileBytes : 0);
-                            const uint32_t ka = ring + kst * L::kTileBytes;
+                        const uint32_t qa = qs + (rows && s ? L::kTileBytes : 0);
+                        const uint32_t ka = ring + kst * L::kTileBytes;
 #pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-                                mma_ss(tmem + s * kKeys, smem_desc(qa + off, 16, 1024),
-                                       smem_desc(ka + off, 16, 1024), idesc_s, k > 0);
-                            }
-                            mma_commit(&s_full[s]);
-                            if (!rows || s) mma_commit(&empty[kst]);
-                            if (j == units - 1) mma_commit(&q_empty[qb]);
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
+                            mma_ss(tmem + s * kKeys, smem_desc(qa + off, 16, 1024),
+                                   smem_desc(ka + off, 16, 1024), idesc_s, k > 0);
                         }
-                        __syncwarp();
+                        mma_commit(&s_full[s]);
+                        if (!rows || s) mma_commit(&empty[kst]);
+                        if (j == units - 1) mma_commit(&q_empty[qb]);
                         return true;
                     };
                     ok = ok && scores(0);
@@ -477,59 +497,74 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (!(rows && s)) {
                             ok = take(&vst);
                             if (!ok) break;
-                            // V rows behind the tile's last key (and what an
-                            // earlier tile left there): zero, so that
-                            // 0 * garbage stays 0.
                             const int i = it.first + (rows ? j >> 1 : j);
                             const int keep = tile_end(it, i) - tile_start(it, i);
-                            if (keep < kKeys) {
-                                uint8_t* vt = smem + L::kRingOff + vst * L::kTileBytes;
-                                for (int c = 0; c < D / 64; ++c)
-                                    for (int e = keep * 8 + lane; e < kKeys * 8; e += 32)
-                                        *reinterpret_cast<uint4*>(vt + c * kPanel + e * 16) =
-                                            make_uint4(0, 0, 0, 0);
-                                fence_proxy_async_smem();
-                                __syncwarp();
+                            clean = keep < kKeys;
+                            if (clean) {
+                                misc[1] = vst;
+                                misc[2] = keep;
+                                mbar_arrive(v_ask);
                             }
                         }
                         if (j < 2) {
                             // The stream's previous O has been read.
-                            if (odone[s] > 0 && !warp_wait(&o_free[s], (odone[s] - 1) & 1)) {
+                            if (odone[s] > 0 && !wait(&o_free[s], (odone[s] - 1) & 1)) {
                                 ok = false;
                                 break;
                             }
                             ++odone[s];
                         }
-                        if (!warp_wait(&p_full[s], pdone[s] & 1)) {
-                            ok = false;
-                            break;
+                        const uint32_t va = ring + vst * L::kTileBytes;
+                        if (clean && !(rows && s)) {
+                            ok = wait(v_clean, cleaned & 1);
+                            if (!ok) break;
+                            ++cleaned;
                         }
-                        ++pdone[s];
-                        tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t va = ring + vst * L::kTileBytes;
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
+                        for (int half = 0; half < 2; ++half) {
+                            if (!wait(half ? &p_full[s] : &p_half[s], pdone[s] & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = half * kKeys / 32; k < (half + 1) * kKeys / 32; ++k)
                                 mma_ts(tmem + 2 * kKeys + s * D, tmem + s * kKeys + k * 8,
                                        smem_desc(va + k * 2048, kPanel, 1024), idesc_o, j > 1 || k > 0);
-                            mma_commit(&o_done[s]);
-                            if (!rows || s) mma_commit(&empty[vst]);
                         }
-                        __syncwarp();
+                        if (!ok) break;
+                        ++pdone[s];
+                        mma_commit(&o_done[s]);
+                        if (!rows || s) mma_commit(&empty[vst]);
                         if (j + 2 < units) ok = scores(j + 2);
                     }
                     if (!ok) break;
                     ++done;
                 }
-                if (lane == 0) mbar_arrive(&item_empty[slot]);
+                mbar_arrive(&item_empty[slot]);
             }
-            if (!ok && lane == 0) give_up();
+            if (!ok) give_up();
             // No product may be in flight when tensor memory is freed.
-            if (lane == 0) {
-                mma_commit(drain);
-                mbar_wait(drain, 0);
+            mma_commit(drain);
+            mbar_wait(drain, 0);
+            misc[1] = L::kStages;  // no more V tiles
+            mbar_arrive(v_ask);
+        } else if (warp == 11) {
+            // ------------------------------------------------- V tile rows --
+            // On demand of the products' thread, which has seen the tile land.
+            // Requests may be far apart: this wait alone has a longer limit.
+            for (int n = 0;; ++n) {
+                if (!__all_sync(0xffffffffu, mbar_wait(v_ask, n & 1, 100 * p.wait_limit_ns))) break;
+                const int st = static_cast<int>(misc[1]);
+                if (st >= L::kStages) break;
+                uint8_t* vt = smem + L::kRingOff + st * L::kTileBytes;
+                for (int c = 0; c < D / 64; ++c)
+                    for (int e = static_cast<int>(misc[2]) * 8 + lane; e < kKeys * 8; e += 32)
+                        *reinterpret_cast<uint4*>(vt + c * kPanel + e * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_clean);
             }
-            __syncwarp();
         } else if (warp == 10) {
             // ------------------------------------------------- next items --
             int w = 0;  // items handed out
@@ -604,6 +639,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int all_hi = __shfl_sync(0xffffffffu, row_hi, 0);
             const int all_lo = __shfl_sync(0xffffffffu, row_lo, 31);
             float m = -INFINITY, l = 0.f;
+            float ahead = -INFINITY;  // maximum of the last tile
             for (int j = s; j < units; j += 2, ++n) {
                 if (!warp_wait(&s_full[s], n & 1)) {
                     ok = false;
@@ -613,39 +649,43 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (any_valid) {
                     const int i = it.first + (rows ? j >> 1 : j);
                     const int j0 = tile_start(it, i);
-                    const int end = tile_end(it, i);
-                    uint32_t x[kKeys];
+                    const int end = min(row_hi, tile_end(it, i)) - j0;
+                    const bool partial = !(j0 + kKeys <= min(all_hi, tile_end(it, i)) &&
+                                           (j0 >= all_lo || j0 + kKeys <= it.sinks));
+                    const int lw = row_lo - j0, sk = it.sinks - j0;
+                    uint32_t x[2][32];
+                    auto hide = [&](int k, uint32_t* v) {
+                        const uint32_t vis = below(end - k) & (~below(lw - k) | below(sk - k));
 #pragma unroll
-                    for (int k = 0; k < kKeys; k += 32) tmem_ld32(ts + k, x + k);
-                    tmem_wait_ld();
-                    if (!(j0 + kKeys <= min(all_hi, end) && (j0 >= all_lo || j0 + kKeys <= it.sinks))) {
-                        const int h = min(row_hi, end) - j0, lw = row_lo - j0, sk = it.sinks - j0;
+                        for (int e = 0; e < 32; ++e)
+                            if (!(vis & (1u << e))) v[e] = 0xff800000u;
+                    };
+                    auto largest = [&](const uint32_t* v, float t) {
 #pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            t = fmaxf(t, fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+                        return t;
+                    };
+                    // The reference moves: to this tile's maximum where there
+                    // is none yet, to the last tiles' where they outgrew it.
+                    if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                        float t = -INFINITY;
+#pragma unroll 1
                         for (int k = 0; k < kKeys; k += 32) {
-                            const uint32_t vis = below(h - k) & (~below(lw - k) | below(sk - k));
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(vis & (1u << e))) x[k + e] = 0xff800000u;
+                            tmem_ld32(ts + k, x[0]);
+                            tmem_wait_ld();
+                            if (partial) hide(k, x[0]);
+                            t = largest(x[0], t);
                         }
+                        if (m == -INFINITY) m = ahead = t * c;
                     }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < kKeys; k += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[k + e]),
-                                                       __uint_as_float(x[k + e + 4])));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                    const bool grow = m != -INFINITY && top > m + kRescale;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        // Not the item's first unit: m was set by an earlier one.
-                        if (!warp_wait(&o_done[s], (n - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const float f = grow ? ex2_approx(m - top) : 1.f;
-                        l *= f;
+                    if (__any_sync(0xffffffffu, ahead > m + kRescale)) {
+                        const float f = ahead > m + kRescale ? ex2_approx(m - ahead) : 1.f;
+                        // Beyond 2^100 in one tile: the row is computed again.
+                        l = ahead > m + kMaxGrowth ? NAN : l * f;
+                        if (ahead > m + kRescale) m = ahead;
+                        // The product that S waited for came after the one
+                        // that last wrote O.
 #pragma unroll 1
                         for (int k = 0; k < D; k += 16) {
                             uint32_t o[16];
@@ -658,29 +698,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                         tmem_wait_st();
                     }
-                    if (grow || m == -INFINITY) m = top;
                     const float base = m == -INFINITY ? 0.f : -m;
                     const uint64_t b2 = pack_f32x2(base, base);
                     uint64_t sum[2] = {0ull, 0ull};
+                    float top = -INFINITY;
+                    tmem_ld32(ts, x[0]);
 #pragma unroll
                     for (int k = 0; k < kKeys; k += 32) {
+                        uint32_t* v = x[(k >> 5) & 1];
+                        tmem_wait_ld();
+                        if (k + 32 < kKeys) tmem_ld32(ts + k + 32, x[((k >> 5) + 1) & 1]);
+                        if (partial) hide(k, v);
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float a, b;
-                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[k + e]),
-                                                              __uint_as_float(x[k + e + 1])), c2, b2), a, b);
+                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[e]),
+                                                              __uint_as_float(v[e + 1])), c2, b2), a, b);
                             a = ex2_approx(a);
                             b = ex2_approx(b);
                             sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
                             pk[e >> 1] = pack_bf16x2(a, b);
                         }
+                        top = largest(v, top);
                         tmem_st16(ts + (k >> 1), pk);
+                        if (k == 32) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&p_half[s]);
+                        }
                     }
                     tmem_wait_st();
                     float a, b;
                     unpack_f32x2(add_f32x2(sum[0], sum[1]), a, b);
                     l += a + b;
+                    ahead = top * c;
+                } else if (lane == 0) {
+                    mbar_arrive(&p_half[s]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -698,7 +753,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int piece = rows ? it.split : it.split * 2 + s;
             const size_t at = static_cast<size_t>(piece) * p.T * p.Hq + row;
             const bool some = valid && l != 0.f;
-            float bad = l * 0.f;  // 0 unless a value is not finite
+            // 0 unless a value is not finite or grew out of hand.
+            float bad = l < 1e30f ? 0.f : NAN;
             if (any_valid) {
                 const float il = some ? 1.f / l : 0.f;
 #pragma unroll
@@ -753,6 +809,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (!ok && lane == 0) give_up();
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 8) tmem_dealloc(tmem, 512);

@@ -79,6 +79,20 @@ __device__ __forceinline__ void tc_fence_after() {
 
 // ------------------------------------------------------- matrix products --
 
+// True in one thread of the (converged) warp, always the same one. Products
+// are issued under this rather than a lane test: the compiler then knows that
+// one thread runs them and keeps their descriptors in uniform registers
+// (under `lane == 0` a 128 x 128 x 16 product took 110 to 140 cycles to issue).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
+
 // Shared-memory operand descriptor, 128-byte swizzle (layout type 2, version
 // 1), byte offsets in units of 16. K-major operand: `stride` is the distance
 // of 8-row groups, `lead` unused. MN-major operand: `stride` is the distance

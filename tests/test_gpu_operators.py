@@ -510,3 +510,23 @@ def test_prompt_then_samples_together():
         ws.copy_(nxt)
     assert (mask >= 0).all()
     no_errors()
+
+
+def test_window_many_items_per_cta():
+    """More query tiles than the GPU has SMs, long and short ones: each CTA takes several, in both
+    ways the streams are paired; every 397th row against the definition."""
+    for nq, kv, Hq, Hkv, window in (([9000], [9000], 8, 8, 0), ([5000, 40, 4001], [5000, 3000, 6000], 4, 4, 700),
+                                    ([1] * 2500, [30 + i % 300 for i in range(2500)], 2, 1, 0)):
+        g = gen(len(nq))
+        B, T, S = len(nq), sum(nq), max(kv)
+        starts = [sum(nq[:i]) for i in range(B + 1)]
+        q, k, v = normal(g, T, Hq, 64), normal(g, B, Hkv, S, 64), normal(g, B, Hkv, S, 64)
+        out = torch.empty_like(q)
+        lf.window_attention(q, k, v, ints(starts), ints(kv), out, window, 3, 0.125)
+        no_errors()
+        for b in range(B):
+            for i in range((97 * b) % 397 if nq[b] > 397 else 0, nq[b], 397):
+                t = starts[b] + i
+                ref, tol = _plain.window_rows(q[t:t + 1], k[b:b + 1], v[b:b + 1], [0, 1],
+                                              [kv[b] - nq[b] + i + 1], window, 3, 0.125)
+                near(out[t:t + 1], ref, tol, f"sequence {b} row {i}")
