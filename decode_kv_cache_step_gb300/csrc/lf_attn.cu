@@ -25,9 +25,9 @@
 //                   tensor memory, m, l, P (bf16) back over S, at the end O
 //   warp 8          one thread issues S = Q K^T (both in shared memory) and
 //                   O += P V (P in tensor memory, V as it lies in the cache)
-//   warp 9          TMA loads: Q, then K and V tiles through a ring
+//   warp 9          TMA loads: K and V tiles through a ring
 //   warp 10         next work item: cancels a pending CTA, finds the item's
-//                   sequence, rows and tiles, hands it to the others
+//                   sequence, rows and tiles, hands it to the others; loads Q
 //   warp 11         zeroes the rows of V tiles behind a range's last key
 // A tensor product of 128 x 128 x 128 takes 512 cycles; a pair of tiles needs
 // four of them per 128 keys, and the two streams' softmax must fit in between.
@@ -72,7 +72,7 @@ constexpr float kRescale = 8.f;      // log2 growth of the maximum that moves m
 constexpr float kMaxGrowth = 100.f;  // log2 growth within one tile that l and O are trusted with
 
 constexpr int kItemSlots = 3;        // items in flight between the warps
-constexpr int kAskTiles = 2;         // K/V tiles of an item left to load when the next is asked for
+constexpr int kAskTiles = 4;         // K/V tiles of an item left to load when the next is asked for
 
 // What the warps work on.
 struct Item {
@@ -369,8 +369,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 9 && lane == 0) {
             // --------------------------------------------------- producer --
-            int n = 0;     // ring entries issued
-            int done = 0;  // items with work
+            int n = 0;  // ring entries issued
             bool ok = true;
             for (int w = 0;; ++w) {
                 const int slot = w % kItemSlots;
@@ -381,16 +380,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int units = rows ? 2 * it.count : it.count;
                 if (units > 0) {
                     const int unit = it.seq * p.Hkv + it.kvh;
-                    // Q: both tiles in rows mode, alternating buffers in keys mode.
-                    const int qb = rows ? 0 : done & 1;
-                    const int use = rows ? done : done >> 1;
-                    ok = mbar_wait(&q_empty[qb], (use & 1) ^ 1, p.wait_limit_ns);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&q_full[qb], (rows ? 2 : 1) * L::kTileBytes);
-                    for (int s = 0; s < (rows ? 2 : 1); ++s)
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load(smem + (s + qb) * L::kTileBytes + c * kPanel, &tmQ, c * 64,
-                                     it.kvh << gs, it.tok0 + s * (kRows >> gs), &q_full[qb]);
                     auto load = [&](const CUtensorMap* map, int i) {
                         const int st = n % L::kStages;
                         if (!mbar_wait(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_limit_ns))
@@ -420,7 +409,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (ok && j + 2 < units) ok = load(&tmK, rows ? (j >> 1) + 1 : j + 2);
                     }
                     if (!ok) break;
-                    ++done;
                 } else {
                     mbar_arrive(want);
                 }
@@ -431,10 +419,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 // No copy may be in flight when the CTA leaves.
                 for (int k = max(0, n - L::kStages); k < n; ++k)
                     mbar_wait(&full[k % L::kStages], (k / L::kStages) & 1);
-                for (int k = max(0, done - 1); k < done + 1; ++k) {
-                    const int use = rows ? k : k >> 1;
-                    mbar_wait(&q_full[rows ? 0 : k & 1], use & 1, 1000000);
-                }
             }
         } else if (warp == 8 && elect_one()) {
             // -------------------------------------------- matrix products --
@@ -567,7 +551,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         } else if (warp == 10) {
             // ------------------------------------------------- next items --
-            int w = 0;  // items handed out
+            int w = 0;     // items handed out
+            int done = 0;  // items with work
             bool ok = true;
             int work = blockIdx.x;
             for (int round = 0;; ++round) {
@@ -591,6 +576,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     __syncwarp();
                     if (it.stop) break;
+                    if (it.count > 0) {
+                        // Q: both tiles in rows mode, alternating buffers in keys mode.
+                        const int qb = rows ? 0 : done & 1;
+                        const int use = rows ? done : done >> 1;
+                        ok = warp_wait(&q_empty[qb], (use & 1) ^ 1);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&q_full[qb], (rows ? 2 : 1) * L::kTileBytes);
+                            for (int s = 0; s < (rows ? 2 : 1); ++s)
+                                for (int c = 0; c < D / 64; ++c)
+                                    tma_load(smem + (s + qb) * L::kTileBytes + c * kPanel, &tmQ, c * 64,
+                                             it.kvh << gs, it.tok0 + s * (kRows >> gs), &q_full[qb]);
+                        }
+                        __syncwarp();
+                        ++done;
+                    }
                     ok = warp_wait(want, w & 1);
                     if (!ok) break;
                     ++w;
@@ -607,7 +608,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (!ok && lane == 0) {
                 give_up();
-                mbar_wait(next, 0, 1000000);  // an answer under way lands before the CTA leaves
+                // What is under way (Q, an answer) lands before the CTA leaves.
+                for (int k = max(0, done - 2); k < done; ++k)
+                    mbar_wait(&q_full[rows ? 0 : k & 1], (rows ? k : k >> 1) & 1, 1000000);
+                mbar_wait(next, 0, 1000000);
                 mbar_wait(next, 1, 1000000);
             }
         }
