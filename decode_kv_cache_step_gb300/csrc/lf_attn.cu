@@ -72,6 +72,7 @@ constexpr float kRescale = 8.f;      // log2 growth of the maximum that moves m
 constexpr float kMaxGrowth = 100.f;  // log2 growth within one tile that l and O are trusted with
 
 constexpr int kItemSlots = 3;        // items in flight between the warps
+constexpr uint32_t kDrainTries = 1000000;
 constexpr int kAskTiles = 4;         // K/V tiles of an item left to load when the next is asked for
 
 // What the warps work on.
@@ -151,6 +152,7 @@ __device__ void attn_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const _
                          float& l, float (&o)[D / 32]) {
     const int lane = threadIdx.x & 31;
     constexpr int kC = D / 32;
+#pragma unroll 1
     for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
         const int j = j0 + lane;
         const bool vis = j < j_hi && j < hi && (j >= lo || j < sinks);
@@ -161,6 +163,7 @@ __device__ void attn_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const _
             const uint4* kr = reinterpret_cast<const uint4*>(k + static_cast<size_t>(j) * D);
             const uint4* qr = reinterpret_cast<const uint4*>(q);
             float a = 0.f;
+#pragma unroll 2
             for (int c = 0; c < D / 8; ++c) {
                 const uint4 kk = __ldg(kr + c), qq = __ldg(qr + c);
                 const __nv_bfloat162* kb = reinterpret_cast<const __nv_bfloat162*>(&kk);
@@ -188,6 +191,7 @@ __device__ void attn_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const _
         m = mx;
 #pragma unroll
         for (int c = 0; c < kC; ++c) o[c] = keep == 0.f ? 0.f : o[c] * keep;
+#pragma unroll 1
         for (unsigned left = any; left; left &= left - 1) {
             const int i = __ffs(left) - 1;
             const float pj = __shfl_sync(0xffffffffu, p, i);
@@ -235,6 +239,23 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
+// Waits for a barrier's phase; false after `tries` suspensions of about a
+// microsecond (small code: a CTA has some twenty waits, and its roles share
+// the instruction cache).
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t tries) {
+    uint32_t ok = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; !ok && i < tries; ++i)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    return ok != 0;
+}
+
 // One warp: the sequence and rows of query tile x, and its part of the K/V
 // tiles. Sequence b's tiles start at index floor(q_start[b] / tok) + b: enough
 // for its rows wherever they start, so no prefix sum over the sequences is
@@ -246,6 +267,7 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int work, Ite
     const int rest = work / pl.nsplit;
     const int x = pl.items - 1 - rest / p.Hkv;
     int b = 0, len = p.N;
+#pragma unroll 1
     while (len > 1) {
         const int step = (len + 31) >> 5;
         const int i = b + lane * step;
@@ -361,7 +383,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // A wait of a whole warp: every lane learns whether all of them saw the
     // barrier complete.
     auto warp_wait = [&](uint64_t* bar, int parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_limit_ns)) != 0;
+        return __all_sync(0xffffffffu, wait_phase(bar, parity, p.wait_tries)) != 0;
     };
     auto give_up = [&]() { atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT); };
 
@@ -373,40 +395,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bool ok = true;
             for (int w = 0;; ++w) {
                 const int slot = w % kItemSlots;
-                ok = mbar_wait(&item_full[slot], (w / kItemSlots) & 1, p.wait_limit_ns);
+                ok = wait_phase(&item_full[slot], (w / kItemSlots) & 1, p.wait_tries);
                 if (!ok) break;
                 const Item& it = items[slot];
                 if (it.stop) break;
                 const int units = rows ? 2 * it.count : it.count;
                 if (units > 0) {
                     const int unit = it.seq * p.Hkv + it.kvh;
-                    auto load = [&](const CUtensorMap* map, int i) {
-                        const int st = n % L::kStages;
-                        if (!mbar_wait(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_limit_ns))
-                            return false;
-                        uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes;
-                        const int y = tile_start(it, it.first + i);
-                        // The second half only where it holds a key.
-                        const int halves = tile_end(it, it.first + i) - y > 64 ? 2 : 1;
-                        mbar_arrive_expect_tx(&full[st], halves * (L::kTileBytes / 2));
-                        for (int h = 0; h < halves; ++h)
-                            for (int c = 0; c < D / 64; ++c)
-                                tma_load(dst + c * kPanel + h * (kPanel / 2), map, c * 64, y + h * 64,
-                                         unit, &full[st]);
-                        ++n;
-                        return true;
-                    };
                     // Late enough that another CTA may still be the one to take
                     // the next item, early enough that it is found in time.
                     const int ask = max(0, units - (rows ? 2 * kAskTiles : kAskTiles));
-                    // The order in which the products take the tiles.
-                    ok = load(&tmK, 0);
-                    if (ok && !rows && units > 1) ok = load(&tmK, 1);
-                    for (int j = 0; ok && j < units; ++j) {
-                        if (rows && (j & 1)) continue;
-                        if (j == ask) mbar_arrive(want);
-                        ok = load(&tmV, rows ? j >> 1 : j);
-                        if (ok && j + 2 < units) ok = load(&tmK, rows ? (j >> 1) + 1 : j + 2);
+                    // The order in which the products take the tiles: K of
+                    // unit t after V of unit t - 2 (in rows mode, two units
+                    // share the tile of the even one).
+                    const int step = rows ? 2 : 1;
+                    for (int t = 0; ok && t < units + 2; t += step) {
+                        if (t == ask) mbar_arrive(want);
+#pragma unroll 1
+                        for (int kv = t >= 2 ? 0 : 1; kv < (t < units ? 2 : 1); ++kv) {
+                            const int st = n % L::kStages;
+                            ok = wait_phase(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_tries);
+                            if (!ok) break;
+                            const int i = it.first + (kv ? t : t - 2) / step;
+                            const int y = tile_start(it, i);
+                            // The second half only where it holds a key.
+                            const int halves = tile_end(it, i) - y > 64 ? 2 : 1;
+                            mbar_arrive_expect_tx(&full[st], halves * (L::kTileBytes / 2));
+                            uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes;
+#pragma unroll 1
+                            for (int h = 0; h < halves; ++h)
+                                for (int c = 0; c < D / 64; ++c)
+                                    tma_load(dst + c * kPanel + h * (kPanel / 2), kv ? &tmK : &tmV,
+                                             c * 64, y + h * 64, unit, &full[st]);
+                            ++n;
+                        }
                     }
                     if (!ok) break;
                 } else {
@@ -418,7 +440,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 give_up();
                 // No copy may be in flight when the CTA leaves.
                 for (int k = max(0, n - L::kStages); k < n; ++k)
-                    mbar_wait(&full[k % L::kStages], (k / L::kStages) & 1);
+                    wait_phase(&full[k % L::kStages], (k / L::kStages) & 1, kDrainTries);
             }
         } else if (warp == 8 && elect_one()) {
             // -------------------------------------------- matrix products --
@@ -437,7 +459,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bool clean = false;         // the V tile has rows to zero
             bool ok = true;
             auto wait = [&](uint64_t* bar, int parity) {
-                return mbar_wait(bar, parity, p.wait_limit_ns);
+                return wait_phase(bar, parity, p.wait_tries);
             };
             for (int w = 0;; ++w) {
                 const int slot = w % kItemSlots;
@@ -456,71 +478,71 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         ++n;
                         return got;
                     };
-                    // S of unit j: Q tile times K tile.
-                    auto scores = [&](int j) {
-                        const int s = j & 1;
-                        if (!(rows && s) && !take(&kst)) return false;
-                        tc_fence_after();
-                        const uint32_t qa = qs + (rows && s ? L::kTileBytes : 0);
-                        const uint32_t ka = ring + kst * L::kTileBytes;
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-                            mma_ss(tmem + s * kKeys, smem_desc(qa + off, 16, 1024),
-                                   smem_desc(ka + off, 16, 1024), idesc_s, k > 0);
-                        }
-                        mma_commit(&s_full[s]);
-                        if (!rows || s) mma_commit(&empty[kst]);
-                        if (j == units - 1) mma_commit(&q_empty[qb]);
-                        return true;
-                    };
-                    ok = ok && scores(0);
-                    if (ok && units > 1) ok = scores(1);
-                    for (int j = 0; ok && j < units; ++j) {
-                        const int s = j & 1;
-                        if (!(rows && s)) {
-                            ok = take(&vst);
-                            if (!ok) break;
-                            const int i = it.first + (rows ? j >> 1 : j);
-                            const int keep = tile_end(it, i) - tile_start(it, i);
-                            clean = keep < kKeys;
-                            if (clean) {
-                                misc[1] = vst;
-                                misc[2] = keep;
-                                mbar_arrive(v_ask);
+                    // O of unit t - 2, then S of unit t: a stream's next S
+                    // follows the product that read its P.
+#pragma unroll 1
+                    for (int t = 0; ok && t < units + 2; ++t) {
+                        const int s = t & 1;
+                        if (t >= 2) {
+                            if (!(rows && s)) {
+                                ok = take(&vst);
+                                if (!ok) break;
+                                const int i = it.first + (rows ? (t - 2) >> 1 : t - 2);
+                                const int keep = tile_end(it, i) - tile_start(it, i);
+                                clean = keep < kKeys;
+                                if (clean) {
+                                    misc[1] = vst;
+                                    misc[2] = keep;
+                                    mbar_arrive(v_ask);
+                                }
                             }
-                        }
-                        if (j < 2) {
-                            // The stream's previous O has been read.
-                            if (odone[s] > 0 && !wait(&o_free[s], (odone[s] - 1) & 1)) {
-                                ok = false;
-                                break;
+                            if (t < 4) {
+                                // The stream's previous O has been read.
+                                ok = odone[s] == 0 || wait(&o_free[s], (odone[s] - 1) & 1);
+                                if (!ok) break;
+                                ++odone[s];
                             }
-                            ++odone[s];
-                        }
-                        const uint32_t va = ring + vst * L::kTileBytes;
-                        if (clean && !(rows && s)) {
-                            ok = wait(v_clean, cleaned & 1);
-                            if (!ok) break;
-                            ++cleaned;
-                        }
+                            if (clean && !(rows && s)) {
+                                ok = wait(v_clean, cleaned & 1);
+                                if (!ok) break;
+                                ++cleaned;
+                            }
+                            const uint64_t vd = smem_desc(ring + vst * L::kTileBytes, kPanel, 1024);
+                            const uint32_t od = tmem + 2 * kKeys + s * D;
+#pragma unroll 1
+                            for (int half = 0; half < 2; ++half) {
+                                ok = wait(half ? &p_full[s] : &p_half[s], pdone[s] & 1);
+                                if (!ok) break;
+                                tc_fence_after();
+                                const uint32_t pa = tmem + s * kKeys + half * (kKeys / 4);
+                                const uint64_t vh = vd + half * (kKeys / 2 * 128 / 16);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            if (!wait(half ? &p_full[s] : &p_half[s], pdone[s] & 1)) {
-                                ok = false;
-                                break;
+                                for (int k = 0; k < kKeys / 32; ++k)
+                                    mma_ts(od, pa + k * 8, vh + k * (2048 / 16), idesc_o,
+                                           t > 3 || half > 0 || k > 0);
+                            }
+                            if (!ok) break;
+                            ++pdone[s];
+                            mma_commit(&o_done[s]);
+                            if (!rows || s) mma_commit(&empty[vst]);
+                        }
+                        if (t < units) {
+                            if (!(rows && s)) {
+                                ok = take(&kst);
+                                if (!ok) break;
                             }
                             tc_fence_after();
+                            const uint64_t qd = smem_desc(qs + (rows && s ? L::kTileBytes : 0), 16, 1024);
+                            const uint64_t kd = smem_desc(ring + kst * L::kTileBytes, 16, 1024);
 #pragma unroll
-                            for (int k = half * kKeys / 32; k < (half + 1) * kKeys / 32; ++k)
-                                mma_ts(tmem + 2 * kKeys + s * D, tmem + s * kKeys + k * 8,
-                                       smem_desc(va + k * 2048, kPanel, 1024), idesc_o, j > 1 || k > 0);
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint64_t off = ((k >> 2) * kPanel + (k & 3) * 32) / 16;
+                                mma_ss(tmem + s * kKeys, qd + off, kd + off, idesc_s, k > 0);
+                            }
+                            mma_commit(&s_full[s]);
+                            if (!rows || s) mma_commit(&empty[kst]);
+                            if (t == units - 1) mma_commit(&q_empty[qb]);
                         }
-                        if (!ok) break;
-                        ++pdone[s];
-                        mma_commit(&o_done[s]);
-                        if (!rows || s) mma_commit(&empty[vst]);
-                        if (j + 2 < units) ok = scores(j + 2);
                     }
                     if (!ok) break;
                     ++done;
@@ -530,7 +552,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!ok) give_up();
             // No product may be in flight when tensor memory is freed.
             mma_commit(drain);
-            mbar_wait(drain, 0);
+            wait_phase(drain, 0, kDrainTries);
             misc[1] = L::kStages;  // no more V tiles
             mbar_arrive(v_ask);
         } else if (warp == 11) {
@@ -538,12 +560,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // On demand of the products' thread, which has seen the tile land.
             // Requests may be far apart: this wait alone has a longer limit.
             for (int n = 0;; ++n) {
-                if (!__all_sync(0xffffffffu, mbar_wait(v_ask, n & 1, 100 * p.wait_limit_ns))) break;
+                if (!__all_sync(0xffffffffu, wait_phase(v_ask, n & 1, 100 * p.wait_tries))) break;
                 const int st = static_cast<int>(misc[1]);
                 if (st >= L::kStages) break;
                 uint8_t* vt = smem + L::kRingOff + st * L::kTileBytes;
+                const int keep = static_cast<int>(misc[2]);
                 for (int c = 0; c < D / 64; ++c)
-                    for (int e = static_cast<int>(misc[2]) * 8 + lane; e < kKeys * 8; e += 32)
+#pragma unroll 1
+                    for (int e = keep * 8 + lane; e < kKeys * 8; e += 32)
                         *reinterpret_cast<uint4*>(vt + c * kPanel + e * 16) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -610,9 +634,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 give_up();
                 // What is under way (Q, an answer) lands before the CTA leaves.
                 for (int k = max(0, done - 2); k < done; ++k)
-                    mbar_wait(&q_full[rows ? 0 : k & 1], (rows ? k : k >> 1) & 1, 1000000);
-                mbar_wait(next, 0, 1000000);
-                mbar_wait(next, 1, 1000000);
+                    wait_phase(&q_full[rows ? 0 : k & 1], (rows ? k : k >> 1) & 1, 1000);
+                wait_phase(next, 0, 1000);
+                wait_phase(next, 1, 1000);
             }
         }
     } else {
@@ -658,11 +682,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                            (j0 >= all_lo || j0 + kKeys <= it.sinks));
                     const int lw = row_lo - j0, sk = it.sinks - j0;
                     uint32_t x[2][32];
+                    // Keys the row does not see: weight 0. Most 32-key chunks
+                    // of a partial tile hold none.
                     auto hide = [&](int k, uint32_t* v) {
                         const uint32_t vis = below(end - k) & (~below(lw - k) | below(sk - k));
+                        if (__any_sync(0xffffffffu, vis != 0xffffffffu)) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(vis & (1u << e))) v[e] = 0xff800000u;
+                            for (int e = 0; e < 32; ++e)
+                                v[e] = (vis & (1u << e)) ? v[e] : 0xff800000u;
+                        }
                     };
                     auto largest = [&](const uint32_t* v, float t) {
 #pragma unroll
@@ -707,26 +735,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     uint64_t sum[2] = {0ull, 0ull};
                     float top = -INFINITY;
                     tmem_ld32(ts, x[0]);
+#pragma unroll 1
+                    for (int k0 = 0; k0 < kKeys; k0 += 64) {
 #pragma unroll
-                    for (int k = 0; k < kKeys; k += 32) {
-                        uint32_t* v = x[(k >> 5) & 1];
-                        tmem_wait_ld();
-                        if (k + 32 < kKeys) tmem_ld32(ts + k + 32, x[((k >> 5) + 1) & 1]);
-                        if (partial) hide(k, v);
-                        uint32_t pk[16];
+                        for (int q = 0; q < 2; ++q) {
+                            const int k = k0 + 32 * q;
+                            uint32_t* v = x[q];
+                            tmem_wait_ld();
+                            if (k + 32 < kKeys) tmem_ld32(ts + k + 32, x[q ^ 1]);
+                            if (partial) hide(k, v);
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float a, b;
-                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[e]),
-                                                              __uint_as_float(v[e + 1])), c2, b2), a, b);
-                            a = ex2_approx(a);
-                            b = ex2_approx(b);
-                            sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
-                            pk[e >> 1] = pack_bf16x2(a, b);
+                            for (int e = 0; e < 32; e += 2) {
+                                float a, b;
+                                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[e]),
+                                                                  __uint_as_float(v[e + 1])), c2, b2),
+                                             a, b);
+                                a = ex2_approx(a);
+                                b = ex2_approx(b);
+                                sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
+                                pk[e >> 1] = pack_bf16x2(a, b);
+                            }
+                            top = largest(v, top);
+                            tmem_st16(ts + (k >> 1), pk);
                         }
-                        top = largest(v, top);
-                        tmem_st16(ts + (k >> 1), pk);
-                        if (k == 32) {
+                        if (k0 == 0) {
                             tmem_wait_st();
                             tc_fence_before();
                             __syncwarp();
@@ -761,7 +794,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float bad = l < 1e30f ? 0.f : NAN;
             if (any_valid) {
                 const float il = some ? 1.f / l : 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     uint32_t o[32];
                     if (worked) {
