@@ -831,7 +831,7 @@ lf_status run_attention(lf::AttnParams p, int d, float scale, int dev, cudaStrea
     p.scale_log2 = std::max(
         static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634), 1e-30f);
     p.negate = scale < 0.f;
-    p.wait_tries = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(wait_limit_ns() / 1000, 1), 10000000));
+    p.wait_limit_ns = wait_limit_ns();
     ProfScope prof(LF_KERNEL_PACKED_ATTENTION, stream);
     cudaError_t e = lf::launch_attention(d, tmQ, tmK, tmV, p, sm_count(dev), stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");

@@ -72,7 +72,6 @@ constexpr float kRescale = 8.f;      // log2 growth of the maximum that moves m
 constexpr float kMaxGrowth = 100.f;  // log2 growth within one tile that l and O are trusted with
 
 constexpr int kItemSlots = 3;        // items in flight between the warps
-constexpr uint32_t kDrainTries = 1000000;
 constexpr int kAskTiles = 4;         // K/V tiles of an item left to load when the next is asked for
 
 // What the warps work on.
@@ -239,33 +238,37 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
-// Waits for a barrier's phase; false after `tries` suspensions of about a
-// microsecond (small code: a CTA has some twenty waits, and its roles share
-// the instruction cache).
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t tries) {
-    uint32_t ok = 0;
-#pragma unroll 1
-    for (uint32_t i = 0; !ok && i < tries; ++i)
+// Waits for a barrier's phase; false after limit_ns. (Small code: a CTA has
+// some twenty waits, and its roles share the instruction cache. A wait may
+// last as long as an item, hundreds of microseconds, so its limit is a time:
+// the hardware ends a suspension when it likes.)
+constexpr uint64_t kDrainNs = 1000000000;
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000000;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
             : "r"(smem_u32(bar)), "r"(parity)
             : "memory");
-    return ok != 0;
+        if (ok) return true;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit_ns) return false;
+    }
 }
 
 // One warp: the sequence and rows of query tile x, and its part of the K/V
 // tiles. Sequence b's tiles start at index floor(q_start[b] / tok) + b: enough
 // for its rows wherever they start, so no prefix sum over the sequences is
 // needed. False where the tile holds no rows.
-__device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int work, Item* it) {
+__device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int3 work, Item* it) {
     const int lane = threadIdx.x & 31;
-    // The last tiles (the longest rows of a causal prompt) come first.
-    const int split = work % pl.nsplit;
-    const int rest = work / pl.nsplit;
-    const int x = pl.items - 1 - rest / p.Hkv;
+    // A head's last tiles (the longest rows of a causal prompt) come first.
+    const int x = pl.items - 1 - work.x;
     int b = 0, len = p.N;
 #pragma unroll 1
     while (len > 1) {
@@ -295,13 +298,44 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int work, Ite
         it->nsink = (it->sinks + kKeys - 1) / kKeys;
     }
     const int tiles = it->nsink + (it->hi - it->lo + kKeys - 1) / kKeys;
-    const int per = (tiles + pl.nsplit - 1) / pl.nsplit;
-    it->first = split * per;
+    const int per = pl.nsplit == 1 ? tiles : (tiles + pl.nsplit - 1) / pl.nsplit;
+    it->first = work.z * per;
     it->count = max(0, min(tiles - it->first, per));
-    it->kvh = rest % p.Hkv;
-    it->split = split;
+    it->kvh = work.y;
+    it->split = work.z;
     it->stop = 0;
     return true;
+}
+
+// Stores 64 bytes of each lane's row (v: the lane's own row) at byte `off` of
+// the rows. A lane's row lies far from its neighbours', so plain 16-byte
+// stores would touch 32 lines each; four lanes exchange their pieces first
+// and store 64 bytes of one row together: a quarter of the lines. dst[i] is
+// the address of row i of the lane's group of four, or null (not stored).
+__device__ __forceinline__ void store_rows(uint4 (&v)[4], char* const (&dst)[4], int off) {
+    const int q = threadIdx.x & 3;
+    auto swap = [&](uint4& a, uint4& b, int bit) {
+        // Lanes with the bit set give a and get b of the other, and so on.
+        const bool up = (q & bit) != 0;
+        const uint4 give = up ? a : b;
+        uint4 got;
+        got.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+        got.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+        got.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+        got.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+        if (up)
+            a = got;
+        else
+            b = got;
+    };
+    // 4 x 4 transpose of 16-byte pieces: v[i] becomes piece q of row i.
+    swap(v[0], v[1], 1);
+    swap(v[2], v[3], 1);
+    swap(v[0], v[2], 2);
+    swap(v[1], v[3], 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + off + q * 16) = v[i];
 }
 
 // Bits [0, n) of a 32-key chunk.
@@ -383,7 +417,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // A wait of a whole warp: every lane learns whether all of them saw the
     // barrier complete.
     auto warp_wait = [&](uint64_t* bar, int parity) {
-        return __all_sync(0xffffffffu, wait_phase(bar, parity, p.wait_tries)) != 0;
+        return __all_sync(0xffffffffu, wait_phase(bar, parity, p.wait_limit_ns)) != 0;
     };
     auto give_up = [&]() { atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT); };
 
@@ -395,7 +429,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bool ok = true;
             for (int w = 0;; ++w) {
                 const int slot = w % kItemSlots;
-                ok = wait_phase(&item_full[slot], (w / kItemSlots) & 1, p.wait_tries);
+                ok = wait_phase(&item_full[slot], (w / kItemSlots) & 1, p.wait_limit_ns);
                 if (!ok) break;
                 const Item& it = items[slot];
                 if (it.stop) break;
@@ -414,7 +448,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
                         for (int kv = t >= 2 ? 0 : 1; kv < (t < units ? 2 : 1); ++kv) {
                             const int st = n % L::kStages;
-                            ok = wait_phase(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_tries);
+                            ok = wait_phase(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_limit_ns);
                             if (!ok) break;
                             const int i = it.first + (kv ? t : t - 2) / step;
                             const int y = tile_start(it, i);
@@ -440,7 +474,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 give_up();
                 // No copy may be in flight when the CTA leaves.
                 for (int k = max(0, n - L::kStages); k < n; ++k)
-                    wait_phase(&full[k % L::kStages], (k / L::kStages) & 1, kDrainTries);
+                    wait_phase(&full[k % L::kStages], (k / L::kStages) & 1, kDrainNs);
             }
         } else if (warp == 8 && elect_one()) {
             // -------------------------------------------- matrix products --
@@ -459,7 +493,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bool clean = false;         // the V tile has rows to zero
             bool ok = true;
             auto wait = [&](uint64_t* bar, int parity) {
-                return wait_phase(bar, parity, p.wait_tries);
+                return wait_phase(bar, parity, p.wait_limit_ns);
             };
             for (int w = 0;; ++w) {
                 const int slot = w % kItemSlots;
@@ -552,7 +586,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!ok) give_up();
             // No product may be in flight when tensor memory is freed.
             mma_commit(drain);
-            wait_phase(drain, 0, kDrainTries);
+            wait_phase(drain, 0, kDrainNs);
             misc[1] = L::kStages;  // no more V tiles
             mbar_arrive(v_ask);
         } else if (warp == 11) {
@@ -560,7 +594,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // On demand of the products' thread, which has seen the tile land.
             // Requests may be far apart: this wait alone has a longer limit.
             for (int n = 0;; ++n) {
-                if (!__all_sync(0xffffffffu, wait_phase(v_ask, n & 1, 100 * p.wait_tries))) break;
+                if (!__all_sync(0xffffffffu, wait_phase(v_ask, n & 1, 100 * p.wait_limit_ns))) break;
                 const int st = static_cast<int>(misc[1]);
                 if (st >= L::kStages) break;
                 uint8_t* vt = smem + L::kRingOff + st * L::kTileBytes;
@@ -578,10 +612,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int w = 0;     // items handed out
             int done = 0;  // items with work
             bool ok = true;
-            int work = blockIdx.x;
+            int3 work = make_int3(blockIdx.x, blockIdx.y, blockIdx.z);
             for (int round = 0;; ++round) {
                 Item it;
-                if (work >= 0) {
+                if (work.x >= 0) {
                     if (find_item(p, pl, work, &it)) {
                         it.stop = 0;
                     } else {
@@ -634,9 +668,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 give_up();
                 // What is under way (Q, an answer) lands before the CTA leaves.
                 for (int k = max(0, done - 2); k < done; ++k)
-                    wait_phase(&q_full[rows ? 0 : k & 1], (rows ? k : k >> 1) & 1, 1000);
-                wait_phase(next, 0, 1000);
-                wait_phase(next, 1, 1000);
+                    wait_phase(&q_full[rows ? 0 : k & 1], (rows ? k : k >> 1) & 1, 1000000);
+                wait_phase(next, 0, 1000000);
+                wait_phase(next, 1, 1000000);
             }
         }
     } else {
@@ -692,25 +726,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 v[e] = (vis & (1u << e)) ? v[e] : 0xff800000u;
                         }
                     };
-                    auto largest = [&](const uint32_t* v, float t) {
+                    auto largest = [&](const uint32_t* v) {
+                        float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
-                            t = fmaxf(t, fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
-                        return t;
+                            t[(e >> 1) & 1] = fmaxf(t[(e >> 1) & 1], fmaxf(__uint_as_float(v[e]),
+                                                                          __uint_as_float(v[e + 1])));
+                        return fmaxf(t[0], t[1]);
                     };
-                    // The reference moves: to this tile's maximum where there
-                    // is none yet, to the last tiles' where they outgrew it.
-                    if (__any_sync(0xffffffffu, m == -INFINITY)) {
-                        float t = -INFINITY;
-#pragma unroll 1
-                        for (int k = 0; k < kKeys; k += 32) {
-                            tmem_ld32(ts + k, x[0]);
-                            tmem_wait_ld();
-                            if (partial) hide(k, x[0]);
-                            t = largest(x[0], t);
-                        }
-                        if (m == -INFINITY) m = ahead = t * c;
-                    }
+                    // The reference moves where the last tile outgrew it.
                     if (__any_sync(0xffffffffu, ahead > m + kRescale)) {
                         const float f = ahead > m + kRescale ? ex2_approx(m - ahead) : 1.f;
                         // Beyond 2^100 in one tile: the row is computed again.
@@ -730,12 +754,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                         tmem_wait_st();
                     }
+                    if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                        float t = -INFINITY;
+#pragma unroll 1
+                        for (int k = 0; k < kKeys; k += 32) {
+                            tmem_ld32(ts + k, x[0]);
+                            tmem_wait_ld();
+                            if (partial) hide(k, x[0]);
+                            t = fmaxf(t, largest(x[0]));
+                        }
+                        if (m == -INFINITY) m = t * c;
+                    }
                     const float base = m == -INFINITY ? 0.f : -m;
                     const uint64_t b2 = pack_f32x2(base, base);
                     uint64_t sum[2] = {0ull, 0ull};
                     float top = -INFINITY;
                     tmem_ld32(ts, x[0]);
-#pragma unroll 1
+#pragma unroll
                     for (int k0 = 0; k0 < kKeys; k0 += 64) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
@@ -756,7 +791,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
                                 pk[e >> 1] = pack_bf16x2(a, b);
                             }
-                            top = largest(v, top);
+                            top = fmaxf(top, largest(v));
                             tmem_st16(ts + (k >> 1), pk);
                         }
                         if (k0 == 0) {
@@ -794,6 +829,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float bad = l < 1e30f ? 0.f : NAN;
             if (any_valid) {
                 const float il = some ? 1.f / l : 0.f;
+                // Rows to store, of the lane's group of four.
+                char* const mine = (p.pieces == 0 ? reinterpret_cast<char*>(p.out) + row * D * 2
+                                                  : reinterpret_cast<char*>(p.part_o) + at * D * 4);
+                const uint64_t addr =
+                    (p.pieces == 0 ? valid : some) ? reinterpret_cast<uint64_t>(mine) : 0ull;
+                char* dst[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dst[i] = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, addr, i, 4));
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     uint32_t o[32];
@@ -806,23 +850,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (!some) o[e] = 0u;
                         bad = fmaf(__uint_as_float(o[e]), 0.f, bad);
                     }
+                    uint4 v[4];
                     if (p.pieces == 0) {
-                        if (valid) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint4 v;
-                                v.x = pack_bf16x2(__uint_as_float(o[e]) * il, __uint_as_float(o[e + 1]) * il);
-                                v.y = pack_bf16x2(__uint_as_float(o[e + 2]) * il, __uint_as_float(o[e + 3]) * il);
-                                v.z = pack_bf16x2(__uint_as_float(o[e + 4]) * il, __uint_as_float(o[e + 5]) * il);
-                                v.w = pack_bf16x2(__uint_as_float(o[e + 6]) * il, __uint_as_float(o[e + 7]) * il);
-                                *reinterpret_cast<uint4*>(p.out + row * D + k + e) = v;
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t* w = o + 8 * i;
+                            v[i].x = pack_bf16x2(__uint_as_float(w[0]) * il, __uint_as_float(w[1]) * il);
+                            v[i].y = pack_bf16x2(__uint_as_float(w[2]) * il, __uint_as_float(w[3]) * il);
+                            v[i].z = pack_bf16x2(__uint_as_float(w[4]) * il, __uint_as_float(w[5]) * il);
+                            v[i].w = pack_bf16x2(__uint_as_float(w[6]) * il, __uint_as_float(w[7]) * il);
                         }
-                    } else if (some) {
+                        store_rows(v, dst, k * 2);
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(p.part_o + at * D + k + e) =
-                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                v[i] = make_uint4(o[16 * h + 4 * i], o[16 * h + 4 * i + 1],
+                                                  o[16 * h + 4 * i + 2], o[16 * h + 4 * i + 3]);
+                            store_rows(v, dst, k * 4 + h * 64);
+                        }
                     }
                 }
                 if (valid && p.pieces > 0) p.part_ml[at] = make_float2(m, l);
@@ -919,7 +966,8 @@ cudaError_t launch_attention_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
         if (e != cudaSuccess) return e;
         configured_for = dev;
     }
-    const unsigned grid = static_cast<unsigned>(pl.items) * p.Hkv * pl.nsplit;
+    const dim3 grid(static_cast<unsigned>(pl.items), static_cast<unsigned>(p.Hkv),
+                    static_cast<unsigned>(pl.nsplit));
     kernel<<<grid, kAttnThreads, L::kAlloc, stream>>>(tmQ, tmK, tmV, p, pl);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.pieces == 0 || !p.out) return e;

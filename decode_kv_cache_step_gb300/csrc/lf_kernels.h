@@ -172,7 +172,7 @@ struct AttnParams {
     int pieces;
     float scale_log2;            // |scale| * log2(e)
     bool negate;                 // scale < 0: the kernel negates q
-    uint32_t wait_tries;         // limit of the pipeline waits, about a microsecond each
+    uint64_t wait_limit_ns;
 };
 // Pieces of the key axis such a call writes (0: the output directly), a rule
 // on its sizes alone. The plan for the prefix (causal false) has at least one.
