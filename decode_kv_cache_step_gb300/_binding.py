@@ -9,6 +9,7 @@ or PyTorch fallback, and a missing library is an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -366,10 +367,16 @@ class _Here:
 
 
 _HERE = _Here()
+_gpus = 0  # visible GPUs, once known
 
 
 def _on_device(device, *tensors):
     """The device guard of a call on `device`, where every tensor has to be."""
+    global _gpus
+    if _gpus == 0:
+        _gpus = torch.cuda.device_count()
+    if _gpus == 1:  # CUDA tensors cannot be anywhere else
+        return _HERE
     index = device.index
     for t in tensors:
         if t is not None and t.get_device() != index:
@@ -414,7 +421,7 @@ def _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv):
         raise TypeError("qkv and q_out: expected torch.Tensors")
     if q_out.dim() != 3 or qkv.dim() != 3:
         raise ValueError("qkv must be [T,Hq+2*Hkv,d] and q_out [T,Hq,d]")
-    T, Hq, d = (int(x) for x in q_out.shape)
+    T, Hq, d = q_out.shape
     bf = torch.bfloat16
     _need(q_out, "q_out", bf, (T, Hq, d), True)
     if qkv.dtype != bf:
@@ -469,7 +476,7 @@ def prefill_append(qkv, q_weight, k_weight, inv_freq, q_start, kv_len, q_out, k_
     lib = load_library()
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [B,Hkv,S,d]")
-    B, Hkv, S = (int(x) for x in k_cache.shape[:3])
+    B, Hkv, S, _ = k_cache.shape
     T, Hq, d, rot, stride = _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv)
     bf, i32 = torch.bfloat16, torch.int32
     _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
@@ -498,6 +505,11 @@ def window_attention_workspace(T, B, Hq, Hkv, d, S, window=0, sinks=0) -> int:
     return int(n.value)
 
 
+# The size is a function of the sizes and the device alone.
+_window_bytes = functools.lru_cache(maxsize=1024)(
+    lambda index, *sizes: window_attention_workspace(*sizes))
+
+
 def window_attention(q, k_cache, v_cache, q_start, kv_len, out, window, sinks, scale,
                      workspace=None, stream=None):
     """lf_window_attention: packed rows q [T,Hq,d] over in-order caches
@@ -509,8 +521,8 @@ def window_attention(q, k_cache, v_cache, q_start, kv_len, out, window, sinks, s
         raise TypeError("q and k_cache: expected torch.Tensors")
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [T,Hq,d] and k_cache [B,Hkv,S,d]")
-    T, Hq, d = (int(x) for x in q.shape)
-    B, Hkv, S = (int(x) for x in k_cache.shape[:3])
+    T, Hq, d = q.shape
+    B, Hkv, S, _ = k_cache.shape
     bf, i32 = torch.bfloat16, torch.int32
     _need(q, "q", bf, (T, Hq, d), True)
     _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
@@ -519,7 +531,7 @@ def window_attention(q, k_cache, v_cache, q_start, kv_len, out, window, sinks, s
     _need(kv_len, "kv_len", i32, (B,), True)
     _need(out, "out", bf, (T, Hq, d), True)
     with _on_device(q.device, k_cache, v_cache, q_start, kv_len, out):
-        n = window_attention_workspace(T, B, Hq, Hkv, d, S, window, sinks)
+        n = _window_bytes(q.device.index, T, B, Hq, Hkv, d, S, int(window), int(sinks))
         ws = _workspace(workspace, n, q.device, stream) if n or workspace is not None else None
         _check(lib, lib.lf_window_attention(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), q_start.data_ptr(),

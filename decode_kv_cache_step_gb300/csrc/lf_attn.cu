@@ -80,8 +80,8 @@ struct Item {
     int pos0;             // position of the first token (causal)
     int lo, hi;           // keys some row sees: [lo, hi) and below sinks
     int sinks;
-    int nsink;            // tile i of the list starts at key i * kKeys below nsink (its keys end
-                          // at sinks), at lo + (i - nsink) * kKeys from there (its keys end at hi)
+    int nsink;            // tiles of the list that hold first keys only
+    int joined;           // the tile whose second half holds the first keys, or -1
     int first, count;     // this item's part of the list
     int kvh, split;
     int stop;             // no more work
@@ -104,12 +104,19 @@ struct AttnSmem {
     static_assert(kAlloc <= 232448, "shared memory of a CTA");
 };
 
-__device__ __forceinline__ int tile_start(const Item& it, int i) {
-    return i < it.nsink ? i * kKeys : it.lo + (i - it.nsink) * kKeys;
+// Half h (64 keys) of tile i of the list: its first key and the end of what it
+// may hold. Below nsink: the keys from 0 to sinks; then those from lo to hi.
+// Few first keys fit into the last tile's second half when the window leaves
+// it empty: a tile less.
+struct Half {
+    int start, end;
+};
+__device__ __forceinline__ Half tile_half(const Item& it, int i, int h) {
+    if (i < it.nsink) return {i * kKeys + h * 64, it.sinks};
+    if (h && i == it.joined) return {0, it.sinks};
+    return {it.lo + (i - it.nsink) * kKeys + h * 64, it.hi};
 }
-__device__ __forceinline__ int tile_end(const Item& it, int i) {
-    return i < it.nsink ? it.sinks : it.hi;
-}
+__device__ __forceinline__ int half_keys(Half x) { return max(0, min(64, x.end - x.start)); }
 
 struct AttnPlan {
     bool rows_mode;
@@ -210,10 +217,12 @@ __device__ __noinline__ void redo_row(const AttnParams& p, const Item& it, size_
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
     for (int i = first; i < it.count; i += step) {
-        const int j0 = tile_start(it, it.first + i);
-        attn_row<D>(p.q + row * D, p.k + cache, p.v + cache, j0,
-                    min(j0 + kKeys, tile_end(it, it.first + i)), lo, hi, it.sinks,
-                    p.negate ? -p.scale_log2 : p.scale_log2, m, l, o);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            const Half x = tile_half(it, it.first + i, h);
+            attn_row<D>(p.q + row * D, p.k + cache, p.v + cache, x.start, x.start + half_keys(x), lo, hi,
+                        it.sinks, p.negate ? -p.scale_log2 : p.scale_log2, m, l, o);
+        }
     }
     if (p.pieces == 0) {
         const float il = 1.f / l;
@@ -291,13 +300,17 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int3 work, It
     it->hi = p.causal ? it->pos0 + it->ntok : r.kv;
     it->lo = (p.causal && p.window > 0) ? max(0, it->pos0 + 1 - p.window) : 0;
     it->sinks = p.causal ? p.sinks : 0;
-    if (it->sinks >= it->lo) {
-        it->lo = 0;  // one range
-        it->nsink = 0;
-    } else {
-        it->nsink = (it->sinks + kKeys - 1) / kKeys;
+    it->nsink = 0;
+    it->joined = -1;
+    if (it->sinks >= it->lo) it->lo = 0;  // one range
+    int tiles = (it->hi - it->lo + kKeys - 1) / kKeys;
+    if (it->sinks < it->lo && it->sinks > 0) {
+        if (it->sinks <= 64 && it->hi - it->lo - (tiles - 1) * kKeys <= 64)
+            it->joined = tiles - 1;
+        else
+            it->nsink = (it->sinks + kKeys - 1) / kKeys;
+        tiles += it->nsink;
     }
-    const int tiles = it->nsink + (it->hi - it->lo + kKeys - 1) / kKeys;
     const int per = pl.nsplit == 1 ? tiles : (tiles + pl.nsplit - 1) / pl.nsplit;
     it->first = work.z * per;
     it->count = max(0, min(tiles - it->first, per));
@@ -312,7 +325,17 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int3 work, It
 // stores would touch 32 lines each; four lanes exchange their pieces first
 // and store 64 bytes of one row together: a quarter of the lines. dst[i] is
 // the address of row i of the lane's group of four, or null (not stored).
-__device__ __forceinline__ void store_rows(uint4 (&v)[4], char* const (&dst)[4], int off) {
+// With few rows to store in the warp (own: the lane's, or null) the plain
+// stores are as quick and spare the exchange.
+__device__ __forceinline__ void store_rows(uint4 (&v)[4], char* const (&dst)[4], char* own, bool few,
+                                           int off) {
+    if (few) {
+        if (own) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(own + off + i * 16) = v[i];
+        }
+        return;
+    }
     const int q = threadIdx.x & 3;
     auto swap = [&](uint4& a, uint4& b, int bit) {
         // Lanes with the bit set give a and get b of the other, and so on.
@@ -451,16 +474,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             ok = wait_phase(&empty[st], ((n / L::kStages) & 1) ^ 1, p.wait_limit_ns);
                             if (!ok) break;
                             const int i = it.first + (kv ? t : t - 2) / step;
-                            const int y = tile_start(it, i);
                             // The second half only where it holds a key.
-                            const int halves = tile_end(it, i) - y > 64 ? 2 : 1;
+                            const int halves = half_keys(tile_half(it, i, 1)) > 0 ? 2 : 1;
                             mbar_arrive_expect_tx(&full[st], halves * (L::kTileBytes / 2));
                             uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes;
 #pragma unroll 1
-                            for (int h = 0; h < halves; ++h)
+                            for (int h = 0; h < halves; ++h) {
+                                const int y = tile_half(it, i, h).start;
                                 for (int c = 0; c < D / 64; ++c)
                                     tma_load(dst + c * kPanel + h * (kPanel / 2), kv ? &tmK : &tmV,
-                                             c * 64, y + h * 64, unit, &full[st]);
+                                             c * 64, y, unit, &full[st]);
+                            }
                             ++n;
                         }
                     }
@@ -522,11 +546,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 ok = take(&vst);
                                 if (!ok) break;
                                 const int i = it.first + (rows ? (t - 2) >> 1 : t - 2);
-                                const int keep = tile_end(it, i) - tile_start(it, i);
-                                clean = keep < kKeys;
+                                const int keep0 = half_keys(tile_half(it, i, 0));
+                                const int keep1 = half_keys(tile_half(it, i, 1));
+                                clean = keep0 + keep1 < kKeys;
                                 if (clean) {
                                     misc[1] = vst;
-                                    misc[2] = keep;
+                                    misc[2] = keep0 | keep1 << 8;
                                     mbar_arrive(v_ask);
                                 }
                             }
@@ -598,11 +623,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int st = static_cast<int>(misc[1]);
                 if (st >= L::kStages) break;
                 uint8_t* vt = smem + L::kRingOff + st * L::kTileBytes;
-                const int keep = static_cast<int>(misc[2]);
-                for (int c = 0; c < D / 64; ++c)
+                const uint32_t keep = misc[2];
 #pragma unroll 1
-                    for (int e = keep * 8 + lane; e < kKeys * 8; e += 32)
-                        *reinterpret_cast<uint4*>(vt + c * kPanel + e * 16) = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < 2 * (D / 64); ++c)  // panel c >> 1, half c & 1
+#pragma unroll 1
+                    for (int e = ((keep >> (c & 1) * 8) & 255) * 8 + lane; e < 64 * 8; e += 32)
+                        *reinterpret_cast<uint4*>(vt + c * (kPanel / 2) + e * 16) =
+                            make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_clean);
@@ -710,16 +737,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 tc_fence_after();
                 if (any_valid) {
                     const int i = it.first + (rows ? j >> 1 : j);
-                    const int j0 = tile_start(it, i);
-                    const int end = min(row_hi, tile_end(it, i)) - j0;
-                    const bool partial = !(j0 + kKeys <= min(all_hi, tile_end(it, i)) &&
-                                           (j0 >= all_lo || j0 + kKeys <= it.sinks));
-                    const int lw = row_lo - j0, sk = it.sinks - j0;
+                    const Half h0 = tile_half(it, i, 0), h1 = tile_half(it, i, 1);
+                    const bool partial =
+                        i == it.joined || !(h0.start + kKeys <= min(all_hi, h0.end) &&
+                                            (h0.start >= all_lo || h0.start + kKeys <= it.sinks));
                     uint32_t x[2][32];
                     // Keys the row does not see: weight 0. Most 32-key chunks
                     // of a partial tile hold none.
                     auto hide = [&](int k, uint32_t* v) {
-                        const uint32_t vis = below(end - k) & (~below(lw - k) | below(sk - k));
+                        const Half x = k < 64 ? h0 : h1;
+                        const int j0 = x.start + (k & 32);
+                        const uint32_t vis = below(min(row_hi, x.end) - j0) &
+                                             (~below(row_lo - j0) | below(it.sinks - j0));
                         if (__any_sync(0xffffffffu, vis != 0xffffffffu)) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
@@ -834,6 +863,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                                   : reinterpret_cast<char*>(p.part_o) + at * D * 4);
                 const uint64_t addr =
                     (p.pieces == 0 ? valid : some) ? reinterpret_cast<uint64_t>(mine) : 0ull;
+                char* const own = reinterpret_cast<char*>(addr);
+                const bool few = __popc(__ballot_sync(0xffffffffu, addr != 0)) <= 8;
                 char* dst[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -860,7 +891,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             v[i].z = pack_bf16x2(__uint_as_float(w[4]) * il, __uint_as_float(w[5]) * il);
                             v[i].w = pack_bf16x2(__uint_as_float(w[6]) * il, __uint_as_float(w[7]) * il);
                         }
-                        store_rows(v, dst, k * 2);
+                        store_rows(v, dst, own, few, k * 2);
                     } else {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -868,7 +899,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             for (int i = 0; i < 4; ++i)
                                 v[i] = make_uint4(o[16 * h + 4 * i], o[16 * h + 4 * i + 1],
                                                   o[16 * h + 4 * i + 2], o[16 * h + 4 * i + 3]);
-                            store_rows(v, dst, k * 4 + h * 64);
+                            store_rows(v, dst, own, few, k * 4 + h * 64);
                         }
                     }
                 }

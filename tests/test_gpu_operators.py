@@ -167,6 +167,7 @@ WINDOW = [  # rows per sequence, lengths, S, window, sinks
     ([129], [400], 400, 130, 5), ([257], [257], 260, 64, 200), ([1] * 37, list(range(1, 38)), 40, 7, 1),
     ([300, 1, 5], [300, 300, 300], 384, 0, 0), ([2, 150], [2, 511], 513, 127, 129),
     ([64, 64], [64, 128], 128, 1000, 7), ([5], [1024], 1024, 0, 0),
+    ([64], [400], 400, 129, 5), ([2, 3], [500, 700], 704, 180, 64), ([1], [1000], 1000, 140, 65),
 ]
 SHAPES = [(1, 1, 64), (8, 1, 64), (4, 2, 128), (8, 2, 128), (2, 1, 128)]
 
