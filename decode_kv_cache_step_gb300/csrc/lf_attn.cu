@@ -274,10 +274,11 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint6
 // tiles. Sequence b's tiles start at index floor(q_start[b] / tok) + b: enough
 // for its rows wherever they start, so no prefix sum over the sequences is
 // needed. False where the tile holds no rows.
-__device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int3 work, Item* it) {
+__device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int2 work, Item* it) {
     const int lane = threadIdx.x & 31;
-    // A head's last tiles (the longest rows of a causal prompt) come first.
-    const int x = pl.items - 1 - work.x;
+    // The last tiles (the longest rows of a causal prompt) come first, a
+    // tile's KV heads together (they share its rows of Q and out).
+    const int x = pl.items - 1 - work.x / p.Hkv;
     int b = 0, len = p.N;
 #pragma unroll 1
     while (len > 1) {
@@ -312,10 +313,10 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int3 work, It
         tiles += it->nsink;
     }
     const int per = pl.nsplit == 1 ? tiles : (tiles + pl.nsplit - 1) / pl.nsplit;
-    it->first = work.z * per;
+    it->first = work.y * per;
     it->count = max(0, min(tiles - it->first, per));
-    it->kvh = work.y;
-    it->split = work.z;
+    it->kvh = work.x % p.Hkv;
+    it->split = work.y;
     it->stop = 0;
     return true;
 }
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int w = 0;     // items handed out
             int done = 0;  // items with work
             bool ok = true;
-            int3 work = make_int3(blockIdx.x, blockIdx.y, blockIdx.z);
+            int2 work = make_int2(blockIdx.x, blockIdx.y);
             for (int round = 0;; ++round) {
                 Item it;
                 if (work.x >= 0) {
@@ -798,36 +799,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const uint64_t b2 = pack_f32x2(base, base);
                     uint64_t sum[2] = {0ull, 0ull};
                     float top = -INFINITY;
-                    tmem_ld32(ts, x[0]);
+                    // Weights of 32 keys: exponentials, sum, P.
+                    auto weigh = [&](int k, const uint32_t* v) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int k0 = 0; k0 < kKeys; k0 += 64) {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int k = k0 + 32 * q;
-                            uint32_t* v = x[q];
-                            tmem_wait_ld();
-                            if (k + 32 < kKeys) tmem_ld32(ts + k + 32, x[q ^ 1]);
-                            if (partial) hide(k, v);
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float a, b;
-                                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[e]),
-                                                                  __uint_as_float(v[e + 1])), c2, b2),
-                                             a, b);
-                                a = ex2_approx(a);
-                                b = ex2_approx(b);
-                                sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
-                                pk[e >> 1] = pack_bf16x2(a, b);
-                            }
-                            top = fmaxf(top, largest(v));
-                            tmem_st16(ts + (k >> 1), pk);
+                        for (int e = 0; e < 32; e += 2) {
+                            float a, b;
+                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[e]),
+                                                              __uint_as_float(v[e + 1])), c2, b2), a, b);
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                            sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
+                            pk[e >> 1] = pack_bf16x2(a, b);
                         }
-                        if (k0 == 0) {
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&p_half[s]);
+                        top = fmaxf(top, largest(v));
+                        tmem_st16(ts + (k >> 1), pk);
+                    };
+                    auto hand_over = [&]() {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_half[s]);
+                    };
+                    if (!partial) {
+                        tmem_ld32(ts, x[0]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            tmem_wait_ld();
+                            if (q < 3) tmem_ld32(ts + 32 * (q + 1), x[(q + 1) & 1]);
+                            weigh(32 * q, x[q & 1]);
+                            if (q == 1) hand_over();
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < kKeys; k += 32) {
+                            tmem_ld32(ts + k, x[0]);
+                            tmem_wait_ld();
+                            hide(k, x[0]);
+                            weigh(k, x[0]);
+                            if (k == 32) hand_over();
                         }
                     }
                     tmem_wait_st();
@@ -997,8 +1007,7 @@ cudaError_t launch_attention_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
         if (e != cudaSuccess) return e;
         configured_for = dev;
     }
-    const dim3 grid(static_cast<unsigned>(pl.items), static_cast<unsigned>(p.Hkv),
-                    static_cast<unsigned>(pl.nsplit));
+    const dim3 grid(static_cast<unsigned>(pl.items) * p.Hkv, static_cast<unsigned>(pl.nsplit));
     kernel<<<grid, kAttnThreads, L::kAlloc, stream>>>(tmQ, tmK, tmV, p, pl);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.pieces == 0 || !p.out) return e;

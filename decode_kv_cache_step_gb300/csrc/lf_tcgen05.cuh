@@ -150,23 +150,22 @@ __device__ __forceinline__ void cancel_next_cta(void* answer, uint64_t* bar) {
         : "memory");
 }
 
-// The answer: blockIdx of the CTA, or x = -1 (none was left; no further
+// The answer: blockIdx (x, y) of the CTA, or x = -1 (none was left; no further
 // request may follow).
-__device__ __forceinline__ int3 cancelled_cta(const void* answer) {
-    uint32_t got, x, y, z;
+__device__ __forceinline__ int2 cancelled_cta(const void* answer) {
+    uint32_t got, x, y;
     asm volatile(
         "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
-        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "ld.shared.b128 h, [%4];\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+        "ld.shared.b128 h, [%3];\n\t"
         "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t"
         "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, h;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::z.b32.b128 %3, h;\n\t}"
-        : "=r"(got), "=r"(x), "=r"(y), "=r"(z)
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, h;\n\t}"
+        : "=r"(got), "=r"(x), "=r"(y)
         : "r"(smem_u32(answer))
         : "memory");
-    return make_int3(got ? static_cast<int>(x) : -1, static_cast<int>(y), static_cast<int>(z));
+    return make_int2(got ? static_cast<int>(x) : -1, static_cast<int>(y));
 }
 
 // ------------------------------------------------------------ packed fp32 --
