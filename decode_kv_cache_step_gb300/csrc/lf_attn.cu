@@ -281,7 +281,7 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int2 work, It
     const int x = pl.items - 1 - work.x / p.Hkv;
     int b = 0, len = p.N;
 #pragma unroll 1
-    while (len > 1) {
+    while (len > 32) {
         const int step = (len + 31) >> 5;
         const int i = b + lane * step;
         const bool le = lane * step < len && (p.q_start[i] >> pl.tok_shift) + i <= x;
@@ -290,8 +290,21 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int2 work, It
         b += top * step;
         len = min(step, len - top * step);
     }
+    // The last 32 sequences: their ranges and lengths in one round trip.
     SeqRange r;
-    if (!seq_range(p.q_start, p.kv_len, b, p.T, p.S, p.causal, p.dev_err, &r)) return false;
+    const int i = b + min(lane, len - 1);
+    const bool good = seq_range(p.q_start, p.kv_len, i, p.T, p.S, p.causal, &r);
+    const unsigned hit =
+        __ballot_sync(0xffffffffu, lane < len && (r.q0 >> pl.tok_shift) + i <= x);
+    const int top = hit ? 31 - __clz(hit) : 0;
+    b += top;
+    r.q0 = __shfl_sync(0xffffffffu, r.q0, top);
+    r.n = __shfl_sync(0xffffffffu, r.n, top);
+    r.kv = __shfl_sync(0xffffffffu, r.kv, top);
+    if (!__shfl_sync(0xffffffffu, good, top)) {
+        if (lane == 0) atomicOr(p.dev_err, kErrBadLength);
+        return false;
+    }
     const int rel = (x - (r.q0 >> pl.tok_shift) - b) << pl.tok_shift;
     if (rel < 0 || rel >= r.n) return false;
     it->seq = b;
@@ -312,9 +325,8 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int2 work, It
             it->nsink = (it->sinks + kKeys - 1) / kKeys;
         tiles += it->nsink;
     }
-    const int per = pl.nsplit == 1 ? tiles : (tiles + pl.nsplit - 1) / pl.nsplit;
-    it->first = work.y * per;
-    it->count = max(0, min(tiles - it->first, per));
+    it->first = tiles * work.y / pl.nsplit;
+    it->count = tiles * (work.y + 1) / pl.nsplit - it->first;
     it->kvh = work.x % p.Hkv;
     it->split = work.y;
     it->stop = 0;
@@ -431,6 +443,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // Everything above may run while the previous kernel of the stream ends.
+    grid_dependency_wait();
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     // Work units of the streams: unit j of an item belongs to stream j & 1 and
     // reads K/V tile j >> 1 (rows mode) or j (keys mode) of the item's part of
@@ -952,15 +966,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) lf_attn_merge_kernel(const A
     allow_dependent_launch();
     const size_t row = at < rows ? at : rows - 1;
     const int t = static_cast<int>(row / p.Hq);
-    // A batch of single tokens has its row t in sequence t. (The lengths were
-    // there before the attention kernel started: they need no wait.)
+    // Every thread waits, so this grid ends after the attention grid.
+    grid_dependency_wait();
+    // A batch of single tokens has its row t in sequence t.
     int n = min(t, p.N - 1);
     if (!(p.q_start[n] <= t && t < p.q_start[n + 1])) n = seq_of_row(p.q_start, p.N, t);
     SeqRange r;
-    const bool mine = seq_range(p.q_start, p.kv_len, n, p.T, p.S, p.causal, p.dev_err, &r) &&
-                      t >= r.q0 && t < r.q0 + r.n && at < rows;
-    // Every thread waits, so this grid ends after the attention grid.
-    grid_dependency_wait();
+    const bool mine = seq_range(p.q_start, p.kv_len, n, p.T, p.S, p.causal, &r) && t >= r.q0 && t < r.q0 + r.n && at < rows;
     if (!mine) return;
     const float2 ml = lane < p.pieces ? __ldcg(&p.part_ml[lane * rows + row])
                                       : make_float2(-INFINITY, 0.f);
@@ -972,20 +984,33 @@ __global__ void __launch_bounds__(kMergeWarps * 32) lf_attn_merge_kernel(const A
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
     w = l == 0.f ? 0.f : w / l;
+    // The pieces' outputs, eight loads in flight; one without a visible key
+    // was not written and is not read.
     constexpr int kC = D / 32;
+    constexpr int kBatch = 8;
     float o[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) o[c] = 0.f;
-    for (int i = 0; i < p.pieces; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        if (wi == 0.f) continue;  // nothing visible: the piece's output was not written
-        const float* po = p.part_o + (i * rows + row) * D + lane * kC;
+    const float* po = p.part_o + row * D + lane * kC;
+    for (int i0 = 0; i0 < p.pieces; i0 += kBatch) {
+        float wi[kBatch], v[kBatch][kC];
 #pragma unroll
-        for (int c = 0; c < kC; c += 2) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(po + c));
-            o[c] += wi * v.x;
-            o[c + 1] += wi * v.y;
+        for (int i = 0; i < kBatch; ++i) {
+            wi[i] = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+            if (i0 + i >= p.pieces) wi[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kC; c += 2) {
+                float2 x = make_float2(0.f, 0.f);
+                if (wi[i] != 0.f)
+                    x = __ldcg(reinterpret_cast<const float2*>(po + (i0 + i) * rows * D + c));
+                v[i][c] = x.x;
+                v[i][c + 1] = x.y;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int c = 0; c < kC; ++c) o[c] += wi[i] * v[i][c];
     }
 #pragma unroll
     for (int c = 0; c < kC; c += 2)
@@ -1008,20 +1033,23 @@ cudaError_t launch_attention_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
         configured_for = dev;
     }
     const dim3 grid(static_cast<unsigned>(pl.items) * p.Hkv, static_cast<unsigned>(pl.nsplit));
-    kernel<<<grid, kAttnThreads, L::kAlloc, stream>>>(tmQ, tmK, tmV, p, pl);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || p.pieces == 0 || !p.out) return e;
-    const size_t rows = static_cast<size_t>(p.T) * p.Hq;
     const char* env = std::getenv("LF_PDL");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
-    cfg.blockDim = dim3(kMergeWarps * 32);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = L::kAlloc;
+    cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = (env && std::atoi(env) == 0) ? 0 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, tmQ, tmK, tmV, p, pl);
+    if (e != cudaSuccess || p.pieces == 0 || !p.out) return e != cudaSuccess ? e : cudaGetLastError();
+    const size_t rows = static_cast<size_t>(p.T) * p.Hq;
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, lf_attn_merge_kernel<D>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

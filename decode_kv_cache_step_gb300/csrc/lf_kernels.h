@@ -188,24 +188,20 @@ cudaError_t launch_attention(int D, const CUtensorMap& tmQ, const CUtensorMap& t
 // Error bit of lengths that do not fit (LF_DEVERR_BAD_LENGTH).
 constexpr uint32_t kErrBadLength = 0x4u;
 
-// Range of sequence n in packed rows and its cache length; false (and the
-// error bit) when they do not fit: the sequence is then skipped.
+// Range of sequence b in packed rows and its cache length; false when they do
+// not fit: the sequence is then skipped and kErrBadLength raised.
 struct SeqRange {
     int q0, n, kv;
 };
 __device__ __forceinline__ bool seq_range(const int32_t* q_start, const int32_t* kv_len, int b,
-                                          int T, int S, bool causal, uint32_t* dev_err,
-                                          SeqRange* r) {
+                                          int T, int S, bool causal, SeqRange* r) {
     const int q0 = q_start[b];
     const int q1 = q_start[b + 1];
     const int kv = kv_len[b];
     r->q0 = q0;
     r->n = q1 - q0;
     r->kv = kv;
-    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= T && kv >= 0 && kv <= S &&
-                    (!causal || q1 - q0 <= kv);
-    if (!ok) atomicOr(dev_err, kErrBadLength);
-    return ok;
+    return q0 >= 0 && q1 >= q0 && q1 <= T && kv >= 0 && kv <= S && (!causal || q1 - q0 <= kv);
 }
 
 // The sequence of packed row t: the last b with q_start[b] <= t (0 if none;

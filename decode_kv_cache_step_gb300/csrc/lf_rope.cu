@@ -16,6 +16,8 @@
 // reduction to one turn: positions of a million times frequencies near 1 need
 // more than 32 bits, and a CTA has only a few hundred of them) while the
 // first heads' loads are in flight.
+#include <stdlib.h>
+
 #include <algorithm>
 
 #include "lf_kernels.h"
@@ -65,13 +67,18 @@ __global__ void __launch_bounds__(kRopeThreads) lf_rope_kernel(const RopeParams 
     __shared__ TokenAt at[kMaxTokens];
     __shared__ float2 cs[kMaxTokens][D / 2];
     const int tid = threadIdx.x;
+    allow_dependent_launch();
+    grid_dependency_wait();
     const bool append = p.q_start != nullptr;
     if (static_cast<int>(blockIdx.x) >= tok_ctas) {
         // Ages of the prompt's tokens, one CTA per (sequence, KV head).
         const int u = blockIdx.x - tok_ctas;
         const int b = u / p.Hkv;
         SeqRange r;
-        if (!seq_range(p.q_start, p.kv_len, b, p.T, p.S, true, p.dev_err, &r)) return;
+        if (!seq_range(p.q_start, p.kv_len, b, p.T, p.S, true, &r)) {
+            if (tid == 0) atomicOr(p.dev_err, kErrBadLength);
+            return;
+        }
         int32_t* m = p.mask + static_cast<size_t>(u) * p.S;
         for (int j = tid; j < r.kv; j += kRopeThreads) m[j] = r.kv - 1 - j;
         return;
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(kRopeThreads) lf_rope_kernel(const RopeParams 
         if (append) {
             a.b = warp_seq_of_row(p.q_start, p.B, t);
             SeqRange r;
-            if (seq_range(p.q_start, p.kv_len, a.b, p.T, p.S, true, p.dev_err, &r) && t >= r.q0 &&
+            if (seq_range(p.q_start, p.kv_len, a.b, p.T, p.S, true, &r) && t >= r.q0 &&
                 t < r.q0 + r.n) {
                 a.slot = r.kv - r.n + (t - r.q0);
                 a.pos = a.slot + (p.pos_offset ? p.pos_offset[a.b] : 0);
@@ -238,8 +245,18 @@ cudaError_t launch_rope_t(const RopeParams& p, int sms, cudaStream_t stream) {
     while (per > 1 && (p.T + per - 1) / per < 4 * sms) per >>= 1;
     const int tok_ctas = (p.T + per - 1) / per;
     const int age_ctas = p.q_start ? p.B * p.Hkv : 0;
-    lf_rope_kernel<D><<<tok_ctas + age_ctas, kRopeThreads, 0, stream>>>(p, per, tok_ctas);
-    return cudaGetLastError();
+    const char* env = std::getenv("LF_PDL");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tok_ctas + age_ctas);
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = (env && std::atoi(env) == 0) ? 0 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, lf_rope_kernel<D>, p, per, tok_ctas);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

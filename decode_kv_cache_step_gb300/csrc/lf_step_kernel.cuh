@@ -446,24 +446,6 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
                                  uint8_t* topk_area, uint8_t* scan_area, int scan_bytes,
                                  uint64_t* scan_bars, int tid);
 
-// Running maximum and sum of a query row's shared-prefix pieces (log2 domain).
-__device__ __forceinline__ float prefix_max(const StepParams& p, size_t row, size_t rows, float m) {
-    for (int c = 0; c < p.pre_pieces; ++c) {
-        const float2 v = __ldcg(&p.pre_ml[c * rows + row]);
-        if (v.y != 0.f) m = fmaxf(m, v.x);
-    }
-    return m;
-}
-
-__device__ __forceinline__ float prefix_sum(const StepParams& p, size_t row, size_t rows, float m) {
-    float l = 0.f;
-    for (int c = 0; c < p.pre_pieces; ++c) {
-        const float2 v = __ldcg(&p.pre_ml[c * rows + row]);
-        if (v.y != 0.f) l += v.y * exp2f(v.x - m);
-    }
-    return l;
-}
-
 // Merge of the unit's chunks by its last CTA (consumer threads only). The
 // shared memory below `usable` is free; scan_bars are two spare mbarriers.
 // kPrefix: the pieces of the unit's shared-prefix attention (pre_ml, pre_o of
@@ -483,10 +465,13 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
     // [nchunk]: the chunk's live-tile bit mask (0: no live slot; all ones
     // when the masks were not kept)
     int* s_live = s_ncand + 4;
-    // kPrefix, [pieces][G]: 2^(m_piece - m) / l
-    float* s_wp = reinterpret_cast<float*>(s_live + nchunk);
+    // kPrefix: the joined (m, l) of the pieces [G], then [G][pieces] the
+    // pieces' (m, l), and from that 2^(m_piece - m) / l
+    float2* s_pre = reinterpret_cast<float2*>(
+        (reinterpret_cast<uintptr_t>(s_live + nchunk) + 7) & ~static_cast<uintptr_t>(7));
+    float2* s_piece = s_pre + G;
     uint8_t* topk_area = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(s_wp + (kPrefix ? p.pre_pieces * G : 0)) + 15) &
+        (reinterpret_cast<uintptr_t>(s_pre + (kPrefix ? (p.pre_pieces + 1) * G : 0)) + 15) &
         ~static_cast<uintptr_t>(15));
     uint8_t* scan_area = topk_area + (p.topk > 1 ? kTopKAreaBytes : 0);
     const int scan_bytes = usable - static_cast<int>(scan_area - smem);
@@ -497,6 +482,26 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
     const size_t row0 = static_cast<size_t>(b) * p.Hq + kvh * G;  // the unit's first query row
     __nv_bfloat16* out = p.out + row0 * D;
     const size_t pre_rows = kPrefix ? static_cast<size_t>(gridDim.y) / p.Hkv * p.Hq : 0;  // B * Hq
+
+    // Prefix pieces: a warp per head, a lane per piece (at most 32).
+    if constexpr (kPrefix) {
+        const int lane = tid & 31;
+        for (int h = tid >> 5; h < G; h += kConsumerWarps) {
+            float2 v = make_float2(-INFINITY, 0.f);
+            if (lane < p.pre_pieces) v = __ldcg(&p.pre_ml[lane * pre_rows + row0 + h]);
+            if (v.y == 0.f) v.x = -INFINITY;
+            float m = v.x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            float l = v.y == 0.f ? 0.f : v.y * exp2f(v.x - m);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+            if (lane < p.pre_pieces) s_piece[h * p.pre_pieces + lane] = v;
+            if (lane == 0) s_pre[h] = make_float2(m, l);
+        }
+        consumer_bar_sync();
+    }
 
     // The partial outputs of the first four chunks are requested first: they
     // do not depend on (m, l), so their round trip overlaps the weights'.
@@ -534,12 +539,14 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
 #pragma unroll
             for (int c = 0; c < kFastChunks; ++c)
                 if (c < nchunk) m = fmaxf(m, mlv[c].x);
-            if constexpr (kPrefix) m = prefix_max(p, row0 + tid, pre_rows, m);
+            if constexpr (kPrefix) m = fmaxf(m, s_pre[tid].x);
             float l = 0.f;
 #pragma unroll
             for (int c = 0; c < kFastChunks; ++c)
                 if (c < nchunk && mlv[c].x != -INFINITY) l += mlv[c].y * exp2f(mlv[c].x - m);
-            if constexpr (kPrefix) l += prefix_sum(p, row0 + tid, pre_rows, m);
+            if constexpr (kPrefix) {
+                if (s_pre[tid].y != 0.f) l += s_pre[tid].y * exp2f(s_pre[tid].x - m);
+            }
             const float il = (l > 0.f) ? 1.f / l : 0.f;
             s_m[tid] = m;
             s_il[tid] = il;
@@ -554,21 +561,17 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
         } else {
             float m = -INFINITY;
             for (int c = 0; c < nchunk; ++c) m = fmaxf(m, __ldcg(&ml[c * G + tid]).x);
-            if constexpr (kPrefix) m = prefix_max(p, row0 + tid, pre_rows, m);
+            if constexpr (kPrefix) m = fmaxf(m, s_pre[tid].x);
             float l = 0.f;
             for (int c = 0; c < nchunk; ++c) {
                 const float2 v = __ldcg(&ml[c * G + tid]);
                 if (v.x != -INFINITY) l += v.y * exp2f(v.x - m);
             }
-            if constexpr (kPrefix) l += prefix_sum(p, row0 + tid, pre_rows, m);
+            if constexpr (kPrefix) {
+                if (s_pre[tid].y != 0.f) l += s_pre[tid].y * exp2f(s_pre[tid].x - m);
+            }
             s_m[tid] = m;
             s_il[tid] = (l > 0.f) ? 1.f / l : 0.f;
-        }
-        if constexpr (kPrefix) {
-            for (int c = 0; c < p.pre_pieces; ++c) {
-                const float2 v = __ldcg(&p.pre_ml[c * pre_rows + row0 + tid]);
-                s_wp[c * G + tid] = v.y == 0.f ? 0.f : exp2f(v.x - s_m[tid]) * s_il[tid];
-            }
         }
     }
     if (kScore && ptl) {
@@ -596,6 +599,12 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
 #pragma unroll
     for (int k = 0; k < kPerT; ++k) o[k] = 0.f;
     if constexpr (kPrefix) {
+        for (int e = tid; e < p.pre_pieces * G; e += kConsumers) {
+            const int h = e / p.pre_pieces;
+            const float2 v = s_piece[e];
+            s_piece[e].x = v.y == 0.f ? 0.f : exp2f(v.x - s_m[h]) * s_il[h];
+        }
+        consumer_bar_sync();
         // Four pieces' loads in flight at a time; the row's address is in
         // bounds for every piece, and a piece without a key is selected away.
         for (int c0 = 0; c0 < p.pre_pieces; c0 += 4) {
@@ -617,7 +626,7 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
 #pragma unroll
                 for (int k = 0; k < kPerT; ++k) {
                     const int e = tid + k * kConsumers;
-                    const float w = (e < G * D) ? s_wp[c * G + e / D] : 0.f;
+                    const float w = (e < G * D) ? s_piece[e / D * p.pre_pieces + c].x : 0.f;
                     o[k] += (w != 0.f) ? w * v[cc][k] : 0.f;
                 }
             }
@@ -1947,7 +1956,7 @@ cudaError_t launch_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepP
     using L = StepSmem<D, kStages>;
     static_assert(!(kCluster && kPrefix), "the cluster merge takes no prefix pieces");
     if (finish_smem_bytes(p_in.nchunk, G, kScore ? p_in.topk : 1) +
-            (kPrefix ? static_cast<size_t>(p_in.pre_pieces) * G * 4 : 0) >
+            (kPrefix ? static_cast<size_t>(p_in.pre_pieces + 1) * G * 8 + 8 : 0) >
         static_cast<size_t>(L::kBarOff))
         return cudaErrorInvalidConfiguration;
     auto kernel = lf_decode_step_kernel<D, G, kStages, kScore, kCluster, kPrefix>;
