@@ -12,22 +12,23 @@
 // halves' chunks at the same offset, or the neighbours of an interleaved
 // pair, so only the norm's sum crosses lanes. A CTA takes all heads of one to
 // four tokens, and a lane keeps its 4 angles and its weights for all of them.
-// The angles are formed once per CTA in shared memory (fp64 product and
-// reduction to one turn: positions of a million times frequencies near 1 need
-// more than 32 bits, and a CTA has only a few hundred of them) while the
-// first heads' loads are in flight.
+// The angles are formed once per CTA in shared memory while the first heads'
+// loads are in flight: positions of a million times frequencies near 1 need
+// some 44 bits, which two floats hold (fp64 would take 1000 cycles of an SM's
+// fp64 unit per CTA).
 #include <stdlib.h>
 
 #include <algorithm>
 
 #include "lf_kernels.h"
-#include "lf_ptx.cuh"
+#include "lf_tcgen05.cuh"
 
 namespace lf {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kBatch = 6;      // heads whose loads a lane has in flight
+constexpr int kRopePerSm = 4;
+constexpr int kBatch = 4;      // heads whose loads a lane has in flight
 constexpr int kMaxTokens = 4;  // tokens of a CTA
 
 struct TokenAt {
@@ -50,17 +51,38 @@ __device__ __forceinline__ int warp_seq_of_row(const int32_t* q_start, int B, in
     return b;
 }
 
-__device__ __forceinline__ void widen4(const uint2& v, float* x) {
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-    x[0] = a.x;
-    x[1] = a.y;
-    x[2] = b.x;
-    x[3] = b.y;
+// Two bf16 values as packed fp32 (exact).
+__device__ __forceinline__ uint64_t widen2(uint32_t v) {
+    return pack_f32x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t narrow2(uint64_t v) {
+    float x, y;
+    unpack_f32x2(v, x, y);
+    return pack_bf16x2(x, y);
+}
+
+__device__ __forceinline__ uint64_t swap2(uint64_t v) {
+    float x, y;
+    unpack_f32x2(v, x, y);
+    return pack_f32x2(y, x);
+}
+
+// n * f / (2 pi) reduced to a turn, for an n with at most 24 significant bits:
+// the product is exact in two floats (fused multiply-add), 1 / (2 pi) is held
+// in two, and the leading part's fraction is exact.
+__device__ __forceinline__ float turns(float n, float f) {
+    constexpr float kHi = 0.15915494f;       // 1 / (2 pi) to 24 bits
+    constexpr float kLo = 6.4206383e-09f;    // and the rest of it
+    const float p = n * f;
+    const float p_lo = fmaf(n, f, -p);
+    const float t = p * kHi;
+    const float t_lo = fmaf(p, kHi, -t) + fmaf(p, kLo, p_lo * kHi);
+    return (t - rintf(t)) + t_lo;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) lf_rope_kernel(const RopeParams p, int tok_per_cta,
+__global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const RopeParams p, int tok_per_cta,
                                                                int tok_ctas) {
     constexpr int kLanes = D / 8;                   // lanes of one head
     constexpr int kGroups = kRopeThreads / kLanes;  // heads a CTA holds at a time
@@ -150,27 +172,48 @@ __global__ void __launch_bounds__(kRopeThreads) lf_rope_kernel(const RopeParams 
     __syncthreads();
     for (int i = tid; i < ntok * half; i += kRopeThreads) {
         const int kk = i / half;
-        // Half turns, reduced to [-1, 1]: sin and cos of pi times that.
-        double a = static_cast<double>(at[kk].pos) *
-                   static_cast<double>(__ldg(p.inv_freq + (i - kk * half))) * 0.31830988618379067154;
-        a -= 2.0 * rint(a * 0.5);
+        // In two parts that are exact in fp32, so any int32 position is.
+        const int n = at[kk].pos;
+        const float f = __ldg(p.inv_freq + (i - kk * half));
+        float t = turns(static_cast<float>(n & ~0xfff), f) + turns(static_cast<float>(n & 0xfff), f);
+        t -= rintf(t);
         float s, c;
-        sincospif(static_cast<float>(a), &s, &c);
+        sincospif(2.f * t, &s, &c);
         cs[kk][i - kk * half] = make_float2(c, s);
     }
     __syncthreads();
     if (!active) return;
     const TokenAt a = at[k];
     if (a.b < 0) return;
-    float c[4], s[4];
+    // y = x cos + other sin, two values at a time: other is the chunk's
+    // partner, or (interleaved) its own values swapped, the sign in sin.
+    uint64_t ca[2], cb[2], sa[2], sb[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 v = turned ? cs[k][4 * lane + i] : make_float2(1.f, 0.f);
-        c[i] = v.x;
-        s[i] = v.y;
+    for (int i = 0; i < 2; ++i) {
+        const float2 one = make_float2(1.f, 0.f);
+        const float2 u = turned ? cs[k][4 * lane + (p.interleaved ? i : 2 * i)] : one;
+        const float2 v = turned ? cs[k][4 * lane + (p.interleaved ? i + 2 : 2 * i + 1)] : one;
+        if (p.interleaved) {
+            ca[i] = pack_f32x2(u.x, u.x);
+            sa[i] = pack_f32x2(-u.y, u.y);
+            cb[i] = pack_f32x2(v.x, v.x);
+            sb[i] = pack_f32x2(-v.y, v.y);
+        } else {
+            ca[i] = cb[i] = pack_f32x2(u.x, v.x);
+            sa[i] = pack_f32x2(-u.y, -v.y);
+            sb[i] = pack_f32x2(u.y, v.y);
+        }
     }
     const unsigned gmask = ((1u << kLanes) - 1u) << ((tid & 31) / kLanes * kLanes);
     const int t = tok0 + k;
+    // Where the token's heads go: queries, keys, values.
+    const int64_t kv_step = append ? static_cast<int64_t>(p.S) * D : D;
+    const int64_t kv0 = append ? (static_cast<int64_t>(a.b) * p.Hkv * p.S + a.slot) * D
+                               : static_cast<int64_t>(t) * p.Hkv * D;
+    __nv_bfloat16* const qd = p.q_out + static_cast<int64_t>(t) * p.Hq * D;
+    __nv_bfloat16* const kd = p.k_out + kv0 - p.Hq * kv_step;
+    __nv_bfloat16* const vd = p.v_out + kv0 - (p.Hq + p.Hkv) * kv_step;
+    const bool norm = p.q_weight != nullptr;
     for (int h = h0; h < heads; h += kBatch * per_tok) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -180,57 +223,36 @@ __global__ void __launch_bounds__(kRopeThreads) lf_rope_kernel(const RopeParams 
             const bool is_v = hh >= p.Hq + p.Hkv;
             uint2 oa = ra[i], ob = rb[i];
             if (!is_v) {
-                float x[4], y[4];
-                widen4(ra[i], x);
-                widen4(rb[i], y);
-                if (p.q_weight) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) ss += x[e] * x[e] + y[e] * y[e];
+                uint64_t x[2] = {widen2(oa.x), widen2(oa.y)}, y[2] = {widen2(ob.x), widen2(ob.y)};
+                if (norm) {
+                    float s0, s1;
+                    unpack_f32x2(fma_f32x2(x[0], x[0], fma_f32x2(x[1], x[1],
+                                 fma_f32x2(y[0], y[0], mul_f32x2(y[1], y[1])))), s0, s1);
+                    float ss = s0 + s1;
 #pragma unroll
                     for (int off = kLanes / 2; off > 0; off >>= 1)
                         ss += __shfl_xor_sync(gmask, ss, off);
-                    const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-                    float wa[4], wb[4];
-                    widen4(is_q ? wq[0] : wk[0], wa);
-                    widen4(is_q ? wq[1] : wk[1], wb);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] *= inv * wa[e];
-                        y[e] *= inv * wb[e];
-                    }
+                    const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+                    const uint64_t inv2 = pack_f32x2(inv, inv);
+                    const uint2 wa = is_q ? wq[0] : wk[0], wb = is_q ? wq[1] : wk[1];
+                    // The norm first: a weight times a large value may overflow.
+                    x[0] = mul_f32x2(mul_f32x2(x[0], inv2), widen2(wa.x));
+                    x[1] = mul_f32x2(mul_f32x2(x[1], inv2), widen2(wa.y));
+                    y[0] = mul_f32x2(mul_f32x2(y[0], inv2), widen2(wb.x));
+                    y[1] = mul_f32x2(mul_f32x2(y[1], inv2), widen2(wb.y));
                 }
-                if (turned) {
-                    if (p.interleaved) {
 #pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            const float x0 = x[e], y0 = y[e];
-                            x[e] = x0 * c[e / 2] - x[e + 1] * s[e / 2];
-                            x[e + 1] = x[e + 1] * c[e / 2] + x0 * s[e / 2];
-                            y[e] = y0 * c[2 + e / 2] - y[e + 1] * s[2 + e / 2];
-                            y[e + 1] = y[e + 1] * c[2 + e / 2] + y0 * s[2 + e / 2];
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float x0 = x[e];
-                            x[e] = x0 * c[e] - y[e] * s[e];
-                            y[e] = y[e] * c[e] + x0 * s[e];
-                        }
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const uint64_t u = p.interleaved ? swap2(x[e]) : y[e];
+                    const uint64_t v = p.interleaved ? swap2(y[e]) : x[e];
+                    const uint64_t nx = fma_f32x2(u, sa[e], mul_f32x2(x[e], ca[e]));
+                    y[e] = fma_f32x2(v, sb[e], mul_f32x2(y[e], cb[e]));
+                    x[e] = nx;
                 }
-                oa = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-                ob = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                oa = make_uint2(narrow2(x[0]), narrow2(x[1]));
+                ob = make_uint2(narrow2(y[0]), narrow2(y[1]));
             }
-            __nv_bfloat16* dst;
-            if (is_q) {
-                dst = p.q_out + (static_cast<size_t>(t) * p.Hq + hh) * D;
-            } else {
-                const int kvh = is_v ? hh - p.Hq - p.Hkv : hh - p.Hq;
-                dst = (is_v ? p.v_out : p.k_out) +
-                      (append ? ((static_cast<size_t>(a.b) * p.Hkv + kvh) * p.S + a.slot)
-                              : (static_cast<size_t>(t) * p.Hkv + kvh)) * D;
-            }
+            __nv_bfloat16* const dst = is_q ? qd + hh * D : (is_v ? vd : kd) + hh * kv_step;
             *reinterpret_cast<uint2*>(dst + ea) = oa;
             *reinterpret_cast<uint2*>(dst + eb) = ob;
         }
