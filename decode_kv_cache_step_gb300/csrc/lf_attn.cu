@@ -798,19 +798,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                         tmem_wait_st();
                     }
-                    if (__any_sync(0xffffffffu, m == -INFINITY)) {
-                        float t = -INFINITY;
-#pragma unroll 1
-                        for (int k = 0; k < kKeys; k += 32) {
-                            tmem_ld32(ts + k, x[0]);
-                            tmem_wait_ld();
-                            if (partial) hide(k, x[0]);
-                            t = fmaxf(t, largest(x[0]));
-                        }
-                        if (m == -INFINITY) m = t * c;
-                    }
-                    const float base = m == -INFINITY ? 0.f : -m;
-                    const uint64_t b2 = pack_f32x2(base, base);
+                    uint64_t b2 = 0;
                     uint64_t sum[2] = {0ull, 0ull};
                     float top = -INFINITY;
                     // Weights of 32 keys: exponentials, sum, P.
@@ -835,8 +823,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&p_half[s]);
                     };
+                    auto refer = [&]() {
+                        const float base = m == -INFINITY ? 0.f : -m;
+                        b2 = pack_f32x2(base, base);
+                    };
                     if (!partial) {
                         tmem_ld32(ts, x[0]);
+                        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                            // No reference yet: the largest of the first 32.
+                            tmem_wait_ld();
+                            const float t = largest(x[0]) * c;
+                            if (m == -INFINITY) m = t;
+                        }
+                        refer();
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             tmem_wait_ld();
@@ -845,13 +844,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             if (q == 1) hand_over();
                         }
                     } else {
-#pragma unroll 1
-                        for (int k = 0; k < kKeys; k += 32) {
-                            tmem_ld32(ts + k, x[0]);
-                            tmem_wait_ld();
-                            hide(k, x[0]);
-                            weigh(k, x[0]);
-                            if (k == 32) hand_over();
+                        uint32_t v[4][32];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, v[q]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) hide(32 * q, v[q]);
+                        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                            const float t = fmaxf(fmaxf(largest(v[0]), largest(v[1])),
+                                                  fmaxf(largest(v[2]), largest(v[3]))) * c;
+                            if (m == -INFINITY) m = t;
+                        }
+                        refer();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            weigh(32 * q, v[q]);
+                            if (q == 1) hand_over();
                         }
                     }
                     tmem_wait_st();
