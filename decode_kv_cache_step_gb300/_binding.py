@@ -395,8 +395,15 @@ def _call_stream(stream, device):
     return _stream_handle(stream)
 
 
+# Workspaces of calls that bring none, per thread, device and stream: a
+# thread's calls on a stream run one after the other. Calls that may outlive
+# that order take their own from torch's allocator: captured ones (from the
+# graph's pool) and those on a stream named by the caller.
+_held = threading.local()
+
+
 def _workspace(workspace, nbytes, device, stream):
-    """The caller's workspace, or one from torch's allocator on the call's stream."""
+    """The caller's workspace, or one of at least nbytes for this call."""
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
             raise TypeError("workspace: expected a uint8 torch.Tensor")
@@ -404,7 +411,14 @@ def _workspace(workspace, nbytes, device, stream):
             raise ValueError(f"workspace: must be a contiguous tensor on {device}")
         return workspace
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if _raw_stream is None or torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        key = (device.index, _raw_stream(device.index))
+        held = _held.__dict__
+        ws = held.get(key)
+        if ws is None or ws.numel() < nbytes:
+            held[key] = ws = torch.empty(nbytes + nbytes // 4, dtype=torch.uint8, device=device)
+        return ws
     if not isinstance(stream, torch.cuda.Stream):
         stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                   else torch.cuda.default_stream(device))
@@ -647,7 +661,9 @@ def profile_collect(kernel_id: int):
 
 
 def release_workspace():
+    """Free the library's scratch, and this thread's workspaces."""
     lib = load_library()
+    _held.__dict__.clear()
     _check(lib, lib.lf_release_workspace())
 
 

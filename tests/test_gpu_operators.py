@@ -531,3 +531,48 @@ def test_window_many_items_per_cta():
                 ref, tol = _plain.window_rows(q[t:t + 1], k[b:b + 1], v[b:b + 1], [0, 1],
                                               [kv[b] - nq[b] + i + 1], window, 3, 0.125)
                 near(out[t:t + 1], ref, tol, f"sequence {b} row {i}")
+
+
+def test_held_workspaces_do_not_mix():
+    """Calls without a workspace of the caller, from two threads on one stream and on two streams,
+    of growing and shrinking sizes: each gives what it gives alone."""
+    import threading
+
+    cases = [prefix_case(B, [0, B], [p], p, 130, None, 4, 2, 64, seed=B) for B, p in
+             ((3, 900), (9, 100), (2, 2500))]
+    for c in cases:
+        c["ws"].fill_(-1)
+    extra = [(ints([0, c["q"].shape[0]]), ints(c["plen"])) for c in cases]
+
+    def run(i, out):
+        c = cases[i]
+        lf.decode_attention_prefix(c["q"], c["k"], c["v"], c["mask"], c["nk"], c["nv"], c["ws"],
+                                   c["kp"], c["vp"], *extra[i], out, c["scale"])
+
+    want = [torch.empty_like(c["q"]) for c in cases]
+    for i, w in enumerate(want):
+        run(i, w)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(order, stream):
+        with torch.cuda.stream(stream):
+            outs = [(i, torch.empty_like(want[i])) for i in order * 20]
+            for i, out in outs:
+                run(i, out)
+            stream.synchronize()
+            bad.extend(i for i, out in outs if not torch.equal(out, want[i]))
+
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for streams in ((main, main), (main, other)):
+        threads = [threading.Thread(target=work, args=(o, s)) for o, s in
+                   zip(([0, 1, 2], [2, 0, 1]), streams)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    assert not bad
+    lf.release_workspace()
+    out = torch.empty_like(want[0])
+    run(0, out)
+    assert torch.equal(out, want[0])
