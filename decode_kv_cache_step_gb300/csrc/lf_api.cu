@@ -559,7 +559,7 @@ lf_status build_launch(const StepArgs& a, const Shape& s, char* base, uint32_t* 
     sp.pre_ml = a.pre_ml;
     sp.pre_o = a.pre_o;
     sp.pre_pieces = a.pre_pieces;
-    if (!lf::step_fits(s.d, g, pl.stages, a.score, pl.nchunk, sp.topk))
+    if (!lf::step_fits(s.d, g, pl.stages, a.score, pl.nchunk, sp.topk, a.pre_pieces))
         return fail(LF_ERR_UNSUPPORTED,
                     "k = %d with %d chunks of the slot axis does not fit in shared memory",
                     sp.topk, pl.nchunk);
@@ -924,8 +924,10 @@ lf_status run_prefix(StepArgs a, const Shape& s, const void* k_prefix, const voi
     const size_t pre = static_cast<size_t>(x.N) * s.Hkv * x.P * s.d * 2;
     const size_t qb = static_cast<size_t>(s.B) * s.Hq * s.d * 2;
     if (overlaps(a.q, qb, a.out, qb) || overlaps(k_prefix, pre, a.k_cache, own) ||
-        overlaps(v_prefix, pre, a.v_cache, own))
-        return fail(LF_ERR_INVALID_ARG, "out overlaps q, or a prefix the cache");
+        overlaps(v_prefix, pre, a.v_cache, own) || overlaps(k_prefix, pre, a.v_cache, own) ||
+        overlaps(v_prefix, pre, a.k_cache, own) || overlaps(k_prefix, pre, a.out, qb) ||
+        overlaps(v_prefix, pre, a.out, qb))
+        return fail(LF_ERR_INVALID_ARG, "out overlaps q or a prefix, or a prefix a cache");
     PrefixLayout L;
     if ((st = prefix_layout(s, x, a.score, &L)) != LF_OK) return st;
     if (workspace_bytes < L.total)
@@ -1193,8 +1195,10 @@ lf_status lf_window_attention(const void* q, const void* k_cache, const void* v_
     const Shape s{B, Hq, Hkv, d, S, 0, scale};
     if ((st = check_window(T, s, window, sinks)) != LF_OK) return st;
     const size_t rows = static_cast<size_t>(T) * Hq;
-    if (overlaps(q, rows * d * 2, out, rows * d * 2))
-        return fail(LF_ERR_INVALID_ARG, "out overlaps q");
+    const size_t cache = static_cast<size_t>(B) * Hkv * S * d * 2;
+    if (overlaps(q, rows * d * 2, out, rows * d * 2) || overlaps(k_cache, cache, out, rows * d * 2) ||
+        overlaps(v_cache, cache, out, rows * d * 2))
+        return fail(LF_ERR_INVALID_ARG, "out overlaps q or a cache");
     int pieces = 0;
     if ((st = window_pieces(T, s, window, sinks, &pieces)) != LF_OK) return st;
     const size_t need = piece_bytes(pieces, rows, d);

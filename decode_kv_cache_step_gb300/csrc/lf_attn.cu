@@ -253,15 +253,16 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
 // the hardware ends a suspension when it likes.)
 constexpr uint64_t kDrainNs = 1000000000;
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    const uint32_t hint = limit_ns < 10000000 ? static_cast<uint32_t>(limit_ns) : 10000000u;
     uint64_t t0 = 0;
     for (;;) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000000;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(hint)
             : "memory");
         if (ok) return true;
         const uint64_t t = global_timer_ns();
@@ -509,12 +510,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 mbar_arrive(&item_empty[slot]);
             }
-            if (!ok) {
-                give_up();
-                // No copy may be in flight when the CTA leaves.
-                for (int k = max(0, n - L::kStages); k < n; ++k)
-                    wait_phase(&full[k % L::kStages], (k / L::kStages) & 1, kDrainNs);
-            }
+            if (!ok) give_up();
+            // No copy may be in flight when the CTA leaves (there is one here
+            // only after some wait has run out).
+            for (int k = max(0, n - L::kStages); k < n; ++k)
+                wait_phase(&full[k % L::kStages], (k / L::kStages) & 1, kDrainNs);
         } else if (warp == 8 && elect_one()) {
             // -------------------------------------------- matrix products --
             // All of it in one thread: with the whole warp in the loop and
@@ -706,11 +706,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 fence_proxy_async_smem();  // the answer is read before the next one lands
                 __syncwarp();
             }
-            if (!ok && lane == 0) {
-                give_up();
-                // What is under way (Q, an answer) lands before the CTA leaves.
-                for (int k = max(0, done - 2); k < done; ++k)
-                    wait_phase(&q_full[rows ? 0 : k & 1], (rows ? k : k >> 1) & 1, 1000000);
+            if (!ok && lane == 0) give_up();
+            // Neither Q's copies nor, after a wait that ran out, an answer.
+            // (The last use of each buffer.)
+            for (int k = max(0, done - (rows ? 1 : 2)); k < done; ++k)
+                wait_phase(&q_full[rows ? 0 : k & 1], (rows ? k : k >> 1) & 1, kDrainNs);
+            if (!ok) {
                 wait_phase(next, 0, 1000000);
                 wait_phase(next, 1, 1000000);
             }

@@ -223,8 +223,9 @@ cudaError_t launch_score_t(const StepParams& p, int units, cudaStream_t stream, 
 
 }  // namespace
 
-bool step_fits(int D, int G, int stages, bool score, int nchunk, int topk) {
-    const size_t need = finish_smem_bytes(nchunk, G, score ? topk : 1);
+bool step_fits(int D, int G, int stages, bool score, int nchunk, int topk, int pre_pieces) {
+    const size_t need =
+        finish_smem_bytes(nchunk, G, score ? topk : 1) + prefix_smem_bytes(pre_pieces, G);
     size_t have;
     if (stages == kDeepStages)
         have = D == 64 ? StepSmem<64, kDeepStages>::kBarOff : StepSmem<128, kDeepStages>::kBarOff;

@@ -84,7 +84,7 @@ constexpr int kCounterWordsPerUnit = 5;
 size_t step_smem_bytes(int D, int stages);
 
 // Whether finish-stage shared memory (chunk weights, top-k list) fits.
-bool step_fits(int D, int G, int stages, bool score, int nchunk, int topk);
+bool step_fits(int D, int G, int stages, bool score, int nchunk, int topk, int pre_pieces = 0);
 
 // score = false runs the attention-only variant: the slot write (the written
 // slot becomes live; no other age changes) and the attention output, without

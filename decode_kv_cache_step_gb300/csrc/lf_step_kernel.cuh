@@ -982,6 +982,11 @@ __host__ __device__ constexpr size_t finish_smem_bytes(int nchunk, int G, int to
            (topk > 1 ? kTopKAreaBytes : 0);
 }
 
+// ... and what the prefix pieces add to that.
+__host__ __device__ constexpr size_t prefix_smem_bytes(int pieces, int G) {
+    return pieces > 0 ? static_cast<size_t>(pieces + 1) * G * 8 + 8 : 0;
+}
+
 // Score terms of the cluster epilogues' first scan batch, requested before
 // the merge so that their round trip overlaps it.
 constexpr int kScoreBatch = 8;
@@ -1956,7 +1961,7 @@ cudaError_t launch_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepP
     using L = StepSmem<D, kStages>;
     static_assert(!(kCluster && kPrefix), "the cluster merge takes no prefix pieces");
     if (finish_smem_bytes(p_in.nchunk, G, kScore ? p_in.topk : 1) +
-            (kPrefix ? static_cast<size_t>(p_in.pre_pieces + 1) * G * 8 + 8 : 0) >
+            (kPrefix ? prefix_smem_bytes(p_in.pre_pieces, G) : 0) >
         static_cast<size_t>(L::kBarOff))
         return cudaErrorInvalidConfiguration;
     auto kernel = lf_decode_step_kernel<D, G, kStages, kScore, kCluster, kPrefix>;

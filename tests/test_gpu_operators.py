@@ -576,3 +576,40 @@ def test_held_workspaces_do_not_mix():
     out = torch.empty_like(want[0])
     run(0, out)
     assert torch.equal(out, want[0])
+
+
+def test_waits_that_run_out_are_reported(monkeypatch):
+    """With the wait limit cut to 1 ns the packed attention's waits give up before the copies
+    land: the call retires and reports it, and the next one is right."""
+    g = gen(3)
+    q, k, v = normal(g, 300, 4, 64), normal(g, 1, 2, 400, 64), normal(g, 1, 2, 400, 64)
+    out = torch.empty_like(q)
+    for rows in (300, 3):
+        monkeypatch.setenv("LF_WAIT_LIMIT_NS", "1")
+        lf.window_attention(q[:rows], k, v, ints([0, rows]), ints([400]), out[:rows], 90, 2, 0.125)
+        assert lf.device_errors(clear=True) & lf.LF_DEVERR_WAIT_TIMEOUT
+        monkeypatch.delenv("LF_WAIT_LIMIT_NS")
+        lf.window_attention(q[:rows], k, v, ints([0, rows]), ints([400]), out[:rows], 90, 2, 0.125)
+        ref, tol = _plain.window_rows(q[:rows], k, v, [0, rows], [400], 90, 2, 0.125)
+        near(out[:rows], ref, tol)
+        no_errors()
+
+
+def test_first_call_inside_a_capture():
+    """Calls that allocate nothing but from the graph's pool: captured without a warm-up of their
+    own shapes, replayed on new inputs."""
+    g = gen(4)
+    q, k, v = normal(g, 5, 8, 128), normal(g, 5, 2, 900, 128), normal(g, 5, 2, 900, 128)
+    qs, kv = ints([0, 1, 2, 3, 4, 5]), ints([900, 1, 450, 129, 64])
+    out = torch.empty_like(q)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        lf.window_attention(q, k, v, qs, kv, out, 0, 0, 0.1)
+    for _ in range(2):
+        q.copy_(normal(g, 5, 8, 128))
+        out.zero_()
+        gr.replay()
+        torch.cuda.synchronize()
+        ref, tol = _plain.window_rows(q, k, v, [0, 1, 2, 3, 4, 5], [900, 1, 450, 129, 64], 0, 0, 0.1)
+        near(out, ref, tol)
+    no_errors()

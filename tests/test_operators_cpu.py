@@ -80,7 +80,8 @@ def window(lib, **kw):
     ({"kv": None}, BAD), ({"out": None}, BAD), ({"out": FAKE[0]}, BAD), ({"T": 0}, BAD),
     ({"T": (1 << 22) + 1}, NO), ({"w": -1}, BAD), ({"sinks": -1}, BAD), ({"w": (1 << 30) + 1}, BAD),
     ({"scale": float("inf")}, BAD), ({"d": 32}, NO), ({"Hq": 32}, NO), ({"S": MB + 1}, NO),
-    ({"B": 0}, BAD), ({"out": FAKE[0] + 1024}, BAD),
+    ({"B": 0}, BAD), ({"out": FAKE[0] + 1024}, BAD), ({"out": FAKE[1]}, BAD),
+    ({"out": FAKE[2] + 256}, BAD), ({"T": 1 << 22, "Hq": 1024, "Hkv": 1024}, NO),
 ])
 def test_window_refusals(lib, kw, status):
     assert window(lib, **kw) == status
@@ -106,6 +107,7 @@ def prefix(lib, step, **kw):
     ({"vp": None}, BAD), ({"ps": None}, BAD), ({"pl": FAKE[10] + 2}, BAD), ({"work": None}, BAD),
     ({"work": FAKE[13] + 16}, BAD), ({"N": 0}, BAD), ({"P": 0}, BAD), ({"P": MB + 1}, NO),
     ({"N": 40000}, NO), ({"kp": FAKE[1]}, BAD), ({"vp": FAKE[2]}, BAD), ({"out": FAKE[0]}, BAD),
+    ({"kp": FAKE[2]}, BAD), ({"vp": FAKE[1]}, BAD), ({"out": FAKE[7]}, BAD), ({"out": FAKE[8]}, BAD),
     ({"d": 256}, NO), ({"B": 0}, BAD), ({"scale": float("nan")}, BAD),
 ])
 def test_prefix_refusals(lib, step, kw, status):
