@@ -413,7 +413,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int lane = tid & 31;
 
-    allow_dependent_launch();
     if (warp == 8) {
         tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kMiscOff), 512);
     } else if (warp == 9 && lane == 0) {
@@ -445,7 +444,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     // Everything above may run while the previous kernel of the stream ends.
+    // The next one may start once every CTA is past this point (not before:
+    // the decode step with a prefix reads its own inputs without waiting for
+    // this grid, relying on the kernels before it being over).
     grid_dependency_wait();
+    allow_dependent_launch();
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     // Work units of the streams: unit j of an item belongs to stream j & 1 and
     // reads K/V tile j >> 1 (rows mode) or j (keys mode) of the item's part of

@@ -483,8 +483,10 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
     __nv_bfloat16* out = p.out + row0 * D;
     const size_t pre_rows = kPrefix ? static_cast<size_t>(gridDim.y) / p.Hkv * p.Hq : 0;  // B * Hq
 
-    // Prefix pieces: a warp per head, a lane per piece (at most 32).
+    // Prefix pieces: a warp per head, a lane per piece (at most 32). The
+    // attention that writes them is complete after the wait.
     if constexpr (kPrefix) {
+        grid_dependency_wait();
         const int lane = tid & 31;
         for (int h = tid >> 5; h < G; h += kConsumerWarps) {
             float2 v = make_float2(-INFINITY, 0.f);
@@ -1473,9 +1475,17 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
         }
     }
 
-    if (!p.split) allow_dependent_launch();
-    grid_dependency_wait();
-    if (p.split) allow_dependent_launch();
+    // A step with a shared prefix does not wait here: the kernel before it,
+    // the prefix's attention, lets it start only once every kernel before
+    // that is over, and its result is first read in the merge, which waits.
+    // So the slots stream while the prefix's last CTAs run.
+    if constexpr (kPrefix) {
+        allow_dependent_launch();
+    } else {
+        if (!p.split) allow_dependent_launch();
+        grid_dependency_wait();
+        if (p.split) allow_dependent_launch();
+    }
 
     if (warp == kConsumerWarps && lane == 0) {
         const uint64_t pol = l2_policy_evict_first();
