@@ -562,6 +562,11 @@ def decode_prefix_workspace(B, Hq, Hkv, d, S, N, P) -> int:
     return int(n.value)
 
 
+# The size is a function of the sizes, the device and one switch alone.
+_prefix_bytes = functools.lru_cache(maxsize=1024)(
+    lambda index, chunk_tiles, *sizes: decode_prefix_workspace(*sizes))
+
+
 def _check_prefix(k_prefix, v_prefix, prefix_start, prefix_len, Hkv, d):
     if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 4:
         raise ValueError("k_prefix must be [N,Hkv,P,d]")
@@ -595,7 +600,8 @@ def decode_attention_prefix(q, k_cache, v_cache, mask, new_k, new_v, write_slot,
     with _on_device(q.device, k_cache, v_cache, mask, new_k, new_v, write_slot, out, k_prefix,
                     v_prefix, prefix_start, prefix_len):
         ws = _workspace(workspace, 0 if workspace is not None else
-                        decode_prefix_workspace(B, Hq, Hkv, d, S, N, P), q.device, stream)
+                        _prefix_bytes(q.device.index, os.environ.get("LF_CHUNK_TILES"), B, Hq, Hkv,
+                                      d, S, N, P), q.device, stream)
         _check(lib, lib.lf_decode_attention_prefix(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(),
             new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(), k_prefix.data_ptr(),
@@ -619,7 +625,8 @@ def decode_step_prefix(q, k_cache, v_cache, mask, new_k, new_v, write_slot, k_pr
     with _on_device(q.device, k_cache, v_cache, mask, new_k, new_v, write_slot, out, next_slots,
                     scores, k_prefix, v_prefix, prefix_start, prefix_len):
         ws = _workspace(workspace, 0 if workspace is not None else
-                        decode_prefix_workspace(B, Hq, Hkv, d, S, N, P), q.device, stream)
+                        _prefix_bytes(q.device.index, os.environ.get("LF_CHUNK_TILES"), B, Hq, Hkv,
+                                      d, S, N, P), q.device, stream)
         _check(lib, lib.lf_decode_step_prefix(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(),
             new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(), k_prefix.data_ptr(),
