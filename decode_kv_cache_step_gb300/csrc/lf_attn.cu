@@ -15,8 +15,8 @@
 //   rows mode  the streams are two query tiles over the same K/V tiles (each
 //              K/V tile is read from L2 once per 256 rows);
 //   keys mode  (at most 128 rows per sequence on average) the streams are
-//              the even and odd K/V tiles of one query tile, joined later
-//              like any other pieces of the key axis.
+//              the even and odd K/V tiles of one query tile; at its end the
+//              warps of stream 0 read both O and join them.
 // A CTA (one per SM: 224 KB of shared memory, all of TMEM) keeps taking work
 // items until the grid has none left (cluster launch control hands it the
 // index of a CTA that has not started), so one item's loads and products run
@@ -36,16 +36,17 @@
 // a row's maximum only after a tile that exceeds it by more than 2^8 (O and l
 // are rescaled before the next tile's P), which is rare. Until then the
 // weights stay as they are, relative precision and all: bf16 and fp32 hold up
-// to 2^127, and a row that outgrows 2^100 within one tile is computed again. P is handed over in two halves, the first
-// while the second is still in the making.
+// to 2^127, and a row that outgrows 2^100 within one tile is computed again.
+// P is handed over in two halves, the first while the second is still in the
+// making.
 // P is rounded to bf16 (2^-9 of each weight) because the tensor cores take
 // it; l sums the unrounded weights.
 //
 // Keys a row does not see are removed by select before the exponentials, and
 // what a V tile holds behind the range's last key is zeroed in shared memory,
-// so it does not matter what lies there. A NaN or infinity in a row that others of the
-// tile do see would still reach this row's O as 0 * NaN: a row whose result
-// is not finite is computed again by attn_row, key by key.
+// so it does not matter what lies there. A NaN or infinity in a row that
+// others of the tile do see would still reach this row's O as 0 * NaN: a row
+// whose result is not finite is computed again by attn_row, key by key.
 #include <math.h>
 #include <stdlib.h>
 
@@ -95,12 +96,13 @@ struct AttnSmem {
     static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
     // barriers: q_full[2], q_empty[2], full[], empty[], s_full[2], p_half[2],
     // p_full[2], o_done[2], o_free[2], item_full[], item_empty[], v_ask,
-    // v_clean, drain, next, want
-    static constexpr int kBars = 4 + 2 * kStages + 10 + 2 * kItemSlots + 5;
+    // v_clean, drain, next, want, other
+    static constexpr int kBars = 4 + 2 * kStages + 10 + 2 * kItemSlots + 6;
     static constexpr int kItemOff = kBarOff + kBars * 8;
     static constexpr int kNextOff = (kItemOff + kItemSlots * static_cast<int>(sizeof(Item)) + 15) / 16 * 16;
     static constexpr int kMiscOff = kNextOff + 16;  // TMEM base; V tile to clean, its rows to keep
-    static constexpr int kAlloc = kMiscOff + 16 + 1024;
+    static constexpr int kOtherOff = kMiscOff + 16;  // stream 1's (m, l) [128], keys mode
+    static constexpr int kAlloc = kOtherOff + kRows * 8 + 1024;
     static_assert(kAlloc <= 232448, "shared memory of a CTA");
 };
 
@@ -208,15 +210,16 @@ __device__ void attn_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const _
     }
 }
 
-// A stream's row again, over the stream's tiles; the warp writes its result.
+// An item's row again, over all its tiles; the warp writes the result.
 template <int D>
 __device__ __noinline__ void redo_row(const AttnParams& p, const Item& it, size_t row,
-                                      size_t cache, int first, int step, int lo, int hi, int piece) {
+                                      size_t cache, int lo, int hi) {
     const int lane = threadIdx.x & 31;
     float m = -INFINITY, l = 0.f, o[D / 32];
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
-    for (int i = first; i < it.count; i += step) {
+#pragma unroll 1
+    for (int i = 0; i < it.count; ++i) {
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             const Half x = tile_half(it, it.first + i, h);
@@ -230,7 +233,7 @@ __device__ __noinline__ void redo_row(const AttnParams& p, const Item& it, size_
         for (int c = 0; c < D / 32; ++c)
             p.out[row * D + lane * (D / 32) + c] = __float2bfloat16_rn(l == 0.f ? 0.f : o[c] * il);
     } else {
-        const size_t at = static_cast<size_t>(piece) * p.T * p.Hq + row;
+        const size_t at = static_cast<size_t>(it.split) * p.T * p.Hq + row;
         if (lane == 0) p.part_ml[at] = make_float2(m, l);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) p.part_o[at * D + lane * (D / 32) + c] = o[c];
@@ -380,7 +383,7 @@ __device__ __forceinline__ uint32_t below(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-template <int D>
+template <int D, bool kRowsMode>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     lf_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnParams p,
@@ -405,6 +408,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* drain = v_clean + 1;
     uint64_t* next = drain + 1;
     uint64_t* want = next + 1;
+    uint64_t* other = want + 1;
+    float2* const other_ml = reinterpret_cast<float2*>(smem + L::kOtherOff);
     Item* items = reinterpret_cast<Item*>(smem + L::kItemOff);
     volatile uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
 
@@ -438,6 +443,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(drain, 1);
         mbar_init(next, 1);
         mbar_init(want, 1);
+        mbar_init(other, 4);
         fence_barrier_init();
     }
     tc_fence_before();
@@ -453,7 +459,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // Work units of the streams: unit j of an item belongs to stream j & 1 and
     // reads K/V tile j >> 1 (rows mode) or j (keys mode) of the item's part of
     // the list.
-    const bool rows = pl.rows_mode;
+    constexpr bool rows = kRowsMode;
     const int gs = __ffs(p.Hq / p.Hkv) - 1;
 
     // A wait of a whole warp: every lane learns whether all of them saw the
@@ -730,7 +736,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int tt = (rows && s ? kRows >> gs : 0) + (r >> gs);  // token of the item
         const float c = p.scale_log2;
         const uint64_t c2 = pack_f32x2(c, c);
-        int n = 0;  // units of this stream so far
+        int n = 0;       // units of this stream so far
+        int others = 0;  // results of stream 1 joined
         bool ok = true;
         for (int w = 0;; ++w) {
             const int slot = w % kItemSlots;
@@ -885,15 +892,47 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
             }
-            const size_t row = static_cast<size_t>(it.tok0 + tt) * p.Hq + (it.kvh << gs) +
-                               (r & ((1 << gs) - 1));
-            const int piece = rows ? it.split : it.split * 2 + s;
-            const size_t at = static_cast<size_t>(piece) * p.T * p.Hq + row;
-            const bool some = valid && l != 0.f;
+            if (!rows && s) {
+                // Stream 0 joins this stream's result with its own. (The next
+                // one waits for O to be read, and this with it.)
+                if (worked) {
+                    other_ml[r] = make_float2(m, l);
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (worked) mbar_arrive(other);
+                    mbar_arrive(&item_empty[slot]);
+                }
+                continue;
+            }
+            const bool two = !rows && units > 1;
             // 0 unless a value is not finite or grew out of hand.
             float bad = l < 1e30f ? 0.f : NAN;
+            float f0 = 1.f, f1 = 0.f;  // weights of the two O
+            if (two) {
+                ok = warp_wait(other, others++ & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const float2 v = other_ml[r];
+                bad = v.y < 1e30f ? bad : NAN;
+                const float top = fmaxf(l == 0.f ? -INFINITY : m, v.y == 0.f ? -INFINITY : v.x);
+                f0 = l == 0.f ? 0.f : exp2f(m - top);
+                f1 = v.y == 0.f ? 0.f : exp2f(v.x - top);
+                l = l * f0 + v.y * f1;
+                m = top;
+            }
+            const size_t row = static_cast<size_t>(it.tok0 + tt) * p.Hq + (it.kvh << gs) +
+                               (r & ((1 << gs) - 1));
+            const size_t at = static_cast<size_t>(it.split) * p.T * p.Hq + row;
+            const bool some = valid && l != 0.f;
             if (any_valid) {
-                const float il = some ? 1.f / l : 0.f;
+                if (p.pieces == 0) {
+                    const float il = some ? 1.f / l : 0.f;
+                    f0 *= il;
+                    f1 *= il;
+                }
+                const bool use0 = some && f0 != 0.f, use1 = some && f1 != 0.f;
                 // Rows to store, of the lane's group of four.
                 char* const mine = (p.pieces == 0 ? reinterpret_cast<char*>(p.out) + row * D * 2
                                                   : reinterpret_cast<char*>(p.part_o) + at * D * 4);
@@ -912,20 +951,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         tmem_ld32(to + k, o);
                         tmem_wait_ld();
                     }
+                    // (An O without a key has weight 0 and is not looked at.)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if (!some) o[e] = 0u;
-                        bad = fmaf(__uint_as_float(o[e]), 0.f, bad);
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = use0 ? __float_as_uint(__uint_as_float(o[e]) * f0) : 0u;
+                    if (two) {
+                        uint32_t o1[32];
+                        tmem_ld32(to + D + k, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (use1)
+                                o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
                     }
+                    float odd[4] = {bad, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) odd[e & 3] = fmaf(__uint_as_float(o[e]), 0.f, odd[e & 3]);
+                    bad = (odd[0] + odd[1]) + (odd[2] + odd[3]);
                     uint4 v[4];
                     if (p.pieces == 0) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t* w = o + 8 * i;
-                            v[i].x = pack_bf16x2(__uint_as_float(w[0]) * il, __uint_as_float(w[1]) * il);
-                            v[i].y = pack_bf16x2(__uint_as_float(w[2]) * il, __uint_as_float(w[3]) * il);
-                            v[i].z = pack_bf16x2(__uint_as_float(w[4]) * il, __uint_as_float(w[5]) * il);
-                            v[i].w = pack_bf16x2(__uint_as_float(w[6]) * il, __uint_as_float(w[7]) * il);
+                            v[i].x = pack_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+                            v[i].y = pack_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+                            v[i].z = pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5]));
+                            v[i].w = pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7]));
                         }
                         store_rows(v, dst, own, few, k * 2);
                     } else {
@@ -943,7 +994,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (worked && lane == 0) mbar_arrive(&o_free[s]);
+            if (lane == 0) {
+                if (worked) mbar_arrive(&o_free[s]);
+                if (two) mbar_arrive(&o_free[1]);
+            }
             for (unsigned redo = __ballot_sync(0xffffffffu, some && !(bad == 0.f)); redo;
                  redo &= redo - 1) {
                 const int from = __ffs(redo) - 1;
@@ -952,8 +1006,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         << 32 |
                     __shfl_sync(0xffffffffu, static_cast<unsigned>(row), from);
                 redo_row<D>(p, it, rr, (static_cast<size_t>(it.seq) * p.Hkv + it.kvh) * p.S * D,
-                            rows ? 0 : s, rows ? 1 : 2, __shfl_sync(0xffffffffu, row_lo, from),
-                            __shfl_sync(0xffffffffu, row_hi, from), piece);
+                            __shfl_sync(0xffffffffu, row_lo, from),
+                            __shfl_sync(0xffffffffu, row_hi, from));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
@@ -1029,12 +1083,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) lf_attn_merge_kernel(const A
         *reinterpret_cast<uint32_t*>(p.out + row * D + lane * kC + c) = pack_bf16x2(o[c], o[c + 1]);
 }
 
-template <int D>
+template <int D, bool kRowsMode>
 cudaError_t launch_attention_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                const CUtensorMap& tmV, const AttnParams& p, const AttnPlan& pl,
                                cudaStream_t stream) {
     using L = AttnSmem<D>;
-    auto kernel = lf_attn_kernel<D>;
+    auto kernel = lf_attn_kernel<D, kRowsMode>;
     static int configured_for = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1071,8 +1125,7 @@ cudaError_t launch_attention_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
 int attention_pieces(int T, int N, int Hq, int Hkv, int S, bool causal, int window, int sinks,
                      int sms) {
     const AttnPlan pl = attn_plan(T, N, Hq, Hkv, S, causal, window, sinks, sms);
-    if (pl.rows_mode) return causal && pl.nsplit == 1 ? 0 : pl.nsplit;
-    return 2 * pl.nsplit;
+    return causal && pl.nsplit == 1 ? 0 : pl.nsplit;
 }
 
 cudaError_t launch_attention(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK,
@@ -1080,8 +1133,12 @@ cudaError_t launch_attention(int D, const CUtensorMap& tmQ, const CUtensorMap& t
                              cudaStream_t stream) {
     const AttnPlan pl = attn_plan(p.T, p.N, p.Hq, p.Hkv, p.S, p.causal, p.window, p.sinks, sms);
     if (p.pieces > kMaxPieces) return cudaErrorInvalidConfiguration;
-    if (D == 64) return launch_attention_t<64>(tmQ, tmK, tmV, p, pl, stream);
-    if (D == 128) return launch_attention_t<128>(tmQ, tmK, tmV, p, pl, stream);
+    if (D == 64)
+        return pl.rows_mode ? launch_attention_t<64, true>(tmQ, tmK, tmV, p, pl, stream)
+                            : launch_attention_t<64, false>(tmQ, tmK, tmV, p, pl, stream);
+    if (D == 128)
+        return pl.rows_mode ? launch_attention_t<128, true>(tmQ, tmK, tmV, p, pl, stream)
+                            : launch_attention_t<128, false>(tmQ, tmK, tmV, p, pl, stream);
     return cudaErrorInvalidValue;
 }
 
