@@ -1,6 +1,14 @@
 // Instantiations of the decode-step kernel whose merge joins a shared-prefix
 // attention: the unit's slots and the prefix share one softmax, so the output
 // and LongFlowScore's weights are normalised over both.
+//
+// The pieces of the prefix's attention enter the merge of the unit's last CTA
+// like chunks of its own. Only that merge waits for the attention kernel, so
+// the slots stream while the prefix's last CTAs run (us per call, with the
+// wait at the step's start -> in the merge: nine prefixes of up to 5003
+// tokens over 67 ragged sequences 63 -> 50, a 16384-token prefix over 128
+// full caches of 2400 slots 219 -> 213, of which the slots alone take 186 at
+// the measured copy rate).
 #include "lf_step_kernel.cuh"
 
 namespace lf {

@@ -16,6 +16,11 @@
 // loads are in flight: positions of a million times frequencies near 1 need
 // some 44 bits, which two floats hold (fp64 would take 1000 cycles of an SM's
 // fp64 unit per CTA).
+//
+// Measured (32 query, 8 KV heads of 128): 20.3K prompt tokens into their
+// caches 93 us, 5.4 TB/s read and written, 80% of the measured copy rate (the
+// instruction issue is 62% busy); one token 3.0 us, 128 tokens 3.4 us, which
+// is the latency of a launch and three dependent round trips.
 #include <stdlib.h>
 
 #include <algorithm>
@@ -263,6 +268,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const
 template <int D>
 cudaError_t launch_rope_t(const RopeParams& p, int sms, cudaStream_t stream) {
     // Four tokens per CTA, fewer when the call is too small to fill the GPU.
+    // Measured, us by tokens per CTA 1 / 2 / 4: 128 tokens 3.6 / 4.2 / 6.2,
+    // 600 tokens 4.8 / 5.6 / 6.8, 2000 tokens 13.6 / 11.8 / 11.1, 20000
+    // tokens 120 / 100 / 90.
     int per = kMaxTokens;
     while (per > 1 && (p.T + per - 1) / per < 4 * sms) per >>= 1;
     const int tok_ctas = (p.T + per - 1) / per;
