@@ -613,3 +613,98 @@ def test_first_call_inside_a_capture():
         ref, tol = _plain.window_rows(q, k, v, [0, 1, 2, 3, 4, 5], [900, 1, 450, 129, 64], 0, 0, 0.1)
         near(out, ref, tol)
     no_errors()
+
+
+def test_offsets_past_32_bits():
+    """Caches, and packed rows, of more than 2^31 values: their last parts are right."""
+    g = gen(12)
+    B, Hkv, S, d = 33, 8, 65536, 128
+    k, v = (torch.zeros(B, Hkv, S, d, dtype=BF, device="cuda") for _ in range(2))
+    assert k.numel() > 1 << 31
+    mask = torch.full((B, Hkv, S), -1, dtype=torch.int32, device="cuda")
+    qkv, w = normal(g, 100, 8 + 16, d), normal(g, d)
+    freq = (1e4 ** (-torch.arange(64).double() / 64)).float().cuda()
+    q = torch.empty(100, 8, d, dtype=BF, device="cuda")
+    starts, lens = [0] * B + [100], [0] * (B - 1) + [S]
+    k[-1, :, S - 300:], v[-1, :, S - 300:] = normal(g, Hkv, 300, d), normal(g, Hkv, 300, d)
+    lf.prefill_append(qkv, w, w, freq, ints(starts), ints(lens), q, k, v, mask)
+    want = _plain.rope(qkv[:, 8:16], w, freq, torch.arange(S - 100, S), 1e-6, False)
+    near(k[-1, :, S - 100:].transpose(0, 1), want, _plain.rope_bound(want))
+    assert torch.equal(v[-1, :, S - 100:].transpose(0, 1), qkv[:, 16:])
+    assert (mask[:-1] == -1).all() and mask[-1, -1, -1] == 0 and mask[-1, -1, 0] == S - 1
+    out = torch.empty_like(q)
+    lf.window_attention(q, k, v, ints(starts), ints(lens), out, 150, 0, 0.09)
+    at = slice(S - 300, S)
+    ref, tol = _plain.window_rows(q, k[-1:, :, at], v[-1:, :, at], [0, 100], [300], 150, 0, 0.09)
+    near(out, ref, tol)
+    # the same caches as prefixes of one sequence each, the last one read
+    own = prefix_case(B, [0, B], [1], 1, 40, None, 8, 8, d)
+    o2 = torch.empty(B, 8, d, dtype=BF, device="cuda")
+    lf.decode_attention_prefix(own["q"], own["k"], own["v"], own["mask"], own["nk"], own["nv"],
+                               own["ws"], k, v, ints(list(range(B + 1))), ints(lens), o2, 0.09)
+    i = B - 1
+    ref = _plain.prefix_step(*(own[x][i:] for x in ("q", "k", "v", "mask", "nk", "nv", "ws")),
+                             k[i:], v[i:], [0, 1], [S], 0, 0.09, ageing=False)
+    near(o2[i:], ref["out"], ref["tol"])
+    del k, v, mask
+    T, Hq = 540000, 32
+    k, v = normal(g, 1, 1, 1, d).expand(1, 4, T, d).contiguous(), torch.zeros(1, 4, T, d, dtype=BF, device="cuda")
+    k[0, :, -400:], v[0, :, -400:] = normal(g, 4, 400, d), normal(g, 4, 400, d)
+    q = torch.zeros(T, Hq, d, dtype=BF, device="cuda")
+    assert q.numel() > 1 << 31
+    q[-400:] = normal(g, 400, Hq, d)
+    out = torch.empty_like(q)
+    lf.window_attention(q, k, v, ints([0, T]), ints([T]), out, 90, 0, 0.09)
+    ref, tol = _plain.window_rows(q[-60:], k[:, :, -400:], v[:, :, -400:], [0, 60], [400], 90, 0, 0.09)
+    near(out[-60:], ref, tol)
+    assert (out[:1000] == 0).all()
+    no_errors()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_window_random_sweep(seed):
+    """Random batches: lengths from none, windows, first keys, heads, garbage behind the lengths."""
+    g = gen(1000 + seed)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    B, Hkv, gg, d = r(1, 9), r(1, 3), 1 << r(0, 3), 64 << r(0, 1)
+    S = r(1, 700)
+    kv = [r(0, S) for _ in range(B)]
+    nq = [min(c, (0, 1, r(0, 40), r(0, S))[r(0, 3)]) for c in kv]
+    if sum(nq) == 0:
+        kv[0], nq[0] = S, 1
+    window, sinks = (0, 1, r(1, 60), r(1, S), r(60, 260))[r(0, 4)], (0, r(0, 8), r(0, 200))[r(0, 2)]
+    starts = [sum(nq[:i]) for i in range(B + 1)]
+    lead, T = r(0, 3), starts[-1]
+    starts = [s + lead for s in starts]
+    T += lead + r(0, 5)
+    q, k, v = normal(g, T, Hkv * gg, d), normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    k *= torch.exp(0.7 * torch.randn(B, Hkv, S, 1, generator=g)).cuda().to(BF)
+    for b in range(B):
+        k[b, :, kv[b]:], v[b, :, kv[b]:] = math.inf, NAN
+    out = torch.full_like(q, 7.0)
+    lf.window_attention(q, k, v, ints(starts), ints(kv), out, window, sinks, d ** -0.5)
+    ref, tol = _plain.window_rows(q, k, v, starts, kv, window, sinks, d ** -0.5)
+    inside = slice(starts[0], starts[-1])
+    near(out[inside], ref[inside], tol[inside], f"window {window} sinks {sinks} nq {nq} kv {kv}")
+    assert (out[:starts[0]] == 7).all() and (out[starts[-1]:] == 7).all()
+    no_errors()
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_prefix_random_sweep(seed):
+    g = gen(2000 + seed)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    B, Hkv, gg, d = r(1, 40), r(1, 3), 1 << r(0, 3), 64 << r(0, 1)
+    N = r(1, 5)
+    starts = sorted(r(0, B) for _ in range(N + 1))
+    P = r(1, 900)
+    plen = [r(0, P) for _ in range(N)]
+    c = prefix_case(B, starts, plen, P, r(1, 300), None, Hkv * gg, Hkv, d, seed=seed)
+    out = torch.empty_like(c["q"])
+    ref = _plain.prefix_step(c["q"], c["k"], c["v"], c["mask"], c["nk"], c["nv"], c["ws"], c["kp"],
+                             c["vp"], starts, plen, 0, c["scale"], ageing=False)
+    lf.decode_attention_prefix(c["q"], c["k"], c["v"], c["mask"], c["nk"], c["nv"], c["ws"], c["kp"],
+                               c["vp"], ints(starts), ints(plen), out, c["scale"])
+    near(out, ref["out"], ref["tol"], f"starts {starts} lengths {plen}")
+    assert torch.equal(c["mask"].cpu(), ref["mask"])
+    no_errors()
