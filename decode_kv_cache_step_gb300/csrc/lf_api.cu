@@ -831,7 +831,10 @@ lf_status run_attention(lf::AttnParams p, int d, float scale, int dev, cudaStrea
     p.scale_log2 = std::max(
         static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634), 1e-30f);
     p.negate = scale < 0.f;
+    // A warp that computes rows again key by key keeps the others waiting, some
+    // 2 us for 32 keys of each of its 32 rows.
     p.wait_limit_ns = wait_limit_ns();
+    if (!std::getenv("LF_WAIT_LIMIT_NS")) p.wait_limit_ns += static_cast<uint64_t>(p.S) * 8000;
     ProfScope prof(LF_KERNEL_PACKED_ATTENTION, stream);
     cudaError_t e = lf::launch_attention(d, tmQ, tmK, tmV, p, sm_count(dev), stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");

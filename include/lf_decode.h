@@ -382,7 +382,10 @@ lf_status lf_prefill_append(const void* qkv, int64_t qkv_stride, const void* q_w
  * window, sinks  the token at position i sees key j iff j <= i and
  *                (window == 0 or i - j < window or j < sinks)
  * Slots from kv_len[b] on, and keys a row does not see, may hold anything
- * (NaN and infinities included) without changing the row.
+ * (NaN and infinities included) without changing the row. (A value that is
+ * not finite in a key that some rows of a tile see costs all of them a slower
+ * second pass.) A row without a visible key, or with every logit -infinity,
+ * is zero.
  */
 lf_status lf_window_attention(const void* q, const void* k_cache, const void* v_cache,
                               const int32_t* q_start, const int32_t* kv_len, void* out, int T,

@@ -708,3 +708,36 @@ def test_prefix_random_sweep(seed):
     near(out, ref["out"], ref["tol"], f"starts {starts} lengths {plen}")
     assert torch.equal(c["mask"].cpu(), ref["mask"])
     no_errors()
+
+
+def test_nonfinite_key_seen_by_a_long_prompt():
+    """A NaN in the first key reaches every row of a causal prompt, and only it: the slower second
+    pass of all rows stays within the waits' limit."""
+    g = gen(21)
+    q, k, v = normal(g, 6000, 8, 64), normal(g, 1, 2, 6000, 64), normal(g, 1, 2, 6000, 64)
+    k[0, 1, 0, 0] = NAN
+    out = torch.empty_like(q)
+    lf.window_attention(q, k, v, ints([0, 6000]), ints([6000]), out, 0, 0, 0.125)
+    no_errors()
+    assert torch.isnan(out[:, 4:]).all()
+    for i in (0, 777, 5999):
+        ref, tol = _plain.window_rows(q[i:i + 1, :4], k[:, :1], v[:, :1], [0, 1], [i + 1], 0, 0, 0.125)
+        near(out[i:i + 1, :4], ref, tol)
+
+
+def test_without_programmatic_launch(monkeypatch):
+    """LF_PDL=0: the same bits."""
+    c = prefix_case(5, [0, 2, 5], [700, 33], 700, 200, None, 8, 2, 64)
+    got = []
+    for mode in ("1", "0"):
+        monkeypatch.setenv("LF_PDL", mode)
+        kc, vc, mask = c["k"].clone(), c["v"].clone(), c["mask"].clone()
+        out, w = torch.empty_like(c["q"]), torch.empty_like(c["q"])
+        nxt = torch.empty(5, 2, dtype=torch.int32, device="cuda")
+        lf.decode_step_prefix(c["q"], kc, vc, mask, c["nk"], c["nv"], c["ws"], c["kp"], c["vp"],
+                              ints([0, 2, 5]), ints([700, 33]), out, nxt, 5, c["scale"])
+        lf.window_attention(c["q"], c["kp"], c["vp"], ints([0, 2, 5]), ints([700, 33]), w, 0, 0, 0.1)
+        got.append((out, nxt, mask, w))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    no_errors()
