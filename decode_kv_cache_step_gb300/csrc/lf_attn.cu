@@ -439,7 +439,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int lane = tid & 31;
 
-    if (warp == 8) {
+    // Everything before this wait may run while the previous kernel of the
+    // stream ends. (Warp 10 waits first: it reads the lengths.)
+    Item it0;
+    bool found0 = false;
+    if (warp == 10) {
+        grid_dependency_wait();
+        found0 = find_item(p, pl, make_int2(blockIdx.x, blockIdx.y), &it0);
+    } else if (warp == 8) {
         tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kMiscOff), 512);
     } else if (warp == 9 && lane == 0) {
         for (int s = 0; s < L::kStages; ++s) {
@@ -470,8 +477,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // Everything above may run while the previous kernel of the stream ends.
-    // The next one may start once every CTA is past this point (not before:
+    // The next kernel may start once every CTA is past its wait (not before:
     // the decode step with a prefix reads its own inputs without waiting for
     // this grid, relying on the kernels before it being over).
     grid_dependency_wait();
@@ -684,18 +690,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int w = 0;     // items handed out
             int done = 0;  // items with work
             bool ok = true;
-            int2 work = make_int2(blockIdx.x, blockIdx.y);
+            Item it = it0;
+            it.stop = found0 ? 0 : -1;  // -1: no rows there, ask again
             for (int round = 0;; ++round) {
-                Item it;
-                if (work.x >= 0) {
-                    if (find_item(p, pl, work, &it)) {
-                        it.stop = 0;
-                    } else {
-                        it.stop = -1;  // no rows here: ask again
-                    }
-                } else {
-                    it.stop = 1;
-                }
                 if (it.stop >= 0) {
                     const int slot = w % kItemSlots;
                     ok = warp_wait(&item_empty[slot], ((w / kItemSlots) & 1) ^ 1);
@@ -732,9 +729,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 ok = warp_wait(next, round & 1);
                 if (!ok) break;
-                work = cancelled_cta(smem + L::kNextOff);
+                const int2 work = cancelled_cta(smem + L::kNextOff);
                 fence_proxy_async_smem();  // the answer is read before the next one lands
                 __syncwarp();
+                if (work.x < 0)
+                    it.stop = 1;
+                else
+                    it.stop = find_item(p, pl, work, &it) ? 0 : -1;
             }
             if (!ok && lane == 0) give_up();
             // Neither Q's copies nor, after a wait that ran out, an answer.
