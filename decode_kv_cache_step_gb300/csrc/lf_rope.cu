@@ -11,16 +11,16 @@
 // each lane two chunks of 4 values (8 bytes) that rotate among themselves: the
 // halves' chunks at the same offset, or the neighbours of an interleaved
 // pair, so only the norm's sum crosses lanes. A CTA takes all heads of one to
-// four tokens, and a lane keeps its 4 angles and its weights for all of them.
-// The angles are formed once per CTA in shared memory while the first heads'
-// loads are in flight: positions of a million times frequencies near 1 need
-// some 44 bits, which two floats hold (fp64 would take 1000 cycles of an SM's
-// fp64 unit per CTA).
+// four tokens (one warp a token where there are many), and a lane keeps its 4
+// angles and its weights for all of them. The angles are formed once per CTA in
+// shared memory while the first heads' loads are in flight: positions of a
+// million times frequencies near 1 need some 44 bits, which two floats hold
+// (fp64 would take 1000 cycles of an SM's fp64 unit per CTA).
 //
 // Measured (32 query, 8 KV heads of 128): 20.3K prompt tokens into their
-// caches 93 us, 5.4 TB/s read and written, 80% of the measured copy rate (the
-// instruction issue is 62% busy); one token 3.0 us, 128 tokens 3.4 us, which
-// is the latency of a launch and three dependent round trips.
+// caches 83 us, 6.0 TB/s read and written, 89% of the measured copy rate (the
+// same accesses without the arithmetic take 79.6); one token 3.0 us, 128 tokens
+// 3.4 us, which is the latency of a launch and three dependent round trips.
 #include <stdlib.h>
 
 #include <algorithm>
@@ -31,10 +31,14 @@
 namespace lf {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopePerSm = 4;
-constexpr int kBatch = 4;      // heads whose loads a lane has in flight
-constexpr int kMaxTokens = 4;  // tokens of a CTA
+constexpr int kRopeThreads = 256;  // of a CTA when the call is small
+constexpr int kRopeWarps = 32;     // resident per SM, at 64 registers a thread
+constexpr int kBatch = 4;          // heads whose loads a lane has in flight
+constexpr int kMaxAgeParts = 16;   // CTAs that write one head's ages
+constexpr int kAgesPerPart = 2048;
+
+// Tokens a CTA may take.
+__host__ __device__ constexpr int max_tokens(int threads) { return threads >= 128 ? 4 : 1; }
 
 struct TokenAt {
     int b, slot, pos;  // b < 0: no output for this token
@@ -86,11 +90,12 @@ __device__ __forceinline__ float turns(float n, float f) {
     return (t - rintf(t)) + t_lo;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const RopeParams p, int tok_per_cta,
-                                                               int tok_ctas) {
-    constexpr int kLanes = D / 8;                   // lanes of one head
-    constexpr int kGroups = kRopeThreads / kLanes;  // heads a CTA holds at a time
+template <int D, bool kInterleaved, int kThreads>
+__global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
+    lf_rope_kernel(const RopeParams p, int tok_per_cta, int tok_ctas, int age_parts) {
+    constexpr int kLanes = D / 8;                    // lanes of one head
+    constexpr int kGroups = kThreads / kLanes;       // heads a CTA holds at a time
+    constexpr int kMaxTokens = max_tokens(kThreads);
     __shared__ TokenAt at[kMaxTokens];
     __shared__ float2 cs[kMaxTokens][D / 2];
     const int tid = threadIdx.x;
@@ -98,8 +103,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const
     grid_dependency_wait();
     const bool append = p.q_start != nullptr;
     if (static_cast<int>(blockIdx.x) >= tok_ctas) {
-        // Ages of the prompt's tokens, one CTA per (sequence, KV head).
-        const int u = blockIdx.x - tok_ctas;
+        // Ages of the prompt's tokens, age_parts CTAs per (sequence, KV head).
+        const int u = (blockIdx.x - tok_ctas) / age_parts;
+        const int part = (blockIdx.x - tok_ctas) % age_parts;
         const int b = u / p.Hkv;
         SeqRange r;
         if (!seq_range(p.q_start, p.kv_len, b, p.T, p.S, true, &r)) {
@@ -107,7 +113,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const
             return;
         }
         int32_t* m = p.mask + static_cast<size_t>(u) * p.S;
-        for (int j = tid; j < r.kv; j += kRopeThreads) m[j] = r.kv - 1 - j;
+        const int first = part * kThreads + tid;
+        const int step = age_parts * kThreads;
+        const int fours = reinterpret_cast<uintptr_t>(m) % 16 ? 0 : r.kv / 4;
+        for (int i = first; i < fours; i += step) {
+            const int a = r.kv - 1 - 4 * i;
+            reinterpret_cast<int4*>(m)[i] = make_int4(a, a - 1, a - 2, a - 3);
+        }
+        for (int j = 4 * fours + first; j < r.kv; j += step) m[j] = r.kv - 1 - j;
         return;
     }
     const int heads = p.Hq + 2 * p.Hkv;
@@ -125,7 +138,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const
     const int lane = tid % kLanes;
     const bool turned = 8 * lane < p.rot;
     int ea, eb;
-    if (p.interleaved || !turned) {
+    if (kInterleaved || !turned) {
         ea = 8 * lane;
         eb = ea + 4;
     } else {
@@ -175,7 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const
         if ((tid & 31) == 0) at[i] = a;
     }
     __syncthreads();
-    for (int i = tid; i < ntok * half; i += kRopeThreads) {
+    for (int i = tid; i < ntok * half; i += kThreads) {
         const int kk = i / half;
         // In two parts that are exact in fp32, so any int32 position is.
         const int n = at[kk].pos;
@@ -196,9 +209,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float2 one = make_float2(1.f, 0.f);
-        const float2 u = turned ? cs[k][4 * lane + (p.interleaved ? i : 2 * i)] : one;
-        const float2 v = turned ? cs[k][4 * lane + (p.interleaved ? i + 2 : 2 * i + 1)] : one;
-        if (p.interleaved) {
+        const float2 u = turned ? cs[k][4 * lane + (kInterleaved ? i : 2 * i)] : one;
+        const float2 v = turned ? cs[k][4 * lane + (kInterleaved ? i + 2 : 2 * i + 1)] : one;
+        if (kInterleaved) {
             ca[i] = pack_f32x2(u.x, u.x);
             sa[i] = pack_f32x2(-u.y, u.y);
             cb[i] = pack_f32x2(v.x, v.x);
@@ -248,8 +261,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint64_t u = p.interleaved ? swap2(x[e]) : y[e];
-                    const uint64_t v = p.interleaved ? swap2(y[e]) : x[e];
+                    const uint64_t u = kInterleaved ? swap2(x[e]) : y[e];
+                    const uint64_t v = kInterleaved ? swap2(y[e]) : x[e];
                     const uint64_t nx = fma_f32x2(u, sa[e], mul_f32x2(x[e], ca[e]));
                     y[e] = fma_f32x2(v, sb[e], mul_f32x2(y[e], cb[e]));
                     x[e] = nx;
@@ -265,35 +278,49 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm) lf_rope_kernel(const
     }
 }
 
-template <int D>
-cudaError_t launch_rope_t(const RopeParams& p, int sms, cudaStream_t stream) {
-    // Four tokens per CTA, fewer when the call is too small to fill the GPU.
-    // Measured, us by tokens per CTA 1 / 2 / 4: 128 tokens 3.6 / 4.2 / 6.2,
-    // 600 tokens 4.8 / 5.6 / 6.8, 2000 tokens 13.6 / 11.8 / 11.1, 20000
-    // tokens 120 / 100 / 90.
-    int per = kMaxTokens;
-    while (per > 1 && (p.T + per - 1) / per < 4 * sms) per >>= 1;
+template <int D, int kThreads>
+cudaError_t launch_rope_t(const RopeParams& p, int per, cudaStream_t stream) {
     const int tok_ctas = (p.T + per - 1) / per;
-    const int age_ctas = p.q_start ? p.B * p.Hkv : 0;
+    const int parts = std::max(1, std::min(kMaxAgeParts, p.S / kAgesPerPart));
+    const int age_ctas = p.q_start ? p.B * p.Hkv * parts : 0;
     const char* env = std::getenv("LF_PDL");
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tok_ctas + age_ctas);
-    cfg.blockDim = dim3(kRopeThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = (env && std::atoi(env) == 0) ? 0 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, lf_rope_kernel<D>, p, per, tok_ctas);
+    const cudaError_t e =
+        p.interleaved
+            ? cudaLaunchKernelEx(&cfg, lf_rope_kernel<D, true, kThreads>, p, per, tok_ctas, parts)
+            : cudaLaunchKernelEx(&cfg, lf_rope_kernel<D, false, kThreads>, p, per, tok_ctas, parts);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_rope_d(const RopeParams& p, int sms, cudaStream_t stream) {
+    // Many tokens: a warp takes one, and warps do not wait for one another.
+    // Fewer: 256 threads take one, two or four, so that a token's heads are in
+    // flight together. Measured, us for 256 threads (best of 1, 2, 4 tokens) /
+    // one warp: 32 + 16 heads of 128, 2000 tokens 12.9 / 17.2, 5000 tokens
+    // 27.9 / 28.8, 8000 tokens 39.7 / 37.1, 20000 tokens 89.5 / 84.1; 8 + 16
+    // heads of 64, 2000 tokens 5.5 / 6.8, 5000 tokens 10.8 / 10.1, 20000 tokens
+    // 32.0 / 26.3. And by tokens per CTA 1 / 2 / 4 (the first heads): 128 tokens
+    // 3.8 / 5.6 / 7.1, 600 tokens 5.8 / 7.5 / 10.4, 2000 tokens 15.5 / 13.8 / 12.9.
+    if (p.T >= 40 * sms) return launch_rope_t<D, 32>(p, 1, stream);
+    int per = max_tokens(kRopeThreads);
+    while (per > 1 && (p.T + per - 1) / per < 4 * sms) per >>= 1;
+    return launch_rope_t<D, kRopeThreads>(p, per, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(int D, const RopeParams& p, int sms, cudaStream_t stream) {
-    if (D == 64) return launch_rope_t<64>(p, sms, stream);
-    if (D == 128) return launch_rope_t<128>(p, sms, stream);
+    if (D == 64) return launch_rope_d<64>(p, sms, stream);
+    if (D == 128) return launch_rope_d<128>(p, sms, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -124,6 +124,36 @@ def test_append(nq, kv, S, extra, Hq, Hkv, d, offset):
     no_errors()
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,d,rot,inter,norm", [
+    (7001, 2, 1, 64, 48, True, True), (6500, 4, 2, 128, 128, False, True), (8000, 1, 1, 64, 64, False, False),
+    (6200, 6, 3, 128, 32, True, True)])
+def test_norm_rope_many_tokens(T, Hq, Hkv, d, rot, inter, norm):
+    """As many tokens as take a warp each."""
+    test_norm_rope(T, Hq, Hkv, d, rot, inter, norm)
+
+
+@pytest.mark.parametrize("nq,kv,S,extra", [
+    ([3000, 0, 1, 3500], [3100, 0, 1, 3501], 3601, 5),  # rows of ages off 16 bytes
+    ([5000, 1500], [5000, 4999], 5000, 0), ([1] * 100 + [6001], [7] * 100 + [6003], 6004, 1)])
+@pytest.mark.parametrize("Hq,Hkv,d,offset", [(2, 1, 64, 3), (4, 2, 128, None)])
+def test_append_many_tokens(nq, kv, S, extra, Hq, Hkv, d, offset):
+    test_append(nq, kv, S, extra, Hq, Hkv, d, offset)
+
+
+def test_bad_lengths_are_skipped_among_many_tokens():
+    g = gen(3)
+    qkv, f = normal(g, 7000, 3, 64), torch.ones(32, device="cuda")
+    q = torch.zeros(7000, 1, 64, dtype=BF, device="cuda")
+    k, v = (torch.zeros(3, 1, 4100, 64, dtype=BF, device="cuda") for _ in range(2))
+    mask = torch.full((3, 1, 4100), -1, dtype=torch.int32, device="cuda")
+    lf.prefill_append(qkv, None, None, f, ints([0, 3000, 3500, 7000]), ints([3000, 4101, 3500]),
+                      q, k, v, mask)
+    assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_LENGTH
+    assert (q[3000:3500] == 0).all() and (k[1] == 0).all() and (v[1] == 0).all()
+    assert (mask[1] == -1).all() and (mask[0, 0, :3000] >= 0).all()
+    assert torch.equal(v[2, 0, :3500], qkv[3500:, 2]) and (v[2, 0, 3500:] == 0).all()
+
+
 def test_bad_lengths_are_skipped():
     """A sequence whose lengths do not fit is skipped and reported; its neighbours are not."""
     g = gen(1)
