@@ -465,6 +465,10 @@ struct StepArgs {
     const float2* pre_ml = nullptr;
     const float* pre_o = nullptr;
     int pre_pieces = 0;
+    const int32_t* prefix_start = nullptr;
+    const int32_t* prefix_len = nullptr;
+    int prefixes = 0;
+    int prefix_cap = 0;
 };
 
 lf_status check_args(const StepArgs& a, const Shape& s) {
@@ -559,6 +563,10 @@ lf_status build_launch(const StepArgs& a, const Shape& s, char* base, uint32_t* 
     sp.pre_ml = a.pre_ml;
     sp.pre_o = a.pre_o;
     sp.pre_pieces = a.pre_pieces;
+    sp.prefix_start = a.prefix_start;
+    sp.prefix_len = a.prefix_len;
+    sp.prefixes = a.prefixes;
+    sp.prefix_cap = a.prefix_cap;
     if (!lf::step_fits(s.d, g, pl.stages, a.score, pl.nchunk, sp.topk, a.pre_pieces))
         return fail(LF_ERR_UNSUPPORTED,
                     "k = %d with %d chunks of the slot axis does not fit in shared memory",
@@ -880,14 +888,13 @@ lf_status check_prefix_shape(const Shape& s, const PrefixShape& x) {
     return LF_OK;
 }
 
-// Workspace of a step with shared prefixes: the counters and the pieces'
-// (m, l), both zeroed by every call, then the step's scratch and the pieces'
-// outputs.
+// Workspace of a step with shared prefixes: the counters (set to 0 by every
+// call), the pieces' (m, l), the step's scratch and the pieces' outputs.
 struct PrefixLayout {
     Plan pl;
     Layout step;
     int pieces;
-    size_t ml, zeroed, scratch, o, total;
+    size_t counters, ml, scratch, o, total;
 };
 
 lf_status prefix_layout(const Shape& s, const PrefixShape& x, bool score, PrefixLayout* out) {
@@ -904,9 +911,9 @@ lf_status prefix_layout(const Shape& s, const PrefixShape& x, bool score, Prefix
     L.step = scratch_layout(s, L.pl, 0);
     L.pieces = lf::attention_pieces(s.B, x.N, s.Hq, s.Hkv, x.P, false, 0, 0, sms);
     const size_t rows = static_cast<size_t>(s.B) * s.Hq;
-    L.ml = align_up(lf::kCounterWordsPerUnit * static_cast<size_t>(units) * sizeof(uint32_t), 256);
-    L.zeroed = L.ml + L.pieces * rows * sizeof(float2);
-    L.scratch = align_up(L.zeroed, 256);
+    L.counters = lf::kCounterWordsPerUnit * static_cast<size_t>(units) * sizeof(uint32_t);
+    L.ml = align_up(L.counters, 256);
+    L.scratch = align_up(L.ml + L.pieces * rows * sizeof(float2), 256);
     L.o = align_up(L.scratch + L.step.total, 256);
     L.total = L.o + L.pieces * rows * s.d * sizeof(float);
     return LF_OK;
@@ -961,13 +968,28 @@ lf_status run_prefix(StepArgs a, const Shape& s, const void* k_prefix, const voi
     a.pre_ml = ap.part_ml;
     a.pre_o = ap.part_o;
     a.pre_pieces = L.pieces;
+    a.prefix_start = prefix_start;
+    a.prefix_len = prefix_len;
+    a.prefixes = x.N;
+    a.prefix_cap = x.P;
     Launch r;
     if ((st = build_launch(a, s, ws + L.scratch, reinterpret_cast<uint32_t*>(ws), err, L.step, L.pl,
                            &r)) != LF_OK)
         return st;
     g_last_error[0] = '\0';
-    if ((e = cudaMemsetAsync(ws, 0, L.zeroed, stream)) != cudaSuccess)
-        return cuda_fail(e, "cudaMemsetAsync(workspace)");
+    // The chunks' arrival counters are set to 0 by each CTA of the prefix's
+    // attention before it lets the step start. A split finish has four more
+    // words per unit, and long caches: a memset beforehand. (Measured against
+    // a memset in every call, us per call: one sequence of 2400 slots and a
+    // prefix of 1000 tokens 12.8 against 16.5, four short sequences 10.1
+    // against 14.5, 64 sequences 96.2 against 97.4.)
+    if (r.sp.split) {
+        if ((e = cudaMemsetAsync(ws, 0, L.counters, stream)) != cudaSuccess)
+            return cuda_fail(e, "cudaMemsetAsync(workspace)");
+    } else if (r.sp.nchunk > 1) {
+        ap.zero = reinterpret_cast<uint4*>(ws);  // (the counters are five words per unit)
+        ap.zero_quads = (s.B * s.Hkv + 3) / 4;
+    }
     if ((st = run_attention(ap, s.d, s.scale, dev, stream)) != LF_OK) return st;
     return launch(r, stream);
 }

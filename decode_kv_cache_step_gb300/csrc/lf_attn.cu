@@ -479,8 +479,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc_fence_after();
     // The next kernel may start once every CTA is past its wait (not before:
     // the decode step with a prefix reads its own inputs without waiting for
-    // this grid, relying on the kernels before it being over).
+    // this grid, relying on the kernels before it being over, and counts in
+    // words that every CTA sets to 0 before that).
     grid_dependency_wait();
+    if (warp == 11 && p.zero != nullptr) {
+        for (int i = lane; i < p.zero_quads; i += 32) p.zero[i] = make_uint4(0u, 0u, 0u, 0u);
+        __threadfence();
+    }
     allow_dependent_launch();
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     // Work units of the streams: unit j of an item belongs to stream j & 1 and

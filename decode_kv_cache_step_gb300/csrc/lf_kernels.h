@@ -65,6 +65,12 @@ struct StepParams {
     const float2* pre_ml = nullptr;  // [pre_pieces][B * Hq]
     const float* pre_o = nullptr;    // [pre_pieces][B * Hq][D]
     int pre_pieces = 0;
+    // Which pieces hold something: prefix n, if its range and length fit, is
+    // that of sequences prefix_start[n] .. prefix_start[n + 1].
+    const int32_t* prefix_start = nullptr;  // [prefixes + 1]
+    const int32_t* prefix_len = nullptr;    // [prefixes]
+    int prefixes = 0;
+    int prefix_cap = 0;                     // tokens a prefix may have
 };
 
 constexpr int kFlagFillEmptyFirst = 1;  // empty (masked) slots are returned before any score
@@ -173,6 +179,9 @@ struct AttnParams {
     float scale_log2;            // |scale| * log2(e)
     bool negate;                 // scale < 0: the kernel negates q
     uint64_t wait_limit_ns;
+    // 16-byte quads set to 0 before the next kernel may start (nullptr: none).
+    uint4* zero;
+    int zero_quads;
 };
 // Pieces of the key axis such a call writes (0: the output directly), a rule
 // on its sizes alone. The plan for the prefix (causal false) has at least one.

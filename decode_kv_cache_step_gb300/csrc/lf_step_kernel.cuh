@@ -451,7 +451,8 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
 // kPrefix: the pieces of the unit's shared-prefix attention (pre_ml, pre_o of
 // the unit's sequence and heads) join the chunks in the softmax, so m_h, l_h,
 // the output and the scores' normalisation cover the prefix and the slots. A
-// piece with l = 0 holds no key and its output is not read.
+// piece with l = 0 holds no key and its output is not read; where the sequence
+// has no prefix, nothing wrote its pieces.
 template <int D, int G, bool kScore, bool kPrefix>
 __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usable,
                             uint64_t* scan_bars, int tid) {
@@ -483,14 +484,47 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
     __nv_bfloat16* out = p.out + row0 * D;
     const size_t pre_rows = kPrefix ? static_cast<size_t>(gridDim.y) / p.Hkv * p.Hq : 0;  // B * Hq
 
+    constexpr int kPerT = (G * D + kConsumers - 1) / kConsumers;
     // Prefix pieces: a warp per head, a lane per piece (at most 32). The
-    // attention that writes them is complete after the wait.
+    // attention that writes them is complete after the wait. Four pieces'
+    // outputs are requested first: a row's address is in bounds for every
+    // piece, and a piece without a key is selected away.
+    float w0[4][kPerT];
+    const auto load_pieces = [&](int c0, float(&v)[4][kPerT]) {
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+            const float* src = p.pre_o + (min(c0 + cc, p.pre_pieces - 1) * pre_rows + row0) * D;
+#pragma unroll
+            for (int k = 0; k < kPerT; ++k) {
+                const int e = tid + k * kConsumers;
+                v[cc][k] = (e < G * D) ? __ldcg(src + e) : 0.f;
+            }
+        }
+    };
     if constexpr (kPrefix) {
+        // The prefix of the sequence, if one holds: a thread per prefix. (One
+        // warp's search by ballots, inlined here, cost 1 to 4 us per step.)
+        bool mine = false;
+        for (int n = tid; n < p.prefixes; n += kConsumers) {
+            SeqRange r;
+            mine |= seq_range(p.prefix_start, p.prefix_len, n, static_cast<int>(gridDim.y) / p.Hkv,
+                              p.prefix_cap, false, &r) &&
+                    b >= r.q0 && b < r.q0 + r.n;
+        }
+        if (tid == 0) s_ncand[3] = 0;
         grid_dependency_wait();
+        load_pieces(0, w0);
         const int lane = tid & 31;
-        for (int h = tid >> 5; h < G; h += kConsumerWarps) {
-            float2 v = make_float2(-INFINITY, 0.f);
-            if (lane < p.pre_pieces) v = __ldcg(&p.pre_ml[lane * pre_rows + row0 + h]);
+        const int warp = tid >> 5;
+        const float2* row_ml = p.pre_ml + min(lane, p.pre_pieces - 1) * pre_rows + row0;
+        const float2 first = __ldcg(row_ml + min(warp, G - 1));
+        consumer_bar_sync();
+        if (mine) s_ncand[3] = 1;
+        consumer_bar_sync();
+        const bool holds = s_ncand[3] != 0 && lane < p.pre_pieces;
+        for (int h = warp; h < G; h += kConsumerWarps) {
+            float2 v = h == warp ? first : __ldcg(row_ml + h);
+            if (!holds) v.y = 0.f;
             if (v.y == 0.f) v.x = -INFINITY;
             float m = v.x;
 #pragma unroll
@@ -507,7 +541,6 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
 
     // The partial outputs of the first four chunks are requested first: they
     // do not depend on (m, l), so their round trip overlaps the weights'.
-    constexpr int kPerT = (G * D + kConsumers - 1) / kConsumers;
     float v0[4][kPerT];
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
@@ -607,32 +640,6 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
             s_piece[e].x = v.y == 0.f ? 0.f : exp2f(v.x - s_m[h]) * s_il[h];
         }
         consumer_bar_sync();
-        // Four pieces' loads in flight at a time; the row's address is in
-        // bounds for every piece, and a piece without a key is selected away.
-        for (int c0 = 0; c0 < p.pre_pieces; c0 += 4) {
-            float v[4][kPerT];
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-                const int c = min(c0 + cc, p.pre_pieces - 1);
-#pragma unroll
-                for (int k = 0; k < kPerT; ++k) {
-                    const int e = tid + k * kConsumers;
-                    v[cc][k] =
-                        (e < G * D) ? __ldcg(&p.pre_o[(c * pre_rows + row0) * D + e]) : 0.f;
-                }
-            }
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-                const int c = c0 + cc;
-                if (c >= p.pre_pieces) break;
-#pragma unroll
-                for (int k = 0; k < kPerT; ++k) {
-                    const int e = tid + k * kConsumers;
-                    const float w = (e < G * D) ? s_piece[e / D * p.pre_pieces + c].x : 0.f;
-                    o[k] += (w != 0.f) ? w * v[cc][k] : 0.f;
-                }
-            }
-        }
     }
     for (int c0 = 0; c0 < nchunk; c0 += 4) {
         float v[4][kPerT];
@@ -662,6 +669,24 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
                 const float w = (e < G * D) ? s_w[c * G + e / D] : 0.f;
                 o[k] += (w != 0.f) ? w * v[cc][k] : 0.f;
             }
+        }
+    }
+    if constexpr (kPrefix) {
+        for (int c0 = 0;;) {
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+                const int c = c0 + cc;
+                if (c >= p.pre_pieces) break;
+#pragma unroll
+                for (int k = 0; k < kPerT; ++k) {
+                    const int e = tid + k * kConsumers;
+                    const float w = (e < G * D) ? s_piece[e / D * p.pre_pieces + c].x : 0.f;
+                    o[k] += (w != 0.f) ? w * w0[cc][k] : 0.f;
+                }
+            }
+            c0 += 4;
+            if (c0 >= p.pre_pieces) break;
+            load_pieces(c0, w0);
         }
     }
 #pragma unroll

@@ -771,3 +771,34 @@ def test_without_programmatic_launch(monkeypatch):
     for a, b in zip(*got):
         assert torch.equal(a, b)
     no_errors()
+
+
+@pytest.mark.parametrize("B,S,P,fill", [(1, 2400, 700, 255), (3, 700, 2000, 127), (40, 640, 300, 255), (2, 100, 90, 255)])
+@pytest.mark.parametrize("score", [False, True])
+def test_prefix_workspace_of_any_contents(B, S, P, fill, score):
+    """The workspace needs no preparation: sequences with, beside and after the prefixes."""
+    g = gen(B + S)
+    Hq, Hkv, d, N = 8, 2, 64, 3
+    q, k, v = normal(g, B, Hq, d), normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    nk, nv = normal(g, B, Hkv, d), normal(g, B, Hkv, d)
+    kp, vp = normal(g, N, Hkv, P, d), normal(g, N, Hkv, P, d)
+    start, plen = ints([0, B // 3, B // 3, max(B // 3, B - 1)]), ints([P, P // 2, P])
+    write = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(lf.decode_prefix_workspace(B, Hq, Hkv, d, S, N, P), dtype=torch.uint8, device="cuda")
+    got = []
+    for contents in (0, fill, 0x41):
+        mask = torch.arange(S, dtype=torch.int32).flip(0).expand(B, Hkv, S).contiguous().cuda()
+        out = torch.zeros(B, Hq, d, dtype=BF, device="cuda")
+        slots = torch.zeros(B, Hkv, dtype=torch.int32, device="cuda")
+        ws.fill_(contents)
+        if score:
+            lf.decode_step_prefix(q, k, v, mask, nk, nv, write, kp, vp, start, plen, out, slots, 4, 0.1,
+                                  workspace=ws)
+        else:
+            lf.decode_attention_prefix(q, k, v, mask, nk, nv, write, kp, vp, start, plen, out, 0.1,
+                                       workspace=ws)
+        got.append((out, slots))
+    no_errors()
+    assert not torch.isnan(got[0][0]).any()
+    for out, slots in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(slots, got[0][1])
