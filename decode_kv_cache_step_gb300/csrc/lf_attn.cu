@@ -483,7 +483,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // words that every CTA sets to 0 before that).
     grid_dependency_wait();
     if (warp == 11 && p.zero != nullptr) {
-        for (int i = lane; i < p.zero_quads; i += 32) p.zero[i] = make_uint4(0u, 0u, 0u, 0u);
+        // Device-scope stores, fenced: the step's atomics meet them in L2.
+        for (int i = lane; i < p.zero_quads; i += 32)
+            asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1, %1, %1, %1};" ::"l"(p.zero + i), "r"(0u)
+                         : "memory");
         __threadfence();
     }
     allow_dependent_launch();

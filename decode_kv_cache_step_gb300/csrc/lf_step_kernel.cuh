@@ -502,15 +502,24 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
         }
     };
     if constexpr (kPrefix) {
-        // The prefix of the sequence, if one holds: a thread per prefix. (One
-        // warp's search by ballots, inlined here, cost 1 to 4 us per step.)
-        bool mine = false;
-        for (int n = tid; n < p.prefixes; n += kConsumers) {
-            SeqRange r;
-            mine |= seq_range(p.prefix_start, p.prefix_len, n, static_cast<int>(gridDim.y) / p.Hkv,
-                              p.prefix_cap, false, &r) &&
-                    b >= r.q0 && b < r.q0 + r.n;
+        // The prefix of the sequence, if one holds: a thread per prefix, among
+        // the last 128. (One warp's search by ballots, inlined here, cost 1 to
+        // 4 us per step.)
+        int from = 0, left = p.prefixes;
+        while (left > kConsumers) {
+            const int half = left / 2;
+            if (p.prefix_start[from + half] <= b) {
+                from += half;
+                left -= half;
+            } else {
+                left = half;
+            }
         }
+        SeqRange range;
+        const bool mine = tid < left &&
+                          seq_range(p.prefix_start, p.prefix_len, from + tid,
+                                    static_cast<int>(gridDim.y) / p.Hkv, p.prefix_cap, false, &range) &&
+                          b >= range.q0 && b < range.q0 + range.n;
         if (tid == 0) s_ncand[3] = 0;
         grid_dependency_wait();
         load_pieces(0, w0);

@@ -777,6 +777,15 @@ def test_without_programmatic_launch(monkeypatch):
 @pytest.mark.parametrize("score", [False, True])
 def test_prefix_workspace_of_any_contents(B, S, P, fill, score):
     """The workspace needs no preparation: sequences with, beside and after the prefixes."""
+    workspace_of_any_contents(B, S, P, fill, score)
+
+
+def test_prefix_workspace_of_any_contents_split_finish():
+    """Long caches, whose scores a second kernel takes."""
+    workspace_of_any_contents(2, 20000, 300, 255, True)
+
+
+def workspace_of_any_contents(B, S, P, fill, score):
     g = gen(B + S)
     Hq, Hkv, d, N = 8, 2, 64, 3
     q, k, v = normal(g, B, Hq, d), normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
@@ -802,3 +811,29 @@ def test_prefix_workspace_of_any_contents(B, S, P, fill, score):
     assert not torch.isnan(got[0][0]).any()
     for out, slots in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(slots, got[0][1])
+
+
+@pytest.mark.parametrize("N", [129, 300, 1000])
+def test_more_prefixes_than_threads(N):
+    """Each of many sequences has its own prefix, or none: against the sequences one by one."""
+    g = gen(N)
+    Hq, Hkv, d, S, P, B = 4, 2, 64, 70, 9, N - 3
+    q, k, v = normal(g, B, Hq, d), normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    nk, nv = normal(g, B, Hkv, d), normal(g, B, Hkv, d)
+    kp, vp = normal(g, N, Hkv, P, d), normal(g, N, Hkv, P, d)
+    starts = [min(max(n - 1, 0), B) for n in range(N + 1)]  # prefix 0 has none, n has n - 1
+    lens = [n % (P + 1) for n in range(N)]
+    mask = torch.zeros(B, Hkv, S, dtype=torch.int32, device="cuda")
+    write = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    out, ref = (torch.zeros(B, Hq, d, dtype=BF, device="cuda") for _ in range(2))
+    lf.decode_attention_prefix(q, k, v, mask, nk, nv, write, kp, vp, ints(starts), ints(lens), out, 0.2)
+    for b in list(range(0, B, 41)) + [B - 1]:
+        n = b + 1
+        one = slice(b, b + 1)
+        lf.decode_attention_prefix(q[one], k[one], v[one], mask[one], nk[one], nv[one], write[one],
+                                   kp[n:n + 1], vp[n:n + 1], ints([0, 1]), ints([lens[n]]),
+                                   ref[one], 0.2)
+        # Two orders of the same sums, each rounded to bf16 once from fp32.
+        a, c = out[b].double(), ref[b].double()
+        assert ((a - c).abs() <= 2 ** -7 * c.abs() + 1e-3).all(), b
+    no_errors()
