@@ -28,7 +28,8 @@
 //   warp 9          TMA loads: K and V tiles through a ring
 //   warp 10         next work item: cancels a pending CTA, finds the item's
 //                   sequence, rows and tiles, hands it to the others; loads Q
-//   warp 11         zeroes the rows of V tiles behind a range's last key
+//   warp 11         zeroes the rows of V tiles behind a range's last key, and
+//                   first the counters of the step that follows a prefix
 // A tensor product of 128 x 128 x 128 takes 512 cycles; a pair of tiles needs
 // four of them per 128 keys, and the two streams' softmax must fit in between.
 // So the chain from S to P is kept short: the exponentials start on the first

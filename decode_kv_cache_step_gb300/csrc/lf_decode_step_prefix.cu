@@ -8,7 +8,9 @@
 // wait at the step's start -> in the merge: nine prefixes of up to 5003
 // tokens over 67 ragged sequences 63 -> 50, a 16384-token prefix over 128
 // full caches of 2400 slots 219 -> 213, of which the slots alone take 186 at
-// the measured copy rate).
+// the measured copy rate). Without a memset of the counters and pieces before
+// the attention these take 48 and 212, one sequence of 2400 slots with a prefix
+// of 1000 tokens 12.7 instead of 16.5.
 #include "lf_step_kernel.cuh"
 
 namespace lf {
