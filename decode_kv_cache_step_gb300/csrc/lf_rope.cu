@@ -18,9 +18,9 @@
 // (fp64 would take 1000 cycles of an SM's fp64 unit per CTA).
 //
 // Measured (32 query, 8 KV heads of 128): 20.3K prompt tokens into their
-// caches 83 us, 6.0 TB/s read and written, 89% of the measured copy rate (the
-// same accesses without the arithmetic take 79.6); one token 3.0 us, 128 tokens
-// 3.4 us, which is the latency of a launch and three dependent round trips.
+// caches 80.5 us, 6.2 TB/s read and written, 92% of the measured copy rate (82.8
+// with loads marked evict-first); one token 3.0 us, 128 tokens 3.4 us, which is
+// the latency of a launch and three dependent round trips.
 #include <stdlib.h>
 
 #include <algorithm>
@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
             const int hh = h + i * per_tok;
             if (active && hh < heads) {
                 const __nv_bfloat16* src = row + static_cast<size_t>(hh) * D;
-                ra[i] = __ldcs(reinterpret_cast<const uint2*>(src + ea));
-                rb[i] = __ldcs(reinterpret_cast<const uint2*>(src + eb));
+                ra[i] = __ldcg(reinterpret_cast<const uint2*>(src + ea));
+                rb[i] = __ldcg(reinterpret_cast<const uint2*>(src + eb));
             }
         }
     };
@@ -305,10 +305,10 @@ cudaError_t launch_rope_d(const RopeParams& p, int sms, cudaStream_t stream) {
     // Many tokens: a warp takes one, and warps do not wait for one another.
     // Fewer: 256 threads take one, two or four, so that a token's heads are in
     // flight together. Measured, us for 256 threads (best of 1, 2, 4 tokens) /
-    // one warp: 32 + 16 heads of 128, 2000 tokens 12.9 / 17.2, 5000 tokens
-    // 27.9 / 28.8, 8000 tokens 39.7 / 37.1, 20000 tokens 89.5 / 84.1; 8 + 16
-    // heads of 64, 2000 tokens 5.5 / 6.8, 5000 tokens 10.8 / 10.1, 20000 tokens
-    // 32.0 / 26.3. And by tokens per CTA 1 / 2 / 4 (the first heads): 128 tokens
+    // one warp (with evict-first loads, some 3% slower): 32 + 16 heads of 128,
+    // 2000 tokens 12.9 / 17.2, 5000 tokens 27.9 / 28.8, 8000 tokens 39.7 / 37.1,
+    // 20000 tokens 89.5 / 84.1; 8 + 16 heads of 64, 2000 tokens 5.5 / 6.8, 5000
+    // tokens 10.8 / 10.1, 20000 tokens 32.0 / 26.3. And by tokens per CTA 1 / 2 / 4 (the first heads): 128 tokens
     // 3.8 / 5.6 / 7.1, 600 tokens 5.8 / 7.5 / 10.4, 2000 tokens 15.5 / 13.8 / 12.9.
     if (p.T >= 40 * sms) return launch_rope_t<D, 32>(p, 1, stream);
     int per = max_tokens(kRopeThreads);
