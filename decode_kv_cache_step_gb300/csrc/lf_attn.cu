@@ -481,16 +481,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // The next kernel may start once every CTA is past its wait (not before:
     // the decode step with a prefix reads its own inputs without waiting for
     // this grid, relying on the kernels before it being over, and counts in
-    // words that every CTA sets to 0 before that).
+    // words that every CTA sets to 0 before that). A CTA counts as having let
+    // it start with the first of its threads that says so, so one warp alone
+    // does, the one that stores the zeros, after its fence.
     grid_dependency_wait();
-    if (warp == 11 && p.zero != nullptr) {
-        // Device-scope stores, fenced: the step's atomics meet them in L2.
-        for (int i = lane; i < p.zero_quads; i += 32)
-            asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1, %1, %1, %1};" ::"l"(p.zero + i), "r"(0u)
-                         : "memory");
-        __threadfence();
+    if (warp == 11) {
+        if (p.zero != nullptr) {
+            // Device-scope stores, fenced: the step's atomics meet them in L2.
+            for (int i = lane; i < p.zero_quads; i += 32)
+                asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1, %1, %1, %1};" ::"l"(p.zero + i), "r"(0u)
+                             : "memory");
+            __threadfence();
+        }
+        __syncwarp();  // every lane's zeros
+        allow_dependent_launch();
     }
-    allow_dependent_launch();
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     // Work units of the streams: unit j of an item belongs to stream j & 1 and
     // reads K/V tile j >> 1 (rows mode) or j (keys mode) of the item's part of

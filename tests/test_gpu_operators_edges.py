@@ -1,0 +1,55 @@
+"""The prompt and shared-prefix operators where it is easy to go wrong: against their plain
+fp64 definitions (tests/_plain.py, which also derives the bounds)."""
+import math
+
+import pytest
+import torch
+
+import decode_kv_cache_step_gb300 as lf
+
+import _plain
+from test_gpu_operators import BF, gen, ints, near, no_errors, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B,Hkv,S,P,live", [(2250, 8, 2112, 300, 0), (2250, 8, 2112, 300, 3), (64, 8, 2400, 300, 0),
+                                            (1, 1, 700, 2000, 0), (7, 3, 2112, 64, 1)])
+def test_prefix_counters_are_zero_before_the_step_counts(monkeypatch, B, Hkv, S, P, live):
+    """Several chunks a unit, which count in words that the prefix's attention sets to 0; chunks
+    without a live slot count at once. Every unit's merge runs, whatever the workspace held and
+    however early the step starts."""
+    g = gen(B)
+    d = 64
+    q, nk = normal(g, B, Hkv, d), normal(g, B, Hkv, d)
+    k = torch.zeros(B, Hkv, S, d, dtype=BF, device="cuda")
+    v = torch.zeros_like(k)
+    k[:, :, :4], v[:, :, :4] = normal(g, B, Hkv, 4, d), normal(g, B, Hkv, 4, d)
+    kp, vp = normal(g, 1, Hkv, P, d), normal(g, 1, Hkv, P, d)
+    write = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    start, plen = ints([0, B]), ints([P])
+    mask = torch.full((B, Hkv, S), -1, dtype=torch.int32, device="cuda")
+    mask[:, :, :live] = 9
+    ws = torch.empty(lf.decode_prefix_workspace(B, Hkv, Hkv, d, S, 1, P), dtype=torch.uint8, device="cuda")
+
+    def step(fill):
+        ws.fill_(fill)
+        out = torch.full((B, Hkv, d), 7.0, dtype=BF, device="cuda")
+        slots = torch.full((B, Hkv), 77, dtype=torch.int32, device="cuda")
+        lf.decode_step_prefix(q, k, v, mask.clone(), nk, nk, write, kp, vp, start, plen, out, slots, 4, 0.125,
+                              flags=lf.LF_STEP_FILL_EMPTY_FIRST, workspace=ws)
+        return out, slots
+
+    monkeypatch.setenv("LF_PDL", "0")
+    want, slots = step(0)
+    assert (slots == live).all()  # the first empty slot
+    some = slice(0, B, max(1, B // 3))
+    for b in range(B)[some]:
+        one = _plain.prefix_step(q[b:b + 1], k[b:b + 1], v[b:b + 1], mask[b:b + 1], nk[b:b + 1], nk[b:b + 1],
+                                 write[b:b + 1], kp, vp, [0, 1], [P], 0, 0.125, ageing=False)
+        near(want[b:b + 1], one["out"], one["tol"])
+    monkeypatch.delenv("LF_PDL")
+    for fill in (0, 1, 255, 0x41, 255, 1):
+        out, slots = step(fill)
+        assert torch.equal(out, want) and (slots == live).all()
+    no_errors()
