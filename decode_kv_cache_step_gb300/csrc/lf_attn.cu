@@ -59,7 +59,8 @@
 // what a V tile holds behind the range's last key is zeroed in shared memory,
 // so it does not matter what lies there. A NaN or infinity in a row that
 // others of the tile do see would still reach this row's O as 0 * NaN: a row
-// whose result is not finite is computed again by attn_row, key by key.
+// whose result is not finite is computed again by attn_row, key by key. So is
+// one left without a reference (m = -infinity) by a tile that holds finite logits.
 #include <math.h>
 #include <stdlib.h>
 
@@ -922,6 +923,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) mbar_arrive(&p_full[s]);
             }
             if (!ok) break;
+            // The last tile has finite logits behind 32 of -infinity: its weights
+            // have no reference, so l (even 0) and O count for nothing.
+            if (m == -INFINITY && ahead > -INFINITY) l = NAN;
             const bool worked = units > s;  // the stream had a unit
             if (worked) {
                 ok = warp_wait(&o_done[s], (n - 1) & 1);

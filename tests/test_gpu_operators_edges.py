@@ -53,3 +53,50 @@ def test_prefix_counters_are_zero_before_the_step_counts(monkeypatch, B, Hkv, S,
         out, slots = step(fill)
         assert torch.equal(out, want) and (slots == live).all()
     no_errors()
+
+
+def low_first(k, at, value):
+    """Keys whose logit with a positive query is -infinity: 40 from `at`; the others' logits near
+    value (a column of the query is 1)."""
+    k[..., 0] = value
+    k[..., at:at + 40, 0] = -math.inf
+
+
+@pytest.mark.parametrize("value", [0.0, -300.0])
+@pytest.mark.parametrize("kv,at,Hq,Hkv,d", [
+    (128, 0, 1, 1, 64), (256, 128, 4, 1, 128), (256, 0, 2, 2, 64), (512, 0, 8, 1, 64), (512, 384, 4, 2, 128),
+    (2048, 1920, 4, 1, 64), (2048, 896, 1, 1, 128)])
+def test_minus_infinity_before_the_last_tiles_keys(kv, at, Hq, Hkv, d, value):
+    """The first logits of a tile are -infinity and the rest are not, in tiles that no other of
+    their stream follows, with the keys in parts and not; the finite logits large and small."""
+    g = gen(kv + at)
+    q, k, v = normal(g, 1, Hq, d), normal(g, 1, Hkv, kv, d), normal(g, 1, Hkv, kv, d)
+    q[..., 0] = 1
+    low_first(k, at, value)
+    out = torch.empty_like(q)
+    lf.window_attention(q, k, v, ints([0, 1]), ints([kv]), out, 0, 0, 1.0 if value else 0.125)
+    ref, tol = _plain.window_rows(q, k, v, [0, 1], [kv], 0, 0, 1.0 if value else 0.125)
+    # A logit near -300 is held to 2^-16, and its weight to that: beyond _plain's bound for N(0, 1).
+    near(out, ref, tol + 2.0 ** -10 * v.abs().max().double().cpu())
+    no_errors()
+
+
+@pytest.mark.parametrize("value", [0.0, -300.0])
+@pytest.mark.parametrize("P,at,live", [(128, 0, 0), (256, 128, 30), (512, 0, 5), (2048, 1920, 0), (2048, 384, 64)])
+def test_minus_infinity_in_a_shared_prefix(P, at, live, value):
+    g = gen(P + at)
+    B, Hq, Hkv, d, S = 3, 4, 2, 64, 64
+    q, k, v = normal(g, B, Hq, d), normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    kp, vp, nk = normal(g, 1, Hkv, P, d), normal(g, 1, Hkv, P, d), normal(g, B, Hkv, d)
+    q[..., 0] = 1
+    k[..., 0] = value
+    low_first(kp, at, value)
+    mask = torch.full((B, Hkv, S), -1, dtype=torch.int32, device="cuda")
+    mask[:, :, :live] = 7
+    write = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    scale = 1.0 if value else 0.125
+    lf.decode_attention_prefix(q, k, v, mask, nk, nk, write, kp, vp, ints([0, B]), ints([P]), out, scale)
+    ref = _plain.prefix_step(q, k, v, mask, nk, nk, write, kp, vp, [0, B], [P], 0, scale, ageing=False)
+    near(out, ref["out"], ref["tol"] + 2.0 ** -10 * vp.abs().max().double().cpu())
+    no_errors()
