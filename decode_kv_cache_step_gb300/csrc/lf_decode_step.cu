@@ -35,8 +35,9 @@ template <int G>
 __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel(const StepParams p, int parts) {
     // Launched behind the decode-step kernel with programmatic dependent
     // launch, this grid starts only once every decode-step CTA has passed its
-    // own dependency wait: all of them run or have run, and none waits on
-    // this kernel, so every unit's flag goes up. Instead of waiting for the
+    // own dependency wait (or, with a shared prefix, has either passed it or
+    // left its unit to another): all of them run or have run, and none waits
+    // on this kernel, so every unit's flag goes up. Instead of waiting for the
     // whole decode-step grid to finish, each CTA waits for its own unit's
     // flag (acquire; every write the flag releases is then visible), so the
     // early units are scored while the decode-step kernel's tail still runs.

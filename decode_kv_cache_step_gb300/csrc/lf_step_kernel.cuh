@@ -522,6 +522,7 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
                           b >= range.q0 && b < range.q0 + range.n;
         if (tid == 0) s_ncand[3] = 0;
         grid_dependency_wait();
+        if (p.split) allow_dependent_launch();
         load_pieces(0, w0);
         const int lane = tid & 31;
         const int warp = tid >> 5;
@@ -1512,9 +1513,11 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
     // A step with a shared prefix does not wait here: the kernel before it,
     // the prefix's attention, lets it start only once every kernel before
     // that is over, and its result is first read in the merge, which waits.
-    // So the slots stream while the prefix's last CTAs run.
+    // So the slots stream while the prefix's last CTAs run. The scoring kernel
+    // of a split finish may start only once no CTA has the prefix to wait for
+    // (see finish_unit): its waits for the units' flags have a limit.
     if constexpr (kPrefix) {
-        allow_dependent_launch();
+        if (!p.split) allow_dependent_launch();
     } else {
         if (!p.split) allow_dependent_launch();
         grid_dependency_wait();

@@ -100,3 +100,31 @@ def test_minus_infinity_in_a_shared_prefix(P, at, live, value):
     ref = _plain.prefix_step(q, k, v, mask, nk, nk, write, kp, vp, [0, B], [P], 0, scale, ageing=False)
     near(out, ref["out"], ref["tol"] + 2.0 ** -10 * vp.abs().max().double().cpu())
     no_errors()
+
+
+def test_prefix_scores_wait_as_long_as_the_prefix_takes(monkeypatch):
+    """Prefixes of 2^19 keys with an infinite value each: every row takes the second pass, more
+    than a second. The scoring kernel behind the step waits for that, and scores as the step
+    itself does. (Few enough units that the step's CTAs all run beside the prefixes'.)"""
+    g = gen(31)
+    N, Hq, Hkv, d, S, P = 80, 8, 1, 64, 128, 1 << 19
+    B = 2 * N
+    q, nk = normal(g, B, Hq, d), normal(g, B, Hkv, d)
+    k, v = normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    kp, vp = (torch.zeros(N, Hkv, P, d, dtype=BF, device="cuda") for _ in range(2))
+    vp[:, 0, 17, 3] = math.inf
+    write = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    mask = torch.randint(0, 90, (B, Hkv, S), generator=g, dtype=torch.int32).cuda()
+    got = []
+    for mode in ("0", "1"):
+        monkeypatch.setenv("LF_SPLIT", mode)
+        out, m = torch.empty_like(q), mask.clone()
+        nxt = torch.full((B, Hkv), 7777, dtype=torch.int32, device="cuda")
+        scores = torch.zeros(B, Hkv, S, device="cuda")
+        lf.decode_step_prefix(q, k, v, m, nk, nk, write, kp, vp, ints(list(range(0, B + 1, 2))), ints([P] * N), out,
+                              nxt, 5, 0.125, scores=scores)
+        no_errors()
+        got.append((out, nxt, scores, m))
+    assert torch.isinf(got[0][0][..., 3]).all() and torch.isfinite(got[0][0][..., 4:]).all()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
