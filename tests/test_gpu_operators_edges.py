@@ -128,3 +128,28 @@ def test_prefix_scores_wait_as_long_as_the_prefix_takes(monkeypatch):
     assert torch.isinf(got[0][0][..., 3]).all() and torch.isfinite(got[0][0][..., 4:]).all()
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_second_pass_of_every_row_outlasts_no_wait(d):
+    """An infinite value in a prefix of 2^18 keys, for more query tiles than the GPU has SMs: every
+    row of a CTA's items takes the second pass while its other warps wait."""
+    g = gen(d)
+    B, Hq, Hkv, S, P = 6000, 8, 1, 64, 1 << 18
+    q, nk = normal(g, B, Hq, d), normal(g, B, Hkv, d)
+    k = normal(g, B, Hkv, S, d)
+    kp, vp = (normal(g, 1, Hkv, 2048, d).repeat(1, 1, P // 2048, 1) for _ in range(2))
+    vp[0, 0, 17, 3] = math.inf
+    write = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    mask = torch.zeros(B, Hkv, S, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    lf.decode_attention_prefix(q, k, k, mask, nk, nk, write, kp, vp, ints([0, B]), ints([P]), out, 0.125)
+    no_errors()
+    assert torch.isinf(out[..., 3]).all()
+    vp[0, 0, 17, 3] = 0.0  # the reference of the other columns
+    for b in (0, 2999, 5999):
+        one = slice(b, b + 1)
+        ref = _plain.prefix_step(q[one], k[one], k[one], mask[one], nk[one], nk[one], write[one], kp, vp, [0, 1], [P],
+                                 0, 0.125, ageing=False)
+        # fp32 sums of P keys in sequence: P * 2^-24 of sum p |v| at most, 2^-6.
+        near(out[one, :, 4:], ref["out"][..., 4:], (ref["tol"] * (1 + 2.0 ** 2))[..., 4:])
