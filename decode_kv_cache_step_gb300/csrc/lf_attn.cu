@@ -33,15 +33,22 @@
 // A tensor product of 128 x 128 x 128 takes 512 cycles; a pair of tiles needs
 // four of them per 128 keys, and the two streams' softmax must fit in between.
 // So the chain from S to P is kept short: the exponentials start on the first
-// 32 columns of S, with the reference m left by the tiles before. m moves to
-// a row's maximum only after a tile that exceeds it by more than 2^8 (O and l
-// are rescaled before the next tile's P), which is rare. Until then the
+// 32 columns of S, with the reference m left by the tiles before. m moves only
+// after a tile whose weights add up to more than 2^10, by the logarithm of that
+// sum (O and l are rescaled before the next tile's P), which is rare: any
+// reference serves, so the tile's maximum is not looked for. Until then the
 // weights stay as they are, relative precision and all: bf16 and fp32 hold up
 // to 2^127, and a row that outgrows 2^100 within one tile is computed again.
 // P is handed over in two halves, the first while the second is still in the
 // making.
 // P is rounded to bf16 (at most 2^-8 of each weight) because the tensor cores
-// take it; l sums the unrounded weights.
+// take it; l sums the rounded weights, so what the rounding does to a weight
+// that dominates the row cancels: 0.0018 of the exact outputs' norm, where the
+// unrounded sum gave 0.0023 and rounding exact outputs gives 0.0016. (The sum
+// adds bf16 to fp32 in one instruction a weight; widened first, two by two, a
+// causal prompt of 16384 tokens took 2% longer, with a maximum beside it 10%.)
+// A shared prefix keeps the sum of its unrounded weights as well, which is its
+// share of the softmax that the step's slots, outputs and scores see.
 //
 // What bounds it, and what it measured (32 query and 8 KV heads of 128):
 //   a causal prompt of 16384 tokens 1.56 ms, 1406 TFLOP/s, at the board's
@@ -83,8 +90,8 @@ constexpr int kAttnThreads = kSoftmaxThreads + 128;
 constexpr int kSoftmaxRegs = 224;
 constexpr int kOtherRegs = 56;
 constexpr int kPanel = kRows * 128;  // bytes of 64 columns of a tile
-constexpr float kRescale = 8.f;      // log2 growth of the maximum that moves m
-constexpr float kMaxGrowth = 100.f;  // log2 growth within one tile that l and O are trusted with
+constexpr float kRescale = 1024.f;      // a tile's sum of weights that moves m
+constexpr float kMaxGrowth = 1.27e30f;  // 2^100: the largest sum that l and O are trusted with
 
 constexpr int kItemSlots = 3;        // items in flight between the warps
 constexpr int kAskTiles = 4;         // K/V tiles of an item left to load when the next is asked for
@@ -426,7 +433,7 @@ __device__ __forceinline__ uint32_t below(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-template <int D, bool kRowsMode>
+template <int D, bool kRowsMode, bool kCausal>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     lf_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnParams p,
@@ -805,13 +812,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int units = rows ? 2 * it.count : it.count;
             const bool valid = tt < it.ntok;
             const bool any_valid = __any_sync(0xffffffffu, valid);
-            const int row_hi = p.causal ? it.pos0 + tt + 1 : it.hi;
-            const int row_lo = (p.causal && p.window > 0) ? max(0, row_hi - p.window) : 0;
+            const int row_hi = kCausal ? it.pos0 + tt + 1 : it.hi;
+            const int row_lo = (kCausal && p.window > 0) ? max(0, row_hi - p.window) : 0;
             // Keys every row of the warp sees: [all_lo, all_hi), and below sinks.
             const int all_hi = __shfl_sync(0xffffffffu, row_hi, 0);
             const int all_lo = __shfl_sync(0xffffffffu, row_lo, 31);
-            float m = -INFINITY, l = 0.f;
-            float ahead = -INFINITY;  // maximum of the last tile
+            float m = -INFINITY, l = 0.f;  // l: of the rounded weights
+            float l_all = 0.f;             // of the weights themselves (prefix)
+            float grown = 0.f;             // of the last tile's weights
             for (int j = s; j < units; j += 2, ++n) {
                 if (!warp_wait(&s_full[s], n & 1)) {
                     ok = false;
@@ -847,11 +855,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         return fmaxf(t[0], t[1]);
                     };
                     // The reference moves where the last tile outgrew it.
-                    if (__any_sync(0xffffffffu, ahead > m + kRescale)) {
-                        const float f = ahead > m + kRescale ? ex2_approx(m - ahead) : 1.f;
+                    if (__any_sync(0xffffffffu, grown > kRescale)) {
+                        const float to_m = grown > kRescale ? m + __log2f(grown) : m;
+                        const float f = grown > kRescale ? ex2_approx(m - to_m) : 1.f;
+                        m = to_m;
                         // Beyond 2^100 in one tile: the row is computed again.
-                        l = ahead > m + kMaxGrowth ? NAN : l * f;
-                        if (ahead > m + kRescale) m = ahead;
+                        l = grown > kMaxGrowth ? NAN : l * f;
+                        if (!kCausal) l_all *= f;
                         // The product that S waited for came after the one
                         // that last wrote O.
 #pragma unroll 1
@@ -867,9 +877,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         tmem_wait_st();
                     }
                     uint64_t b2 = 0;
-                    uint64_t sum[2] = {0ull, 0ull};
-                    float top = -INFINITY;
-                    // Weights of 32 keys: exponentials, sum, P.
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint64_t all[2] = {0ull, 0ull};
+                    // Weights of 32 keys: exponentials, P, its sum.
                     auto weigh = [&](int k, const uint32_t* v) {
                         uint32_t pk[16];
 #pragma unroll
@@ -879,10 +889,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                                               __uint_as_float(v[e + 1])), c2, b2), a, b);
                             a = ex2_approx(a);
                             b = ex2_approx(b);
-                            sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], pack_f32x2(a, b));
+                            if (!kCausal) all[(e >> 1) & 1] = add_f32x2(all[(e >> 1) & 1], pack_f32x2(a, b));
                             pk[e >> 1] = pack_bf16x2(a, b);
+                            add_bf16x2(sum[e & 2], sum[(e & 2) + 1], pk[e >> 1]);
                         }
-                        top = fmaxf(top, largest(v));
                         tmem_st16(ts + (k >> 1), pk);
                     };
                     auto hand_over = [&]() {
@@ -901,7 +911,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             // No reference yet: the largest of the first 32.
                             tmem_wait_ld();
                             const float t = largest(x[0]) * c;
-                            if (m == -INFINITY) m = t;
+                            if (m == -INFINITY) {
+                                m = t;
+                                // -infinity all: no reference for the others.
+                                if (t == -INFINITY) l = NAN;
+                            }
                         }
                         refer();
 #pragma unroll
@@ -931,21 +945,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         }
                     }
                     tmem_wait_st();
-                    float a, b;
-                    unpack_f32x2(add_f32x2(sum[0], sum[1]), a, b);
-                    l += a + b;
-                    ahead = top * c;
-                } else if (lane == 0) {
-                    mbar_arrive(&p_half[s]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[s]);
+                    grown = (sum[0] + sum[2]) + (sum[1] + sum[3]);
+                    l += grown;
+                    if (!kCausal) {
+                        float a, b;
+                        unpack_f32x2(add_f32x2(all[0], all[1]), a, b);
+                        l_all += a + b;
+                    }
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&p_half[s]);
+                        mbar_arrive(&p_full[s]);
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[s]);
             }
             if (!ok) break;
-            // The last tile has finite logits behind 32 of -infinity: its weights
-            // have no reference, so l (even 0) and O count for nothing.
-            if (m == -INFINITY && ahead > -INFINITY) l = NAN;
+            // A prefix's share of the softmax is that of its unrounded weights: with
+            // the base moved by the sums' quotient, l_all 2^m = l 2^m', O stays O / l.
+            if (!kCausal && l > 0.f) m += __log2f(l_all / l);
             const bool worked = units > s;  // the stream had a unit
             if (worked) {
                 ok = warp_wait(&o_done[s], (n - 1) & 1);
@@ -1143,12 +1165,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) lf_attn_merge_kernel(const A
         *reinterpret_cast<uint32_t*>(p.out + row * D + lane * kC + c) = pack_bf16x2(o[c], o[c + 1]);
 }
 
-template <int D, bool kRowsMode>
+template <int D, bool kRowsMode, bool kCausal>
 cudaError_t launch_attention_t(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                const CUtensorMap& tmV, const AttnParams& p, const AttnPlan& pl,
                                cudaStream_t stream) {
     using L = AttnSmem<D>;
-    auto kernel = lf_attn_kernel<D, kRowsMode>;
+    auto kernel = lf_attn_kernel<D, kRowsMode, kCausal>;
     static int configured_for = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1193,12 +1215,14 @@ cudaError_t launch_attention(int D, const CUtensorMap& tmQ, const CUtensorMap& t
                              cudaStream_t stream) {
     const AttnPlan pl = attn_plan(p.T, p.N, p.Hq, p.Hkv, p.S, p.causal, p.window, p.sinks, sms);
     if (p.pieces > kMaxPieces) return cudaErrorInvalidConfiguration;
-    if (D == 64)
-        return pl.rows_mode ? launch_attention_t<64, true>(tmQ, tmK, tmV, p, pl, stream)
-                            : launch_attention_t<64, false>(tmQ, tmK, tmV, p, pl, stream);
-    if (D == 128)
-        return pl.rows_mode ? launch_attention_t<128, true>(tmQ, tmK, tmV, p, pl, stream)
-                            : launch_attention_t<128, false>(tmQ, tmK, tmV, p, pl, stream);
+#define LF_ATTN_CASE(DD, RR, CC) \
+    if (D == DD && pl.rows_mode == RR && p.causal == CC) \
+        return launch_attention_t<DD, RR, CC>(tmQ, tmK, tmV, p, pl, stream);
+    LF_ATTN_CASE(64, true, true) LF_ATTN_CASE(64, false, true)
+    LF_ATTN_CASE(64, true, false) LF_ATTN_CASE(64, false, false)
+    LF_ATTN_CASE(128, true, true) LF_ATTN_CASE(128, false, true)
+    LF_ATTN_CASE(128, true, false) LF_ATTN_CASE(128, false, false)
+#undef LF_ATTN_CASE
     return cudaErrorInvalidValue;
 }
 

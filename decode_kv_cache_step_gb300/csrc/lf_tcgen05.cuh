@@ -198,4 +198,14 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// x and y plus the two bf16 values of v.
+__device__ __forceinline__ void add_bf16x2(float& x, float& y, uint32_t v) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "add.f32.bf16 %0, a, %0;\n\t"
+        "add.f32.bf16 %1, b, %1;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "r"(v));
+}
+
 }  // namespace lf

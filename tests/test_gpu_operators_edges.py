@@ -153,3 +153,59 @@ def test_second_pass_of_every_row_outlasts_no_wait(d):
                                  0, 0.125, ageing=False)
         # fp32 sums of P keys in sequence: P * 2^-24 of sum p |v| at most, 2^-6.
         near(out[one, :, 4:], ref["out"][..., 4:], (ref["tol"] * (1 + 2.0 ** 2))[..., 4:])
+
+
+# Equal values in every key: an output is their weights' sum over the weights' sum. Where both
+# sums are of the same (rounded) weights, only fp32 accumulation is left, below n * 2^-24 for n <=
+# 5000 keys, 3e-4: less than half a step of bf16 (2^-9 of the value or more), so it is exact.
+CONSTANT = [  # rows per sequence, lengths, window, sinks, Hq, Hkv, d
+    ([1], [200], 0, 0, 8, 1, 64), ([1, 1, 1], [129, 1000, 4999], 0, 0, 4, 2, 128), ([1], [5000], 1024, 4, 2, 2, 64),
+    ([1] * 40, [300 + 17 * i for i in range(40)], 256, 3, 8, 2, 128), ([700], [700], 0, 0, 4, 1, 64),
+    ([300, 2, 150], [1300, 900, 150], 200, 70, 4, 2, 128), ([33, 5], [161, 512], 130, 0, 8, 1, 64)]
+
+
+@pytest.mark.parametrize("sharp", [0.5, 3.0])
+@pytest.mark.parametrize("nq,kv,window,sinks,Hq,Hkv,d", CONSTANT)
+def test_equal_values_come_out_exactly(nq, kv, window, sinks, Hq, Hkv, d, sharp):
+    g = gen(sum(kv))
+    B, T, S = len(nq), sum(nq), max(kv)
+    starts = [sum(nq[:i]) for i in range(B + 1)]
+    q, k = normal(g, T, Hq, d), normal(g, B, Hkv, S, d)
+    row = normal(g, Hkv, d)
+    v = row[None, :, None].expand(B, Hkv, S, d).contiguous()
+    out = torch.empty_like(q)
+    lf.window_attention(q, k, v, ints(starts), ints(kv), out, window, sinks, sharp * d ** -0.5)
+    assert torch.equal(out, row.repeat_interleave(Hq // Hkv, 0).expand(T, Hq, d))
+    no_errors()
+
+
+@pytest.mark.parametrize("sharp", [0.5, 3.0])
+@pytest.mark.parametrize("B,P,Hq,Hkv,d", [(1, 200, 8, 1, 64), (5, 1000, 4, 2, 128), (70, 4999, 8, 2, 64), (9, 129, 2, 2, 64)])
+def test_equal_values_of_a_prefix_come_out_exactly(B, P, Hq, Hkv, d, sharp):
+    """And the scores' normalisation stays that of the weights themselves: own slots with equal
+    logits score alike to fp32, whatever the prefix's weights round to."""
+    g = gen(B + P)
+    S, W = 40, 2
+    q, nk = normal(g, B, Hq, d), normal(g, B, Hkv, d)
+    kp, row = normal(g, 1, Hkv, P, d), normal(g, Hkv, d)
+    vp = row[None, :, None].expand(1, Hkv, P, d).contiguous()
+    k, v = normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    write = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    mask = torch.full((B, Hkv, S), -1, dtype=torch.int32, device="cuda")
+    out, nxt = torch.empty_like(q), torch.empty(B, Hkv, dtype=torch.int32, device="cuda")
+    tail = (kp, vp, ints([0, B]), ints([P]))
+    scale = sharp * d ** -0.5
+    lf.decode_attention_prefix(q, k, v, mask, nk, nk, write, *tail, out, scale)
+    assert torch.equal(out, row.repeat_interleave(Hq // Hkv, 0).expand(B, Hq, d))
+    mask.fill_(9)
+    scores = torch.empty(B, Hkv, S, device="cuda")
+    lf.decode_step_prefix(q, k, v, mask, nk, nk, write, *tail, out, nxt, W, scale, scores=scores)
+    one = slice(0, min(B, 9))
+    ref = _plain.prefix_step(q[one], k[one], v[one], mask[one], nk[one], nk[one], write[one], kp, vp,
+                             [0, min(B, 9)], [P], W, scale, ageing=False)
+    # A logit is within d * 2^-24 * sum |q k| * scale of its value, with sum |q k| * scale <= 32 sharp
+    # (2^-9 of a weight at most, less by the square root of d and of the terms); the approximate
+    # exponential, the row's L1 norm and the sums are within 2^-18.
+    s, r = scores[one].double().cpu(), ref["scores"]
+    assert ((s - r).abs() <= (sharp * 2.0 ** -12 + 2.0 ** -18) * r + 1e-37).all(), float(((s - r).abs() / r).max())
+    no_errors()
