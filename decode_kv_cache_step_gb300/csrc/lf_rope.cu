@@ -13,9 +13,9 @@
 // pair, so only the norm's sum crosses lanes. A CTA takes all heads of one to
 // four tokens (one warp a token where there are many), and a lane keeps its 4
 // angles and its weights for all of them. The angles are formed once per CTA in
-// shared memory while the first heads' loads are in flight: positions of a
-// million times frequencies near 1 need some 44 bits, which two floats hold
-// (fp64 would take 1000 cycles of an SM's fp64 unit per CTA).
+// shared memory while the first heads' loads are in flight, with integers:
+// any int32 position times a frequency, less its whole turns, needs some 60
+// bits (fp64 would take 1000 cycles of an SM's fp64 unit per CTA).
 //
 // Measured (32 query, 8 KV heads of 128): 20.3K prompt tokens into their
 // caches 80.5 us, 6.2 TB/s read and written, 92% of the measured copy rate (82.8
@@ -77,17 +77,33 @@ __device__ __forceinline__ uint64_t swap2(uint64_t v) {
     return pack_f32x2(y, x);
 }
 
-// n * f / (2 pi) reduced to a turn, for an n with at most 24 significant bits:
-// the product is exact in two floats (fused multiply-add), 1 / (2 pi) is held
-// in two, and the leading part's fraction is exact.
-__device__ __forceinline__ float turns(float n, float f) {
-    constexpr float kHi = 0.15915494f;       // 1 / (2 pi) to 24 bits
-    constexpr float kLo = 6.4206383e-09f;    // and the rest of it
-    const float p = n * f;
-    const float p_lo = fmaf(n, f, -p);
-    const float t = p * kHi;
-    const float t_lo = fmaf(p, kHi, -t) + fmaf(p, kLo, p_lo * kHi);
-    return (t - rintf(t)) + t_lo;
+// n * f / (2 pi) less its whole turns, to 2^-25 of a turn (the result's last
+// bit) for any n and any f below 2^24 (to 2^-23 below 2^32), after Payne and Hanek's reduction: f = M 2^E
+// with an integer M of 24 bits, so the fraction of f / (2 pi) is a window of 64
+// bits of M times the bits of 1 / (2 pi). n is whole: the product with the
+// window, modulo 2^64, is the fraction of a turn.
+__device__ __forceinline__ float turns(int n, float f) {
+    // 1 / (2 pi), 96 bits behind the point.
+    constexpr uint32_t k0 = 0x28be60dbu, k1 = 0x9391054au, k2 = 0x7f09d5f4u;
+    const uint32_t bits = __float_as_uint(f);
+    const int ex = bits >> 23 & 255;
+    if (ex == 255) return NAN;
+    const uint64_t m = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
+    const uint64_t p1 = m * k1 + (m * k2 >> 32);
+    const uint64_t p0 = m * k0 + (p1 >> 32);
+    const uint64_t lo = p0 << 32 | static_cast<uint32_t>(p1);
+    const uint64_t hi = p0 >> 32;
+    const int s = 150 - max(ex, 1);
+    uint64_t r;
+    if (s <= 0)
+        r = s > -64 ? lo << -s : 0;
+    else if (s < 64)
+        r = lo >> s | hi << (64 - s);
+    else
+        r = s < 128 ? hi >> (s - 64) : 0;
+    const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(n)) * r;
+    const float a = static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-32f;
+    return bits >> 31 ? -a : a;
 }
 
 template <int D, bool kInterleaved, int kThreads>
@@ -190,11 +206,7 @@ __global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
     __syncthreads();
     for (int i = tid; i < ntok * half; i += kThreads) {
         const int kk = i / half;
-        // In two parts that are exact in fp32, so any int32 position is.
-        const int n = at[kk].pos;
-        const float f = __ldg(p.inv_freq + (i - kk * half));
-        float t = turns(static_cast<float>(n & ~0xfff), f) + turns(static_cast<float>(n & 0xfff), f);
-        t -= rintf(t);
+        const float t = turns(at[kk].pos, __ldg(p.inv_freq + (i - kk * half)));
         float s, c;
         sincospif(2.f * t, &s, &c);
         cs[kk][i - kk * half] = make_float2(c, s);

@@ -333,9 +333,11 @@ lf_status lf_device_errors(void* stream, uint32_t* flags, int clear);
  * k_weight   in  bf16 [d] norm weights, or both NULL for no norm. A query or
  *                key head becomes y = x * weight / sqrt(mean(x^2) + eps).
  * inv_freq   in  float [rot / 2]: pair i of a token at position n turns by
- *                n * inv_freq[i] (formed in fp64). rot is a multiple of 16 in
- *                [16, d]; values from rot on stay as they are. The pairs are
- *                (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved != 0.
+ *                n * inv_freq[i], whole turns taken off in integers: within
+ *                2^-25 of a turn for every n and frequencies below 2^24. rot
+ *                is a multiple of 16 in [16, d]; values from rot on stay as
+ *                they are. The pairs are (i, i + rot / 2), or (2 i, 2 i + 1)
+ *                with interleaved != 0.
  * positions  in  int32 [T]
  * q_out      out bf16 [T][Hq][d]
  * k_out,

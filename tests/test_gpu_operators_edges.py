@@ -209,3 +209,39 @@ def test_equal_values_of_a_prefix_come_out_exactly(B, P, Hq, Hkv, d, sharp):
     s, r = scores[one].double().cpu(), ref["scores"]
     assert ((s - r).abs() <= (sharp * 2.0 ** -12 + 2.0 ** -18) * r + 1e-37).all(), float(((s - r).abs() / r).max())
     no_errors()
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,d,rot,inter", [(500, 8, 2, 128, 128, False), (700, 4, 1, 64, 48, True),
+                                                  (6500, 2, 1, 128, 112, True)])
+@pytest.mark.parametrize("top", [1 << 24, 1 << 28, (1 << 31) - 1, -(1 << 31)])
+def test_rotation_at_far_positions(T, Hq, Hkv, d, rot, inter, top):
+    """Any int32 position, frequencies from 1e-6 to above 1 and below 0: the bound of _plain.rope_bound
+    (its own angles, n * f in fp64, are within 2^-22)."""
+    g = gen(T + rot)
+    qkv = normal(g, T, Hq + 2 * Hkv, d)
+    freq = (1e6 ** (-torch.arange(rot // 2).double() * 2 / rot)).float()
+    freq[1], freq[2], freq[3], freq[4] = 1.9, -0.7, 0.0, 1e-30
+    freq = freq.cuda()
+    span = torch.randint(0, 4096, (T,), generator=g, dtype=torch.int32)
+    pos = (torch.tensor(top, dtype=torch.int32) + (span if top < 0 else -span)).cuda()
+    pos[0] = top
+    q = torch.empty(T, Hq, d, dtype=BF, device="cuda")
+    k, v = (torch.empty(T, Hkv, d, dtype=BF, device="cuda") for _ in range(2))
+    lf.qk_norm_rope(qkv, None, None, freq, pos, q, k, v, 1e-6, interleaved=inter)
+    ref = _plain.rope(qkv[:, :Hq + Hkv], None, freq, pos, 1e-6, inter)
+    near(torch.cat([q, k], 1), ref, _plain.rope_bound(ref))
+    no_errors()
+
+
+def test_rotation_by_large_frequencies():
+    """Frequencies beyond a turn per position: what counts is their fraction of a turn."""
+    g = gen(8)
+    T, d = 300, 64
+    qkv = normal(g, T, 3, d)
+    freq = torch.exp2(torch.linspace(0, 24, 32).double()).float().cuda()
+    pos = torch.randint(-1000, 1000, (T,), generator=g, dtype=torch.int32).cuda()
+    q, k, v = (torch.empty(T, 1, d, dtype=BF, device="cuda") for _ in range(3))
+    lf.qk_norm_rope(qkv, None, None, freq, pos, q, k, v, 1e-6)
+    ref = _plain.rope(qkv[:, :2], None, freq, pos, 1e-6, False)  # |n f| < 2^34: exact in fp64
+    near(torch.cat([q, k], 1), ref, _plain.rope_bound(ref))
+    no_errors()
