@@ -36,6 +36,10 @@ constexpr int kRopeWarps = 32;     // resident per SM, at 64 registers a thread
 constexpr int kBatch = 4;          // heads whose loads a lane has in flight
 constexpr int kMaxAgeParts = 16;   // CTAs that write one head's ages
 constexpr int kAgesPerPart = 2048;
+// Mean squares taken as they are: none of a head's squares overflows, and what
+// the smallest lose below fp32's normal range does not count.
+constexpr float kMeanMax = 0x1p110f;
+constexpr float kMeanMin = 0x1p-100f;
 
 // Tokens a CTA may take.
 __host__ __device__ constexpr int max_tokens(int threads) { return threads >= 128 ? 4 : 1; }
@@ -244,49 +248,79 @@ __global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
     __nv_bfloat16* const kd = p.k_out + kv0 - p.Hq * kv_step;
     __nv_bfloat16* const vd = p.v_out + kv0 - (p.Hq + p.Hkv) * kv_step;
     const bool norm = p.q_weight != nullptr;
+    auto sum_squares = [&](const uint64_t* x, const uint64_t* y) {
+        float s0, s1;
+        unpack_f32x2(fma_f32x2(x[0], x[0], fma_f32x2(x[1], x[1],
+                     fma_f32x2(y[0], y[0], mul_f32x2(y[1], y[1])))), s0, s1);
+        float ss = s0 + s1;
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(gmask, ss, off);
+        return ss;
+    };
+    // Head hh from its two chunks: times inv and the weights, turned, stored.
+    auto finish = [&](int hh, uint64_t* x, uint64_t* y, float inv) {
+        const bool is_q = hh < p.Hq;
+        if (norm) {
+            const uint64_t inv2 = pack_f32x2(inv, inv);
+            const uint2 wa = is_q ? wq[0] : wk[0], wb = is_q ? wq[1] : wk[1];
+            // The norm first: a weight times a large value may overflow.
+            x[0] = mul_f32x2(mul_f32x2(x[0], inv2), widen2(wa.x));
+            x[1] = mul_f32x2(mul_f32x2(x[1], inv2), widen2(wa.y));
+            y[0] = mul_f32x2(mul_f32x2(y[0], inv2), widen2(wb.x));
+            y[1] = mul_f32x2(mul_f32x2(y[1], inv2), widen2(wb.y));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint64_t u = kInterleaved ? swap2(x[e]) : y[e];
+            const uint64_t v = kInterleaved ? swap2(y[e]) : x[e];
+            const uint64_t nx = fma_f32x2(u, sa[e], mul_f32x2(x[e], ca[e]));
+            y[e] = fma_f32x2(v, sb[e], mul_f32x2(y[e], cb[e]));
+            x[e] = nx;
+        }
+        __nv_bfloat16* const dst = is_q ? qd + hh * D : kd + hh * kv_step;
+        *reinterpret_cast<uint2*>(dst + ea) = make_uint2(narrow2(x[0]), narrow2(x[1]));
+        *reinterpret_cast<uint2*>(dst + eb) = make_uint2(narrow2(y[0]), narrow2(y[1]));
+    };
+    bool odd = false;  // a mean square near the ends of fp32's range, or beyond
     for (int h = h0; h < heads; h += kBatch * per_tok) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int hh = h + i * per_tok;
             if (hh >= heads) break;
-            const bool is_q = hh < p.Hq;
-            const bool is_v = hh >= p.Hq + p.Hkv;
-            uint2 oa = ra[i], ob = rb[i];
-            if (!is_v) {
-                uint64_t x[2] = {widen2(oa.x), widen2(oa.y)}, y[2] = {widen2(ob.x), widen2(ob.y)};
-                if (norm) {
-                    float s0, s1;
-                    unpack_f32x2(fma_f32x2(x[0], x[0], fma_f32x2(x[1], x[1],
-                                 fma_f32x2(y[0], y[0], mul_f32x2(y[1], y[1])))), s0, s1);
-                    float ss = s0 + s1;
-#pragma unroll
-                    for (int off = kLanes / 2; off > 0; off >>= 1)
-                        ss += __shfl_xor_sync(gmask, ss, off);
-                    const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-                    const uint64_t inv2 = pack_f32x2(inv, inv);
-                    const uint2 wa = is_q ? wq[0] : wk[0], wb = is_q ? wq[1] : wk[1];
-                    // The norm first: a weight times a large value may overflow.
-                    x[0] = mul_f32x2(mul_f32x2(x[0], inv2), widen2(wa.x));
-                    x[1] = mul_f32x2(mul_f32x2(x[1], inv2), widen2(wa.y));
-                    y[0] = mul_f32x2(mul_f32x2(y[0], inv2), widen2(wb.x));
-                    y[1] = mul_f32x2(mul_f32x2(y[1], inv2), widen2(wb.y));
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint64_t u = kInterleaved ? swap2(x[e]) : y[e];
-                    const uint64_t v = kInterleaved ? swap2(y[e]) : x[e];
-                    const uint64_t nx = fma_f32x2(u, sa[e], mul_f32x2(x[e], ca[e]));
-                    y[e] = fma_f32x2(v, sb[e], mul_f32x2(y[e], cb[e]));
-                    x[e] = nx;
-                }
-                oa = make_uint2(narrow2(x[0]), narrow2(x[1]));
-                ob = make_uint2(narrow2(y[0]), narrow2(y[1]));
+            if (hh >= p.Hq + p.Hkv) {
+                __nv_bfloat16* const dst = vd + hh * kv_step;
+                *reinterpret_cast<uint2*>(dst + ea) = ra[i];
+                *reinterpret_cast<uint2*>(dst + eb) = rb[i];
+                continue;
             }
-            __nv_bfloat16* const dst = is_q ? qd + hh * D : (is_v ? vd : kd) + hh * kv_step;
-            *reinterpret_cast<uint2*>(dst + ea) = oa;
-            *reinterpret_cast<uint2*>(dst + eb) = ob;
+            uint64_t x[2] = {widen2(ra[i].x), widen2(ra[i].y)}, y[2] = {widen2(rb[i].x), widen2(rb[i].y)};
+            float inv = 1.f;
+            if (norm) {
+                const float mean = sum_squares(x, y) * (1.f / D) + p.eps;
+                odd |= !(mean < kMeanMax && mean > kMeanMin);
+                inv = rsqrtf(mean);
+            }
+            finish(hh, x, y, inv);
         }
         if (h + kBatch * per_tok < heads) load(h + kBatch * per_tok);
+    }
+    if (!odd) return;
+    // Rare: such heads again, scaled by a power of two (eps too).
+#pragma unroll 1
+    for (int hh = h0; hh < p.Hq + p.Hkv; hh += per_tok) {
+        const __nv_bfloat16* src = row + static_cast<size_t>(hh) * D;
+        const uint2 a = __ldcg(reinterpret_cast<const uint2*>(src + ea));
+        const uint2 b = __ldcg(reinterpret_cast<const uint2*>(src + eb));
+        uint64_t x[2] = {widen2(a.x), widen2(a.y)}, y[2] = {widen2(b.x), widen2(b.y)};
+        const float mean = sum_squares(x, y) * (1.f / D) + p.eps;
+        if (mean < kMeanMax && mean > kMeanMin) continue;  // as its lanes all find
+        const float by = mean > 1.f ? 0x1p-100f : 0x1p100f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            x[e] = mul_f32x2(x[e], pack_f32x2(by, by));
+            y[e] = mul_f32x2(y[e], pack_f32x2(by, by));
+        }
+        finish(hh, x, y, rsqrtf(sum_squares(x, y) * (1.f / D) + p.eps * by * by));
     }
 }
 

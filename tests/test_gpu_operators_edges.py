@@ -245,3 +245,33 @@ def test_rotation_by_large_frequencies():
     ref = _plain.rope(qkv[:, :2], None, freq, pos, 1e-6, False)  # |n f| < 2^34: exact in fp64
     near(torch.cat([q, k], 1), ref, _plain.rope_bound(ref))
     no_errors()
+
+
+@pytest.mark.parametrize("T", [5, 6500])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("d", [64, 128])
+def test_norm_of_the_largest_and_smallest_heads(T, eps, d):
+    """Heads whose sum of squares leaves fp32's range either way: the norm is the formula's."""
+    g = gen(d)
+    qkv = normal(g, T, 4, d)
+    scales = [3e38 / 8, 1e30, 1e20, 2e-19, 1e-25, 1e-36, 1.0]  # (below 8 standard deviations)
+    for i, s in enumerate(scales):
+        qkv[i::len(scales)] = (qkv[i::len(scales)].double() * s).to(BF)
+    qkv[T - 1, 0, 0], qkv[T - 1, 0, 1:] = 3e38, 1e-38  # one value counts
+    qkv[T - 2, 0] = 0.0
+    qkv[T - 2, 1, 0] = 2e-39  # subnormal
+    qkv[T - 2, 1, 1:] = 0.0
+    w = normal(g, d)
+    f = torch.full((d // 2,), 0.5, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    q = torch.empty(T, 2, d, dtype=BF, device="cuda")
+    k, v = (torch.empty(T, 1, d, dtype=BF, device="cuda") for _ in range(2))
+    lf.qk_norm_rope(qkv, w, w, f, pos, q, k, v, eps)
+    ref = _plain.rope(qkv[:, :3], w, f, pos, eps, False)
+    got = torch.cat([q, k], 1)
+    if eps == 0.0:  # 0 / 0
+        assert torch.isnan(got[T - 2, 0]).all() and torch.isnan(ref[T - 2, 0]).all()
+        got[T - 2, 0], ref[T - 2, 0] = 0, 0
+    # (Results below fp32's normal range are rounded to its steps.)
+    near(got, ref, _plain.rope_bound(ref) + 2.0 ** -126)
+    no_errors()
