@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <limits>
 #include <map>
 #include <mutex>
 #include <new>
@@ -834,10 +835,11 @@ lf_status run_attention(lf::AttnParams p, int d, float scale, int dev, cudaStrea
     const int units = p.N * p.Hkv;
     if ((st = encode_cache_map(&tmK, const_cast<__nv_bfloat16*>(p.k), d, p.S, units)) != LF_OK) return st;
     if ((st = encode_cache_map(&tmV, const_cast<__nv_bfloat16*>(p.v), d, p.S, units)) != LF_OK) return st;
-    // Not 0: the kernel multiplies masked logits (-inf) by it. Any logit below
-    // 1e-6 in magnitude weighs like 0.
+    // Not 0: the kernel multiplies masked logits (-inf) by it. With the smallest
+    // positive float any finite logit weighs like 0.
     p.scale_log2 = std::max(
-        static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634), 1e-30f);
+        static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634),
+        std::numeric_limits<float>::denorm_min());
     p.negate = scale < 0.f;
     // A warp that computes rows again key by key keeps the others waiting: 2.9 us
     // (d = 64) or 4.8 us (d = 128) for a key of its 32 rows, measured with every

@@ -275,3 +275,17 @@ def test_norm_of_the_largest_and_smallest_heads(T, eps, d):
     # (Results below fp32's normal range are rounded to its steps.)
     near(got, ref, _plain.rope_bound(ref) + 2.0 ** -126)
     no_errors()
+
+
+@pytest.mark.parametrize("scale,size", [(0.0, 1e17), (0.0, 1.0), (3e-33, 1e16), (-3e-33, 1e16), (1e-36, 1e17)])
+@pytest.mark.parametrize("T,kv", [(1, 700), (200, 400)])
+def test_scales_near_zero(scale, size, T, kv):
+    """Queries and keys as large as bf16 holds them: a scale near zero is that scale."""
+    g = gen(T + kv)
+    q, k, v = normal(g, T, 4, 64), normal(g, 1, 2, kv, 64), normal(g, 1, 2, kv, 64)
+    q, k = (q.double() * size).to(BF), (k.double() * size).to(BF)
+    out = torch.empty_like(q)
+    lf.window_attention(q, k, v, ints([0, T]), ints([kv]), out, 150, 3, scale)
+    ref, tol = _plain.window_rows(q, k, v, [0, T], [kv], 150, 3, scale)
+    near(out, ref, tol)
+    no_errors()
