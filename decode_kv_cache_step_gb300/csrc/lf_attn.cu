@@ -327,7 +327,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint6
 // One warp: the sequence and rows of query tile x, and its part of the K/V
 // tiles. Sequence b's tiles start at index floor(q_start[b] / tok) + b: enough
 // for its rows wherever they start, so no prefix sum over the sequences is
-// needed. False where the tile holds no rows.
+// needed. False where the tile holds no rows (report_sequence tells why).
 __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int2 work, Item* it) {
     const int lane = threadIdx.x & 31;
     // The last tiles (the longest rows of a causal prompt) come first, a
@@ -355,10 +355,7 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int2 work, It
     r.q0 = __shfl_sync(0xffffffffu, r.q0, top);
     r.n = __shfl_sync(0xffffffffu, r.n, top);
     r.kv = __shfl_sync(0xffffffffu, r.kv, top);
-    if (!__shfl_sync(0xffffffffu, good, top)) {
-        if (lane == 0) atomicOr(p.dev_err, kErrBadLength);
-        return false;
-    }
+    if (!__shfl_sync(0xffffffffu, good, top)) return false;
     const int rel = (x - (r.q0 >> pl.tok_shift) - b) << pl.tok_shift;
     if (rel < 0 || rel >= r.n) return false;
     it->seq = b;
@@ -385,6 +382,16 @@ __device__ bool find_item(const AttnParams& p, const AttnPlan& pl, int2 work, It
     it->split = work.y;
     it->stop = 0;
     return true;
+}
+
+// One thread: reports sequence work.x if it does not fit. There are at least as
+// many items as sequences, and the search above may miss a sequence whose rows
+// end before they start.
+__device__ __forceinline__ void report_sequence(const AttnParams& p, int2 work) {
+    SeqRange r;
+    if (work.y == 0 && work.x < p.N &&
+        !seq_range(p.q_start, p.kv_len, work.x, p.T, p.S, p.causal, &r))
+        atomicOr(p.dev_err, kErrBadLength);
 }
 
 // Stores 64 bytes of each lane's row (v: the lane's own row) at byte `off` of
@@ -734,6 +741,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bool ok = true;
             Item it = it0;
             it.stop = found0 ? 0 : -1;  // -1: no rows there, ask again
+            int2 work = make_int2(blockIdx.x, blockIdx.y);
             for (int round = 0;; ++round) {
                 if (it.stop >= 0) {
                     const int slot = w % kItemSlots;
@@ -768,10 +776,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) {
                     mbar_arrive_expect_tx(next, 16);
                     cancel_next_cta(smem + L::kNextOff, next);
+                    report_sequence(p, work);  // under the answer's round trip
                 }
                 ok = warp_wait(next, round & 1);
                 if (!ok) break;
-                const int2 work = cancelled_cta(smem + L::kNextOff);
+                work = cancelled_cta(smem + L::kNextOff);
                 fence_proxy_async_smem();  // the answer is read before the next one lands
                 __syncwarp();
                 if (work.x < 0)

@@ -289,3 +289,26 @@ def test_scales_near_zero(scale, size, T, kv):
     ref, tol = _plain.window_rows(q, k, v, [0, T], [kv], 150, 3, scale)
     near(out, ref, tol)
     no_errors()
+
+
+@pytest.mark.parametrize("Hq,Hkv,N", [(8, 1, 3), (1, 1, 3), (4, 2, 70)])
+def test_row_starts_that_do_not_ascend_are_reported(Hq, Hkv, N):
+    """A sequence that ends before it starts, behind whose start no later one lies: it has no rows
+    to skip, and is reported all the same."""
+    g = gen(N)
+    T, S, d = 4000, 3904, 64
+    q, k, v = normal(g, T, Hq, d), normal(g, N, Hkv, S, d), normal(g, N, Hkv, S, d)
+    starts, lens = [0, 3900] + [3] * (N - 1), [3900] + [5] * (N - 1)
+    out = torch.full_like(q, 7.0)
+    lf.window_attention(q, k, v, ints(starts), ints(lens), out, 60, 0, 0.125)
+    assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_LENGTH
+    assert (out[3900:] == 7).all()
+    lf.window_attention(q, k, v, ints([0] + [3900] * N), ints(lens), out, 60, 0, 0.125)
+    no_errors()
+    B = 40
+    ws = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    mask = torch.zeros(B, Hkv, 70, dtype=torch.int32, device="cuda")
+    own, nk = normal(g, B, Hkv, 70, d), normal(g, B, Hkv, d)
+    lf.decode_attention_prefix(q[:B], own, own, mask, nk, nk, ws, k, v, ints([0, 39] + [3] * (N - 1)),
+                               ints([100] * N), out[:B], 0.125)
+    assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_LENGTH
