@@ -11,6 +11,7 @@ import _plain
 from test_gpu_operators import BF, gen, ints, near, no_errors, normal
 
 pytestmark = pytest.mark.gpu
+F64 = torch.float64
 
 
 @pytest.mark.parametrize("B,Hkv,S,P,live", [(2250, 8, 2112, 300, 0), (2250, 8, 2112, 300, 3), (64, 8, 2400, 300, 0),
@@ -312,3 +313,107 @@ def test_row_starts_that_do_not_ascend_are_reported(Hq, Hkv, N):
     lf.decode_attention_prefix(q[:B], own, own, mask, nk, nk, ws, k, v, ints([0, 39] + [3] * (N - 1)),
                                ints([100] * N), out[:B], 0.125)
     assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_LENGTH
+
+
+def marked(kv, d, part):
+    """Values that count keys: 64 keys in turn mark each column, from key part * 64 * d on. [kv, d]"""
+    j = torch.arange(kv)
+    rel = j - part * 64 * d
+    v = torch.zeros(kv, d, dtype=torch.float64)
+    inside = (rel >= 0) & (rel < 64 * d)
+    v[j[inside], rel[inside] % d] = 1
+    return v
+
+
+def seen_marks(v, T, kv, window, sinks):
+    """How many keys that mark column c each of the last T rows sees, and how many keys at all."""
+    c = torch.cat([torch.zeros(1, v.shape[1], dtype=F64), v.cumsum(0)])
+    pos = torch.arange(kv - T, kv)
+    lo = (pos + 1 - window).clamp(min=0) if window else torch.zeros(T, dtype=torch.long)
+    first = lo.clamp(max=sinks)
+    return c[pos + 1] - c[lo] + c[first], pos + 1 - lo + first
+
+
+@pytest.mark.parametrize("T,kv,window,sinks,Hq,Hkv,d", [
+    (1500, 1500, 0, 0, 4, 1, 128), (700, 3000, 1000, 16, 4, 2, 64), (1, 20000, 0, 0, 8, 2, 128),
+    (1, 9000, 4096, 4, 4, 2, 64), (20, 5000, 0, 0, 8, 1, 64), (1, 16384, 4096, 100, 32, 8, 128),
+    (3000, 3001, 1024, 4, 1, 1, 128), (130, 7777, 999, 333, 8, 8, 64), (9000, 9000, 0, 0, 8, 8, 64)])
+def test_every_key_counts_once(T, kv, window, sinks, Hq, Hkv, d):
+    """Queries of zero weigh all keys they see alike, so an output times the number of keys seen is
+    a count of marked keys: at most 64 a column, which bf16's half step of 2^-8 (a quarter of a
+    key) and fp32's sums tell apart exactly. Every row, every column, every key."""
+    q = torch.zeros(T, Hq, d, dtype=BF, device="cuda")
+    k = normal(gen(kv), 1, Hkv, kv, d)
+    out = torch.empty_like(q)
+    starts, lens = ints([0, T]), ints([kv])
+    for part in range(-(-kv // (64 * d))):
+        v = marked(kv, d, part)
+        lf.window_attention(q, k, v.to(BF).cuda().expand(1, Hkv, kv, d).contiguous(), starts, lens, out, window,
+                            sinks, 0.125)
+        want, n = seen_marks(v, T, kv, window, sinks)
+        got = (out.double().cpu() * n[:, None, None]).round()
+        assert torch.equal(got, want[:, None].expand(T, Hq, d)), f"part {part}"
+    no_errors()
+
+
+@pytest.mark.parametrize("B,starts,plen,P,S,live", [
+    (1, [0, 1], [20000], 20000, 300, 100), (40, [0, 40], [5003], 5003, 700, 650), (67, [0, 30, 60, 67], [5003, 0, 3001], 5003, 2400, 1999),
+    (3, [0, 3], [129], 200, 9000, 8999)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 1, 128), (4, 4, 64)])
+def test_every_key_of_prefix_and_cache_counts_once(B, starts, plen, P, S, live, Hq, Hkv, d):
+    q = torch.zeros(B, Hq, d, dtype=BF, device="cuda")
+    N = len(plen)
+    k, kp = torch.zeros(B, Hkv, S, d, dtype=BF, device="cuda"), torch.zeros(N, Hkv, P, d, dtype=BF, device="cuda")
+    nk = torch.zeros(B, Hkv, d, dtype=BF, device="cuda")
+    write = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    mask = torch.full((B, Hkv, S), -1, dtype=torch.int32, device="cuda")
+    mask[:, :, S - live:] = 3
+    out = torch.empty_like(q)
+    for part in range(-(-max(P, S) // (64 * d))):
+        vp, v = marked(P, d, part), marked(S, d, part)
+        # the cache marks the upper half of the columns, the prefix the lower
+        vp[:, d // 2:], v[:, :d // 2] = 0, 0
+        lf.decode_attention_prefix(q, k, v.to(BF).cuda().expand(B, Hkv, S, d).contiguous(), mask, nk, nk, write, kp,
+                                   vp.to(BF).cuda().expand(N, Hkv, P, d).contiguous(), ints(starts), ints(plen), out,
+                                   0.125)
+        got = out.double().cpu()
+        for b in range(B):
+            n = plen[next(i for i in range(N) if starts[i] <= b < starts[i + 1])]
+            want = vp[:n].sum(0) + v[S - live:].sum(0)
+            assert torch.equal((got[b] * (n + live)).round(), want.expand(Hq, d)), f"sequence {b} part {part}"
+    no_errors()
+
+
+@pytest.mark.parametrize("S,P", [(8300, 3000), (2400, 700)])
+def test_captured_step_with_a_prefix(S, P):
+    """The step with its scoring kernel, and without, captured and replayed token by token: what
+    the same calls give one by one."""
+    g = gen(S)
+    B, Hq, Hkv, d = 3, 8, 2, 64
+    q, nk = normal(g, B, Hq, d), normal(g, B, Hkv, d)
+    k, v = normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    kp, vp = normal(g, 2, Hkv, P, d), normal(g, 2, Hkv, P, d)
+    mask = torch.randint(-30, 200, (B, Hkv, S), generator=g, dtype=torch.int32).clamp_(min=-1).cuda()
+    starts, plen = ints([0, 2, 3]), ints([P, P // 3])
+
+    def state():
+        return dict(k=k.clone(), v=v.clone(), m=mask.clone(), ws=torch.zeros(B, Hkv, dtype=torch.int32, device="cuda"),
+                    nx=torch.zeros(B, Hkv, dtype=torch.int32, device="cuda"), out=torch.zeros_like(q))
+
+    def token(s):
+        lf.decode_step_prefix(q, s["k"], s["v"], s["m"], nk, nk, s["ws"], kp, vp, starts, plen, s["out"], s["nx"], 5,
+                              0.125)
+        s["ws"].copy_(s["nx"])
+
+    eager, graph = state(), state()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        token(graph)
+        token(graph)
+    for _ in range(4):
+        token(eager)
+        token(eager)
+        gr.replay()
+        for x in eager:
+            assert torch.equal(eager[x], graph[x]), x
+    no_errors()
