@@ -529,7 +529,8 @@ def window_attention(q, k_cache, v_cache, q_start, kv_len, out, window, sinks, s
     """lf_window_attention: packed rows q [T,Hq,d] over in-order caches
     [B,Hkv,S,d]; a token sees its last `window` keys (0: all) and the first
     `sinks`. workspace: uint8 of window_attention_workspace bytes (None: taken
-    from torch's allocator)."""
+    from torch's allocator; bring one to a capture that torch.cuda.graph does
+    not make)."""
     lib = load_library()
     if not isinstance(q, torch.Tensor) or not isinstance(k_cache, torch.Tensor):
         raise TypeError("q and k_cache: expected torch.Tensors")

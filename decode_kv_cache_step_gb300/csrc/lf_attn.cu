@@ -51,16 +51,17 @@
 // share of the softmax that the step's slots, outputs and scores see.
 //
 // What bounds it, and what it measured (32 query and 8 KV heads of 128):
-//   a causal prompt of 16384 tokens 1.56 ms, 1406 TFLOP/s, at the board's
-//   power limit; the same pipeline without its softmax arithmetic takes
-//   1.33 ms, the sustained rate of a large plain matrix product would be
-//   1.27 ms (1726 TFLOP/s);
-//   eight prompts of 1200 to 2400 tokens, window 1024: 183 us, 900 TFLOP/s
+//   a causal prompt of 16384 tokens 1.49 ms, 1470 TFLOP/s, and 1.56 ms a call in
+//   a loop of seconds, where the board's power cap takes the clock from 2.07 to
+//   1.96 GHz. The softmax warps' arithmetic: without the weights' sum it takes
+//   1.32 ms, without any arithmetic 1.33, and 1.27 ms would be the sustained
+//   rate of a large plain matrix product (1726 TFLOP/s);
+//   eight prompts of 1200 to 2400 tokens, window 1024: 174 us, 947 TFLOP/s
 //   of visible pairs; 9 tiles are worked for 8 tiles' worth of pairs, and a
 //   tile with a mask costs about 1.5 times one without;
-//   128 single tokens, window 1024: 94 us, 5.6 TB/s (the loads, in halves of
+//   128 single tokens, window 1024: 92 us, 5.7 TB/s (the loads, in halves of
 //   64 keys, are 4.5% more than the keys seen); 32 single tokens over 16384
-//   keys each: 313 us, 6.86 TB/s, the measured copy rate.
+//   keys each: 312 us, 6.88 TB/s, the measured copy rate.
 //
 // Keys a row does not see are removed by select before the exponentials, and
 // what a V tile holds behind the range's last key is zeroed in shared memory,

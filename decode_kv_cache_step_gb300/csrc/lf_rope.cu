@@ -18,8 +18,8 @@
 // bits (fp64 would take 1000 cycles of an SM's fp64 unit per CTA).
 //
 // Measured (32 query, 8 KV heads of 128): 20.3K prompt tokens into their
-// caches 80.5 us, 6.2 TB/s read and written, 92% of the measured copy rate (82.8
-// with loads marked evict-first); one token 3.0 us, 128 tokens 3.4 us, which is
+// caches 81 us, 6.2 TB/s read and written, 91% of the measured copy rate (2 us
+// more with loads marked evict-first); one token 2.9 us, 128 tokens 3.5 us, which is
 // the latency of a launch and three dependent round trips.
 #include <stdlib.h>
 

@@ -324,6 +324,8 @@ lf_status lf_device_errors(void* stream, uint32_t* flags, int clear);
  * (q_start not ascending or outside [0, T], a length outside [0, S], more
  * rows than tokens) is skipped and raises LF_DEVERR_BAD_LENGTH.
  *
+ * Every size is at least 1: a batch without rows needs no call.
+ *
  * lf_qk_norm_rope: head norms and rotation of single tokens.
  *
  * qkv        in  bf16 [T] rows of (Hq + 2 Hkv) heads of d (queries, keys,
@@ -386,7 +388,7 @@ lf_status lf_prefill_append(const void* qkv, int64_t qkv_stride, const void* q_w
  * Slots from kv_len[b] on, and keys a row does not see, may hold anything
  * (NaN and infinities included) without changing the row. (A value that is
  * not finite in a key that some rows of a tile see costs all of them a slower
- * second pass.) A row without a visible key, or with every logit -infinity,
+ * second pass, key by key.) A row without a visible key, or with every logit -infinity,
  * is zero.
  */
 lf_status lf_window_attention(const void* q, const void* k_cache, const void* v_cache,
