@@ -1,5 +1,12 @@
 """The prompt and shared-prefix operators where it is easy to go wrong: against their plain
-fp64 definitions (tests/_plain.py, which also derives the bounds)."""
+fp64 definitions (tests/_plain.py, which also derives the bounds).
+
+The attention divides by the sum of the rounded weights, so that rounding weight j by e_j <= 2^-8 of
+it moves an output o by sum_j p_j e_j (v_j - o): at most 2^-8 * sum_j p_j |v_j - o|, with 2^-8 * |o|
+for the output's own rounding. That is 0 where one key has the weight or all values are alike, and
+exceeds _plain's 2^-8 * sum_j p_j |v_j| only where a few sharp weights add up values unlike the
+output; the weights here are spread, or the test says what it allows.
+"""
 import math
 
 import pytest
