@@ -12,12 +12,15 @@ workloads (``workloads``).
 from ._binding import (  # noqa: F401
     EXPORTED, KERNEL_NAMES, LF_DEVERR_BAD_LENGTH, LF_DEVERR_BAD_WRITE_SLOT, LF_DEVERR_WAIT_TIMEOUT,
     LF_ERR_CUDA, LF_ERR_INVALID_ARG, LF_ERR_NO_MEMORY, LF_ERR_UNSUPPORTED,
-    LF_KERNEL_ATTENTION, LF_KERNEL_DECODE_STEP, LF_KERNEL_NORM_ROPE, LF_KERNEL_PACKED_ATTENTION,
-    LF_KERNEL_SCORE, LF_MAX_TOPK, LF_OK,
+    LF_KERNEL_ATTENTION, LF_KERNEL_DECODE_STEP, LF_KERNEL_KV4, LF_KERNEL_NORM_ROPE,
+    LF_KERNEL_PACKED_ATTENTION, LF_KERNEL_PROMPT_WEIGHTS, LF_KERNEL_SCORE, LF_MAX_AXES, LF_MAX_TOPK,
+    LF_OK,
     LF_STEP_FILL_EMPTY_FIRST, LF_STEP_LOG2_SCORES, LF_STEP_MASK_EVICTED, LFError, PreparedStep,
-    decode_attention, decode_attention_prefix, decode_prefix_workspace,
-    decode_step, decode_step_ex,
+    decode_attention, decode_attention_kv4, decode_attention_prefix, decode_kv4_workspace,
+    decode_prefix_workspace, decode_step, decode_step_ex,
     decode_step_host, decode_step_noalloc, decode_step_prefix,
-    decode_step_scores, device_errors, library_path, load_library, prefill_append,
-    profile_collect, profile_enable, qk_norm_rope, release_workspace, status_string, step_plan,
+    decode_step_scores, decode_step_weights, decode_weights_workspace, device_errors, kv4_pack,
+    kv4_unpack, library_path, load_library, prefill_append, prefill_append_axes,
+    profile_collect, profile_enable, prompt_weights, prompt_weights_workspace, qk_norm_rope,
+    qk_norm_rope_axes, release_workspace, status_string, step_plan,
     version, window_attention, window_attention_workspace)

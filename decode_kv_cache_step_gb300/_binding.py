@@ -32,16 +32,21 @@ LF_KERNEL_ATTENTION = 1
 LF_KERNEL_SCORE = 2
 LF_KERNEL_NORM_ROPE = 3
 LF_KERNEL_PACKED_ATTENTION = 4
+LF_KERNEL_KV4 = 5
+LF_KERNEL_PROMPT_WEIGHTS = 6
 KERNEL_NAMES = {LF_KERNEL_DECODE_STEP: "lf_decode_step_kernel",
                 LF_KERNEL_ATTENTION: "lf_decode_step_kernel (attention-only variant)",
                 LF_KERNEL_SCORE: "lf_score_kernel",
                 LF_KERNEL_NORM_ROPE: "lf_rope_kernel",
-                LF_KERNEL_PACKED_ATTENTION: "lf_attn_kernel"}
+                LF_KERNEL_PACKED_ATTENTION: "lf_attn_kernel",
+                LF_KERNEL_KV4: "lf_kv4_pack_kernel, lf_kv4_unpack_kernel, lf_kv4_attn_kernel",
+                LF_KERNEL_PROMPT_WEIGHTS: "lf_prompt_weights_kernel"}
 
 LF_STEP_FILL_EMPTY_FIRST = 0x1
 LF_STEP_MASK_EVICTED = 0x2
 LF_STEP_LOG2_SCORES = 0x4
 LF_MAX_TOPK = 1024
+LF_MAX_AXES = 4
 
 # Every exported symbol of include/lf_decode.h.
 EXPORTED = (
@@ -51,6 +56,9 @@ EXPORTED = (
     "lf_qk_norm_rope", "lf_prefill_append", "lf_window_attention",
     "lf_window_attention_workspace", "lf_decode_step_prefix", "lf_decode_attention_prefix",
     "lf_decode_prefix_workspace",
+    "lf_qk_norm_rope_axes", "lf_prefill_append_axes", "lf_decode_step_weights",
+    "lf_decode_weights_workspace", "lf_prompt_weights", "lf_prompt_weights_workspace",
+    "lf_kv4_pack", "lf_kv4_unpack", "lf_decode_attention_kv4", "lf_decode_kv4_workspace",
     "lf_profile_enable", "lf_profile_collect", "lf_release_workspace", "lf_status_string",
     "lf_last_error", "lf_version",
 )
@@ -118,9 +126,24 @@ def load_library(path: str | None = None):
         lib.lf_decode_step_prefix.argtypes = [P] * 13 + [I, I, P] + [I] * 8 + [F, P, Z, P]
         lib.lf_decode_attention_prefix.argtypes = [P] * 12 + [I] * 7 + [F, P, Z, P]
         lib.lf_decode_prefix_workspace.argtypes = [I] * 7 + [ctypes.POINTER(Z)]
+        lib.lf_qk_norm_rope_axes.argtypes = [P, L] + [P] * 4 + [ctypes.c_char_p, I] + [P] * 3 + [I] * 6 + [F, P]
+        lib.lf_prefill_append_axes.argtypes = ([P, L] + [P] * 6 + [ctypes.c_char_p, I] + [P] * 4
+                                               + [I] * 8 + [F, P])
+        lib.lf_decode_step_weights.argtypes = [P] * 10 + [I] * 8 + [F, F, P, Z, P]
+        lib.lf_decode_weights_workspace.argtypes = [I] * 6 + [ctypes.POINTER(Z)]
+        lib.lf_prompt_weights.argtypes = [P] * 5 + [I] * 7 + [F, P, Z, P]
+        lib.lf_prompt_weights_workspace.argtypes = [I] * 7 + [ctypes.POINTER(Z)]
+        lib.lf_kv4_pack.argtypes = [P] * 9 + [I] * 5 + [P]
+        lib.lf_kv4_unpack.argtypes = [P] * 8 + [I] * 5 + [P]
+        lib.lf_decode_attention_kv4.argtypes = [P] * 10 + [I] * 5 + [F, P, Z, P]
+        lib.lf_decode_kv4_workspace.argtypes = [I] * 5 + [ctypes.POINTER(Z)]
         for fn in (lib.lf_qk_norm_rope, lib.lf_prefill_append, lib.lf_window_attention,
                    lib.lf_window_attention_workspace, lib.lf_decode_step_prefix,
-                   lib.lf_decode_attention_prefix, lib.lf_decode_prefix_workspace):
+                   lib.lf_decode_attention_prefix, lib.lf_decode_prefix_workspace,
+                   lib.lf_qk_norm_rope_axes, lib.lf_prefill_append_axes,
+                   lib.lf_decode_step_weights, lib.lf_decode_weights_workspace,
+                   lib.lf_prompt_weights, lib.lf_prompt_weights_workspace, lib.lf_kv4_pack,
+                   lib.lf_kv4_unpack, lib.lf_decode_attention_kv4, lib.lf_decode_kv4_workspace):
             fn.restype = I
         lib.lf_device_errors.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), I]
         lib.lf_device_errors.restype = I
@@ -509,6 +532,69 @@ def prefill_append(qkv, q_weight, k_weight, inv_freq, q_start, kv_len, q_out, k_
             int(bool(interleaved)), float(eps), _call_stream(stream, qkv.device)))
 
 
+def _check_axes(positions, pair_axis, T, rot):
+    """(axes, the pairs' axes as bytes)."""
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 2:
+        raise ValueError("positions must be [axes,T]")
+    _need(positions, "positions", torch.int32, (positions.shape[0], T), True)
+    if isinstance(pair_axis, torch.Tensor) and pair_axis.is_cuda:
+        raise ValueError("pair_axis: must be on the host")
+    try:
+        pairs = bytes(int(a) for a in pair_axis)
+    except (TypeError, ValueError) as e:
+        raise ValueError(f"pair_axis: expected rot/2 axes, {e}") from None
+    if len(pairs) != rot // 2:
+        raise ValueError(f"pair_axis: {len(pairs)} entries, expected {rot // 2}")
+    return int(positions.shape[0]), pairs
+
+
+def qk_norm_rope_axes(qkv, q_weight, k_weight, inv_freq, positions, pair_axis, q_out, k_out, v_out,
+                      eps=1e-6, interleaved=False, stream=None):
+    """lf_qk_norm_rope_axes: qk_norm_rope with a position on each of several axes,
+    positions [axes,T] int32. pair_axis: the axis of each rotated pair, rot/2
+    integers on the host (a list, bytes or CPU tensor)."""
+    lib = load_library()
+    if not isinstance(k_out, torch.Tensor) or k_out.dim() != 3:
+        raise ValueError("k_out must be [T,Hkv,d]")
+    Hkv = int(k_out.shape[1])
+    T, Hq, d, rot, stride = _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv)
+    axes, pairs = _check_axes(positions, pair_axis, T, rot)
+    bf = torch.bfloat16
+    _need(k_out, "k_out", bf, (T, Hkv, d), True)
+    _need(v_out, "v_out", bf, (T, Hkv, d), True)
+    with _on_device(qkv.device, q_weight, k_weight, inv_freq, positions, q_out, k_out, v_out):
+        _check(lib, lib.lf_qk_norm_rope_axes(
+            qkv.data_ptr(), stride, _ptr(q_weight), _ptr(k_weight), inv_freq.data_ptr(),
+            positions.data_ptr(), pairs, axes, q_out.data_ptr(), k_out.data_ptr(),
+            v_out.data_ptr(), T, Hq, Hkv, d, rot, int(bool(interleaved)), float(eps),
+            _call_stream(stream, qkv.device)))
+
+
+def prefill_append_axes(qkv, q_weight, k_weight, inv_freq, q_start, kv_len, positions, pair_axis,
+                        q_out, k_cache, v_cache, mask, eps=1e-6, interleaved=False, stream=None):
+    """lf_prefill_append_axes: prefill_append with the rotation's positions given per
+    row and axis, positions [axes,T] int32 (slots still follow q_start and kv_len)."""
+    lib = load_library()
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be [B,Hkv,S,d]")
+    B, Hkv, S, _ = k_cache.shape
+    T, Hq, d, rot, stride = _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv)
+    axes, pairs = _check_axes(positions, pair_axis, T, rot)
+    bf, i32 = torch.bfloat16, torch.int32
+    _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
+    _need(v_cache, "v_cache", bf, (B, Hkv, S, d), True)
+    _need(mask, "mask", i32, (B, Hkv, S), True)
+    _need(q_start, "q_start", i32, (B + 1,), True)
+    _need(kv_len, "kv_len", i32, (B,), True)
+    with _on_device(qkv.device, q_weight, k_weight, inv_freq, q_start, kv_len, positions, q_out,
+                    k_cache, v_cache, mask):
+        _check(lib, lib.lf_prefill_append_axes(
+            qkv.data_ptr(), stride, _ptr(q_weight), _ptr(k_weight), inv_freq.data_ptr(),
+            q_start.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), pairs, axes,
+            q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(), T, B, Hq,
+            Hkv, d, S, rot, int(bool(interleaved)), float(eps), _call_stream(stream, qkv.device)))
+
+
 def window_attention_workspace(T, B, Hq, Hkv, d, S, window=0, sinks=0) -> int:
     """Workspace bytes of window_attention for these sizes on the current device."""
     lib = load_library()
@@ -635,6 +721,177 @@ def decode_step_prefix(q, k_cache, v_cache, mask, new_k, new_v, write_slot, k_pr
             next_slots.data_ptr(), 1 if k is None else int(k), int(flags),
             None if scores is None else scores.data_ptr(), B, Hq, Hkv, d, S, N, P, int(W),
             float(scale), ws.data_ptr(), ws.numel(), _call_stream(stream, q.device)))
+
+
+def decode_weights_workspace(B, Hq, Hkv, d, S, k=1) -> int:
+    """Workspace bytes of decode_step_weights for these sizes on the current device."""
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib, lib.lf_decode_weights_workspace(int(B), int(Hq), int(Hkv), int(d), int(S), int(k),
+                                                ctypes.byref(n)))
+    return int(n.value)
+
+
+# The size is a function of the sizes, the device and the plan's switches alone.
+_PLAN_SWITCHES = ("LF_CHUNK_TILES", "LF_STAGES", "LF_CLUSTER", "LF_CLUSTER_MAX", "LF_DEEP")
+_weights_bytes = functools.lru_cache(maxsize=1024)(
+    lambda index, switches, *sizes: decode_weights_workspace(*sizes))
+
+
+def decode_step_weights(q, k_cache, v_cache, mask, weights, new_k, new_v, write_slot, out,
+                        next_slots, W, scale, decay=1.0, k=None, flags=0, workspace=None,
+                        stream=None):
+    """lf_decode_step_weights: the decode step that adds the token's attention weights
+    to weights [B,Hkv,S] fp32 (decay * old + new) and returns the slots with the
+    least. next_slots [B,Hkv] (k None: the argmin) or [B,Hkv,k]."""
+    lib = load_library()
+    B, Hq, Hkv, d, S = _check_step(q, k_cache, v_cache, mask, new_k, new_v, write_slot, out,
+                                   next_slots, k=k)
+    _need(weights, "weights", torch.float32, (B, Hkv, S), True)
+    topk = 1 if k is None else int(k)
+    with _on_device(q.device, k_cache, v_cache, mask, weights, new_k, new_v, write_slot, out,
+                    next_slots):
+        ws = _workspace(workspace, 0 if workspace is not None else
+                        _weights_bytes(q.device.index, tuple(map(os.environ.get, _PLAN_SWITCHES)),
+                                       B, Hq, Hkv, d, S, topk), q.device, stream)
+        _check(lib, lib.lf_decode_step_weights(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(),
+            weights.data_ptr(), new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(),
+            out.data_ptr(), next_slots.data_ptr(), topk, int(flags), B, Hq, Hkv, d, S, int(W),
+            float(scale), float(decay), ws.data_ptr(), ws.numel(), _call_stream(stream, q.device)))
+
+
+def prompt_weights_workspace(T, B, Hq, Hkv, d, S, rows=0) -> int:
+    """Workspace bytes of prompt_weights for these sizes on the current device."""
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib, lib.lf_prompt_weights_workspace(int(T), int(B), int(Hq), int(Hkv), int(d), int(S),
+                                                int(rows), ctypes.byref(n)))
+    return int(n.value)
+
+
+# The size is a function of the sizes and the device alone.
+_prompt_bytes = functools.lru_cache(maxsize=1024)(
+    lambda index, *sizes: prompt_weights_workspace(*sizes))
+
+
+def prompt_weights(q, k_cache, q_start, kv_len, weights, scale, rows=0, workspace=None, stream=None):
+    """lf_prompt_weights: the causal attention weights that the last `rows` rows (0:
+    all) of each sequence give its keys, into weights [B,Hkv,S] fp32 (set for this
+    call's tokens, added for earlier ones): decode_step_weights' start."""
+    lib = load_library()
+    if not isinstance(q, torch.Tensor) or not isinstance(k_cache, torch.Tensor):
+        raise TypeError("q and k_cache: expected torch.Tensors")
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [T,Hq,d] and k_cache [B,Hkv,S,d]")
+    T, Hq, d = q.shape
+    B, Hkv, S, _ = k_cache.shape
+    bf, i32 = torch.bfloat16, torch.int32
+    _need(q, "q", bf, (T, Hq, d), True)
+    _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
+    _need(q_start, "q_start", i32, (B + 1,), True)
+    _need(kv_len, "kv_len", i32, (B,), True)
+    _need(weights, "weights", torch.float32, (B, Hkv, S), True)
+    with _on_device(q.device, k_cache, q_start, kv_len, weights):
+        ws = _workspace(workspace, 0 if workspace is not None else
+                        _prompt_bytes(q.device.index, T, B, Hq, Hkv, d, S, int(rows)), q.device, stream)
+        _check(lib, lib.lf_prompt_weights(
+            q.data_ptr(), k_cache.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+            weights.data_ptr(), T, B, Hq, Hkv, d, S, int(rows), float(scale), ws.data_ptr(),
+            ws.numel(), _call_stream(stream, q.device)))
+
+
+def _check_kv4(k4, k_scale, v4, v_scale):
+    """(B, Hkv, S, d) of a 4-bit cache's arrays."""
+    if not isinstance(k4, torch.Tensor) or k4.dim() != 4:
+        raise ValueError("k4 must be [B,Hkv,S,d/2]")
+    B, Hkv, S, half = (int(x) for x in k4.shape)
+    d = 2 * half
+    u8, bf = torch.uint8, torch.bfloat16
+    _need(k4, "k4", u8, (B, Hkv, S, half), True)
+    _need(v4, "v4", u8, (B, Hkv, S, half), True)
+    _need(k_scale, "k_scale", bf, (B, Hkv, S, d // 32), True)
+    _need(v_scale, "v_scale", bf, (B, Hkv, S, d // 32), True)
+    return B, Hkv, S, d
+
+
+def _check_kv4_slots(k_cache, v_cache, kv_from, kv_len, B, Hkv, d):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be [B,Hkv,P,d]")
+    P = int(k_cache.shape[2])
+    bf, i32 = torch.bfloat16, torch.int32
+    _need(k_cache, "k_cache", bf, (B, Hkv, P, d), True)
+    _need(v_cache, "v_cache", bf, (B, Hkv, P, d), True)
+    _need(kv_len, "kv_len", i32, (B,), True)
+    if kv_from is not None:
+        _need(kv_from, "kv_from", i32, (B,), True)
+    return P
+
+
+def kv4_pack(k_cache, v_cache, kv_from, kv_len, k4, k_scale, v4, v_scale, mask, stream=None):
+    """lf_kv4_pack: slots kv_from[b]..kv_len[b] (kv_from None: from 0) of bf16 caches
+    [B,Hkv,P,d] into a 4-bit cache: k4, v4 uint8 [B,Hkv,S,d/2], k_scale, v_scale
+    bf16 [B,Hkv,S,d/32]; mask [B,Hkv,S] gets the ages of an in-order cache."""
+    lib = load_library()
+    B, Hkv, S, d = _check_kv4(k4, k_scale, v4, v_scale)
+    P = _check_kv4_slots(k_cache, v_cache, kv_from, kv_len, B, Hkv, d)
+    _need(mask, "mask", torch.int32, (B, Hkv, S), True)
+    with _on_device(k4.device, k_scale, v4, v_scale, k_cache, v_cache, kv_from, kv_len, mask):
+        _check(lib, lib.lf_kv4_pack(
+            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_from), kv_len.data_ptr(),
+            k4.data_ptr(), k_scale.data_ptr(), v4.data_ptr(), v_scale.data_ptr(), mask.data_ptr(),
+            B, Hkv, d, P, S, _call_stream(stream, k4.device)))
+
+
+def kv4_unpack(k4, k_scale, v4, v_scale, kv_from, kv_len, k_cache, v_cache, stream=None):
+    """lf_kv4_unpack: the values of slots kv_from[b]..kv_len[b] of a 4-bit cache back
+    into bf16 caches [B,Hkv,P,d]."""
+    lib = load_library()
+    B, Hkv, S, d = _check_kv4(k4, k_scale, v4, v_scale)
+    P = _check_kv4_slots(k_cache, v_cache, kv_from, kv_len, B, Hkv, d)
+    with _on_device(k4.device, k_scale, v4, v_scale, k_cache, v_cache, kv_from, kv_len):
+        _check(lib, lib.lf_kv4_unpack(
+            k4.data_ptr(), k_scale.data_ptr(), v4.data_ptr(), v_scale.data_ptr(), _ptr(kv_from),
+            kv_len.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, Hkv, d, P, S,
+            _call_stream(stream, k4.device)))
+
+
+def decode_kv4_workspace(B, Hq, Hkv, d, S) -> int:
+    """Workspace bytes of decode_attention_kv4 for these sizes on the current device."""
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib, lib.lf_decode_kv4_workspace(int(B), int(Hq), int(Hkv), int(d), int(S), ctypes.byref(n)))
+    return int(n.value)
+
+
+# The size is a function of the sizes and the device alone.
+_kv4_bytes = functools.lru_cache(maxsize=1024)(lambda index, *sizes: decode_kv4_workspace(*sizes))
+
+
+def decode_attention_kv4(q, k4, k_scale, v4, v_scale, mask, new_k, new_v, write_slot, out, scale,
+                         workspace=None, stream=None):
+    """lf_decode_attention_kv4: decode_attention over a 4-bit cache (the token's row
+    is put into 4 bits in write_slot and attended as the values it then stands for)."""
+    lib = load_library()
+    B, Hkv, S, d = _check_kv4(k4, k_scale, v4, v_scale)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [B,Hq,d]")
+    Hq = int(q.shape[1])
+    bf, i32 = torch.bfloat16, torch.int32
+    _need(q, "q", bf, (B, Hq, d), True)
+    _need(mask, "mask", i32, (B, Hkv, S), True)
+    _need(new_k, "new_k", bf, (B, Hkv, d), True)
+    _need(new_v, "new_v", bf, (B, Hkv, d), True)
+    _need(write_slot, "write_slot", i32, (B, Hkv), True)
+    _need(out, "out", bf, (B, Hq, d), True)
+    with _on_device(q.device, k4, k_scale, v4, v_scale, mask, new_k, new_v, write_slot, out):
+        n = _kv4_bytes(q.device.index, B, Hq, Hkv, d, S)
+        ws = _workspace(workspace, n, q.device, stream) if n or workspace is not None else None
+        _check(lib, lib.lf_decode_attention_kv4(
+            q.data_ptr(), k4.data_ptr(), k_scale.data_ptr(), v4.data_ptr(), v_scale.data_ptr(),
+            mask.data_ptr(), new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(),
+            out.data_ptr(), B, Hq, Hkv, d, S, float(scale), _ptr(ws),
+            0 if ws is None else ws.numel(), _call_stream(stream, q.device)))
 
 
 def step_plan(B: int, Hq: int, Hkv: int, d: int, S: int, topk: int = 1) -> dict:

@@ -309,7 +309,7 @@ void plan_split_finish(Plan* pl, int S, int units, int sms, bool allowed) {
 // step against 80.5 for 20 of 13). A batch too small to fill the GPU that
 // way uses short chunks of about 5 tiles instead. At most kMaxChunkTiles
 // tiles and kMaxNChunk chunks.
-Plan plan_split(int S, int units, int sms, bool want_cluster, int D, int G, bool score) {
+Plan plan_split(int S, int units, int sms, bool want_cluster, int D, int G, int score) {
     Plan pl;
     pl.tiles = (S + lf::kTile - 1) / lf::kTile;
     int nchunk = 0;
@@ -461,7 +461,9 @@ struct StepArgs {
     float* scores;
     int topk = 1;        // slots returned per unit into next_slot[B][Hkv][topk]
     int flags = 0;       // LF_STEP_* bits
-    bool score = true;   // false: attention only (no score, no eviction, no ageing)
+    int score = 1;       // 0: attention only (no score, no eviction, no ageing); 2: by weights
+    float* weights = nullptr;  // [B][Hkv][S] (score 2)
+    float decay = 1.f;
     // Shared-prefix pieces joined in the merge (pre_pieces > 0).
     const float2* pre_ml = nullptr;
     const float* pre_o = nullptr;
@@ -516,7 +518,8 @@ struct Launch {
     CUtensorMap tmK, tmV;
     Plan pl;
     int d, g, units;
-    bool score;
+    int score;
+    bool zero_counters = false;  // the arrival counters are a workspace's, not zero yet
 };
 
 lf_status build_launch(const StepArgs& a, const Shape& s, char* base, uint32_t* arrivals,
@@ -539,6 +542,8 @@ lf_status build_launch(const StepArgs& a, const Shape& s, char* base, uint32_t* 
     sp.out = static_cast<__nv_bfloat16*>(a.out);
     sp.next_slot = a.next_slot;
     sp.scores = a.scores;
+    sp.weights = a.weights;
+    sp.decay = a.decay;
     sp.part_o = reinterpret_cast<float*>(base + L.o);
     sp.part_ml = reinterpret_cast<float2*>(base + L.ml);
     sp.stash = reinterpret_cast<float*>(base + L.stash);
@@ -603,13 +608,16 @@ lf_status launch(const Launch& r, cudaStream_t stream) {
         // A cluster that cannot be scheduled: the last-CTA merge, scoring
         // in the same kernel.
         (void)cudaGetLastError();
+        if (r.zero_counters &&
+            (e = cudaMemsetAsync(r.sp.arrivals, 0, r.units * sizeof(uint32_t), stream)) != cudaSuccess)
+            return cuda_fail(e, "cudaMemsetAsync(workspace)");
         e = lf::launch_decode_step(r.d, r.g, 2, r.score, false, r.tmK, r.tmV, r.sp, r.units,
                                    stream);
     }
     if (e != cudaSuccess) return cuda_fail(e, "decode-step launch");
     if (r.sp.split) {
         prof_count(LF_KERNEL_SCORE);
-        e = lf::launch_score(r.g, r.sp, r.units, stream);
+        e = lf::launch_score(r.g, r.score, r.sp, r.units, stream);
         if (e != cudaSuccess) return cuda_fail(e, "scoring-kernel launch");
     }
     return LF_OK;
@@ -810,6 +818,46 @@ lf_status run_rope(const RopeArgs& a, lf::RopeParams rp, const Shape& s, cudaStr
     return LF_OK;
 }
 
+// Prompt rows into the caches; rp holds where their positions come from.
+lf_status append(lf::RopeParams rp, const void* qkv, int64_t qkv_stride, const void* q_weight,
+                 const void* k_weight, const float* inv_freq, const int32_t* q_start,
+                 const int32_t* kv_len, void* q_out, void* k_cache, void* v_cache, int32_t* mask,
+                 int T, int B, int Hq, int Hkv, int d, int S, int rot, int interleaved, float eps,
+                 void* stream) {
+    const Shape s{B, Hq, Hkv, d, S, 0, 1.f};
+    lf_status st;
+    if ((st = check_ptr(q_start, 4, "q_start")) != LF_OK) return st;
+    if ((st = check_ptr(kv_len, 4, "kv_len")) != LF_OK) return st;
+    if ((st = check_ptr(mask, 4, "mask")) != LF_OK) return st;
+    if ((st = check_shape(s)) != LF_OK) return st;
+    const RopeArgs a{qkv, qkv_stride, q_weight, k_weight, inv_freq, rot, interleaved, eps,
+                     q_out, k_cache, v_cache, static_cast<size_t>(B) * Hkv * S * d * 2};
+    if ((st = check_rope(a, T, s)) != LF_OK) return st;
+    rp.q_start = q_start;
+    rp.kv_len = kv_len;
+    rp.mask = mask;
+    rp.T = T;
+    rp.B = B;
+    return run_rope(a, rp, s, static_cast<cudaStream_t>(stream));
+}
+
+// The axes of the rotated pairs, from the caller's host memory.
+static_assert(LF_MAX_AXES == lf::kMaxAxes, "axes of a rotation");
+lf_status set_axes(lf::RopeParams* rp, const uint8_t* pair_axis, int axes, int rot) {
+    if (!pair_axis) return fail(LF_ERR_INVALID_ARG, "pair_axis is NULL");
+    if (axes < 1 || axes > LF_MAX_AXES)
+        return fail(LF_ERR_INVALID_ARG, "axes = %d is outside [1, %d]", axes, LF_MAX_AXES);
+    if (rot < 16 || rot / 2 > static_cast<int>(sizeof rp->pair_axis) || rot % 16 != 0)
+        return fail(LF_ERR_INVALID_ARG, "rot = %d must be a multiple of 16 in [16, d]", rot);
+    for (int i = 0; i < rot / 2; ++i) {
+        if (pair_axis[i] >= axes)
+            return fail(LF_ERR_INVALID_ARG, "pair_axis[%d] = %d; there are %d axes", i, pair_axis[i], axes);
+        rp->pair_axis[i] = pair_axis[i];
+    }
+    rp->axes = axes;
+    return LF_OK;
+}
+
 // q [T][Hq][D] in boxes of 128 / g tokens, the g heads of a group and 64
 // columns: a box is one 128-row panel of a query tile.
 lf_status encode_query_map(CUtensorMap* m, const void* q, int D, int Hq, int g, int T) {
@@ -827,6 +875,13 @@ lf_status encode_query_map(CUtensorMap* m, const void* q, int D, int Hq, int g, 
     return LF_OK;
 }
 
+// |scale| in the log2 domain. Not 0: the kernels multiply masked logits (-inf) by
+// it. With the smallest positive float any finite logit weighs like 0.
+float positive_scale(float scale) {
+    return std::max(static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634),
+                    std::numeric_limits<float>::denorm_min());
+}
+
 // Tensor maps and launch of an attention call; p holds everything else.
 lf_status run_attention(lf::AttnParams p, int d, float scale, int dev, cudaStream_t stream) {
     CUtensorMap tmQ, tmK, tmV;
@@ -835,11 +890,7 @@ lf_status run_attention(lf::AttnParams p, int d, float scale, int dev, cudaStrea
     const int units = p.N * p.Hkv;
     if ((st = encode_cache_map(&tmK, const_cast<__nv_bfloat16*>(p.k), d, p.S, units)) != LF_OK) return st;
     if ((st = encode_cache_map(&tmV, const_cast<__nv_bfloat16*>(p.v), d, p.S, units)) != LF_OK) return st;
-    // Not 0: the kernel multiplies masked logits (-inf) by it. With the smallest
-    // positive float any finite logit weighs like 0.
-    p.scale_log2 = std::max(
-        static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634),
-        std::numeric_limits<float>::denorm_min());
+    p.scale_log2 = positive_scale(scale);
     p.negate = scale < 0.f;
     // A warp that computes rows again key by key keeps the others waiting: 2.9 us
     // (d = 64) or 4.8 us (d = 128) for a key of its 32 rows, measured with every
@@ -881,6 +932,112 @@ lf_status window_pieces(int T, const Shape& s, int window, int sinks, int* piece
     return LF_OK;
 }
 
+// Workspace of a step that evicts by accumulated weight: the counters, then the
+// step's scratch.
+struct WeightsLayout {
+    Plan pl;
+    Layout step;
+    size_t counters, scratch, total;
+};
+
+lf_status weights_layout(const Shape& s, int topk, int dev, WeightsLayout* out) {
+    WeightsLayout& L = *out;
+    const int units = s.B * s.Hkv;
+    L.pl = plan_split(s.S, units, sm_count(dev), topk == 1, s.d, s.Hq / s.Hkv, 2);
+    if (L.pl.stages == 3) L.pl.stages = 2;  // (LF_STAGES; there is no such instance)
+    L.step = scratch_layout(s, L.pl, 0);
+    L.counters = lf::kCounterWordsPerUnit * static_cast<size_t>(units) * sizeof(uint32_t);
+    L.scratch = align_up(L.counters, 256);
+    L.total = L.scratch + L.step.total;
+    return LF_OK;
+}
+
+// What weights of a prompt a call asks for, and its plan.
+lf_status plan_weights(int T, const Shape& s, int rows, int dev, lf::PromptWeightsParams* p) {
+    lf_status st;
+    if ((st = check_rows(T)) != LF_OK) return st;
+    if ((st = check_shape(s)) != LF_OK) return st;
+    if (static_cast<int64_t>(T) * s.Hq > (int64_t(1) << 30))
+        return fail(LF_ERR_UNSUPPORTED, "T * Hq exceeds 2^30");
+    if (rows < 0) return fail(LF_ERR_INVALID_ARG, "rows must be >= 0 (got %d)", rows);
+    p->T = T;
+    p->B = s.B;
+    p->Hq = s.Hq;
+    p->Hkv = s.Hkv;
+    p->S = s.S;
+    p->rows = std::min(rows, s.S);  // (a sequence has no more)
+    lf::plan_prompt_weights(p, sm_count(dev));
+    return LF_OK;
+}
+
+size_t stats_bytes(const lf::PromptWeightsParams& p) {
+    return static_cast<size_t>(p.pieces) * p.stat_rows * p.Hq * sizeof(float2);
+}
+
+// The arrays of a 4-bit cache of `slots` rows.
+struct Kv4Cache {
+    void *k4, *k_scale, *v4, *v_scale;
+};
+
+lf_status check_kv4(const Kv4Cache& c) {
+    lf_status st;
+    if ((st = check_ptr(c.k4, 16, "k4")) != LF_OK) return st;
+    if ((st = check_ptr(c.k_scale, 16, "k_scale")) != LF_OK) return st;
+    if ((st = check_ptr(c.v4, 16, "v4")) != LF_OK) return st;
+    return check_ptr(c.v_scale, 16, "v_scale");
+}
+
+bool kv4_overlaps(const Kv4Cache& c, size_t slots, int d, const void* x, size_t bytes) {
+    const size_t codes = slots * (d / 2), scales = slots * (d / 32) * 2;
+    return overlaps(c.k4, codes, x, bytes) || overlaps(c.v4, codes, x, bytes) ||
+           overlaps(c.k_scale, scales, x, bytes) || overlaps(c.v_scale, scales, x, bytes);
+}
+
+// Whether two of the arrays share bytes.
+bool kv4_shared(const Kv4Cache& c, size_t slots, int d) {
+    const size_t codes = slots * (d / 2), scales = slots * (d / 32) * 2;
+    return overlaps(c.k4, codes, c.v4, codes) || overlaps(c.k_scale, scales, c.v_scale, scales) ||
+           overlaps(c.k4, codes, c.k_scale, scales) || overlaps(c.k4, codes, c.v_scale, scales) ||
+           overlaps(c.v4, codes, c.k_scale, scales) || overlaps(c.v4, codes, c.v_scale, scales);
+}
+
+// Packing (p.k, p.v, p.mask are set) or unpacking (p.k_out, p.v_out).
+lf_status run_kv4_pack(lf::Kv4PackParams p, bool unpack, const void* k_cache, const void* v_cache,
+                       const int32_t* kv_from, const int32_t* kv_len, const Kv4Cache& c, int B,
+                       int Hkv, int d, int P, int S, cudaStream_t stream) {
+    lf_status st;
+    if ((st = check_ptr(k_cache, 16, "k_cache")) != LF_OK) return st;
+    if ((st = check_ptr(v_cache, 16, "v_cache")) != LF_OK) return st;
+    if ((st = check_ptr(kv_len, 4, "kv_len")) != LF_OK) return st;
+    if (kv_from && !aligned(kv_from, 4)) return fail(LF_ERR_INVALID_ARG, "kv_from is not 4-byte aligned");
+    if ((st = check_kv4(c)) != LF_OK) return st;
+    if ((st = check_shape(Shape{B, Hkv, Hkv, d, S, 0, 1.f})) != LF_OK) return st;
+    if ((st = check_shape(Shape{B, Hkv, Hkv, d, P, 0, 1.f})) != LF_OK) return st;
+    const size_t slots = static_cast<size_t>(B) * Hkv * S;
+    const size_t cache = static_cast<size_t>(B) * Hkv * P * d * 2;
+    if (kv4_overlaps(c, slots, d, k_cache, cache) || kv4_overlaps(c, slots, d, v_cache, cache) ||
+        kv4_shared(c, slots, d) || (unpack && overlaps(k_cache, cache, v_cache, cache)))
+        return fail(LF_ERR_INVALID_ARG, "the caches' arrays overlap");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if ((st = static_err_word(dev, &p.dev_err)) != LF_OK) return st;
+    p.k4 = static_cast<uint8_t*>(c.k4);
+    p.k_scale = static_cast<__nv_bfloat16*>(c.k_scale);
+    p.v4 = static_cast<uint8_t*>(c.v4);
+    p.v_scale = static_cast<__nv_bfloat16*>(c.v_scale);
+    p.kv_from = kv_from;
+    p.kv_len = kv_len;
+    p.Hkv = Hkv;
+    p.P = P;
+    p.S = S;
+    g_last_error[0] = '\0';
+    ProfScope prof(LF_KERNEL_KV4, stream);
+    if ((e = lf::launch_kv4_pack(d, unpack, p, B * Hkv, stream)) != cudaSuccess)
+        return cuda_fail(e, "4-bit packing launch");
+    return LF_OK;
+}
+
 struct PrefixShape {
     int N, P;
 };
@@ -905,7 +1062,7 @@ struct PrefixLayout {
     size_t counters, ml, scratch, o, total;
 };
 
-lf_status prefix_layout(const Shape& s, const PrefixShape& x, bool score, PrefixLayout* out) {
+lf_status prefix_layout(const Shape& s, const PrefixShape& x, int score, PrefixLayout* out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -1041,7 +1198,7 @@ lf_status lf_decode_attention(const void* q, void* k_cache, void* v_cache, int32
                               void* out, int B, int Hq, int Hkv, int d, int S, float scale,
                               void* stream) {
     StepArgs a{q, k_cache, v_cache, mask, new_k, new_v, write_slot, out, nullptr, nullptr};
-    a.score = false;
+    a.score = 0;
     return run_step(a, Shape{B, Hq, Hkv, d, S, 0, scale}, stream);
 }
 
@@ -1182,24 +1339,47 @@ lf_status lf_prefill_append(const void* qkv, int64_t qkv_stride, const void* q_w
                             void* k_cache, void* v_cache, int32_t* mask, int T, int B, int Hq,
                             int Hkv, int d, int S, int rot, int interleaved, float eps,
                             void* stream) {
-    const Shape s{B, Hq, Hkv, d, S, 0, 1.f};
-    lf_status st;
-    if ((st = check_ptr(q_start, 4, "q_start")) != LF_OK) return st;
-    if ((st = check_ptr(kv_len, 4, "kv_len")) != LF_OK) return st;
-    if ((st = check_ptr(mask, 4, "mask")) != LF_OK) return st;
     if (pos_offset && !aligned(pos_offset, 4)) return fail(LF_ERR_INVALID_ARG, "pos_offset is not 4-byte aligned");
-    if ((st = check_shape(s)) != LF_OK) return st;
+    lf::RopeParams rp = {};
+    rp.pos_offset = pos_offset;
+    return append(rp, qkv, qkv_stride, q_weight, k_weight, inv_freq, q_start, kv_len, q_out, k_cache,
+                  v_cache, mask, T, B, Hq, Hkv, d, S, rot, interleaved, eps, stream);
+}
+
+lf_status lf_qk_norm_rope_axes(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                               const void* k_weight, const float* inv_freq,
+                               const int32_t* positions, const uint8_t* pair_axis, int axes,
+                               void* q_out, void* k_out, void* v_out, int T, int Hq, int Hkv,
+                               int d, int rot, int interleaved, float eps, void* stream) {
+    const Shape s{1, Hq, Hkv, d, 1, 0, 1.f};
+    lf_status st;
+    if ((st = check_ptr(positions, 4, "positions")) != LF_OK) return st;
+    const size_t kv = (T > 0 && Hkv > 0 && d > 0) ? static_cast<size_t>(T) * Hkv * d * 2 : 0;
     const RopeArgs a{qkv, qkv_stride, q_weight, k_weight, inv_freq, rot, interleaved, eps,
-                     q_out, k_cache, v_cache, static_cast<size_t>(B) * Hkv * S * d * 2};
+                     q_out, k_out, v_out, kv};
     if ((st = check_rope(a, T, s)) != LF_OK) return st;
     lf::RopeParams rp = {};
-    rp.q_start = q_start;
-    rp.kv_len = kv_len;
-    rp.pos_offset = pos_offset;
-    rp.mask = mask;
+    if ((st = set_axes(&rp, pair_axis, axes, rot)) != LF_OK) return st;
+    rp.positions = positions;
     rp.T = T;
-    rp.B = B;
+    rp.B = 1;
     return run_rope(a, rp, s, static_cast<cudaStream_t>(stream));
+}
+
+lf_status lf_prefill_append_axes(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                                 const void* k_weight, const float* inv_freq,
+                                 const int32_t* q_start, const int32_t* kv_len,
+                                 const int32_t* positions, const uint8_t* pair_axis, int axes,
+                                 void* q_out, void* k_cache, void* v_cache, int32_t* mask, int T,
+                                 int B, int Hq, int Hkv, int d, int S, int rot, int interleaved,
+                                 float eps, void* stream) {
+    lf_status st;
+    if ((st = check_ptr(positions, 4, "positions")) != LF_OK) return st;
+    lf::RopeParams rp = {};
+    if ((st = set_axes(&rp, pair_axis, axes, rot)) != LF_OK) return st;
+    rp.positions = positions;
+    return append(rp, qkv, qkv_stride, q_weight, k_weight, inv_freq, q_start, kv_len, q_out, k_cache,
+                  v_cache, mask, T, B, Hq, Hkv, d, S, rot, interleaved, eps, stream);
 }
 
 lf_status lf_window_attention_workspace(int T, int B, int Hq, int Hkv, int d, int S, int window,
@@ -1276,7 +1456,7 @@ lf_status lf_decode_prefix_workspace(int B, int Hq, int Hkv, int d, int S, int N
     lf_status st = check_prefix_shape(s, x);
     if (st != LF_OK) return st;
     PrefixLayout L;
-    if ((st = prefix_layout(s, x, true, &L)) != LF_OK) return st;
+    if ((st = prefix_layout(s, x, 1, &L)) != LF_OK) return st;
     *bytes = L.total;
     return LF_OK;
 }
@@ -1303,9 +1483,232 @@ lf_status lf_decode_attention_prefix(const void* q, void* k_cache, void* v_cache
                                      int d, int S, int N, int P, float scale, void* workspace,
                                      size_t workspace_bytes, void* stream) {
     StepArgs a{q, k_cache, v_cache, mask, new_k, new_v, write_slot, out, nullptr, nullptr};
-    a.score = false;
+    a.score = 0;
     return run_prefix(a, Shape{B, Hq, Hkv, d, S, 0, scale}, k_prefix, v_prefix, prefix_start,
                       prefix_len, PrefixShape{N, P}, workspace, workspace_bytes, stream);
+}
+
+lf_status lf_decode_weights_workspace(int B, int Hq, int Hkv, int d, int S, int k, size_t* bytes) {
+    if (!bytes) return fail(LF_ERR_INVALID_ARG, "bytes is NULL");
+    const Shape s{B, Hq, Hkv, d, S, 0, 1.f};
+    lf_status st = check_shape(s);
+    if (st != LF_OK) return st;
+    if (k < 1 || k > LF_MAX_TOPK)
+        return fail(LF_ERR_INVALID_ARG, "k = %d is outside [1, %d]", k, LF_MAX_TOPK);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    WeightsLayout L;
+    if ((st = weights_layout(s, k, dev, &L)) != LF_OK) return st;
+    *bytes = L.total;
+    return LF_OK;
+}
+
+lf_status lf_decode_step_weights(const void* q, void* k_cache, void* v_cache, int32_t* mask,
+                                 float* weights, const void* new_k, const void* new_v,
+                                 const int32_t* write_slot, void* out, int32_t* next_slots, int k,
+                                 int flags, int B, int Hq, int Hkv, int d, int S, int W,
+                                 float scale, float decay, void* workspace,
+                                 size_t workspace_bytes, void* stream_v) {
+    StepArgs a{q, k_cache, v_cache, mask, new_k, new_v, write_slot, out, next_slots, nullptr};
+    a.topk = k;
+    a.flags = flags;
+    a.score = 2;
+    a.weights = weights;
+    a.decay = decay;
+    const Shape s{B, Hq, Hkv, d, S, W, scale};
+    lf_status st;
+    if ((st = check_ptr(weights, 4, "weights")) != LF_OK) return st;
+    if ((st = check_args(a, s)) != LF_OK) return st;
+    if (flags & LF_STEP_LOG2_SCORES) return fail(LF_ERR_INVALID_ARG, "LF_STEP_LOG2_SCORES: there is no score export");
+    if (!(decay >= 0.f && decay <= 1.f)) return fail(LF_ERR_INVALID_ARG, "decay must be in [0, 1]");
+    const size_t slots = static_cast<size_t>(B) * Hkv * S;
+    const size_t cache = slots * d * 2, qb = static_cast<size_t>(B) * Hq * d * 2;
+    if (overlaps(q, qb, out, qb) || overlaps(weights, slots * 4, mask, slots * 4) ||
+        overlaps(weights, slots * 4, k_cache, cache) || overlaps(weights, slots * 4, v_cache, cache) ||
+        overlaps(weights, slots * 4, out, qb))
+        return fail(LF_ERR_INVALID_ARG, "out overlaps q, or weights another array");
+    if ((st = check_ptr(workspace, 256, "workspace")) != LF_OK) return st;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    WeightsLayout L;
+    if ((st = weights_layout(s, k, dev, &L)) != LF_OK) return st;
+    if (workspace_bytes < L.total)
+        return fail(LF_ERR_INVALID_ARG, "workspace of %zu bytes; this call needs %zu", workspace_bytes, L.total);
+    uint32_t* err = nullptr;
+    if ((st = static_err_word(dev, &err)) != LF_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    Launch r;
+    if ((st = build_launch(a, s, ws + L.scratch, reinterpret_cast<uint32_t*>(ws), err, L.step, L.pl,
+                           &r)) != LF_OK)
+        return st;
+    r.zero_counters = true;
+    g_last_error[0] = '\0';
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    // A cluster merge counts nothing in the workspace. A last-CTA merge counts
+    // one word per unit, a split finish four more.
+    const bool cluster = r.pl.cluster && k == 1;
+    if (!cluster && (r.sp.split || r.sp.nchunk > 1)) {
+        const size_t n = r.sp.split ? L.counters : static_cast<size_t>(r.units) * sizeof(uint32_t);
+        if ((e = cudaMemsetAsync(ws, 0, n, stream)) != cudaSuccess)
+            return cuda_fail(e, "cudaMemsetAsync(workspace)");
+    }
+    return launch(r, stream);
+}
+
+lf_status lf_prompt_weights_workspace(int T, int B, int Hq, int Hkv, int d, int S, int rows,
+                                      size_t* bytes) {
+    if (!bytes) return fail(LF_ERR_INVALID_ARG, "bytes is NULL");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    lf::PromptWeightsParams p = {};
+    lf_status st = plan_weights(T, Shape{B, Hq, Hkv, d, S, 0, 1.f}, rows, dev, &p);
+    if (st != LF_OK) return st;
+    *bytes = stats_bytes(p);
+    return LF_OK;
+}
+
+lf_status lf_prompt_weights(const void* q, const void* k_cache, const int32_t* q_start,
+                            const int32_t* kv_len, float* weights, int T, int B, int Hq, int Hkv,
+                            int d, int S, int rows, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream_v) {
+    lf_status st;
+    if ((st = check_ptr(q, 16, "q")) != LF_OK) return st;
+    if ((st = check_ptr(k_cache, 16, "k_cache")) != LF_OK) return st;
+    if ((st = check_ptr(q_start, 4, "q_start")) != LF_OK) return st;
+    if ((st = check_ptr(kv_len, 4, "kv_len")) != LF_OK) return st;
+    if ((st = check_ptr(weights, 4, "weights")) != LF_OK) return st;
+    const Shape s{B, Hq, Hkv, d, S, 0, scale};
+    int dev = 0;
+    cudaError_t e;
+    lf::PromptWeightsParams p = {};
+    if ((st = check_shape(s)) != LF_OK) return st;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if ((st = plan_weights(T, s, rows, dev, &p)) != LF_OK) return st;
+    const size_t slots = static_cast<size_t>(B) * Hkv * S;
+    if (overlaps(weights, slots * 4, q, static_cast<size_t>(T) * Hq * d * 2) ||
+        overlaps(weights, slots * 4, k_cache, slots * d * 2))
+        return fail(LF_ERR_INVALID_ARG, "weights overlaps q or k_cache");
+    if ((st = check_ptr(workspace, 256, "workspace")) != LF_OK) return st;
+    const size_t need = stats_bytes(p);
+    if (workspace_bytes < need)
+        return fail(LF_ERR_INVALID_ARG, "workspace of %zu bytes; this call needs %zu", workspace_bytes, need);
+    if ((st = static_err_word(dev, &p.dev_err)) != LF_OK) return st;
+    p.q_start = q_start;
+    p.kv_len = kv_len;
+    p.weights = weights;
+    p.stats = static_cast<float2*>(workspace);
+    p.scale_log2 = positive_scale(scale);
+    p.negate = scale < 0.f;
+    p.wait_limit_ns = wait_limit_ns();
+    CUtensorMap tmQ, tmK;
+    if ((st = encode_query_map(&tmQ, q, d, Hq, Hq / Hkv, T)) != LF_OK) return st;
+    if ((st = encode_cache_map(&tmK, const_cast<void*>(k_cache), d, S, B * Hkv)) != LF_OK) return st;
+    g_last_error[0] = '\0';
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    ProfScope prof(LF_KERNEL_PROMPT_WEIGHTS, stream);
+    if ((e = lf::launch_prompt_weights(d, tmQ, tmK, p, stream)) != cudaSuccess)
+        return cuda_fail(e, "prompt weights launch");
+    return LF_OK;
+}
+
+lf_status lf_kv4_pack(const void* k_cache, const void* v_cache, const int32_t* kv_from,
+                      const int32_t* kv_len, void* k4, void* k_scale, void* v4, void* v_scale,
+                      int32_t* mask, int B, int Hkv, int d, int P, int S, void* stream) {
+    lf::Kv4PackParams p = {};
+    lf_status st;
+    if ((st = check_ptr(mask, 4, "mask")) != LF_OK) return st;
+    p.k = static_cast<const __nv_bfloat16*>(k_cache);
+    p.v = static_cast<const __nv_bfloat16*>(v_cache);
+    p.mask = mask;
+    return run_kv4_pack(p, false, k_cache, v_cache, kv_from, kv_len, Kv4Cache{k4, k_scale, v4, v_scale},
+                        B, Hkv, d, P, S, static_cast<cudaStream_t>(stream));
+}
+
+lf_status lf_kv4_unpack(const void* k4, const void* k_scale, const void* v4, const void* v_scale,
+                        const int32_t* kv_from, const int32_t* kv_len, void* k_cache,
+                        void* v_cache, int B, int Hkv, int d, int P, int S, void* stream) {
+    lf::Kv4PackParams p = {};
+    p.k_out = static_cast<__nv_bfloat16*>(k_cache);
+    p.v_out = static_cast<__nv_bfloat16*>(v_cache);
+    const Kv4Cache c{const_cast<void*>(k4), const_cast<void*>(k_scale), const_cast<void*>(v4),
+                     const_cast<void*>(v_scale)};
+    return run_kv4_pack(p, true, k_cache, v_cache, kv_from, kv_len, c, B, Hkv, d, P, S,
+                        static_cast<cudaStream_t>(stream));
+}
+
+lf_status lf_decode_kv4_workspace(int B, int Hq, int Hkv, int d, int S, size_t* bytes) {
+    if (!bytes) return fail(LF_ERR_INVALID_ARG, "bytes is NULL");
+    const Shape s{B, Hq, Hkv, d, S, 0, 1.f};
+    lf_status st = check_shape(s);
+    if (st != LF_OK) return st;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const lf::Kv4Plan pl = lf::kv4_plan(B * Hkv, S, sm_count(dev));
+    *bytes = pl.nchunk > 1 ? piece_bytes(pl.nchunk, static_cast<size_t>(B) * Hq, d) : 0;
+    return LF_OK;
+}
+
+lf_status lf_decode_attention_kv4(const void* q, void* k4, void* k_scale, void* v4, void* v_scale,
+                                  int32_t* mask, const void* new_k, const void* new_v,
+                                  const int32_t* write_slot, void* out, int B, int Hq, int Hkv,
+                                  int d, int S, float scale, void* workspace,
+                                  size_t workspace_bytes, void* stream_v) {
+    const Shape s{B, Hq, Hkv, d, S, 0, scale};
+    const Kv4Cache c{k4, k_scale, v4, v_scale};
+    lf_status st;
+    if ((st = check_ptr(q, 16, "q")) != LF_OK) return st;
+    if ((st = check_ptr(mask, 4, "mask")) != LF_OK) return st;
+    if ((st = check_ptr(new_k, 16, "new_k")) != LF_OK) return st;
+    if ((st = check_ptr(new_v, 16, "new_v")) != LF_OK) return st;
+    if ((st = check_ptr(write_slot, 4, "write_slot")) != LF_OK) return st;
+    if ((st = check_ptr(out, 16, "out")) != LF_OK) return st;
+    if ((st = check_kv4(c)) != LF_OK) return st;
+    if ((st = check_shape(s)) != LF_OK) return st;
+    const size_t rows = static_cast<size_t>(B) * Hq;
+    const size_t slots = static_cast<size_t>(B) * Hkv * S;
+    if (overlaps(q, rows * d * 2, out, rows * d * 2) || kv4_overlaps(c, slots, d, out, rows * d * 2) ||
+        kv4_overlaps(c, slots, d, q, rows * d * 2) || kv4_shared(c, slots, d))
+        return fail(LF_ERR_INVALID_ARG, "out, q and the cache's arrays overlap");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const lf::Kv4Plan pl = lf::kv4_plan(B * Hkv, S, sm_count(dev));
+    const size_t need = pl.nchunk > 1 ? piece_bytes(pl.nchunk, rows, d) : 0;
+    if (need > 0) {
+        if ((st = check_ptr(workspace, 256, "workspace")) != LF_OK) return st;
+        if (workspace_bytes < need)
+            return fail(LF_ERR_INVALID_ARG, "workspace of %zu bytes; this call needs %zu", workspace_bytes, need);
+    }
+    lf::Kv4Params p = {};
+    if ((st = static_err_word(dev, &p.dev_err)) != LF_OK) return st;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k4 = static_cast<uint8_t*>(k4);
+    p.k_scale = static_cast<__nv_bfloat16*>(k_scale);
+    p.v4 = static_cast<uint8_t*>(v4);
+    p.v_scale = static_cast<__nv_bfloat16*>(v_scale);
+    p.mask = mask;
+    p.new_k = static_cast<const __nv_bfloat16*>(new_k);
+    p.new_v = static_cast<const __nv_bfloat16*>(new_v);
+    p.write_slot = write_slot;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.part_ml = static_cast<float2*>(workspace);
+    p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        align_up(pl.nchunk * rows * sizeof(float2), 256));
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.S = S;
+    p.chunk_slots = pl.chunk_slots;
+    p.unit = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * 16777216.0);
+    g_last_error[0] = '\0';
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    ProfScope prof(LF_KERNEL_KV4, stream);
+    if ((e = lf::launch_kv4_attention(d, Hq / Hkv, p, B * Hkv, pl.nchunk, stream)) != cudaSuccess)
+        return cuda_fail(e, "4-bit attention launch");
+    return LF_OK;
 }
 
 lf_status lf_step_plan(int B, int Hq, int Hkv, int d, int S, int topk, int32_t* plan) {

@@ -31,7 +31,7 @@ constexpr int kScoreMaxChunks = 1024;
 // u = split_from + y, per = ceil(nchunk / parts) (one chunk by default). Warps take whole
 // 64-slot tiles, so a tile's chunk and liveness are warp-uniform and a tile
 // of a chunk without a live slot costs no load.
-template <int G>
+template <int G, int kScore>
 __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel(const StepParams p, int parts) {
     // Launched behind the decode-step kernel with programmatic dependent
     // launch, this grid starts only once every decode-step CTA has passed its
@@ -73,12 +73,16 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
     float* scores = p.scores ? p.scores + static_cast<size_t>(u) * S : nullptr;
     const bool fill_first = (p.flags & kFlagFillEmptyFirst) != 0;
     const bool all = fill_first || scores != nullptr;
+    constexpr bool kAdd = kScore == kWeights;
+    float* weights = kAdd ? p.weights + static_cast<size_t>(u) * S : nullptr;
+    const int ws = kAdd ? p.write_slot[u] : -1;
     const float* stash = p.stash + static_cast<size_t>(u) * S * G;
     const int32_t* age = p.mask + static_cast<size_t>(u) * S;
     // A chunk whose softmax maximum is -inf holds no live slot: no scored
     // candidate there (empty slots and scores are still visited when wanted).
+    // (A live slot whose logits are all -inf still has its weight decayed.)
     for (int c = c0 + tid; c < c1; c += kScoreThreads)
-        s_live[c - c0] = all || __ldcg(&p.part_ml[(static_cast<size_t>(u) * nchunk + c) * G].x) != -INFINITY;
+        s_live[c - c0] = all || kAdd || __ldcg(&p.part_ml[(static_cast<size_t>(u) * nchunk + c) * G].x) != -INFINITY;
     float cf[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) cf[h] = __ldcg(&p.cfold[static_cast<size_t>(u) * G + h]);
@@ -102,6 +106,7 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
          tb += kScoreWarps * kScoreTilesPerWarp) {
         int a[kSlots];
         float t[kSlots][G];
+        float old[kSlots];
         bool in[kScoreTilesPerWarp];
 #pragma unroll
         for (int q = 0; q < kScoreTilesPerWarp; ++q) {
@@ -113,6 +118,7 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
                 const int j = tile * kTile + r * 32 + lane;
                 const bool ok = in[q] && j < S;
                 a[2 * q + r] = ok ? __ldcg(age + j) : -1;
+                old[2 * q + r] = (kAdd && ok) ? weights[j] : 0.f;
                 if (ok) load_terms<G>(stash + j * G, t[2 * q + r]);
             }
         }
@@ -123,8 +129,10 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
             for (int r = 0; r < 2; ++r) {
                 const int j = (tb + q) * kTile + r * 32 + lane;
                 const int aa = a[2 * q + r];
-                const float L = log2_score<G>(t[2 * q + r], cf);
                 const bool live = aa >= 0;
+                const float L = kAdd ? add_weight<G>(p, old[2 * q + r], j == ws, t[2 * q + r], cf)
+                                     : log2_score<G>(t[2 * q + r], cf);
+                if (kAdd && live) weights[j] = L;
                 const bool cand = live ? (aa >= W && L == L) : fill_first;
                 const uint32_t key = live ? ordered_key(L) : 0u;
                 if (cand && j < S && key < bkey) {
@@ -191,13 +199,13 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
 
 template <int D, int G>
 cudaError_t launch_dg(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepParams& p,
-                      int units, cudaStream_t stream, int stages, bool score, bool pdl) {
+                      int units, cudaStream_t stream, int stages, int score, bool pdl) {
     if (!score) return launch_t<D, G, 2, false, false>(tmK, tmV, p, units, stream, pdl);
     return stages == 2 ? launch_t<D, G, 2, true, false>(tmK, tmV, p, units, stream, pdl)
                        : launch_t<D, G, 3, true, false>(tmK, tmV, p, units, stream, pdl);
 }
 
-template <int G>
+template <int G, int kScore>
 cudaError_t launch_score_t(const StepParams& p, int units, cudaStream_t stream, bool pdl) {
     // One CTA per chunk: the CTAs of a unit wait for its flag, not for each
     // other or for the grid, so the grid need not be resident at once, and
@@ -217,14 +225,14 @@ cudaError_t launch_score_t(const StepParams& p, int units, cudaStream_t stream, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, lf_score_kernel<G>, p, parts);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, lf_score_kernel<G, kScore>, p, parts);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 }  // namespace
 
-bool step_fits(int D, int G, int stages, bool score, int nchunk, int topk, int pre_pieces) {
+bool step_fits(int D, int G, int stages, int score, int nchunk, int topk, int pre_pieces) {
     const size_t need =
         finish_smem_bytes(nchunk, G, score ? topk : 1) + prefix_smem_bytes(pre_pieces, G);
     size_t have;
@@ -244,13 +252,15 @@ size_t step_smem_bytes(int D, int stages) {
     return D == 64 ? StepSmem<64, 3>::kAlloc : StepSmem<128, 3>::kAlloc;
 }
 
-cudaError_t launch_decode_step(int D, int G, int stages, bool score, bool cluster,
+cudaError_t launch_decode_step(int D, int G, int stages, int score, bool cluster,
                                const CUtensorMap& tmK, const CUtensorMap& tmV,
                                const StepParams& p, int units, cudaStream_t stream) {
     // Programmatic dependent launch overlaps this step's launch and set-up
     // with the tail of the previous kernel in the stream (LF_PDL=0: off).
     const char* env = std::getenv("LF_PDL");
     const bool pdl = !(env && std::atoi(env) == 0);
+    if (score == kWeights)
+        return launch_decode_step_weights(D, G, stages, cluster, tmK, tmV, p, units, stream, pdl);
     if (cluster) return launch_decode_step_cluster(D, G, stages, score, tmK, tmV, p, units, stream, pdl);
 #define LF_STEP_CASE(DD, GG) \
     if (D == DD && G == GG)  \
@@ -261,17 +271,19 @@ cudaError_t launch_decode_step(int D, int G, int stages, bool score, bool cluste
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_score(int G, const StepParams& p, int units, cudaStream_t stream) {
+cudaError_t launch_score(int G, int score, const StepParams& p, int units, cudaStream_t stream) {
     if (p.chunk_tiles > kMaxChunkTiles || p.nchunk > kScoreMaxChunks) return cudaErrorInvalidValue;
     const char* env = std::getenv("LF_PDL");
     const bool pdl = !(env && std::atoi(env) == 0);
+#define LF_SCORE_CASE(GG)                                                      \
+    case GG:                                                                   \
+        return score == kWeights ? launch_score_t<GG, kWeights>(p, units, stream, pdl) \
+                                 : launch_score_t<GG, kLongFlow>(p, units, stream, pdl);
     switch (G) {
-        case 1: return launch_score_t<1>(p, units, stream, pdl);
-        case 2: return launch_score_t<2>(p, units, stream, pdl);
-        case 4: return launch_score_t<4>(p, units, stream, pdl);
-        case 8: return launch_score_t<8>(p, units, stream, pdl);
+        LF_SCORE_CASE(1) LF_SCORE_CASE(2) LF_SCORE_CASE(4) LF_SCORE_CASE(8)
         default: return cudaErrorInvalidValue;
     }
+#undef LF_SCORE_CASE
 }
 
 }  // namespace lf

@@ -12,7 +12,7 @@ namespace {
 
 template <int D, int G>
 cudaError_t launch_cluster_dg(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepParams& p,
-                              int units, cudaStream_t stream, int stages, bool score, bool pdl) {
+                              int units, cudaStream_t stream, int stages, int score, bool pdl) {
     if (stages == kDeepStages)
         return score ? launch_t<D, G, kDeepStages, true, true>(tmK, tmV, p, units, stream, pdl)
                      : launch_t<D, G, kDeepStages, false, true>(tmK, tmV, p, units, stream, pdl);
@@ -21,7 +21,7 @@ cudaError_t launch_cluster_dg(const CUtensorMap& tmK, const CUtensorMap& tmV, co
 }
 
 template <int D, int G>
-int clusters_dg(int stages, bool score, int csize) {
+int clusters_dg(int stages, int score, int csize) {
     if (stages == kDeepStages)
         return score ? max_active_clusters_t<D, G, kDeepStages, true>(csize)
                      : max_active_clusters_t<D, G, kDeepStages, false>(csize);
@@ -31,23 +31,28 @@ int clusters_dg(int stages, bool score, int csize) {
 
 }  // namespace
 
-int max_active_clusters(int D, int G, int stages, bool score, int csize) {
+int max_active_clusters(int D, int G, int stages, int score, int csize) {
     if (csize < 1 || csize > kMaxClusterChunks) return 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     // One query per device and instance (the answer is fixed for a process);
     // an entry holds the count + 1, 0 while unknown.
     constexpr int kDevs = 16;
-    static std::atomic<int> cache[kDevs][2][4][2][2][kMaxClusterChunks + 1];
+    static std::atomic<int> cache[kDevs][2][4][2][3][kMaxClusterChunks + 1];
     const int gi = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
     std::atomic<int>* c = dev < kDevs ? &cache[dev][D == 128 ? 1 : 0][gi]
-                                              [stages == kDeepStages ? 1 : 0][score ? 1 : 0][csize]
+                                              [stages == kDeepStages ? 1 : 0][score][csize]
                                       : nullptr;
     if (c) {
         const int v = c->load(std::memory_order_relaxed);
         if (v > 0) return v - 1;
     }
     int n = 0;
+    if (score == kWeights) {
+        n = max_active_clusters_weights(D, G, stages, csize);
+        if (c) c->store(n + 1, std::memory_order_relaxed);
+        return n;
+    }
 #define LF_STEP_CASE(DD, GG) \
     if (D == DD && G == GG) n = clusters_dg<DD, GG>(stages, score, csize);
     LF_STEP_CASE(64, 1) LF_STEP_CASE(64, 2) LF_STEP_CASE(64, 4) LF_STEP_CASE(64, 8)
@@ -66,7 +71,7 @@ int deep_term_slots(int D, int G) {
     return 0;
 }
 
-cudaError_t launch_decode_step_cluster(int D, int G, int stages, bool score,
+cudaError_t launch_decode_step_cluster(int D, int G, int stages, int score,
                                        const CUtensorMap& tmK, const CUtensorMap& tmV,
                                        const StepParams& p, int units, cudaStream_t stream,
                                        bool pdl) {

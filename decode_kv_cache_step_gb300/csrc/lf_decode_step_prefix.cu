@@ -18,14 +18,14 @@ namespace {
 
 template <int D, int G>
 cudaError_t launch_dg(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepParams& p,
-                      int units, cudaStream_t stream, bool score, bool pdl) {
+                      int units, cudaStream_t stream, int score, bool pdl) {
     return score ? launch_t<D, G, 2, true, false, true>(tmK, tmV, p, units, stream, pdl)
                  : launch_t<D, G, 2, false, false, true>(tmK, tmV, p, units, stream, pdl);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_step_prefix(int D, int G, bool score, const CUtensorMap& tmK,
+cudaError_t launch_decode_step_prefix(int D, int G, int score, const CUtensorMap& tmK,
                                       const CUtensorMap& tmV, const StepParams& p, int units,
                                       cudaStream_t stream) {
     const char* env = std::getenv("LF_PDL");

@@ -28,6 +28,8 @@ struct StepParams {
     __nv_bfloat16* out;          // [B][Hq][D]
     int32_t* next_slot;          // [units][topk] slots to overwrite, ascending (score, slot)
     float* scores;               // [units][S] or nullptr
+    float* weights = nullptr;    // [units][S] accumulated weights (score 2), updated in place
+    float decay = 1.f;
     // scratch
     float* part_o;               // [units][nchunk][G][D]  unnormalised output, base m
     float2* part_ml;             // [units][nchunk][G]     (m, l), log2 domain
@@ -90,35 +92,44 @@ constexpr int kCounterWordsPerUnit = 5;
 size_t step_smem_bytes(int D, int stages);
 
 // Whether finish-stage shared memory (chunk weights, top-k list) fits.
-bool step_fits(int D, int G, int stages, bool score, int nchunk, int topk, int pre_pieces = 0);
+bool step_fits(int D, int G, int stages, int score, int nchunk, int topk, int pre_pieces = 0);
 
-// score = false runs the attention-only variant: the slot write (the written
-// slot becomes live; no other age changes) and the attention output, without
-// LongFlowScore or eviction. next_slot, scores and topk are then unused.
+// score: 1 ranks by LongFlowScore, 2 by the accumulated weight (weights, decay;
+// the 2-stage ring and the deep one). 0 runs the attention-only variant: the slot
+// write (the written slot becomes live; no other age changes) and the attention
+// output, without score or eviction. next_slot, scores and topk are then unused.
 // cluster = true launches each unit's nchunk (<= kMaxClusterChunks) CTAs as
 // one thread-block cluster that merges through distributed shared memory
 // (2-stage ring, topk == 1 only); otherwise the unit's last CTA merges.
-cudaError_t launch_decode_step(int D, int G, int stages, bool score, bool cluster,
+cudaError_t launch_decode_step(int D, int G, int stages, int score, bool cluster,
                                const CUtensorMap& tmK, const CUtensorMap& tmV,
                                const StepParams& p, int units, cudaStream_t stream);
 
 // The cluster instantiations (lf_decode_step_cluster.cu); stages is 2 or
 // kDeepStages.
-cudaError_t launch_decode_step_cluster(int D, int G, int stages, bool score,
+cudaError_t launch_decode_step_cluster(int D, int G, int stages, int score,
                                        const CUtensorMap& tmK, const CUtensorMap& tmV,
                                        const StepParams& p, int units, cudaStream_t stream,
                                        bool pdl);
 
 // The step with the prefix pieces of p.pre_* in its merge
 // (lf_decode_step_prefix.cu): last-CTA merge, 2-stage ring.
-cudaError_t launch_decode_step_prefix(int D, int G, bool score, const CUtensorMap& tmK,
+cudaError_t launch_decode_step_prefix(int D, int G, int score, const CUtensorMap& tmK,
                                       const CUtensorMap& tmV, const StepParams& p, int units,
                                       cudaStream_t stream);
+
+// The instances that rank by the accumulated weight (lf_decode_step_weights.cu),
+// behind launch_decode_step and max_active_clusters.
+cudaError_t launch_decode_step_weights(int D, int G, int stages, bool cluster,
+                                       const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                       const StepParams& p, int units, cudaStream_t stream,
+                                       bool pdl);
+int max_active_clusters_weights(int D, int G, int stages, int csize);
 
 // How many clusters of csize CTAs (one unit each) of the cluster instance
 // (stages 2 or kDeepStages) can be resident at once on the current device;
 // 0 if none can or the query fails. Cached per device and instance.
-int max_active_clusters(int D, int G, int stages, bool score, int csize);
+int max_active_clusters(int D, int G, int stages, int score, int csize);
 
 // Slots of a chunk whose score terms the deep-ring cluster instance keeps
 // in shared memory (the plan gives that ring no longer chunks).
@@ -128,7 +139,7 @@ int deep_term_slots(int D, int G);
 // CTA (c, y) takes unit u = split_from + y: it waits for unit u's ready flag, scores its chunks from the ages, the score
 // terms and c_h, and the unit's last CTA writes next_slot (and masks it with
 // kFlagMaskEvicted). It does not wait for the decode-step grid as a whole.
-cudaError_t launch_score(int G, const StepParams& p, int units, cudaStream_t stream);
+cudaError_t launch_score(int G, int score, const StepParams& p, int units, cudaStream_t stream);
 
 // Norm and rotation of query and key heads (lf_rope.cu). Row t of qkv holds
 // Hq query, Hkv key and Hkv value heads of D. Without q_start, row t has
@@ -136,13 +147,16 @@ cudaError_t launch_score(int G, const StepParams& p, int units, cudaStream_t str
 // (prompt rows into a cache), the rows q_start[b] .. q_start[b + 1] are the
 // last tokens of sequence b's kv_len[b] tokens: token i of the sequence has
 // position i (+ pos_offset[b]) and slot i, and mask gets the tokens' ages.
+// With axes, row t has a position on each of them, positions[a * T + t], for
+// its rotation, and pair i turns by that of axis pair_axis[i].
+constexpr int kMaxAxes = 4;
 struct RopeParams {
     const __nv_bfloat16* qkv;
     int64_t stride;                 // elements between rows
     const __nv_bfloat16* q_weight;  // [D] or nullptr: no norm
     const __nv_bfloat16* k_weight;
     const float* inv_freq;          // [rot / 2]
-    const int32_t* positions;       // [T]
+    const int32_t* positions;       // [T], or [axes][T]
     const int32_t* q_start;         // [B + 1] or nullptr
     const int32_t* kv_len;          // [B]
     const int32_t* pos_offset;      // [B] or nullptr
@@ -154,6 +168,8 @@ struct RopeParams {
     int T, B, Hq, Hkv, S, rot;
     bool interleaved;
     float eps;
+    int axes;                       // 0: one position per row
+    uint8_t pair_axis[64];          // [rot / 2]
 };
 cudaError_t launch_rope(int D, const RopeParams& p, int sms, cudaStream_t stream);
 
@@ -193,6 +209,72 @@ int attention_pieces(int T, int N, int Hq, int Hkv, int S, bool causal, int wind
 cudaError_t launch_attention(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                              const CUtensorMap& tmV, const AttnParams& p, int sms,
                              cudaStream_t stream);
+
+// Attention weights of a prompt's last rows, summed per key (lf_weights.cu).
+struct PromptWeightsParams {
+    const int32_t* q_start;  // [B + 1]
+    const int32_t* kv_len;   // [B]
+    float* weights;          // [B][Hkv][S]
+    float2* stats;           // [pieces][stat_rows][Hq]: (m, l) of the counted rows
+    uint32_t* dev_err;
+    int T, B, Hq, Hkv, S;
+    int rows;                // counted rows of a sequence at most (0: all)
+    float scale_log2;        // |scale| * log2(e), not 0
+    bool negate;             // scale < 0: the kernel negates the held operand
+    uint64_t wait_limit_ns;
+    // The plan (plan_prompt_weights), from the sizes above.
+    bool by_sequence;        // statistics and tiles counted per sequence, not by packed row
+    int items, pieces, stat_rows;
+};
+void plan_prompt_weights(PromptWeightsParams* p, int sms);
+// tmQ and tmK as in launch_attention.
+cudaError_t launch_prompt_weights(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                  const PromptWeightsParams& p, cudaStream_t stream);
+
+// A cache in 4 bits (lf_kv4.cu): codes [units][S][D / 2], scales [units][S][D / 32].
+struct Kv4PackParams {
+    const __nv_bfloat16* k;   // [B][Hkv][P][D]: pack reads these
+    const __nv_bfloat16* v;
+    __nv_bfloat16* k_out;     // [B][Hkv][P][D]: unpack writes these
+    __nv_bfloat16* v_out;
+    uint8_t* k4;
+    __nv_bfloat16* k_scale;
+    uint8_t* v4;
+    __nv_bfloat16* v_scale;
+    const int32_t* kv_from;   // [B] or nullptr: 0
+    const int32_t* kv_len;    // [B]
+    int32_t* mask;            // [B][Hkv][S] (pack)
+    uint32_t* dev_err;
+    int Hkv, P, S;
+};
+// Slots kv_from .. kv_len of every sequence into the 4-bit cache (and the mask's
+// ages), or back.
+cudaError_t launch_kv4_pack(int D, bool unpack, const Kv4PackParams& p, int units, cudaStream_t stream);
+
+// Slot write and attention of single tokens over a 4-bit cache.
+struct Kv4Params {
+    const __nv_bfloat16* q;      // [B][Hq][D]
+    uint8_t* k4;
+    __nv_bfloat16* k_scale;
+    uint8_t* v4;
+    __nv_bfloat16* v_scale;
+    int32_t* mask;               // [units][S]
+    const __nv_bfloat16* new_k;  // [units][D]
+    const __nv_bfloat16* new_v;
+    const int32_t* write_slot;   // [units]
+    __nv_bfloat16* out;          // [B][Hq][D]
+    float2* part_ml;             // [units][nchunk][G]     (nchunk > 1)
+    float* part_o;               // [units][nchunk][G][D]
+    uint32_t* dev_err;
+    int Hq, Hkv, S, chunk_slots;
+    float unit;                  // scale * log2(e) over what a code counts (2^-24)
+};
+struct Kv4Plan {
+    int chunk_slots, nchunk;
+};
+Kv4Plan kv4_plan(int units, int S, int sms);
+cudaError_t launch_kv4_attention(int D, int G, const Kv4Params& p, int units, int nchunk,
+                                 cudaStream_t stream);
 
 // Error bit of lengths that do not fit (LF_DEVERR_BAD_LENGTH).
 constexpr uint32_t kErrBadLength = 0x4u;

@@ -1,0 +1,654 @@
+// A cache held in 4 bits: a prompt's rows into it and back, and decode
+// attention over it (sm_103a).
+//
+// A row of d values has d / 32 groups of 32. A group's scale is s = max|x| / 7
+// rounded to bf16, a value's code round(x / s) in [-7, 7] (ties to even), and
+// the value it stands for code * s. A row takes d / 2 bytes of codes (plus 8, in
+// nibbles) and d / 32 scales: 4.5 bits a value, 3.56 times fewer bytes than
+// bf16. (A power of two as the scale would save 8 bits in 136 and double the
+// error of half the groups.)
+//
+// Order of a row's codes: value c of group g lies in nibble
+// ((r / e) * (d / 32) + g) * e + r % e, r = c % 32, low nibble of a byte first,
+// with pieces of e = 8 in keys and e = 4 in values. The pieces of the groups
+// take turns so that what one lane of a matrix product needs of a row, some
+// codes of each group, lies together (see lf_kv4_attn_kernel).
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdlib.h>
+
+#include <algorithm>
+
+#include "../../include/lf_decode.h"
+#include "lf_kernels.h"
+#include "lf_ptx.cuh"
+
+namespace lf {
+namespace {
+
+constexpr int kPackThreads = 256;
+constexpr int kPackSlots = 64;  // slots of one (sequence, KV head) a CTA packs or unpacks
+
+// ------------------------------------------------------------ quantisation --
+
+// Codes of 8 values (4 lanes hold a group): nibble i of the result is value i's
+// code plus 8. *scale gets the group's scale.
+//
+// The codes are those of the exact quotients. x = X 2^a and s = Y 2^b have
+// 8-bit integers X, Y, so where x / s is not halfway between two integers it is
+// at least 2^-10 away from that: a product with the rounded reciprocal (off by
+// 2^-20 at most), rounded to multiples of 2^-12, is on the right side, and a tie
+// is a tie again.
+__device__ __forceinline__ uint32_t quantise8(const uint4 v, unsigned mask, __nv_bfloat16* scale) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) top = max(top, __shfl_xor_sync(mask, top, off));
+    // A group with a value that is not finite stands for NaN.
+    const float amax = __uint_as_float(top << 16);
+    const __nv_bfloat16 s = top < 0x7f80u ? __float2bfloat16_rn(amax / 7.f) : __ushort_as_bfloat16(0x7fffu);
+    *scale = s;
+    // Small groups times 2^64, so that the reciprocal is finite.
+    const float up = amax < 0x1p-60f ? 0x1p64f : 1.f;
+    const float sf = __bfloat162float(s) * up;
+    const bool some = sf > 0.f;  // neither 0 nor NaN
+    const float inv = some ? 1.f / sf : 0.f;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        float t = some ? x * up * inv : 0.f;
+        constexpr float kSnap = 0x1.8p11f;  // adds to a multiple of 2^-12
+        t = __fadd_rn(__fadd_rn(t, kSnap), -kSnap);
+        const int c = min(7, max(-7, __float2int_rn(t)));
+        codes |= static_cast<uint32_t>(c + 8) << (4 * i);
+    }
+    return codes;
+}
+
+// Where the 8 codes of values 8 i .. 8 i + 7 of a row lie: one piece of 8, or
+// two of 4 that lie `kPair` bytes apart.
+template <int D>
+__device__ __forceinline__ void store_k8(uint8_t* row, int i, uint32_t codes) {
+    const int g = i >> 2, r8 = i & 3;
+    *reinterpret_cast<uint32_t*>(row + (r8 * (D / 32) + g) * 4) = codes;
+}
+template <int D>
+__device__ __forceinline__ void store_v8(uint8_t* row, int i, uint32_t codes) {
+    const int g = i >> 2, r4 = (i & 3) * 2;
+    *reinterpret_cast<uint16_t*>(row + (r4 * (D / 32) + g) * 2) = static_cast<uint16_t>(codes);
+    *reinterpret_cast<uint16_t*>(row + ((r4 + 1) * (D / 32) + g) * 2) = static_cast<uint16_t>(codes >> 16);
+}
+template <int D>
+__device__ __forceinline__ uint32_t load_k8(const uint8_t* row, int i) {
+    return __ldg(reinterpret_cast<const uint32_t*>(row + ((i & 3) * (D / 32) + (i >> 2)) * 4));
+}
+template <int D>
+__device__ __forceinline__ uint32_t load_v8(const uint8_t* row, int i) {
+    const int g = i >> 2, r4 = (i & 3) * 2;
+    const uint32_t lo = __ldg(reinterpret_cast<const uint16_t*>(row + (r4 * (D / 32) + g) * 2));
+    const uint32_t hi = __ldg(reinterpret_cast<const uint16_t*>(row + ((r4 + 1) * (D / 32) + g) * 2));
+    return lo | hi << 16;
+}
+
+// The range of slots of sequence b, and whether it fits both buffers.
+struct SlotRange {
+    int first, end;
+};
+__device__ __forceinline__ bool slot_range(const Kv4PackParams& p, int b, SlotRange* r) {
+    r->first = p.kv_from ? p.kv_from[b] : 0;
+    r->end = p.kv_len[b];
+    return r->first >= 0 && r->first <= r->end && r->end <= min(p.P, p.S);
+}
+
+// Slots of bf16 caches [B][Hkv][P][D] into the 4-bit cache [B][Hkv][S], and the
+// ages of an in-order cache. Memory bound: a thread takes 16 bytes of a row.
+template <int D>
+__global__ void __launch_bounds__(kPackThreads) lf_kv4_pack_kernel(const Kv4PackParams p) {
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int u = blockIdx.y;
+    const int b = u / p.Hkv;
+    const int j0 = blockIdx.x * kPackSlots;
+    const int tid = threadIdx.x;
+    SlotRange r;
+    if (!slot_range(p, b, &r)) {
+        if (tid == 0 && blockIdx.x == 0) atomicOr(p.dev_err, kErrBadLength);
+        return;
+    }
+    if (tid < kPackSlots && j0 + tid < r.end)
+        p.mask[static_cast<size_t>(u) * p.S + j0 + tid] = r.end - 1 - (j0 + tid);
+    constexpr int kLanes = D / 8;
+    constexpr int kRows = kPackThreads / kLanes;
+    const int i = tid % kLanes;
+    const unsigned mask = 0xfu << (tid & 28);
+    const int last = min(j0 + kPackSlots, r.end);
+    for (int j = max(j0, r.first) + tid / kLanes; j < last; j += kRows) {
+        const size_t src = (static_cast<size_t>(u) * p.P + j) * D;
+        const size_t dst = static_cast<size_t>(u) * p.S + j;
+        const uint4 k = __ldcs(reinterpret_cast<const uint4*>(p.k + src) + i);
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p.v + src) + i);
+        __nv_bfloat16 s;
+        store_k8<D>(p.k4 + dst * (D / 2), i, quantise8(k, mask, &s));
+        if ((i & 3) == 0) p.k_scale[dst * (D / 32) + (i >> 2)] = s;
+        store_v8<D>(p.v4 + dst * (D / 2), i, quantise8(v, mask, &s));
+        if ((i & 3) == 0) p.v_scale[dst * (D / 32) + (i >> 2)] = s;
+    }
+}
+
+// Two codes (plus 8) at bits 4 i and 4 i + 4 of a word times a scale, as bf16.
+__device__ __forceinline__ uint32_t stand_for2(uint32_t codes, int i, float s) {
+    const float x = static_cast<float>(static_cast<int>((codes >> (4 * i)) & 15u) - 8) * s;
+    const float y = static_cast<float>(static_cast<int>((codes >> (4 * i + 4)) & 15u) - 8) * s;
+    return pack_bf16x2(x, y);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPackThreads) lf_kv4_unpack_kernel(const Kv4PackParams p) {
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int u = blockIdx.y;
+    const int b = u / p.Hkv;
+    const int j0 = blockIdx.x * kPackSlots;
+    const int tid = threadIdx.x;
+    SlotRange r;
+    if (!slot_range(p, b, &r)) {
+        if (tid == 0 && blockIdx.x == 0) atomicOr(p.dev_err, kErrBadLength);
+        return;
+    }
+    constexpr int kLanes = D / 8;
+    constexpr int kRows = kPackThreads / kLanes;
+    const int i = tid % kLanes;
+    const int last = min(j0 + kPackSlots, r.end);
+    for (int j = max(j0, r.first) + tid / kLanes; j < last; j += kRows) {
+        const size_t src = static_cast<size_t>(u) * p.S + j;
+        const size_t dst = (static_cast<size_t>(u) * p.P + j) * D;
+        const uint32_t k = load_k8<D>(p.k4 + src * (D / 2), i);
+        const uint32_t v = load_v8<D>(p.v4 + src * (D / 2), i);
+        const float ks = __bfloat162float(p.k_scale[src * (D / 32) + (i >> 2)]);
+        const float vs = __bfloat162float(p.v_scale[src * (D / 32) + (i >> 2)]);
+        __stcs(reinterpret_cast<uint4*>(p.k_out + dst) + i,
+               make_uint4(stand_for2(k, 0, ks), stand_for2(k, 2, ks), stand_for2(k, 4, ks), stand_for2(k, 6, ks)));
+        __stcs(reinterpret_cast<uint4*>(p.v_out + dst) + i,
+               make_uint4(stand_for2(v, 0, vs), stand_for2(v, 2, vs), stand_for2(v, 4, vs), stand_for2(v, 6, vs)));
+    }
+}
+
+// -------------------------------------------------------- decode attention --
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxChunkSlots = 2048;
+constexpr int kMaxWarpTiles = kMaxChunkSlots / 16 / kWarps;
+constexpr float kCode = 0x1p-24f;  // what the integer 1 in a half's low bits is worth
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1, const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 32-bit words of the cache: read once per step, past L1.
+template <int N>
+__device__ __forceinline__ void load_words(const void* a, uint32_t (&w)[N]) {
+    static_assert(N == 1 || N == 2 || N == 4, "words of a load");
+    if constexpr (N == 1)
+        asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(a) : "memory");
+    else if constexpr (N == 2)
+        asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(a) : "memory");
+    else
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "l"(a)
+                     : "memory");
+}
+
+__device__ __forceinline__ float scale_of(uint32_t word, int odd) {
+    return __uint_as_float(odd ? word & 0xffff0000u : word << 16);
+}
+
+// One CTA: chunk blockIdx.x of unit blockIdx.y. Each warp takes 16 live slots at
+// a time, straight from global memory into the registers of its products:
+//   S^T[16 x 8] = K[16 x d] Q^T[d x 8]          per group, times the key's scale
+//   O^T[d x 8] += V^T[d x 16] (P s)^T[16 x 8]   per group, P s the weights times
+//                                               the values' scales
+// A code needs no conversion: an integer n in the low bits of a half is the half
+// n 2^-24 (a subnormal; linear up to n = 2047, and the tensor cores take it), so
+// the codes at bits 0 and 16 of a word are an operand after one AND, those at
+// bits 4 and 20, as 16 n, after another. The 16 is taken out of q, or of the row
+// of O. Codes are stored plus 8: the products' accumulators start at
+// -8 sum q, and 8 sum P s, one more product a group with constant codes, is
+// taken off O at the end.
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Params p) {
+    constexpr int NG = D / 32;
+    __shared__ uint32_t s_tiles[kWarps][kMaxWarpTiles];
+    __shared__ float s_o[kWarps][G][D + 4];
+    __shared__ float s_m[kWarps][G], s_l[kWarps][G];
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const int lane = tid & 31;
+    const int r = lane >> 2;
+    const int c = lane & 3;
+    const int u = blockIdx.y;
+    const int b = u / p.Hkv;
+    const int kvh = u - b * p.Hkv;
+    const int S = p.S;
+    const int slot0 = blockIdx.x * p.chunk_slots;
+    const int slots = min(p.chunk_slots, S - slot0);
+    allow_dependent_launch();
+    grid_dependency_wait();
+
+    int ws = p.write_slot[u];
+    // The warp's slots: 32 of every 128. Their ages first, all in flight.
+    constexpr int kBlocks = kMaxChunkSlots / 32 / kWarps;
+    int32_t* const ages = p.mask + static_cast<size_t>(u) * S + slot0;
+    int age[kBlocks];
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+        const int i = (k * kWarps + warp) * 32 + lane;
+        age[k] = i < slots ? ages[i] : -1;
+    }
+    // q of head r: the lane's values 8 c .. 8 c + 7 of each group.
+    const size_t row0 = static_cast<size_t>(b) * p.Hq + static_cast<size_t>(kvh) * G;
+    uint4 qv[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        qv[g] = r < G ? *reinterpret_cast<const uint4*>(p.q + (row0 + r) * D + 32 * g + 8 * c)
+                      : make_uint4(0, 0, 0, 0);
+    if (ws < -1 || ws >= S) {
+        if (tid == 0 && blockIdx.x == 0) atomicOr(p.dev_err, LF_DEVERR_BAD_WRITE_SLOT);
+        ws = -1;
+    }
+    // The token's row into its slot, by the warp that will read it: lanes below
+    // D / 8 the key, the next D / 8 the value.
+    const int wi = ws - slot0;
+    const bool mine = ws >= 0 && wi >= 0 && wi < slots && ((wi >> 5) & (kWarps - 1)) == warp;
+    if (mine) {
+        const int i = lane % (D / 8);
+        const bool is_v = lane / (D / 8) == 1;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (lane < D / 4)
+            x = *reinterpret_cast<const uint4*>((is_v ? p.new_v : p.new_k) + static_cast<size_t>(u) * D + 8 * i);
+        __nv_bfloat16 s;
+        const uint32_t codes = quantise8(x, 0xfu << (lane & 28), &s);
+        const size_t at = static_cast<size_t>(u) * S + ws;
+        if (lane < D / 4) {
+            if (is_v)
+                store_v8<D>(p.v4 + at * (D / 2), i, codes);
+            else
+                store_k8<D>(p.k4 + at * (D / 2), i, codes);
+            if ((i & 3) == 0) (is_v ? p.v_scale : p.k_scale)[at * NG + (i >> 2)] = s;
+        }
+        __syncwarp();  // before the warp's loads of the row
+    }
+    // The warp's live tiles of 16 slots.
+    int tiles = 0;
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+        const int block = k * kWarps + warp;
+        bool live = age[k] >= 0;
+        if (mine && block * 32 + lane == wi && !live) {
+            ages[wi] = 0;
+            live = true;
+        }
+        const uint32_t bits = __ballot_sync(0xffffffffu, live);
+        const int two = (bits & 0xffffu ? 1 : 0) + (bits >> 16 ? 1 : 0);
+        if (lane == 0) {
+            if (bits & 0xffffu) s_tiles[warp][tiles] = static_cast<uint32_t>(2 * block) << 16 | (bits & 0xffffu);
+            if (bits >> 16) s_tiles[warp][tiles + two - 1] = static_cast<uint32_t>(2 * block + 1) << 16 | bits >> 16;
+        }
+        tiles += two;
+    }
+    __syncwarp();
+
+    // q as halves of 2^13 to 2^14 for the largest: what is below 2^-38 of that is lost.
+    uint32_t qf[NG][4];      // k steps of a group: codes at even, then odd nibbles
+    float start[NG][2];      // -8 sum q of heads 2 c, 2 c + 1
+    float qs[2];             // what the halves are worth
+    {
+        uint32_t top = 0;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const uint32_t w[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+                if (lo < 0x7f80u) top = max(top, lo);
+                if (hi < 0x7f80u) top = max(top, hi);
+            }
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = min(126, 13 + 127 - static_cast<int>(top >> 7));  // >= -114
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);     // 2^e
+        const float unit = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
+        float sum[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const uint32_t w[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = scale_of(w[i >> 1], i & 1) * f;
+            // Nibbles n and n + 4 of a word share a register.
+            qf[g][0] = pack_f16x2(x[0], x[4]);
+            qf[g][1] = pack_f16x2(x[2], x[6]);
+            qf[g][2] = pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f);
+            qf[g][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
+            float2 a[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = __half22float2(*reinterpret_cast<const __half2*>(&qf[g][i]));
+            float t = (a[0].x + a[0].y) + (a[1].x + a[1].y) + 16.f * ((a[2].x + a[2].y) + (a[3].x + a[3].y));
+            t += __shfl_xor_sync(0xffffffffu, t, 1);
+            t += __shfl_xor_sync(0xffffffffu, t, 2);
+            sum[g] = -8.f * kCode * t;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            qs[h] = __shfl_sync(0xffffffffu, unit, 4 * (2 * c + h));
+#pragma unroll
+            for (int g = 0; g < NG; ++g) start[g][h] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * c + h));
+        }
+    }
+
+    const size_t unit0 = static_cast<size_t>(u) * S;
+    uint32_t kw[2][NG], ks[2][NG / 2], vw[4][NG / 2], vs[2][NG / 2];
+    auto tile_slot = [&](uint32_t t, int i) {
+        return unit0 + min(slot0 + static_cast<int>(t >> 16) * 16 + i, S - 1);
+    };
+    auto load_k = [&](uint32_t t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const size_t at = tile_slot(t, r + 8 * h);
+            load_words<NG>(p.k4 + at * (D / 2) + c * (D / 8), kw[h]);
+            load_words<NG / 2>(p.k_scale + at * NG, ks[h]);
+        }
+    };
+    auto load_v = [&](uint32_t t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            load_words<NG / 2>(p.v4 + tile_slot(t, 2 * c + (i & 1) + 8 * (i >> 1)) * (D / 2) + r * (D / 16), vw[i]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_words<NG / 2>(p.v_scale + tile_slot(t, r + 8 * h) * NG, vs[h]);
+    };
+
+    const float NEG = -INFINITY;
+    float acc[2 * NG][4];  // [group][values 4 r + 0, 1 | 2, 3], of heads 2 c and 2 c + 1
+    float off[NG][4];      // 8 sum P s
+#pragma unroll
+    for (int i = 0; i < 2 * NG; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) off[g][0] = off[g][1] = off[g][2] = off[g][3] = 0.f;
+    float m0 = NEG, m1 = NEG, l0 = 0.f, l1 = 0.f;
+    // P s is held as halves of p s 2^(14 - E), 2^E the largest scale's power of
+    // two so far: weights that count keep 11 bits, down to 2^-28 of the largest
+    // possible, and 2^-39 of that is the least that is kept.
+    uint32_t E = 20;
+    float fE = __uint_as_float((14 + 127 + 127 - 20) << 23);
+
+    uint32_t next = 0;
+    if (tiles > 0) {
+        next = s_tiles[warp][0];
+        load_k(next);
+        load_v(next);
+    }
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+        const uint32_t t = next;
+        if (i + 1 < tiles) next = s_tiles[warp][i + 1];
+        const bool liveA = (t >> r) & 1u;
+        const bool liveB = (t >> (r + 8)) & 1u;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float init[4] = {start[g][0], start[g][1], start[g][0], start[g][1]};
+            float sc[4];
+            uint32_t a[4] = {kw[0][g] & 0x000f000fu, kw[1][g] & 0x000f000fu,
+                             (kw[0][g] >> 8) & 0x000f000fu, (kw[1][g] >> 8) & 0x000f000fu};
+            mma_f16_16816(sc, a, qf[g][0], qf[g][1], init);
+            uint32_t o[4] = {kw[0][g] & 0x00f000f0u, kw[1][g] & 0x00f000f0u,
+                             (kw[0][g] >> 8) & 0x00f000f0u, (kw[1][g] >> 8) & 0x00f000f0u};
+            mma_f16_16816(sc, o, qf[g][2], qf[g][3], sc);
+            const float sa = scale_of(ks[0][g >> 1], g & 1), sb = scale_of(ks[1][g >> 1], g & 1);
+            x[0] += sc[0] * sa;
+            x[1] += sc[1] * sa;
+            x[2] += sc[2] * sb;
+            x[3] += sc[3] * sb;
+        }
+        if (i + 1 < tiles) load_k(next);
+        // (In two steps: either factor may be far from 1.)
+        x[0] = liveA ? x[0] * p.unit * qs[0] : NEG;
+        x[1] = liveA ? x[1] * p.unit * qs[1] : NEG;
+        x[2] = liveB ? x[2] * p.unit * qs[0] : NEG;
+        x[3] = liveB ? x[3] * p.unit * qs[1] : NEG;
+        float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        }
+        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+        const float mu0 = mn0 == NEG ? 0.f : mn0, mu1 = mn1 == NEG ? 0.f : mn1;
+        float al0 = ex2_approx(m0 - mu0), al1 = ex2_approx(m1 - mu1);
+        m0 = mn0;
+        m1 = mn1;
+        const float p0 = ex2_approx(x[0] - mu0), p1 = ex2_approx(x[1] - mu1);
+        const float p2 = ex2_approx(x[2] - mu0), p3 = ex2_approx(x[3] - mu1);
+        l0 = l0 * al0 + (p0 + p2);
+        l1 = l1 * al1 + (p1 + p3);
+        // The values' scales; a masked slot's are 0. The largest finite one.
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < NG / 2; ++k) {
+            vs[0][k] = liveA ? vs[0][k] : 0u;
+            vs[1][k] = liveB ? vs[1][k] : 0u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t lo = vs[h][k] & 0x7f80u, hi = (vs[h][k] >> 16) & 0x7f80u;
+                if (lo != 0x7f80u) top = max(top, lo);
+                if (hi != 0x7f80u) top = max(top, hi);
+            }
+        }
+        top = __reduce_max_sync(0xffffffffu, top) >> 7;
+        if (top > E) {
+            const float down = __uint_as_float(static_cast<uint32_t>(max(0, 127 - static_cast<int>(top - E))) << 23);
+            al0 *= down;
+            al1 *= down;
+            E = top;
+            fE = __uint_as_float((14 + 127 + 127 - E) << 23);
+        }
+        if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+#pragma unroll
+            for (int k = 0; k < 2 * NG; ++k) {
+                acc[k][0] *= al0;
+                acc[k][1] *= al1;
+                acc[k][2] *= al0;
+                acc[k][3] *= al1;
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                off[g][0] *= al0;
+                off[g][1] *= al1;
+                off[g][2] *= al0;
+                off[g][3] *= al1;
+            }
+        }
+        const float f0 = p0 * fE, f1 = p1 * fE, f2 = p2 * fE, f3 = p3 * fE;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float sa = scale_of(vs[0][g >> 1], g & 1), sb = scale_of(vs[1][g >> 1], g & 1);
+            const uint32_t b0 = movmatrix_trans(pack_f16x2(f0 * sa, f1 * sa));
+            const uint32_t b1 = movmatrix_trans(pack_f16x2(f2 * sb, f3 * sb));
+            // Slots 2 c and 2 c + 1 side by side: the lane's four codes of group g.
+            const uint32_t pick = g & 1 ? 0x7632u : 0x5410u;
+            const uint32_t ya = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], pick);
+            const uint32_t yb = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], pick);
+            const uint32_t lo[4] = {ya & 0x000f000fu, ya & 0x00f000f0u, yb & 0x000f000fu, yb & 0x00f000f0u};
+            mma_f16_16816(acc[2 * g], lo, b0, b1, acc[2 * g]);
+            const uint32_t za = ya >> 8, zb = yb >> 8;
+            const uint32_t hi[4] = {za & 0x000f000fu, za & 0x00f000f0u, zb & 0x000f000fu, zb & 0x00f000f0u};
+            mma_f16_16816(acc[2 * g + 1], hi, b0, b1, acc[2 * g + 1]);
+            const uint32_t eight[4] = {0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u};
+            mma_f16_16816(off[g], eight, b0, b1, off[g]);
+        }
+        if (i + 1 < tiles) load_v(next);
+    }
+
+    // The four warps' states, joined.
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    const int h0 = 2 * c;
+    if (r == 0) {
+        if (h0 < G) { s_m[warp][h0] = m0; s_l[warp][h0] = l0; }
+        if (h0 + 1 < G) { s_m[warp][h0 + 1] = m1; s_l[warp][h0 + 1] = l1; }
+    }
+    {
+        const float back = __uint_as_float((E + 127 - 127 - 14) << 23);  // 2^(E - 127 - 14)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int dd = 32 * g + 4 * r + 2 * k;
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = (acc[2 * g + k][e] - off[g][e]) * (e < 2 ? 0x1p24f : 0x1p20f) * back;
+                if (h0 < G) { s_o[warp][h0][dd] = v[0]; s_o[warp][h0][dd + 1] = v[2]; }
+                if (h0 + 1 < G) { s_o[warp][h0 + 1][dd] = v[1]; s_o[warp][h0 + 1][dd + 1] = v[3]; }
+            }
+    }
+    __syncthreads();
+    const size_t part = static_cast<size_t>(u) * gridDim.x + blockIdx.x;
+    for (int e = tid; e < G * D; e += kThreads) {
+        const int h = e / D, dd = e % D;
+        float mh = NEG;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mh = fmaxf(mh, s_m[w][h]);
+        float o = 0.f, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            // A warp without a live slot has l = 0 (with one, l is NaN or > 0).
+            if (s_l[w][h] == 0.f) continue;
+            const float f = exp2f(s_m[w][h] - (mh == NEG ? 0.f : mh));
+            o += s_o[w][h][dd] * f;
+            l += s_l[w][h] * f;
+        }
+        if (gridDim.x == 1) {
+            p.out[(row0 + h) * D + dd] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+        } else {
+            p.part_o[part * G * D + e] = o;
+            if (dd == 0) p.part_ml[part * G + h] = make_float2(mh, l);
+        }
+    }
+}
+
+// The chunks of a query row joined: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(kThreads) lf_kv4_join_kernel(const Kv4Params p, int rows, int G, int nchunk) {
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int row = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const int u = row / G, h = row % G;
+    const float2* ml = p.part_ml + static_cast<size_t>(u) * nchunk * G + h;
+    const float* po = p.part_o + (static_cast<size_t>(u) * nchunk * G + h) * D + lane * (D / 32);
+    float m = -INFINITY;
+    for (int k = lane; k < nchunk; k += 32) m = fmaxf(m, ml[static_cast<size_t>(k) * G].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.f;
+    float o[D / 32], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < nchunk; ++k) {
+        const float2 v = ml[static_cast<size_t>(k) * G];
+        const float f = v.y == 0.f ? 0.f : exp2f(v.x - m);
+        l += v.y == 0.f ? 0.f : v.y * f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            const float x = po[static_cast<size_t>(k) * G * D + e];
+            o[e] += v.y == 0.f ? 0.f : x * f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+        p.out[static_cast<size_t>(row) * D + lane * (D / 32) + e] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
+}
+
+// Launch configuration with programmatic dependent launch (LF_PDL=0: without).
+struct Config {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    Config(dim3 grid, int threads, cudaStream_t stream) {
+        const char* env = std::getenv("LF_PDL");
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(threads);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = (env && std::atoi(env) == 0) ? 0 : 1;
+    }
+};
+
+template <int D>
+cudaError_t launch_kv4_d(int G, const Kv4Params& p, int units, int nchunk, cudaStream_t stream) {
+    Config c(dim3(nchunk, units), kThreads, stream);
+    cudaError_t e = cudaErrorInvalidValue;
+    if (G == 1) e = cudaLaunchKernelEx(&c.cfg, lf_kv4_attn_kernel<D, 1>, p);
+    if (G == 2) e = cudaLaunchKernelEx(&c.cfg, lf_kv4_attn_kernel<D, 2>, p);
+    if (G == 4) e = cudaLaunchKernelEx(&c.cfg, lf_kv4_attn_kernel<D, 4>, p);
+    if (G == 8) e = cudaLaunchKernelEx(&c.cfg, lf_kv4_attn_kernel<D, 8>, p);
+    if (e != cudaSuccess || nchunk == 1) return e;
+    const int rows = units * G;
+    Config j(dim3((rows + kWarps - 1) / kWarps), kThreads, stream);
+    return cudaLaunchKernelEx(&j.cfg, lf_kv4_join_kernel<D>, p, rows, G, nchunk);
+}
+
+}  // namespace
+
+Kv4Plan kv4_plan(int units, int S, int sms) {
+    // Four CTAs are resident per SM; chunks of whole 128 slots (32 a warp).
+    const int steps = (S + 127) / 128;
+    const int longest = kMaxChunkSlots / 128;
+    const int fill = std::max(1, 4 * sms / units);
+    const int n = std::max((steps + longest - 1) / longest, std::min(steps, fill));
+    const int per = (steps + n - 1) / n;
+    return Kv4Plan{per * 128, (steps + per - 1) / per};
+}
+
+cudaError_t launch_kv4_attention(int D, int G, const Kv4Params& p, int units, int nchunk,
+                                 cudaStream_t stream) {
+    if (D == 64) return launch_kv4_d<64>(G, p, units, nchunk, stream);
+    if (D == 128) return launch_kv4_d<128>(G, p, units, nchunk, stream);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_kv4_pack(int D, bool unpack, const Kv4PackParams& p, int units, cudaStream_t stream) {
+    Config c(dim3((p.P + kPackSlots - 1) / kPackSlots, units), kPackThreads, stream);
+    if (D == 64)
+        return unpack ? cudaLaunchKernelEx(&c.cfg, lf_kv4_unpack_kernel<64>, p)
+                      : cudaLaunchKernelEx(&c.cfg, lf_kv4_pack_kernel<64>, p);
+    if (D == 128)
+        return unpack ? cudaLaunchKernelEx(&c.cfg, lf_kv4_unpack_kernel<128>, p)
+                      : cudaLaunchKernelEx(&c.cfg, lf_kv4_pack_kernel<128>, p);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace lf

@@ -110,7 +110,7 @@ __device__ __forceinline__ float turns(int n, float f) {
     return bits >> 31 ? -a : a;
 }
 
-template <int D, bool kInterleaved, int kThreads>
+template <int D, bool kInterleaved, int kThreads, bool kAxes>
 __global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
     lf_rope_kernel(const RopeParams p, int tok_per_cta, int tok_ctas, int age_parts) {
     constexpr int kLanes = D / 8;                    // lanes of one head
@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
     constexpr int kMaxTokens = max_tokens(kThreads);
     __shared__ TokenAt at[kMaxTokens];
     __shared__ float2 cs[kMaxTokens][D / 2];
+    __shared__ int axis_pos[kMaxTokens][kMaxAxes];
     const int tid = threadIdx.x;
     allow_dependent_launch();
     grid_dependency_wait();
@@ -202,15 +203,18 @@ __global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
             } else {
                 a.b = -1;
             }
-        } else {
+        } else if (!kAxes) {
             a.pos = p.positions[t];
         }
+        if (kAxes && (tid & 31) < p.axes)
+            axis_pos[i][tid & 31] = p.positions[static_cast<size_t>(tid & 31) * p.T + t];
         if ((tid & 31) == 0) at[i] = a;
     }
     __syncthreads();
     for (int i = tid; i < ntok * half; i += kThreads) {
         const int kk = i / half;
-        const float t = turns(at[kk].pos, __ldg(p.inv_freq + (i - kk * half)));
+        const int pos = kAxes ? axis_pos[kk][p.pair_axis[i - kk * half]] : at[kk].pos;
+        const float t = turns(pos, __ldg(p.inv_freq + (i - kk * half)));
         float s, c;
         sincospif(2.f * t, &s, &c);
         cs[kk][i - kk * half] = make_float2(c, s);
@@ -339,10 +343,11 @@ cudaError_t launch_rope_t(const RopeParams& p, int per, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = (env && std::atoi(env) == 0) ? 0 : 1;
-    const cudaError_t e =
-        p.interleaved
-            ? cudaLaunchKernelEx(&cfg, lf_rope_kernel<D, true, kThreads>, p, per, tok_ctas, parts)
-            : cudaLaunchKernelEx(&cfg, lf_rope_kernel<D, false, kThreads>, p, per, tok_ctas, parts);
+    const auto kernel = p.axes > 0 ? (p.interleaved ? lf_rope_kernel<D, true, kThreads, true>
+                                                    : lf_rope_kernel<D, false, kThreads, true>)
+                                   : (p.interleaved ? lf_rope_kernel<D, true, kThreads, false>
+                                                    : lf_rope_kernel<D, false, kThreads, false>);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, per, tok_ctas, parts);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -55,8 +55,13 @@
 // rank 0 reduces the argmin (top-1 only). A cluster grid of at most one CTA
 // per SM uses a kDeepStages-deep TMA ring, so every tile of a short chunk is
 // in flight at once.
-// An attention-only instantiation (kScore = false) drops the row norms, the
+// An attention-only instantiation (kScore = kNoScore) drops the row norms, the
 // score terms, the ageing and the selection: the baseline for the overhead.
+// One for eviction by accumulated weight (kWeights) drops the row norms alone:
+// its terms are t_hj = log2 exp(s_hj), the sum over the heads is the slot's
+// weight w_j, and where the others rank I_j the scan ranks and stores
+// decay * (what earlier steps left) + w_j. It costs the weights' traffic and
+// saves a third of the products: the Fig. 1 shape took the same time per step.
 // Launches use programmatic dependent launch: a CTA lets the next kernel of
 // the stream start launching as soon as it starts, and waits for the previous
 // one before its first global read.
@@ -81,6 +86,10 @@ constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kThreads = kConsumers + 32;
 constexpr uint32_t kOnesBf16x2 = 0x3F803F80u;   // (1.0, 1.0) in bf16
 constexpr uint32_t kAbsBf16x2 = 0x7FFF7FFFu;
+// What the step ranks its slots by (kScore).
+constexpr int kNoScore = 0;    // nothing: attention alone
+constexpr int kLongFlow = 1;   // LongFlowScore
+constexpr int kWeights = 2;    // the accumulated attention weight
 constexpr int kSlotLive = 1;  // slot flag: age >= 0 after the step's ageing
 constexpr int kSlotOld = 2;   // slot flag: age >= W (may be evicted)
 
@@ -239,7 +248,23 @@ __device__ __forceinline__ float linear_score(const float (&t)[G], const float (
     return I;
 }
 
-// Selection key of a live slot: the bits of log2 I_j mapped so that unsigned
+// The accumulated weight of a live slot: what earlier steps left (nothing in the
+// slot just written, or with decay 0), and this step's weight over the heads.
+template <int G>
+__device__ __forceinline__ float add_weight(const StepParams& p, float old, bool written,
+                                            const float (&t)[G], const float (&c)[G]) {
+    const float kept = (written || p.decay == 0.f) ? 0.f : p.decay * old;
+    return kept + linear_score<G>(t, c) + 0.f;
+}
+
+// c_h = log2(1 / l_h) - m_h: what turns a score term into the weight's log2. A
+// head without any finite logit has no weight to add.
+template <int kScore>
+__device__ __forceinline__ float fold_of(float il, float m) {
+    return kScore == kWeights && il == 0.f ? -INFINITY : __log2f(il) - m;
+}
+
+// Selection key of a live slot: the bits of log2 I_j (or of the weight) mapped so that unsigned
 // order is float order (negative values complemented, the sign bit set on
 // the others). -inf maps to 0x007fffff and +inf to 0xff800000, which leaves
 // key 0 for an empty slot ranked first (fill-empty-first) and 0xffffffff for
@@ -440,7 +465,7 @@ __device__ void select_topk(const StepParams& p, int u, const uint32_t* keys, in
     }
 }
 
-template <int G>
+template <int G, int kScore>
 __device__ void score_and_select(const StepParams& p, int u, const float* s_m, const float* s_il,
                                  float* red_v, int* red_j, int* s_ncand, const int* s_live,
                                  uint8_t* topk_area, uint8_t* scan_area, int scan_bytes,
@@ -453,7 +478,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
 // the output and the scores' normalisation cover the prefix and the slots. A
 // piece with l = 0 holds no key and its output is not read; where the sequence
 // has no prefix, nothing wrote its pieces.
-template <int D, int G, bool kScore, bool kPrefix>
+template <int D, int G, int kScore, bool kPrefix>
 __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usable,
                             uint64_t* scan_bars, int tid) {
     const int nchunk = p.nchunk;
@@ -710,11 +735,12 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
             // once the unit's flag is up: publish c_h, then release the flag
             // after every write it reads (c_h, and through the arrival
             // counter, the chunks' score terms and ages).
-            if (tid < G) p.cfold[static_cast<size_t>(u) * G + tid] = __log2f(s_il[tid]) - s_m[tid];
+            if (tid < G)
+                p.cfold[static_cast<size_t>(u) * G + tid] = fold_of<kScore>(s_il[tid], s_m[tid]);
             consumer_bar_sync();
             if (tid == 0) st_release_gpu(p.ready + u, 1u);  // after the barrier: the CTA's writes
         } else {
-            score_and_select<G>(p, u, s_m, s_il, red_v, red_j, s_ncand, s_live, topk_area,
+            score_and_select<G, kScore>(p, u, s_m, s_il, red_v, red_j, s_ncand, s_live, topk_area,
                                 scan_area, scan_bytes, scan_bars, tid);
         }
     }
@@ -763,9 +789,10 @@ constexpr int kBulkScanMinSlots = 4096;
 // The live-tile list of the top-1 register scan holds at most this many tiles.
 constexpr int kMaxScanTiles = 1024;
 
-// LongFlowScore of every live slot of unit u and the selection of the slots to
-// evict, by the unit's last CTA once the final (m_h, l_h) are known.
-template <int G>
+// LongFlowScore (or the accumulated weight) of every live slot of unit u and the
+// selection of the slots to evict, by the unit's last CTA once the final
+// (m_h, l_h) are known.
+template <int G, int kScore>
 __device__ void score_and_select(const StepParams& p, int u, const float* s_m, const float* s_il,
                                  float* red_v, int* red_j, int* s_ncand, const int* s_live,
                                  uint8_t* topk_area, uint8_t* scan_area, int scan_bytes,
@@ -775,7 +802,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
     // I_j = sum_h 2^(t_hj - m_h) / l_h = sum_h 2^(t_hj + c_h), c_h = log2(1/l_h) - m_h.
     float c[G];
 #pragma unroll
-    for (int h = 0; h < G; ++h) c[h] = __log2f(s_il[h]) - s_m[h];
+    for (int h = 0; h < G; ++h) c[h] = fold_of<kScore>(s_il[h], s_m[h]);
     const int S = p.S;
     const int nchunk = p.nchunk;
     const int cs = p.chunk_tiles * kTile;
@@ -784,6 +811,9 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
     // For top-k the slot's first stash word is reused for its selection key.
     uint32_t* keys = reinterpret_cast<uint32_t*>(stash);
     float* scores = p.scores ? p.scores + static_cast<size_t>(u) * S : nullptr;
+    constexpr bool kAdd = kScore == kWeights;
+    float* weights = kAdd ? p.weights + static_cast<size_t>(u) * S : nullptr;
+    const int ws = kAdd ? p.write_slot[u] : -1;
     const bool fill_first = (p.flags & kFlagFillEmptyFirst) != 0;
     const bool top1 = p.topk == 1;
     // Chunks without a live slot hold no scored candidate; they are visited
@@ -796,9 +826,10 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
     int bestj = 0x7fffffff;
     int ncand = 0;
 
-    auto visit = [&](int j, int a, const float (&t)[G]) {
-        const float L = log2_score<G>(t, c);
+    auto visit = [&](int j, int a, const float (&t)[G], float old) {
+        const float L = kAdd ? add_weight<G>(p, old, j == ws, t, c) : log2_score<G>(t, c);
         const bool live = a >= 0;
+        if (kAdd && live) weights[j] = L;
         const bool cand = live ? (a >= W && L == L) : fill_first;
         const uint32_t key = live ? ordered_key(L) : 0u;
         if (top1) {
@@ -826,7 +857,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
     // A long scan streams each segment's ages and score terms into shared memory
     // with bulk copies, two segments in flight, so it runs at L2 bandwidth
     // instead of one round trip per slot.
-    constexpr int kSlotBytes = (G + 1) * 4;
+    constexpr int kSlotBytes = (G + 1 + (kAdd ? 1 : 0)) * 4;
     int seg = (scan_bytes / 2) / kSlotBytes;
     seg = min(2048, seg & ~(kConsumers - 1));
     // Short units are cheaper with loads batched in registers (one or two
@@ -838,7 +869,8 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
         live_tiles += __popc(static_cast<uint32_t>(s_live[c]));
     }
     const bool bulk = seg >= kConsumers && nlive * cs > kBulkScanMinSlots && (S & 3) == 0 &&
-                      (reinterpret_cast<uintptr_t>(p.mask) & 15) == 0;
+                      (reinterpret_cast<uintptr_t>(p.mask) & 15) == 0 &&
+                      (!kAdd || (reinterpret_cast<uintptr_t>(p.weights) & 15) == 0);
     if (bulk) {
         const int half = seg * kSlotBytes;
         uint8_t* buf0 = reinterpret_cast<uint8_t*>(
@@ -865,6 +897,8 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
             bulk_load(b, age + wi.j0, static_cast<uint32_t>(n * 4), bar);
             bulk_load(b + seg * 4, stash + static_cast<size_t>(wi.j0) * G,
                       static_cast<uint32_t>(n * G * 4), bar);
+            if constexpr (kAdd)
+                bulk_load(b + seg * (G + 1) * 4, weights + wi.j0, static_cast<uint32_t>(n * 4), bar);
             seg_advance(wi, cs, seg, S, nchunk, s_live, all);
         };
         if (tid == 0) {
@@ -885,6 +919,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
             }
             const int32_t* s_age = reinterpret_cast<const int32_t*>(buf0 + b * half);
             const float* s_t = reinterpret_cast<const float*>(buf0 + b * half + seg * 4);
+            const float* s_old = s_t + seg * G;  // (kAdd)
             const int n = seg_end(wc, seg) - wc.j0;
 #pragma unroll 4
             for (int i = tid; i < n; i += kConsumers) {
@@ -902,7 +937,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
 #pragma unroll
                     for (int h = 0; h < G; ++h) t[h] = s_t[i * G + h];
                 }
-                visit(wc.j0 + i, s_age[i], t);
+                visit(wc.j0 + i, s_age[i], t, kAdd ? s_old[i] : 0.f);
             }
             consumer_bar_sync();  // everyone is done with buffer b
             if (tid == 0 && wi.j0 < S) issue(issued++);
@@ -935,11 +970,13 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
             int a[kBatch];
             int jj[kBatch];
             float t[kBatch][G];
+            float old[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int i = i0 + k * kConsumers;
                 jj[k] = (i < nslots) ? s_tl[i >> 6] * kTile + (i & (kTile - 1)) : S;
                 a[k] = (jj[k] < S) ? __ldcg(&age[jj[k]]) : -1;
+                old[k] = (kAdd && jj[k] < S) ? weights[jj[k]] : 0.f;
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
@@ -947,7 +984,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 if (jj[k] >= S) break;
-                visit(jj[k], a[k], t[k]);
+                visit(jj[k], a[k], t[k], old[k]);
             }
         }
     } else {
@@ -958,10 +995,12 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
         for (int j0 = tid; j0 < S; j0 += kBatch * kConsumers) {
             int a[kBatch];
             float t[kBatch][G];
+            float old[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int j = j0 + k * kConsumers;
                 a[k] = (j < S) ? __ldcg(&age[j]) : -1;
+                old[k] = (kAdd && j < S) ? weights[j] : 0.f;
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
@@ -972,7 +1011,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
             for (int k = 0; k < kBatch; ++k) {
                 const int j = j0 + k * kConsumers;
                 if (j >= S) break;
-                visit(j, a[k], t[k]);  // a slot of a chunk with no live slot is no candidate
+                visit(j, a[k], t[k], old[k]);  // a slot of a chunk with no live slot is no candidate
             }
         }
     }
@@ -1045,16 +1084,20 @@ __device__ __forceinline__ void preload_terms(const StepParams& p, int u, int sl
 // tid takes slots tid, tid + 128, ...) from their score terms and c_h, the
 // score export, and the thread's best candidate (key, slot): key 0xffffffff
 // and slot 0x7fffffff when it has none. t0 holds the first batch when
-// kPreloaded.
-template <int G, bool kPreloaded, bool kSmemTerms = false>
+// kPreloaded; old0 the first batch's accumulated weights (kWeights), ws the
+// written slot.
+template <int G, int kScore, bool kPreloaded, bool kSmemTerms = false>
 __device__ __forceinline__ void score_chunk(const StepParams& p, int u, int slot0, int n,
                                             const uint8_t* sflags, const float (&cexp)[G],
-                                            const float (&t0)[kScoreBatch][G], int tid,
+                                            const float (&t0)[kScoreBatch][G],
+                                            const float (&old0)[kScoreBatch], int ws, int tid,
                                             uint32_t& bkey, int& bestj,
                                             const float* sterm = nullptr) {
     const int S = p.S;
     const float* stash = p.stash + static_cast<size_t>(u) * S * G;
     float* scores = p.scores ? p.scores + static_cast<size_t>(u) * S : nullptr;
+    constexpr bool kAdd = kScore == kWeights;
+    float* weights = kAdd ? p.weights + static_cast<size_t>(u) * S + slot0 : nullptr;
     const bool fill_first = (p.flags & kFlagFillEmptyFirst) != 0;
     // A thread visits its slots in increasing order, so a strict "<" on
     // the key (ordered_key(log2 I_j); 0 for an empty slot under
@@ -1066,7 +1109,7 @@ __device__ __forceinline__ void score_chunk(const StepParams& p, int u, int slot
         // computed without a branch between them, so their dependent chains
         // interleave (one warp per SM sub-partition hides no latency here).
         constexpr int kB = 2;
-        for (int i0 = tid; i0 < n; i0 += kB * kConsumers) {
+        const auto round = [&](int i0, const float (&old)[kB]) {
             float L[kB], t[kB][G];
             int f[kB];
 #pragma unroll
@@ -1079,7 +1122,9 @@ __device__ __forceinline__ void score_chunk(const StepParams& p, int u, int slot
 #pragma unroll
                     for (int h = 0; h < G; ++h) t[k][h] = -INFINITY;
                 }
-                L[k] = log2_score<G>(t[k], cexp);
+                L[k] = kAdd ? add_weight<G>(p, old[k], slot0 + i == ws, t[k], cexp)
+                            : log2_score<G>(t[k], cexp);
+                if (kAdd && (f[k] & kSlotLive)) weights[i] = L[k];
             }
 #pragma unroll
             for (int k = 0; k < kB; ++k) {
@@ -1097,10 +1142,31 @@ __device__ __forceinline__ void score_chunk(const StepParams& p, int u, int slot
                         scores[j] = live ? exported_score<G>(p, L[k], t[k], cexp) : INFINITY;
                 }
             }
+        };
+        int i0 = tid;
+        if constexpr (kAdd) {
+#pragma unroll
+            for (int q = 0; q < kScoreBatch; q += kB) {
+                if (i0 < n) round(i0, {old0[q], old0[q + 1]});
+                i0 += kB * kConsumers;
+            }
+        }
+        for (; i0 < n; i0 += kB * kConsumers) {
+            float old[kB];
+#pragma unroll
+            for (int k = 0; k < kB; ++k)
+                old[k] = (kAdd && i0 + k * kConsumers < n) ? weights[i0 + k * kConsumers] : 0.f;
+            round(i0, old);
         }
     } else {
         for (int i0 = tid; i0 < n; i0 += kScoreBatch * kConsumers) {
             float t[kScoreBatch][G];
+            float old[kScoreBatch];
+#pragma unroll
+            for (int k = 0; k < kScoreBatch; ++k) {
+                const int i = i0 + k * kConsumers;
+                old[k] = i0 == tid ? old0[k] : (kAdd && i < n) ? weights[i] : 0.f;
+            }
             if (kPreloaded && i0 == tid) {
 #pragma unroll
                 for (int k = 0; k < kScoreBatch; ++k)
@@ -1120,8 +1186,10 @@ __device__ __forceinline__ void score_chunk(const StepParams& p, int u, int slot
                 if (i >= n) break;
                 const int f = sflags[i];
                 const int j = slot0 + i;
-                const float L = log2_score<G>(t[k], cexp);
                 const bool live = (f & kSlotLive) != 0;
+                const float L = kAdd ? add_weight<G>(p, old[k], j == ws, t[k], cexp)
+                                     : log2_score<G>(t[k], cexp);
+                if (kAdd && live) weights[i] = L;
                 const bool cand = live ? ((f & kSlotOld) && L == L) : fill_first;
                 const uint32_t key = live ? ordered_key(L) : 0u;
                 if (cand && key < bkey) {
@@ -1156,7 +1224,7 @@ __device__ __forceinline__ void warp_best_redux(uint32_t& bkey, int& bestj) {
 // reduces the cluster's argmin. No cluster barrier follows the main loop:
 // every store into a CTA is counted on one of its barriers, and a CTA leaves
 // only after its own have completed.
-template <int D, int G, int kStages, bool kScore, bool kSmemTerms>
+template <int D, int G, int kStages, int kScore, bool kSmemTerms>
 __device__ __forceinline__ void cluster_merge_push(const StepParams& p, int u, int slot0, int n,
                                                    const uint8_t* sflags, uint8_t* smem,
                                                    uint8_t* pbase, uint8_t* wstage,
@@ -1198,6 +1266,14 @@ __device__ __forceinline__ void cluster_merge_push(const StepParams& p, int u, i
     // these loads.
     constexpr bool kPreload = kScore && !kSmemTerms && (G <= 4 || kStages == kDeepStages);
     float t0[kScoreBatch][G];
+    // The accumulated weights of the first batch, requested likewise.
+    float old0[kScoreBatch];
+#pragma unroll
+    for (int k = 0; k < kScoreBatch; ++k) {
+        const int i = tid + k * kConsumers;
+        old0[k] = (kScore == kWeights && i < n) ? p.weights[static_cast<size_t>(u) * p.S + slot0 + i] : 0.f;
+    }
+    const int ws = kScore == kWeights ? p.write_slot[u] : -1;
     if constexpr (!kStageOutside) {
         consumer_bar_sync();
         if constexpr (kPreload) preload_terms<G>(p, u, slot0, n, sflags, tid, t0);
@@ -1318,10 +1394,10 @@ __device__ __forceinline__ void cluster_merge_push(const StepParams& p, int u, i
     if constexpr (kScore) {
         float cexp[G];
 #pragma unroll
-        for (int h = 0; h < G; ++h) cexp[h] = __log2f(s_il[h]) - s_m[h];
+        for (int h = 0; h < G; ++h) cexp[h] = fold_of<kScore>(s_il[h], s_m[h]);
         // (Terms in shared memory: the barrier after the staging ordered them.)
-        score_chunk<G, kPreload, kSmemTerms>(p, u, slot0, n, sflags, cexp, t0, tid, bkey, bestj,
-                                             sterm);
+        score_chunk<G, kScore, kPreload, kSmemTerms>(p, u, slot0, n, sflags, cexp, t0, old0, ws, tid,
+                                                     bkey, bestj, sterm);
         warp_best_redux(bkey, bestj);
         if (lane == 0) {
             red_k[warp] = bkey;
@@ -1404,7 +1480,7 @@ __device__ __forceinline__ void arm_receive(uint64_t* bar, uint32_t bytes) {
 // owns and, at rank 0, their (key, slot) pairs. The (m, l) and output
 // barriers also count the four consumer warps' arrivals for their local
 // stores.
-template <int D, int G, bool kScore>
+template <int D, int G, int kScore>
 __device__ __forceinline__ void push_barriers_init(uint8_t* pbase, int nchunk) {
     using P = PushSmem<D, G>;
     uint64_t* bar_ml = reinterpret_cast<uint64_t*>(pbase + P::kBarOff);
@@ -1427,7 +1503,7 @@ __device__ __forceinline__ void push_barriers_init(uint8_t* pbase, int nchunk) {
 // kCluster: the grid is launched in clusters of nchunk CTAs (one per unit).
 // kPrefix: the merge adds the pieces of a shared-prefix attention (StepParams
 // pre_*), computed by the kernel before this one; not with kCluster.
-template <int D, int G, int kStages, bool kScore, bool kCluster, bool kPrefix = false>
+template <int D, int G, int kStages, int kScore, bool kCluster, bool kPrefix = false>
 __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2 : 1))
     lf_decode_step_kernel(const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const StepParams p) {
@@ -1737,7 +1813,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
                 uint32_t a[4];
                 ldsm_x4(kbase + off, a);
                 mma_bf16_16816(odd ? sc1 : sc, a, qf[kk][0], qf[kk][1]);
-                if constexpr (kScore) {
+                if constexpr (kScore == kLongFlow) {
                     uint32_t v[4];
                     ldsm_x4(vbase + off, v);
 #pragma unroll
@@ -1760,19 +1836,19 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
         const float x2 = (liveB && hv0) ? sc[2] * sl : NEG;
         const float x3 = (liveB && hv1) ? sc[3] * sl : NEG;
 
-        // Per-slot score terms t = log2(exp(s) * ||v||_1).
+        // Per-slot score terms t = log2(exp(s) * ||v||_1), or log2 exp(s).
         if (kScore && hv0) {
             const int slotA = tslot0 + wrow0 + r;
             float* st = A::kSmemTerms
                             ? sterm + (slotA - slot0) * G + h0
                             : p.stash + (static_cast<size_t>(u) * S + slotA) * G + h0;
             if (liveA) {
-                const float lv = __log2f(nv[0]);
+                const float lv = kScore == kLongFlow ? __log2f(nv[0]) : 0.f;
                 if (G == 1) st[0] = x0 + lv;
                 else *reinterpret_cast<float2*>(st) = make_float2(x0 + lv, x1 + lv);
             }
             if (liveB) {
-                const float lv = __log2f(nv[2]);
+                const float lv = kScore == kLongFlow ? __log2f(nv[2]) : 0.f;
                 if (G == 1) st[8 * G] = x2 + lv;
                 else *reinterpret_cast<float2*>(st + 8 * G) = make_float2(x2 + lv, x3 + lv);
             }
@@ -1934,7 +2010,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
 
 // Sets the kernel's function attributes (shared memory above 48 KB; cluster
 // instances: clusters of more than 8 CTAs, an opt-in size) once per device.
-template <int D, int G, int kStages, bool kScore, bool kCluster, bool kPrefix = false>
+template <int D, int G, int kStages, int kScore, bool kCluster, bool kPrefix = false>
 cudaError_t configure_t() {
     using A = StepAlloc<D, G, kStages, kCluster>;
     auto kernel = lf_decode_step_kernel<D, G, kStages, kScore, kCluster, kPrefix>;
@@ -1956,7 +2032,7 @@ cudaError_t configure_t() {
 
 // How many clusters of `csize` CTAs of the cluster instance can be resident
 // at once on the current device (0: none, or the query failed).
-template <int D, int G, int kStages, bool kScore>
+template <int D, int G, int kStages, int kScore>
 int max_active_clusters_t(int csize) {
     if (configure_t<D, G, kStages, kScore, true>() != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
@@ -1981,7 +2057,7 @@ int max_active_clusters_t(int csize) {
 
 // How many CTAs of the (non-cluster) instance are resident at once on the
 // current device: the grid's first wave. Cached per device.
-template <int D, int G, int kStages, bool kScore, bool kPrefix = false>
+template <int D, int G, int kStages, int kScore, bool kPrefix = false>
 int first_wave_t() {
     static int cached_for = -1;
     static int ctas = 0;
@@ -2002,7 +2078,7 @@ int first_wave_t() {
     return ctas;
 }
 
-template <int D, int G, int kStages, bool kScore, bool kCluster, bool kPrefix = false>
+template <int D, int G, int kStages, int kScore, bool kCluster, bool kPrefix = false>
 cudaError_t launch_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepParams& p_in,
                      int units, cudaStream_t stream, bool pdl) {
     using L = StepSmem<D, kStages>;

@@ -109,12 +109,14 @@ typedef enum lf_status {
  * and the argmin of every chunk in parallel, each unit as soon as the
  * decode-step kernel has merged it (the two kernels overlap).
  */
-#define LF_KERNEL_DECODE_STEP 0 /* slot write, mask ageing, attention (+ score, eviction) */
+#define LF_KERNEL_DECODE_STEP 0 /* slot write, mask ageing, attention (+ score or weights, eviction) */
 #define LF_KERNEL_ATTENTION 1   /* lf_decode_attention: slot write and attention only */
 #define LF_KERNEL_SCORE 2       /* split finish: LongFlowScore and eviction */
-#define LF_KERNEL_NORM_ROPE 3        /* lf_qk_norm_rope, lf_prefill_append */
+#define LF_KERNEL_NORM_ROPE 3        /* lf_qk_norm_rope, lf_prefill_append, and with axes */
 #define LF_KERNEL_PACKED_ATTENTION 4 /* lf_window_attention; the prefix part of lf_decode_*_prefix */
-#define LF_KERNEL_COUNT 5
+#define LF_KERNEL_KV4 5              /* lf_kv4_pack, lf_kv4_unpack, lf_decode_attention_kv4 */
+#define LF_KERNEL_PROMPT_WEIGHTS 6   /* lf_prompt_weights */
+#define LF_KERNEL_COUNT 7
 
 /* Flags of lf_decode_step_ex. */
 #define LF_STEP_FILL_EMPTY_FIRST 0x1 /* return empty (masked) slots, lowest first, before any score */
@@ -375,6 +377,32 @@ lf_status lf_prefill_append(const void* qkv, int64_t qkv_stride, const void* q_w
                             void* stream);
 
 /*
+ * Both with positions on several axes (the time, height and width of image and
+ * video tokens): pair i of row t turns by its position on axis pair_axis[i].
+ *
+ * positions  in  int32 [axes][T] on the device: the rotation's positions of
+ *                every row of qkv. (In lf_prefill_append_axes the slots still
+ *                follow q_start and kv_len.)
+ * pair_axis  in  uint8 [rot / 2] on the HOST, values below axes: sections of
+ *                pairs per axis, or axes that take turns. Read during the call.
+ * axes           1 .. LF_MAX_AXES
+ * The other arguments are those of the calls above.
+ */
+#define LF_MAX_AXES 4
+lf_status lf_qk_norm_rope_axes(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                               const void* k_weight, const float* inv_freq,
+                               const int32_t* positions, const uint8_t* pair_axis, int axes,
+                               void* q_out, void* k_out, void* v_out, int T, int Hq, int Hkv,
+                               int d, int rot, int interleaved, float eps, void* stream);
+lf_status lf_prefill_append_axes(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                                 const void* k_weight, const float* inv_freq,
+                                 const int32_t* q_start, const int32_t* kv_len,
+                                 const int32_t* positions, const uint8_t* pair_axis, int axes,
+                                 void* q_out, void* k_cache, void* v_cache, int32_t* mask, int T,
+                                 int B, int Hq, int Hkv, int d, int S, int rot, int interleaved,
+                                 float eps, void* stream);
+
+/*
  * Attention over in-order caches with a sliding window and visible first
  * tokens: whole prompts, chunks of prompts and single tokens of a batch.
  *
@@ -434,6 +462,104 @@ lf_status lf_decode_attention_prefix(const void* q, void* k_cache, void* v_cache
 /* Workspace bytes of either call, for any k and flags. */
 lf_status lf_decode_prefix_workspace(int B, int Hq, int Hkv, int d, int S, int N, int P,
                                      size_t* bytes);
+
+/*
+ * Eviction by accumulated attention weight: a slot is worth what the tokens so
+ * far have attended to it, not what the current one does (LongFlowScore).
+ *
+ * lf_decode_step_weights: the decode step that keeps that sum. With p the step's
+ * final weights, every live slot's becomes
+ *     weights[j] = decay * weights[j] + sum over the unit's heads h of p[h][j],
+ * starting from 0 in the slot that the step writes, and the step returns the k
+ * slots with the lowest (weights[j], slot) among live slots of age >= W.
+ *
+ * weights    in/out float [B][Hkv][S]: entries of masked slots are neither read
+ *                nor written. A slot whose sum is NaN is never returned.
+ * decay      0 <= decay <= 1 (1: the plain sum; 0: the current step's weights)
+ * next_slots, k, flags   as in lf_decode_step_ex (without LF_STEP_LOG2_SCORES)
+ * The other arguments are those of lf_decode_step. weights must not overlap the
+ * other arrays, nor out q.
+ */
+lf_status lf_decode_step_weights(const void* q, void* k_cache, void* v_cache, int32_t* mask,
+                                 float* weights, const void* new_k, const void* new_v,
+                                 const int32_t* write_slot, void* out, int32_t* next_slots, int k,
+                                 int flags, int B, int Hq, int Hkv, int d, int S, int W,
+                                 float scale, float decay, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+/* Workspace bytes of that call. */
+lf_status lf_decode_weights_workspace(int B, int Hq, int Hkv, int d, int S, int k, size_t* bytes);
+
+/*
+ * What a prompt leaves to start from: the attention weights that the last rows of
+ * each sequence give its keys (causal, softmax(scale * q.k)), summed over those
+ * rows and the heads of a KV head.
+ *
+ * q          in  bf16 [T][Hq][d]; q_start, kv_len as in lf_prefill_append
+ * k_cache    in  bf16 [B][Hkv][S][d], tokens in slot order
+ * rows           how many of a sequence's last rows count (0: all of them)
+ * weights    in/out float [B][Hkv][S]: the slots of this call's tokens (the last
+ *                q_start[b + 1] - q_start[b] below kv_len[b]) are set, those of
+ *                earlier chunks added to; slots from kv_len[b] on stay.
+ * Slots from kv_len[b] on, and keys a row does not see, may hold anything. With a
+ * q_start that does not ascend, other sequences may be skipped too.
+ */
+lf_status lf_prompt_weights(const void* q, const void* k_cache, const int32_t* q_start,
+                            const int32_t* kv_len, float* weights, int T, int B, int Hq, int Hkv,
+                            int d, int S, int rows, float scale, void* workspace,
+                            size_t workspace_bytes, void* stream);
+/* Workspace bytes of that call. */
+lf_status lf_prompt_weights_workspace(int T, int B, int Hq, int Hkv, int d, int S, int rows,
+                                      size_t* bytes);
+
+/*
+ * A cache held in 4 bits: 4.5 bits a value, 3.56 times fewer bytes per step.
+ *
+ * A row of d values has d / 32 groups of 32 values. A group's scale s is its
+ * largest magnitude over 7, rounded to bf16; a value's code is x / s rounded to
+ * the nearest integer (ties to even), -7 .. 7, and stands for code * s. A group
+ * of zeros has s = 0; one with a value that is not finite stands for NaN.
+ *
+ * k4, v4     uint8 [B][Hkv][S][d / 2]   codes plus 8, two a byte, low nibble
+ *            first: value c of group g in nibble ((r / e) * (d / 32) + g) * e +
+ *            r % e of the row, r = c % 32, with e = 8 in k4 and e = 4 in v4
+ * k_scale,
+ * v_scale    bf16 [B][Hkv][S][d / 32]
+ * All four 16-byte aligned.
+ *
+ * lf_kv4_pack: slots kv_from[b] .. kv_len[b] - 1 of bf16 caches (a prompt's, after
+ * lf_prefill_append) into the same slots of the 4-bit cache; the other slots stay.
+ * k_cache,
+ * v_cache    in  bf16 [B][Hkv][P][d]
+ * kv_from    in  int32 [B], or NULL: 0
+ * kv_len     in  int32 [B], kv_from[b] <= kv_len[b] <= min(P, S)
+ * mask       in/out int32 [B][Hkv][S]: slots below kv_len[b] get the ages of an
+ *                in-order cache, as in lf_prefill_append
+ * lf_kv4_unpack: the values of those slots back into bf16 caches (rounded once),
+ * for the next chunk's lf_window_attention; their other rows stay.
+ */
+lf_status lf_kv4_pack(const void* k_cache, const void* v_cache, const int32_t* kv_from,
+                      const int32_t* kv_len, void* k4, void* k_scale, void* v4, void* v_scale,
+                      int32_t* mask, int B, int Hkv, int d, int P, int S, void* stream);
+lf_status lf_kv4_unpack(const void* k4, const void* k_scale, const void* v4, const void* v_scale,
+                        const int32_t* kv_from, const int32_t* kv_len, void* k_cache,
+                        void* v_cache, int B, int Hkv, int d, int P, int S, void* stream);
+
+/*
+ * lf_decode_attention over a 4-bit cache: the token's row is put into 4 bits in
+ * write_slot, then every live slot, that one included, is attended as the
+ * values that its codes stand for. The arithmetic is fp32 with weights of 11
+ * bits; outputs are rounded to bf16 once. Of the values, what is below 2^-38 of
+ * the sequence's largest is lost, and finite logits are expected.
+ * new_k, new_v in bf16 [B][Hkv][d]; the other arguments as above and in
+ * lf_decode_attention.
+ */
+lf_status lf_decode_attention_kv4(const void* q, void* k4, void* k_scale, void* v4, void* v_scale,
+                                  int32_t* mask, const void* new_k, const void* new_v,
+                                  const int32_t* write_slot, void* out, int B, int Hq, int Hkv,
+                                  int d, int S, float scale, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+/* Workspace bytes of that call (may be 0: workspace may then be NULL). */
+lf_status lf_decode_kv4_workspace(int B, int Hq, int Hkv, int d, int S, size_t* bytes);
 
 /*
  * The launch plan lf_decode_step / lf_decode_step_ex (k = topk, score on)

@@ -1,0 +1,678 @@
+"""Rotation with axes, eviction by accumulated weight and the 4-bit cache against
+their plain fp64 definitions (tests/_plain_long.py, which also derives the bounds)."""
+import math
+
+import pytest
+import torch
+
+import decode_kv_cache_step_gb300 as lf
+
+import _plain
+import _plain_long as plain
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+NAN, INF = float("nan"), float("inf")
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape):
+    return torch.randn(shape, generator=g).to(BF).cuda()
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def near(got, ref, tol, what=""):
+    got = got.double().cpu()
+    bad = ~((got - ref).abs() <= tol)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} outside, first at "
+                           f"{torch.nonzero(bad)[0].tolist()}: {got[bad][0]} vs {ref[bad][0]} "
+                           f"+- {tol[bad][0]}")
+
+
+def no_errors():
+    assert lf.device_errors(clear=True) == 0
+
+
+# --------------------------------------------------------- rotation by axes --
+
+AXES = [  # T, Hq, Hkv, d, rot, interleaved, norm, axes
+    (1, 32, 8, 128, 128, False, True, 3), (7, 8, 1, 64, 64, True, True, 2),
+    (33, 6, 3, 128, 48, False, False, 4), (130, 4, 4, 64, 16, True, False, 1),
+    (700, 2, 1, 128, 112, False, True, 3), (7001, 1, 1, 64, 32, True, True, 3)]
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,d,rot,inter,norm,axes", AXES)
+def test_axes(T, Hq, Hkv, d, rot, inter, norm, axes):
+    g = gen(T + rot)
+    wide = normal(g, T, Hq + 2 * Hkv + 1, d)
+    qkv = wide[:, :Hq + 2 * Hkv]                      # strided rows
+    wq, wk = (normal(g, d), normal(g, d)) if norm else (None, None)
+    freq = (1e4 ** (-torch.arange(rot // 2).double() * 2 / rot)).float().cuda()
+    pos = torch.randint(-1000, 1 << 20, (axes, T), generator=g, dtype=torch.int32)
+    pos[0, 0], pos[-1, -1] = 0, (1 << 31) - 1
+    pair = torch.randint(0, axes, (rot // 2,), generator=g).tolist()
+    q = torch.empty(T, Hq, d, dtype=BF, device="cuda")
+    k, v = (torch.empty(T, Hkv, d, dtype=BF, device="cuda") for _ in range(2))
+    lf.qk_norm_rope_axes(qkv, wq, wk, freq, pos.cuda(), pair, q, k, v, 1e-6, interleaved=inter)
+    for got, x, w in ((q, qkv[:, :Hq], wq), (k, qkv[:, Hq:Hq + Hkv], wk)):
+        ref = plain.axes_rope(x, w, freq, pos, pair, 1e-6, inter)
+        near(got, ref, _plain.rope_bound(ref))
+    assert torch.equal(v, qkv[:, Hq + Hkv:])
+    no_errors()
+
+
+@pytest.mark.parametrize("T,d,rot,inter", [(1, 128, 128, False), (90, 64, 32, True), (6500, 64, 64, False)])
+def test_equal_axes_are_one_axis(T, d, rot, inter):
+    """Text: the same position on every axis gives the bits of the rotation without axes."""
+    g = gen(T)
+    qkv, w = normal(g, T, 8, d), normal(g, d)
+    freq = (1e6 ** (-torch.arange(rot // 2).double() * 2 / rot)).float().cuda()
+    pos = torch.randint(0, 1 << 17, (T,), generator=g, dtype=torch.int32).cuda()
+    a, b = ([torch.empty(T, h, d, dtype=BF, device="cuda") for h in (4, 2, 2)] for _ in range(2))
+    lf.qk_norm_rope(qkv, w, w, freq, pos, *a, interleaved=inter)
+    lf.qk_norm_rope_axes(qkv, w, w, freq, pos.expand(3, T).contiguous(), torch.arange(rot // 2) % 3, *b,
+                         interleaved=inter)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("nq,kv,S,extra", [
+    ([5, 0, 17], [5, 0, 20], 24, 3), ([130, 257], [130, 300], 301, 11),
+    ([3000, 0, 1, 3500], [3100, 0, 1, 3501], 3601, 5)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (8, 1, 128)])
+def test_append_axes(nq, kv, S, extra, Hq, Hkv, d):
+    g = gen(S)
+    B, T = len(nq), sum(nq) + extra
+    starts = [sum(nq[:i]) for i in range(B + 1)]
+    qkv, w = normal(g, T, Hq + 2 * Hkv, d), normal(g, d)
+    freq = (1e4 ** (-torch.arange(d // 2).double() * 2 / d)).float().cuda()
+    pos = torch.randint(0, 5000, (3, T), generator=g, dtype=torch.int32)
+    pair = [i % 3 for i in range(d // 2)]
+    q, k, v = normal(g, T, Hq, d), normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    mask = torch.full((B, Hkv, S), -1, dtype=torch.int32, device="cuda")
+    q0, k0, v0 = q.clone(), k.clone(), v.clone()
+    lf.prefill_append_axes(qkv, w, w, freq, ints(starts), ints(kv), pos.cuda(), pair, q, k, v, mask)
+    assert torch.equal(q[sum(nq):], q0[sum(nq):])
+    for b in range(B):
+        rows, at = slice(starts[b], starts[b + 1]), slice(kv[b] - nq[b], kv[b])
+        ref = plain.axes_rope(qkv[rows, :Hq], w, freq, pos[:, rows], pair, 1e-6, False)
+        near(q[rows], ref, _plain.rope_bound(ref))
+        ref = plain.axes_rope(qkv[rows, Hq:Hq + Hkv], w, freq, pos[:, rows], pair, 1e-6, False)
+        near(k[b, :, at].transpose(0, 1), ref, _plain.rope_bound(ref))
+        assert torch.equal(v[b, :, at].transpose(0, 1), qkv[rows, Hq + Hkv:])
+        k0[b, :, at], v0[b, :, at] = k[b, :, at], v[b, :, at]
+        want = torch.full((S,), -1, dtype=torch.int32)
+        want[:kv[b]] = torch.arange(kv[b] - 1, -1, -1)
+        assert torch.equal(mask[b].cpu(), want.expand(Hkv, S))
+    assert torch.equal(k, k0) and torch.equal(v, v0)  # every other slot as it was
+    no_errors()
+
+
+# ------------------------------------------------- the step with its weights --
+
+def step_case(g, B, Hq, Hkv, d, S, live=None, holes=0.1):
+    mask = torch.randint(0, S, (B, Hkv, S), generator=g, dtype=torch.int32)
+    mask[torch.rand((B, Hkv, S), generator=g) < holes] = -1
+    for b in range(B if live is not None else 0):
+        mask[b, :, live[b % len(live)]:] = -1
+    dead = mask < 0
+    k, v = normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    w = torch.exp(torch.randn((B, Hkv, S), generator=g))
+    # What masked slots hold does not matter.
+    k[dead.cuda()], v[dead.cuda()] = NAN, INF
+    w[dead] = NAN
+    return dict(q=normal(g, B, Hq, d), k=k, v=v, mask=mask.cuda(), weights=w.cuda(),
+                nk=normal(g, B, Hkv, d), nv=normal(g, B, Hkv, d))
+
+
+def run_step(c, ws, W, scale, decay=1.0, k=None, flags=0, **kw):
+    B, Hq, d = c["q"].shape
+    Hkv = c["k"].shape[1]
+    out = torch.full((B, Hq, d), 7.0, dtype=BF, device="cuda")
+    nxt = torch.full((B, Hkv) if k is None else (B, Hkv, k), -9, dtype=torch.int32, device="cuda")
+    lf.decode_step_weights(c["q"], c["k"], c["v"], c["mask"], c["weights"], c["nk"], c["nv"], ws, out,
+                           nxt, W, scale, decay=decay, k=k, flags=flags, **kw)
+    return out, nxt
+
+
+def check_step(c, ws, W, scale, decay=1.0, k=None, flags=0, **kw):
+    before = {n: t.clone() for n, t in c.items()}
+    fill = bool(flags & lf.LF_STEP_FILL_EMPTY_FIRST)
+    want = plain.weights_step(before["q"], before["k"], before["v"], before["mask"], before["weights"],
+                              before["nk"], before["nv"], ws, W, scale, decay, k or 1, fill)
+    out, nxt = run_step(c, ws, W, scale, decay, k, flags, **kw)
+    near(out, want["out"], want["tol"], "out")
+    live = want["mask"] >= 0
+    got = c["weights"].cpu()
+    near(got[live], want["weights"][live], want["wtol"][live], "weights")
+    assert torch.equal(got[~live].view(torch.int32), before["weights"].cpu()[~live].view(torch.int32))
+    slots = plain.chosen(got, want["mask"], W, k or 1, fill)
+    assert torch.equal(nxt.cpu().view(slots.shape), slots)
+    if flags & lf.LF_STEP_MASK_EVICTED:
+        for b, u, i in torch.nonzero(slots >= 0).tolist():
+            want["mask"][b, u, slots[b, u, i]] = -1
+    assert torch.equal(c["mask"].cpu(), want["mask"])
+    for name in ("k", "v"):
+        want_bits = want[name].to(BF)[live]
+        assert torch.equal(c[name].cpu()[live], want_bits)
+    return out, nxt
+
+
+STEP = [  # B, Hq, Hkv, d, S, live lengths, W, decay, k, flags
+    (1, 1, 1, 64, 1, None, 0, 1.0, None, 0), (1, 4, 1, 128, 5, [0], 0, 1.0, None, 0),
+    (2, 4, 2, 64, 65, None, 3, 0.5, None, 0), (1, 32, 8, 128, 700, None, 32, 1.0, None, 0),
+    (3, 8, 1, 128, 129, [129, 0, 70], 100, 0.9, None, lf.LF_STEP_FILL_EMPTY_FIRST),
+    (2, 8, 4, 64, 1000, [1000, 333], 0, 0.0, None, lf.LF_STEP_MASK_EVICTED),
+    (2, 16, 2, 128, 333, None, 50, 1.0, 7, 0),
+    (2, 2, 2, 64, 40, [40, 3], 0, 1.0, 64, lf.LF_STEP_FILL_EMPTY_FIRST | lf.LF_STEP_MASK_EVICTED),
+    (1, 8, 1, 64, 4500, [3000], 10, 1.0, None, 0), (1, 2, 1, 128, 9001, [9001], 64, 0.97, None, 0),
+    (1, 4, 2, 64, 8200, [8200], 64, 0.97, 3, 0), (40, 8, 8, 64, 200, [200, 0, 17], 5, 1.0, None, 0),
+]
+
+
+@pytest.mark.parametrize("case", STEP)
+@pytest.mark.parametrize("write", [True, False])
+def test_weights_step(case, write):
+    B, Hq, Hkv, d, S, live, W, decay, k, flags = case
+    g = gen(S + B)
+    c = step_case(g, B, Hq, Hkv, d, S, live)
+    ws = torch.randint(0, S, (B, Hkv), generator=g, dtype=torch.int32) if write else torch.full((B, Hkv), -1, dtype=torch.int32)
+    check_step(c, ws.cuda(), W, d ** -0.5, decay, k, flags)
+    no_errors()
+
+
+@pytest.mark.parametrize("env", [
+    {"LF_CLUSTER": "0"}, {"LF_CLUSTER": "0", "LF_CHUNK_TILES": "1"}, {"LF_CLUSTER": "1", "LF_DEEP": "0"},
+    {"LF_CLUSTER": "1", "LF_DEEP": "1"}, {"LF_CLUSTER": "0", "LF_SPLIT": "1"}, {"LF_STAGES": "3"},
+    {"LF_CLUSTER": "0", "LF_SPLIT": "1", "LF_SPLIT_TAIL": "1", "LF_SCORE_PARTS": "2"},
+    {"LF_PDL": "0"}, {"LF_CHUNK_TILES": "32"}])
+@pytest.mark.parametrize("shape", [(1, 4, 1, 128, 1029, None), (3, 16, 2, 64, 700, [700, 30, 0])])
+def test_weights_step_by_every_merge(monkeypatch, env, shape):
+    """Each way to merge a unit's chunks; a second step continues from the first's state."""
+    for name, value in env.items():
+        monkeypatch.setenv(name, value)
+    B, Hq, Hkv, d, S, live = shape
+    g = gen(S)
+    c = step_case(g, B, Hq, Hkv, d, S, live)
+    ws = torch.randint(0, S, (B, Hkv), generator=g, dtype=torch.int32).cuda()
+    _, nxt = check_step(c, ws, 16, d ** -0.5, 0.9)
+    check_step(c, nxt, 16, d ** -0.5, 0.9, flags=lf.LF_STEP_FILL_EMPTY_FIRST)
+    no_errors()
+
+
+def test_weights_step_long_cache_off_16_bytes():
+    """Arrays whose rows do not start on 16 bytes take the other way through the scan."""
+    g = gen(3)
+    c = step_case(g, 1, 4, 2, 64, 5000)
+    for name in ("mask", "weights"):
+        wide = torch.empty(c[name].numel() + 1, dtype=c[name].dtype, device="cuda")
+        t = wide[1:].view(c[name].shape)
+        t.copy_(c[name])
+        c[name] = t
+    check_step(c, ints([[0, 4999]]), 16, 0.125, 1.0, k=3)
+    check_step(c, ints([[17, -1]]), 16, 0.125, 1.0)
+    no_errors()
+
+
+def test_weights_step_values_that_are_not_finite():
+    """A live slot's NaN weight stays and is never returned; logits of -infinity weigh nothing."""
+    g = gen(5)
+    c = step_case(g, 1, 2, 2, 64, 100, holes=0.0)
+    c["weights"][0, 0, 3] = NAN
+    c["weights"][0, 0, 5] = INF
+    c["q"][0, 1] = 1.0
+    c["k"][0, 1] = -INF  # every logit of unit 1
+    w1 = c["weights"][0, 1].clone()
+    out, nxt = run_step(c, ints([[-1, -1]]), 0, 1.0, decay=0.5)
+    w = c["weights"][0].cpu()
+    assert torch.isnan(w[0, 3]) and w[0, 5] == INF and nxt[0, 0] not in (3, 5)
+    assert (out[0, 1] == 0).all() and torch.equal(w[1], (0.5 * w1).cpu())
+    assert int(nxt[0, 1]) == int(torch.argmin(w[1]))
+    no_errors()
+
+
+def test_weights_step_bad_write_slot():
+    g = gen(6)
+    c = step_case(g, 1, 2, 2, 64, 100)
+    check_step(c, ints([[100, -2]]), 0, 0.125)
+    assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_WRITE_SLOT
+
+
+def test_weights_steps_in_place_of_the_slot():
+    """next_slots may be write_slot's own buffer: a loop of steps on one buffer."""
+    g = gen(7)
+    c = step_case(g, 2, 8, 2, 128, 300, holes=0.0)
+    d = {n: t.clone() for n, t in c.items()}
+    slot = ints([[0, 1], [2, 3]])
+    out = torch.empty_like(c["q"])
+    for _ in range(5):
+        lf.decode_step_weights(c["q"], c["k"], c["v"], c["mask"], c["weights"], c["nk"], c["nv"], slot, out,
+                               slot, 8, 0.1)
+    other = ints([[0, 1], [2, 3]])
+    for _ in range(5):
+        _, nxt = run_step(d, other, 8, 0.1)
+        other = nxt
+    assert torch.equal(slot, other) and torch.equal(c["weights"], d["weights"])
+
+
+# ---------------------------------------------------------- a prompt's weights --
+
+PROMPT = [  # rows per sequence, lengths, S, counted rows
+    ([1], [1], 1, 0), ([1], [200], 200, 0), ([40], [40], 40, 0), ([40, 0, 3], [40, 0, 3], 64, 0),
+    ([33, 70], [161, 70], 200, 32), ([129], [400], 401, 0), ([257], [257], 260, 5),
+    ([300, 1, 5], [300, 300, 300], 384, 0), ([64, 64], [64, 128], 128, 200), ([1] * 37, list(range(1, 38)), 40, 0),
+    ([2, 150], [2, 511], 513, 1), ([5], [1024], 1024, 0), ([0, 0], [0, 7], 8, 0),
+]
+
+
+@pytest.mark.parametrize("nq,kv,S,rows", PROMPT)
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 128), (2, 2, 64), (8, 1, 64), (2, 1, 128)])
+def test_prompt_weights(nq, kv, S, rows, Hq, Hkv, d):
+    g = gen(S + rows)
+    B, T = len(nq), sum(nq) + 2
+    starts = [sum(nq[:i]) for i in range(B + 1)]
+    q, k = normal(g, T, Hq, d), normal(g, B, Hkv, S, d)
+    for b in range(B):
+        k[b, :, kv[b]:] = NAN
+    q[sum(nq):] = NAN
+    w = torch.randn((B, Hkv, S), generator=g).cuda()
+    w0 = w.clone()
+    lf.prompt_weights(q, k, ints(starts), ints(kv), w, d ** -0.5, rows=rows)
+    ref, tol = plain.prompt_weights(q, k, starts, kv, w0, rows, d ** -0.5)
+    near(w, ref, tol)
+    for b in range(B):
+        assert torch.equal(w[b, :, kv[b]:], w0[b, :, kv[b]:])
+    no_errors()
+
+
+def test_prompt_weights_in_chunks_add_up():
+    g = gen(1)
+    q, k = normal(g, 300, 4, 64), normal(g, 1, 2, 300, 64)
+    one, two = (torch.full((1, 2, 300), NAN, device="cuda") for _ in range(2))
+    lf.prompt_weights(q, k, ints([0, 300]), ints([300]), one, 0.125)
+    lf.prompt_weights(q[:111].clone(), k, ints([0, 111]), ints([111]), two, 0.125)
+    lf.prompt_weights(q[111:].clone(), k, ints([0, 189]), ints([300]), two, 0.125)
+    assert (one - two).abs().max() <= 2.0 ** -11 * one.max()
+    # Every row of every head gives one in all.
+    assert abs(float(one.double().sum()) - 1200) < 1e-3
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0])
+def test_prompt_weights_scales(scale):
+    g = gen(2)
+    q, k = normal(g, 150, 4, 64), normal(g, 1, 1, 170, 64)
+    w = torch.zeros(1, 1, 170, device="cuda")
+    lf.prompt_weights(q, k, ints([0, 150]), ints([170]), w, scale)
+    ref, tol = plain.prompt_weights(q, k, [0, 150], [170], torch.zeros(1, 1, 170), 0, scale)
+    near(w, ref, 8 * tol)  # logits of up to 24 times those of the bound's scale 0.125
+
+
+def test_prompt_weights_infinite_logits():
+    """Keys of -infinity weigh nothing; a row that sees no others gives none."""
+    g = gen(4)
+    q, k = torch.ones(200, 1, 64, dtype=BF, device="cuda"), normal(g, 1, 1, 200, 64)
+    k[0, 0, :150] = -INF
+    w = torch.zeros(1, 1, 200, device="cuda")
+    lf.prompt_weights(q, k, ints([0, 200]), ints([200]), w, 0.125)
+    assert (w[0, 0, :150] == 0).all() and abs(float(w.double().sum()) - 50) < 1e-3
+    no_errors()
+
+
+def test_prompt_weights_bad_lengths():
+    g = gen(8)
+    q, k = normal(g, 6, 2, 64), normal(g, 3, 1, 8, 64)
+    for lens in ([2, 9, 2], [2, 1, 2], [2, -1, 2]):
+        w = torch.full((3, 1, 8), 7.0, device="cuda")
+        lf.prompt_weights(q, k, ints([0, 2, 4, 6]), ints(lens), w, 0.125)
+        assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_LENGTH
+        assert (w[1] == 7).all() and (w[0, 0, :2] != 7).all() and (w[2, 0, :2] != 7).all()
+    for bad in ([0, 9, 9, 9], [-1, 2, 4, 6], [0, 5, 3, 6]):
+        w = torch.full((3, 1, 8), 7.0, device="cuda")
+        lf.prompt_weights(q, k, ints(bad), ints([8, 8, 8]), w, 0.125)
+        assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_LENGTH
+
+
+# ----------------------------------------------------------------- 4-bit cache --
+
+def empty4(B, Hkv, S, d, fill=0):
+    return (torch.full((B, Hkv, S, d // 2), fill, dtype=torch.uint8, device="cuda"),
+            torch.full((B, Hkv, S, d // 32), NAN if fill else 0.0, dtype=BF, device="cuda"))
+
+
+def odd_rows(g, *shape):
+    """Rows with groups of zeros, tiny, huge and outlying values, and exact ties."""
+    x = torch.randn(shape, generator=g)
+    f = torch.randint(0, 8, shape[:-1] + (shape[-1] // 32, 1), generator=g)
+    y = x.unflatten(-1, (-1, 32))
+    y = torch.where(f == 0, 0.0, torch.where(f == 1, y * 1e-38, torch.where(f == 2, y * 1e37, y)))
+    y[..., 0] = torch.where(f[..., 0] == 3, 30.0, y[..., 0])
+    ties = torch.randint(-7, 8, y.shape, generator=g).float() - 0.5
+    ties[..., 0] = 7.0
+    y = torch.where(f == 4, ties, y)
+    y = torch.where(f == 5, torch.round(y * 3) * 2.0 ** -133, y)  # subnormal
+    return y.flatten(-2).to(BF)
+
+
+@pytest.mark.parametrize("B,Hkv,d,P,S", [(1, 1, 64, 1, 1), (2, 2, 128, 70, 90), (3, 1, 64, 333, 300),
+                                         (1, 3, 128, 129, 129)])
+def test_kv4_pack_and_unpack(B, Hkv, d, P, S):
+    g = gen(P)
+    k, v = odd_rows(g, B, Hkv, P, d).cuda(), odd_rows(g, B, Hkv, P, d).cuda()
+    top = min(P, S)
+    first = torch.randint(0, top + 1, (B,), generator=g)
+    last = torch.maximum(first, torch.randint(0, top + 1, (B,), generator=g))
+    first[0], last[0] = 0, top
+    (k4, ks), (v4, vs) = empty4(B, Hkv, S, d, 0x5a), empty4(B, Hkv, S, d, 0x5a)
+    mask = torch.full((B, Hkv, S), -5, dtype=torch.int32, device="cuda")
+    lf.kv4_pack(k, v, first.int().cuda(), last.int().cuda(), k4, ks, v4, vs, mask)
+    k2, v2 = (torch.full_like(k, 7.0) for _ in range(2))
+    lf.kv4_unpack(k4, ks, v4, vs, first.int().cuda(), last.int().cuda(), k2, v2)
+    for x, c, s, back, piece in ((k, k4, ks, k2, 8), (v, v4, vs, v2, 4)):
+        code, scale, value = plain.quantise(x)
+        laid = plain.lay(code, piece)
+        for b in range(B):
+            i, j = int(first[b]), int(last[b])
+            assert torch.equal(c[b, :, i:j].cpu(), laid[b, :, i:j])
+            assert torch.equal(s[b, :, i:j].double().cpu(), scale[b, :, i:j])
+            assert torch.equal(back[b, :, i:j].cpu(), value[b, :, i:j].to(BF))
+            assert (c[b, :, :i] == 0x5a).all() and (c[b, :, j:] == 0x5a).all()
+            assert torch.isnan(s[b, :, :i]).all() and torch.isnan(s[b, :, j:]).all()
+            assert (back[b, :, :i] == 7).all() and (back[b, :, j:] == 7).all()
+            assert torch.equal(mask[b, :, :j].cpu(), torch.arange(j - 1, -1, -1, dtype=torch.int32).expand(Hkv, j))
+            assert (mask[b, :, j:] == -5).all()
+    no_errors()
+
+
+def test_kv4_pack_every_pair_of_magnitudes():
+    """Codes of every quotient that two bf16 magnitudes of a binade can have."""
+    x = torch.zeros(128, 128, 32)
+    m = 1 + torch.arange(128) / 128
+    x[:, :, 0] = 7 * m[:, None]                    # scale m exactly
+    steps = torch.arange(16) / 2                   # quotients by halves, and 1/8 below and above
+    for i in range(15):
+        x[:, :, 1 + 2 * i] = m[None, :] * steps[1 + i] / 2
+        x[:, :, 2 + 2 * i] = -(m[:, None] * steps[1 + i]).to(BF).float()
+    k = x.view(1, 1, -1, 128).to(BF).cuda()
+    (k4, ks), (v4, vs) = empty4(1, 1, k.shape[2], 128), empty4(1, 1, k.shape[2], 128)
+    mask = torch.zeros(1, 1, k.shape[2], dtype=torch.int32, device="cuda")
+    lf.kv4_pack(k, k, None, ints([k.shape[2]]), k4, ks, v4, vs, mask)
+    code, scale, _ = plain.quantise(k)
+    assert torch.equal(ks.double().cpu(), scale) and torch.equal(vs.double().cpu(), scale)
+    assert torch.equal(k4.cpu(), plain.lay(code, 8)) and torch.equal(v4.cpu(), plain.lay(code, 4))
+
+
+def test_kv4_pack_groups_that_are_not_finite():
+    k = torch.ones(1, 1, 3, 64, dtype=BF, device="cuda")
+    k[0, 0, 0, 5], k[0, 0, 1, 40] = NAN, -INF
+    (k4, ks), (v4, vs) = empty4(1, 1, 3, 64), empty4(1, 1, 3, 64)
+    mask = torch.zeros(1, 1, 3, dtype=torch.int32, device="cuda")
+    lf.kv4_pack(k, k, None, ints([3]), k4, ks, v4, vs, mask)
+    k2, v2 = torch.zeros_like(k), torch.zeros_like(k)
+    lf.kv4_unpack(k4, ks, v4, vs, None, ints([3]), k2, v2)
+    want = torch.full((3, 64), float(torch.tensor(1 / 7).to(BF)) * 7, dtype=torch.float64).to(BF)
+    want[0, :32], want[1, 32:] = NAN, NAN
+    assert torch.equal(torch.nan_to_num(k2[0, 0].cpu(), nan=99.0), torch.nan_to_num(want, nan=99.0))
+    assert torch.equal(torch.nan_to_num(v2[0, 0].cpu(), nan=99.0), torch.nan_to_num(want, nan=99.0))
+
+
+def test_kv4_bad_lengths():
+    g = gen(2)
+    k = normal(g, 3, 1, 8, 64)
+    for first, last in (([0, 3, 0], [8, 2, 8]), ([0, -1, 0], [8, 4, 8]), ([0, 0, 0], [8, 9, 8]), ([0, 0, 0], [8, -1, 8])):
+        (k4, ks), (v4, vs) = empty4(3, 1, 8, 64, 0x5a), empty4(3, 1, 8, 64, 0x5a)
+        mask = torch.full((3, 1, 8), -5, dtype=torch.int32, device="cuda")
+        lf.kv4_pack(k, k, ints(first), ints(last), k4, ks, v4, vs, mask)
+        assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_LENGTH
+        assert (k4[1] == 0x5a).all() and (mask[1] == -5).all() and (mask[0] >= 0).all() and (mask[2] >= 0).all()
+        k2, v2 = torch.full_like(k, 7.0), torch.full_like(k, 7.0)
+        lf.kv4_unpack(k4, ks, v4, vs, ints(first), ints(last), k2, v2)
+        assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_LENGTH
+        assert (k2[1] == 7).all() and (v2[0] != 7).any()
+
+
+def kv4_case(g, B, Hq, Hkv, d, S, live=None, holes=0.1, spread=1.0):
+    mask = torch.randint(0, S, (B, Hkv, S), generator=g, dtype=torch.int32)
+    mask[torch.rand((B, Hkv, S), generator=g) < holes] = -1
+    for b in range(B if live is not None else 0):
+        mask[b, :, live[b % len(live)]:] = -1
+    k, v = normal(g, B, Hkv, S, d), normal(g, B, Hkv, S, d)
+    v = (v.float() * torch.exp(spread * torch.randn((B, Hkv, S, 1), generator=g)).cuda()).to(BF)
+    (k4, ks), (v4, vs) = empty4(B, Hkv, S, d), empty4(B, Hkv, S, d)
+    ages = torch.empty_like(mask).cuda()
+    lf.kv4_pack(k, v, None, ints([S] * B), k4, ks, v4, vs, ages)
+    dead = (mask < 0).cuda()
+    for t in (ks, vs):
+        t[dead] = torch.tensor([NAN, INF] * (t.shape[-1] // 2), dtype=BF, device="cuda")
+    return dict(q=normal(g, B, Hq, d), k4=k4, ks=ks, v4=v4, vs=vs, mask=mask.cuda(),
+                nk=normal(g, B, Hkv, d), nv=normal(g, B, Hkv, d))
+
+
+def run_kv4(c, ws, scale, **kw):
+    out = torch.full_like(c["q"], 7.0)
+    lf.decode_attention_kv4(c["q"], c["k4"], c["ks"], c["v4"], c["vs"], c["mask"], c["nk"], c["nv"], ws,
+                            out, scale, **kw)
+    return out
+
+
+def check_kv4(c, ws, scale, **kw):
+    before = {n: t.clone() for n, t in c.items()}
+    S = c["mask"].shape[2]
+    for b, u in [(b, u) for b in range(ws.shape[0]) for u in range(ws.shape[1])]:
+        w = int(ws[b, u])
+        if not 0 <= w < S:
+            continue
+        for new, codes, scales, piece in (("nk", "k4", "ks", 8), ("nv", "v4", "vs", 4)):
+            code, s, _ = plain.quantise(before[new][b, u])
+            before[codes][b, u, w] = plain.lay(code, piece).cuda()
+            before[scales][b, u, w] = s.to(BF).cuda()
+        before["mask"][b, u, w].clamp_(min=0)
+    out = run_kv4(c, ws, scale, **kw)
+    for name in ("k4", "v4", "mask"):
+        assert torch.equal(c[name], before[name]), name
+    for name in ("ks", "vs"):
+        assert torch.equal(c[name].view(torch.int16), before[name].view(torch.int16)), name
+    k, v = plain.stand_for(c["k4"], c["ks"], 8), plain.stand_for(c["v4"], c["vs"], 4)
+    ref, tol = plain.kv4_attention(c["q"], k, v, c["ks"], c["vs"], c["mask"], scale)
+    near(out, ref, tol, "out")
+    return out
+
+
+KV4 = [  # B, Hq, Hkv, d, S, live lengths
+    (1, 1, 1, 64, 1, None), (1, 8, 1, 128, 3, [0]), (2, 4, 2, 64, 17, None), (1, 32, 8, 128, 700, None),
+    (3, 8, 1, 128, 129, [129, 0, 70]), (2, 8, 4, 64, 1000, [1000, 333]), (2, 16, 2, 128, 2050, None),
+    (1, 2, 1, 64, 5001, [4999]), (40, 8, 8, 64, 200, [200, 0, 17]), (150, 4, 4, 128, 33, [33, 1, 16, 17]),
+    (80, 8, 8, 64, 2500, [2500, 31]),
+]
+
+
+@pytest.mark.parametrize("case", KV4)
+@pytest.mark.parametrize("write", [True, False])
+def test_kv4_attention(case, write):
+    B, Hq, Hkv, d, S, live = case
+    g = gen(S + B)
+    c = kv4_case(g, B, Hq, Hkv, d, S, live)
+    ws = torch.randint(0, S, (B, Hkv), generator=g, dtype=torch.int32) if write else torch.full((B, Hkv), -1, dtype=torch.int32)
+    check_kv4(c, ws.cuda(), d ** -0.5)
+    no_errors()
+
+
+def test_kv4_attention_fills_an_empty_cache():
+    """A loop that starts from nothing, slot by slot."""
+    g = gen(11)
+    c = kv4_case(g, 2, 4, 2, 64, 70, live=[0])
+    for t in range(6):
+        c["nk"], c["nv"], c["q"] = normal(g, 2, 2, 64), normal(g, 2, 2, 64), normal(g, 2, 4, 64)
+        check_kv4(c, ints([[t, 69 - t], [t * 11, 15 + t]]), 0.125)
+    no_errors()
+
+
+def test_kv4_attention_bad_write_slot():
+    c = kv4_case(gen(12), 1, 2, 2, 64, 100)
+    check_kv4(c, ints([[100, -2]]), 0.125)
+    assert lf.device_errors(clear=True) == lf.LF_DEVERR_BAD_WRITE_SLOT
+
+
+@pytest.mark.parametrize("d,factor", [(64, 1e-30), (128, 1e30), (64, 1e-4), (128, 3e4)])
+def test_kv4_attention_of_any_size_of_values(d, factor):
+    """Values far from 1, and queries whose keys make up for them."""
+    g = gen(13)
+    c = kv4_case(g, 1, 4, 2, d, 300)
+    live = (c["mask"] >= 0)[..., None]
+    c["vs"] = torch.where(live, (c["vs"].float() * factor).to(BF), c["vs"])
+    c["ks"] = torch.where(live, (c["ks"].float() * factor).to(BF), c["ks"])
+    c["q"] = (c["q"].float() / factor).to(BF)
+    check_kv4(c, ints([[-1, -1]]), d ** -0.5)
+    no_errors()
+
+
+def test_kv4_attention_scales_that_grow():
+    """Later slots with ever larger and smaller values, the small ones with the weight."""
+    g = gen(14)
+    c = kv4_case(g, 1, 4, 1, 128, 600, holes=0.0, spread=0.0)
+    grow = 2.0 ** (torch.arange(600, device="cuda") / 40).floor()
+    c["vs"] = (c["vs"].float() * grow[:, None]).to(BF)
+    check_kv4(c, ints([[-1]]), 128 ** -0.5)
+    c["ks"][0, 0, 64:] = 0  # logits of 0 but for the first slots
+    check_kv4(c, ints([[-1]]), 1.0)
+    no_errors()
+
+
+def test_kv4_attention_values_that_are_not_finite():
+    """A live group that stands for NaN reaches its own 32 outputs of its KV head alone."""
+    g = gen(15)
+    c = kv4_case(g, 1, 4, 2, 128, 200, holes=0.0)
+    ref = run_kv4({n: t.clone() for n, t in c.items()}, ints([[-1, -1]]), 0.1)
+    c["vs"][0, 1, 77, 2] = NAN
+    out = run_kv4(c, ints([[-1, -1]]), 0.1)
+    bad = torch.zeros(1, 4, 128, dtype=torch.bool)
+    bad[:, 2:, 64:96] = True
+    assert torch.equal(torch.isnan(out).cpu(), bad)
+    assert torch.equal(out[~bad.cuda()], ref[~bad.cuda()])
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 2.0])
+def test_kv4_attention_scales(scale):
+    g = gen(16)
+    c = kv4_case(g, 2, 8, 1, 64, 333)
+    k, v = plain.stand_for(c["k4"], c["ks"], 8), plain.stand_for(c["v4"], c["vs"], 4)
+    ref, tol = plain.kv4_attention(c["q"], k, v, c["ks"], c["vs"], c["mask"], scale)
+    near(run_kv4(c, ints([[-1], [-1]]), scale), ref, 4 * tol)  # logits of 16 times the bound's scale
+
+
+# -------------------------------------------------------- streams and graphs --
+
+def test_other_streams_and_workspaces():
+    """Calls on a stream of the caller's, with workspaces of their own, give the same bits."""
+    g = gen(21)
+    s = torch.cuda.Stream()
+    c = kv4_case(g, 2, 8, 2, 128, 3000)
+    ws = ints([[1, 2], [3, 4]])
+    a = run_kv4({n: t.clone() for n, t in c.items()}, ws, 0.1)
+    e = step_case(g, 2, 8, 2, 64, 900)
+    f = {n: t.clone() for n, t in e.items()}
+    out, nxt = run_step(e, ws, 4, 0.1)
+    q, k = normal(g, 200, 8, 64), normal(g, 1, 2, 256, 64)
+    w1, w2 = torch.zeros(1, 2, 256, device="cuda"), torch.zeros(1, 2, 256, device="cuda")
+    lf.prompt_weights(q, k, ints([0, 200]), ints([256]), w1, 0.1)
+    torch.cuda.synchronize()
+    own = torch.full((lf.decode_kv4_workspace(2, 8, 2, 128, 3000),), 0xff, dtype=torch.uint8, device="cuda")
+    own2 = torch.full((lf.decode_weights_workspace(2, 8, 2, 64, 900),), 0xff, dtype=torch.uint8, device="cuda")
+    own3 = torch.full((lf.prompt_weights_workspace(200, 1, 8, 2, 64, 256),), 0xff, dtype=torch.uint8, device="cuda")
+    starts, lens = ints([0, 200]), ints([256])
+    torch.cuda.synchronize()
+    b = run_kv4(c, ws, 0.1, workspace=own, stream=s)
+    out2, nxt2 = run_step(f, ws, 4, 0.1, workspace=own2, stream=s)
+    lf.prompt_weights(q, k, starts, lens, w2, 0.1, workspace=own3, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(a, b) and torch.equal(out, out2) and torch.equal(nxt, nxt2) and torch.equal(w1, w2)
+    live = e["mask"] >= 0
+    assert torch.equal(e["weights"][live], f["weights"][live])
+    no_errors()
+
+
+def test_two_graphs_at_once():
+    """Two captured graphs of each call, replayed on two streams at the same time."""
+    g = gen(22)
+    cases = [(kv4_case(g, 4, 8, 2, 64, 5000), step_case(g, 4, 8, 2, 64, 9000),
+              normal(g, 500, 8, 64), normal(g, 1, 2, 600, 64)) for _ in range(2)]
+    ws = torch.full((4, 2), -1, dtype=torch.int32, device="cuda")
+    starts, lens = ints([0, 500]), ints([600])
+    want, graphs = [], []
+    for c, e, q, k in cases:
+        w = torch.zeros(1, 2, 600, device="cuda")
+        lf.prompt_weights(q, k, starts, lens, w, 0.1, rows=100)
+        a = run_kv4(c, ws, 0.1)
+        f = {n: t.clone() for n, t in e.items()}
+        out, nxt = run_step(f, ws, 4, 0.1, decay=0.0)
+        want.append((a, out, nxt, w))
+    torch.cuda.synchronize()
+    for c, e, q, k in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            w = torch.zeros(1, 2, 600, device="cuda")
+            lf.prompt_weights(q, k, starts, lens, w, 0.1, rows=100)
+            a = run_kv4(c, ws, 0.1)
+            out, nxt = run_step(e, ws, 4, 0.1, decay=0.0)
+        graphs.append((graph, (a, out, nxt, w)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for s, (graph, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, got), ref in zip(graphs, want):
+        assert all(torch.equal(x, y) for x, y in zip(got, ref))
+    no_errors()
+
+
+# ------------------------------------------------------------------- together --
+
+def test_a_long_prompt_then_tokens():
+    """An image prompt in two chunks into bf16 caches, its weights, then evicting tokens over a
+    full budget; and the same prompt's cache in 4 bits with tokens appended to it."""
+    g = gen(31)
+    B, Hq, Hkv, d, S, n1, n2 = 2, 8, 2, 64, 96, 50, 46
+    freq = (1e4 ** (-torch.arange(16).double() / 16)).float().cuda()
+    pair, scale = [0] * 8 + [1] * 4 + [2] * 4, d ** -0.5
+    k, v = (torch.full((B, Hkv, S, d), NAN, dtype=BF, device="cuda") for _ in range(2))
+    mask = torch.full((B, Hkv, S), -1, dtype=torch.int32, device="cuda")
+    weights = torch.full((B, Hkv, S), NAN, device="cuda")
+    total = torch.zeros((B, Hkv, S), dtype=torch.float64)
+    w = torch.ones(d, dtype=BF, device="cuda")
+    done = 0
+    for n in (n1, n2):
+        qkv = normal(g, B * n, Hq + 2 * Hkv, d)
+        pos = torch.randint(0, 200, (3, B * n), generator=g, dtype=torch.int32).cuda()
+        q = torch.empty(B * n, Hq, d, dtype=BF, device="cuda")
+        starts, lens = ints([0, n, 2 * n]), ints([done + n] * B)
+        lf.prefill_append_axes(qkv, w, w, freq, starts, lens, pos, pair, q, k, v, mask)
+        out = torch.empty_like(q)
+        lf.window_attention(q, k, v, starts, lens, out, 0, 0, scale)
+        lf.prompt_weights(q, k, starts, lens, weights, scale)
+        total, _ = plain.prompt_weights(q, k, [0, n, 2 * n], [done + n] * B, total, 0, scale)
+        done += n
+    near(weights, total, 2.0 ** -11 * total)
+    (k4, ks), (v4, vs) = empty4(B, Hkv, S + 8, d), empty4(B, Hkv, S + 8, d)
+    mask4 = torch.full((B, Hkv, S + 8), -1, dtype=torch.int32, device="cuda")
+    lf.kv4_pack(k, v, None, ints([S] * B), k4, ks, v4, vs, mask4)
+    c = dict(k=k, v=v, mask=mask, weights=weights)
+    c4 = dict(k4=k4, ks=ks, v4=v4, vs=vs, mask=mask4)
+    ws = torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    for t in range(5):
+        qkv = normal(g, B, Hq + 2 * Hkv, d)
+        pos = torch.full((3, B), S + t, dtype=torch.int32, device="cuda")
+        q = torch.empty(B, Hq, d, dtype=BF, device="cuda")
+        nk, nv = (torch.empty(B, Hkv, d, dtype=BF, device="cuda") for _ in range(2))
+        lf.qk_norm_rope_axes(qkv, w, w, freq, pos, pair, q, nk, nv)
+        c.update(q=q, nk=nk, nv=nv)
+        _, ws = check_step(c, ws, 16, scale)
+        c4.update(q=q, nk=nk, nv=nv)
+        check_kv4(c4, torch.full_like(ws, S + t), scale)
+    no_errors()
