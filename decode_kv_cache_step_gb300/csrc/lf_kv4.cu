@@ -182,6 +182,22 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxChunkSlots = 2048;
 constexpr int kMaxWarpTiles = kMaxChunkSlots / 16 / kWarps;
+// A warp's ring of tiles of 16 slots in shared memory.
+template <int D>
+struct Ring {
+    static constexpr int kKRow = D / 2;
+    // Rows of values 16 bytes apart: four lanes that read rows 2 c at once then
+    // touch different banks.
+    static constexpr int kVRow = D / 2 + 16;
+    static constexpr int kScaleRow = D / 16;
+    static constexpr int kVOff = 16 * kKRow;
+    static constexpr int kKScaleOff = kVOff + 16 * kVRow;
+    static constexpr int kVScaleOff = kKScaleOff + 16 * kScaleRow;
+    static constexpr int kStage = kVScaleOff + 16 * kScaleRow;
+    static constexpr int kStages = D == 128 ? 5 : 9;
+    static constexpr int kWarp = kStages * kStage;
+    static constexpr int kAlloc = kWarps * kWarp;
+};
 constexpr float kCode = 0x1p-24f;  // what the integer 1 in a half's low bits is worth
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -199,19 +215,39 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 32-bit words of the cache: read once per step, past L1.
+// Asynchronous copies of N bytes into shared memory (nothing is read and zeros are
+// stored with there = false), in groups that complete in order.
 template <int N>
-__device__ __forceinline__ void load_words(const void* a, uint32_t (&w)[N]) {
-    static_assert(N == 1 || N == 2 || N == 4, "words of a load");
-    if constexpr (N == 1)
-        asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(a) : "memory");
-    else if constexpr (N == 2)
-        asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(a) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+    const int bytes = there ? N : 0;
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
     else
-        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "l"(a)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes)
                      : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void shared_words(const uint8_t* a, uint32_t (&w)[N]) {
+    static_assert(N == 1 || N == 2 || N == 4, "words of a load");
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(a);
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(a);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(a);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
 }
 
 __device__ __forceinline__ float scale_of(uint32_t word, int odd) {
@@ -219,7 +255,8 @@ __device__ __forceinline__ float scale_of(uint32_t word, int odd) {
 }
 
 // One CTA: chunk blockIdx.x of unit blockIdx.y. Each warp takes 16 live slots at
-// a time, straight from global memory into the registers of its products:
+// a time through a ring of its own in shared memory (asynchronous copies; no
+// other warp is waited for):
 //   S^T[16 x 8] = K[16 x d] Q^T[d x 8]          per group, times the key's scale
 //   O^T[d x 8] += V^T[d x 16] (P s)^T[16 x 8]   per group, P s the weights times
 //                                               the values' scales
@@ -227,15 +264,18 @@ __device__ __forceinline__ float scale_of(uint32_t word, int odd) {
 // n 2^-24 (a subnormal; linear up to n = 2047, and the tensor cores take it), so
 // the codes at bits 0 and 16 of a word are an operand after one AND, those at
 // bits 4 and 20, as 16 n, after another. The 16 is taken out of q, or of the row
-// of O. Codes are stored plus 8: the products' accumulators start at
-// -8 sum q, and 8 sum P s, one more product a group with constant codes, is
-// taken off O at the end.
+// of O. Codes are stored plus 8: the logits start at -8 sum q s (one product of
+// the scales with q's sums over the groups, in three bf16 parts), and 8 sum P s,
+// a product per group with constant codes, is taken off O at the end.
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Params p) {
+    using R = Ring<D>;
     constexpr int NG = D / 32;
+    extern __shared__ __align__(16) uint8_t s_ring[];
     __shared__ uint32_t s_tiles[kWarps][kMaxWarpTiles];
-    __shared__ float s_o[kWarps][G][D + 4];
     __shared__ float s_m[kWarps][G], s_l[kWarps][G];
+    __shared__ __align__(16) uint8_t s_new[2][D / 2];  // the token's row in 4 bits
+    __shared__ __nv_bfloat16 s_new_scale[2][NG];
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
     const int lane = tid & 31;
@@ -271,28 +311,8 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
         if (tid == 0 && blockIdx.x == 0) atomicOr(p.dev_err, LF_DEVERR_BAD_WRITE_SLOT);
         ws = -1;
     }
-    // The token's row into its slot, by the warp that will read it: lanes below
-    // D / 8 the key, the next D / 8 the value.
     const int wi = ws - slot0;
     const bool mine = ws >= 0 && wi >= 0 && wi < slots && ((wi >> 5) & (kWarps - 1)) == warp;
-    if (mine) {
-        const int i = lane % (D / 8);
-        const bool is_v = lane / (D / 8) == 1;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (lane < D / 4)
-            x = *reinterpret_cast<const uint4*>((is_v ? p.new_v : p.new_k) + static_cast<size_t>(u) * D + 8 * i);
-        __nv_bfloat16 s;
-        const uint32_t codes = quantise8(x, 0xfu << (lane & 28), &s);
-        const size_t at = static_cast<size_t>(u) * S + ws;
-        if (lane < D / 4) {
-            if (is_v)
-                store_v8<D>(p.v4 + at * (D / 2), i, codes);
-            else
-                store_k8<D>(p.k4 + at * (D / 2), i, codes);
-            if ((i & 3) == 0) (is_v ? p.v_scale : p.k_scale)[at * NG + (i >> 2)] = s;
-        }
-        __syncwarp();  // before the warp's loads of the row
-    }
     // The warp's live tiles of 16 slots.
     int tiles = 0;
 #pragma unroll
@@ -313,9 +333,77 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
     }
     __syncwarp();
 
+    // Copies of a tile: 16 bytes of codes a lane at a time, one row's scales.
+    const size_t unit0 = static_cast<size_t>(u) * S + slot0;
+    constexpr int kRowChunks = D / 32;             // 16-byte chunks of a row's codes
+    constexpr int kCopies = kRowChunks / 2;        // of a lane, per tile and operand
+    constexpr int kStep = 32 / kRowChunks;         // rows between them
+    const int crow = lane / kRowChunks;
+    const uint8_t* const pk = p.k4 + unit0 * (D / 2) + lane * 16;
+    const uint8_t* const pv = p.v4 + unit0 * (D / 2) + lane * 16;
+    const uint8_t* const ps = reinterpret_cast<const uint8_t*>(lane < 16 ? p.k_scale : p.v_scale) +
+                              (unit0 + (lane & 15)) * R::kScaleRow;
+    uint8_t* const ring = s_ring + warp * R::kWarp;
+    const uint32_t dk = smem_u32(ring) + lane * 16;
+    const uint32_t dv = smem_u32(ring) + R::kVOff + crow * R::kVRow + (lane % kRowChunks) * 16;
+    const uint32_t ds = smem_u32(ring) + R::kKScaleOff + lane * R::kScaleRow;
+    auto copy_tile = [&](uint32_t t, int stage) {
+        const int tile = t >> 16;
+        const int at = stage * R::kStage;
+        const uint8_t* const k = pk + tile * (8 * D);
+        const uint8_t* const v = pv + tile * (8 * D);
+        const uint8_t* const scales = ps + tile * (16 * R::kScaleRow);
+        const auto rows = [&](int most) {  // copies of the rows that are there
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                copy_async<16>(dk + at + i * 512, k + i * 512, crow + i * kStep < most);
+                copy_async<16>(dv + at + i * kStep * R::kVRow, v + i * 512, crow + i * kStep < most);
+            }
+            copy_async<R::kScaleRow>(ds + at, scales, (lane & 15) < most);
+        };
+        const int most = slots - tile * 16;
+        if (most >= 16)
+            rows(16);
+        else
+            rows(most);
+    };
+#pragma unroll
+    for (int i = 0; i < R::kStages; ++i) {
+        if (i < tiles) copy_tile(s_tiles[warp][i], i);
+        copy_commit();
+    }
+
+    // The token's row into its slot, by the warp that holds it: lanes below D / 8
+    // the key, the next D / 8 the value. What the copies bring of the row may be
+    // old or new: the warp puts s_new in its place.
+    if (mine) {
+        const int i = lane % (D / 8);
+        const bool is_v = lane / (D / 8) == 1;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (lane < D / 4)
+            x = *reinterpret_cast<const uint4*>((is_v ? p.new_v : p.new_k) + static_cast<size_t>(u) * D + 8 * i);
+        __nv_bfloat16 s;
+        const uint32_t codes = quantise8(x, 0xfu << (lane & 28), &s);
+        const size_t at = static_cast<size_t>(u) * S + ws;
+        if (lane < D / 4) {
+            if (is_v) {
+                store_v8<D>(p.v4 + at * (D / 2), i, codes);
+                store_v8<D>(s_new[1], i, codes);
+            } else {
+                store_k8<D>(p.k4 + at * (D / 2), i, codes);
+                store_k8<D>(s_new[0], i, codes);
+            }
+            if ((i & 3) == 0) {
+                (is_v ? p.v_scale : p.k_scale)[at * NG + (i >> 2)] = s;
+                s_new_scale[is_v][i >> 2] = s;
+            }
+        }
+        __syncwarp();
+    }
+
     // q as halves of 2^13 to 2^14 for the largest: what is below 2^-38 of that is lost.
     uint32_t qf[NG][4];      // k steps of a group: codes at even, then odd nibbles
-    float start[NG][2];      // -8 sum q of heads 2 c, 2 c + 1
+    uint32_t start[2];       // -8 sum q of the groups: an operand with the scales
     float qs[2];             // what the halves are worth
     {
         uint32_t top = 0;
@@ -354,34 +442,26 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             t += __shfl_xor_sync(0xffffffffu, t, 2);
             sum[g] = -8.f * kCode * t;
         }
+        // Row k = NG part + g of that operand: part 0, 1 or 2 of group g's sum. A
+        // lane holds rows 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 of head r.
+        float part[3][NG];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            qs[h] = __shfl_sync(0xffffffffu, unit, 4 * (2 * c + h));
-#pragma unroll
-            for (int g = 0; g < NG; ++g) start[g][h] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * c + h));
+        for (int g = 0; g < NG; ++g) {
+            part[0][g] = __bfloat162float(__float2bfloat16_rn(sum[g]));
+            part[1][g] = __bfloat162float(__float2bfloat16_rn(sum[g] - part[0][g]));
+            part[2][g] = sum[g] - part[0][g] - part[1][g];
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 3 * NG; ++k)
+                if (k / 2 == c + 4 * i) v[k & 1] = part[k / NG][k % NG];
+            start[i] = pack_bf16x2(v[0], v[1]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) qs[h] = __shfl_sync(0xffffffffu, unit, 4 * (2 * c + h));
     }
-
-    const size_t unit0 = static_cast<size_t>(u) * S;
-    uint32_t kw[2][NG], ks[2][NG / 2], vw[4][NG / 2], vs[2][NG / 2];
-    auto tile_slot = [&](uint32_t t, int i) {
-        return unit0 + min(slot0 + static_cast<int>(t >> 16) * 16 + i, S - 1);
-    };
-    auto load_k = [&](uint32_t t) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const size_t at = tile_slot(t, r + 8 * h);
-            load_words<NG>(p.k4 + at * (D / 2) + c * (D / 8), kw[h]);
-            load_words<NG / 2>(p.k_scale + at * NG, ks[h]);
-        }
-    };
-    auto load_v = [&](uint32_t t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load_words<NG / 2>(p.v4 + tile_slot(t, 2 * c + (i & 1) + 8 * (i >> 1)) * (D / 2) + r * (D / 16), vw[i]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) load_words<NG / 2>(p.v_scale + tile_slot(t, r + 8 * h) * NG, vs[h]);
-    };
 
     const float NEG = -INFINITY;
     float acc[2 * NG][4];  // [group][values 4 r + 0, 1 | 2, 3], of heads 2 c and 2 c + 1
@@ -390,35 +470,85 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
     for (int i = 0; i < 2 * NG; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) off[g][0] = off[g][1] = off[g][2] = off[g][3] = 0.f;
-    float m0 = NEG, m1 = NEG, l0 = 0.f, l1 = 0.f;
-    // P s is held as halves of p s 2^(14 - E), 2^E the largest scale's power of
-    // two so far: weights that count keep 11 bits, down to 2^-28 of the largest
-    // possible, and 2^-39 of that is the least that is kept.
-    uint32_t E = 20;
-    float fE = __uint_as_float((14 + 127 + 127 - 20) << 23);
-
-    uint32_t next = 0;
-    if (tiles > 0) {
-        next = s_tiles[warp][0];
-        load_k(next);
-        load_v(next);
-    }
-#pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-        const uint32_t t = next;
-        if (i + 1 < tiles) next = s_tiles[warp][i + 1];
-        const bool liveA = (t >> r) & 1u;
-        const bool liveB = (t >> (r + 8)) & 1u;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+    auto rescale = [&](float f0, float f1) {
+#pragma unroll
+        for (int k = 0; k < 2 * NG; ++k) {
+            acc[k][0] *= f0;
+            acc[k][1] *= f1;
+            acc[k][2] *= f0;
+            acc[k][3] *= f1;
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float init[4] = {start[g][0], start[g][1], start[g][0], start[g][1]};
+            off[g][0] *= f0;
+            off[g][1] *= f1;
+            off[g][2] *= f0;
+            off[g][3] *= f1;
+        }
+    };
+    // The reference of the softmax follows a head's largest logit only once one
+    // is more than kGrowth above it: weights up to 2^kGrowth serve as well, and
+    // most tiles need no maximum across the lanes.
+    constexpr float kGrowth = 8.f;
+    float m0 = NEG, m1 = NEG, base0 = 0.f, base1 = 0.f, l0 = 0.f, l1 = 0.f;
+    // P s is held as halves of p s 2^(6 - E), 2^E the power of two of the largest
+    // scale so far: below 2^15, 11 bits down to 2^-20 of the largest possible
+    // value, and nothing below 2^-31 of it.
+    constexpr int kHalfExp = 6;
+    uint32_t E = 20;
+    float fE = __uint_as_float((kHalfExp + 254 - 20) << 23);
+
+    int stage = 0;
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+        const uint32_t t = s_tiles[warp][i];
+        uint8_t* const tile = ring + stage * R::kStage;
+        copy_wait<R::kStages - 1>();
+        __syncwarp();
+        if (mine && static_cast<int>(t >> 16) == wi >> 4) {
+            const int row = wi & 15;
+            if (lane < D / 32)
+                reinterpret_cast<uint4*>(tile + row * R::kKRow)[lane] = reinterpret_cast<const uint4*>(s_new[0])[lane];
+            else if (lane < D / 16)
+                reinterpret_cast<uint4*>(tile + R::kVOff + row * R::kVRow)[lane - D / 32] =
+                    reinterpret_cast<const uint4*>(s_new[1])[lane - D / 32];
+            else if (lane < D / 16 + 2 * NG) {
+                const int g = (lane - D / 16) % NG, is_v = (lane - D / 16) / NG;
+                reinterpret_cast<__nv_bfloat16*>(tile + (is_v ? R::kVScaleOff : R::kKScaleOff) +
+                                                 row * R::kScaleRow)[g] = s_new_scale[is_v][g];
+            }
+            __syncwarp();
+        }
+        uint32_t kw[2][NG], ks[2][NG / 2], vw[4][NG / 2], vs[2][NG / 2], kz[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = r + 8 * h;
+            shared_words<NG>(tile + row * R::kKRow + c * (D / 8), kw[h]);
+            shared_words<NG / 2>(tile + R::kKScaleOff + row * R::kScaleRow, ks[h]);
+            shared_words<NG / 2>(tile + R::kVScaleOff + row * R::kScaleRow, vs[h]);
+            kz[h] = *reinterpret_cast<const uint32_t*>(tile + R::kKScaleOff + row * R::kScaleRow +
+                                                       c % (NG / 2) * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            shared_words<NG / 2>(tile + R::kVOff + (2 * c + (k & 1) + 8 * (k >> 1)) * R::kVRow + r * (D / 16), vw[k]);
+        __syncwarp();
+        if (i + R::kStages < tiles) copy_tile(s_tiles[warp][i + R::kStages], stage);
+        copy_commit();
+        stage = stage + 1 == R::kStages ? 0 : stage + 1;
+
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t z[4] = {kz[0], kz[1], kz[0], kz[1]};
+        mma_bf16_16816(x, z, start[0], start[1]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
             float sc[4];
-            uint32_t a[4] = {kw[0][g] & 0x000f000fu, kw[1][g] & 0x000f000fu,
-                             (kw[0][g] >> 8) & 0x000f000fu, (kw[1][g] >> 8) & 0x000f000fu};
-            mma_f16_16816(sc, a, qf[g][0], qf[g][1], init);
-            uint32_t o[4] = {kw[0][g] & 0x00f000f0u, kw[1][g] & 0x00f000f0u,
-                             (kw[0][g] >> 8) & 0x00f000f0u, (kw[1][g] >> 8) & 0x00f000f0u};
+            const uint32_t a[4] = {kw[0][g] & 0x000f000fu, kw[1][g] & 0x000f000fu,
+                                   (kw[0][g] >> 8) & 0x000f000fu, (kw[1][g] >> 8) & 0x000f000fu};
+            mma_f16_16816(sc, a, qf[g][0], qf[g][1], zero);
+            const uint32_t o[4] = {kw[0][g] & 0x00f000f0u, kw[1][g] & 0x00f000f0u,
+                                   (kw[0][g] >> 8) & 0x00f000f0u, (kw[1][g] >> 8) & 0x00f000f0u};
             mma_f16_16816(sc, o, qf[g][2], qf[g][3], sc);
             const float sa = scale_of(ks[0][g >> 1], g & 1), sb = scale_of(ks[1][g >> 1], g & 1);
             x[0] += sc[0] * sa;
@@ -426,62 +556,67 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             x[2] += sc[2] * sb;
             x[3] += sc[3] * sb;
         }
-        if (i + 1 < tiles) load_k(next);
         // (In two steps: either factor may be far from 1.)
-        x[0] = liveA ? x[0] * p.unit * qs[0] : NEG;
-        x[1] = liveA ? x[1] * p.unit * qs[1] : NEG;
-        x[2] = liveB ? x[2] * p.unit * qs[0] : NEG;
-        x[3] = liveB ? x[3] * p.unit * qs[1] : NEG;
+        x[0] = x[0] * p.unit * qs[0];
+        x[1] = x[1] * p.unit * qs[1];
+        x[2] = x[2] * p.unit * qs[0];
+        x[3] = x[3] * p.unit * qs[1];
+        if ((t & 0xffffu) != 0xffffu) {
+            // Masked slots: weight 0, and 0 for the scales of whatever lies there.
+            const bool liveA = (t >> r) & 1u, liveB = (t >> (r + 8)) & 1u;
+            x[0] = liveA ? x[0] : NEG;
+            x[1] = liveA ? x[1] : NEG;
+            x[2] = liveB ? x[2] : NEG;
+            x[3] = liveB ? x[3] : NEG;
+#pragma unroll
+            for (int k = 0; k < NG / 2; ++k) {
+                vs[0][k] = liveA ? vs[0][k] : 0u;
+                vs[1][k] = liveB ? vs[1][k] : 0u;
+            }
+        }
         float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+        if (__any_sync(0xffffffffu, mx0 > m0 + kGrowth || mx1 > m1 + kGrowth)) {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-        }
-        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-        const float mu0 = mn0 == NEG ? 0.f : mn0, mu1 = mn1 == NEG ? 0.f : mn1;
-        float al0 = ex2_approx(m0 - mu0), al1 = ex2_approx(m1 - mu1);
-        m0 = mn0;
-        m1 = mn1;
-        const float p0 = ex2_approx(x[0] - mu0), p1 = ex2_approx(x[1] - mu1);
-        const float p2 = ex2_approx(x[2] - mu0), p3 = ex2_approx(x[3] - mu1);
-        l0 = l0 * al0 + (p0 + p2);
-        l1 = l1 * al1 + (p1 + p3);
-        // The values' scales; a masked slot's are 0. The largest finite one.
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < NG / 2; ++k) {
-            vs[0][k] = liveA ? vs[0][k] : 0u;
-            vs[1][k] = liveB ? vs[1][k] : 0u;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t lo = vs[h][k] & 0x7f80u, hi = (vs[h][k] >> 16) & 0x7f80u;
-                if (lo != 0x7f80u) top = max(top, lo);
-                if (hi != 0x7f80u) top = max(top, hi);
+            for (int o = 4; o < 32; o <<= 1) {
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
             }
+            mx0 = fmaxf(mx0, m0);
+            mx1 = fmaxf(mx1, m1);
+            base0 = mx0 == NEG ? 0.f : mx0;
+            base1 = mx1 == NEG ? 0.f : mx1;
+            const float f0 = ex2_approx(m0 - base0), f1 = ex2_approx(m1 - base1);
+            l0 *= f0;
+            l1 *= f1;
+            m0 = mx0;
+            m1 = mx1;
+            rescale(f0, f1);
         }
-        top = __reduce_max_sync(0xffffffffu, top) >> 7;
-        if (top > E) {
-            const float down = __uint_as_float(static_cast<uint32_t>(max(0, 127 - static_cast<int>(top - E))) << 23);
-            al0 *= down;
-            al1 *= down;
-            E = top;
-            fE = __uint_as_float((14 + 127 + 127 - E) << 23);
-        }
-        if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+        const float p0 = ex2_approx(x[0] - base0), p1 = ex2_approx(x[1] - base1);
+        const float p2 = ex2_approx(x[2] - base0), p3 = ex2_approx(x[3] - base1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        // The largest scale, as the bits of two bf16 side by side.
+        uint32_t two = 0;
 #pragma unroll
-            for (int k = 0; k < 2 * NG; ++k) {
-                acc[k][0] *= al0;
-                acc[k][1] *= al1;
-                acc[k][2] *= al0;
-                acc[k][3] *= al1;
-            }
+        for (int k = 0; k < NG / 2; ++k) two = __vimax3_u16x2(two, vs[0][k], vs[1][k]);
+        if (__any_sync(0xffffffffu, max(two & 0xffffu, two >> 16) >= (E + 1) << 7)) {
+            // Rare: a new power of two, of the finite ones.
+            uint32_t top = 0;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                off[g][0] *= al0;
-                off[g][1] *= al1;
-                off[g][2] *= al0;
-                off[g][3] *= al1;
+            for (int k = 0; k < NG / 2; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t lo = vs[h][k] & 0x7f80u, hi = (vs[h][k] >> 16) & 0x7f80u;
+                    if (lo != 0x7f80u) top = max(top, lo);
+                    if (hi != 0x7f80u) top = max(top, hi);
+                }
+            top = __reduce_max_sync(0xffffffffu, top) >> 7;
+            if (top > E) {
+                const float down = __uint_as_float(static_cast<uint32_t>(max(0, 127 - static_cast<int>(top - E))) << 23);
+                rescale(down, down);
+                E = top;
+                fE = __uint_as_float((kHalfExp + 254 - E) << 23);
             }
         }
         const float f0 = p0 * fE, f1 = p1 * fE, f2 = p2 * fE, f3 = p3 * fE;
@@ -502,10 +637,14 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             const uint32_t eight[4] = {0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u};
             mma_f16_16816(off[g], eight, b0, b1, off[g]);
         }
-        if (i + 1 < tiles) load_v(next);
     }
 
-    // The four warps' states, joined.
+    // The four warps' states, joined (each warp's part of O over its ring).
+    copy_wait<0>();
+    __syncwarp();
+    constexpr int kORow = D + 4;
+    static_assert(G * kORow * 4 <= R::kWarp, "a warp's part of O exceeds its ring");
+    float* const my_o = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, o);
@@ -517,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
         if (h0 + 1 < G) { s_m[warp][h0 + 1] = m1; s_l[warp][h0 + 1] = l1; }
     }
     {
-        const float back = __uint_as_float((E + 127 - 127 - 14) << 23);  // 2^(E - 127 - 14)
+        const float back = __uint_as_float((E - kHalfExp) << 23);  // 2^(E - 127 - kHalfExp)
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -527,8 +666,8 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     v[e] = (acc[2 * g + k][e] - off[g][e]) * (e < 2 ? 0x1p24f : 0x1p20f) * back;
-                if (h0 < G) { s_o[warp][h0][dd] = v[0]; s_o[warp][h0][dd + 1] = v[2]; }
-                if (h0 + 1 < G) { s_o[warp][h0 + 1][dd] = v[1]; s_o[warp][h0 + 1][dd + 1] = v[3]; }
+                if (h0 < G) { my_o[h0 * kORow + dd] = v[0]; my_o[h0 * kORow + dd + 1] = v[2]; }
+                if (h0 + 1 < G) { my_o[(h0 + 1) * kORow + dd] = v[1]; my_o[(h0 + 1) * kORow + dd + 1] = v[3]; }
             }
     }
     __syncthreads();
@@ -544,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             // A warp without a live slot has l = 0 (with one, l is NaN or > 0).
             if (s_l[w][h] == 0.f) continue;
             const float f = exp2f(s_m[w][h] - (mh == NEG ? 0.f : mh));
-            o += s_o[w][h][dd] * f;
+            o += reinterpret_cast<const float*>(s_ring + w * R::kWarp)[h * kORow + dd] * f;
             l += s_l[w][h] * f;
         }
         if (gridDim.x == 1) {
@@ -556,39 +695,65 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
     }
 }
 
-// The chunks of a query row joined: one warp per row.
+// The chunks of a query row joined by one CTA: its warps share the chunks, whose
+// loads are in flight eight at a time.
 template <int D>
-__global__ void __launch_bounds__(kThreads) lf_kv4_join_kernel(const Kv4Params p, int rows, int G, int nchunk) {
+__global__ void __launch_bounds__(kThreads) lf_kv4_join_kernel(const Kv4Params p, int G, int nchunk) {
+    __shared__ float s_o[kWarps][D];
+    __shared__ float s_l[kWarps];
     allow_dependent_launch();
     grid_dependency_wait();
-    const int row = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
+    const int row = blockIdx.x;
     const int u = row / G, h = row % G;
     const float2* ml = p.part_ml + static_cast<size_t>(u) * nchunk * G + h;
-    const float* po = p.part_o + (static_cast<size_t>(u) * nchunk * G + h) * D + lane * (D / 32);
+    const float* po = p.part_o + (static_cast<size_t>(u) * nchunk * G + h) * D;
+    constexpr int kE = D / 32;  // values of a lane
+    constexpr int kAhead = 8;
     float m = -INFINITY;
-    for (int k = lane; k < nchunk; k += 32) m = fmaxf(m, ml[static_cast<size_t>(k) * G].x);
+    for (int k = lane; k < nchunk; k += 32) m = fmaxf(m, __ldcg(&ml[static_cast<size_t>(k) * G].x));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (m == -INFINITY) m = 0.f;
-    float o[D / 32], l = 0.f;
+    float o[kE], l = 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < nchunk; ++k) {
-        const float2 v = ml[static_cast<size_t>(k) * G];
-        const float f = v.y == 0.f ? 0.f : exp2f(v.x - m);
-        l += v.y == 0.f ? 0.f : v.y * f;
+    for (int e = 0; e < kE; ++e) o[e] = 0.f;
+    for (int k0 = warp; k0 < nchunk; k0 += kWarps * kAhead) {
+        float2 v[kAhead];
+        float x[kAhead][kE];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            const float x = po[static_cast<size_t>(k) * G * D + e];
-            o[e] += v.y == 0.f ? 0.f : x * f;
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = k0 + i * kWarps;
+            v[i] = k < nchunk ? __ldcg(ml + static_cast<size_t>(k) * G) : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < kE; ++e)
+                x[i][e] = k < nchunk ? __ldcg(po + static_cast<size_t>(k) * G * D + e * 32 + lane) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            // A chunk without a live slot has l = 0, its output is not there.
+            if (v[i].y == 0.f) continue;
+            const float f = exp2f(v[i].x - m);
+            l += v[i].y * f;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[e] += x[i][e] * f;
         }
     }
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e)
-        p.out[static_cast<size_t>(row) * D + lane * (D / 32) + e] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
+    for (int e = 0; e < kE; ++e) s_o[warp][e * 32 + lane] = o[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    const int dd = threadIdx.x;
+    if (dd < D) {
+        float sum = 0.f, all = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            sum += s_o[w][dd];
+            all += s_l[w];
+        }
+        p.out[static_cast<size_t>(row) * D + dd] = __float2bfloat16_rn(all == 0.f ? 0.f : sum / all);
+    }
 }
 
 // Launch configuration with programmatic dependent launch (LF_PDL=0: without).
@@ -607,18 +772,27 @@ struct Config {
     }
 };
 
+template <int D, int G>
+cudaError_t launch_kv4_dg(const Kv4Params& p, int units, int nchunk, cudaStream_t stream) {
+    const auto kernel = lf_kv4_attn_kernel<D, G>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kAlloc);
+    if (e != cudaSuccess) return e;
+    Config c(dim3(nchunk, units), kThreads, stream);
+    c.cfg.dynamicSmemBytes = Ring<D>::kAlloc;
+    return cudaLaunchKernelEx(&c.cfg, kernel, p);
+}
+
 template <int D>
 cudaError_t launch_kv4_d(int G, const Kv4Params& p, int units, int nchunk, cudaStream_t stream) {
-    Config c(dim3(nchunk, units), kThreads, stream);
     cudaError_t e = cudaErrorInvalidValue;
-    if (G == 1) e = cudaLaunchKernelEx(&c.cfg, lf_kv4_attn_kernel<D, 1>, p);
-    if (G == 2) e = cudaLaunchKernelEx(&c.cfg, lf_kv4_attn_kernel<D, 2>, p);
-    if (G == 4) e = cudaLaunchKernelEx(&c.cfg, lf_kv4_attn_kernel<D, 4>, p);
-    if (G == 8) e = cudaLaunchKernelEx(&c.cfg, lf_kv4_attn_kernel<D, 8>, p);
+    if (G == 1) e = launch_kv4_dg<D, 1>(p, units, nchunk, stream);
+    if (G == 2) e = launch_kv4_dg<D, 2>(p, units, nchunk, stream);
+    if (G == 4) e = launch_kv4_dg<D, 4>(p, units, nchunk, stream);
+    if (G == 8) e = launch_kv4_dg<D, 8>(p, units, nchunk, stream);
     if (e != cudaSuccess || nchunk == 1) return e;
-    const int rows = units * G;
-    Config j(dim3((rows + kWarps - 1) / kWarps), kThreads, stream);
-    return cudaLaunchKernelEx(&j.cfg, lf_kv4_join_kernel<D>, p, rows, G, nchunk);
+    Config j(dim3(units * G), kThreads, stream);
+    return cudaLaunchKernelEx(&j.cfg, lf_kv4_join_kernel<D>, p, G, nchunk);
 }
 
 }  // namespace
