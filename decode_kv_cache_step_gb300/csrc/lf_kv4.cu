@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
     // q as halves of 2^13 to 2^14 for the largest: what is below 2^-38 of that is lost.
     uint32_t qf[NG][4];      // k steps of a group: codes at even, then odd nibbles
     uint32_t start[2];       // -8 sum q of the groups: an operand with the scales
-    float qs[2];             // what the halves are worth
+    float qs[2];             // what a logit's sum is worth (log2 domain)
     {
         uint32_t top = 0;
 #pragma unroll
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = min(126, 13 + 127 - static_cast<int>(top >> 7));  // >= -114
         const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);     // 2^e
-        const float unit = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
+        const float unit = p.unit * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // times 2^-e
         float sum[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -498,14 +498,12 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
     uint32_t E = 20;
     float fE = __uint_as_float((kHalfExp + 254 - 20) << 23);
 
-    int stage = 0;
-#pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-        const uint32_t t = s_tiles[warp][i];
-        uint8_t* const tile = ring + stage * R::kStage;
-        copy_wait<R::kStages - 1>();
+    // Waits for tile i of the list and puts the token's row in its place there.
+    auto arrive = [&](int i, const uint8_t* tile_c) {
+        uint8_t* const tile = const_cast<uint8_t*>(tile_c);
+        copy_wait<R::kStages - 2>();
         __syncwarp();
-        if (mine && static_cast<int>(t >> 16) == wi >> 4) {
+        if (mine && i < tiles && static_cast<int>(s_tiles[warp][i] >> 16) == wi >> 4) {
             const int row = wi & 15;
             if (lane < D / 32)
                 reinterpret_cast<uint4*>(tile + row * R::kKRow)[lane] = reinterpret_cast<const uint4*>(s_new[0])[lane];
@@ -519,26 +517,21 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             }
             __syncwarp();
         }
-        uint32_t kw[2][NG], ks[2][NG / 2], vw[4][NG / 2], vs[2][NG / 2], kz[2];
+    };
+    // Logits of the tile's slots r and r + 8, heads 2 c and 2 c + 1.
+    float x[4];
+    auto logits = [&](const uint8_t* tile) {
+        uint32_t kw[2][NG], ks[2][NG / 2], kz[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = r + 8 * h;
             shared_words<NG>(tile + row * R::kKRow + c * (D / 8), kw[h]);
             shared_words<NG / 2>(tile + R::kKScaleOff + row * R::kScaleRow, ks[h]);
-            shared_words<NG / 2>(tile + R::kVScaleOff + row * R::kScaleRow, vs[h]);
             kz[h] = *reinterpret_cast<const uint32_t*>(tile + R::kKScaleOff + row * R::kScaleRow +
                                                        c % (NG / 2) * 4);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            shared_words<NG / 2>(tile + R::kVOff + (2 * c + (k & 1) + 8 * (k >> 1)) * R::kVRow + r * (D / 16), vw[k]);
-        __syncwarp();
-        if (i + R::kStages < tiles) copy_tile(s_tiles[warp][i + R::kStages], stage);
-        copy_commit();
-        stage = stage + 1 == R::kStages ? 0 : stage + 1;
-
         const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        x[0] = x[1] = x[2] = x[3] = 0.f;
         const uint32_t z[4] = {kz[0], kz[1], kz[0], kz[1]};
         mma_bf16_16816(x, z, start[0], start[1]);
 #pragma unroll
@@ -556,11 +549,25 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             x[2] += sc[2] * sb;
             x[3] += sc[3] * sb;
         }
-        // (In two steps: either factor may be far from 1.)
-        x[0] = x[0] * p.unit * qs[0];
-        x[1] = x[1] * p.unit * qs[1];
-        x[2] = x[2] * p.unit * qs[0];
-        x[3] = x[3] * p.unit * qs[1];
+        x[0] *= qs[0];
+        x[1] *= qs[1];
+        x[2] *= qs[0];
+        x[3] *= qs[1];
+    };
+
+    const uint8_t* tile = ring;
+    int stage = 0;
+    if (tiles > 0) {
+        arrive(0, tile);
+        logits(tile);
+    }
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+        const uint32_t t = s_tiles[warp][i];
+        uint32_t vs[2][NG / 2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            shared_words<NG / 2>(tile + R::kVScaleOff + (r + 8 * h) * R::kScaleRow, vs[h]);
         if ((t & 0xffffu) != 0xffffu) {
             // Masked slots: weight 0, and 0 for the scales of whatever lies there.
             const bool liveA = (t >> r) & 1u, liveB = (t >> (r + 8)) & 1u;
@@ -620,6 +627,16 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             }
         }
         const float f0 = p0 * fE, f1 = p1 * fE, f2 = p2 * fE, f3 = p3 * fE;
+        uint32_t vw[4][NG / 2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            shared_words<NG / 2>(tile + R::kVOff + (2 * c + (k & 1) + 8 * (k >> 1)) * R::kVRow + r * (D / 16), vw[k]);
+        // The next tile's logits (of nothing behind the last one) beside this
+        // one's values: two chains of products to keep the pipes busy.
+        const int next_stage = stage + 1 == R::kStages ? 0 : stage + 1;
+        const uint8_t* const next = ring + next_stage * R::kStage;
+        arrive(i + 1, next);
+        logits(next);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const float sa = scale_of(vs[0][g >> 1], g & 1), sb = scale_of(vs[1][g >> 1], g & 1);
@@ -637,6 +654,11 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             const uint32_t eight[4] = {0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u};
             mma_f16_16816(off[g], eight, b0, b1, off[g]);
         }
+        __syncwarp();
+        if (i + R::kStages < tiles) copy_tile(s_tiles[warp][i + R::kStages], stage);
+        copy_commit();
+        stage = next_stage;
+        tile = next;
     }
 
     // The four warps' states, joined (each warp's part of O over its ring).
