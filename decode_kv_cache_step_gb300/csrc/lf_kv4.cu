@@ -181,8 +181,9 @@ __global__ void __launch_bounds__(kPackThreads) lf_kv4_unpack_kernel(const Kv4Pa
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxChunkSlots = 2048;
-constexpr int kMaxWarpTiles = kMaxChunkSlots / 16 / kWarps;
-// A warp's ring of tiles of 16 slots in shared memory.
+constexpr int kTileSlots = 32;
+constexpr int kMaxWarpTiles = kMaxChunkSlots / kTileSlots / kWarps;
+// A warp's ring of tiles of 32 slots in shared memory.
 template <int D>
 struct Ring {
     static constexpr int kKRow = D / 2;
@@ -190,11 +191,11 @@ struct Ring {
     // touch different banks.
     static constexpr int kVRow = D / 2 + 16;
     static constexpr int kScaleRow = D / 16;
-    static constexpr int kVOff = 16 * kKRow;
-    static constexpr int kKScaleOff = kVOff + 16 * kVRow;
-    static constexpr int kVScaleOff = kKScaleOff + 16 * kScaleRow;
-    static constexpr int kStage = kVScaleOff + 16 * kScaleRow;
-    static constexpr int kStages = D == 128 ? 5 : 9;
+    static constexpr int kVOff = kTileSlots * kKRow;
+    static constexpr int kKScaleOff = kVOff + kTileSlots * kVRow;
+    static constexpr int kVScaleOff = kKScaleOff + kTileSlots * kScaleRow;
+    static constexpr int kStage = kVScaleOff + kTileSlots * kScaleRow;
+    static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kWarp = kStages * kStage;
     static constexpr int kAlloc = kWarps * kWarp;
 };
@@ -254,8 +255,8 @@ __device__ __forceinline__ float scale_of(uint32_t word, int odd) {
     return __uint_as_float(odd ? word & 0xffff0000u : word << 16);
 }
 
-// One CTA: chunk blockIdx.x of unit blockIdx.y. Each warp takes 16 live slots at
-// a time through a ring of its own in shared memory (asynchronous copies; no
+// One CTA: chunk blockIdx.x of unit blockIdx.y. Each warp takes 32 slots at a
+// time, where one of them is live, through a ring of its own in shared memory (asynchronous copies; no
 // other warp is waited for):
 //   S^T[16 x 8] = K[16 x d] Q^T[d x 8]          per group, times the key's scale
 //   O^T[d x 8] += V^T[d x 16] (P s)^T[16 x 8]   per group, P s the weights times
@@ -268,11 +269,11 @@ __device__ __forceinline__ float scale_of(uint32_t word, int odd) {
 // the scales with q's sums over the groups, in three bf16 parts), and 8 sum P s,
 // a product per group with constant codes, is taken off O at the end.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Params p) {
+__global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Params p) {
     using R = Ring<D>;
     constexpr int NG = D / 32;
     extern __shared__ __align__(16) uint8_t s_ring[];
-    __shared__ uint32_t s_tiles[kWarps][kMaxWarpTiles];
+    __shared__ uint2 s_tiles[kWarps][kMaxWarpTiles];  // live slots, index in the chunk
     __shared__ float s_m[kWarps][G], s_l[kWarps][G];
     __shared__ __align__(16) uint8_t s_new[2][D / 2];  // the token's row in 4 bits
     __shared__ __nv_bfloat16 s_new_scale[2][NG];
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
     }
     const int wi = ws - slot0;
     const bool mine = ws >= 0 && wi >= 0 && wi < slots && ((wi >> 5) & (kWarps - 1)) == warp;
-    // The warp's live tiles of 16 slots.
+    // The warp's tiles with a live slot.
     int tiles = 0;
 #pragma unroll
     for (int k = 0; k < kBlocks; ++k) {
@@ -324,52 +325,49 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             live = true;
         }
         const uint32_t bits = __ballot_sync(0xffffffffu, live);
-        const int two = (bits & 0xffffu ? 1 : 0) + (bits >> 16 ? 1 : 0);
-        if (lane == 0) {
-            if (bits & 0xffffu) s_tiles[warp][tiles] = static_cast<uint32_t>(2 * block) << 16 | (bits & 0xffffu);
-            if (bits >> 16) s_tiles[warp][tiles + two - 1] = static_cast<uint32_t>(2 * block + 1) << 16 | bits >> 16;
-        }
-        tiles += two;
+        if (lane == 0 && bits) s_tiles[warp][tiles] = make_uint2(bits, block);
+        tiles += bits ? 1 : 0;
     }
     __syncwarp();
 
-    // Copies of a tile: 16 bytes of codes a lane at a time, one row's scales.
+    // Copies of a tile: 16 bytes of codes a lane at a time, a row's scales.
     const size_t unit0 = static_cast<size_t>(u) * S + slot0;
     constexpr int kRowChunks = D / 32;             // 16-byte chunks of a row's codes
-    constexpr int kCopies = kRowChunks / 2;        // of a lane, per tile and operand
+    constexpr int kCopies = kRowChunks;            // of a lane, per tile and operand
     constexpr int kStep = 32 / kRowChunks;         // rows between them
     const int crow = lane / kRowChunks;
     const uint8_t* const pk = p.k4 + unit0 * (D / 2) + lane * 16;
     const uint8_t* const pv = p.v4 + unit0 * (D / 2) + lane * 16;
-    const uint8_t* const ps = reinterpret_cast<const uint8_t*>(lane < 16 ? p.k_scale : p.v_scale) +
-                              (unit0 + (lane & 15)) * R::kScaleRow;
+    const uint8_t* const pks = reinterpret_cast<const uint8_t*>(p.k_scale) + (unit0 + lane) * R::kScaleRow;
+    const uint8_t* const pvs = reinterpret_cast<const uint8_t*>(p.v_scale) + (unit0 + lane) * R::kScaleRow;
     uint8_t* const ring = s_ring + warp * R::kWarp;
     const uint32_t dk = smem_u32(ring) + lane * 16;
     const uint32_t dv = smem_u32(ring) + R::kVOff + crow * R::kVRow + (lane % kRowChunks) * 16;
     const uint32_t ds = smem_u32(ring) + R::kKScaleOff + lane * R::kScaleRow;
-    auto copy_tile = [&](uint32_t t, int stage) {
-        const int tile = t >> 16;
+    auto copy_tile = [&](int tile, int stage) {
         const int at = stage * R::kStage;
-        const uint8_t* const k = pk + tile * (8 * D);
-        const uint8_t* const v = pv + tile * (8 * D);
-        const uint8_t* const scales = ps + tile * (16 * R::kScaleRow);
+        const uint8_t* const k = pk + tile * (kTileSlots * D / 2);
+        const uint8_t* const v = pv + tile * (kTileSlots * D / 2);
+        const uint8_t* const k_scales = pks + tile * (kTileSlots * R::kScaleRow);
+        const uint8_t* const v_scales = pvs + tile * (kTileSlots * R::kScaleRow);
         const auto rows = [&](int most) {  // copies of the rows that are there
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
                 copy_async<16>(dk + at + i * 512, k + i * 512, crow + i * kStep < most);
                 copy_async<16>(dv + at + i * kStep * R::kVRow, v + i * 512, crow + i * kStep < most);
             }
-            copy_async<R::kScaleRow>(ds + at, scales, (lane & 15) < most);
+            copy_async<R::kScaleRow>(ds + at, k_scales, lane < most);
+            copy_async<R::kScaleRow>(ds + at + kTileSlots * R::kScaleRow, v_scales, lane < most);
         };
-        const int most = slots - tile * 16;
-        if (most >= 16)
-            rows(16);
+        const int most = slots - tile * kTileSlots;
+        if (most >= kTileSlots)
+            rows(kTileSlots);
         else
             rows(most);
     };
 #pragma unroll
     for (int i = 0; i < R::kStages; ++i) {
-        if (i < tiles) copy_tile(s_tiles[warp][i], i);
+        if (i < tiles) copy_tile(s_tiles[warp][i].y, i);
         copy_commit();
     }
 
@@ -499,12 +497,11 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
     float fE = __uint_as_float((kHalfExp + 254 - 20) << 23);
 
     // Waits for tile i of the list and puts the token's row in its place there.
-    auto arrive = [&](int i, const uint8_t* tile_c) {
-        uint8_t* const tile = const_cast<uint8_t*>(tile_c);
+    auto arrive = [&](int i, uint8_t* tile) {
         copy_wait<R::kStages - 2>();
         __syncwarp();
-        if (mine && i < tiles && static_cast<int>(s_tiles[warp][i] >> 16) == wi >> 4) {
-            const int row = wi & 15;
+        if (mine && i < tiles && static_cast<int>(s_tiles[warp][i].y) == wi / kTileSlots) {
+            const int row = wi % kTileSlots;
             if (lane < D / 32)
                 reinterpret_cast<uint4*>(tile + row * R::kKRow)[lane] = reinterpret_cast<const uint4*>(s_new[0])[lane];
             else if (lane < D / 16)
@@ -518,44 +515,47 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             __syncwarp();
         }
     };
-    // Logits of the tile's slots r and r + 8, heads 2 c and 2 c + 1.
-    float x[4];
+    // Logits of the tile's slots r + 8 h: x[2 h] and x[2 h + 1], heads 2 c and 2 c + 1.
+    float x[8];
     auto logits = [&](const uint8_t* tile) {
-        uint32_t kw[2][NG], ks[2][NG / 2], kz[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = r + 8 * h;
-            shared_words<NG>(tile + row * R::kKRow + c * (D / 8), kw[h]);
-            shared_words<NG / 2>(tile + R::kKScaleOff + row * R::kScaleRow, ks[h]);
-            kz[h] = *reinterpret_cast<const uint32_t*>(tile + R::kKScaleOff + row * R::kScaleRow +
-                                                       c % (NG / 2) * 4);
-        }
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        x[0] = x[1] = x[2] = x[3] = 0.f;
-        const uint32_t z[4] = {kz[0], kz[1], kz[0], kz[1]};
-        mma_bf16_16816(x, z, start[0], start[1]);
+        for (int half = 0; half < 2; ++half) {
+            uint32_t kw[2][NG], ks[2][NG / 2], kz[2];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            float sc[4];
-            const uint32_t a[4] = {kw[0][g] & 0x000f000fu, kw[1][g] & 0x000f000fu,
-                                   (kw[0][g] >> 8) & 0x000f000fu, (kw[1][g] >> 8) & 0x000f000fu};
-            mma_f16_16816(sc, a, qf[g][0], qf[g][1], zero);
-            const uint32_t o[4] = {kw[0][g] & 0x00f000f0u, kw[1][g] & 0x00f000f0u,
-                                   (kw[0][g] >> 8) & 0x00f000f0u, (kw[1][g] >> 8) & 0x00f000f0u};
-            mma_f16_16816(sc, o, qf[g][2], qf[g][3], sc);
-            const float sa = scale_of(ks[0][g >> 1], g & 1), sb = scale_of(ks[1][g >> 1], g & 1);
-            x[0] += sc[0] * sa;
-            x[1] += sc[1] * sa;
-            x[2] += sc[2] * sb;
-            x[3] += sc[3] * sb;
+            for (int h = 0; h < 2; ++h) {
+                const int row = r + 8 * h + 16 * half;
+                shared_words<NG>(tile + row * R::kKRow + c * (D / 8), kw[h]);
+                shared_words<NG / 2>(tile + R::kKScaleOff + row * R::kScaleRow, ks[h]);
+                kz[h] = *reinterpret_cast<const uint32_t*>(tile + R::kKScaleOff + row * R::kScaleRow +
+                                                           c % (NG / 2) * 4);
+            }
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t z[4] = {kz[0], kz[1], kz[0], kz[1]};
+            mma_bf16_16816(y, z, start[0], start[1]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float sc[4];
+                const uint32_t a[4] = {kw[0][g] & 0x000f000fu, kw[1][g] & 0x000f000fu,
+                                       (kw[0][g] >> 8) & 0x000f000fu, (kw[1][g] >> 8) & 0x000f000fu};
+                mma_f16_16816(sc, a, qf[g][0], qf[g][1], zero);
+                const uint32_t o[4] = {kw[0][g] & 0x00f000f0u, kw[1][g] & 0x00f000f0u,
+                                       (kw[0][g] >> 8) & 0x00f000f0u, (kw[1][g] >> 8) & 0x00f000f0u};
+                mma_f16_16816(sc, o, qf[g][2], qf[g][3], sc);
+                const float sa = scale_of(ks[0][g >> 1], g & 1), sb = scale_of(ks[1][g >> 1], g & 1);
+                y[0] += sc[0] * sa;
+                y[1] += sc[1] * sa;
+                y[2] += sc[2] * sb;
+                y[3] += sc[3] * sb;
+            }
+            x[4 * half] = y[0] * qs[0];
+            x[4 * half + 1] = y[1] * qs[1];
+            x[4 * half + 2] = y[2] * qs[0];
+            x[4 * half + 3] = y[3] * qs[1];
         }
-        x[0] *= qs[0];
-        x[1] *= qs[1];
-        x[2] *= qs[0];
-        x[3] *= qs[1];
     };
 
-    const uint8_t* tile = ring;
+    uint8_t* tile = ring;
     int stage = 0;
     if (tiles > 0) {
         arrive(0, tile);
@@ -563,25 +563,24 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
     }
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
-        const uint32_t t = s_tiles[warp][i];
-        uint32_t vs[2][NG / 2];
+        const uint32_t live = s_tiles[warp][i].x;
+        uint32_t vs[4][NG / 2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 4; ++h)
             shared_words<NG / 2>(tile + R::kVScaleOff + (r + 8 * h) * R::kScaleRow, vs[h]);
-        if ((t & 0xffffu) != 0xffffu) {
+        if (live != 0xffffffffu) {
             // Masked slots: weight 0, and 0 for the scales of whatever lies there.
-            const bool liveA = (t >> r) & 1u, liveB = (t >> (r + 8)) & 1u;
-            x[0] = liveA ? x[0] : NEG;
-            x[1] = liveA ? x[1] : NEG;
-            x[2] = liveB ? x[2] : NEG;
-            x[3] = liveB ? x[3] : NEG;
 #pragma unroll
-            for (int k = 0; k < NG / 2; ++k) {
-                vs[0][k] = liveA ? vs[0][k] : 0u;
-                vs[1][k] = liveB ? vs[1][k] : 0u;
+            for (int h = 0; h < 4; ++h) {
+                const bool is = (live >> (r + 8 * h)) & 1u;
+                x[2 * h] = is ? x[2 * h] : NEG;
+                x[2 * h + 1] = is ? x[2 * h + 1] : NEG;
+#pragma unroll
+                for (int k = 0; k < NG / 2; ++k) vs[h][k] = is ? vs[h][k] : 0u;
             }
         }
-        float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+        float mx0 = fmaxf(fmaxf(x[0], x[2]), fmaxf(x[4], x[6]));
+        float mx1 = fmaxf(fmaxf(x[1], x[3]), fmaxf(x[5], x[7]));
         if (__any_sync(0xffffffffu, mx0 > m0 + kGrowth || mx1 > m1 + kGrowth)) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
@@ -599,21 +598,20 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
             m1 = mx1;
             rescale(f0, f1);
         }
-        const float p0 = ex2_approx(x[0] - base0), p1 = ex2_approx(x[1] - base1);
-        const float p2 = ex2_approx(x[2] - base0), p3 = ex2_approx(x[3] - base1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
         // The largest scale, as the bits of two bf16 side by side.
         uint32_t two = 0;
 #pragma unroll
-        for (int k = 0; k < NG / 2; ++k) two = __vimax3_u16x2(two, vs[0][k], vs[1][k]);
+        for (int k = 0; k < NG / 2; ++k) {
+            two = __vimax3_u16x2(two, vs[0][k], vs[1][k]);
+            two = __vimax3_u16x2(two, vs[2][k], vs[3][k]);
+        }
         if (__any_sync(0xffffffffu, max(two & 0xffffu, two >> 16) >= (E + 1) << 7)) {
             // Rare: a new power of two, of the finite ones.
             uint32_t top = 0;
 #pragma unroll
             for (int k = 0; k < NG / 2; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 4; ++h) {
                     const uint32_t lo = vs[h][k] & 0x7f80u, hi = (vs[h][k] >> 16) & 0x7f80u;
                     if (lo != 0x7f80u) top = max(top, lo);
                     if (hi != 0x7f80u) top = max(top, hi);
@@ -626,36 +624,52 @@ __global__ void __launch_bounds__(kThreads, 4) lf_kv4_attn_kernel(const Kv4Param
                 fE = __uint_as_float((kHalfExp + 254 - E) << 23);
             }
         }
-        const float f0 = p0 * fE, f1 = p1 * fE, f2 = p2 * fE, f3 = p3 * fE;
-        uint32_t vw[4][NG / 2];
+        // The weights; the sums take them unrounded.
+        float f[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            shared_words<NG / 2>(tile + R::kVOff + (2 * c + (k & 1) + 8 * (k >> 1)) * R::kVRow + r * (D / 16), vw[k]);
+        for (int h = 0; h < 4; ++h) {
+            f[2 * h] = ex2_approx(x[2 * h] - base0);
+            f[2 * h + 1] = ex2_approx(x[2 * h + 1] - base1);
+        }
+        l0 += (f[0] + f[2]) + (f[4] + f[6]);
+        l1 += (f[1] + f[3]) + (f[5] + f[7]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= fE;
         // The next tile's logits (of nothing behind the last one) beside this
         // one's values: two chains of products to keep the pipes busy.
         const int next_stage = stage + 1 == R::kStages ? 0 : stage + 1;
-        const uint8_t* const next = ring + next_stage * R::kStage;
+        uint8_t* const next = ring + next_stage * R::kStage;
         arrive(i + 1, next);
         logits(next);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float sa = scale_of(vs[0][g >> 1], g & 1), sb = scale_of(vs[1][g >> 1], g & 1);
-            const uint32_t b0 = movmatrix_trans(pack_f16x2(f0 * sa, f1 * sa));
-            const uint32_t b1 = movmatrix_trans(pack_f16x2(f2 * sb, f3 * sb));
-            // Slots 2 c and 2 c + 1 side by side: the lane's four codes of group g.
-            const uint32_t pick = g & 1 ? 0x7632u : 0x5410u;
-            const uint32_t ya = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], pick);
-            const uint32_t yb = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], pick);
-            const uint32_t lo[4] = {ya & 0x000f000fu, ya & 0x00f000f0u, yb & 0x000f000fu, yb & 0x00f000f0u};
-            mma_f16_16816(acc[2 * g], lo, b0, b1, acc[2 * g]);
-            const uint32_t za = ya >> 8, zb = yb >> 8;
-            const uint32_t hi[4] = {za & 0x000f000fu, za & 0x00f000f0u, zb & 0x000f000fu, zb & 0x00f000f0u};
-            mma_f16_16816(acc[2 * g + 1], hi, b0, b1, acc[2 * g + 1]);
-            const uint32_t eight[4] = {0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u};
-            mma_f16_16816(off[g], eight, b0, b1, off[g]);
+        for (int half = 0; half < 2; ++half) {
+            uint32_t vw[4][NG / 2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                shared_words<NG / 2>(tile + R::kVOff + (16 * half + 2 * c + (k & 1) + 8 * (k >> 1)) * R::kVRow +
+                                         r * (D / 16),
+                                     vw[k]);
+            const float* const fh = f + 4 * half;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float sa = scale_of(vs[2 * half][g >> 1], g & 1), sb = scale_of(vs[2 * half + 1][g >> 1], g & 1);
+                const uint32_t b0 = movmatrix_trans(pack_f16x2(fh[0] * sa, fh[1] * sa));
+                const uint32_t b1 = movmatrix_trans(pack_f16x2(fh[2] * sb, fh[3] * sb));
+                // Slots 2 c and 2 c + 1 side by side: the lane's four codes of group g.
+                const uint32_t pick = g & 1 ? 0x7632u : 0x5410u;
+                const uint32_t ya = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], pick);
+                const uint32_t yb = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], pick);
+                const uint32_t lo[4] = {ya & 0x000f000fu, ya & 0x00f000f0u, yb & 0x000f000fu, yb & 0x00f000f0u};
+                mma_f16_16816(acc[2 * g], lo, b0, b1, acc[2 * g]);
+                const uint32_t za = ya >> 8, zb = yb >> 8;
+                const uint32_t hi[4] = {za & 0x000f000fu, za & 0x00f000f0u, zb & 0x000f000fu, zb & 0x00f000f0u};
+                mma_f16_16816(acc[2 * g + 1], hi, b0, b1, acc[2 * g + 1]);
+                const uint32_t eight[4] = {0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u};
+                mma_f16_16816(off[g], eight, b0, b1, off[g]);
+            }
         }
         __syncwarp();
-        if (i + R::kStages < tiles) copy_tile(s_tiles[warp][i + R::kStages], stage);
+        if (i + R::kStages < tiles) copy_tile(s_tiles[warp][i + R::kStages].y, stage);
         copy_commit();
         stage = next_stage;
         tile = next;
@@ -820,10 +834,10 @@ cudaError_t launch_kv4_d(int G, const Kv4Params& p, int units, int nchunk, cudaS
 }  // namespace
 
 Kv4Plan kv4_plan(int units, int S, int sms) {
-    // Four CTAs are resident per SM; chunks of whole 128 slots (32 a warp).
+    // Three CTAs are resident per SM; chunks of whole 128 slots (32 a warp).
     const int steps = (S + 127) / 128;
     const int longest = kMaxChunkSlots / 128;
-    const int fill = std::max(1, 4 * sms / units);
+    const int fill = std::max(1, 3 * sms / units);
     const int n = std::max((steps + longest - 1) / longest, std::min(steps, fill));
     const int per = (steps + n - 1) / n;
     return Kv4Plan{per * 128, (steps + per - 1) / per};
