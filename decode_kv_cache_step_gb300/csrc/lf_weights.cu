@@ -8,9 +8,10 @@
 //   rows     a CTA holds 128 query rows (128 / g tokens times the g heads that
 //            share a KV head) and streams key tiles: each row's running maximum
 //            and sum (in pieces of the key axis when rows are few);
-//   columns  a CTA holds 128 keys and streams the query tiles that see them:
-//            the products' transpose, so a thread owns a key and adds up its
-//            weights in registers, in a fixed order.
+//   columns  the products' transpose, so a thread owns a key and adds up its
+//            weights in registers, in a fixed order. A CTA holds 128 keys and
+//            streams the query tiles that see them; where no sequence has more
+//            rows than one tile, it holds that tile and streams the keys.
 // Neither pass writes a score. Both are one tensor product per tile, a thread
 // issuing them into two accumulators in tensor memory, TMA loads ahead through a
 // ring, and four warps that read the accumulators; two CTAs share an SM, so one's
@@ -54,6 +55,13 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
+// 2^x of two packed values.
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x2) {
+    float a, b;
+    unpack_f32x2(x2, a, b);
+    return pack_f32x2(ex2_approx(a), ex2_approx(b));
+}
+
 // The counted rows of a sequence: its tokens first .. r.n - 1.
 __device__ __forceinline__ int first_row(const PromptWeightsParams& p, const SeqRange& r) {
     return p.rows > 0 ? max(0, r.n - p.rows) : 0;
@@ -72,10 +80,15 @@ struct Work {
     int end;    // behind the last
 };
 
-// Rows pass: CTA x's tile of rows and its piece of the keys.
-__device__ __forceinline__ bool rows_work(const PromptWeightsParams& p, int tok, Work* w) {
+// A tile of rows and a piece of the keys they see (rows pass; columns pass with
+// few rows).
+__device__ __forceinline__ bool rows_work(const PromptWeightsParams& p, int tok, bool report, Work* w) {
     const int item = p.items - 1 - static_cast<int>(blockIdx.x) / p.Hkv;  // longest rows first
     w->kvh = blockIdx.x % p.Hkv;
+    // (There are at least as many items as sequences.)
+    if (report && item < p.B && w->kvh == 0 && blockIdx.y == 0 && threadIdx.x == 0 &&
+        !seq_range(p.q_start, p.kv_len, item, p.T, p.S, true, &w->r))
+        atomicOr(p.dev_err, kErrBadLength);
     int rel;
     if (p.by_sequence) {
         const int per = (p.rows + tok - 1) / tok;
@@ -100,39 +113,31 @@ __device__ __forceinline__ bool rows_work(const PromptWeightsParams& p, int tok,
     if (w->at >= w->r.n) return false;
     const int keys = w->r.kv - w->r.n + min(w->at + tok, w->r.n);  // the last row's
     const int tiles = (keys + kRows - 1) / kRows;
-    const int piece = blockIdx.y;
-    w->first = static_cast<int>(static_cast<int64_t>(tiles) * piece / p.pieces) * kRows;
-    w->end = min(keys, static_cast<int>(static_cast<int64_t>(tiles) * (piece + 1) / p.pieces) * kRows);
+    const int pieces = gridDim.y;
+    w->first = static_cast<int>(static_cast<int64_t>(tiles) * blockIdx.y / pieces) * kRows;
+    w->end = min(keys, static_cast<int>(static_cast<int64_t>(tiles) * (blockIdx.y + 1) / pieces) * kRows);
     return true;
 }
 
-// Columns pass: CTA x's keys and the rows that see one of them. (All threads:
-// the rows pass finds packed tiles by their order, so unless q_start ascends
-// nothing is written.)
-__device__ __forceinline__ bool columns_work(const PromptWeightsParams& p, int, Work* w) {
+// 128 keys and the rows that see one of them (columns pass).
+__device__ __forceinline__ bool keys_work(const PromptWeightsParams& p, Work* w) {
     w->kvh = blockIdx.x % p.Hkv;
     const int y = blockIdx.x / p.Hkv;
     w->b = y % p.B;
     w->at = y / p.B * kRows;
-    if (!seq_range(p.q_start, p.kv_len, w->b, p.T, p.S, true, &w->r)) {
-        if (threadIdx.x == 0 && w->at == 0 && w->kvh == 0) atomicOr(p.dev_err, kErrBadLength);
-        return false;
-    }
-    if (!p.by_sequence) {
-        bool good = true;
-        for (int i = threadIdx.x; i < p.B; i += kThreads) {
-            const int a = p.q_start[i], b = p.q_start[i + 1];
-            good = good && a >= 0 && a <= b && b <= p.T;
-        }
-        if (!__syncthreads_and(good)) return false;
-    }
+    if (!seq_range(p.q_start, p.kv_len, w->b, p.T, p.S, true, &w->r)) return false;
     if (w->r.n == 0 || w->at >= w->r.kv) return false;
     w->first = max(first_row(p, w->r), w->at - (w->r.kv - w->r.n));
     w->end = w->r.n;
     return true;
 }
 
-template <int D, bool kColumns>
+// The kernel's forms.
+constexpr int kRowsPass = 0;
+constexpr int kColumnsPass = 1;  // keys held
+constexpr int kFewRows = 2;      // the columns pass with the one tile of rows held
+
+template <int D, int kForm>
 __global__ void __launch_bounds__(kThreads, 2)
     lf_prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ,
                              const __grid_constant__ CUtensorMap tmK,
@@ -158,9 +163,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int g = p.Hq / p.Hkv;
     const int gs = __ffs(g) - 1;
     const int tok = kRows >> gs;
+    constexpr bool kKeysHeld = kForm == kColumnsPass;
     Work w;
-    if (kColumns ? !columns_work(p, tok, &w) : !rows_work(p, tok, &w)) return;
-    const int step = kColumns ? tok : kRows;
+    if (kKeysHeld ? !keys_work(p, &w) : !rows_work(p, tok, kForm == kRowsPass, &w)) return;
+    if (kForm != kRowsPass && !p.by_sequence) {
+        // The rows pass finds packed tiles by their order: unless q_start ascends
+        // nothing is written.
+        bool good = true;
+        for (int i = tid; i < p.B; i += kThreads) {
+            const int from = p.q_start[i], to = p.q_start[i + 1];
+            good = good && from >= 0 && from <= to && to <= p.T;
+        }
+        if (!__syncthreads_and(good)) return;
+    }
+    const int step = kKeysHeld ? tok : kRows;
     const int tiles = w.end > w.first ? (w.end - w.first + step - 1) / step : 0;
 
     if (warp == 5) {
@@ -197,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         tma_load(dst + c * kPanel + h * (kPanel / 2), &tmK, c * 64, j + h * 64, unit, bar);
             };
             mbar_arrive_expect_tx(held, L::kTileBytes);
-            if (kColumns)
+            if (kKeysHeld)
                 load_k(smem, w.at, held);
             else
                 load_q(smem, w.at, held);
@@ -210,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 mbar_arrive_expect_tx(&full[st], L::kTileBytes);
                 uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes;
-                if (kColumns)
+                if (kKeysHeld)
                     load_q(dst, w.first + n * step, &full[st]);
                 else
                     load_k(dst, w.first + n * step, &full[st]);
@@ -224,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (tiles > 0 && elect_one()) {
             // -------------------------------------------------- products --
             const uint32_t idesc = instr_desc(kRows, kRows, false) | (p.negate ? kInstrNegateA : 0u);
-            const uint64_t ad = smem_desc(smem_u32(smem), 16, 1024);
+            // The accumulators' lanes are the keys, but for the rows pass: the
+            // streamed tile is the first operand where the rows are held.
+            const uint64_t hd = smem_desc(smem_u32(smem), 16, 1024);
             bool ok = mbar_wait(held, 0, p.wait_limit_ns);
             for (int n = 0; ok && n < tiles; ++n) {
                 const int st = n % kRing, s = n & 1;
@@ -232,7 +250,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                      mbar_wait(&s_free[s], ((n >> 1) & 1) ^ 1, p.wait_limit_ns);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t bd = smem_desc(smem_u32(smem + L::kRingOff + st * L::kTileBytes), 16, 1024);
+                const uint64_t sd = smem_desc(smem_u32(smem + L::kRingOff + st * L::kTileBytes), 16, 1024);
+                const uint64_t ad = kForm == kFewRows ? sd : hd;
+                const uint64_t bd = kForm == kFewRows ? hd : sd;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = ((k >> 2) * kPanel + (k & 3) * 32) / 16;
@@ -266,7 +286,52 @@ __global__ void __launch_bounds__(kThreads, 2)
             return true;
         };
         bool ok = true;
-        if (!kColumns) {
+        // -r of the row of token t, head tid % g: -inf (no weight) without a sum.
+        const size_t next_piece = static_cast<size_t>(p.stat_rows) * p.Hq;
+        const auto stat_at = [&](int t) {
+            return p.stats + static_cast<size_t>(stat_row(p, w.b, w.r, t)) * p.Hq + (w.kvh << gs) + (tid & (g - 1));
+        };
+        const auto minus_r = [&](float2 v) { return v.y == 0.f ? -INFINITY : -(v.x + __log2f(v.y)); };
+        const auto joined = [&](int t) {
+            const float2* src = stat_at(t);
+            float2 sum = make_float2(-INFINITY, 0.f);
+            for (int k = 0; k < p.pieces; ++k) sum.x = fmaxf(sum.x, __ldcg(src + k * next_piece).x);
+            if (sum.x == -INFINITY) sum.x = 0.f;
+            for (int k = 0; k < p.pieces; ++k) {
+                const float2 v = __ldcg(src + k * next_piece);
+                sum.y += v.y * exp2f(v.x - sum.x);
+            }
+            return sum;
+        };
+        // A key's weights of the tile's 128 rows; columns [lo, hi) see it.
+        const auto column_sum = [&](uint32_t (&x)[128], const float* minus, bool some, int lo, int hi) {
+            const float4* r4 = reinterpret_cast<const float4*>(minus);
+            if (some) {
+#pragma unroll
+                for (int e = 0; e < 128; ++e) x[e] = e >= lo && e < hi ? x[e] : 0xff800000u;
+            }
+            uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 128; e += 4) {
+                const float4 r = r4[e >> 2];
+                const uint64_t y0 = fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2,
+                                              pack_f32x2(r.x, r.y));
+                const uint64_t y1 = fma_f32x2(pack_f32x2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), c2,
+                                              pack_f32x2(r.z, r.w));
+                const int q = e >> 1;
+                sum[q & 3] = add_f32x2(sum[q & 3], ex2_pair(y0));
+                sum[(q + 1) & 3] = add_f32x2(sum[(q + 1) & 3], ex2_pair(y1));
+            }
+            float a, b;
+            unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), a, b);
+            return a + b;
+        };
+        const auto store = [&](int j, float total) {
+            if (j >= w.r.kv) return;
+            float* dst = p.weights + static_cast<size_t>(unit) * p.S + j;
+            *dst = j < past ? *dst + total : total;
+        };
+        if (kForm == kRowsPass) {
             // A thread owns the row of token w.at + tid / g, head tid % g.
             const int t = w.at + (tid >> gs);
             const int seen = past + t + 1;  // keys the row sees
@@ -283,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
+                for (int e = 0; e < 128; e += 2)
+                    mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
                 const float to = fmaxf(m, top);
                 const float base = to == -INFINITY ? 0.f : to;
@@ -292,86 +358,56 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint64_t b2 = pack_f32x2(-base, -base);
                 uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < 128; e += 2) {
-                    float a, b;
-                    unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, b2), a, b);
-                    sum[(e >> 1) & 3] = add_f32x2(sum[(e >> 1) & 3], pack_f32x2(ex2_approx(a), ex2_approx(b)));
+                for (int q = 0; q < 64; ++q) {
+                    const uint64_t y = fma_f32x2(pack_f32x2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])), c2, b2);
+                    sum[q & 3] = add_f32x2(sum[q & 3], ex2_pair(y));
                 }
                 float a, b;
                 unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), a, b);
                 l += a + b;
             }
-            if (!ok && lane == 0) atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT);
-            if (t < w.r.n)
-                p.stats[static_cast<size_t>(blockIdx.y) * p.stat_rows * p.Hq +
-                        static_cast<size_t>(stat_row(p, w.b, w.r, t)) * p.Hq + (w.kvh << gs) + (tid & (g - 1))] =
-                    make_float2(m, l);
-        } else {
+            if (t < w.r.n) const_cast<float2*>(stat_at(t))[blockIdx.y * next_piece] = make_float2(m, l);
+        } else if (kForm == kColumnsPass) {
             // A thread owns key w.at + tid; columns are rows of the query tile.
             const int j = w.at + tid;
-            // -r of the row that is this thread's column of query tile n: -inf
-            // (no weight) for a row without a sum.
-            const auto statistic = [&](int n) {
-                const int t = w.first + n * step + (tid >> gs);
-                if (n >= tiles || t >= w.r.n) return -INFINITY;
-                const float2* src = p.stats + static_cast<size_t>(stat_row(p, w.b, w.r, t)) * p.Hq +
-                                    (w.kvh << gs) + (tid & (g - 1));
-                const size_t next = static_cast<size_t>(p.stat_rows) * p.Hq;
-                float m = -INFINITY;
-                for (int k = 0; k < p.pieces; ++k) m = fmaxf(m, __ldcg(src + k * next).x);
-                const float base = m == -INFINITY ? 0.f : m;
-                float l = 0.f;
-                for (int k = 0; k < p.pieces; ++k) {
-                    const float2 v = __ldcg(src + k * next);
-                    l += v.y * exp2f(v.x - base);
-                }
-                return l == 0.f ? -INFINITY : -(base + __log2f(l));
-            };
+            // Statistics of the row that is this thread's column of tile n.
+            const auto row_of = [&](int n) { return min(w.first + n * step + (tid >> gs), w.r.n - 1); };
             float total = 0.f;
-            if (tiles > 0) stat[tid] = statistic(0);
+            stat[tid] = minus_r(p.pieces > 1 ? joined(row_of(0)) : __ldcg(stat_at(row_of(0))));
             asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll 1
             for (int n = 0; n < tiles; ++n) {
-                const float then = statistic(n + 1);
+                // (In flight while the tile is worked.)
+                const float2 then = p.pieces > 1 ? joined(row_of(n + 1)) : __ldcg(stat_at(row_of(n + 1)));
                 uint32_t x[128];
                 // (A warp that has given up keeps to the barriers below.)
                 ok = ok && take(n, x);
                 const int t0 = w.first + n * step;
                 // Column e is a row of token t0 + e / g. From token j - past on
                 // they see the key, up to the sequence's last.
-                const int hidden = (j - past - t0) << gs;
                 const int there = (w.r.n - t0) << gs;
                 const bool some = w.at + kRows > past + t0 + 1 || there < kRows;
-                const float4* r4 = reinterpret_cast<const float4*>(stat + (n & 1) * kRows);
-                uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int e = 0; e < 128; e += 4) {
-                    const float4 r = r4[e >> 2];
-                    float a[4];
-                    unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2,
-                                           pack_f32x2(r.x, r.y)), a[0], a[1]);
-                    unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), c2,
-                                           pack_f32x2(r.z, r.w)), a[2], a[3]);
-                    if (some) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) a[k] = e + k >= hidden && e + k < there ? a[k] : -INFINITY;
-                    }
-                    sum[(e >> 1) & 3] = add_f32x2(sum[(e >> 1) & 3], pack_f32x2(ex2_approx(a[0]), ex2_approx(a[1])));
-                    sum[((e >> 1) + 1) & 3] =
-                        add_f32x2(sum[((e >> 1) + 1) & 3], pack_f32x2(ex2_approx(a[2]), ex2_approx(a[3])));
-                }
-                float a, b;
-                unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), a, b);
-                if (ok) total += a + b;
-                stat[((n + 1) & 1) * kRows + tid] = then;
+                const float sum = column_sum(x, stat + (n & 1) * kRows, some, (j - past - t0) << gs, there);
+                if (ok) total += sum;
+                stat[((n + 1) & 1) * kRows + tid] = minus_r(then);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
-            if (!ok && lane == 0) atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT);
-            if (j < w.r.kv) {
-                float* dst = p.weights + static_cast<size_t>(unit) * p.S + j;
-                *dst = j < past ? *dst + total : total;
+            store(j, total);
+        } else {
+            // Streamed keys; every tile's sums are final.
+            stat[tid] = minus_r(joined(min(w.at + (tid >> gs), w.r.n - 1)));
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll 1
+            for (int n = 0; n < tiles; ++n) {
+                uint32_t x[128];
+                if (!(ok = take(n, x))) break;
+                const int j0 = w.first + n * kRows;
+                const int there = (w.r.n - w.at) << gs;
+                const bool some = j0 + kRows > past + w.at + 1 || there < kRows;
+                store(j0 + tid, column_sum(x, stat, some, (j0 + tid - past - w.at) << gs, there));
             }
         }
+        if (!ok && lane == 0) atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT);
     }
     tc_fence_before();
     __syncthreads();
@@ -379,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 5) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool kColumns>
+template <int D, int kForm>
 cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmK, const PromptWeightsParams& p,
                         dim3 grid, cudaStream_t stream) {
-    const auto kernel = lf_prompt_weights_kernel<D, kColumns>;
+    const auto kernel = lf_prompt_weights_kernel<D, kForm>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          WeightsSmem<D>::kAlloc);
     if (e != cudaSuccess) return e;
@@ -403,10 +439,14 @@ cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmK, const Pr
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const PromptWeightsParams& p,
                      cudaStream_t stream) {
-    const cudaError_t e = launch_pass<D, false>(tmQ, tmK, p, dim3(p.items * p.Hkv, p.pieces), stream);
+    const dim3 rows(p.items * p.Hkv, p.pieces);
+    const cudaError_t e = launch_pass<D, kRowsPass>(tmQ, tmK, p, rows, stream);
     if (e != cudaSuccess) return e;
+    // No more rows in a sequence than a tile holds?
+    const int most = p.rows > 0 ? std::min(p.rows, p.T) : p.T;
+    if (most * (p.Hq / p.Hkv) <= kRows) return launch_pass<D, kFewRows>(tmQ, tmK, p, rows, stream);
     const int tiles = (p.S + kRows - 1) / kRows;
-    return launch_pass<D, true>(tmQ, tmK, p, dim3(tiles * p.B * p.Hkv), stream);
+    return launch_pass<D, kColumnsPass>(tmQ, tmK, p, dim3(tiles * p.B * p.Hkv), stream);
 }
 
 }  // namespace
