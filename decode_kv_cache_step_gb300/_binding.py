@@ -537,10 +537,10 @@ def _check_axes(positions, pair_axis, T, rot):
     if not isinstance(positions, torch.Tensor) or positions.dim() != 2:
         raise ValueError("positions must be [axes,T]")
     _need(positions, "positions", torch.int32, (positions.shape[0], T), True)
-    if isinstance(pair_axis, torch.Tensor) and pair_axis.is_cuda:
-        raise ValueError("pair_axis: must be on the host")
+    if isinstance(pair_axis, int) or isinstance(pair_axis, torch.Tensor) and pair_axis.is_cuda:
+        raise ValueError("pair_axis: expected rot/2 axes on the host")
     try:
-        pairs = bytes(int(a) for a in pair_axis)
+        pairs = bytes(pair_axis.tolist() if isinstance(pair_axis, torch.Tensor) else pair_axis)
     except (TypeError, ValueError) as e:
         raise ValueError(f"pair_axis: expected rot/2 axes, {e}") from None
     if len(pairs) != rot // 2:
@@ -732,10 +732,10 @@ def decode_weights_workspace(B, Hq, Hkv, d, S, k=1) -> int:
     return int(n.value)
 
 
-# The size is a function of the sizes, the device and the plan's switches alone.
-_PLAN_SWITCHES = ("LF_CHUNK_TILES", "LF_STAGES", "LF_CLUSTER", "LF_CLUSTER_MAX", "LF_DEEP")
+# The size is a function of the sizes and the device, and of the plan's switches:
+# a call that finds it too small asks again.
 _weights_bytes = functools.lru_cache(maxsize=1024)(
-    lambda index, switches, *sizes: decode_weights_workspace(*sizes))
+    lambda index, *sizes: decode_weights_workspace(*sizes))
 
 
 def decode_step_weights(q, k_cache, v_cache, mask, weights, new_k, new_v, write_slot, out,
@@ -751,14 +751,25 @@ def decode_step_weights(q, k_cache, v_cache, mask, weights, new_k, new_v, write_
     topk = 1 if k is None else int(k)
     with _on_device(q.device, k_cache, v_cache, mask, weights, new_k, new_v, write_slot, out,
                     next_slots):
-        ws = _workspace(workspace, 0 if workspace is not None else
-                        _weights_bytes(q.device.index, tuple(map(os.environ.get, _PLAN_SWITCHES)),
-                                       B, Hq, Hkv, d, S, topk), q.device, stream)
-        _check(lib, lib.lf_decode_step_weights(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(),
-            weights.data_ptr(), new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(),
-            out.data_ptr(), next_slots.data_ptr(), topk, int(flags), B, Hq, Hkv, d, S, int(W),
-            float(scale), float(decay), ws.data_ptr(), ws.numel(), _call_stream(stream, q.device)))
+        def call(ws):
+            return lib.lf_decode_step_weights(
+                q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(),
+                weights.data_ptr(), new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(),
+                out.data_ptr(), next_slots.data_ptr(), topk, int(flags), B, Hq, Hkv, d, S, int(W),
+                float(scale), float(decay), ws.data_ptr(), ws.numel(),
+                _call_stream(stream, q.device))
+
+        n = 0 if workspace is not None else _weights_bytes(q.device.index, B, Hq, Hkv, d, S, topk)
+        ws = _workspace(workspace, n, q.device, stream)
+        status = call(ws)
+        if status == LF_ERR_INVALID_ARG and workspace is None:
+            # (Nothing was enqueued.) The plan's switches may have changed.
+            n = decode_weights_workspace(B, Hq, Hkv, d, S, topk)
+            if n > ws.numel():
+                status = call(_workspace(None, n, q.device, stream))
+            else:
+                status = call(ws)
+        _check(lib, status)
 
 
 def prompt_weights_workspace(T, B, Hq, Hkv, d, S, rows=0) -> int:

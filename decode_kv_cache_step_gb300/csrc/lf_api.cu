@@ -615,6 +615,11 @@ lf_status launch(const Launch& r, cudaStream_t stream) {
                                    stream);
     }
     if (e != cudaSuccess) return cuda_fail(e, "decode-step launch");
+    if (r.score == 2 && r.sp.topk > 1) {
+        prof_count(LF_KERNEL_SCORE);
+        e = lf::launch_select(r.g, r.sp, r.units, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "selection launch");
+    }
     if (r.sp.split) {
         prof_count(LF_KERNEL_SCORE);
         e = lf::launch_score(r.g, r.score, r.sp, r.units, stream);

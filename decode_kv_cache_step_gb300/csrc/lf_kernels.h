@@ -125,6 +125,8 @@ cudaError_t launch_decode_step_weights(int D, int G, int stages, bool cluster,
                                        const StepParams& p, int units, cudaStream_t stream,
                                        bool pdl);
 int max_active_clusters_weights(int D, int G, int stages, int csize);
+// The k lowest (key, slot) of every unit, behind such a step with topk > 1.
+cudaError_t launch_select(int G, const StepParams& p, int units, cudaStream_t stream);
 
 // How many clusters of csize CTAs (one unit each) of the cluster instance
 // (stages 2 or kDeepStages) can be resident at once on the current device;
@@ -225,6 +227,7 @@ struct PromptWeightsParams {
     // The plan (plan_prompt_weights), from the sizes above.
     bool by_sequence;        // statistics and tiles counted per sequence, not by packed row
     int items, pieces, stat_rows;
+    int share;
 };
 void plan_prompt_weights(PromptWeightsParams* p, int sms);
 // tmQ and tmK as in launch_attention.

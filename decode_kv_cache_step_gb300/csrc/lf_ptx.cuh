@@ -216,8 +216,19 @@ __device__ __forceinline__ void cluster_arrive_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
 
+// The same barrier with its default ordering: what was written before the arrival
+// is visible to the cluster after the wait.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive;" ::: "memory");
+}
+
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait;" ::: "memory");
+}
+
+// 4-byte store into the shared memory of a CTA of the cluster (a from dsmem_addr).
+__device__ __forceinline__ void st_cluster(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
 // Asynchronous 16-byte store into the shared memory of a CTA of the cluster

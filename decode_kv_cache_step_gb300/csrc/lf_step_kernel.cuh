@@ -35,7 +35,8 @@
 // unit's scratch lines from L2 without writing them back. The selection is
 // the lexicographic (I_j, j) argmin over slots with age >= W, or, for k > 1,
 // the k smallest by an 8-bit radix select on the score keys (then on the slot
-// index among equal scores) and a bitonic sort of the k winners; the periodic
+// index among equal scores) and a bitonic sort of the k winners (kWeights: by a
+// kernel of its own, lf_select_kernel); the periodic
 // k-at-once compression of the Fig. 3 caption. Candidates are compared by an
 // order-preserving key of log2 I_j, so slots whose scores lie far below
 // fp32's normal range (weights hundreds of nats under the unit's maximum)
@@ -1043,6 +1044,8 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
             if (slot >= 0 && (p.flags & kFlagMaskEvicted))
                 p.mask[static_cast<size_t>(u) * S + slot] = -1;
         }
+    } else if constexpr (kAdd) {
+        return;  // the selection kernel that follows takes the keys from here
     } else {
         if (ncand) atomicAdd(s_ncand, ncand);
         consumer_bar_sync();

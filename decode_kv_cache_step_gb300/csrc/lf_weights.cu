@@ -33,6 +33,7 @@ constexpr int kPanel = kRows * 128;       // bytes of 64 columns of a tile
 constexpr int kThreads = 192;             // four warps on the scores, loads, products
 constexpr int kRing = 2;                  // tiles of the streamed operand
 constexpr uint32_t kTmemCols = 2 * kRows;
+constexpr int kMaxShare = 8;              // CTAs that share a tile of keys, a cluster
 
 template <int D>
 struct WeightsSmem {
@@ -43,7 +44,8 @@ struct WeightsSmem {
     static constexpr int kBars = 1 + 2 * kRing + 5;
     static constexpr int kMiscOff = kBarOff + kBars * 8;
     static constexpr int kStatOff = (kMiscOff + 16 + 15) / 16 * 16;  // -r of two query tiles
-    static constexpr int kAlloc = kStatOff + 2 * kRows * 4 + 1024;
+    static constexpr int kTotalOff = kStatOff + 2 * kRows * 4;  // the cluster's sums
+    static constexpr int kAlloc = kTotalOff + kMaxShare * kRows * 4 + 1024;
 };
 
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, int z,
@@ -119,16 +121,19 @@ __device__ __forceinline__ bool rows_work(const PromptWeightsParams& p, int tok,
     return true;
 }
 
-// 128 keys and the rows that see one of them (columns pass).
-__device__ __forceinline__ bool keys_work(const PromptWeightsParams& p, Work* w) {
-    w->kvh = blockIdx.x % p.Hkv;
-    const int y = blockIdx.x / p.Hkv;
+// 128 keys and this CTA's share of the rows that see one of them (columns pass).
+__device__ __forceinline__ bool keys_work(const PromptWeightsParams& p, int tok, Work* w) {
+    const int x = blockIdx.x / p.share, rank = blockIdx.x % p.share;
+    w->kvh = x % p.Hkv;
+    const int y = x / p.Hkv;
     w->b = y % p.B;
     w->at = y / p.B * kRows;
     if (!seq_range(p.q_start, p.kv_len, w->b, p.T, p.S, true, &w->r)) return false;
     if (w->r.n == 0 || w->at >= w->r.kv) return false;
-    w->first = max(first_row(p, w->r), w->at - (w->r.kv - w->r.n));
-    w->end = w->r.n;
+    const int from = max(first_row(p, w->r), w->at - (w->r.kv - w->r.n));
+    const int tiles = (w->r.n - from + tok - 1) / tok;
+    w->first = from + static_cast<int>(static_cast<int64_t>(tiles) * rank / p.share) * tok;
+    w->end = min(w->r.n, from + static_cast<int>(static_cast<int64_t>(tiles) * (rank + 1) / p.share) * tok);
     return true;
 }
 
@@ -154,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t* drain = s_free + 2;
     volatile uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     float* stat = reinterpret_cast<float*>(smem + L::kStatOff);  // [2][kRows]
+    float* totals = reinterpret_cast<float*>(smem + L::kTotalOff);  // [share][kRows]
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tok = kRows >> gs;
     constexpr bool kKeysHeld = kForm == kColumnsPass;
     Work w;
-    if (kKeysHeld ? !keys_work(p, &w) : !rows_work(p, tok, kForm == kRowsPass, &w)) return;
+    if (kKeysHeld ? !keys_work(p, tok, &w) : !rows_work(p, tok, kForm == kRowsPass, &w)) return;
     if (kForm != kRowsPass && !p.by_sequence) {
         // The rows pass finds packed tiles by their order: unless q_start ascends
         // nothing is written.
@@ -176,6 +182,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (!__syncthreads_and(good)) return;
     }
+    // (Every CTA of a cluster has work, or none.)
+    const bool shared = kKeysHeld && p.share > 1;
+    if (shared) cluster_arrive_relaxed();
     const int step = kKeysHeld ? tok : kRows;
     const int tiles = w.end > w.first ? (w.end - w.first + step - 1) / step : 0;
 
@@ -199,6 +208,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     const int unit = w.b * p.Hkv + w.kvh;
+    const int past = w.r.kv - w.r.n;
+    float my_total = 0.f;  // of a shared tile
+    const auto store = [&](int j, float total) {
+        if (j >= w.r.kv) return;
+        float* dst = p.weights + static_cast<size_t>(unit) * p.S + j;
+        *dst = j < past ? *dst + total : total;
+    };
 
     if (warp == 4) {
         if (lane == 0 && tiles > 0) {
@@ -272,7 +288,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t ts = tmem + (static_cast<uint32_t>(warp) << 21);
         const float c1 = p.scale_log2;
         const uint64_t c2 = pack_f32x2(c1, c1);
-        const int past = w.r.kv - w.r.n;
         const auto take = [&](int n, uint32_t (&x)[128]) {
             const bool ok = __all_sync(0xffffffffu, mbar_wait(&s_full[n & 1], (n >> 1) & 1, p.wait_limit_ns));
             if (!ok) return false;
@@ -325,11 +340,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             float a, b;
             unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), a, b);
             return a + b;
-        };
-        const auto store = [&](int j, float total) {
-            if (j >= w.r.kv) return;
-            float* dst = p.weights + static_cast<size_t>(unit) * p.S + j;
-            *dst = j < past ? *dst + total : total;
         };
         if (kForm == kRowsPass) {
             // A thread owns the row of token w.at + tid / g, head tid % g.
@@ -392,7 +402,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 stat[((n + 1) & 1) * kRows + tid] = minus_r(then);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
-            store(j, total);
+            if (shared)
+                my_total = total;
+            else
+                store(j, total);
         } else {
             // Streamed keys; every tile's sums are final.
             stat[tid] = minus_r(joined(min(w.at + (tid >> gs), w.r.n - 1)));
@@ -409,6 +422,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (!ok && lane == 0) atomicOr(p.dev_err, LF_DEVERR_WAIT_TIMEOUT);
     }
+    if (shared) {
+        // The cluster's sums to its first CTA, added in the order of the rows.
+        cluster_wait();  // its CTAs have all started
+        if (tid < kRows) st_cluster(dsmem_addr(totals + cluster_ctarank() * kRows + tid, 0u), my_total);
+        cluster_arrive();
+        cluster_wait();
+        if (cluster_ctarank() == 0 && tid < kRows) {
+            float total = 0.f;
+            for (int k = 0; k < p.share; ++k) total += totals[k * kRows + tid];
+            store(w.at + tid, total);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -417,22 +442,31 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int D, int kForm>
 cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmK, const PromptWeightsParams& p,
-                        dim3 grid, cudaStream_t stream) {
+                        dim3 grid, int cluster, cudaStream_t stream) {
     const auto kernel = lf_prompt_weights_kernel<D, kForm>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          WeightsSmem<D>::kAlloc);
     if (e != cudaSuccess) return e;
     const char* env = std::getenv("LF_PDL");
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    int attrs = 0;
+    if (!(env && std::atoi(env) == 0)) {
+        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[attrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[attrs].id = cudaLaunchAttributeClusterDimension;
+        attr[attrs].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[attrs].val.clusterDim.y = 1;
+        attr[attrs++].val.clusterDim.z = 1;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = WeightsSmem<D>::kAlloc;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = (env && std::atoi(env) == 0) ? 0 : 1;
+    cfg.numAttrs = attrs;
     return cudaLaunchKernelEx(&cfg, kernel, tmQ, tmK, p);
 }
 
@@ -440,13 +474,11 @@ template <int D>
 cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const PromptWeightsParams& p,
                      cudaStream_t stream) {
     const dim3 rows(p.items * p.Hkv, p.pieces);
-    const cudaError_t e = launch_pass<D, kRowsPass>(tmQ, tmK, p, rows, stream);
+    const cudaError_t e = launch_pass<D, kRowsPass>(tmQ, tmK, p, rows, 1, stream);
     if (e != cudaSuccess) return e;
-    // No more rows in a sequence than a tile holds?
-    const int most = p.rows > 0 ? std::min(p.rows, p.T) : p.T;
-    if (most * (p.Hq / p.Hkv) <= kRows) return launch_pass<D, kFewRows>(tmQ, tmK, p, rows, stream);
+    if (p.share == 0) return launch_pass<D, kFewRows>(tmQ, tmK, p, rows, 1, stream);
     const int tiles = (p.S + kRows - 1) / kRows;
-    return launch_pass<D, kColumnsPass>(tmQ, tmK, p, dim3(tiles * p.B * p.Hkv), stream);
+    return launch_pass<D, kColumnsPass>(tmQ, tmK, p, dim3(tiles * p.B * p.Hkv * p.share), p.share, stream);
 }
 
 }  // namespace
@@ -462,6 +494,14 @@ void plan_prompt_weights(PromptWeightsParams* p, int sms) {
     const int64_t rows = p->rows > 0 ? std::min<int64_t>(p->T, static_cast<int64_t>(p->rows) * p->B) : p->T;
     const int64_t busy = std::max<int64_t>(1, (rows + tok - 1) / tok) * p->Hkv;
     const int64_t tiles = (p->S + kRows - 1) / kRows;
+    // The columns pass: no tiles of keys (share 0) where no sequence has more rows
+    // than a tile holds; else CTAs that share a tile's rows, so that the longest
+    // CTA is short beside the whole (six waves of two CTAs an SM).
+    const int64_t most = p->rows > 0 ? std::min(p->rows, p->T) : p->T;
+    p->share = most <= tok ? 0 : 1;
+    while (p->share > 0 && p->share < kMaxShare && p->share * tok * 2 < most &&
+           tiles * p->B * p->Hkv * p->share < 12 * sms)
+        p->share *= 2;
     p->pieces = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({tiles, 2 * sms / busy, 16})));
 }
 
