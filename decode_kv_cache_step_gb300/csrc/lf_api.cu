@@ -564,7 +564,7 @@ lf_status build_launch(const StepArgs& a, const Shape& s, char* base, uint32_t* 
     sp.wait_limit_ns = wait_limit_ns();
     sp.topk = a.score ? a.topk : 1;
     sp.flags = a.score ? a.flags : 0;
-    sp.split = (a.score && pl.split && sp.topk == 1) ? 1 : 0;
+    sp.split = (a.score && pl.split && (sp.topk == 1 || a.score == 2)) ? 1 : 0;
     sp.split_from = sp.split ? pl.split_from : 0;
     sp.pre_ml = a.pre_ml;
     sp.pre_o = a.pre_o;
@@ -615,15 +615,15 @@ lf_status launch(const Launch& r, cudaStream_t stream) {
                                    stream);
     }
     if (e != cudaSuccess) return cuda_fail(e, "decode-step launch");
-    if (r.score == 2 && r.sp.topk > 1) {
-        prof_count(LF_KERNEL_SCORE);
-        e = lf::launch_select(r.g, r.sp, r.units, stream);
-        if (e != cudaSuccess) return cuda_fail(e, "selection launch");
-    }
     if (r.sp.split) {
         prof_count(LF_KERNEL_SCORE);
         e = lf::launch_score(r.g, r.score, r.sp, r.units, stream);
         if (e != cudaSuccess) return cuda_fail(e, "scoring-kernel launch");
+    }
+    if (r.score == 2 && r.sp.topk > 1) {
+        prof_count(LF_KERNEL_SCORE);
+        e = lf::launch_select(r.g, r.sp, r.units, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "selection launch");
     }
     return LF_OK;
 }
@@ -950,6 +950,7 @@ lf_status weights_layout(const Shape& s, int topk, int dev, WeightsLayout* out) 
     const int units = s.B * s.Hkv;
     L.pl = plan_split(s.S, units, sm_count(dev), topk == 1, s.d, s.Hq / s.Hkv, 2);
     if (L.pl.stages == 3) L.pl.stages = 2;  // (LF_STAGES; there is no such instance)
+    if (topk > 1) plan_split_finish(&L.pl, s.S, units, sm_count(dev), true);
     L.step = scratch_layout(s, L.pl, 0);
     L.counters = lf::kCounterWordsPerUnit * static_cast<size_t>(units) * sizeof(uint32_t);
     L.scratch = align_up(L.counters, 256);

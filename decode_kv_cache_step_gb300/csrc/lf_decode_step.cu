@@ -135,7 +135,10 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
                 if (kAdd && live) weights[j] = L;
                 const bool cand = live ? (aa >= W && L == L) : fill_first;
                 const uint32_t key = live ? ordered_key(L) : 0u;
-                if (cand && j < S && key < bkey) {
+                if (kAdd && p.topk > 1) {
+                    // (For the selection kernel, in the slot's first term.)
+                    if (j < S) reinterpret_cast<uint32_t*>(p.stash)[(static_cast<size_t>(u) * S + j) * G] = cand ? key : 0xffffffffu;
+                } else if (cand && j < S && key < bkey) {
                     bkey = key;
                     bj = j;
                 }
@@ -174,6 +177,8 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
         }
         if (last) {
             p.ready[u] = 0u;  // every CTA of the unit has seen the flag
+        }
+        if (last && !(kAdd && p.topk > 1)) {
             const int slot = best ? static_cast<int>(static_cast<uint32_t>(~best)) : -1;
             p.next_slot[u] = slot;
             if (slot >= 0 && (p.flags & kFlagMaskEvicted))
@@ -183,7 +188,7 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
     // Every read of these chunks' score terms is done: drop the lines.
     const int cs = ct * kTile;
     for (int c = c0; c < c1; ++c)
-        if (s_live[c - c0])
+        if (s_live[c - c0] && !(kAdd && p.topk > 1))
             discard_range(stash + static_cast<size_t>(c) * cs * G,
                           static_cast<size_t>(min(S, (c + 1) * cs) - c * cs) * G * 4, tid,
                           kScoreThreads);

@@ -38,32 +38,49 @@ constexpr int kPackSlots = 64;  // slots of one (sequence, KV head) a CTA packs 
 // 8-bit integers X, Y, so where x / s is not halfway between two integers it is
 // at least 2^-10 away from that: a product with the rounded reciprocal (off by
 // 2^-20 at most), rounded to multiples of 2^-12, is on the right side, and a tie
-// is a tie again.
+// is a tie again. Both roundings are sums with a constant, the second of which
+// leaves the code plus 8 in the low bits, and a sum of those times powers of 16
+// is the word: packing is bound by memory, and a conversion per value is not.
+__device__ __forceinline__ float bf16_at(const uint32_t (&w)[4], int i) {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+}
+
 __device__ __forceinline__ uint32_t quantise8(const uint4 v, unsigned mask, __nv_bfloat16* scale) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;
+    uint32_t two = 0;  // the largest magnitudes of the halves
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    for (int i = 0; i < 4; ++i) two = __vimax3_u16x2(two, w[i] & 0x7fff7fffu, 0u);
+    uint32_t top = max(two & 0xffffu, two >> 16);
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) top = max(top, __shfl_xor_sync(mask, top, off));
     // A group with a value that is not finite stands for NaN.
     const float amax = __uint_as_float(top << 16);
     const __nv_bfloat16 s = top < 0x7f80u ? __float2bfloat16_rn(amax / 7.f) : __ushort_as_bfloat16(0x7fffu);
     *scale = s;
-    // Small groups times 2^64, so that the reciprocal is finite.
-    const float up = amax < 0x1p-60f ? 0x1p64f : 1.f;
-    const float sf = __bfloat162float(s) * up;
-    const bool some = sf > 0.f;  // neither 0 nor NaN
-    const float inv = some ? 1.f / sf : 0.f;
+    constexpr float kSnap = 0x1.8p11f;              // sums are multiples of 2^-12
+    constexpr float kWhole = 0x1.8p23f + 8 - kSnap;  // and then integers
     uint32_t codes = 0;
+    if (amax >= 0x1p-60f && top < 0x7f80u) {
+        const float inv = 1.f / __bfloat162float(s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-        float t = some ? x * up * inv : 0.f;
-        constexpr float kSnap = 0x1.8p11f;  // adds to a multiple of 2^-12
-        t = __fadd_rn(__fadd_rn(t, kSnap), -kSnap);
-        const int c = min(7, max(-7, __float2int_rn(t)));
-        codes |= static_cast<uint32_t>(c + 8) << (4 * i);
+        for (int i = 7; i >= 0; --i) {
+            const float t = __fadd_rn(__fmaf_rn(bf16_at(w, i), inv, kSnap), kWhole);
+            codes = codes * 16u + __float_as_uint(t);
+        }
+        // Less what else the eight sums hold.
+        codes -= 0x4b400000u * 0x11111111u;
+    } else {
+        // Small groups times 2^64, so that the reciprocal is finite.
+        const float sf = __bfloat162float(s) * 0x1p64f;
+        const bool some = sf > 0.f;  // neither 0 nor NaN
+        const float inv = some ? 1.f / sf : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float t = some ? bf16_at(w, i) * 0x1p64f * inv : 0.f;
+            t = __fadd_rn(__fadd_rn(t, kSnap), -kSnap);
+            const int c = min(7, max(-7, __float2int_rn(t)));
+            codes |= static_cast<uint32_t>(c + 8) << (4 * i);
+        }
     }
     return codes;
 }
@@ -122,18 +139,27 @@ __global__ void __launch_bounds__(kPackThreads) lf_kv4_pack_kernel(const Kv4Pack
         p.mask[static_cast<size_t>(u) * p.S + j0 + tid] = r.end - 1 - (j0 + tid);
     constexpr int kLanes = D / 8;
     constexpr int kRows = kPackThreads / kLanes;
+    constexpr int kBatch = kPackSlots / kRows;  // rows of a thread, all in flight
     const int i = tid % kLanes;
     const unsigned mask = 0xfu << (tid & 28);
-    const int last = min(j0 + kPackSlots, r.end);
-    for (int j = max(j0, r.first) + tid / kLanes; j < last; j += kRows) {
+    uint4 k[kBatch], v[kBatch];
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+        const int j = j0 + tid / kLanes + n * kRows;
+        if (j < r.first || j >= r.end) continue;
         const size_t src = (static_cast<size_t>(u) * p.P + j) * D;
+        k[n] = __ldcs(reinterpret_cast<const uint4*>(p.k + src) + i);
+        v[n] = __ldcs(reinterpret_cast<const uint4*>(p.v + src) + i);
+    }
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+        const int j = j0 + tid / kLanes + n * kRows;
+        if (j < r.first || j >= r.end) continue;
         const size_t dst = static_cast<size_t>(u) * p.S + j;
-        const uint4 k = __ldcs(reinterpret_cast<const uint4*>(p.k + src) + i);
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p.v + src) + i);
         __nv_bfloat16 s;
-        store_k8<D>(p.k4 + dst * (D / 2), i, quantise8(k, mask, &s));
+        store_k8<D>(p.k4 + dst * (D / 2), i, quantise8(k[n], mask, &s));
         if ((i & 3) == 0) p.k_scale[dst * (D / 32) + (i >> 2)] = s;
-        store_v8<D>(p.v4 + dst * (D / 2), i, quantise8(v, mask, &s));
+        store_v8<D>(p.v4 + dst * (D / 2), i, quantise8(v[n], mask, &s));
         if ((i & 3) == 0) p.v_scale[dst * (D / 32) + (i >> 2)] = s;
     }
 }
@@ -161,18 +187,29 @@ __global__ void __launch_bounds__(kPackThreads) lf_kv4_unpack_kernel(const Kv4Pa
     constexpr int kLanes = D / 8;
     constexpr int kRows = kPackThreads / kLanes;
     const int i = tid % kLanes;
-    const int last = min(j0 + kPackSlots, r.end);
-    for (int j = max(j0, r.first) + tid / kLanes; j < last; j += kRows) {
+    constexpr int kBatch = kPackSlots / kRows;
+    uint32_t k[kBatch], v[kBatch];
+    float ks[kBatch], vs[kBatch];
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+        const int j = j0 + tid / kLanes + n * kRows;
+        if (j < r.first || j >= r.end) continue;
         const size_t src = static_cast<size_t>(u) * p.S + j;
+        k[n] = load_k8<D>(p.k4 + src * (D / 2), i);
+        v[n] = load_v8<D>(p.v4 + src * (D / 2), i);
+        ks[n] = __bfloat162float(p.k_scale[src * (D / 32) + (i >> 2)]);
+        vs[n] = __bfloat162float(p.v_scale[src * (D / 32) + (i >> 2)]);
+    }
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+        const int j = j0 + tid / kLanes + n * kRows;
+        if (j < r.first || j >= r.end) continue;
         const size_t dst = (static_cast<size_t>(u) * p.P + j) * D;
-        const uint32_t k = load_k8<D>(p.k4 + src * (D / 2), i);
-        const uint32_t v = load_v8<D>(p.v4 + src * (D / 2), i);
-        const float ks = __bfloat162float(p.k_scale[src * (D / 32) + (i >> 2)]);
-        const float vs = __bfloat162float(p.v_scale[src * (D / 32) + (i >> 2)]);
-        __stcs(reinterpret_cast<uint4*>(p.k_out + dst) + i,
-               make_uint4(stand_for2(k, 0, ks), stand_for2(k, 2, ks), stand_for2(k, 4, ks), stand_for2(k, 6, ks)));
-        __stcs(reinterpret_cast<uint4*>(p.v_out + dst) + i,
-               make_uint4(stand_for2(v, 0, vs), stand_for2(v, 2, vs), stand_for2(v, 4, vs), stand_for2(v, 6, vs)));
+        const auto values = [](uint32_t c, float s) {
+            return make_uint4(stand_for2(c, 0, s), stand_for2(c, 2, s), stand_for2(c, 4, s), stand_for2(c, 6, s));
+        };
+        __stcs(reinterpret_cast<uint4*>(p.k_out + dst) + i, values(k[n], ks[n]));
+        __stcs(reinterpret_cast<uint4*>(p.v_out + dst) + i, values(v[n], vs[n]));
     }
 }
 
@@ -835,9 +872,11 @@ cudaError_t launch_kv4_d(int G, const Kv4Params& p, int units, int nchunk, cudaS
 
 Kv4Plan kv4_plan(int units, int S, int sms) {
     // Three CTAs are resident per SM; chunks of whole 128 slots (32 a warp).
+    // Few slots: one chunk, which needs no join (measured on a call of 8 units of
+    // 256 slots, two chunks and one: PLACEHOLDER us).
     const int steps = (S + 127) / 128;
     const int longest = kMaxChunkSlots / 128;
-    const int fill = std::max(1, 3 * sms / units);
+    const int fill = steps <= 4 ? 1 : std::max(1, 3 * sms / units);
     const int n = std::max((steps + longest - 1) / longest, std::min(steps, fill));
     const int per = (steps + n - 1) / n;
     return Kv4Plan{per * 128, (steps + per - 1) / per};
