@@ -227,7 +227,8 @@ struct PromptWeightsParams {
     // The plan (plan_prompt_weights), from the sizes above.
     bool by_sequence;        // statistics and tiles counted per sequence, not by packed row
     int items, pieces, stat_rows;
-    int share;
+    int piece_tiles;         // tiles of 128 keys of a piece
+    int share;               // CTAs that share tiles of keys; 0: rows are held in both passes
 };
 void plan_prompt_weights(PromptWeightsParams* p, int sms);
 // tmQ and tmK as in launch_attention.

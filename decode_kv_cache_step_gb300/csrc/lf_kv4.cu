@@ -55,13 +55,16 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 v, unsigned mask, __nv
     for (int off = 1; off < 4; off <<= 1) top = max(top, __shfl_xor_sync(mask, top, off));
     // A group with a value that is not finite stands for NaN.
     const float amax = __uint_as_float(top << 16);
-    const __nv_bfloat16 s = top < 0x7f80u ? __float2bfloat16_rn(amax / 7.f) : __ushort_as_bfloat16(0x7fffu);
+    // (The product with the rounded 1 / 7 rounds like the quotient: that is at
+    // least 2^-12 of itself away from halfway between two bf16, as 8 bits over 7.)
+    const __nv_bfloat16 s =
+        top < 0x7f80u ? __float2bfloat16_rn(__fmul_rn(amax, 1.f / 7.f)) : __ushort_as_bfloat16(0x7fffu);
     *scale = s;
     constexpr float kSnap = 0x1.8p11f;              // sums are multiples of 2^-12
     constexpr float kWhole = 0x1.8p23f + 8 - kSnap;  // and then integers
     uint32_t codes = 0;
     if (amax >= 0x1p-60f && top < 0x7f80u) {
-        const float inv = 1.f / __bfloat162float(s);
+        const float inv = __frcp_rn(__bfloat162float(s));
 #pragma unroll
         for (int i = 7; i >= 0; --i) {
             const float t = __fadd_rn(__fmaf_rn(bf16_at(w, i), inv, kSnap), kWhole);
@@ -142,33 +145,48 @@ __global__ void __launch_bounds__(kPackThreads) lf_kv4_pack_kernel(const Kv4Pack
     constexpr int kBatch = kPackSlots / kRows;  // rows of a thread, all in flight
     const int i = tid % kLanes;
     const unsigned mask = 0xfu << (tid & 28);
+    // The thread's first row; the others follow kRows apart.
+    const int jt = j0 + tid / kLanes;
+    const size_t src = (static_cast<size_t>(u) * p.P + jt) * D + 8 * i;
+    const size_t dst = static_cast<size_t>(u) * p.S + jt;
+    const auto inside = [&](int n) { return jt + n * kRows >= r.first && jt + n * kRows < r.end; };
     uint4 k[kBatch], v[kBatch];
 #pragma unroll
     for (int n = 0; n < kBatch; ++n) {
-        const int j = j0 + tid / kLanes + n * kRows;
-        if (j < r.first || j >= r.end) continue;
-        const size_t src = (static_cast<size_t>(u) * p.P + j) * D;
-        k[n] = __ldcs(reinterpret_cast<const uint4*>(p.k + src) + i);
-        v[n] = __ldcs(reinterpret_cast<const uint4*>(p.v + src) + i);
+        if (!inside(n)) continue;
+        k[n] = __ldcs(reinterpret_cast<const uint4*>(p.k + src + n * kRows * D));
+        v[n] = __ldcs(reinterpret_cast<const uint4*>(p.v + src + n * kRows * D));
     }
+    uint8_t* const k4 = p.k4 + dst * (D / 2);
+    uint8_t* const v4 = p.v4 + dst * (D / 2);
+    __nv_bfloat16* const k_scale = p.k_scale + dst * (D / 32) + (i >> 2);
+    __nv_bfloat16* const v_scale = p.v_scale + dst * (D / 32) + (i >> 2);
 #pragma unroll
     for (int n = 0; n < kBatch; ++n) {
-        const int j = j0 + tid / kLanes + n * kRows;
-        if (j < r.first || j >= r.end) continue;
-        const size_t dst = static_cast<size_t>(u) * p.S + j;
+        if (!inside(n)) continue;
         __nv_bfloat16 s;
-        store_k8<D>(p.k4 + dst * (D / 2), i, quantise8(k[n], mask, &s));
-        if ((i & 3) == 0) p.k_scale[dst * (D / 32) + (i >> 2)] = s;
-        store_v8<D>(p.v4 + dst * (D / 2), i, quantise8(v[n], mask, &s));
-        if ((i & 3) == 0) p.v_scale[dst * (D / 32) + (i >> 2)] = s;
+        store_k8<D>(k4 + n * kRows * (D / 2), i, quantise8(k[n], mask, &s));
+        if ((i & 3) == 0) k_scale[n * kRows * (D / 32)] = s;
+        store_v8<D>(v4 + n * kRows * (D / 2), i, quantise8(v[n], mask, &s));
+        if ((i & 3) == 0) v_scale[n * kRows * (D / 32)] = s;
     }
 }
 
-// Two codes (plus 8) at bits 4 i and 4 i + 4 of a word times a scale, as bf16.
-__device__ __forceinline__ uint32_t stand_for2(uint32_t codes, int i, float s) {
-    const float x = static_cast<float>(static_cast<int>((codes >> (4 * i)) & 15u) - 8) * s;
-    const float y = static_cast<float>(static_cast<int>((codes >> (4 * i + 4)) & 15u) - 8) * s;
-    return pack_bf16x2(x, y);
+// The values of 8 codes (plus 8), two at a time: 0x4300 | c is the bf16 128 + c, so
+// a difference gives the code, exactly, and the product with the scale is rounded
+// once. Codes i and i + 4 share a register.
+__device__ __forceinline__ uint4 values8(uint32_t codes, __nv_bfloat16 scale) {
+    const __nv_bfloat162 bias = __halves2bfloat162(__ushort_as_bfloat16(0x4308u), __ushort_as_bfloat16(0x4308u));
+    const __nv_bfloat162 s2 = __halves2bfloat162(scale, scale);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = ((codes >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+        const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), bias), s2);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return make_uint4(__byte_perm(w[0], w[1], 0x5410u), __byte_perm(w[2], w[3], 0x5410u),
+                      __byte_perm(w[0], w[1], 0x7632u), __byte_perm(w[2], w[3], 0x7632u));
 }
 
 template <int D>
@@ -188,28 +206,29 @@ __global__ void __launch_bounds__(kPackThreads) lf_kv4_unpack_kernel(const Kv4Pa
     constexpr int kRows = kPackThreads / kLanes;
     const int i = tid % kLanes;
     constexpr int kBatch = kPackSlots / kRows;
+    const int jt = j0 + tid / kLanes;
+    const size_t src = static_cast<size_t>(u) * p.S + jt;
+    const size_t dst = (static_cast<size_t>(u) * p.P + jt) * D + 8 * i;
+    const auto inside = [&](int n) { return jt + n * kRows >= r.first && jt + n * kRows < r.end; };
+    const uint8_t* const k4 = p.k4 + src * (D / 2);
+    const uint8_t* const v4 = p.v4 + src * (D / 2);
+    const __nv_bfloat16* const k_scale = p.k_scale + src * (D / 32) + (i >> 2);
+    const __nv_bfloat16* const v_scale = p.v_scale + src * (D / 32) + (i >> 2);
     uint32_t k[kBatch], v[kBatch];
-    float ks[kBatch], vs[kBatch];
+    __nv_bfloat16 ks[kBatch], vs[kBatch];
 #pragma unroll
     for (int n = 0; n < kBatch; ++n) {
-        const int j = j0 + tid / kLanes + n * kRows;
-        if (j < r.first || j >= r.end) continue;
-        const size_t src = static_cast<size_t>(u) * p.S + j;
-        k[n] = load_k8<D>(p.k4 + src * (D / 2), i);
-        v[n] = load_v8<D>(p.v4 + src * (D / 2), i);
-        ks[n] = __bfloat162float(p.k_scale[src * (D / 32) + (i >> 2)]);
-        vs[n] = __bfloat162float(p.v_scale[src * (D / 32) + (i >> 2)]);
+        if (!inside(n)) continue;
+        k[n] = load_k8<D>(k4 + n * kRows * (D / 2), i);
+        v[n] = load_v8<D>(v4 + n * kRows * (D / 2), i);
+        ks[n] = k_scale[n * kRows * (D / 32)];
+        vs[n] = v_scale[n * kRows * (D / 32)];
     }
 #pragma unroll
     for (int n = 0; n < kBatch; ++n) {
-        const int j = j0 + tid / kLanes + n * kRows;
-        if (j < r.first || j >= r.end) continue;
-        const size_t dst = (static_cast<size_t>(u) * p.P + j) * D;
-        const auto values = [](uint32_t c, float s) {
-            return make_uint4(stand_for2(c, 0, s), stand_for2(c, 2, s), stand_for2(c, 4, s), stand_for2(c, 6, s));
-        };
-        __stcs(reinterpret_cast<uint4*>(p.k_out + dst) + i, values(k[n], ks[n]));
-        __stcs(reinterpret_cast<uint4*>(p.v_out + dst) + i, values(v[n], vs[n]));
+        if (!inside(n)) continue;
+        __stcs(reinterpret_cast<uint4*>(p.k_out + dst + n * kRows * D), values8(k[n], ks[n]));
+        __stcs(reinterpret_cast<uint4*>(p.v_out + dst + n * kRows * D), values8(v[n], vs[n]));
     }
 }
 
