@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -197,6 +199,41 @@ def _need(t: torch.Tensor, name: str, dtype, shape, cuda: bool):
         raise ValueError(f"{name}: must be a CUDA tensor")
     if not cuda and t.is_cuda:
         raise ValueError(f"{name}: must be a host tensor")
+
+
+def _load_check():
+    """lib/_lf_check.so's pointers(), None where it was not built or does not load."""
+    if not os.path.exists(_build.CHECK_PATH):
+        return None
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_lf_check", _build.CHECK_PATH)
+        spec = importlib.util.spec_from_loader("_lf_check", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        return module.pointers
+    except ImportError:  # built for another torch
+        return None
+
+
+_fast_pointers = _load_check()
+
+
+def _pointers(*args):
+    """Data pointers of tensors (None for None), given as tensor, name, dtype, shape
+    each: contiguous CUDA tensors on one device, or an error that names the fault."""
+    if _fast_pointers is not None:
+        got = _fast_pointers(*args)
+        if got is not None:
+            return got
+    each = [args[i:i + 4] for i in range(0, len(args), 4)]
+    for t, name, dtype, shape in each:
+        if t is not None:
+            _need(t, name, dtype, shape, True)
+    there = [t for t, _, _, _ in each if t is not None]
+    for t in there:
+        if t.device != there[0].device:
+            raise ValueError(f"tensors on {there[0].device} and {t.device}: all must be on one device")
+    return tuple(None if t is None else t.data_ptr() for t, _, _, _ in each)
 
 
 def _shapes(q, k_cache):
@@ -409,6 +446,8 @@ def _on_device(device, *tensors):
 
 # The current stream's handle without a Stream object, where torch offers it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
+                     torch.cuda.is_current_stream_capturing)
 
 
 def _call_stream(stream, device):
@@ -434,7 +473,7 @@ def _workspace(workspace, nbytes, device, stream):
             raise ValueError(f"workspace: must be a contiguous tensor on {device}")
         return workspace
     if stream is None:
-        if _raw_stream is None or torch.cuda.is_current_stream_capturing():
+        if _raw_stream is None or _capturing():
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
         key = (device.index, _raw_stream(device.index))
         held = _held.__dict__
@@ -454,33 +493,44 @@ def _ptr(t):
 
 
 def _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv):
+    T, Hq, d = _rope_shape(qkv, q_weight, k_weight, inv_freq, q_out)
+    bf = torch.bfloat16
+    _need(q_out, "q_out", bf, (T, Hq, d), True)
+    if q_weight is not None:
+        _need(q_weight, "q_weight", bf, (d,), True)
+        _need(k_weight, "k_weight", bf, (d,), True)
+    _need(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), True)
+    return T, Hq, d, 2 * inv_freq.numel(), _qkv_stride(qkv, T, Hq, Hkv, d)
+
+
+def _rope_shape(qkv, q_weight, k_weight, inv_freq, q_out):
     if not isinstance(qkv, torch.Tensor) or not isinstance(q_out, torch.Tensor):
         raise TypeError("qkv and q_out: expected torch.Tensors")
     if q_out.dim() != 3 or qkv.dim() != 3:
         raise ValueError("qkv must be [T,Hq+2*Hkv,d] and q_out [T,Hq,d]")
-    T, Hq, d = q_out.shape
-    bf = torch.bfloat16
-    _need(q_out, "q_out", bf, (T, Hq, d), True)
-    if qkv.dtype != bf:
-        raise TypeError(f"qkv: dtype {qkv.dtype}, expected {bf}")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight must both be given or both be None")
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a [rot/2] tensor")
+    return q_out.shape
+
+
+def _qkv_stride(qkv, T, Hq, Hkv, d):
+    """Elements between the rows of qkv, which may be strided."""
+    if qkv.dtype != torch.bfloat16:
+        raise TypeError(f"qkv: dtype {qkv.dtype}, expected {torch.bfloat16}")
     if tuple(qkv.shape) != (T, Hq + 2 * Hkv, d):
         raise ValueError(f"qkv: shape {tuple(qkv.shape)}, expected {(T, Hq + 2 * Hkv, d)}")
     if not qkv.is_cuda:
         raise ValueError("qkv: must be a CUDA tensor")
-    if qkv.stride(2) != 1 or qkv.stride(1) != d:
+    stride, head, one = qkv.stride()
+    if one != 1 or head != d:
         raise ValueError("qkv: a row's heads must be contiguous")
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight must both be given or both be None")
-    if q_weight is not None:
-        _need(q_weight, "q_weight", bf, (d,), True)
-        _need(k_weight, "k_weight", bf, (d,), True)
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be a [rot/2] tensor")
-    _need(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), True)
-    stride = qkv.stride(0) if T > 1 else max(int(qkv.stride(0)), (Hq + 2 * Hkv) * d)
-    if T == 1 and stride % 8:
-        stride = (Hq + 2 * Hkv) * d  # a single row has no stride to speak of
-    return T, Hq, d, 2 * inv_freq.numel(), stride
+    if T == 1:
+        stride = max(int(stride), (Hq + 2 * Hkv) * d)
+        if stride % 8:
+            stride = (Hq + 2 * Hkv) * d  # a single row has no stride to speak of
+    return stride
 
 
 def qk_norm_rope(qkv, q_weight, k_weight, inv_freq, positions, q_out, k_out, v_out, eps=1e-6,
@@ -532,11 +582,10 @@ def prefill_append(qkv, q_weight, k_weight, inv_freq, q_start, kv_len, q_out, k_
             int(bool(interleaved)), float(eps), _call_stream(stream, qkv.device)))
 
 
-def _check_axes(positions, pair_axis, T, rot):
+def _check_axes(positions, pair_axis, rot):
     """(axes, the pairs' axes as bytes)."""
     if not isinstance(positions, torch.Tensor) or positions.dim() != 2:
         raise ValueError("positions must be [axes,T]")
-    _need(positions, "positions", torch.int32, (positions.shape[0], T), True)
     if isinstance(pair_axis, int) or isinstance(pair_axis, torch.Tensor) and pair_axis.is_cuda:
         raise ValueError("pair_axis: expected rot/2 axes on the host")
     try:
@@ -545,7 +594,7 @@ def _check_axes(positions, pair_axis, T, rot):
         raise ValueError(f"pair_axis: expected rot/2 axes, {e}") from None
     if len(pairs) != rot // 2:
         raise ValueError(f"pair_axis: {len(pairs)} entries, expected {rot // 2}")
-    return int(positions.shape[0]), pairs
+    return positions.shape[0], pairs
 
 
 def qk_norm_rope_axes(qkv, q_weight, k_weight, inv_freq, positions, pair_axis, q_out, k_out, v_out,
@@ -553,46 +602,50 @@ def qk_norm_rope_axes(qkv, q_weight, k_weight, inv_freq, positions, pair_axis, q
     """lf_qk_norm_rope_axes: qk_norm_rope with a position on each of several axes,
     positions [axes,T] int32. pair_axis: the axis of each rotated pair, rot/2
     integers on the host (a list, bytes or CPU tensor)."""
-    lib = load_library()
+    lib = _lib or load_library()
     if not isinstance(k_out, torch.Tensor) or k_out.dim() != 3:
         raise ValueError("k_out must be [T,Hkv,d]")
-    Hkv = int(k_out.shape[1])
-    T, Hq, d, rot, stride = _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv)
-    axes, pairs = _check_axes(positions, pair_axis, T, rot)
+    Hkv = k_out.shape[1]
+    T, Hq, d = _rope_shape(qkv, q_weight, k_weight, inv_freq, q_out)
+    half = inv_freq.shape[0]
+    axes, pairs = _check_axes(positions, pair_axis, 2 * half)
     bf = torch.bfloat16
-    _need(k_out, "k_out", bf, (T, Hkv, d), True)
-    _need(v_out, "v_out", bf, (T, Hkv, d), True)
-    with _on_device(qkv.device, q_weight, k_weight, inv_freq, positions, q_out, k_out, v_out):
+    qo, ko, vo, pos, freq, wq, wk = _pointers(
+        q_out, "q_out", bf, (T, Hq, d), k_out, "k_out", bf, (T, Hkv, d), v_out, "v_out", bf, (T, Hkv, d),
+        positions, "positions", torch.int32, (axes, T), inv_freq, "inv_freq", torch.float32, (half,),
+        q_weight, "q_weight", bf, (d,), k_weight, "k_weight", bf, (d,))
+    stride = _qkv_stride(qkv, T, Hq, Hkv, d)
+    device = qkv.device
+    with _on_device(device, q_out):
         _check(lib, lib.lf_qk_norm_rope_axes(
-            qkv.data_ptr(), stride, _ptr(q_weight), _ptr(k_weight), inv_freq.data_ptr(),
-            positions.data_ptr(), pairs, axes, q_out.data_ptr(), k_out.data_ptr(),
-            v_out.data_ptr(), T, Hq, Hkv, d, rot, int(bool(interleaved)), float(eps),
-            _call_stream(stream, qkv.device)))
+            qkv.data_ptr(), stride, wq, wk, freq, pos, pairs, axes, qo, ko, vo, T, Hq, Hkv, d, 2 * half,
+            int(bool(interleaved)), float(eps), _call_stream(stream, device)))
 
 
 def prefill_append_axes(qkv, q_weight, k_weight, inv_freq, q_start, kv_len, positions, pair_axis,
                         q_out, k_cache, v_cache, mask, eps=1e-6, interleaved=False, stream=None):
     """lf_prefill_append_axes: prefill_append with the rotation's positions given per
     row and axis, positions [axes,T] int32 (slots still follow q_start and kv_len)."""
-    lib = load_library()
+    lib = _lib or load_library()
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [B,Hkv,S,d]")
     B, Hkv, S, _ = k_cache.shape
-    T, Hq, d, rot, stride = _check_qkv(qkv, q_weight, k_weight, inv_freq, q_out, Hkv)
-    axes, pairs = _check_axes(positions, pair_axis, T, rot)
+    T, Hq, d = _rope_shape(qkv, q_weight, k_weight, inv_freq, q_out)
+    half = inv_freq.shape[0]
+    axes, pairs = _check_axes(positions, pair_axis, 2 * half)
     bf, i32 = torch.bfloat16, torch.int32
-    _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
-    _need(v_cache, "v_cache", bf, (B, Hkv, S, d), True)
-    _need(mask, "mask", i32, (B, Hkv, S), True)
-    _need(q_start, "q_start", i32, (B + 1,), True)
-    _need(kv_len, "kv_len", i32, (B,), True)
-    with _on_device(qkv.device, q_weight, k_weight, inv_freq, q_start, kv_len, positions, q_out,
-                    k_cache, v_cache, mask):
+    qo, kc, vc, m, qs, kl, pos, freq, wq, wk = _pointers(
+        q_out, "q_out", bf, (T, Hq, d), k_cache, "k_cache", bf, (B, Hkv, S, d),
+        v_cache, "v_cache", bf, (B, Hkv, S, d), mask, "mask", i32, (B, Hkv, S),
+        q_start, "q_start", i32, (B + 1,), kv_len, "kv_len", i32, (B,),
+        positions, "positions", i32, (axes, T), inv_freq, "inv_freq", torch.float32, (half,),
+        q_weight, "q_weight", bf, (d,), k_weight, "k_weight", bf, (d,))
+    stride = _qkv_stride(qkv, T, Hq, Hkv, d)
+    device = qkv.device
+    with _on_device(device, q_out):
         _check(lib, lib.lf_prefill_append_axes(
-            qkv.data_ptr(), stride, _ptr(q_weight), _ptr(k_weight), inv_freq.data_ptr(),
-            q_start.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), pairs, axes,
-            q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(), T, B, Hq,
-            Hkv, d, S, rot, int(bool(interleaved)), float(eps), _call_stream(stream, qkv.device)))
+            qkv.data_ptr(), stride, wq, wk, freq, qs, kl, pos, pairs, axes, qo, kc, vc, m, T, B, Hq,
+            Hkv, d, S, 2 * half, int(bool(interleaved)), float(eps), _call_stream(stream, device)))
 
 
 def window_attention_workspace(T, B, Hq, Hkv, d, S, window=0, sinks=0) -> int:
@@ -744,31 +797,33 @@ def decode_step_weights(q, k_cache, v_cache, mask, weights, new_k, new_v, write_
     """lf_decode_step_weights: the decode step that adds the token's attention weights
     to weights [B,Hkv,S] fp32 (decay * old + new) and returns the slots with the
     least. next_slots [B,Hkv] (k None: the argmin) or [B,Hkv,k]."""
-    lib = load_library()
-    B, Hq, Hkv, d, S = _check_step(q, k_cache, v_cache, mask, new_k, new_v, write_slot, out,
-                                   next_slots, k=k)
-    _need(weights, "weights", torch.float32, (B, Hkv, S), True)
+    lib = _lib or load_library()
+    B, Hq, Hkv, d, S = _shapes(q, k_cache)
+    bf, i32 = torch.bfloat16, torch.int32
     topk = 1 if k is None else int(k)
-    with _on_device(q.device, k_cache, v_cache, mask, weights, new_k, new_v, write_slot, out,
-                    next_slots):
-        def call(ws):
-            return lib.lf_decode_step_weights(
-                q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), mask.data_ptr(),
-                weights.data_ptr(), new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(),
-                out.data_ptr(), next_slots.data_ptr(), topk, int(flags), B, Hq, Hkv, d, S, int(W),
-                float(scale), float(decay), ws.data_ptr(), ws.numel(),
-                _call_stream(stream, q.device))
+    ptrs = _pointers(
+        q, "q", bf, (B, Hq, d), k_cache, "k_cache", bf, (B, Hkv, S, d),
+        v_cache, "v_cache", bf, (B, Hkv, S, d), mask, "mask", i32, (B, Hkv, S),
+        weights, "weights", torch.float32, (B, Hkv, S), new_k, "new_k", bf, (B, Hkv, d),
+        new_v, "new_v", bf, (B, Hkv, d), write_slot, "write_slot", i32, (B, Hkv),
+        out, "out", bf, (B, Hq, d),
+        next_slots, "next_slots", i32, (B, Hkv) if k is None else (B, Hkv, topk))
+    device = q.device
+    with _on_device(device, q):
+        handle = _call_stream(stream, device)
 
-        n = 0 if workspace is not None else _weights_bytes(q.device.index, B, Hq, Hkv, d, S, topk)
-        ws = _workspace(workspace, n, q.device, stream)
+        def call(ws):
+            return lib.lf_decode_step_weights(*ptrs, topk, int(flags), B, Hq, Hkv, d, S, int(W),
+                                              float(scale), float(decay), ws.data_ptr(), ws.numel(),
+                                              handle)
+
+        n = 0 if workspace is not None else _weights_bytes(device.index, B, Hq, Hkv, d, S, topk)
+        ws = _workspace(workspace, n, device, stream)
         status = call(ws)
         if status == LF_ERR_INVALID_ARG and workspace is None:
             # (Nothing was enqueued.) The plan's switches may have changed.
             n = decode_weights_workspace(B, Hq, Hkv, d, S, topk)
-            if n > ws.numel():
-                status = call(_workspace(None, n, q.device, stream))
-            else:
-                status = call(ws)
+            status = call(_workspace(None, n, device, stream) if n > ws.numel() else ws)
         _check(lib, status)
 
 
@@ -790,81 +845,76 @@ def prompt_weights(q, k_cache, q_start, kv_len, weights, scale, rows=0, workspac
     """lf_prompt_weights: the causal attention weights that the last `rows` rows (0:
     all) of each sequence give its keys, into weights [B,Hkv,S] fp32 (set for this
     call's tokens, added for earlier ones): decode_step_weights' start."""
-    lib = load_library()
+    lib = _lib or load_library()
     if not isinstance(q, torch.Tensor) or not isinstance(k_cache, torch.Tensor):
         raise TypeError("q and k_cache: expected torch.Tensors")
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [T,Hq,d] and k_cache [B,Hkv,S,d]")
     T, Hq, d = q.shape
     B, Hkv, S, _ = k_cache.shape
-    bf, i32 = torch.bfloat16, torch.int32
-    _need(q, "q", bf, (T, Hq, d), True)
-    _need(k_cache, "k_cache", bf, (B, Hkv, S, d), True)
-    _need(q_start, "q_start", i32, (B + 1,), True)
-    _need(kv_len, "kv_len", i32, (B,), True)
-    _need(weights, "weights", torch.float32, (B, Hkv, S), True)
-    with _on_device(q.device, k_cache, q_start, kv_len, weights):
-        ws = _workspace(workspace, 0 if workspace is not None else
-                        _prompt_bytes(q.device.index, T, B, Hq, Hkv, d, S, int(rows)), q.device, stream)
-        _check(lib, lib.lf_prompt_weights(
-            q.data_ptr(), k_cache.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
-            weights.data_ptr(), T, B, Hq, Hkv, d, S, int(rows), float(scale), ws.data_ptr(),
-            ws.numel(), _call_stream(stream, q.device)))
+    i32 = torch.int32
+    ptrs = _pointers(
+        q, "q", torch.bfloat16, (T, Hq, d), k_cache, "k_cache", torch.bfloat16, (B, Hkv, S, d),
+        q_start, "q_start", i32, (B + 1,), kv_len, "kv_len", i32, (B,),
+        weights, "weights", torch.float32, (B, Hkv, S))
+    device = q.device
+    with _on_device(device, q):
+        n = 0 if workspace is not None else _prompt_bytes(device.index, T, B, Hq, Hkv, d, S, int(rows))
+        ws = _workspace(workspace, n, device, stream)
+        _check(lib, lib.lf_prompt_weights(*ptrs, T, B, Hq, Hkv, d, S, int(rows), float(scale),
+                                          ws.data_ptr(), ws.numel(), _call_stream(stream, device)))
 
 
-def _check_kv4(k4, k_scale, v4, v_scale):
-    """(B, Hkv, S, d) of a 4-bit cache's arrays."""
+def _kv4_shape(k4):
+    """(B, Hkv, S, d) of a 4-bit cache's keys."""
     if not isinstance(k4, torch.Tensor) or k4.dim() != 4:
         raise ValueError("k4 must be [B,Hkv,S,d/2]")
-    B, Hkv, S, half = (int(x) for x in k4.shape)
-    d = 2 * half
-    u8, bf = torch.uint8, torch.bfloat16
-    _need(k4, "k4", u8, (B, Hkv, S, half), True)
-    _need(v4, "v4", u8, (B, Hkv, S, half), True)
-    _need(k_scale, "k_scale", bf, (B, Hkv, S, d // 32), True)
-    _need(v_scale, "v_scale", bf, (B, Hkv, S, d // 32), True)
-    return B, Hkv, S, d
+    B, Hkv, S, half = k4.shape
+    return B, Hkv, S, 2 * half
 
 
-def _check_kv4_slots(k_cache, v_cache, kv_from, kv_len, B, Hkv, d):
+def _kv4_slots(k4, k_scale, v4, v_scale, kv_from, kv_len, k_cache, v_cache, mask):
+    """The sizes and pointers of a call that packs or unpacks (mask None)."""
+    B, Hkv, S, d = _kv4_shape(k4)
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [B,Hkv,P,d]")
-    P = int(k_cache.shape[2])
-    bf, i32 = torch.bfloat16, torch.int32
-    _need(k_cache, "k_cache", bf, (B, Hkv, P, d), True)
-    _need(v_cache, "v_cache", bf, (B, Hkv, P, d), True)
-    _need(kv_len, "kv_len", i32, (B,), True)
-    if kv_from is not None:
-        _need(kv_from, "kv_from", i32, (B,), True)
-    return P
+    P = k_cache.shape[2]
+    bf, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    return (B, Hkv, d, P, S), _pointers(
+        k4, "k4", u8, (B, Hkv, S, d // 2), k_scale, "k_scale", bf, (B, Hkv, S, d // 32),
+        v4, "v4", u8, (B, Hkv, S, d // 2), v_scale, "v_scale", bf, (B, Hkv, S, d // 32),
+        kv_from, "kv_from", i32, (B,), kv_len, "kv_len", i32, (B,),
+        k_cache, "k_cache", bf, (B, Hkv, P, d), v_cache, "v_cache", bf, (B, Hkv, P, d),
+        mask, "mask", i32, (B, Hkv, S))
 
 
 def kv4_pack(k_cache, v_cache, kv_from, kv_len, k4, k_scale, v4, v_scale, mask, stream=None):
     """lf_kv4_pack: slots kv_from[b]..kv_len[b] (kv_from None: from 0) of bf16 caches
     [B,Hkv,P,d] into a 4-bit cache: k4, v4 uint8 [B,Hkv,S,d/2], k_scale, v_scale
     bf16 [B,Hkv,S,d/32]; mask [B,Hkv,S] gets the ages of an in-order cache."""
-    lib = load_library()
-    B, Hkv, S, d = _check_kv4(k4, k_scale, v4, v_scale)
-    P = _check_kv4_slots(k_cache, v_cache, kv_from, kv_len, B, Hkv, d)
-    _need(mask, "mask", torch.int32, (B, Hkv, S), True)
-    with _on_device(k4.device, k_scale, v4, v_scale, k_cache, v_cache, kv_from, kv_len, mask):
-        _check(lib, lib.lf_kv4_pack(
-            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_from), kv_len.data_ptr(),
-            k4.data_ptr(), k_scale.data_ptr(), v4.data_ptr(), v_scale.data_ptr(), mask.data_ptr(),
-            B, Hkv, d, P, S, _call_stream(stream, k4.device)))
+    lib = _lib or load_library()
+    if kv_len is None or mask is None:
+        raise TypeError("kv_len and mask: expected torch.Tensors")
+    sizes, (c, cs, w, wsc, first, last, kc, vc, m) = _kv4_slots(
+        k4, k_scale, v4, v_scale, kv_from, kv_len, k_cache, v_cache, mask)
+    device = k4.device
+    with _on_device(device, k4):
+        _check(lib, lib.lf_kv4_pack(kc, vc, first, last, c, cs, w, wsc, m, *sizes,
+                                    _call_stream(stream, device)))
 
 
 def kv4_unpack(k4, k_scale, v4, v_scale, kv_from, kv_len, k_cache, v_cache, stream=None):
     """lf_kv4_unpack: the values of slots kv_from[b]..kv_len[b] of a 4-bit cache back
     into bf16 caches [B,Hkv,P,d]."""
-    lib = load_library()
-    B, Hkv, S, d = _check_kv4(k4, k_scale, v4, v_scale)
-    P = _check_kv4_slots(k_cache, v_cache, kv_from, kv_len, B, Hkv, d)
-    with _on_device(k4.device, k_scale, v4, v_scale, k_cache, v_cache, kv_from, kv_len):
-        _check(lib, lib.lf_kv4_unpack(
-            k4.data_ptr(), k_scale.data_ptr(), v4.data_ptr(), v_scale.data_ptr(), _ptr(kv_from),
-            kv_len.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, Hkv, d, P, S,
-            _call_stream(stream, k4.device)))
+    lib = _lib or load_library()
+    if kv_len is None:
+        raise TypeError("kv_len: expected a torch.Tensor")
+    sizes, (c, cs, w, wsc, first, last, kc, vc, _) = _kv4_slots(
+        k4, k_scale, v4, v_scale, kv_from, kv_len, k_cache, v_cache, None)
+    device = k4.device
+    with _on_device(device, k4):
+        _check(lib, lib.lf_kv4_unpack(c, cs, w, wsc, first, last, kc, vc, *sizes,
+                                      _call_stream(stream, device)))
 
 
 def decode_kv4_workspace(B, Hq, Hkv, d, S) -> int:
@@ -883,26 +933,25 @@ def decode_attention_kv4(q, k4, k_scale, v4, v_scale, mask, new_k, new_v, write_
                          workspace=None, stream=None):
     """lf_decode_attention_kv4: decode_attention over a 4-bit cache (the token's row
     is put into 4 bits in write_slot and attended as the values it then stands for)."""
-    lib = load_library()
-    B, Hkv, S, d = _check_kv4(k4, k_scale, v4, v_scale)
+    lib = _lib or load_library()
+    B, Hkv, S, d = _kv4_shape(k4)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [B,Hq,d]")
-    Hq = int(q.shape[1])
-    bf, i32 = torch.bfloat16, torch.int32
-    _need(q, "q", bf, (B, Hq, d), True)
-    _need(mask, "mask", i32, (B, Hkv, S), True)
-    _need(new_k, "new_k", bf, (B, Hkv, d), True)
-    _need(new_v, "new_v", bf, (B, Hkv, d), True)
-    _need(write_slot, "write_slot", i32, (B, Hkv), True)
-    _need(out, "out", bf, (B, Hq, d), True)
-    with _on_device(q.device, k4, k_scale, v4, v_scale, mask, new_k, new_v, write_slot, out):
-        n = _kv4_bytes(q.device.index, B, Hq, Hkv, d, S)
-        ws = _workspace(workspace, n, q.device, stream) if n or workspace is not None else None
+    Hq = q.shape[1]
+    bf, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    ptrs = _pointers(
+        q, "q", bf, (B, Hq, d), k4, "k4", u8, (B, Hkv, S, d // 2),
+        k_scale, "k_scale", bf, (B, Hkv, S, d // 32), v4, "v4", u8, (B, Hkv, S, d // 2),
+        v_scale, "v_scale", bf, (B, Hkv, S, d // 32), mask, "mask", i32, (B, Hkv, S),
+        new_k, "new_k", bf, (B, Hkv, d), new_v, "new_v", bf, (B, Hkv, d),
+        write_slot, "write_slot", i32, (B, Hkv), out, "out", bf, (B, Hq, d))
+    device = q.device
+    with _on_device(device, q):
+        n = _kv4_bytes(device.index, B, Hq, Hkv, d, S)
+        ws = _workspace(workspace, n, device, stream) if n or workspace is not None else None
         _check(lib, lib.lf_decode_attention_kv4(
-            q.data_ptr(), k4.data_ptr(), k_scale.data_ptr(), v4.data_ptr(), v_scale.data_ptr(),
-            mask.data_ptr(), new_k.data_ptr(), new_v.data_ptr(), write_slot.data_ptr(),
-            out.data_ptr(), B, Hq, Hkv, d, S, float(scale), _ptr(ws),
-            0 if ws is None else ws.numel(), _call_stream(stream, q.device)))
+            *ptrs, B, Hq, Hkv, d, S, float(scale), _ptr(ws), 0 if ws is None else ws.numel(),
+            _call_stream(stream, device)))
 
 
 def step_plan(B: int, Hq: int, Hkv: int, d: int, S: int, topk: int = 1) -> dict:

@@ -1,8 +1,10 @@
 """Build liblf_decode.so (sm_103a) in-tree with nvcc.
 
 Each .cu file compiles to an object in parallel, then one shared library is
-linked. Output: decode_kv_cache_step_gb300/lib/liblf_decode.so. Nothing is
-installed outside the package directory.
+linked. Output: decode_kv_cache_step_gb300/lib/liblf_decode.so, and beside it
+_lf_check.so, the binding's argument checks as an extension of the installed
+torch (left out, with a warning, where it does not compile: the binding then
+checks in Python). Nothing is installed outside the package directory.
 """
 from __future__ import annotations
 
@@ -11,7 +13,9 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "liblf_decode.so")
+CHECK_PATH = os.path.join(LIB_DIR, "_lf_check.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -40,7 +45,8 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+        glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+        glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
 def up_to_date() -> bool:
@@ -48,6 +54,33 @@ def up_to_date() -> bool:
         return False
     t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _build_check() -> None:
+    """lib/_lf_check.so, against the installed torch."""
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    include = os.path.join(base, "include")
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
+    os.close(fd)
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", include,
+           "-I", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "lf_check.cpp"), "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode == 0:
+            os.replace(tmp, CHECK_PATH)
+            return
+        why = r.stderr[-400:]
+    except OSError as e:
+        why = str(e)
+    for path in (tmp, CHECK_PATH):
+        if os.path.exists(path):
+            os.unlink(path)
+    warnings.warn(f"_lf_check.so was not built: {why}")
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -70,8 +103,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj
 
     srcs = _sources()
-    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        check = ex.submit(_build_check)
         objs = list(ex.map(compile_one, srcs))
+        check.result()
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
     os.close(fd)
     cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]

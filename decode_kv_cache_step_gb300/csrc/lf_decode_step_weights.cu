@@ -154,8 +154,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) lf_select_kernel(const Step
 template <int G>
 cudaError_t launch_select_t(const StepParams& p, int units, cudaStream_t stream) {
     const bool staged = p.S <= kSelectKeys;
-    cudaError_t e = cudaFuncSetAttribute(lf_select_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSelectKeys * 4);
+    cudaError_t e = allow_shared<lf_select_kernel<G>>(kSelectKeys * 4);
     if (e != cudaSuccess) return e;
     const char* env = std::getenv("LF_PDL");
     cudaLaunchAttribute attr[1];

@@ -6,7 +6,22 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace lf {
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device; asks
+// the runtime once per device (a device seen again after another is asked again).
+template <auto kKernel>
+cudaError_t allow_shared(int bytes) {
+    static std::atomic<int> allowed_on{-1};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || allowed_on.load(std::memory_order_relaxed) == dev) return e;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) allowed_on.store(dev, std::memory_order_relaxed);
+    return e;
+}
 
 constexpr int kTile = 64;           // cache slots per pipeline tile
 constexpr int kMaxChunkTiles = 32;  // tiles per chunk (split of the slot axis) at most

@@ -866,9 +866,8 @@ struct Config {
 
 template <int D, int G>
 cudaError_t launch_kv4_dg(const Kv4Params& p, int units, int nchunk, cudaStream_t stream) {
-    const auto kernel = lf_kv4_attn_kernel<D, G>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kAlloc);
+    constexpr auto kernel = lf_kv4_attn_kernel<D, G>;
+    const cudaError_t e = allow_shared<kernel>(Ring<D>::kAlloc);
     if (e != cudaSuccess) return e;
     Config c(dim3(nchunk, units), kThreads, stream);
     c.cfg.dynamicSmemBytes = Ring<D>::kAlloc;

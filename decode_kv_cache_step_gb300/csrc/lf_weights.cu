@@ -538,8 +538,8 @@ template <int D, int kForm, int kHeld>
 cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmK, const PromptWeightsParams& p,
                         dim3 grid, int cluster, cudaStream_t stream) {
     using L = WeightsSmem<D, kHeld>;
-    const auto kernel = lf_prompt_weights_kernel<D, kForm, kHeld>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    constexpr auto kernel = lf_prompt_weights_kernel<D, kForm, kHeld>;
+    const cudaError_t e = allow_shared<kernel>(L::kAlloc);
     if (e != cudaSuccess) return e;
     const char* env = std::getenv("LF_PDL");
     cudaLaunchAttribute attr[2];
