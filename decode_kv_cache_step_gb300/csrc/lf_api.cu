@@ -950,7 +950,18 @@ lf_status weights_layout(const Shape& s, int topk, int dev, WeightsLayout* out) 
     const int units = s.B * s.Hkv;
     L.pl = plan_split(s.S, units, sm_count(dev), topk == 1, s.d, s.Hq / s.Hkv, 2);
     if (L.pl.stages == 3) L.pl.stages = 2;  // (LF_STAGES; there is no such instance)
-    if (topk > 1) plan_split_finish(&L.pl, s.S, units, sm_count(dev), true);
+    // A batch too small to fill the GPU with long chunks: no more of the short ones
+    // than are resident at once (18 units of 9001 slots, d = 64, several slots at
+    // once: 29 chunks of 5 tiles, 522 CTAs, 39.3 us; 24 of 6, 432 CTAs, 34.2).
+    const int sms = sm_count(dev);
+    const int longest = (L.pl.tiles + lf::kMaxChunkTiles - 1) / lf::kMaxChunkTiles;
+    if (!L.pl.cluster && static_cast<long>(units) * longest < sms && !std::getenv("LF_CHUNK_TILES") &&
+        static_cast<long>(units) * L.pl.nchunk > 3L * sms) {
+        const int most = std::max(longest, 3 * sms / units);
+        L.pl.chunk_tiles = (L.pl.tiles + most - 1) / most;
+        L.pl.nchunk = (L.pl.tiles + L.pl.chunk_tiles - 1) / L.pl.chunk_tiles;
+    }
+    if (!L.pl.cluster) plan_split_finish(&L.pl, s.S, units, sms, true);
     L.step = scratch_layout(s, L.pl, 0);
     L.counters = lf::kCounterWordsPerUnit * static_cast<size_t>(units) * sizeof(uint32_t);
     L.scratch = align_up(L.counters, 256);
@@ -959,13 +970,17 @@ lf_status weights_layout(const Shape& s, int topk, int dev, WeightsLayout* out) 
 }
 
 // What weights of a prompt a call asks for, and its plan.
-lf_status plan_weights(int T, const Shape& s, int rows, int dev, lf::PromptWeightsParams* p) {
+lf_status check_weights(int T, const Shape& s, int rows) {
     lf_status st;
     if ((st = check_rows(T)) != LF_OK) return st;
     if ((st = check_shape(s)) != LF_OK) return st;
     if (static_cast<int64_t>(T) * s.Hq > (int64_t(1) << 30))
         return fail(LF_ERR_UNSUPPORTED, "T * Hq exceeds 2^30");
     if (rows < 0) return fail(LF_ERR_INVALID_ARG, "rows must be >= 0 (got %d)", rows);
+    return LF_OK;
+}
+
+void plan_weights(int T, const Shape& s, int rows, int dev, lf::PromptWeightsParams* p) {
     p->T = T;
     p->B = s.B;
     p->Hq = s.Hq;
@@ -973,7 +988,6 @@ lf_status plan_weights(int T, const Shape& s, int rows, int dev, lf::PromptWeigh
     p->S = s.S;
     p->rows = std::min(rows, s.S);  // (a sequence has no more)
     lf::plan_prompt_weights(p, sm_count(dev));
-    return LF_OK;
 }
 
 size_t stats_bytes(const lf::PromptWeightsParams& p) {
@@ -1566,12 +1580,14 @@ lf_status lf_decode_step_weights(const void* q, void* k_cache, void* v_cache, in
 lf_status lf_prompt_weights_workspace(int T, int B, int Hq, int Hkv, int d, int S, int rows,
                                       size_t* bytes) {
     if (!bytes) return fail(LF_ERR_INVALID_ARG, "bytes is NULL");
+    const Shape s{B, Hq, Hkv, d, S, 0, 1.f};
+    lf_status st = check_weights(T, s, rows);
+    if (st != LF_OK) return st;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     lf::PromptWeightsParams p = {};
-    lf_status st = plan_weights(T, Shape{B, Hq, Hkv, d, S, 0, 1.f}, rows, dev, &p);
-    if (st != LF_OK) return st;
+    plan_weights(T, s, rows, dev, &p);
     *bytes = stats_bytes(p);
     return LF_OK;
 }
@@ -1587,17 +1603,17 @@ lf_status lf_prompt_weights(const void* q, const void* k_cache, const int32_t* q
     if ((st = check_ptr(kv_len, 4, "kv_len")) != LF_OK) return st;
     if ((st = check_ptr(weights, 4, "weights")) != LF_OK) return st;
     const Shape s{B, Hq, Hkv, d, S, 0, scale};
-    int dev = 0;
-    cudaError_t e;
-    lf::PromptWeightsParams p = {};
-    if ((st = check_shape(s)) != LF_OK) return st;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if ((st = plan_weights(T, s, rows, dev, &p)) != LF_OK) return st;
+    if ((st = check_weights(T, s, rows)) != LF_OK) return st;
     const size_t slots = static_cast<size_t>(B) * Hkv * S;
     if (overlaps(weights, slots * 4, q, static_cast<size_t>(T) * Hq * d * 2) ||
         overlaps(weights, slots * 4, k_cache, slots * d * 2))
         return fail(LF_ERR_INVALID_ARG, "weights overlaps q or k_cache");
     if ((st = check_ptr(workspace, 256, "workspace")) != LF_OK) return st;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    lf::PromptWeightsParams p = {};
+    plan_weights(T, s, rows, dev, &p);
     const size_t need = stats_bytes(p);
     if (workspace_bytes < need)
         return fail(LF_ERR_INVALID_ARG, "workspace of %zu bytes; this call needs %zu", workspace_bytes, need);

@@ -803,17 +803,9 @@ __global__ void __launch_bounds__(kThreads) lf_kv4_join_kernel(const Kv4Params p
     const float* po = p.part_o + (static_cast<size_t>(u) * nchunk * G + h) * D;
     constexpr int kE = D / 32;  // values of a lane
     constexpr int kAhead = 8;
-    float m = -INFINITY;
-    for (int k = lane; k < nchunk; k += 32) m = fmaxf(m, __ldcg(&ml[static_cast<size_t>(k) * G].x));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) m = 0.f;
-    float o[kE], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = 0.f;
-    for (int k0 = warp; k0 < nchunk; k0 += kWarps * kAhead) {
-        float2 v[kAhead];
-        float x[kAhead][kE];
+    float2 v[kAhead];
+    float x[kAhead][kE];
+    const auto load = [&](int k0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int k = k0 + i * kWarps;
@@ -822,6 +814,17 @@ __global__ void __launch_bounds__(kThreads) lf_kv4_join_kernel(const Kv4Params p
             for (int e = 0; e < kE; ++e)
                 x[i][e] = k < nchunk ? __ldcg(po + static_cast<size_t>(k) * G * D + e * 32 + lane) : 0.f;
         }
+    };
+    load(warp);  // in flight with the maximum's loads
+    float m = -INFINITY;
+    for (int k = lane; k < nchunk; k += 32) m = fmaxf(m, __ldcg(&ml[static_cast<size_t>(k) * G].x));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.f;
+    float o[kE], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = 0.f;
+    for (int k0 = warp;;) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             // A chunk without a live slot has l = 0, its output is not there.
@@ -831,6 +834,9 @@ __global__ void __launch_bounds__(kThreads) lf_kv4_join_kernel(const Kv4Params p
 #pragma unroll
             for (int e = 0; e < kE; ++e) o[e] += x[i][e] * f;
         }
+        k0 += kWarps * kAhead;
+        if (k0 >= nchunk) break;
+        load(k0);
     }
 #pragma unroll
     for (int e = 0; e < kE; ++e) s_o[warp][e * 32 + lane] = o[e];
@@ -890,8 +896,8 @@ cudaError_t launch_kv4_d(int G, const Kv4Params& p, int units, int nchunk, cudaS
 
 Kv4Plan kv4_plan(int units, int S, int sms) {
     // Three CTAs are resident per SM; chunks of whole 128 slots (32 a warp).
-    // Few slots: one chunk, which needs no join (measured on a call of 8 units of
-    // 256 slots, two chunks and one: PLACEHOLDER us).
+    // Up to 512 slots: one chunk, which needs no join (8 units, us in one chunk: 128
+    // slots 5.2, 256 6.0, 512 7.8; in chunks of 128 and joined, 640 slots 7.1).
     const int steps = (S + 127) / 128;
     const int longest = kMaxChunkSlots / 128;
     const int fill = steps <= 4 ? 1 : std::max(1, 3 * sms / units);

@@ -500,7 +500,7 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
     uint8_t* topk_area = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(s_pre + (kPrefix ? (p.pre_pieces + 1) * G : 0)) + 15) &
         ~static_cast<uintptr_t>(15));
-    uint8_t* scan_area = topk_area + (p.topk > 1 ? kTopKAreaBytes : 0);
+    uint8_t* scan_area = topk_area + (kScore != kWeights && p.topk > 1 ? kTopKAreaBytes : 0);
     const int scan_bytes = usable - static_cast<int>(scan_area - smem);
     const float2* ml = p.part_ml + static_cast<size_t>(u) * nchunk * G;
     const int b = u / p.Hkv;
@@ -2086,7 +2086,7 @@ cudaError_t launch_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const StepP
                      int units, cudaStream_t stream, bool pdl) {
     using L = StepSmem<D, kStages>;
     static_assert(!(kCluster && kPrefix), "the cluster merge takes no prefix pieces");
-    if (finish_smem_bytes(p_in.nchunk, G, kScore ? p_in.topk : 1) +
+    if (finish_smem_bytes(p_in.nchunk, G, kScore == kLongFlow ? p_in.topk : 1) +
             (kPrefix ? prefix_smem_bytes(p_in.pre_pieces, G) : 0) >
         static_cast<size_t>(L::kBarOff))
         return cudaErrorInvalidConfiguration;
