@@ -210,9 +210,10 @@ def _load_check():
         spec = importlib.util.spec_from_loader("_lf_check", loader)
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
-        return module.pointers
     except ImportError:  # built for another torch
         return None
+    same = getattr(module, "torch_version", None) == torch.__version__
+    return module.pointers if same else None
 
 
 _fast_pointers = _load_check()

@@ -65,7 +65,8 @@ def _build_check() -> None:
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
     os.close(fd)
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", include,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DLF_TORCH_VERSION="{torch.__version__}"', "-I", include,
            "-I", os.path.join(include, "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "lf_check.cpp"), "-o", tmp,
            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]

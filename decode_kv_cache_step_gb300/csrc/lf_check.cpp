@@ -72,4 +72,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lf_check", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__lf_check() { return PyModule_Create(&module); }
+// (The torch whose headers this was compiled against: the binding uses it with no
+// other.)
+PyMODINIT_FUNC PyInit__lf_check() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", LF_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

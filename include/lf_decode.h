@@ -473,8 +473,8 @@ lf_status lf_decode_prefix_workspace(int B, int Hq, int Hkv, int d, int S, int N
  * starting from 0 in the slot that the step writes, and the step returns the k
  * slots with the lowest (weights[j], slot) among live slots of age >= W.
  *
- * weights    in/out float [B][Hkv][S]: entries of masked slots are neither read
- *                nor written. A slot whose sum is NaN is never returned.
+ * weights    in/out float [B][Hkv][S]: what masked slots hold does not matter and
+ *                stays. A slot whose sum is NaN is never returned.
  * decay      0 <= decay <= 1 (1: the plain sum; 0: the current step's weights)
  * next_slots, k, flags   as in lf_decode_step_ex (without LF_STEP_LOG2_SCORES)
  * The other arguments are those of lf_decode_step. weights must not overlap the

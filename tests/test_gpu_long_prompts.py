@@ -207,6 +207,45 @@ def test_weights_step_by_every_merge(monkeypatch, env, shape):
     no_errors()
 
 
+@pytest.mark.parametrize("env", [{"LF_CLUSTER": "0", "LF_SPLIT": "1"}, {"LF_SPLIT": "0"}, {"LF_CHUNK_TILES": "1"}])
+def test_several_slots_by_every_finish(monkeypatch, env):
+    for name, value in env.items():
+        monkeypatch.setenv(name, value)
+    g = gen(9)
+    for S, k, flags in ((700, 20, 0), (9001, 1024, lf.LF_STEP_FILL_EMPTY_FIRST), (130, 200, lf.LF_STEP_MASK_EVICTED)):
+        c = step_case(g, 2, 4, 1, 64, S, [S, S // 3])
+        check_step(c, torch.randint(0, S, (2, 1), generator=g, dtype=torch.int32).cuda(), 5, 0.125, 0.9, k, flags)
+    no_errors()
+
+
+@pytest.mark.parametrize("S,k", [(300, 5), (2000, 1000), (50001, 7)])
+def test_several_slots_with_equal_weights(S, k):
+    """Ties go to the lowest slots; caches beyond what the selection stages."""
+    g = gen(S)
+    c = step_case(g, 1, 1, 1, 64, S, holes=0.05)
+    live = c["mask"] >= 0
+    c["k"][live] = 1.0  # every live slot weighs the same
+    c["weights"][live] = 0.5
+    c["weights"][0, 0, 3::7] = torch.where(live[0, 0, 3::7], 0.25, c["weights"][0, 0, 3::7])
+    mask = c["mask"].cpu()
+    _, nxt = run_step(c, ints([[-1]]), 11, 0.125, k=k)
+    assert torch.equal(nxt.cpu(), plain.chosen(c["weights"].cpu(), mask, 11, k, False))
+    assert torch.unique(c["weights"][live]).numel() == 2
+    no_errors()
+
+
+def test_a_switch_that_changes_after_the_first_call(monkeypatch):
+    """A plan that needs a larger workspace than the one a call of these sizes last had."""
+    g = gen(10)
+    c = step_case(g, 2, 8, 2, 128, 3000)
+    check_step(c, ints([[1, 2], [3, 4]]), 4, 0.1)
+    lf.release_workspace()
+    monkeypatch.setenv("LF_CHUNK_TILES", "1")
+    monkeypatch.setenv("LF_CLUSTER", "0")
+    check_step(c, ints([[5, 6], [7, 8]]), 4, 0.1)
+    no_errors()
+
+
 def test_weights_step_long_cache_off_16_bytes():
     """Arrays whose rows do not start on 16 bytes take the other way through the scan."""
     g = gen(3)
@@ -269,6 +308,7 @@ PROMPT = [  # rows per sequence, lengths, S, counted rows
     ([33, 70], [161, 70], 200, 32), ([129], [400], 401, 0), ([257], [257], 260, 5),
     ([300, 1, 5], [300, 300, 300], 384, 0), ([64, 64], [64, 128], 128, 200), ([1] * 37, list(range(1, 38)), 40, 0),
     ([2, 150], [2, 511], 513, 1), ([5], [1024], 1024, 0), ([0, 0], [0, 7], 8, 0),
+    ([400, 300], [400, 500], 512, 150), ([17, 400, 0], [600, 400, 9], 700, 33), ([1, 2], [1000, 3], 1000, 7),
 ]
 
 
@@ -289,6 +329,33 @@ def test_prompt_weights(nq, kv, S, rows, Hq, Hkv, d):
     near(w, ref, tol)
     for b in range(B):
         assert torch.equal(w[b, :, kv[b]:], w0[b, :, kv[b]:])
+    no_errors()
+
+
+@pytest.mark.parametrize("rows", [0, 20])
+def test_prompt_weights_are_the_same_bits_again(rows):
+    g = gen(3)
+    q, k = normal(g, 900, 8, 128), normal(g, 2, 2, 900, 128)
+    got = []
+    for _ in range(3):
+        w = torch.zeros(2, 2, 900, device="cuda")
+        lf.prompt_weights(q, k, ints([0, 300, 900]), ints([900, 600]), w, 0.1, rows=rows)
+        got.append(w)
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("T,rows", [(900, 0), (900, 10)])
+def test_prompt_weights_waits_that_run_out(monkeypatch, T, rows):
+    """Waits with no time left end the call with an error, and the next call is right."""
+    g = gen(6)
+    q, k = normal(g, T, 4, 128), normal(g, 1, 1, T, 128)
+    w = torch.zeros(1, 1, T, device="cuda")
+    monkeypatch.setenv("LF_WAIT_LIMIT_NS", "1")
+    lf.prompt_weights(q, k, ints([0, T]), ints([T]), w, 0.1, rows=rows)
+    assert lf.device_errors(clear=True) == lf.LF_DEVERR_WAIT_TIMEOUT
+    monkeypatch.delenv("LF_WAIT_LIMIT_NS")
+    lf.prompt_weights(q, k, ints([0, T]), ints([T]), w, 0.1, rows=rows)
+    assert abs(float(w.double().sum()) - 4 * (rows or T)) < 1e-2
     no_errors()
 
 
@@ -541,6 +608,46 @@ def test_kv4_attention_scales_that_grow():
     check_kv4(c, ints([[-1]]), 128 ** -0.5)
     c["ks"][0, 0, 64:] = 0  # logits of 0 but for the first slots
     check_kv4(c, ints([[-1]]), 1.0)
+    no_errors()
+
+
+def test_kv4_attention_offsets_past_32_bits():
+    """The last sequence of a cache of more than 2^32 bytes of codes, and rows written there."""
+    g = gen(17)
+    S, n = 1 << 20, 300
+    c = kv4_case(g, 1, 2, 1, 128, n, holes=0.05)
+    B = 66
+    big = {}
+    for name, row in (("k4", 64), ("v4", 64), ("ks", 4), ("vs", 4)):
+        big[name] = torch.empty((B, 1, S, row), dtype=c[name].dtype, device="cuda")
+        big[name][-1, 0, S - n:] = c[name][0, 0]
+    big["mask"] = torch.full((B, 1, S), -1, dtype=torch.int32, device="cuda")
+    big["mask"][-1, 0, S - n:] = c["mask"][0, 0]
+    big["q"] = c["q"].expand(B, 2, 128).contiguous()
+    big["nk"], big["nv"] = (c[x].expand(B, 1, 128).contiguous() for x in ("nk", "nv"))
+    ws = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    ws[-1] = S - n + 7
+    out = run_kv4(big, ws, 0.1)
+    check_kv4(c, ints([[7]]), 0.1)
+    for name in ("k4", "v4", "mask"):
+        assert torch.equal(big[name][-1, 0, S - n:], c[name][0, 0])
+    k, v = plain.stand_for(c["k4"], c["ks"], 8), plain.stand_for(c["v4"], c["vs"], 4)
+    ref, tol = plain.kv4_attention(c["q"], k, v, c["ks"], c["vs"], c["mask"], 0.1)
+    near(out[-1:], ref, tol)
+    assert (out[:-1] == 0).all()
+    # Packed and unpacked there too.
+    x = normal(g, 1, 1, n, 128)
+    P = S
+    src = torch.empty((B, 1, P, 128), dtype=BF, device="cuda")
+    src[-1, 0, S - n:] = x[0, 0]
+    first = torch.tensor([0] * (B - 1) + [S - n], dtype=torch.int32).cuda()
+    last = torch.tensor([0] * (B - 1) + [S], dtype=torch.int32).cuda()
+    lf.kv4_pack(src, src, first, last, big["k4"], big["ks"], big["v4"], big["vs"], big["mask"])
+    code, scale, value = plain.quantise(x[0, 0])
+    assert torch.equal(big["k4"][-1, 0, S - n:].cpu(), plain.lay(code, 8))
+    assert torch.equal(big["v4"][-1, 0, S - n:].cpu(), plain.lay(code, 4))
+    lf.kv4_unpack(big["k4"], big["ks"], big["v4"], big["vs"], first, last, src, src.clone())
+    assert torch.equal(src[-1, 0, S - n:].cpu(), value.to(BF))
     no_errors()
 
 
