@@ -252,7 +252,11 @@ struct Ring {
     static constexpr int kVScaleOff = kKScaleOff + kTileSlots * kScaleRow;
     static constexpr int kStage = kVScaleOff + kTileSlots * kScaleRow;
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kWarp = kStages * kStage;
+    // Behind the tiles: the scales of one tile's keys, and of one tile's values, in
+    // fp32 (rows of d / 32).
+    static constexpr int kKWideOff = kStages * kStage;
+    static constexpr int kVWideOff = kKWideOff + kTileSlots * (D / 8);
+    static constexpr int kWarp = kVWideOff + kTileSlots * (D / 8);
     static constexpr int kAlloc = kWarps * kWarp;
 };
 constexpr float kCode = 0x1p-24f;  // what the integer 1 in a half's low bits is worth
@@ -552,7 +556,33 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
     uint32_t E = 20;
     float fE = __uint_as_float((kHalfExp + 254 - 20) << 23);
 
-    // Waits for tile i of the list and puts the token's row in its place there.
+    float* const k_wide = reinterpret_cast<float*>(ring + R::kKWideOff);
+    float* const v_wide = reinterpret_cast<float*>(ring + R::kVWideOff);
+    // A lane widens the scales of its row of the tile once for all that read them.
+    auto widen = [&](const uint32_t (&w)[NG / 2], float f, float* to) {
+        float v[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) v[g] = scale_of(w[g >> 1], g & 1) * f;
+        if constexpr (NG == 4)
+            reinterpret_cast<float4*>(to)[lane] = make_float4(v[0], v[1], v[2], v[3]);
+        else
+            reinterpret_cast<float2*>(to)[lane] = make_float2(v[0], v[1]);
+    };
+    auto wide = [&](const float* from, int row, float (&v)[NG]) {
+        if constexpr (NG == 4) {
+            const float4 x = reinterpret_cast<const float4*>(from)[row];
+            v[0] = x.x;
+            v[1] = x.y;
+            v[2] = x.z;
+            v[3] = x.w;
+        } else {
+            const float2 x = reinterpret_cast<const float2*>(from)[row];
+            v[0] = x.x;
+            v[1] = x.y;
+        }
+    };
+    // Waits for tile i of the list, puts the token's row in its place there and
+    // widens the keys' scales.
     auto arrive = [&](int i, uint8_t* tile) {
         copy_wait<R::kStages - 2>();
         __syncwarp();
@@ -570,18 +600,23 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
             }
             __syncwarp();
         }
+        uint32_t ks[NG / 2];
+        shared_words<NG / 2>(tile + R::kKScaleOff + lane * R::kScaleRow, ks);
+        widen(ks, 1.f, k_wide);
+        __syncwarp();
     };
     // Logits of the tile's slots r + 8 h: x[2 h] and x[2 h + 1], heads 2 c and 2 c + 1.
     float x[8];
     auto logits = [&](const uint8_t* tile) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            uint32_t kw[2][NG], ks[2][NG / 2], kz[2];
+            uint32_t kw[2][NG], kz[2];
+            float ks[2][NG];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int row = r + 8 * h + 16 * half;
                 shared_words<NG>(tile + row * R::kKRow + c * (D / 8), kw[h]);
-                shared_words<NG / 2>(tile + R::kKScaleOff + row * R::kScaleRow, ks[h]);
+                wide(k_wide, row, ks[h]);
                 kz[h] = *reinterpret_cast<const uint32_t*>(tile + R::kKScaleOff + row * R::kScaleRow +
                                                            c % (NG / 2) * 4);
             }
@@ -598,11 +633,10 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
                 const uint32_t o[4] = {kw[0][g] & 0x00f000f0u, kw[1][g] & 0x00f000f0u,
                                        (kw[0][g] >> 8) & 0x00f000f0u, (kw[1][g] >> 8) & 0x00f000f0u};
                 mma_f16_16816(sc, o, qf[g][2], qf[g][3], sc);
-                const float sa = scale_of(ks[0][g >> 1], g & 1), sb = scale_of(ks[1][g >> 1], g & 1);
-                y[0] += sc[0] * sa;
-                y[1] += sc[1] * sa;
-                y[2] += sc[2] * sb;
-                y[3] += sc[3] * sb;
+                y[0] += sc[0] * ks[0][g];
+                y[1] += sc[1] * ks[0][g];
+                y[2] += sc[2] * ks[1][g];
+                y[3] += sc[3] * ks[1][g];
             }
             x[4 * half] = y[0] * qs[0];
             x[4 * half + 1] = y[1] * qs[1];
@@ -620,10 +654,8 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
         const uint32_t live = s_tiles[warp][i].x;
-        uint32_t vs[4][NG / 2];
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-            shared_words<NG / 2>(tile + R::kVScaleOff + (r + 8 * h) * R::kScaleRow, vs[h]);
+        uint32_t vs[NG / 2];  // of the lane's row
+        shared_words<NG / 2>(tile + R::kVScaleOff + lane * R::kScaleRow, vs);
         if (live != 0xffffffffu) {
             // Masked slots: weight 0, and 0 for the scales of whatever lies there.
 #pragma unroll
@@ -631,9 +663,9 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
                 const bool is = (live >> (r + 8 * h)) & 1u;
                 x[2 * h] = is ? x[2 * h] : NEG;
                 x[2 * h + 1] = is ? x[2 * h + 1] : NEG;
-#pragma unroll
-                for (int k = 0; k < NG / 2; ++k) vs[h][k] = is ? vs[h][k] : 0u;
             }
+#pragma unroll
+            for (int k = 0; k < NG / 2; ++k) vs[k] = (live >> lane) & 1u ? vs[k] : 0u;
         }
         float mx0 = fmaxf(fmaxf(x[0], x[2]), fmaxf(x[4], x[6]));
         float mx1 = fmaxf(fmaxf(x[1], x[3]), fmaxf(x[5], x[7]));
@@ -655,23 +687,16 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
             rescale(f0, f1);
         }
         // The largest scale, as the bits of two bf16 side by side.
-        uint32_t two = 0;
-#pragma unroll
-        for (int k = 0; k < NG / 2; ++k) {
-            two = __vimax3_u16x2(two, vs[0][k], vs[1][k]);
-            two = __vimax3_u16x2(two, vs[2][k], vs[3][k]);
-        }
+        const uint32_t two = __vimax3_u16x2(vs[0], vs[NG / 2 - 1], 0u);
         if (__any_sync(0xffffffffu, max(two & 0xffffu, two >> 16) >= (E + 1) << 7)) {
             // Rare: a new power of two, of the finite ones.
             uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < NG / 2; ++k)
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const uint32_t lo = vs[h][k] & 0x7f80u, hi = (vs[h][k] >> 16) & 0x7f80u;
-                    if (lo != 0x7f80u) top = max(top, lo);
-                    if (hi != 0x7f80u) top = max(top, hi);
-                }
+            for (int k = 0; k < NG / 2; ++k) {
+                const uint32_t lo = vs[k] & 0x7f80u, hi = (vs[k] >> 16) & 0x7f80u;
+                if (lo != 0x7f80u) top = max(top, lo);
+                if (hi != 0x7f80u) top = max(top, hi);
+            }
             top = __reduce_max_sync(0xffffffffu, top) >> 7;
             if (top > E) {
                 const float down = __uint_as_float(static_cast<uint32_t>(max(0, 127 - static_cast<int>(top - E))) << 23);
@@ -680,6 +705,7 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
                 fE = __uint_as_float((kHalfExp + 254 - E) << 23);
             }
         }
+        widen(vs, fE, v_wide);
         // The weights; the sums take them unrounded.
         float f[8];
 #pragma unroll
@@ -689,8 +715,6 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
         }
         l0 += (f[0] + f[2]) + (f[4] + f[6]);
         l1 += (f[1] + f[3]) + (f[5] + f[7]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= fE;
         // The next tile's logits (of nothing behind the last one) beside this
         // one's values: two chains of products to keep the pipes busy.
         const int next_stage = stage + 1 == R::kStages ? 0 : stage + 1;
@@ -706,11 +730,13 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
                                          r * (D / 16),
                                      vw[k]);
             const float* const fh = f + 4 * half;
+            float sa[NG], sb[NG];
+            wide(v_wide, 16 * half + r, sa);
+            wide(v_wide, 16 * half + r + 8, sb);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const float sa = scale_of(vs[2 * half][g >> 1], g & 1), sb = scale_of(vs[2 * half + 1][g >> 1], g & 1);
-                const uint32_t b0 = movmatrix_trans(pack_f16x2(fh[0] * sa, fh[1] * sa));
-                const uint32_t b1 = movmatrix_trans(pack_f16x2(fh[2] * sb, fh[3] * sb));
+                const uint32_t b0 = movmatrix_trans(pack_f16x2(fh[0] * sa[g], fh[1] * sa[g]));
+                const uint32_t b1 = movmatrix_trans(pack_f16x2(fh[2] * sb[g], fh[3] * sb[g]));
                 // Slots 2 c and 2 c + 1 side by side: the lane's four codes of group g.
                 const uint32_t pick = g & 1 ? 0x7632u : 0x5410u;
                 const uint32_t ya = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], pick);
