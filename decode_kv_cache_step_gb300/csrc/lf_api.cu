@@ -598,7 +598,8 @@ lf_status launch(const Launch& r, cudaStream_t stream) {
     // tail. The scoring launch is counted under LF_KERNEL_SCORE.
     NvtxRange range(r.score ? "lf_decode_step" : "lf_decode_attention");
     ProfScope prof(r.score ? LF_KERNEL_DECODE_STEP : LF_KERNEL_ATTENTION, stream);
-    const bool cluster = r.pl.cluster && r.sp.topk == 1;
+    // (Several slots by the accumulated weight come from the selection kernel.)
+    const bool cluster = r.pl.cluster && (r.sp.topk == 1 || r.score == 2);
     if (r.sp.pre_pieces > 0)
         e = lf::launch_decode_step_prefix(r.d, r.g, r.score, r.tmK, r.tmV, r.sp, r.units, stream);
     else
@@ -622,7 +623,7 @@ lf_status launch(const Launch& r, cudaStream_t stream) {
     }
     if (r.score == 2 && r.sp.topk > 1) {
         prof_count(LF_KERNEL_SCORE);
-        e = lf::launch_select(r.g, r.sp, r.units, stream);
+        e = lf::launch_select(r.sp, r.units, stream);
         if (e != cudaSuccess) return cuda_fail(e, "selection launch");
     }
     return LF_OK;
@@ -942,17 +943,18 @@ lf_status window_pieces(int T, const Shape& s, int window, int sinks, int* piece
 struct WeightsLayout {
     Plan pl;
     Layout step;
-    size_t counters, scratch, total;
+    size_t counters, scratch, keys, total;
 };
 
 lf_status weights_layout(const Shape& s, int topk, int dev, WeightsLayout* out) {
     WeightsLayout& L = *out;
     const int units = s.B * s.Hkv;
-    L.pl = plan_split(s.S, units, sm_count(dev), topk == 1, s.d, s.Hq / s.Hkv, 2);
+    L.pl = plan_split(s.S, units, sm_count(dev), true, s.d, s.Hq / s.Hkv, 2);
     if (L.pl.stages == 3) L.pl.stages = 2;  // (LF_STAGES; there is no such instance)
-    // A batch too small to fill the GPU with long chunks: no more of the short ones
-    // than are resident at once (18 units of 9001 slots, d = 64, several slots at
-    // once: 29 chunks of 5 tiles, 522 CTAs, 39.3 us; 24 of 6, 432 CTAs, 34.2).
+    // A batch too small to fill the GPU with long chunks, and too long for a
+    // cluster a unit: no more of the short chunks than are resident at once (6 units
+    // of 40000 slots, d = 64: 125 chunks of 5 tiles, 750 CTAs, 57.8 us; 70 of 9, 420
+    // CTAs, 39.1; 2 units of 80000: 82.8 and 69.1).
     const int sms = sm_count(dev);
     const int longest = (L.pl.tiles + lf::kMaxChunkTiles - 1) / lf::kMaxChunkTiles;
     if (!L.pl.cluster && static_cast<long>(units) * longest < sms && !std::getenv("LF_CHUNK_TILES") &&
@@ -965,7 +967,8 @@ lf_status weights_layout(const Shape& s, int topk, int dev, WeightsLayout* out) 
     L.step = scratch_layout(s, L.pl, 0);
     L.counters = lf::kCounterWordsPerUnit * static_cast<size_t>(units) * sizeof(uint32_t);
     L.scratch = align_up(L.counters, 256);
-    L.total = L.scratch + L.step.total;
+    L.keys = L.scratch + L.step.total;
+    L.total = L.keys + (topk > 1 ? static_cast<size_t>(units) * s.S * sizeof(uint32_t) : 0);
     return LF_OK;
 }
 
@@ -1563,13 +1566,13 @@ lf_status lf_decode_step_weights(const void* q, void* k_cache, void* v_cache, in
     if ((st = build_launch(a, s, ws + L.scratch, reinterpret_cast<uint32_t*>(ws), err, L.step, L.pl,
                            &r)) != LF_OK)
         return st;
+    r.sp.keys = reinterpret_cast<uint32_t*>(ws + L.keys);
     r.zero_counters = true;
     g_last_error[0] = '\0';
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     // A cluster merge counts nothing in the workspace. A last-CTA merge counts
     // one word per unit, a split finish four more.
-    const bool cluster = r.pl.cluster && k == 1;
-    if (!cluster && (r.sp.split || r.sp.nchunk > 1)) {
+    if (!r.pl.cluster && (r.sp.split || r.sp.nchunk > 1)) {
         const size_t n = r.sp.split ? L.counters : static_cast<size_t>(r.units) * sizeof(uint32_t);
         if ((e = cudaMemsetAsync(ws, 0, n, stream)) != cudaSuccess)
             return cuda_fail(e, "cudaMemsetAsync(workspace)");

@@ -136,8 +136,7 @@ __global__ void __launch_bounds__(kScoreThreads, G >= 8 ? 4 : 8) lf_score_kernel
                 const bool cand = live ? (aa >= W && L == L) : fill_first;
                 const uint32_t key = live ? ordered_key(L) : 0u;
                 if (kAdd && p.topk > 1) {
-                    // (For the selection kernel, in the slot's first term.)
-                    if (j < S) reinterpret_cast<uint32_t*>(p.stash)[(static_cast<size_t>(u) * S + j) * G] = cand ? key : 0xffffffffu;
+                    if (j < S) p.keys[static_cast<size_t>(u) * S + j] = cand ? key : 0xffffffffu;  // (for the selection kernel)
                 } else if (cand && j < S && key < bkey) {
                     bkey = key;
                     bj = j;

@@ -44,6 +44,7 @@ struct StepParams {
     int32_t* next_slot;          // [units][topk] slots to overwrite, ascending (score, slot)
     float* scores;               // [units][S] or nullptr
     float* weights = nullptr;    // [units][S] accumulated weights (score 2), updated in place
+    uint32_t* keys = nullptr;    // [units][S] selection keys (score 2 with topk > 1)
     float decay = 1.f;
     // scratch
     float* part_o;               // [units][nchunk][G][D]  unnormalised output, base m
@@ -141,7 +142,7 @@ cudaError_t launch_decode_step_weights(int D, int G, int stages, bool cluster,
                                        bool pdl);
 int max_active_clusters_weights(int D, int G, int stages, int csize);
 // The k lowest (key, slot) of every unit, behind such a step with topk > 1.
-cudaError_t launch_select(int G, const StepParams& p, int units, cudaStream_t stream);
+cudaError_t launch_select(const StepParams& p, int units, cudaStream_t stream);
 
 // How many clusters of csize CTAs (one unit each) of the cluster instance
 // (stages 2 or kDeepStages) can be resident at once on the current device;

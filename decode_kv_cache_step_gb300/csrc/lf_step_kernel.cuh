@@ -809,10 +809,12 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
     const int cs = p.chunk_tiles * kTile;
     const int32_t* age = p.mask + static_cast<size_t>(u) * S;
     float* stash = p.stash + static_cast<size_t>(u) * S * G;
-    // For top-k the slot's first stash word is reused for its selection key.
-    uint32_t* keys = reinterpret_cast<uint32_t*>(stash);
     float* scores = p.scores ? p.scores + static_cast<size_t>(u) * S : nullptr;
     constexpr bool kAdd = kScore == kWeights;
+    // For top-k the slot's first stash word is reused for its selection key (by
+    // the accumulated weight, the keys lie side by side for the selection kernel).
+    uint32_t* keys = kAdd ? p.keys + static_cast<size_t>(u) * S : reinterpret_cast<uint32_t*>(stash);
+    constexpr int kKeyStep = kAdd ? 1 : G;
     float* weights = kAdd ? p.weights + static_cast<size_t>(u) * S : nullptr;
     const int ws = kAdd ? p.write_slot[u] : -1;
     const bool fill_first = (p.flags & kFlagFillEmptyFirst) != 0;
@@ -841,7 +843,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
                 bestj = j;
             }
         } else {
-            keys[static_cast<size_t>(j) * G] = cand ? key : 0xffffffffu;
+            keys[static_cast<size_t>(j) * kKeyStep] = cand ? key : 0xffffffffu;
             ncand += cand ? 1 : 0;
         }
         if (scores) scores[j] = live ? exported_score<G>(p, L, t, c) : INFINITY;
@@ -852,7 +854,7 @@ __device__ void score_and_select(const StepParams& p, int u, const float* s_m, c
         for (int c = 0; c < nchunk; ++c)
             if (!s_live[c])
                 for (int j = c * cs + tid; j < min(S, (c + 1) * cs); j += kConsumers)
-                    keys[static_cast<size_t>(j) * G] = 0xffffffffu;
+                    keys[static_cast<size_t>(j) * kKeyStep] = 0xffffffffu;
     }
 
     // A long scan streams each segment's ages and score terms into shared memory
@@ -1101,6 +1103,7 @@ __device__ __forceinline__ void score_chunk(const StepParams& p, int u, int slot
     float* scores = p.scores ? p.scores + static_cast<size_t>(u) * S : nullptr;
     constexpr bool kAdd = kScore == kWeights;
     float* weights = kAdd ? p.weights + static_cast<size_t>(u) * S + slot0 : nullptr;
+    const bool several = kAdd && p.topk > 1;  // a key per slot for the selection kernel
     const bool fill_first = (p.flags & kFlagFillEmptyFirst) != 0;
     // A thread visits its slots in increasing order, so a strict "<" on
     // the key (ordered_key(log2 I_j); 0 for an empty slot under
@@ -1137,7 +1140,9 @@ __device__ __forceinline__ void score_chunk(const StepParams& p, int u, int slot
                     const bool live = (f[k] & kSlotLive) != 0;
                     const bool cand = live ? ((f[k] & kSlotOld) && L[k] == L[k]) : fill_first;
                     const uint32_t key = live ? ordered_key(L[k]) : 0u;
-                    if (cand && key < bkey) {
+                    if (several) {
+                        p.keys[static_cast<size_t>(u) * S + j] = cand ? key : 0xffffffffu;
+                    } else if (cand && key < bkey) {
                         bkey = key;
                         bestj = j;
                     }
@@ -1195,7 +1200,9 @@ __device__ __forceinline__ void score_chunk(const StepParams& p, int u, int slot
                 if (kAdd && live) weights[i] = L;
                 const bool cand = live ? ((f & kSlotOld) && L == L) : fill_first;
                 const uint32_t key = live ? ordered_key(L) : 0u;
-                if (cand && key < bkey) {
+                if (several) {
+                    p.keys[static_cast<size_t>(u) * S + j] = cand ? key : 0xffffffffu;
+                } else if (cand && key < bkey) {
                     bkey = key;
                     bestj = j;
                 }
@@ -1457,9 +1464,11 @@ __device__ __forceinline__ void cluster_merge_push(const StepParams& p, int u, i
                 }
             }
             const int slot = (bestj == 0x7fffffff) ? -1 : bestj;
-            p.next_slot[u] = slot;
-            if (slot >= 0 && (p.flags & kFlagMaskEvicted))
-                p.mask[static_cast<size_t>(u) * p.S + slot] = -1;
+            if (kScore == kLongFlow || p.topk == 1) {
+                p.next_slot[u] = slot;
+                if (slot >= 0 && (p.flags & kFlagMaskEvicted))
+                    p.mask[static_cast<size_t>(u) * p.S + slot] = -1;
+            }
         }
         // This chunk's score terms are read: drop them from L2, no write-back.
         if constexpr (!kSmemTerms) {

@@ -234,6 +234,22 @@ def test_several_slots_with_equal_weights(S, k):
     no_errors()
 
 
+@pytest.mark.parametrize("env", [{}, {"LF_CLUSTER": "0", "LF_SPLIT": "0"}, {"LF_CLUSTER": "0", "LF_SPLIT": "1"}])
+@pytest.mark.parametrize("S,k", [(16384, 3), (16385, 8), (40000, 1), (40000, 7), (40000, 9), (70001, 6), (70001, 400),
+                                 (100, 8)])
+def test_several_slots_of_long_caches(monkeypatch, env, S, k):
+    """Exactly the lowest (weight, slot), whatever the finish and the length, ties and empty units too."""
+    for name, value in env.items():
+        monkeypatch.setenv(name, value)
+    g = gen(S + k)
+    c = step_case(g, 3, 2, 1, 64, S, [S, min(S, k // 2), 0], holes=0.1)
+    c["weights"].copy_(torch.randint(1000, 1050, (3, 1, S), generator=g).float() * 1e6)  # (an addition of under 1 is lost)
+    mask = c["mask"].cpu()
+    _, nxt = run_step(c, ints([[-1]] * 3), 11, 0.125, k=k)
+    assert torch.equal(nxt.cpu().view(3, 1, k), plain.chosen(c["weights"].cpu(), mask, 11, k, False).view(3, 1, k))
+    no_errors()
+
+
 def test_a_switch_that_changes_after_the_first_call(monkeypatch):
     """A plan that needs a larger workspace than the one a call of these sizes last had."""
     g = gen(10)
