@@ -18,6 +18,7 @@
 #include <stdlib.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/lf_decode.h"
 #include "lf_kernels.h"
@@ -348,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
     const int S = p.S;
     const int slot0 = blockIdx.x * p.chunk_slots;
     const int slots = min(p.chunk_slots, S - slot0);
-    allow_dependent_launch();
+    // (The join is not let in early: its CTAs, waiting, took the places of this
+    // kernel's next ones, 152 units of 2400 slots, d = 64, 18.9 us against 14.0.)
     grid_dependency_wait();
 
     int ws = p.write_slot[u];
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
     auto arrive = [&](int i, uint8_t* tile) {
         copy_wait<R::kStages - 2>();
         __syncwarp();
-        if (mine && i < tiles && static_cast<int>(s_tiles[warp][i].y) == wi / kTileSlots) {
+        if (mine && static_cast<int>(s_tiles[warp][i].y) == wi / kTileSlots) {
             const int row = wi % kTileSlots;
             if (lane < D / 32)
                 reinterpret_cast<uint4*>(tile + row * R::kKRow)[lane] = reinterpret_cast<const uint4*>(s_new[0])[lane];
@@ -651,8 +653,8 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
         arrive(0, tile);
         logits(tile);
     }
-#pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
+    // The weights and values of tile i, the next tile's logits beside them.
+    const auto step = [&](int i, auto last) {
         const uint32_t live = s_tiles[warp][i].x;
         uint32_t vs[NG / 2];  // of the lane's row
         shared_words<NG / 2>(tile + R::kVScaleOff + lane * R::kScaleRow, vs);
@@ -715,12 +717,15 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
         }
         l0 += (f[0] + f[2]) + (f[4] + f[6]);
         l1 += (f[1] + f[3]) + (f[5] + f[7]);
-        // The next tile's logits (of nothing behind the last one) beside this
-        // one's values: two chains of products to keep the pipes busy.
+        // Two chains of products to keep the pipes busy.
         const int next_stage = stage + 1 == R::kStages ? 0 : stage + 1;
         uint8_t* const next = ring + next_stage * R::kStage;
-        arrive(i + 1, next);
-        logits(next);
+        if constexpr (!last.value) {
+            arrive(i + 1, next);
+            logits(next);
+        } else {
+            __syncwarp();
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t vw[4][NG / 2];
@@ -750,12 +755,17 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
                 mma_f16_16816(off[g], eight, b0, b1, off[g]);
             }
         }
-        __syncwarp();
-        if (i + R::kStages < tiles) copy_tile(s_tiles[warp][i + R::kStages].y, stage);
-        copy_commit();
-        stage = next_stage;
-        tile = next;
-    }
+        if constexpr (!last.value) {
+            __syncwarp();
+            if (i + R::kStages < tiles) copy_tile(s_tiles[warp][i + R::kStages].y, stage);
+            copy_commit();
+            stage = next_stage;
+            tile = next;
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i + 1 < tiles; ++i) step(i, std::false_type());
+    if (tiles > 0) step(tiles - 1, std::true_type());
 
     // The four warps' states, joined (each warp's part of O over its ring).
     copy_wait<0>();
@@ -929,6 +939,10 @@ Kv4Plan kv4_plan(int units, int S, int sms) {
     const int fill = steps <= 4 ? 1 : std::max(1, 3 * sms / units);
     const int n = std::max((steps + longest - 1) / longest, std::min(steps, fill));
     const int per = (steps + n - 1) / n;
+    // One chunk too where an SM's three CTAs would do no less of a unit between them
+    // (152 units, d = 64, us: 1024 slots 7.8 in one chunk, 9.4 in three; 640 slots 6.2
+    // and 8.1 in three; 104 units of 1500 slots 9.7 in one and 9.2 in four).
+    if (steps <= longest && (units + sms - 1) / sms * steps <= 3 * per) return Kv4Plan{steps * 128, 1};
     return Kv4Plan{per * 128, (steps + per - 1) / per};
 }
 
