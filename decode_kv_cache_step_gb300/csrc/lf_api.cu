@@ -853,12 +853,12 @@ lf_status set_axes(lf::RopeParams* rp, const uint8_t* pair_axis, int axes, int r
     if (!pair_axis) return fail(LF_ERR_INVALID_ARG, "pair_axis is NULL");
     if (axes < 1 || axes > LF_MAX_AXES)
         return fail(LF_ERR_INVALID_ARG, "axes = %d is outside [1, %d]", axes, LF_MAX_AXES);
-    if (rot < 16 || rot / 2 > static_cast<int>(sizeof rp->pair_axis) || rot % 16 != 0)
+    if (rot < 16 || rot / 2 > 64 || rot % 16 != 0)
         return fail(LF_ERR_INVALID_ARG, "rot = %d must be a multiple of 16 in [16, d]", rot);
     for (int i = 0; i < rot / 2; ++i) {
         if (pair_axis[i] >= axes)
             return fail(LF_ERR_INVALID_ARG, "pair_axis[%d] = %d; there are %d axes", i, pair_axis[i], axes);
-        rp->pair_axis[i] = pair_axis[i];
+        rp->pair_axis[i / 16] |= static_cast<uint32_t>(pair_axis[i]) << (2 * (i % 16));
     }
     rp->axes = axes;
     return LF_OK;

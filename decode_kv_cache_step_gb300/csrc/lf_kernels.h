@@ -166,8 +166,8 @@ cudaError_t launch_score(int G, int score, const StepParams& p, int units, cudaS
 // last tokens of sequence b's kv_len[b] tokens: token i of the sequence has
 // position i (+ pos_offset[b]) and slot i, and mask gets the tokens' ages.
 // With axes, row t has a position on each of them, positions[a * T + t], for
-// its rotation, and pair i turns by that of axis pair_axis[i].
-constexpr int kMaxAxes = 4;
+// its rotation, and pair i turns by that of axis pair_axis(i).
+constexpr int kMaxAxes = 4;  // (two bits)
 struct RopeParams {
     const __nv_bfloat16* qkv;
     int64_t stride;                 // elements between rows
@@ -187,7 +187,7 @@ struct RopeParams {
     bool interleaved;
     float eps;
     int axes;                       // 0: one position per row
-    uint8_t pair_axis[64];          // [rot / 2]
+    uint32_t pair_axis[4];          // two bits for each of the rot / 2 pairs
 };
 cudaError_t launch_rope(int D, const RopeParams& p, int sms, cudaStream_t stream);
 

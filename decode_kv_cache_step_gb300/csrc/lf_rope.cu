@@ -21,6 +21,12 @@
 // caches 81 us, 6.2 TB/s read and written, 91% of the measured copy rate (2 us
 // more with loads marked evict-first); one token 2.9 us, 128 tokens 3.5 us, which is
 // the latency of a launch and three dependent round trips.
+//
+// With several position axes (kAxes) pair i turns by its axis' position: one more
+// word to load per token and axis, requested before the search for the token's
+// sequence. The same 20.3K tokens on three axes 82.4 us (85.4 with the load
+// behind the search and a byte per pair read from the parameters by each lane),
+// one token 2.9.
 #include <stdlib.h>
 
 #include <algorithm>
@@ -193,6 +199,9 @@ __global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
         const int i = tid >> 5;
         const int t = tok0 + i;
         TokenAt a{0, 0, 0};
+        // (Before the search, so that their round trips overlap.)
+        const bool axis = kAxes && (tid & 31) < p.axes;
+        const int axis_at = axis ? p.positions[static_cast<size_t>(tid & 31) * p.T + t] : 0;
         if (append) {
             a.b = warp_seq_of_row(p.q_start, p.B, t);
             SeqRange r;
@@ -206,18 +215,25 @@ __global__ void __launch_bounds__(kThreads, kRopeWarps * 32 / kThreads)
         } else if (!kAxes) {
             a.pos = p.positions[t];
         }
-        if (kAxes && (tid & 31) < p.axes)
-            axis_pos[i][tid & 31] = p.positions[static_cast<size_t>(tid & 31) * p.T + t];
+        if (axis) axis_pos[i][tid & 31] = axis_at;
         if ((tid & 31) == 0) at[i] = a;
     }
     __syncthreads();
     for (int i = tid; i < ntok * half; i += kThreads) {
         const int kk = i / half;
-        const int pos = kAxes ? axis_pos[kk][p.pair_axis[i - kk * half]] : at[kk].pos;
-        const float t = turns(pos, __ldg(p.inv_freq + (i - kk * half)));
+        const int pair = i - kk * half;
+        int pos = at[kk].pos;
+        if constexpr (kAxes) {
+            // (Selected, not indexed: lanes that read different words of the
+            // parameters do so one after another.)
+            const uint32_t lo = pair & 16 ? p.pair_axis[1] : p.pair_axis[0];
+            const uint32_t hi = pair & 16 ? p.pair_axis[3] : p.pair_axis[2];
+            pos = axis_pos[kk][((pair & 32 ? hi : lo) >> (2 * (pair & 15))) & 3u];
+        }
+        const float t = turns(pos, __ldg(p.inv_freq + pair));
         float s, c;
         sincospif(2.f * t, &s, &c);
-        cs[kk][i - kk * half] = make_float2(c, s);
+        cs[kk][pair] = make_float2(c, s);
     }
     __syncthreads();
     if (!active) return;
