@@ -370,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mma_commit(&s_full[kTurns * h + s]);
                 }
-                if (ok) mma_commit(&empty[st]);
             }
             if (!ok) give_up();
             // No product may be in flight when tensor memory is freed.
@@ -440,6 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = s; n < tiles; n += kTurns) {
             if (!(ok = arrived(&s_full[kTurns * h + s], (n / kTurns) & 1))) break;
             tc_fence_after();
+            // (The streamed tile's products are done.)
+            if (h == w.held - 1 && (warp & 3) == 0 && lane == 0) mbar_arrive(&empty[n % L::kRing]);
             if (kForm == kRowsPass) {
                 // A thread owns the row of token w.at + h * tok + at / g, head at % g.
                 const int t0 = w.at + h * tok;
