@@ -12,22 +12,24 @@
 //            weights in registers, in a fixed order. A CTA holds tiles of 128 keys
 //            and streams the query tiles that see them; where no sequence has more
 //            rows than one tile, it holds that tile and streams the keys.
-// Neither pass writes a score. One thread issues the tensor products (a held tile
-// times the streamed one) into four accumulators in tensor memory, all of it, and
+// Neither pass writes a score. One thread, or two, issues the tensor products (a held
+// tile times the streamed one) into four accumulators in tensor memory, all of it, and
 // TMA loads run ahead through a ring. Four warps read an accumulator, each thread
 // its lane's 128 scores, so sixteen of the SM's warps hide one another's waits.
 // Large calls hold two tiles per CTA (a streamed tile then serves 256 rows) and
 // have two accumulators for each; few rows hold one, and its accumulators take
 // every fourth tile.
 //
-// What bounds it: per tile of scores some 680 cycles of products and 512 of
-// exponentials, twice each, while either overlaps the other only as far as four
-// accumulators go. Measured (32 query, 8 KV heads of 128): every row of 8192
-// tokens 459 us, some 215 and 245 a pass, 599 TFLOP/s of the two passes' products on
-// average and 55% of either unit's cycles; the last 32 rows of 8 prompts of 2000 to
-// 8192 tokens 44.5 us, two passes over 105 MB of keys (the second from L2 in
-// part), where a CTA's start and the few tiles it streams take the most. (A third
-// of the exponentials as polynomials: slower, the units are not what is full.)
+// What bounds it: the score warps. A tile of scores is 512 cycles of products, as
+// many of exponentials, and some 470 instructions for each of the SM's schedulers;
+// alone the products would take 341 us of the 430 below, the rest alone 420. (Streamed
+// tiles of 256 rows, with less to read for the products: 467. Eight score warps with
+// two accumulators each: 500. A third of the exponentials as polynomials: slower.
+// Waits that poll: the same.) Measured (32 query, 8 KV heads of 128): every row of
+// 8192 tokens 430 us, some 205 and 225 a pass, 640 TFLOP/s of both passes'
+// products; the last 32 rows of 8 prompts of 2000 to 8192 tokens 40.7 us, two
+// passes over 113 MB of keys (the second from L2 in part), where a CTA's start and
+// the few tiles it streams take the most.
 #include <math.h>
 #include <stdlib.h>
 
@@ -50,19 +52,27 @@ constexpr int kColumnsPass = 1;  // keys held
 constexpr int kFewRows = 2;      // the columns pass with the one tile of rows held
 
 constexpr int kScoreWarps = 16;
-constexpr int kThreads = kScoreWarps * 32 + 64;
 constexpr uint32_t kTmemCols = 4 * kRows;
 
 template <int D, int kHeld>
 struct WeightsSmem {
     static constexpr int kTurns = 4 / kHeld;  // accumulators of a held tile
-    static constexpr int kRing = D == 64 ? 8 : kHeld == 2 ? 4 : 5;  // streamed tiles
+    // Warps that issue products, behind the loads' warp: a streamed tile's waits,
+    // issue and commits take one warp longer than the products with one held tile
+    // (last 32 rows of 8 prompts: 42.9 us with one, 41.0 with two), not with two
+    // (8192 tokens: 443 and 453).
+    static constexpr int kIssuers = kHeld == 2 ? 1 : 2;
+    static constexpr int kThreads = (kScoreWarps + 1 + kIssuers) * 32;
+    static constexpr int kRing = D == 64 ? 8 : 4;  // streamed tiles
+    // An issuer sees every use of the slots it waits for: it could not tell one
+    // round of a barrier from the one after the next.
+    static_assert(kRing % kIssuers == 0, "a slot's tiles have one issuer");
     static constexpr int kTileBytes = kRows * D * 2;
     static constexpr int kRingOff = kHeld * kTileBytes;
     static constexpr int kBarOff = kRingOff + kRing * kTileBytes;
     // barriers: held, full[], empty[], stat_full[], stat_free[], s_full[], s_free[],
-    // drain
-    static constexpr int kBars = 2 + 4 * kRing + 8;
+    // drain[]
+    static constexpr int kBars = 1 + 4 * kRing + 8 + kIssuers;
     static constexpr int kMiscOff = kBarOff + kBars * 8;
     static constexpr int kStatOff = (kMiscOff + 16 + 15) / 16 * 16;  // -r of the ring's rows
     static constexpr int kOtherOff = kStatOff + kRing * kRows * 4;  // the other turns' results
@@ -176,12 +186,14 @@ __device__ __forceinline__ bool keys_work(const PromptWeightsParams& p, int tok,
 }
 
 template <int D, int kForm, int kHeld>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(WeightsSmem<D, kHeld>::kThreads, 1)
     lf_prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ,
                              const __grid_constant__ CUtensorMap tmK,
                              const __grid_constant__ PromptWeightsParams p) {
     using L = WeightsSmem<D, kHeld>;
     constexpr int kTurns = L::kTurns;
+    constexpr int kIssuers = L::kIssuers;
+    constexpr int kThreads = L::kThreads;
     constexpr bool kKeysHeld = kForm == kColumnsPass;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -231,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(held, 1);
         for (int s = 0; s < L::kRing; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], w.held);
             mbar_init(&stat_full[s], 1);
             mbar_init(&stat_free[s], 4 * w.held);
         }
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_full[s], 1);
             mbar_init(&s_free[s], 4);
         }
-        mbar_init(drain, 1);
+        for (int i = 0; i < kIssuers; ++i) mbar_init(&drain[i], 1);
         fence_barrier_init();
     }
     tc_fence_before();
@@ -344,14 +356,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = max(0, n - L::kRing); k < n; ++k) mbar_wait(&full[k % L::kRing], (k / L::kRing) & 1);
         }
         __syncwarp();
-    } else if (warp == kScoreWarps + 1) {
+    } else if (warp > kScoreWarps) {
         if (tiles > 0 && elect_one()) {
             // -------------------------------------------------- products --
             // The accumulators' lanes are the keys, but for the rows pass: the
             // streamed tile is the first operand where the rows are held.
             const uint32_t idesc = instr_desc(kRows, kRows, false) | (p.negate ? kInstrNegateA : 0u);
+            const int issuer = warp - kScoreWarps - 1;
             bool ok = mbar_wait(held, 0, p.wait_limit_ns);
-            for (int n = 0; ok && n < tiles; ++n) {
+            for (int n = issuer; ok && n < tiles; n += kIssuers) {
                 const int st = n % L::kRing, s = n % kTurns;
                 ok = mbar_wait(&full[st], (n / L::kRing) & 1, p.wait_limit_ns);
                 if (!ok) break;
@@ -373,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) give_up();
             // No product may be in flight when tensor memory is freed.
-            mma_commit(drain);
-            mbar_wait(drain, 0);
+            mma_commit(&drain[issuer]);
+            mbar_wait(&drain[issuer], 0);
         }
         __syncwarp();
     } else if ((warp >> 2) % kHeld < w.held) {
@@ -407,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A key's weights of a tile's rows; columns [lo, hi) see it.
         const auto column_sum = [&](const float* minus, bool some, int lo, int hi) {
             float total = 0.f;
-#pragma unroll 1
+            // (Both halves' code, 20 us less of 450 for 8192 tokens; a few rows spill.)
+#pragma unroll(kForm == kColumnsPass ? 2 : 1)
             for (int half = 0; half < 2; ++half) {
                 uint32_t x[64];
                 take(half, x);
@@ -439,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = s; n < tiles; n += kTurns) {
             if (!(ok = arrived(&s_full[kTurns * h + s], (n / kTurns) & 1))) break;
             tc_fence_after();
-            // (The streamed tile's products are done.)
-            if (h == w.held - 1 && (warp & 3) == 0 && lane == 0) mbar_arrive(&empty[n % L::kRing]);
+            // (The streamed tile's products with this held one are done.)
+            if ((warp & 3) == 0 && lane == 0) mbar_arrive(&empty[n % L::kRing]);
             if (kForm == kRowsPass) {
                 // A thread owns the row of token w.at + h * tok + at / g, head at % g.
                 const int t0 = w.at + h * tok;
@@ -566,7 +580,7 @@ cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmK, const Pr
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = L::kAlloc;
     cfg.stream = stream;
     cfg.attrs = attr;
