@@ -360,6 +360,27 @@ def test_prompt_weights_are_the_same_bits_again(rows):
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
 
 
+@pytest.mark.parametrize("d,rows", [(128, 32), (64, 32), (128, 1), (128, 200)])
+def test_prompt_weights_of_few_rows_over_long_prompts(d, rows):
+    """Long streams past few rows, calls back to back: the same bits, and every row gives one."""
+    g = gen(17)
+    lens = [8192, 5000, 7001, 8000, 6144, 300, 8191, 4097]
+    q, k = normal(g, 8 * rows, 32, d), normal(g, 8, 8, 8192, d)
+    starts, kv = ints([rows * b for b in range(9)]), ints(lens)
+    got = []
+    for _ in range(12):
+        w = torch.zeros(8, 8, 8192, device="cuda")
+        lf.prompt_weights(q, k, starts, kv, w, d ** -0.5, rows=rows)
+        got.append(w)
+    assert all(torch.equal(got[0], w) for w in got[1:])
+    # Rounding, of a weight's own size: its row's sum, some 70 additions one after another,
+    # 2^-18; the logarithm, the argument (below 16) and the exponential 2^-20 each.
+    assert (got[0].double().sum(2) - 4 * rows).abs().max() <= 4 * rows * 2.0 ** -17
+    for b, n in enumerate(lens):
+        assert (got[0][b, :, n:] == 0).all()
+    no_errors()
+
+
 @pytest.mark.parametrize("T,rows", [(900, 0), (900, 10)])
 def test_prompt_weights_waits_that_run_out(monkeypatch, T, rows):
     """Waits with no time left end the call with an error, and the next call is right."""
