@@ -271,7 +271,7 @@ constexpr int kSplitMinSlots = 8192;
 constexpr int kDefaultClusterChunks = 16;
 
 // Whether a step scores in a second kernel, and from which unit on (allowed:
-// a top-1 step without a cluster merge).
+// a top-1 step, or one ranked by weights, without a cluster merge).
 void plan_split_finish(Plan* pl, int S, int units, int sms, bool allowed) {
     // Top-1 steps over long units without clusters score in a second kernel:
     // the last CTA's scan of every slot would otherwise run on the step's

@@ -55,7 +55,7 @@ struct StepParams {
     float* stash;                // [units][S][G]          log2(exp(s) * ||v||_1) per live slot
     uint32_t* arrivals;          // [units] chunk arrival counters, 0 between steps
     uint32_t* dev_err;           // LF_DEVERR_* bits
-    // Split finish (top-1 only): the last CTA publishes c_h = log2(1/l_h) - m_h
+    // Split finish (top-1, or score 2): the last CTA publishes c_h = log2(1/l_h) - m_h
     // and raises the unit's ready flag; a second kernel scores the unit's
     // chunks in parallel as soon as the flag is up.
     float* cfold = nullptr;                // [units][G]

@@ -36,7 +36,7 @@
 // the lexicographic (I_j, j) argmin over slots with age >= W, or, for k > 1,
 // the k smallest by an 8-bit radix select on the score keys (then on the slot
 // index among equal scores) and a bitonic sort of the k winners (kWeights: by a
-// kernel of its own, lf_select_kernel); the periodic
+// kernel of its own behind the step); the periodic
 // k-at-once compression of the Fig. 3 caption. Candidates are compared by an
 // order-preserving key of log2 I_j, so slots whose scores lie far below
 // fp32's normal range (weights hundreds of nats under the unit's maximum)
@@ -53,7 +53,8 @@
 // CTAs push their merged states into one another's shared memory with
 // asynchronous remote stores counted on mbarriers (cluster_merge_push), each
 // writes the part of the output row it owns and scores its own chunk, and
-// rank 0 reduces the argmin (top-1 only). A cluster grid of at most one CTA
+// rank 0 reduces the argmin (top-1 only; kWeights with several slots leaves the
+// keys to lf_select_few_kernel or lf_select_kernel). A cluster grid of at most one CTA
 // per SM uses a kDeepStages-deep TMA ring, so every tile of a short chunk is
 // in flight at once.
 // An attention-only instantiation (kScore = kNoScore) drops the row norms, the

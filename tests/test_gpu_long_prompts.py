@@ -234,7 +234,8 @@ def test_several_slots_with_equal_weights(S, k):
     no_errors()
 
 
-@pytest.mark.parametrize("env", [{}, {"LF_CLUSTER": "0", "LF_SPLIT": "0"}, {"LF_CLUSTER": "0", "LF_SPLIT": "1"}])
+@pytest.mark.parametrize("env", [{}, {"LF_CLUSTER": "0", "LF_SPLIT": "0"}, {"LF_CLUSTER": "0", "LF_SPLIT": "1"},
+                                 {"LF_CLUSTER": "0", "LF_SPLIT": "1", "LF_SPLIT_TAIL": "1"}])
 @pytest.mark.parametrize("S,k", [(16384, 3), (16385, 8), (40000, 1), (40000, 7), (40000, 9), (70001, 6), (70001, 400),
                                  (100, 8)])
 def test_several_slots_of_long_caches(monkeypatch, env, S, k):
