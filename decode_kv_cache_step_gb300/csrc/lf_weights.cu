@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(WeightsSmem<D, kHeld>::kThreads, 1)
     const auto joined = [&](int t, int column) {
         const float2* src = stat_at(t, column);
         float2 sum = __ldcg(src);
-        if (p.pieces > 1) {
+        if (!kKeysHeld && p.pieces > 1) {
             const int pieces = row_pieces(p, kHeld * tok, w.r, t);
             float m = sum.x;
             for (int k = 1; k < pieces; ++k) m = fmaxf(m, __ldcg(src + k * piece).x);
@@ -558,6 +558,55 @@ __global__ void __launch_bounds__(WeightsSmem<D, kHeld>::kThreads, 1)
     }
 }
 
+// The rows' pieces joined in place of the first, for the columns pass, which reads
+// them for every tile of keys (where it joins two of them itself, 1024 tokens take 48
+// us instead of 29). Few rows are read once, by the threads that join them.
+constexpr int kMaxPieces = 16;
+constexpr int kJoinTiles = 6;  // tiles that take as long as the join
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) lf_join_statistics_kernel(const PromptWeightsParams p, int span) {
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+    const int row = static_cast<int>(i / p.Hq);
+    if (row >= p.stat_rows) return;
+    const int b = p.by_sequence ? row / p.rows : seq_of_row(p.q_start, p.B, row);
+    SeqRange r;
+    if (!seq_range(p.q_start, p.kv_len, b, p.T, p.S, true, &r)) return;
+    const int t = p.by_sequence ? first_row(p, r) + row % p.rows : row - r.q0;
+    if (t < first_row(p, r) || t >= r.n) return;
+    const int pieces = row_pieces(p, span, r, t);
+    if (pieces == 1) return;
+    const size_t piece = static_cast<size_t>(p.stat_rows) * p.Hq;
+    float2 v[kMaxPieces];
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxPieces; ++k) {
+        v[k] = k < pieces ? __ldcg(p.stats + k * piece + i) : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, v[k].x);
+    }
+    if (m == -INFINITY) m = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxPieces; ++k)
+        if (k < pieces) l += v[k].y * exp2f(v[k].x - m);
+    p.stats[i] = make_float2(m, l);
+}
+
+cudaError_t launch_join(const PromptWeightsParams& p, cudaStream_t stream) {
+    const char* env = std::getenv("LF_PDL");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t n = static_cast<int64_t>(p.stat_rows) * p.Hq;
+    cfg.gridDim = dim3(static_cast<unsigned>((n + kJoinThreads - 1) / kJoinThreads));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = (env && std::atoi(env) == 0) ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, lf_join_statistics_kernel, p, 2 * kRows / (p.Hq / p.Hkv));
+}
+
 template <int D, int kForm, int kHeld>
 cudaError_t launch_pass(const CUtensorMap& tmQ, const CUtensorMap& tmK, const PromptWeightsParams& p,
                         dim3 grid, int cluster, cudaStream_t stream) {
@@ -596,7 +645,8 @@ cudaError_t launch_d(const CUtensorMap& tmQ, const CUtensorMap& tmK, const Promp
         const cudaError_t e = launch_pass<D, kRowsPass, 1>(tmQ, tmK, p, rows, 1, stream);
         return e != cudaSuccess ? e : launch_pass<D, kFewRows, 1>(tmQ, tmK, p, rows, 1, stream);
     }
-    const cudaError_t e = launch_pass<D, kRowsPass, 2>(tmQ, tmK, p, rows, 1, stream);
+    cudaError_t e = launch_pass<D, kRowsPass, 2>(tmQ, tmK, p, rows, 1, stream);
+    if (e == cudaSuccess && p.pieces > 1) e = launch_join(p, stream);
     if (e != cudaSuccess) return e;
     const int tiles = (p.S + 2 * kRows - 1) / (2 * kRows);
     return launch_pass<D, kColumnsPass, 2>(tmQ, tmK, p, dim3(tiles * p.B * p.Hkv * p.share), p.share, stream);
@@ -616,22 +666,37 @@ void plan_prompt_weights(PromptWeightsParams* p, int sms) {
     p->by_sequence = p->rows > 0 && each * p->B <= packed && static_cast<int64_t>(p->rows) * p->B < p->T;
     p->items = static_cast<int>(p->by_sequence ? each * p->B : packed);
     p->stat_rows = p->by_sequence ? p->rows * p->B : p->T;
-    // Pieces of the keys when the items that hold rows leave SMs idle: of so many
-    // tiles that full caches are one wave of CTAs, whose start takes as long as
-    // several tiles (64 items of 2000 to 8192 keys, 27 tiles a piece 47 us for
-    // both passes, 18: 62, 14: 56, 9: 66).
+    // Pieces of the keys, 16 at most, when the items that hold rows leave SMs idle. Few
+    // rows: of so many tiles that full caches are one wave of CTAs, whose start takes
+    // as long as several tiles (64 items of 2000 to 8192 keys, 27 tiles a piece 47 us
+    // for both passes, 18: 62, 14: 56, 9: 66). Else only where a wave holds two pieces
+    // of all items or more, and if they save more than the join's launch.
     const int64_t rows = p->rows > 0 ? std::min<int64_t>(p->T, static_cast<int64_t>(p->rows) * p->B) : p->T;
     const int64_t busy = std::max<int64_t>(1, (rows + span - 1) / span) * p->Hkv;
     const int64_t tiles = (p->S + kRows - 1) / kRows;
-    const int64_t least = std::max<int64_t>((tiles + 15) / 16, (tiles * busy + sms - 1) / sms);
-    p->piece_tiles = static_cast<int>(std::min(tiles, least));
-    p->pieces = static_cast<int>((tiles + p->piece_tiles - 1) / p->piece_tiles);
-    // CTAs that share tiles of keys, where there are few tiles (with one CTA each
-    // for 256 tiles, or two, 8192 tokens took 467 us; with four 502).
+    const int64_t least = (tiles + kMaxPieces - 1) / kMaxPieces;
+    int64_t per = tiles;
+    if (few)
+        per = std::min(tiles, std::max(least, (tiles * busy + sms - 1) / sms));
+    else if (busy * 2 <= sms)
+        per = std::max(least, (tiles + sms / busy - 1) / (sms / busy));
+    if (!few && tiles - per < kJoinTiles) per = tiles;
+    p->piece_tiles = static_cast<int>(per);
+    p->pieces = static_cast<int>((tiles + per - 1) / per);
+    // CTAs that share two held tiles of keys, a cluster: the first keys are seen by
+    // every row, the last by few, so a call takes at least as long as its first tiles
+    // unless those are shared; but a start takes as long as several tiles, and larger
+    // clusters leave SMs of their group idle. (us, shared by 1, 2, 4, 8; pairs of tiles:
+    // 256 (8192 tokens, 8 KV heads) 432, 430, 472, 600; 192: 287, 257, 278, 356; 96: 130,
+    // 91, 97, 128; 80: 357, 231, 190, 233; 64: 86, 60, 56, 78; 32: 110, 69, 49, 63; 16:
+    // 217, 121, 75, 54.)
+    const int64_t pairs = (tiles + 1) / 2 * p->B * p->Hkv;
+    const int64_t most_pairs[] = {sms * 4 / 3, sms * 4 / 7, sms / 6};
     p->share = few ? 0 : 1;
-    while (p->share > 0 && p->share < kMaxShare && static_cast<int64_t>(p->share) * tok * 2 < most &&
-           (tiles + 1) / 2 * p->B * p->Hkv * p->share < sms)
+    for (int i = 0; i < 3 && p->share > 0 && pairs <= most_pairs[i]; ++i) {
+        if (static_cast<int64_t>(p->share) * tok * 2 >= most) break;
         p->share *= 2;
+    }
 }
 
 cudaError_t launch_prompt_weights(int D, const CUtensorMap& tmQ, const CUtensorMap& tmK,

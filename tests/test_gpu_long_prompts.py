@@ -349,6 +349,23 @@ def test_prompt_weights(nq, kv, S, rows, Hq, Hkv, d):
     no_errors()
 
 
+@pytest.mark.parametrize("nq,kv,rows", [([150], [3000], 0), ([150, 0, 90], [3000, 5, 2000], 0), ([400, 300], [3000, 2500], 150),
+                                        ([70], [1500], 65), ([130, 1], [2900, 2900], 129)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 128), (2, 2, 64), (8, 1, 64)])
+def test_prompt_weights_of_rows_in_pieces(nq, kv, rows, Hq, Hkv, d):
+    """More rows than a tile, few enough that their keys are cut into pieces."""
+    g = gen(sum(kv))
+    B, T, S = len(nq), sum(nq) + 1, 3100
+    starts = [sum(nq[:i]) for i in range(B + 1)]
+    q, k = normal(g, T, Hq, d), normal(g, B, Hkv, S, d)
+    q[sum(nq):] = NAN
+    w = torch.zeros(B, Hkv, S, device="cuda")
+    lf.prompt_weights(q, k, ints(starts), ints(kv), w, d ** -0.5, rows=rows)
+    ref, tol = plain.prompt_weights(q, k, starts, kv, torch.zeros(B, Hkv, S), rows, d ** -0.5)
+    near(w, ref, tol)
+    no_errors()
+
+
 @pytest.mark.parametrize("rows", [0, 20])
 def test_prompt_weights_are_the_same_bits_again(rows):
     g = gen(3)
