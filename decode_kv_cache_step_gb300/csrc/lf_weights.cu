@@ -687,14 +687,15 @@ void plan_prompt_weights(PromptWeightsParams* p, int sms) {
     // every row, the last by few, so a call takes at least as long as its first tiles
     // unless those are shared; but a start takes as long as several tiles, and larger
     // clusters leave SMs of their group idle. (us, shared by 1, 2, 4, 8; pairs of tiles:
-    // 256 (8192 tokens, 8 KV heads) 432, 430, 472, 600; 192: 287, 257, 278, 356; 96: 130,
-    // 91, 97, 128; 80: 357, 231, 190, 233; 64: 86, 60, 56, 78; 32: 110, 69, 49, 63; 16:
-    // 217, 121, 75, 54.)
+    // 256 (8192 tokens, 8 KV heads) 430, 429, 469, 595; 192: 287, 257, 276, 353; 96: 130,
+    // 91, 96, 126; 80: 351, 225, 197, 229; 64: 86, 60, 55, 76; 32: 48, 35, 29, 37; 16:
+    // 75, 49, 36, 27 with 63 tiles of rows, 31, 25, 20, 22 with 16.)
     const int64_t pairs = (tiles + 1) / 2 * p->B * p->Hkv;
     const int64_t most_pairs[] = {sms * 4 / 3, sms * 4 / 7, sms / 6};
+    const int least_rows[] = {2, 4, 32};  // tiles of a sequence's rows
     p->share = few ? 0 : 1;
-    for (int i = 0; i < 3 && p->share > 0 && pairs <= most_pairs[i]; ++i) {
-        if (static_cast<int64_t>(p->share) * tok * 2 >= most) break;
+    for (int i = 0; i < 3 && p->share > 0; ++i) {
+        if (pairs > most_pairs[i] || most <= static_cast<int64_t>(least_rows[i]) * tok) break;
         p->share *= 2;
     }
 }
