@@ -668,18 +668,20 @@ void plan_prompt_weights(PromptWeightsParams* p, int sms) {
     p->stat_rows = p->by_sequence ? p->rows * p->B : p->T;
     // Pieces of the keys, 16 at most, when the items that hold rows leave SMs idle. Few
     // rows: of so many tiles that full caches are one wave of CTAs, whose start takes
-    // as long as several tiles (64 items of 2000 to 8192 keys, 27 tiles a piece 47 us
-    // for both passes, 18: 62, 14: 56, 9: 66). Else only where a wave holds two pieces
-    // of all items or more, and if they save more than the join's launch.
+    // as long as several tiles (64 items of 2000 to 8192 keys, us of both passes, 27
+    // tiles a piece 33, 22: 29, 16: 33, 11: 36, 8: 41, 32: 36); exactly where there are
+    // few items (16 of 8192 keys: 8 tiles, 128 CTAs, 17; 7 tiles, 160 CTAs, 22), while
+    // with many the ragged ends of a second wave fit in. More rows: only where a wave
+    // holds two pieces of all items, and if they save more than the join's launch.
     const int64_t rows = p->rows > 0 ? std::min<int64_t>(p->T, static_cast<int64_t>(p->rows) * p->B) : p->T;
     const int64_t busy = std::max<int64_t>(1, (rows + span - 1) / span) * p->Hkv;
     const int64_t tiles = (p->S + kRows - 1) / kRows;
     const int64_t least = (tiles + kMaxPieces - 1) / kMaxPieces;
     int64_t per = tiles;
-    if (few)
-        per = std::min(tiles, std::max(least, (tiles * busy + sms - 1) / sms));
-    else if (busy * 2 <= sms)
+    if (busy * (few ? 5 : 2) <= sms)
         per = std::max(least, (tiles + sms / busy - 1) / (sms / busy));
+    else if (few)
+        per = std::min(tiles, std::max(least, (tiles * busy + sms - 1) / sms));
     if (!few && tiles - per < kJoinTiles) per = tiles;
     p->piece_tiles = static_cast<int>(per);
     p->pieces = static_cast<int>((tiles + per - 1) / per);
