@@ -794,6 +794,49 @@ def test_two_graphs_at_once():
     no_errors()
 
 
+@pytest.mark.parametrize("rows,T", [(0, 150), (120, 400), (20, 400), (0, 1500)])
+def test_a_captured_call_sees_new_inputs_and_lengths(rows, T):
+    """Every form of a prompt's weights, and steps that return several slots: a replay reads what
+    lies in the tensors then."""
+    g = gen(23 + T)
+    S = 3000
+    q, k = normal(g, T, 4, 128), normal(g, 2, 1, S, 128)
+    starts, lens = ints([0, T - 40, T]), ints([S, 900])
+    w = torch.zeros(2, 1, S, device="cuda")
+    c = step_case(g, 2, 4, 1, 128, S)
+    ws = torch.full((2, 1), -1, dtype=torch.int32, device="cuda")
+    few, many = (torch.full((2, 1, n), -9, dtype=torch.int32, device="cuda") for n in (3, 20))
+    out = torch.empty_like(c["q"])
+
+    def calls():
+        lf.prompt_weights(q, k, starts, lens, w, 0.1, rows=rows)
+        for nxt in (few, many):
+            lf.decode_step_weights(c["q"], c["k"], c["v"], c["mask"], c["weights"], c["nk"], c["nv"], ws, out, nxt,
+                                   4, 0.1, decay=0.5, k=nxt.shape[2])
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    state = (q, lens, w, c["weights"], c["q"])
+    for n in (S, 1700):
+        q.copy_(normal(g, T, 4, 128))
+        c["q"].copy_(normal(g, 2, 4, 128))
+        lens.copy_(ints([n, n // 2 if T < 1500 else 1500]))
+        w.zero_()
+        before = [t.clone() for t in state]
+        graph.replay()
+        got = [t.clone() for t in (w, few, many, out, c["weights"])]
+        for t, old in zip(state, before):
+            t.copy_(old)
+        calls()
+        # (Bits: what masked slots hold is NaN.)
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+                   for x, y in zip(got, (w, few, many, out, c["weights"])))
+    no_errors()
+
+
 # ------------------------------------------------------------------- together --
 
 def test_a_long_prompt_then_tokens():
