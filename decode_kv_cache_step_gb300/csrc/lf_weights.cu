@@ -420,6 +420,27 @@ __global__ void __launch_bounds__(WeightsSmem<D, kHeld>::kThreads, 1)
         // A key's weights of a tile's rows; columns [lo, hi) see it.
         const auto column_sum = [&](const float* minus, bool some, int lo, int hi) {
             float total = 0.f;
+            // A masked logit of -infinity and a row's statistic that is NaN give NaN: where
+            // such a row lies in a tile that not all its keys see, columns are left out instead.
+            // (The test costs nothing: 8192 tokens 430 us with it and without.)
+            const float4 v = some ? reinterpret_cast<const float4*>(minus)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (some && __any_sync(0xffffffffu, isnan(v.x) || isnan(v.y) || isnan(v.z) || isnan(v.w))) {
+#pragma unroll 1
+                for (int e0 = 0; e0 < kRows; e0 += 16) {
+                    uint32_t x[16];
+                    tmem_ld16(ts + e0, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float w = ex2_approx(fmaf(__uint_as_float(x[e]), c1, minus[e0 + e]));
+                        total += e0 + e >= lo && e0 + e < hi ? w : 0.f;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free[kTurns * h + s]);
+                return total;
+            }
             // (Both halves' code, 20 us less of 450 for 8192 tokens; a few rows spill.)
 #pragma unroll(kForm == kColumnsPass ? 2 : 1)
             for (int half = 0; half < 2; ++half) {

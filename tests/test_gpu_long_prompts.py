@@ -881,3 +881,31 @@ def test_a_long_prompt_then_tokens():
         c4.update(q=q, nk=nk, nv=nv)
         check_kv4(c4, torch.full_like(ws, S + t), scale)
     no_errors()
+
+
+# ------------------------------------------- logits that are not finite numbers --
+
+@pytest.mark.parametrize("nq,kv,S,rows", [
+    ([20], [20], 24, 0), ([40, 7], [130, 7], 140, 32), ([300], [300], 300, 0), ([200, 150], [450, 150], 512, 0),
+    ([1100], [1100], 1100, 0), ([700, 60], [700, 900], 1000, 600)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 128), (2, 2, 64), (8, 1, 64)])
+@pytest.mark.parametrize("what", [NAN, INF])
+def test_prompt_weights_of_rows_that_are_not_finite(nq, kv, S, rows, Hq, Hkv, d, what):
+    """A counted row whose softmax is NaN gives NaN to the keys that it sees and nothing to the others."""
+    g = gen(S + Hq)
+    B, T = len(nq), sum(nq)
+    starts = [sum(nq[:i]) for i in range(B + 1)]
+    q, k = normal(g, T, Hq, d), normal(g, B, Hkv, S, d)
+    for b in range(B):
+        k[b, :, kv[b]:] = NAN
+    at = starts[1] - 1 - min(nq[0], rows or nq[0]) // 3  # a counted row of the first sequence
+    q[at, Hq - 1] = what
+    w = torch.zeros(B, Hkv, S, device="cuda")
+    lf.prompt_weights(q, k, ints(starts), ints(kv), w, d ** -0.5, rows=rows)
+    ref, tol = plain.prompt_weights(q, k, starts, kv, torch.zeros(B, Hkv, S), rows, d ** -0.5)
+    seen = kv[0] - nq[0] + at + 1
+    assert torch.isnan(ref[0, -1, :seen]).all() and not torch.isnan(ref[0, -1, seen:]).any()
+    assert torch.equal(torch.isnan(w).cpu(), torch.isnan(ref))
+    fine = ~torch.isnan(ref)
+    near(w.cpu()[fine], ref[fine], tol[fine])
+    no_errors()
