@@ -259,6 +259,26 @@ __device__ __forceinline__ float add_weight(const StepParams& p, float old, bool
     return kept + linear_score<G>(t, c) + 0.f;
 }
 
+// The larger logit. By the accumulated weight a NaN stays, so that the head's sum is
+// NaN too: with fmaxf a NaN beside logits of -infinity alone would leave the maximum of
+// a part without a live slot, which is skipped.
+template <int kScore>
+__device__ __forceinline__ float logit_max(float a, float b) {
+    if constexpr (kScore != kWeights) return fmaxf(a, b);
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// 1 / l, 0 for a head without a weight. By the accumulated weight a NaN sum stays, as in
+// the definition, and with it the head's output and weights; the other instances
+// count it as no weight.
+template <int kScore>
+__device__ __forceinline__ float inverse_sum(float l) {
+    if constexpr (kScore == kWeights) return l == 0.f ? 0.f : 1.f / l;
+    return (l > 0.f) ? 1.f / l : 0.f;
+}
+
 // c_h = log2(1 / l_h) - m_h: what turns a score term into the weight's log2. A
 // head without any finite logit has no weight to add.
 template <int kScore>
@@ -619,7 +639,7 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
             if constexpr (kPrefix) {
                 if (s_pre[tid].y != 0.f) l += s_pre[tid].y * exp2f(s_pre[tid].x - m);
             }
-            const float il = (l > 0.f) ? 1.f / l : 0.f;
+            const float il = inverse_sum<kScore>(l);
             s_m[tid] = m;
             s_il[tid] = il;
 #pragma unroll
@@ -643,7 +663,7 @@ __device__ void finish_unit(const StepParams& p, int u, uint8_t* smem, int usabl
                 if (s_pre[tid].y != 0.f) l += s_pre[tid].y * exp2f(s_pre[tid].x - m);
             }
             s_m[tid] = m;
-            s_il[tid] = (l > 0.f) ? 1.f / l : 0.f;
+            s_il[tid] = inverse_sum<kScore>(l);
         }
     }
     if (kScore && ptl) {
@@ -1326,7 +1346,7 @@ __device__ __forceinline__ void cluster_merge_push(const StepParams& p, int u, i
         const int h = tid - c * G;
         float mh = NEG, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kConsumerWarps; ++w) mh = fmaxf(mh, wm[w * G + h]);
+        for (int w = 0; w < kConsumerWarps; ++w) mh = logit_max<kScore>(mh, wm[w * G + h]);
 #pragma unroll
         for (int w = 0; w < kConsumerWarps; ++w) {
             const float mw = wm[w * G + h];
@@ -1347,7 +1367,7 @@ __device__ __forceinline__ void cluster_merge_push(const StepParams& p, int u, i
 #pragma unroll
         for (int w = 0; w < kConsumerWarps; ++w) {
             mw[w] = wm[w * G + h];
-            mh = fmaxf(mh, mw[w]);
+            mh = logit_max<kScore>(mh, mw[w]);
         }
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1390,7 +1410,7 @@ __device__ __forceinline__ void cluster_merge_push(const StepParams& p, int u, i
         float l = a.y * ea;
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        const float il = (l > 0.f) ? 1.f / l : 0.f;
+        const float il = inverse_sum<kScore>(l);
         if (lane < nchunk) s_w[lane * G + h] = ea * il;
         if (lane == 0) {
             s_m[h] = m;
@@ -1868,15 +1888,15 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
         }
 
         // Online softmax per head (columns h0, h0+1), across the warp's rows.
-        float mx0 = fmaxf(x0, x2);
-        float mx1 = fmaxf(x1, x3);
+        float mx0 = logit_max<kScore>(x0, x2);
+        float mx1 = logit_max<kScore>(x1, x3);
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+            mx0 = logit_max<kScore>(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+            mx1 = logit_max<kScore>(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
         }
-        const float mn0 = fmaxf(m0, mx0);
-        const float mn1 = fmaxf(m1, mx1);
+        const float mn0 = logit_max<kScore>(m0, mx0);
+        const float mn1 = logit_max<kScore>(m1, mx1);
         const float mu0 = (mn0 == NEG) ? 0.f : mn0;
         const float mu1 = (mn1 == NEG) ? 0.f : mn1;
         const float al0 = exp2f(m0 - mu0);
@@ -1974,7 +1994,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
             const int h = e / D;
             float mh = NEG;
 #pragma unroll
-            for (int w = 0; w < kConsumerWarps; ++w) mh = fmaxf(mh, wm[w * G + h]);
+            for (int w = 0; w < kConsumerWarps; ++w) mh = logit_max<kScore>(mh, wm[w * G + h]);
             float o = 0.f;
 #pragma unroll
             for (int w = 0; w < kConsumerWarps; ++w) {
@@ -1989,7 +2009,7 @@ __global__ void __launch_bounds__(kThreads, kStages == 2 ? 3 : (kStages == 3 ? 2
         float l = 0.f;
         if (cnt > 0) {
 #pragma unroll
-            for (int w = 0; w < kConsumerWarps; ++w) mh = fmaxf(mh, wm[w * G + tid]);
+            for (int w = 0; w < kConsumerWarps; ++w) mh = logit_max<kScore>(mh, wm[w * G + tid]);
 #pragma unroll
             for (int w = 0; w < kConsumerWarps; ++w) {
                 const float mw = wm[w * G + tid];

@@ -474,7 +474,9 @@ lf_status lf_decode_prefix_workspace(int B, int Hq, int Hkv, int d, int S, int N
  * slots with the lowest (weights[j], slot) among live slots of age >= W.
  *
  * weights    in/out float [B][Hkv][S]: what masked slots hold does not matter and
- *                stays. A slot whose sum is NaN is never returned.
+ *                stays. A slot whose sum is NaN is never returned. (A live slot whose
+ *                logit is NaN or +infinity makes its head's output NaN, and the sums of all
+ *                live slots of the unit.)
  * decay      0 <= decay <= 1 (1: the plain sum; 0: the current step's weights)
  * next_slots, k, flags   as in lf_decode_step_ex (without LF_STEP_LOG2_SCORES)
  * The other arguments are those of lf_decode_step. weights must not overlap the

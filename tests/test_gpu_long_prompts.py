@@ -909,3 +909,45 @@ def test_prompt_weights_of_rows_that_are_not_finite(nq, kv, S, rows, Hq, Hkv, d,
     fine = ~torch.isnan(ref)
     near(w.cpu()[fine], ref[fine], tol[fine])
     no_errors()
+
+
+@pytest.mark.parametrize("env", [
+    {}, {"LF_CLUSTER": "0"}, {"LF_CLUSTER": "0", "LF_CHUNK_TILES": "1"}, {"LF_CLUSTER": "1", "LF_DEEP": "0"},
+    {"LF_CLUSTER": "1", "LF_DEEP": "1"}, {"LF_CLUSTER": "0", "LF_SPLIT": "1"},
+    {"LF_CLUSTER": "0", "LF_SPLIT": "1", "LF_SPLIT_TAIL": "1"}])
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 2, 64), (4, 2, 128), (16, 2, 64)])
+@pytest.mark.parametrize("others", ["finite", "masked", "-inf"])
+def test_weights_step_logits_that_are_nan(monkeypatch, env, Hq, Hkv, d, others):
+    """A live key of NaN or a logit of +infinity: its unit's heads have no softmax, whatever
+    the other slots hold."""
+    for name, value in env.items():
+        monkeypatch.setenv(name, value)
+    g = gen(d + Hq)
+    for S, at, what in ((70, 3, NAN), (70, 69, INF), (1029, 517, NAN), (4200, 4199, NAN), (4200, 100, INF)):
+        for k in (None, 3):
+            c = step_case(g, 1, Hq, Hkv, d, S, holes=0.05)
+            c["mask"][0, 0, at] = 5
+            if others == "masked":
+                c["mask"][0, 0, :at] = c["mask"][0, 0, at + 1:] = -1
+            if others == "-inf" or what == INF:
+                c["q"][0, :Hq // Hkv] = 1.0
+            if others == "-inf":
+                c["k"][0, 0, :at] = c["k"][0, 0, at + 1:] = -INF
+            c["k"][0, 0, at] = what
+            c["weights"][0, 0, at] = 1.0
+            mask, before = c["mask"].cpu(), c["weights"].cpu()
+            want = plain.weights_step(c["q"][:, Hq // Hkv:], c["k"][:, 1:], c["v"][:, 1:], c["mask"][:, 1:],
+                                      c["weights"][:, 1:], c["nk"][:, 1:], c["nv"][:, 1:], ints([[-1]]), 2,
+                                      d ** -0.5, 0.9, 1)
+            out, nxt = run_step(c, ints([[-1, -1]]), 2, d ** -0.5, decay=0.9, k=k)
+            w = c["weights"].cpu()
+            live = mask[0, 0] >= 0
+            assert torch.isnan(out[0, :Hq // Hkv]).all() and torch.isnan(w[0, 0][live]).all()
+            assert torch.equal(w[0, 0][~live].view(torch.int32), before[0, 0][~live].view(torch.int32))
+            assert (nxt[0, 0] == -1).all()
+            # The other unit knows nothing of it.
+            near(out[:, Hq // Hkv:], want["out"], want["tol"])
+            live = mask[:, 1:] >= 0
+            near(w[:, 1:][live], want["weights"][live], want["wtol"][live])
+            assert torch.equal(nxt.cpu()[:, 1:].view(1, 1, k or 1), plain.chosen(w[:, 1:], mask[:, 1:], 2, k or 1, False))
+    no_errors()
