@@ -694,8 +694,12 @@ void plan_prompt_weights(PromptWeightsParams* p, int sms) {
     // few items (16 of 8192 keys: 8 tiles, 128 CTAs, 17; 7 tiles, 160 CTAs, 22), while
     // with many the ragged ends of a second wave fit in. More rows: only where a wave
     // holds two pieces of all items, and if they save more than the join's launch.
-    const int64_t rows = p->rows > 0 ? std::min<int64_t>(p->T, static_cast<int64_t>(p->rows) * p->B) : p->T;
-    const int64_t busy = std::max<int64_t>(1, (rows + span - 1) / span) * p->Hkv;
+    // (Items: a sequence's rows share no tile with another's, so those of each sequence
+    // take one at least. Counted as if their rows were packed, 8 rows of 8 prompts with
+    // groups of 4 took 63 us for 49, one row 87 for 49.)
+    const int64_t held = p->by_sequence ? each * p->B
+                                        : std::max<int64_t>(std::min(p->B, p->T), (p->T + span - 1) / span);
+    const int64_t busy = held * p->Hkv;
     const int64_t tiles = (p->S + kRows - 1) / kRows;
     const int64_t least = (tiles + kMaxPieces - 1) / kMaxPieces;
     int64_t per = tiles;
@@ -716,9 +720,10 @@ void plan_prompt_weights(PromptWeightsParams* p, int sms) {
     const int64_t pairs = (tiles + 1) / 2 * p->B * p->Hkv;
     const int64_t most_pairs[] = {sms * 4 / 3, sms * 4 / 7, sms / 6};
     const int least_rows[] = {2, 4, 32};  // tiles of a sequence's rows
+    const int64_t mean = std::min<int64_t>(most, (p->T + p->B - 1) / p->B);
     p->share = few ? 0 : 1;
     for (int i = 0; i < 3 && p->share > 0; ++i) {
-        if (pairs > most_pairs[i] || most <= static_cast<int64_t>(least_rows[i]) * tok) break;
+        if (pairs > most_pairs[i] || mean <= static_cast<int64_t>(least_rows[i]) * tok) break;
         p->share *= 2;
     }
 }

@@ -951,3 +951,31 @@ def test_weights_step_logits_that_are_nan(monkeypatch, env, Hq, Hkv, d, others):
             near(w[:, 1:][live], want["weights"][live], want["wtol"][live])
             assert torch.equal(nxt.cpu()[:, 1:].view(1, 1, k or 1), plain.chosen(w[:, 1:], mask[:, 1:], 2, k or 1, False))
     no_errors()
+
+
+# --------------------------------------------- how a prompt's weights split their work --
+
+def pieces(T, B, Hq, Hkv, d, S, rows, kept):
+    """Pieces of the keys, from the workspace: (m, l) of `kept` rows each."""
+    n = lf.prompt_weights_workspace(T, B, Hq, Hkv, d, S, rows)
+    assert n % (8 * kept * Hq) == 0
+    return n // (8 * kept * Hq)
+
+
+@pytest.mark.parametrize("B,S", [(8, 8192), (3, 16384), (64, 4096)])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_prompt_weights_cut_the_keys_of_few_rows_like_those_of_a_full_tile(B, S, G):
+    """A sequence's rows take a tile whether or not they fill it, so the keys have as many pieces."""
+    tile = 128 // G
+    full = pieces(8 * tile * B, B, 8 * G, 8, 128, S, tile, tile * B)
+    for rows in {1, 3, tile // 4, tile - 1}:
+        assert pieces(8 * tile * B, B, 8 * G, 8, 128, S, rows, rows * B) == full
+        # All rows of short chunks too.
+        assert pieces(rows * B, B, 8 * G, 8, 128, S, rows, rows * B) == full
+
+
+@pytest.mark.parametrize("B,n", [(32, 10), (64, 3), (16, 30)])
+def test_prompt_weights_of_many_short_chunks_leave_the_keys_whole(B, n):
+    """Sequences that fill the GPU by themselves gain nothing from pieces and their join."""
+    assert B * 8 >= 100  # items, each on an SM of its own
+    assert pieces(B * n, B, 32, 8, 128, 4096, 0, B * n) == 1
