@@ -401,12 +401,12 @@ __global__ void __launch_bounds__(WeightsSmem<D, kHeld>::kThreads, 1)
         const auto arrived = [&](uint64_t* bar, int parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_limit_ns)) != 0;
         };
-        // Half of a tile's 128 scores; behind the second the accumulator is free.
-        const auto take = [&](int half, uint32_t (&x)[64]) {
+        // Half of a tile's 128 scores; behind the last the accumulator is free.
+        const auto take = [&](int half, bool last, uint32_t (&x)[64]) {
             tmem_ld32(ts + half * 64, x);
             tmem_ld32(ts + half * 64 + 32, x + 32);
             tmem_wait_ld();
-            if (half) {
+            if (last) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_free[kTurns * h + s]);
@@ -441,11 +441,13 @@ __global__ void __launch_bounds__(WeightsSmem<D, kHeld>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&s_free[kTurns * h + s]);
                 return total;
             }
+            // (Few rows may leave the second half without a row: 8 rows 40.8 us for 48.9.)
+            const int halves = kForm == kFewRows && hi <= kRows / 2 ? 1 : 2;
             // (Both halves' code, 20 us less of 450 for 8192 tokens; a few rows spill.)
 #pragma unroll(kForm == kColumnsPass ? 2 : 1)
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < halves; ++half) {
                 uint32_t x[64];
-                take(half, x);
+                take(half, half + 1 == halves, x);
                 if (some) {
 #pragma unroll
                     for (int e = 0; e < 64; ++e) x[e] = half * 64 + e >= lo && half * 64 + e < hi ? x[e] : 0xff800000u;
@@ -485,7 +487,7 @@ __global__ void __launch_bounds__(WeightsSmem<D, kHeld>::kThreads, 1)
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t x[64];
-                    take(half, x);
+                    take(half, half == 1, x);
                     if (some) {
 #pragma unroll
                         for (int e = 0; e < 64; ++e) x[e] = half * 64 + e < seen ? x[e] : 0xff800000u;
@@ -696,7 +698,7 @@ void plan_prompt_weights(PromptWeightsParams* p, int sms) {
     // holds two pieces of all items, and if they save more than the join's launch.
     // (Items: a sequence's rows share no tile with another's, so those of each sequence
     // take one at least. Counted as if their rows were packed, 8 rows of 8 prompts with
-    // groups of 4 took 63 us for 49, one row 87 for 49.)
+    // groups of 4 took 63 us for 41, one row 87.)
     const int64_t held = p->by_sequence ? each * p->B
                                         : std::max<int64_t>(std::min(p->B, p->T), (p->T + span - 1) / span);
     const int64_t busy = held * p->Hkv;
