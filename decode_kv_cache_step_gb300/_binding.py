@@ -87,7 +87,7 @@ def load_library(path: str | None = None):
 
     The environment variable LF_LIBRARY names another build of the same
     library (for comparing two builds in one session)."""
-    global _lib
+    global _lib, _fast_pointers
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -163,6 +163,7 @@ def load_library(path: str | None = None):
         lib.lf_version.argtypes = []
         lib.lf_version.restype = I
         if path is None:
+            _fast_pointers = _load_check()
             _lib = lib
         return lib
 
@@ -216,7 +217,7 @@ def _load_check():
     return module.pointers if same else None
 
 
-_fast_pointers = _load_check()
+_fast_pointers = None  # (load_library sets it: importing the package maps no library)
 
 
 def _pointers(*args):

@@ -1,6 +1,9 @@
 """Refusals of the rotation with axes, of eviction by accumulated weight and of the
 4-bit cache, without a GPU; the plain definitions' own pins; the binding's checks."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -251,3 +254,19 @@ def test_prompt_weights_by_hand():
     assert w.tolist() == [[[1.5, 0.5, 7.0]]]
     w, _ = plain.prompt_weights(q, k, [0, 2], [3], torch.full((1, 1, 3), 7.0), 1, 1.0)
     assert torch.allclose(w, torch.tensor([[[7 + 1 / 3, 1 / 3, 1 / 3]]], dtype=torch.float64))
+
+
+# ------------------------------------------------------------ the compiled checks --
+
+def test_importing_the_package_maps_no_library(lib):
+    """Both libraries are loaded by the first call, not by the import."""
+    code = ("import decode_kv_cache_step_gb300 as lf\n"
+            "ours = lambda: {n for n in ('liblf_decode', '_lf_check') if n in open('/proc/self/maps').read()}\n"
+            "assert not ours(), ours()\n"
+            "lf.load_library()\n"
+            "print(sorted(ours()))")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
+    assert "liblf_decode" in r.stdout
+    assert ("_lf_check" in r.stdout) == os.path.exists(lfbuild.CHECK_PATH)
