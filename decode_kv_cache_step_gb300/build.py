@@ -25,7 +25,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "liblf_decode.so")
 CHECK_PATH = os.path.join(LIB_DIR, "_lf_check.so")
+CHECK_SRC = os.path.join(CSRC, "lf_check.cpp")
 OBJ_DIR = os.path.join(PKG, "_build")
+STAMP_PATH = os.path.join(OBJ_DIR, "_lf_check.torch")  # the torch version CHECK_PATH is for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -45,8 +47,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+        glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
 def up_to_date() -> bool:
@@ -56,37 +57,59 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def _build_check() -> None:
-    """lib/_lf_check.so, against the installed torch."""
-    import torch
-
-    base = os.path.dirname(torch.__file__)
-    include = os.path.join(base, "include")
-    fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
-    os.close(fd)
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           f'-DLF_TORCH_VERSION="{torch.__version__}"', "-I", include,
-           "-I", os.path.join(include, "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "lf_check.cpp"), "-o", tmp,
-           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+def check_up_to_date() -> bool:
+    """Whether lib/_lf_check.so was compiled from the present source against the
+    installed torch (the build notes its version)."""
     try:
+        import torch
+        with open(STAMP_PATH) as f:
+            same = f.read() == torch.__version__
+        t = os.path.getmtime(CHECK_PATH)
+        return same and all(os.path.getmtime(p) <= t for p in (CHECK_SRC, __file__))
+    except Exception:  # missing, or no usable torch: _build_check says so
+        return False
+
+
+def _build_check() -> None:
+    """lib/_lf_check.so, against the installed torch; a warning where that fails."""
+    tmp = None
+    try:
+        import torch
+
+        base = os.path.dirname(torch.__file__)
+        include = os.path.join(base, "include")
+        for path in (LIB_DIR, OBJ_DIR):
+            os.makedirs(path, exist_ok=True)
+        for path in (STAMP_PATH, CHECK_PATH):
+            if os.path.exists(path):
+                os.unlink(path)
+        fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
+        os.close(fd)
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               f'-DLF_TORCH_VERSION="{torch.__version__}"', "-I", include,
+               "-I", os.path.join(include, "torch", "csrc", "api", "include"),
+               "-I", sysconfig.get_paths()["include"], CHECK_SRC, "-o", tmp,
+               "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
         r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode == 0:
-            os.replace(tmp, CHECK_PATH)
-            return
-        why = r.stderr[-400:]
-    except OSError as e:
-        why = str(e)
-    for path in (tmp, CHECK_PATH):
-        if os.path.exists(path):
-            os.unlink(path)
-    warnings.warn(f"_lf_check.so was not built: {why}")
+        if r.returncode != 0:
+            raise RuntimeError(r.stderr[-400:])
+        os.replace(tmp, CHECK_PATH)
+        with open(STAMP_PATH, "w") as f:
+            f.write(torch.__version__)
+    except Exception as e:
+        if tmp is not None and os.path.exists(tmp):
+            os.unlink(tmp)
+        warnings.warn(f"_lf_check.so was not built: {e}")
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every kernel and the C ABI into liblf_decode.so; return its path."""
+    """Compile every kernel and the C ABI into liblf_decode.so; return its path. The
+    argument checks beside it are compiled where they are missing or stale."""
+    check_stale = force or not check_up_to_date()
     if not force and up_to_date():
+        if check_stale:
+            _build_check()
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -105,9 +128,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
     srcs = _sources()
     with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        check = ex.submit(_build_check)
+        check = ex.submit(_build_check) if check_stale else None
         objs = list(ex.map(compile_one, srcs))
-        check.result()
+        if check is not None:
+            check.result()
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
     os.close(fd)
     cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]

@@ -270,3 +270,73 @@ def test_importing_the_package_maps_no_library(lib):
     assert r.returncode == 0, r.stderr
     assert "liblf_decode" in r.stdout
     assert ("_lf_check" in r.stdout) == os.path.exists(lfbuild.CHECK_PATH)
+
+
+@pytest.fixture
+def own_lib(tmp_path, monkeypatch):
+    """The build's output in a folder of its own, compilers replaced by a record of their calls."""
+    for name in ("LIB_PATH", "CHECK_PATH", "STAMP_PATH"):
+        monkeypatch.setattr(lfbuild, name, str(tmp_path / os.path.basename(getattr(lfbuild, name))))
+    monkeypatch.setattr(lfbuild, "LIB_DIR", str(tmp_path))
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        out = cmd[cmd.index("-o") + 1]
+        open(out, "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(lfbuild.subprocess, "run", run)
+    open(lfbuild.LIB_PATH, "w").close()  # newer than every source
+    return ran
+
+
+def compiled(ran):
+    n = sum(lfbuild.CHECK_SRC in cmd for cmd in ran)
+    assert n == len(ran)  # nothing else
+    ran.clear()
+    return n
+
+
+def test_build_renews_stale_checks_alone(own_lib, monkeypatch):
+    lfbuild.build()
+    assert compiled(own_lib) == 1  # missing
+    lfbuild.build()
+    assert compiled(own_lib) == 0
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "9.9.9")
+        lfbuild.build()
+        assert compiled(own_lib) == 1  # for another torch
+        lfbuild.build()
+        assert compiled(own_lib) == 0
+    lfbuild.build()
+    assert compiled(own_lib) == 1
+    os.utime(lfbuild.CHECK_PATH, (1, 1))  # older than its source
+    lfbuild.build()
+    assert compiled(own_lib) == 1
+    os.unlink(lfbuild.STAMP_PATH)
+    lfbuild.build()
+    assert compiled(own_lib) == 1
+
+
+def test_build_warns_where_the_checks_do_not_compile(own_lib, monkeypatch):
+    """Whatever fails there, the library is built and the binding checks in Python."""
+    def fails(cmd, **kw):
+        return subprocess.CompletedProcess(cmd, 1, "", "no such header")
+
+    lfbuild.build()
+    os.unlink(lfbuild.STAMP_PATH)
+    with monkeypatch.context() as m:
+        m.setattr(lfbuild.subprocess, "run", fails)
+        with pytest.warns(UserWarning, match="no such header"):
+            assert lfbuild.build() == lfbuild.LIB_PATH
+    assert not os.path.exists(lfbuild.CHECK_PATH)  # nor a stale one, or pieces of one
+    assert sorted(os.listdir(lfbuild.LIB_DIR)) == [os.path.basename(lfbuild.LIB_PATH)]
+    with monkeypatch.context() as m:
+        m.delattr(torch._C, "_GLIBCXX_USE_CXX11_ABI")
+        with pytest.warns(UserWarning, match="_GLIBCXX_USE_CXX11_ABI"):
+            assert lfbuild.build() == lfbuild.LIB_PATH
+    with monkeypatch.context() as m:
+        m.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+        with pytest.warns(UserWarning, match="was not built"):
+            assert lfbuild.build() == lfbuild.LIB_PATH
