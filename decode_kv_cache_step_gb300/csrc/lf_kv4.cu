@@ -482,7 +482,9 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
         __syncwarp();
     }
 
-    // q as halves of 2^13 to 2^14 for the largest: what is below 2^-38 of that is lost.
+    // q as halves of 2^13 to 2^14 for the largest, a sixteenth of that where odd nibbles
+    // meet it: within 2^-34 of the head's largest value (2^-38 at even places), exact for
+    // values of at least 2^-26 of it.
     uint32_t qf[NG][4];      // k steps of a group: codes at even, then odd nibbles
     uint32_t start[2];       // -8 sum q of the groups: an operand with the scales
     float qs[2];             // what a logit's sum is worth (log2 domain)

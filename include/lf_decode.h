@@ -551,7 +551,8 @@ lf_status lf_kv4_unpack(const void* k4, const void* k_scale, const void* v4, con
  * write_slot, then every live slot, that one included, is attended as the
  * values that its codes stand for. The arithmetic is fp32 with weights of 11
  * bits; outputs are rounded to bf16 once. What a slot's weight leaves of its value
- * below 2^-31 of the largest value is lost, and finite logits are expected.
+ * below 2^-31 of the largest value is lost, and what lies below 2^-34 of a query head's
+ * largest value. Finite logits are expected, and queries times scale below 2^116.
  * new_k, new_v in bf16 [B][Hkv][d]; the other arguments as above and in
  * lf_decode_attention.
  */

@@ -979,3 +979,50 @@ def test_prompt_weights_of_many_short_chunks_leave_the_keys_whole(B, n):
     """Sequences that fill the GPU by themselves gain nothing from pieces and their join."""
     assert B * 8 >= 100  # items, each on an SM of its own
     assert pieces(B * n, B, 32, 8, 128, 4096, 0, B * n) == 1
+
+
+# ------------------------------------------------ small queries beside a large one --
+
+@pytest.mark.parametrize("d,Hq", [(64, 2), (128, 8), (128, 1)])
+@pytest.mark.parametrize("low,places", [(-20, "all"), (-26, "all"), (-30, "even"), (-30, "odd"), (-33, "all")])
+def test_kv4_attention_of_queries_far_below_the_largest(d, Hq, low, places):
+    """One large value that meets zero keys, and values of 2^low of it whose keys make up for that.
+
+    A query is held to 2^-34 of its head's largest value, at even places to 2^-38, and
+    exactly where its last bit is above that (2^-7 of 2^-26, or of 2^-30): an error of a logit of
+    at most scale * sum |k| times that, which moves the output by at most twice as much of
+    sum_j p_j (|v_j| + |o|).
+    """
+    g = gen(d - low)
+    S, scale = 300, d ** -0.5
+    q = torch.zeros(1, Hq, d)
+    # Magnitudes of [1, 2) times 2^low, 8 bits: no last bit below 2^(low - 7).
+    small = torch.randint(128, 256, (1, Hq, d), generator=g) / 128 * 2.0 ** low
+    sign = torch.randint(0, 2, (1, Hq, d), generator=g) * 2 - 1
+    at = torch.arange(d)
+    there = (at >= 32) & ((at % 2 == 0) | (places != "even")) & ((at % 2 == 1) | (places != "odd"))
+    q[:, :, there] = (small * sign)[:, :, there]
+    q[:, :, 5] = 1.0
+    q = q.to(BF).cuda()
+    k, v = torch.randn((1, 1, S, d), generator=g) * 2.0 ** -low, normal(g, 1, 1, S, d)
+    k[..., :32] = 0
+    (k4, ks), (v4, vs) = empty4(1, 1, S, d), empty4(1, 1, S, d)
+    mask = torch.full((1, 1, S), -1, dtype=torch.int32, device="cuda")
+    lf.kv4_pack(k.to(BF).cuda(), v, None, ints([S]), k4, ks, v4, vs, mask)
+    out = torch.full_like(q, 7.0)
+    lf.decode_attention_kv4(q, k4, ks, v4, vs, mask, v[:, :, 0].contiguous(), v[:, :, 0].contiguous(),
+                            ints([[-1]]), out, scale)
+    kk, vv = plain.stand_for(k4, ks, 8), plain.stand_for(v4, vs, 4)
+    ref, tol = plain.kv4_attention(q, kk, vv, ks, vs, mask, scale)
+    held = torch.where(at % 2 == 0, 2.0 ** -38, 2.0 ** -34).double()
+    held[~there] = 0
+    held[(2.0 ** (low - 7) >= 2 * held)] = 0  # exact
+    delta = float((kk[0, 0].abs() @ held).max() * scale)
+    assert (delta == 0) == (low >= -26 or places == "even")
+    for h in range(Hq):
+        p = torch.softmax(kk[0, 0] @ q[0, h].cpu().double() * scale, 0)
+        tol[0, h] += math.expm1(2 * delta) * (p @ vv[0, 0].abs() + ref[0, h].abs())
+    near(out, ref, tol)
+    # (The small values do count: without them every slot weighs the same.)
+    assert (ref - vv[0, 0].mean(0)).abs().max() > 0.1
+    no_errors()
