@@ -1026,3 +1026,92 @@ def test_kv4_attention_of_queries_far_below_the_largest(d, Hq, low, places):
     # (The small values do count: without them every slot weighs the same.)
     assert (ref - vv[0, 0].mean(0)).abs().max() > 0.1
     no_errors()
+
+
+# --------------------------------------------- a prompt's weights: bad lengths, long prompts --
+
+def summed(q, k, starts, lens, rows, scale):
+    """Weights [B, Hkv, S] of one call over zeros, in 64 bits on the GPU, some rows at a time."""
+    q, k = q.double(), k.double()
+    B, Hkv, S, _ = k.shape
+    G = q.shape[1] // Hkv
+    w = torch.zeros(B, Hkv, S, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        n, kv = starts[b + 1] - starts[b], lens[b]
+        at = torch.arange(kv, device="cuda")
+        for i in range(max(0, n - rows) if rows else 0, n, 512):
+            tok = torch.arange(i, min(n, i + 512), device="cuda")
+            for h in range(Hkv * G):
+                s = q[starts[b] + tok, h] @ k[b, h // G, :kv].T * scale
+                s.masked_fill_(at[None] > (kv - n + tok)[:, None], -math.inf)
+                w[b, h // G, :kv] += torch.softmax(s, 1).sum(0)
+    return w.cpu()
+
+
+@pytest.mark.parametrize("nq,kv,rows,Hq,Hkv,d", [
+    # One tile of rows held in both passes.
+    ([100, 40], [70001, 12345], 32, 4, 1, 128), ([7, 3], [30000, 9001], 5, 8, 2, 64),
+    ([20], [262144], 1, 8, 1, 64), ([4], [1 << 20], 0, 1, 1, 64),
+    # Two tiles of rows, their keys in pieces that are joined.
+    ([300], [20000], 0, 8, 2, 128), ([700, 200], [20000, 16001], 130, 2, 1, 64),
+    # Keys held, alone and by clusters of two and four.
+    ([2500, 3], [12000, 11000], 0, 4, 2, 64), ([9000], [12000], 0, 2, 1, 64), ([2000], [10000], 0, 4, 4, 128),
+    # Clusters of eight.
+    ([1100], [1100], 0, 8, 1, 128), ([2000], [2000], 0, 4, 1, 128), ([5000], [5000], 0, 1, 1, 128)])
+def test_prompt_weights_of_long_prompts(nq, kv, rows, Hq, Hkv, d):
+    """Against 64 bits past 8192 keys, and for clusters of eight.
+
+    A weight is off by 2^-12 of itself as in _plain_long, and sums of many terms by their
+    chains of fp32 additions: a row's sum over up to 2^20 keys has at most 300 one after another
+    (16 pieces, four turns, halves of a tile), a key's over 9000 rows 150: below 2^-15.
+    """
+    g = gen(sum(kv) + d)
+    B, T, S = len(nq), sum(nq) + 1, max(kv) + (0 if max(kv) == 1 << 20 else 5)
+    starts = [sum(nq[:i]) for i in range(B + 1)]
+    q, k = normal(g, T, Hq, d), normal(g, B, Hkv, S, d)
+    q[sum(nq):] = NAN
+    for b in range(B):
+        k[b, :, kv[b]:] = NAN
+    w = torch.zeros(B, Hkv, S, device="cuda")
+    lf.prompt_weights(q, k, ints(starts), ints(kv), w, d ** -0.5, rows=rows)
+    ref = summed(q, k, starts, kv, rows, d ** -0.5)
+    near(w, ref, (2.0 ** -12 + 2.0 ** -15) * ref)
+    no_errors()
+
+
+BAD = [  # q_start as shares of T, kv_len
+    ((0, 1 / 3, 2 / 3, 1), (1400, 9999, 1300)), ((0, 1 / 3, 2 / 3, 1), (1400, 100, 1300)),
+    ((0, 1 / 3, 2 / 3, 1), (1400, -1, 1300)), ((0, 1 / 3, 2, 1), (1400, 1400, 1400)),
+    ((-1, 1 / 3, 2 / 3, 1), (1400, 1400, 1400)), ((0, 2 / 3, 1 / 3, 1), (1400, 1400, 1400))]
+
+
+@pytest.mark.parametrize("shares,kv", BAD)
+@pytest.mark.parametrize("T,rows,Hq,d", [
+    (600, 0, 4, 64),      # rows in pieces that are joined, keys held by clusters of four
+    (1800, 0, 8, 128),    # clusters of eight
+    (600, 100, 2, 128),   # counted rows, by sequence
+    (600, 20, 4, 64),     # one tile of rows held
+    (27, 0, 4, 64)])      # the same, packed
+def test_prompt_weights_bad_lengths_in_every_form(shares, kv, T, rows, Hq, d):
+    """A sequence that does not fit keeps its weights; those beside it are right, or (where
+    q_start does not ascend) right or kept."""
+    g = gen(T + Hq)
+    S = 1500
+    starts = [int(x * T) for x in shares]
+    q, k = normal(g, T, Hq, d), normal(g, 3, 1, S, d)
+    w = torch.full((3, 1, S), 7.0, device="cuda")
+    lf.prompt_weights(q, k, ints(starts), ints(kv), w, d ** -0.5, rows=rows)
+    rows_of = [(starts[b], starts[b + 1]) for b in range(3)]
+    fits = [0 <= a <= e <= T and e - a <= kv[b] <= S for b, (a, e) in enumerate(rows_of)]
+    # (A length of 100 fits 9 rows.)
+    assert lf.device_errors(clear=True) == (0 if all(fits) else lf.LF_DEVERR_BAD_LENGTH)
+    ascends = all(0 <= a <= e <= T for a, e in rows_of)
+    for b, (a, e) in enumerate(rows_of):
+        # Without counted rows of its own a sequence's rows are found by their order alone.
+        if not fits[b] or (not ascends and (rows == 0 or (w[b] == 7).all())):
+            assert (w[b] == 7).all(), b
+            continue
+        ref = summed(q, k[b:b + 1], [a, e], [kv[b]], rows, d ** -0.5)[0]
+        ref[:, :kv[b] - (e - a)] += 7.0
+        near(w[b, :, :kv[b]], ref[:, :kv[b]], (2.0 ** -12 + 2.0 ** -15) * ref[:, :kv[b]])
+        assert (w[b, :, kv[b]:] == 7).all()
