@@ -536,11 +536,14 @@ __global__ void __launch_bounds__(kThreads, 3) lf_kv4_attn_kernel(const Kv4Param
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float v[2] = {0.f, 0.f};
+            // (As words: selected one by one, d = 64 kept them in local memory, in the same time.)
+            uint32_t v = 0;
 #pragma unroll
-            for (int k = 0; k < 3 * NG; ++k)
-                if (k / 2 == c + 4 * i) v[k & 1] = part[k / NG][k % NG];
-            start[i] = pack_bf16x2(v[0], v[1]);
+            for (int k = 0; k < 3 * NG; k += 2) {
+                const uint32_t two = pack_bf16x2(part[k / NG][k % NG], part[(k + 1) / NG][(k + 1) % NG]);
+                v = k / 2 == c + 4 * i ? two : v;
+            }
+            start[i] = v;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) qs[h] = __shfl_sync(0xffffffffu, unit, 4 * (2 * c + h));
