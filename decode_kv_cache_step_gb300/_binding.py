@@ -588,10 +588,13 @@ def _check_axes(positions, pair_axis, rot):
     """(axes, the pairs' axes as bytes)."""
     if not isinstance(positions, torch.Tensor) or positions.dim() != 2:
         raise ValueError("positions must be [axes,T]")
-    if isinstance(pair_axis, int) or isinstance(pair_axis, torch.Tensor) and pair_axis.is_cuda:
+    if isinstance(pair_axis, torch.Tensor) and pair_axis.is_cuda:
         raise ValueError("pair_axis: expected rot/2 axes on the host")
     try:
-        pairs = bytes(pair_axis.tolist() if isinstance(pair_axis, torch.Tensor) else pair_axis)
+        if not isinstance(pair_axis, bytes):
+            # (Entry by entry: bytes() would take an array's memory as it lies.)
+            pair_axis = pair_axis.tolist() if isinstance(pair_axis, torch.Tensor) else list(pair_axis)
+        pairs = bytes(pair_axis)
     except (TypeError, ValueError) as e:
         raise ValueError(f"pair_axis: expected rot/2 axes, {e}") from None
     if len(pairs) != rot // 2:

@@ -5,10 +5,12 @@ import os
 import subprocess
 import sys
 
+import numpy
 import pytest
 import torch
 
 import decode_kv_cache_step_gb300 as lf
+from decode_kv_cache_step_gb300 import _binding as binding
 from decode_kv_cache_step_gb300 import build as lfbuild
 
 import _plain_long as plain
@@ -340,3 +342,23 @@ def test_build_warns_where_the_checks_do_not_compile(own_lib, monkeypatch):
         m.setitem(sys.modules, "torch", None)  # import torch raises ImportError
         with pytest.warns(UserWarning, match="was not built"):
             assert lfbuild.build() == lfbuild.LIB_PATH
+
+
+# -------------------------------------------------------------- the pairs' axes --
+
+@pytest.mark.parametrize("make", [list, tuple, bytes, bytearray, numpy.array, torch.tensor,
+                                  lambda x: numpy.array(x, dtype=numpy.uint8),
+                                  lambda x: torch.tensor(x, dtype=torch.uint8), iter])
+def test_pair_axis_is_read_entry_by_entry(make):
+    pairs = [0, 1, 2, 0, 1, 2, 0, 1]
+    got = binding._check_axes(torch.zeros(3, 5, dtype=torch.int32), make(pairs), 16)
+    assert got == (3, bytes(pairs))
+
+
+@pytest.mark.parametrize("wrong", [
+    numpy.array([1]), numpy.int64(1), numpy.array([1, 2], dtype=numpy.int32),  # 8 bytes of memory each
+    8, 2.0, None, "01201201", [0, 1, 2], [0.0] * 8, [0, 1, 2, 0, 1, 2, 0, 256], [0, 1, 2, 0, 1, 2, 0, -1],
+    numpy.zeros(8), torch.zeros(8), torch.zeros(2, 4, dtype=torch.int32)])
+def test_pair_axis_of_another_length_or_kind_is_refused(wrong):
+    with pytest.raises(ValueError, match="pair_axis"):
+        binding._check_axes(torch.zeros(3, 5, dtype=torch.int32), wrong, 16)
