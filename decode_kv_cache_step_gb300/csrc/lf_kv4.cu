@@ -16,7 +16,7 @@
 //
 // Measured (8 KV heads of 128): 20.3K tokens packed in 48 us, 5.6 TB/s read and
 // written, and unpacked in 36; 64 caches of 4096 to 16384 slots attended with 32
-// query heads in 175.7 us, 4.6 TB/s, one of 16384 in 13.
+// query heads in 175 us, 4.6 TB/s, one of 16384 in 12.8.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stdlib.h>
@@ -344,7 +344,7 @@ __device__ __forceinline__ float scale_of(uint32_t word, int odd) {
 // the cycles, issue 55%, DRAM 66%; 12 warps an SM, as many as 168 registers
 // leave. One cache of 16384 slots: latency, 344 CTAs of three tiles a warp, each
 // with a prologue (q, its sums) and an epilogue as long as two more.
-// 64 caches of 4096 to 16384 slots, us: 176. Steps on the way, each against the
+// 64 caches of 4096 to 16384 slots, us: 175. Steps on the way, each against the
 // one before it: the ring and a rare reference 211 (275), the next tile's logits
 // beside this one's values 202, tiles of 32 slots 186 (of 16), scales widened once
 // a tile 178 (182, by each lane that uses them). Two stages at 4 CTAs an SM took

@@ -22,14 +22,14 @@
 //
 // What bounds it: the score warps. A tile of scores is 512 cycles of products, as
 // many of exponentials, and some 470 instructions for each of the SM's schedulers;
-// alone the products would take 341 us of the 430 below, the rest alone 420. (Streamed
+// alone the products would take 341 us of some 430, the rest alone 420. (Streamed
 // tiles of 256 rows, with less to read for the products: 467. Eight score warps with
 // two accumulators each: 500. A third of the exponentials as polynomials: slower.
 // Waits that poll: the same.) Measured (32 query, 8 KV heads of 128): every row of
-// 8192 tokens 430 us, some 205 and 225 a pass, 640 TFLOP/s of both passes'
-// products; the last 32 rows of 8 prompts of 2000 to 8192 tokens 40.7 us, two
-// passes over 113 MB of keys (the second from L2 in part), where a CTA's start and
-// the few tiles it streams take the most.
+// 8192 tokens 430 us in short runs and 436 called without a pause, some 205 and 225 a
+// pass, 1270 TFLOP/s of both passes' products; the last 32 rows of 8 prompts of 2000 to
+// 8192 tokens 41.4 us, two passes over 113 MB of keys (the second from L2 in part), where
+// a CTA's start and the few tiles it streams take the most. One row takes as long.
 #include <math.h>
 #include <stdlib.h>
 

@@ -111,7 +111,7 @@ typedef enum lf_status {
  */
 #define LF_KERNEL_DECODE_STEP 0 /* slot write, mask ageing, attention (+ score or weights, eviction) */
 #define LF_KERNEL_ATTENTION 1   /* lf_decode_attention: slot write and attention only */
-#define LF_KERNEL_SCORE 2       /* split finish: LongFlowScore and eviction */
+#define LF_KERNEL_SCORE 2       /* split finish: LongFlowScore (or weights) and eviction; several slots by weight */
 #define LF_KERNEL_NORM_ROPE 3        /* lf_qk_norm_rope, lf_prefill_append, and with axes */
 #define LF_KERNEL_PACKED_ATTENTION 4 /* lf_window_attention; the prefix part of lf_decode_*_prefix */
 #define LF_KERNEL_KV4 5              /* lf_kv4_pack, lf_kv4_unpack, lf_decode_attention_kv4 */

@@ -1115,3 +1115,37 @@ def test_prompt_weights_bad_lengths_in_every_form(shares, kv, T, rows, Hq, d):
         ref[:, :kv[b] - (e - a)] += 7.0
         near(w[b, :, :kv[b]], ref[:, :kv[b]], (2.0 ** -12 + 2.0 ** -15) * ref[:, :kv[b]])
         assert (w[b, :, kv[b]:] == 7).all()
+
+
+# ------------------------------------------------------------- the same bits again --
+
+@pytest.mark.parametrize("B,Hq,Hkv,d,S,k", [(1, 32, 8, 128, 2400, None), (9, 16, 2, 64, 9001, 4), (2, 8, 1, 128, 40000, None),
+                                            (40, 32, 8, 128, 1500, None), (3, 4, 1, 64, 20000, 20)])
+def test_steps_by_weight_are_the_same_bits_again(B, Hq, Hkv, d, S, k):
+    """By clusters, the last CTA and the scoring kernel, one slot and several."""
+    g = gen(B + S)
+    c = step_case(g, B, Hq, Hkv, d, S, [S, S // 2])
+    ws = torch.randint(0, S, (B, Hkv), generator=g, dtype=torch.int32).cuda()
+    ref = None
+    for _ in range(6):
+        e = {n: t.clone() for n, t in c.items()}
+        out, nxt = run_step(e, ws, 16, d ** -0.5, decay=0.9, k=k)
+        got = [t.view(torch.uint8) for t in (out, nxt, e["weights"], e["mask"], e["k"], e["v"])]
+        assert ref is None or all(torch.equal(x, y) for x, y in zip(got, ref))
+        ref = got
+    no_errors()
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d,S", [(1, 32, 8, 128, 16384), (64, 8, 2, 64, 300), (6, 8, 1, 128, 5001)])
+def test_kv4_attention_is_the_same_bits_again(B, Hq, Hkv, d, S):
+    g = gen(B + S)
+    c = kv4_case(g, B, Hq, Hkv, d, S, [S, S // 2])
+    ws = torch.randint(0, S, (B, Hkv), generator=g, dtype=torch.int32).cuda()
+    ref = None
+    for _ in range(6):
+        e = {n: t.clone() for n, t in c.items()}
+        out = run_kv4(e, ws, d ** -0.5)
+        got = [t.view(torch.uint8) for t in (out, e["mask"], e["k4"], e["ks"], e["v4"], e["vs"])]
+        assert ref is None or all(torch.equal(x, y) for x, y in zip(got, ref))
+        ref = got
+    no_errors()
