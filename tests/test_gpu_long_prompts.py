@@ -1149,3 +1149,72 @@ def test_kv4_attention_is_the_same_bits_again(B, Hq, Hkv, d, S):
         assert ref is None or all(torch.equal(x, y) for x, y in zip(got, ref))
         ref = got
     no_errors()
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 2, 64), (4, 2, 128), (8, 1, 128)])
+def test_weights_step_of_one_head_without_a_softmax(Hq, Hkv, d):
+    """A query of NaN: its head's output and its unit's weights, and no other head's output."""
+    g = gen(d)
+    for S in (40, 900, 9000):
+        c = step_case(g, 1, Hq, Hkv, d, S)
+        c["q"][0, 0, 3] = NAN
+        G, live = Hq // Hkv, c["mask"].cpu() >= 0
+        want = plain.weights_step(*(c[x] for x in ("q", "k", "v", "mask", "weights", "nk", "nv")),
+                                  ints([[-1] * Hkv]), 2, 0.1, 1.0, 1)
+        out, nxt = run_step(c, ints([[-1] * Hkv]), 2, 0.1)
+        w = c["weights"].cpu()
+        assert torch.isnan(out[0, 0]).all() and torch.isnan(w[0, 0][live[0, 0]]).all() and nxt[0, 0] == -1
+        near(out[:, 1:], want["out"][:, 1:], want["tol"][:, 1:])
+        near(w[:, 1:][live[:, 1:]], want["weights"][:, 1:][live[:, 1:]], want["wtol"][:, 1:][live[:, 1:]])
+        assert torch.equal(nxt.cpu()[:, 1:, None], plain.chosen(w[:, 1:], c["mask"].cpu()[:, 1:], 2, 1, False))
+    no_errors()
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_prompt_weights_of_random_batches(seed):
+    """Skewed lengths, empty sequences, counted rows of every size: whatever the plan makes of them."""
+    g = gen(1000 + seed)
+
+    def pick(lo, hi):  # over the logarithm
+        return int(lo * (hi / lo) ** float(torch.rand((), generator=g)))
+
+    B, Hkv, G, d = pick(1, 40), pick(1, 4), 2 ** int(torch.randint(0, 4, (), generator=g)), 64 + 64 * (seed % 2)
+    nq = [0 if torch.rand((), generator=g) < 0.15 else pick(1, 2500 // B + 2) for _ in range(B)]
+    nq[0] = max(nq[0], 1)
+    kv = [n + (pick(1, 3000) if torch.rand((), generator=g) < 0.6 else 0) for n in nq]
+    S = max(kv) + int(torch.randint(0, 9, (), generator=g))
+    rows = 0 if torch.rand((), generator=g) < 0.4 else pick(1, 400)
+    starts = [sum(nq[:i]) for i in range(B + 1)]
+    T = starts[B] + int(torch.randint(0, 5, (), generator=g))
+    q, k = normal(g, T, Hkv * G, d), normal(g, B, Hkv, S, d)
+    q[starts[B]:] = NAN
+    w = torch.full((B, Hkv, S), 2.0, device="cuda")
+    for b in range(B):
+        k[b, :, kv[b]:] = NAN
+    lf.prompt_weights(q, k, ints(starts), ints(kv), w, d ** -0.5, rows=rows)
+    ref = summed(q, k, starts, kv, rows, d ** -0.5)
+    for b in range(B):
+        past = kv[b] - nq[b]
+        ref[b, :, :past] += 2.0
+        ref[b, :, kv[b] if nq[b] else 0:] = 2.0
+    near(w, ref, (2.0 ** -12 + 2.0 ** -15) * ref)
+    no_errors()
+
+
+@pytest.mark.parametrize("Hq,d,k", [(8, 64, None), (1, 128, 5), (2, 64, 300)])
+def test_weights_step_of_the_longest_cache(Hq, d, k):
+    """2^20 slots, in runs of live and masked ones."""
+    g = gen(Hq)
+    S = 1 << 20
+    c = step_case(g, 1, Hq, 1, d, S, holes=0.0)
+    c["mask"][0, 0, 70000:900000] = -1
+    check_step(c, ints([[S - 1]]), 64, d ** -0.5, 0.97, k)
+    no_errors()
+
+
+def test_kv4_attention_of_the_longest_cache():
+    g = gen(5)
+    S = 1 << 20
+    c = kv4_case(g, 1, 8, 1, 64, S, holes=0.01)
+    check_kv4(c, ints([[S - 1]]), 0.125)
+    no_errors()
